@@ -11,7 +11,10 @@
  *     the recurrence W_t = W_{t-1} + eta_t v_t k_t^T, o_t = W_t q_t is causal
  *     linear attention and admits a chunked / prefix-scan form
  *     ("Formulación Paralela").
- *     Its backward pass is ttt_linear_bwd.
+ *     Its backward pass is ttt_linear_bwd.  The same fast weight trained on
+ *     the squared loss is ttt_delta_fwd (with ttt_delta_bwd, and
+ *     ttt_delta_step for single tokens); ttt_norm_fwd holds the norms that
+ *     stand before and after such a layer.
  *   * "Test-Time Training Done Right" (LaCT review): a SwiGLU memory with
  *     three matrices, chunk gradients summed with per-token learning rates,
  *     GD / momentum / Muon (Newton-Schulz) updates followed by L2
@@ -161,6 +164,140 @@ int ttt_linear_bwd(const ttt_linear_desc* desc, const void* q, const void* k, co
                    const float* lr, const float* S0, const void* dout, const float* dS_end,
                    float* dq, float* dk, float* dv, float* dlr, float* dS0, void* ws,
                    size_t ws_bytes, void* stream);
+
+/* ------------------------------------------------------------------------
+ * Linear fast weight trained on the squared binding loss: the gated delta
+ * rule.  Same fast weight and same reads as case (a); the inner step is one
+ * gradient step of size beta_t on 1/2 |W k_t - v_t|^2, taken after the weight
+ * has decayed by exp(g_t), in place of the step on -<W k_t, v_t>.
+ *
+ *   state S = W^T, float32 [B, H, dk, dv];  a_t = exp(g_t)
+ *   e_t = v_t - a_t S_{t-1}^T k_t
+ *   S_t = a_t S_{t-1} + beta_t k_t e_t^T ;  out_t = scale S_t^T q_t
+ *
+ * g is the log decay (0: none, -inf: the state is cleared; values above 0
+ * grow the state and may overflow); beta_t usually lies in [0, 1] and k_t is
+ * usually of unit length (ttt_norm_fwd), which keeps every step a
+ * contraction, but neither is required.  A token with beta = 0 and g = 0
+ * leaves the state as it is.  g, beta: [B, H, N] in the element type of q, k
+ * and v.
+ *
+ * Float32 arithmetic on CUDA cores, token by token, for every type and size.
+ * ---------------------------------------------------------------------- */
+typedef struct {
+  int B, H, N;          /* batch, heads, tokens (N >= 0)                     */
+  int dk, dv;           /* key/query dim, value dim: 1..128                  */
+  float scale;          /* of the reads; <= 0 selects 1 / sqrt(dk)           */
+  ttt_dtype in_dtype;   /* q, k, v, g, beta (and dout and the gradients)     */
+  ttt_dtype out_dtype;  /* out                                               */
+} ttt_delta_desc;
+
+/* Workspace bytes of ttt_delta_fwd.  Errors: TTT_ERR_ARG (null pointers), the
+ * shape and dtype errors of ttt_delta_fwd. */
+int ttt_delta_workspace_bytes(const ttt_delta_desc* desc, size_t* bytes);
+
+/* One call over N tokens.  q, k: [B,H,N,dk]; v: [B,H,N,dv]; g, beta: [B,H,N]
+ * (g NULL: no decay); S: in = state before the first token, out = state after
+ * the last; out: [B,H,N,dv].  ws: device workspace of at least
+ * ttt_delta_workspace_bytes, status block first; it must not be shared by
+ * calls that overlap in time.  No tensor may overlap another one.
+ * A later call with the same S continues the sequence.
+ * Errors: TTT_ERR_ARG (null or non-device pointers, or memory of another
+ * device than the current one), TTT_ERR_SHAPE, TTT_ERR_ALIGN, TTT_ERR_DTYPE,
+ * TTT_ERR_UNSUPPORTED (dims above 128), TTT_ERR_WORKSPACE, TTT_ERR_CUDA;
+ * nothing is enqueued when validation fails. */
+int ttt_delta_fwd(const ttt_delta_desc* desc, const void* q, const void* k, const void* v,
+                  const void* g, const void* beta, float* S, void* out, void* ws, size_t ws_bytes,
+                  void* stream);
+
+/* Backward pass of ttt_delta_fwd: the gradients of
+ *   L = sum_t <dout_t, out_t> + <dS_end, S_end>
+ * with respect to q, k, v, g, beta and the start state S0.  With X the
+ * derivative of L by the state, from the last token back:
+ *   X += scale q_t dout_t^T;  dq_t = scale S_t dout_t;  du = X^T k_t
+ *   dv_t = beta_t du;  dbeta_t = <du, e_t>
+ *   dk_t = beta_t X e_t - a_t beta_t S_{t-1} du
+ *   Y = X - beta_t k_t du^T;  dg_t = a_t <Y, S_{t-1}>;  X <- a_t Y
+ * and dS0 = X after the first token.  Inputs as given to the forward call; S0
+ * [B,H,dk,dv] float32, its start state (NULL: zeros); dout [B,H,N,dv] in
+ * in_dtype; dS_end [B,H,dk,dv] float32 (NULL: zeros).  Outputs, written in
+ * full: dq, dk [B,H,N,dk], dv [B,H,N,dv], dg (NULL exactly when g is), dbeta
+ * [B,H,N] in in_dtype; dS0 float32.  desc->out_dtype is not used.  ws as above, of at
+ * least ttt_delta_bwd_workspace_bytes (the states at the chunk borders and
+ * the tokens' e and du, or their chunk forms).  Errors as ttt_delta_fwd. */
+int ttt_delta_bwd_workspace_bytes(const ttt_delta_desc* desc, size_t* bytes);
+int ttt_delta_bwd(const ttt_delta_desc* desc, const void* q, const void* k, const void* v,
+                  const void* g, const void* beta, const float* S0, const void* dout,
+                  const float* dS_end, void* dq, void* dk, void* dv, void* dg, void* dbeta,
+                  float* dS0, void* ws, size_t ws_bytes, void* stream);
+
+/* Single tokens, for serving: one token of each of B rows, each with its own
+ * state in a pool.  desc->N must be 1.  q, k: [B,H,dk]; v, out: [B,H,dv]; g,
+ * beta: [B,H] (g NULL: no decay); S: float32 pool [n_slots,H,dk,dv], updated in place.  Row b
+ * uses state slots[b] (int32, device; NULL: slot b, then n_slots >= B).  A
+ * row whose slot is negative or not below n_slots is idle: its out row and
+ * every state stay as they are.  Rows with the same slot are successive
+ * tokens of one sequence, in row order.  Every state element is read and
+ * written once per call, whatever the number of rows that share it.
+ * Errors as ttt_delta_fwd, and TTT_ERR_SHAPE for N != 1 or n_slots < 1. */
+int ttt_delta_step(const ttt_delta_desc* desc, const void* q, const void* k, const void* v,
+                   const void* g, const void* beta, const int* slots, int n_slots, float* S,
+                   void* out, void* stream);
+
+/* ------------------------------------------------------------------------
+ * Row norm with weight, gate and scaled residual: what stands before a fast
+ * weight (queries and keys brought to unit length) and after it (its output
+ * normalised, gated and added to the residual).
+ *
+ *   out = res + scale * x r(x) * w * act(z)       row by row
+ *   TTT_NORM_RMS: r = 1 / sqrt(mean(x^2) + eps)
+ *   TTT_NORM_L2:  r = 1 / max(|x|, eps)
+ *   act: TTT_GATE_NONE 1; TTT_GATE_SILU z sigmoid(z); TTT_GATE_SIGMOID sigmoid(z)
+ *
+ * x, z, res, out: [rows, D] contiguous in `dtype`; w: [D] float32.
+ * ---------------------------------------------------------------------- */
+typedef enum { TTT_NORM_RMS = 0, TTT_NORM_L2 = 1 } ttt_norm_kind;
+typedef enum { TTT_GATE_NONE = 0, TTT_GATE_SILU = 1, TTT_GATE_SIGMOID = 2 } ttt_gate;
+typedef struct {
+  long long rows;       /* >= 0                                              */
+  int D;                /* 1..8192, D * sizeof(element) a multiple of 16     */
+  ttt_norm_kind kind;
+  ttt_gate gate;
+  float eps;            /* > 0                                               */
+  float scale;          /* of the normalised term                            */
+  ttt_dtype dtype;
+} ttt_norm_desc;
+
+/* w, res nullable (ones, zeros); z NULL exactly when gate is TTT_GATE_NONE.
+ * out may be x, z or res itself (each row is read before it is written);
+ * other overlaps are not allowed.  Errors: as ttt_delta_fwd. */
+int ttt_norm_fwd(const ttt_norm_desc* desc, const void* x, const float* w, const void* z,
+                 const void* res, void* out, void* stream);
+
+/* Gradients of sum <dout, out> by x, w and z (that of res is dout itself).
+ * dx, dz: [rows, D] in dtype, dw: [D] float32, each written in full; dw NULL
+ * exactly when w is, dz exactly when z is.  dx and dz may be dout, x or z
+ * themselves.  rows = 0 writes dw = 0.  The sum over the rows of dw has a
+ * fixed order.  ws: device workspace of at least ttt_norm_bwd_workspace_bytes
+ * (status block, partial sums of dw; it depends on the device's SM count). */
+int ttt_norm_bwd_workspace_bytes(const ttt_norm_desc* desc, size_t* bytes);
+int ttt_norm_bwd(const ttt_norm_desc* desc, const void* x, const float* w, const void* z,
+                 const void* dout, void* dx, float* dw, void* dz, void* ws, size_t ws_bytes,
+                 void* stream);
+
+/* The delta-rule layer: q and k brought to unit length (TTT_NORM_L2, eps
+ * 1e-6), the gated delta rule, and the output norm with gate and residual,
+ *   out = res + out_scale * rms_norm(o; eps) * w * silu(z).
+ * Shapes as ttt_delta_fwd, with z, res, out [B,H,N,dv] and w [dv] float32; w,
+ * z, res nullable (ones, no gate, zeros).  in_dtype must equal out_dtype, and
+ * dk and dv times the element size be multiples of 16 bytes.  ws: at least
+ * ttt_delta_layer_workspace_bytes (the unit queries and keys, the reads o and
+ * ttt_delta_fwd's own part). */
+int ttt_delta_layer_workspace_bytes(const ttt_delta_desc* desc, size_t* bytes);
+int ttt_delta_layer_fwd(const ttt_delta_desc* desc, float eps, float out_scale, const void* q,
+                        const void* k, const void* v, const void* g, const void* beta,
+                        const float* w, const void* z, const void* res, float* S, void* out,
+                        void* ws, size_t ws_bytes, void* stream);
 
 /* ------------------------------------------------------------------------
  * Case (b): LaCT, SwiGLU fast-weight memory with large chunks.

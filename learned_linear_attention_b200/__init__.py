@@ -15,6 +15,11 @@ from ._lib import (  # noqa: F401
     lact_apply_grad, lact_bwd_workspace_bytes, lact_chunk_bwd, lact_chunk_fwd, lact_chunk_fwd_noalloc, lact_chunk_grad, lact_grad_bytes,
     lact_noalloc_check_status, lact_desc, lact_read,
     lact_layer_fwd, ttt_window_attn_fwd,
+    TTT_GATE_NONE, TTT_GATE_SIGMOID, TTT_GATE_SILU, TTT_NORM_L2, TTT_NORM_RMS,
+    ttt_delta_bwd, ttt_delta_bwd_workspace_bytes, ttt_delta_desc, ttt_delta_fwd,
+    ttt_delta_layer_fwd, ttt_delta_layer_workspace_bytes, ttt_delta_step,
+    ttt_delta_workspace_bytes, ttt_norm_bwd, ttt_norm_bwd_workspace_bytes, ttt_norm_desc,
+    ttt_norm_fwd,
     ttt_window_desc, lact_state_bytes, lact_state_init, lact_state_readout,
     lact_workspace_bytes, lact_workspace_bytes_min, load, status_string, ttt_build_info, ttt_check_device_status,
     ttt_linear_bwd, ttt_linear_bwd_workspace_bytes, ttt_linear_desc, ttt_linear_fwd,
@@ -23,6 +28,8 @@ from ._lib import (  # noqa: F401
 
 _DT = {"f32": TTT_F32, "fp32": TTT_F32, "bf16": TTT_BF16}
 _ORDER = {"causal": TTT_CAUSAL, "bidirectional": TTT_BIDIRECTIONAL}
+_NORM = {"rms": TTT_NORM_RMS, "l2": TTT_NORM_L2}
+_GATE = {"none": TTT_GATE_NONE, "silu": TTT_GATE_SILU, "sigmoid": TTT_GATE_SIGMOID}
 _OPT = {"gd": TTT_OPT_GD, "momentum": TTT_OPT_MOMENTUM, "muon": TTT_OPT_MUON}
 
 
@@ -30,6 +37,17 @@ def make_linear_desc(B, H, N, dk, dv, chunk, include_diag=True, in_dtype="bf16",
                      out_dtype="f32", order="causal") -> ttt_linear_desc:
     return ttt_linear_desc(B, H, N, dk, dv, chunk, _ORDER[order], int(bool(include_diag)),
                            _DT[in_dtype], _DT[out_dtype])
+
+
+def make_delta_desc(B, H, N, dk, dv, *, scale=0.0, in_dtype="bf16",
+                    out_dtype="bf16") -> ttt_delta_desc:
+    """Fill a ttt_delta_desc (scale <= 0 selects 1/sqrt(dk))."""
+    return ttt_delta_desc(B, H, N, dk, dv, scale, _DT[in_dtype], _DT[out_dtype])
+
+
+def make_norm_desc(rows, D, *, kind="rms", gate="none", eps=1e-6, scale=1.0,
+                   dtype="bf16") -> ttt_norm_desc:
+    return ttt_norm_desc(rows, D, _NORM[kind], _GATE[gate], eps, scale, _DT[dtype])
 
 
 def make_lact_desc(B, H, N_in, d, dh, chunk, *, N_q=None, order="causal", opt="gd", beta=0.9,

@@ -17,6 +17,8 @@ TTT_ERR_UNSUPPORTED, TTT_ERR_WORKSPACE, TTT_ERR_CUDA, TTT_ERR_TIMEOUT = -5, -6, 
 TTT_F32, TTT_BF16 = 0, 1
 TTT_CAUSAL, TTT_BIDIRECTIONAL = 0, 1
 TTT_OPT_GD, TTT_OPT_MOMENTUM, TTT_OPT_MUON = 0, 1, 2
+TTT_NORM_RMS, TTT_NORM_L2 = 0, 1
+TTT_GATE_NONE, TTT_GATE_SILU, TTT_GATE_SIGMOID = 0, 1, 2
 TTT_STATUS_BYTES = 256
 
 
@@ -31,6 +33,18 @@ class ttt_linear_desc(ctypes.Structure):
                 ("dk", ctypes.c_int), ("dv", ctypes.c_int), ("chunk", ctypes.c_int),
                 ("order", ctypes.c_int), ("include_diag", ctypes.c_int),
                 ("in_dtype", ctypes.c_int), ("out_dtype", ctypes.c_int)]
+
+
+class ttt_delta_desc(ctypes.Structure):
+    _fields_ = [("B", ctypes.c_int), ("H", ctypes.c_int), ("N", ctypes.c_int),
+                ("dk", ctypes.c_int), ("dv", ctypes.c_int), ("scale", ctypes.c_float),
+                ("in_dtype", ctypes.c_int), ("out_dtype", ctypes.c_int)]
+
+
+class ttt_norm_desc(ctypes.Structure):
+    _fields_ = [("rows", ctypes.c_longlong), ("D", ctypes.c_int), ("kind", ctypes.c_int),
+                ("gate", ctypes.c_int), ("eps", ctypes.c_float), ("scale", ctypes.c_float),
+                ("dtype", ctypes.c_int)]
 
 
 class lact_desc(ctypes.Structure):
@@ -64,6 +78,17 @@ _SIGS = {
                        _VP],
     "ttt_linear_bwd_workspace_bytes": [ctypes.POINTER(ttt_linear_desc), _SZP],
     "ttt_linear_bwd": [ctypes.POINTER(ttt_linear_desc)] + [_VP] * 13 + [_SZ, _VP],
+    "ttt_delta_workspace_bytes": [ctypes.POINTER(ttt_delta_desc), _SZP],
+    "ttt_delta_fwd": [ctypes.POINTER(ttt_delta_desc)] + [_VP] * 8 + [_SZ, _VP],
+    "ttt_delta_bwd_workspace_bytes": [ctypes.POINTER(ttt_delta_desc), _SZP],
+    "ttt_delta_bwd": [ctypes.POINTER(ttt_delta_desc)] + [_VP] * 15 + [_SZ, _VP],
+    "ttt_delta_step": [ctypes.POINTER(ttt_delta_desc)] + [_VP] * 6 + [_I, _VP, _VP, _VP],
+    "ttt_norm_fwd": [ctypes.POINTER(ttt_norm_desc)] + [_VP] * 6,
+    "ttt_norm_bwd_workspace_bytes": [ctypes.POINTER(ttt_norm_desc), _SZP],
+    "ttt_norm_bwd": [ctypes.POINTER(ttt_norm_desc)] + [_VP] * 8 + [_SZ, _VP],
+    "ttt_delta_layer_workspace_bytes": [ctypes.POINTER(ttt_delta_desc), _SZP],
+    "ttt_delta_layer_fwd": [ctypes.POINTER(ttt_delta_desc), ctypes.c_float, ctypes.c_float]
+    + [_VP] * 11 + [_SZ, _VP],
     "ttt_window_attn_fwd": [ctypes.POINTER(ttt_window_desc), _VP, _VP, _VP, _VP, _VP, _SZ, _VP],
     "lact_layer_fwd": [ctypes.POINTER(lact_desc), _I, ctypes.c_float, _VP, _VP, _VP, _VP, _VP, _VP,
                        _VP, _SZ, _VP],
@@ -179,6 +204,83 @@ def ttt_linear_bwd(desc, q, k, v, lr, S0, dout, dS_end, dq, dk, dv, dlr, dS0, ws
                                _ptr(dout), _ptr(dS_end), _ptr(dq), _ptr(dk), _ptr(dv), _ptr(dlr),
                                _ptr(dS0), _ptr(ws), nbytes, _stream(stream))
     return _check("ttt_linear_bwd", st) if check else st
+
+
+# ------------------------------------------------------------------ delta rule
+def _size_of(fn: str, desc) -> int:
+    n = ctypes.c_size_t(0)
+    _check(fn, getattr(load(), fn)(ctypes.byref(desc), ctypes.byref(n)))
+    return n.value
+
+
+def ttt_delta_workspace_bytes(desc: ttt_delta_desc) -> int:
+    return _size_of("ttt_delta_workspace_bytes", desc)
+
+
+def ttt_delta_fwd(desc, q, k, v, g, beta, S, out, ws, ws_bytes=None, stream=None, check=True):
+    """The gated delta rule over N tokens (see include/ttt.h); g may be None (no decay)."""
+    st = load().ttt_delta_fwd(ctypes.byref(desc), _ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(beta),
+                              _ptr(S), _ptr(out), _ptr(ws), _nbytes(ws, ws_bytes),
+                              _stream(stream))
+    return _check("ttt_delta_fwd", st) if check else st
+
+
+def ttt_delta_bwd_workspace_bytes(desc: ttt_delta_desc) -> int:
+    return _size_of("ttt_delta_bwd_workspace_bytes", desc)
+
+
+def ttt_delta_bwd(desc, q, k, v, g, beta, S0, dout, dS_end, dq, dk, dv, dg, dbeta, dS0, ws,
+                  ws_bytes=None, stream=None, check=True):
+    """Gradients of sum <dout, out> + <dS_end, S_end> (see include/ttt.h); S0
+    and dS_end may be None (zeros), dg is None exactly when g is."""
+    st = load().ttt_delta_bwd(ctypes.byref(desc), _ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(beta),
+                              _ptr(S0), _ptr(dout), _ptr(dS_end), _ptr(dq), _ptr(dk), _ptr(dv),
+                              _ptr(dg), _ptr(dbeta), _ptr(dS0), _ptr(ws), _nbytes(ws, ws_bytes),
+                              _stream(stream))
+    return _check("ttt_delta_bwd", st) if check else st
+
+
+def ttt_delta_step(desc, q, k, v, g, beta, slots, n_slots, S, out, stream=None, check=True):
+    """One token of every row, states in the pool S by slot (see include/ttt.h);
+    g may be None (no decay), slots None (row b uses slot b)."""
+    st = load().ttt_delta_step(ctypes.byref(desc), _ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(beta),
+                               _ptr(slots), int(n_slots), _ptr(S), _ptr(out), _stream(stream))
+    return _check("ttt_delta_step", st) if check else st
+
+
+# ------------------------------------------------------------------ row norm
+def ttt_norm_fwd(desc, x, w, z, res, out, stream=None, check=True):
+    """out = res + scale * x r(x) * w * act(z) (see include/ttt.h); w, z and
+    res may be None."""
+    st = load().ttt_norm_fwd(ctypes.byref(desc), _ptr(x), _ptr(w), _ptr(z), _ptr(res), _ptr(out),
+                             _stream(stream))
+    return _check("ttt_norm_fwd", st) if check else st
+
+
+def ttt_norm_bwd_workspace_bytes(desc: ttt_norm_desc) -> int:
+    return _size_of("ttt_norm_bwd_workspace_bytes", desc)
+
+
+def ttt_norm_bwd(desc, x, w, z, dout, dx, dw, dz, ws, ws_bytes=None, stream=None, check=True):
+    """Gradients of sum <dout, out> by x, w and z (see include/ttt.h)."""
+    st = load().ttt_norm_bwd(ctypes.byref(desc), _ptr(x), _ptr(w), _ptr(z), _ptr(dout), _ptr(dx),
+                             _ptr(dw), _ptr(dz), _ptr(ws), _nbytes(ws, ws_bytes), _stream(stream))
+    return _check("ttt_norm_bwd", st) if check else st
+
+
+def ttt_delta_layer_workspace_bytes(desc: ttt_delta_desc) -> int:
+    return _size_of("ttt_delta_layer_workspace_bytes", desc)
+
+
+def ttt_delta_layer_fwd(desc, eps, out_scale, q, k, v, g, beta, w, z, res, S, out, ws,
+                        ws_bytes=None, stream=None, check=True):
+    """Unit queries and keys, the gated delta rule, and the output norm with
+    gate and residual (see include/ttt.h); g, w, z and res may be None."""
+    st = load().ttt_delta_layer_fwd(ctypes.byref(desc), float(eps), float(out_scale), _ptr(q),
+                                    _ptr(k), _ptr(v), _ptr(g), _ptr(beta), _ptr(w), _ptr(z),
+                                    _ptr(res), _ptr(S), _ptr(out), _ptr(ws),
+                                    _nbytes(ws, ws_bytes), _stream(stream))
+    return _check("ttt_delta_layer_fwd", st) if check else st
 
 
 def ttt_window_attn_fwd(desc, q, k, v, out, ws, ws_bytes=None, stream=None, check=True):

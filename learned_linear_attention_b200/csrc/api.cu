@@ -240,6 +240,316 @@ int ttt_linear_bwd(const ttt_linear_desc* d, const void* q, const void* k, const
   return launch_ttt_linear_bwd(L, as_stream(stream)) == 0 ? TTT_OK : TTT_ERR_CUDA;
 }
 
+// ------------------------------------------------------------------ delta rule
+struct Range {
+  const void* p;
+  size_t bytes;
+};
+static bool overlap(const Range& a, const Range& b) {
+  if (!a.p || !b.p || a.bytes == 0 || b.bytes == 0) return false;
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a.p), y = reinterpret_cast<uintptr_t>(b.p);
+  return x < y + b.bytes && y < x + a.bytes;
+}
+// Alignment, then overlaps of the written ranges with each other and with the
+// read ones, then that every range is memory of the current device: a kernel
+// must not touch another address.  (A stream of another device needs no check:
+// the launch itself refuses it.)
+static int check_ranges(const Range* in, int n_in, const Range* out, int n_out) {
+  for (int i = 0; i < n_in; ++i)
+    if (in[i].p && !aligned16(in[i].p)) return TTT_ERR_ALIGN;
+  for (int i = 0; i < n_out; ++i)
+    if (out[i].p && !aligned16(out[i].p)) return TTT_ERR_ALIGN;
+  for (int i = 0; i < n_out; ++i) {
+    for (int j = 0; j < n_in; ++j)
+      if (overlap(out[i], in[j])) return TTT_ERR_ARG;
+    for (int j = 0; j < i; ++j)
+      if (overlap(out[i], out[j])) return TTT_ERR_ARG;
+  }
+  int cur = 0;
+  if (cudaGetDevice(&cur) != cudaSuccess) return TTT_ERR_CUDA;
+  for (int i = 0; i < n_in + n_out; ++i) {
+    const Range& r = i < n_in ? in[i] : out[i - n_in];
+    if (!r.p || r.bytes == 0) continue;
+    cudaPointerAttributes a{};
+    if (cudaPointerGetAttributes(&a, r.p) != cudaSuccess) {
+      cudaGetLastError();
+      return TTT_ERR_CUDA;
+    }
+    if (a.type == cudaMemoryTypeManaged) continue;
+    if (a.type != cudaMemoryTypeDevice || a.device != cur) return TTT_ERR_ARG;
+  }
+  return TTT_OK;
+}
+
+static bool dtype_ok(int t) { return t == TTT_F32 || t == TTT_BF16; }
+static size_t dtype_bytes(int t) { return t == TTT_BF16 ? 2 : 4; }
+
+static int check_delta(const ttt_delta_desc* d) {
+  if (!d) return TTT_ERR_ARG;
+  if (d->B < 1 || d->H < 1 || d->N < 0 || d->dk < 1 || d->dv < 1) return TTT_ERR_SHAPE;
+  if ((long long)d->B * d->H > (1ll << 31) - 1) return TTT_ERR_SHAPE;
+  if (!dtype_ok(d->in_dtype) || !dtype_ok(d->out_dtype)) return TTT_ERR_DTYPE;
+  if (d->scale != d->scale) return TTT_ERR_ARG;
+  if (d->dk > 128 || d->dv > 128) return TTT_ERR_UNSUPPORTED;
+  return TTT_OK;
+}
+
+static DeltaLaunch delta_launch(const ttt_delta_desc* d, const void* q, const void* k,
+                                const void* v, const void* g, const void* beta, float* S,
+                                void* out, void* ws) {
+  DeltaLaunch L{};
+  L.B = d->B; L.H = d->H; L.N = d->N; L.dk = d->dk; L.dv = d->dv;
+  L.scale = d->scale > 0.f ? d->scale : 1.f / sqrtf((float)d->dk);
+  L.in_bf16 = d->in_dtype == TTT_BF16;
+  L.out_bf16 = d->out_dtype == TTT_BF16;
+  L.q = q; L.k = k; L.v = v; L.g = g; L.beta = beta; L.S = S; L.out = out;
+  L.ws = static_cast<uint8_t*>(ws);
+  if (ws) L.st = status_of(ws, 5);
+  return L;
+}
+
+int ttt_delta_workspace_bytes(const ttt_delta_desc* d, size_t* bytes) {
+  int e = check_delta(d);
+  if (e) return e;
+  if (!bytes) return TTT_ERR_ARG;
+  *bytes = TTT_STATUS_BYTES;
+  return TTT_OK;
+}
+
+int ttt_delta_fwd(const ttt_delta_desc* d, const void* q, const void* k, const void* v,
+                  const void* g, const void* beta, float* S, void* out, void* ws, size_t ws_bytes,
+                  void* stream) {
+  int e = check_delta(d);
+  if (e) return e;
+  if (!S || !ws) return TTT_ERR_ARG;
+  size_t need = 0;
+  e = ttt_delta_workspace_bytes(d, &need);
+  if (e) return e;
+  if (ws_bytes < need) return TTT_ERR_WORKSPACE;
+  if (d->N == 0) return TTT_OK;
+  if (!q || !k || !v || !beta || !out) return TTT_ERR_ARG;
+  const size_t T = (size_t)d->B * d->H * d->N, es = dtype_bytes(d->in_dtype);
+  const Range in[] = {{q, T * d->dk * es}, {k, T * d->dk * es}, {v, T * d->dv * es}, {g, T * es}, {beta, T * es}};
+  const Range o[] = {{S, (size_t)d->B * d->H * d->dk * d->dv * 4},
+                     {out, T * d->dv * dtype_bytes(d->out_dtype)},
+                     {ws, need}};
+  e = check_ranges(in, 5, o, 3);
+  if (e) return e;
+  const DeltaLaunch L = delta_launch(d, q, k, v, g, beta, S, out, ws);
+  return launch_delta_rec(L, as_stream(stream)) == 0 ? TTT_OK : TTT_ERR_CUDA;
+}
+
+int ttt_delta_bwd_workspace_bytes(const ttt_delta_desc* d, size_t* bytes) {
+  int e = check_delta(d);
+  if (e) return e;
+  if (!bytes) return TTT_ERR_ARG;
+  *bytes = delta_rec_bwd_layout(d->B * d->H, d->N, d->dk, d->dv).total;
+  return TTT_OK;
+}
+
+int ttt_delta_bwd(const ttt_delta_desc* d, const void* q, const void* k, const void* v,
+                  const void* g, const void* beta, const float* S0, const void* dout,
+                  const float* dS_end, void* dq, void* dk, void* dv, void* dg, void* dbeta,
+                  float* dS0, void* ws, size_t ws_bytes, void* stream) {
+  int e = check_delta(d);
+  if (e) return e;
+  if (!ws || !dS0) return TTT_ERR_ARG;
+  size_t need = 0;
+  e = ttt_delta_bwd_workspace_bytes(d, &need);
+  if (e) return e;
+  if (ws_bytes < need) return TTT_ERR_WORKSPACE;
+  if (d->N > 0 && (!q || !k || !v || !beta || !dout || !dq || !dk || !dv || !dbeta || !g != !dg))
+    return TTT_ERR_ARG;
+  const size_t T = (size_t)d->B * d->H * d->N, es = dtype_bytes(d->in_dtype);
+  const size_t kb = T * d->dk * es, vb = T * d->dv * es, gb = T * es;
+  const size_t sb = (size_t)d->B * d->H * d->dk * d->dv * 4;
+  const Range in[] = {{q, kb}, {k, kb}, {v, vb}, {g, gb}, {beta, gb}, {S0, sb}, {dout, vb}, {dS_end, sb}};
+  const Range o[] = {{dq, kb}, {dk, kb}, {dv, vb}, {dg, gb}, {dbeta, gb}, {dS0, sb}, {ws, need}};
+  e = check_ranges(in, 8, o, 7);
+  if (e) return e;
+  DeltaBwdLaunch L{};
+  L.f = delta_launch(d, q, k, v, g, beta, nullptr, nullptr, ws);
+  L.S0 = S0; L.dS_end = dS_end; L.dout = dout;
+  L.dq = dq; L.dk = dk; L.dv = dv; L.dg = dg; L.dbeta = dbeta; L.dS0 = dS0;
+  L.ws = static_cast<uint8_t*>(ws);
+  L.w = delta_rec_bwd_layout(d->B * d->H, d->N, d->dk, d->dv);
+  return launch_delta_rec_bwd(L, as_stream(stream)) == 0 ? TTT_OK : TTT_ERR_CUDA;
+}
+
+int ttt_delta_step(const ttt_delta_desc* d, const void* q, const void* k, const void* v,
+                   const void* g, const void* beta, const int* slots, int n_slots, float* S,
+                   void* out, void* stream) {
+  int e = check_delta(d);
+  if (e) return e;
+  if (d->N != 1 || n_slots < 1 || (!slots && n_slots < d->B) || d->H > 65535) return TTT_ERR_SHAPE;
+  if (!q || !k || !v || !beta || !S || !out) return TTT_ERR_ARG;
+  const size_t T = (size_t)d->B * d->H, es = dtype_bytes(d->in_dtype);
+  const Range in[] = {{q, T * d->dk * es}, {k, T * d->dk * es}, {v, T * d->dv * es},
+                      {g, T * es}, {beta, T * es}, {slots, (size_t)d->B * sizeof(int)}};
+  const Range o[] = {{S, (size_t)n_slots * d->H * d->dk * d->dv * 4},
+                     {out, T * d->dv * dtype_bytes(d->out_dtype)}};
+  e = check_ranges(in, 6, o, 2);
+  if (e) return e;
+  const DeltaLaunch L = delta_launch(d, q, k, v, g, beta, S, out, nullptr);
+  return launch_delta_step(L, slots, n_slots, as_stream(stream)) == 0 ? TTT_OK : TTT_ERR_CUDA;
+}
+
+// ------------------------------------------------------------------ row norm
+static int check_norm(const ttt_norm_desc* d) {
+  if (!d) return TTT_ERR_ARG;
+  if (d->rows < 0 || d->D < 1) return TTT_ERR_SHAPE;
+  if (d->kind != TTT_NORM_RMS && d->kind != TTT_NORM_L2) return TTT_ERR_ARG;
+  if (d->gate != TTT_GATE_NONE && d->gate != TTT_GATE_SILU && d->gate != TTT_GATE_SIGMOID)
+    return TTT_ERR_ARG;
+  if (!(d->eps > 0.f) || d->scale != d->scale) return TTT_ERR_ARG;
+  if (!dtype_ok(d->dtype)) return TTT_ERR_DTYPE;
+  if (d->D > 8192) return TTT_ERR_UNSUPPORTED;
+  if (d->D * dtype_bytes(d->dtype) % 16 != 0) return TTT_ERR_ALIGN;
+  if (d->rows > (1ll << 46) / d->D) return TTT_ERR_SHAPE;
+  return TTT_OK;
+}
+
+static NormLaunch norm_launch(const ttt_norm_desc* d, const void* x, const float* w, const void* z) {
+  NormLaunch L{};
+  L.rows = d->rows; L.D = d->D; L.kind = (int)d->kind; L.gate = (int)d->gate;
+  L.bf16 = d->dtype == TTT_BF16; L.eps = d->eps; L.scale = d->scale;
+  L.x = x; L.w = w; L.z = z;
+  return L;
+}
+
+int ttt_norm_fwd(const ttt_norm_desc* d, const void* x, const float* w, const void* z,
+                 const void* res, void* out, void* stream) {
+  int e = check_norm(d);
+  if (e) return e;
+  if (d->rows == 0) return TTT_OK;
+  if (!x || !out || (d->gate == TTT_GATE_NONE) != (z == nullptr)) return TTT_ERR_ARG;
+  const size_t n = (size_t)d->rows * d->D * dtype_bytes(d->dtype);
+  // out may be one of the row inputs itself
+  const Range in[] = {{x == out ? nullptr : x, n}, {z == out ? nullptr : z, n},
+                      {res == out ? nullptr : res, n}, {w, (size_t)d->D * 4}};
+  const Range o[] = {{out, n}};
+  e = check_ranges(in, 4, o, 1);
+  if (e) return e;
+  NormLaunch L = norm_launch(d, x, w, z);
+  L.res = res;
+  L.out = out;
+  return launch_norm_fwd(L, device_sms(), as_stream(stream)) == 0 ? TTT_OK : TTT_ERR_CUDA;
+}
+
+int ttt_norm_bwd_workspace_bytes(const ttt_norm_desc* d, size_t* bytes) {
+  int e = check_norm(d);
+  if (e) return e;
+  if (!bytes) return TTT_ERR_ARG;
+  *bytes = TTT_STATUS_BYTES +
+           (size_t)norm_bwd_parts(d->rows, d->D, d->dtype == TTT_BF16, device_sms()) * d->D * 4;
+  return TTT_OK;
+}
+
+int ttt_norm_bwd(const ttt_norm_desc* d, const void* x, const float* w, const void* z,
+                 const void* dout, void* dx, float* dw, void* dz, void* ws, size_t ws_bytes,
+                 void* stream) {
+  int e = check_norm(d);
+  if (e) return e;
+  if (!ws) return TTT_ERR_ARG;
+  size_t need = 0;
+  e = ttt_norm_bwd_workspace_bytes(d, &need);
+  if (e) return e;
+  if (ws_bytes < need) return TTT_ERR_WORKSPACE;
+  if (!w != !dw) return TTT_ERR_ARG;
+  const size_t n = (size_t)d->rows * d->D * dtype_bytes(d->dtype), wb = (size_t)d->D * 4;
+  if (d->rows > 0 &&
+      (!x || !dout || !dx || (d->gate == TTT_GATE_NONE) != (z == nullptr) || !z != !dz))
+    return TTT_ERR_ARG;
+  auto inout = [&](const void* p) { return p == dx || p == dz; };
+  const Range in[] = {{inout(x) ? nullptr : x, n}, {inout(z) ? nullptr : z, n},
+                      {inout(dout) ? nullptr : dout, n}, {w, wb}};
+  const Range o[] = {{dx, n}, {dz, n}, {dw, wb}, {ws, need}};
+  e = check_ranges(in, 4, o, 4);
+  if (e) return e;
+  if (d->rows == 0)
+    return dw ? cuda_ok(cudaMemsetAsync(dw, 0, wb, as_stream(stream))) : TTT_OK;
+  NormLaunch L = norm_launch(d, x, w, z);
+  L.dout = dout; L.dx = dx; L.dz = dz; L.dw = dw;
+  L.part = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + TTT_STATUS_BYTES);
+  return launch_norm_bwd(L, device_sms(), as_stream(stream)) == 0 ? TTT_OK : TTT_ERR_CUDA;
+}
+
+// ------------------------------------------------------------------ delta layer
+// ws: [ttt_delta_fwd's part | unit q | unit k | o]
+struct DeltaLayerLayout {
+  size_t q, k, o, total;
+};
+static int delta_layer_layout(const ttt_delta_desc* d, DeltaLayerLayout* w) {
+  int e = check_delta(d);
+  if (e) return e;
+  if (d->in_dtype != d->out_dtype) return TTT_ERR_DTYPE;
+  const size_t es = dtype_bytes(d->in_dtype);
+  if (d->dk * es % 16 != 0 || d->dv * es % 16 != 0) return TTT_ERR_ALIGN;
+  size_t at = 0;
+  e = ttt_delta_workspace_bytes(d, &at);
+  if (e) return e;
+  const size_t T = (size_t)d->B * d->H * d->N;
+  auto take = [&](size_t bytes) {
+    at = (at + 255) / 256 * 256;
+    const size_t o = at;
+    at += bytes;
+    return o;
+  };
+  w->q = take(T * d->dk * es);
+  w->k = take(T * d->dk * es);
+  w->o = take(T * d->dv * es);
+  w->total = at;
+  return TTT_OK;
+}
+
+int ttt_delta_layer_workspace_bytes(const ttt_delta_desc* d, size_t* bytes) {
+  DeltaLayerLayout w{};
+  int e = delta_layer_layout(d, &w);
+  if (e) return e;
+  if (!bytes) return TTT_ERR_ARG;
+  *bytes = w.total;
+  return TTT_OK;
+}
+
+int ttt_delta_layer_fwd(const ttt_delta_desc* d, float eps, float out_scale, const void* q,
+                        const void* k, const void* v, const void* g, const void* beta,
+                        const float* w, const void* z, const void* res, float* S, void* out,
+                        void* ws, size_t ws_bytes, void* stream) {
+  DeltaLayerLayout lay{};
+  int e = delta_layer_layout(d, &lay);
+  if (e) return e;
+  if (!S || !ws) return TTT_ERR_ARG;
+  if (ws_bytes < lay.total) return TTT_ERR_WORKSPACE;
+  const long long T = (long long)d->B * d->H * d->N;
+  const ttt_norm_desc nk{T, d->dk, TTT_NORM_L2, TTT_GATE_NONE, 1e-6f, 1.f, d->in_dtype};
+  const ttt_norm_desc no{T, d->dv, TTT_NORM_RMS, z ? TTT_GATE_SILU : TTT_GATE_NONE, eps, out_scale, d->in_dtype};
+  e = check_norm(&nk);
+  if (!e) e = check_norm(&no);
+  if (e) return e;
+  if (d->N == 0) return TTT_OK;
+  if (!q || !k || !v || !beta || !out) return TTT_ERR_ARG;
+  const size_t es = dtype_bytes(d->in_dtype), kb = T * d->dk * es, vb = T * d->dv * es;
+  const Range in[] = {{q, kb}, {k, kb}, {v, vb}, {g, T * es}, {beta, T * es}, {w, (size_t)d->dv * 4},
+                      {z == out ? nullptr : z, vb}, {res == out ? nullptr : res, vb}};
+  const Range o[] = {{S, (size_t)d->B * d->H * d->dk * d->dv * 4}, {out, vb}, {ws, lay.total}};
+  e = check_ranges(in, 8, o, 3);
+  if (e) return e;
+  uint8_t* base = static_cast<uint8_t*>(ws);
+  cudaStream_t s = as_stream(stream);
+  NormLaunch n = norm_launch(&nk, q, nullptr, nullptr);
+  n.out = base + lay.q;
+  if (launch_norm_fwd(n, device_sms(), s)) return TTT_ERR_CUDA;
+  n.x = k;
+  n.out = base + lay.k;
+  if (launch_norm_fwd(n, device_sms(), s)) return TTT_ERR_CUDA;
+  e = ttt_delta_fwd(d, base + lay.q, base + lay.k, v, g, beta, S, base + lay.o, ws, lay.q, stream);
+  if (e) return e;
+  n = norm_launch(&no, base + lay.o, w, z);
+  n.res = res;
+  n.out = out;
+  return launch_norm_fwd(n, device_sms(), s) ? TTT_ERR_CUDA : TTT_OK;
+}
+
 // ------------------------------------------------------------------ window attention
 static int check_window(const ttt_window_desc* d) {
   if (!d) return TTT_ERR_ARG;

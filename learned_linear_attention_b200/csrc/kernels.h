@@ -131,6 +131,49 @@ struct LinearBwdLaunch {
 };
 int launch_ttt_linear_bwd(const LinearBwdLaunch& L, cudaStream_t stream);
 
+// ----------------------------------------------------------------- delta rule
+struct DeltaLaunch {
+  int B, H, N, dk, dv;
+  float scale;
+  int in_bf16, out_bf16;
+  const void *q, *k, *v, *g, *beta;   // g nullable: no decay
+  float* S;
+  void* out;
+  uint8_t* ws;
+  DevStatus st;
+};
+struct DeltaBwdWorkspace {            // byte offsets
+  size_t ev, du, Sc, Xc, total;
+};
+struct DeltaBwdLaunch {
+  DeltaLaunch f;
+  const float *S0, *dS_end;           // nullable (zeros)
+  const void* dout;
+  void *dq, *dk, *dv, *dg, *dbeta;
+  float* dS0;
+  uint8_t* ws;
+  DeltaBwdWorkspace w;
+};
+// CUDA cores, float32, any dims up to 128 (ttt_delta.cu)
+int launch_delta_rec(const DeltaLaunch& L, cudaStream_t stream);
+DeltaBwdWorkspace delta_rec_bwd_layout(int BH, int N, int dk, int dv);
+int launch_delta_rec_bwd(const DeltaBwdLaunch& L, cudaStream_t stream);
+int launch_delta_step(const DeltaLaunch& L, const int* slots, int n_slots, cudaStream_t stream);
+
+// ----------------------------------------------------------------- row norm
+struct NormLaunch {
+  long long rows;
+  int D, kind, gate, bf16;
+  float eps, scale;
+  const void *x, *z, *res, *dout;
+  const float* w;
+  void *out, *dx, *dz;
+  float *dw, *part;                   // part: [norm_bwd_parts][D]
+};
+int norm_bwd_parts(long long rows, int D, int bf16, int sms);
+int launch_norm_fwd(const NormLaunch& L, int sms, cudaStream_t stream);
+int launch_norm_bwd(const NormLaunch& L, int sms, cudaStream_t stream);
+
 // ----------------------------------------------------------------- window attention
 // Causal sliding-window softmax attention, head dim 128, bf16 q, k, v
 // [B,H,N,128]; out fp32 or bf16, overwritten or (accumulate) added to.
@@ -305,7 +348,8 @@ int launch_lact_keygrad(const KeyGradLaunch& L, cudaStream_t stream);
 enum KernelKind {
   K_LIN_SIMT, K_LIN_UMMA, K_LACT_CAST, K_KEYPASS, K_GEMM_READ, K_GEMM_GRAD, K_UPDATE,
   K_MUON_MOM, K_NS_PREP, K_GEMM_NS, K_MUON_APPLY, K_KEYGRAD, K_LIN_SEG, K_LIN_BWD_EW, K_SWA, K_LOOP,
-  K_BWD_FWD, K_BWD_GROUP, K_NUM
+  K_BWD_FWD, K_BWD_GROUP, K_DELTA_REC, K_DELTA_REV, K_DELTA_GRAD, K_DELTA_STEP, K_NORM, K_NORM_BWD,
+  K_NUM
 };
 void prof_before(int kind, cudaStream_t s);
 void prof_after(int kind, cudaStream_t s);

@@ -1,0 +1,319 @@
+// ttt_norm.cu -- row norm with weight, gate and scaled residual, and its
+// backward pass:  out = res + scale * x r(x) * w * act(z), row by row.
+//
+// A row belongs to a group of T threads (4 to 32 lanes of a warp, or a whole
+// CTA of 256), each holding the same V 16-byte vectors of every row it meets,
+// so a row is read once, its sum of squares is a few shuffles, and the
+// weight's gradient is summed in registers over the CTA's rows.  Bound by
+// memory.
+#include <algorithm>
+#include <type_traits>
+
+#include "kernels.h"
+
+namespace ttt {
+
+namespace {
+
+constexpr int THREADS = 256;
+
+template <typename T>
+struct Vec;   // 16 bytes of T as floats
+template <>
+struct Vec<float> {
+  static constexpr int N = 4;
+  static TTT_DEVICE_INLINE void load(const float* p, float* x) {
+    const float4 t = *reinterpret_cast<const float4*>(p);
+    x[0] = t.x; x[1] = t.y; x[2] = t.z; x[3] = t.w;
+  }
+  static TTT_DEVICE_INLINE void store(float* p, const float* x) {
+    *reinterpret_cast<float4*>(p) = make_float4(x[0], x[1], x[2], x[3]);
+  }
+};
+template <>
+struct Vec<__nv_bfloat16> {
+  static constexpr int N = 8;
+  static TTT_DEVICE_INLINE void load(const __nv_bfloat16* p, float* x) {
+    const uint4 t = *reinterpret_cast<const uint4*>(p);
+    const uint32_t w[4] = {t.x, t.y, t.z, t.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) { x[2 * i] = bf16lo(w[i]); x[2 * i + 1] = bf16hi(w[i]); }
+  }
+  static TTT_DEVICE_INLINE void store(__nv_bfloat16* p, const float* x) {
+    *reinterpret_cast<uint4*>(p) = make_uint4(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]),
+                                              pack_bf16x2(x[4], x[5]), pack_bf16x2(x[6], x[7]));
+  }
+};
+
+// Sum over the T threads of a row (T = 256: the CTA, through shared memory).
+template <int T>
+TTT_DEVICE_INLINE float row_sum(float x, float* red) {
+#pragma unroll
+  for (int o = 1; o < (T < 32 ? T : 32); o <<= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+  if constexpr (T > 32) {
+    __syncthreads();
+    if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = x;
+    __syncthreads();
+    x = 0.f;
+#pragma unroll
+    for (int w = 0; w < T / 32; ++w) x += red[w];
+  }
+  return x;
+}
+
+TTT_DEVICE_INLINE float sigmoidf(float z) { return 1.f / (1.f + __expf(-z)); }
+
+struct NormArgs {
+  const void *x, *z, *res, *dout;
+  const float* w;
+  void *out, *dx, *dz;
+  float* part;   // partial sums of dw [gridDim.x][D]
+  long long rows;
+  int D, kind, gate;
+  float eps, scale;
+};
+
+// r of a row with sum of squares ss; dr = 0 where r does not depend on x
+TTT_DEVICE_INLINE float row_r(const NormArgs& a, float ss, bool& fixed) {
+  if (a.kind == 0) { fixed = false; return 1.f / sqrtf(ss / a.D + a.eps); }
+  const float len = sqrtf(ss);
+  fixed = !(len > a.eps);
+  return 1.f / (fixed && len == len ? a.eps : len);
+}
+
+template <typename E, int T, int V>
+__global__ void __launch_bounds__(THREADS) norm_fwd_kernel(NormArgs a) {
+  constexpr int N = Vec<E>::N, GROUPS = THREADS / T;
+  __shared__ float red[THREADS / 32];
+  const int t = threadIdx.x % T, gr = threadIdx.x / T;
+  float w[V][N];
+#pragma unroll
+  for (int v = 0; v < V; ++v) {
+    const int c = (v * T + t) * N;
+#pragma unroll
+    for (int i = 0; i < N; ++i) w[v][i] = a.scale * (a.w != nullptr && c < a.D ? a.w[c + i] : 1.f);
+  }
+  // a warp's groups leave the loop together: its rows are adjacent, and the
+  // bound is on the warp's first row
+  const long long step = (long long)gridDim.x * GROUPS;
+  for (long long r0 = (long long)blockIdx.x * GROUPS; r0 < a.rows; r0 += step) {
+    const long long row = r0 + gr;
+    const bool live = row < a.rows;
+    const E* xp = static_cast<const E*>(a.x) + row * a.D;
+    float x[V][N], ss = 0.f;
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      const int c = (v * T + t) * N;
+      if (live && c < a.D) {
+        Vec<E>::load(xp + c, x[v]);
+      } else {
+#pragma unroll
+        for (int i = 0; i < N; ++i) x[v][i] = 0.f;
+      }
+#pragma unroll
+      for (int i = 0; i < N; ++i) ss = fmaf(x[v][i], x[v][i], ss);
+    }
+    float z[V][N], rs[V][N];
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      const int c = (v * T + t) * N;
+      if (live && c < a.D && a.gate != 0) Vec<E>::load(static_cast<const E*>(a.z) + row * a.D + c, z[v]);
+      if (live && c < a.D && a.res != nullptr) Vec<E>::load(static_cast<const E*>(a.res) + row * a.D + c, rs[v]);
+    }
+    ss = row_sum<T>(ss, red);
+    bool fixed;
+    const float r = row_r(a, ss, fixed);
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      const int c = (v * T + t) * N;
+      if (!live || c >= a.D) continue;
+#pragma unroll
+      for (int i = 0; i < N; ++i) {
+        float y = x[v][i] * r * w[v][i];
+        if (a.gate != 0) {
+          const float s = sigmoidf(z[v][i]);
+          y *= a.gate == 1 ? z[v][i] * s : s;
+        }
+        x[v][i] = a.res != nullptr ? y + rs[v][i] : y;
+      }
+      Vec<E>::store(static_cast<E*>(a.out) + row * a.D + c, x[v]);
+    }
+  }
+}
+
+// With n = x r, p = scale dout:  dz = p n w act'(z),  dw = sum p act(z) n,
+// dn = p w act(z),  dx = r (dn - n mean(dn n))  (RMS; for L2 the sum instead
+// of the mean, and no such term where r is 1 / eps).
+template <typename E, int T, int V>
+__global__ void __launch_bounds__(THREADS) norm_bwd_kernel(NormArgs a) {
+  constexpr int N = Vec<E>::N, GROUPS = THREADS / T;
+  __shared__ float red[THREADS / 32];
+  extern __shared__ float acc_s[];   // [GROUPS][D] where dw is wanted
+  const int t = threadIdx.x % T, gr = threadIdx.x / T;
+  float dw[V][N];
+#pragma unroll
+  for (int v = 0; v < V; ++v)
+#pragma unroll
+    for (int i = 0; i < N; ++i) dw[v][i] = 0.f;
+  const long long step = (long long)gridDim.x * GROUPS;
+  for (long long r0 = (long long)blockIdx.x * GROUPS; r0 < a.rows; r0 += step) {
+    const long long row = r0 + gr;
+    const bool live = row < a.rows;
+    float x[V][N], d[V][N], z[V][N], ss = 0.f;
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      const int c = (v * T + t) * N;
+      const bool in = live && c < a.D;
+#pragma unroll
+      for (int i = 0; i < N; ++i) x[v][i] = d[v][i] = z[v][i] = 0.f;
+      if (in) {
+        Vec<E>::load(static_cast<const E*>(a.x) + row * a.D + c, x[v]);
+        Vec<E>::load(static_cast<const E*>(a.dout) + row * a.D + c, d[v]);
+        if (a.gate != 0) Vec<E>::load(static_cast<const E*>(a.z) + row * a.D + c, z[v]);
+      }
+#pragma unroll
+      for (int i = 0; i < N; ++i) ss = fmaf(x[v][i], x[v][i], ss);
+    }
+    ss = row_sum<T>(ss, red);
+    bool fixed;
+    const float r = row_r(a, ss, fixed);
+    float dot = 0.f;
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      const int c = (v * T + t) * N;
+      const bool in = live && c < a.D;
+#pragma unroll
+      for (int i = 0; i < N; ++i) {
+        const float n = x[v][i] * r;
+        float p = a.scale * d[v][i];
+        const float w = in && a.w != nullptr ? a.w[c + i] : 1.f;
+        if (a.gate != 0) {
+          const float s = sigmoidf(z[v][i]);
+          const float act = a.gate == 1 ? z[v][i] * s : s;
+          const float dact = a.gate == 1 ? s * (1.f + z[v][i] * (1.f - s)) : s * (1.f - s);
+          z[v][i] = p * n * w * dact;
+          p *= act;
+        }
+        dw[v][i] = fmaf(p, n, dw[v][i]);
+        d[v][i] = p * w;
+        dot = fmaf(d[v][i], n, dot);
+      }
+      if (in && a.gate != 0) Vec<E>::store(static_cast<E*>(a.dz) + row * a.D + c, z[v]);
+    }
+    dot = row_sum<T>(dot, red);
+    const float m = fixed ? 0.f : a.kind == 0 ? dot / a.D : dot;
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      const int c = (v * T + t) * N;
+      if (!live || c >= a.D) continue;
+#pragma unroll
+      for (int i = 0; i < N; ++i) x[v][i] = r * (d[v][i] - x[v][i] * r * m);
+      Vec<E>::store(static_cast<E*>(a.dx) + row * a.D + c, x[v]);
+    }
+  }
+  if (a.part == nullptr) return;
+#pragma unroll
+  for (int v = 0; v < V; ++v) {
+    const int c = (v * T + t) * N;
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+      if (c < a.D) acc_s[(size_t)gr * a.D + c + i] = dw[v][i];
+  }
+  __syncthreads();
+  for (int c = threadIdx.x; c < a.D; c += THREADS) {
+    float s = 0.f;
+    for (int j = 0; j < GROUPS; ++j) s += acc_s[(size_t)j * a.D + c];
+    a.part[(size_t)blockIdx.x * a.D + c] = s;
+  }
+}
+
+// dw[c] = sum of the CTAs' partial sums, in their order: 32 columns and 8
+// interleaved runs of partial sums to a CTA.
+__global__ void __launch_bounds__(256) norm_dw_kernel(const float* __restrict__ part, int n, int D,
+                                                      float* __restrict__ dw) {
+  __shared__ float s[8][33];
+  const int c = blockIdx.x * 32 + threadIdx.x % 32, j0 = threadIdx.x / 32;
+  float acc = 0.f;
+  if (c < D)
+    for (int j = j0; j < n; j += 8) acc += part[(size_t)j * D + c];
+  s[j0][threadIdx.x % 32] = acc;
+  __syncthreads();
+  if (j0 == 0 && c < D) {
+    for (int j = 1; j < 8; ++j) acc += s[j][threadIdx.x];
+    dw[c] = acc;
+  }
+}
+
+struct Shape { int T, V; };
+// threads of a row and vectors of a thread: few threads keep several rows'
+// loads in flight in a warp, one vector per thread keeps accesses whole
+Shape norm_shape(int D, int per_vec) {
+  const int nv = (D + per_vec - 1) / per_vec;
+  int T = 4;
+  while (T < 32 && T < nv) T *= 2;
+  if (nv > 128) T = 256;
+  int V = 1;
+  while (T * V < nv) V *= 2;
+  return {T, V};
+}
+
+int norm_grid(long long rows, int T, int sms) {
+  const long long groups = THREADS / T;
+  return (int)std::min<long long>((rows + groups - 1) / groups, (long long)sms * 8);
+}
+
+template <typename E, bool BWD>
+int launch_t(const NormArgs& a, int grid, size_t smem, cudaStream_t stream) {
+  const Shape s = norm_shape(a.D, Vec<E>::N);
+#define TTT_NORM(T_, V_)                                                              \
+  if (s.T == T_ && s.V == V_) {                                                       \
+    if constexpr (BWD) norm_bwd_kernel<E, T_, V_><<<grid, THREADS, smem, stream>>>(a); \
+    else norm_fwd_kernel<E, T_, V_><<<grid, THREADS, 0, stream>>>(a);                  \
+    return cudaGetLastError() == cudaSuccess ? 0 : -1;                                 \
+  }
+  TTT_NORM(4, 1) TTT_NORM(8, 1) TTT_NORM(16, 1) TTT_NORM(32, 1) TTT_NORM(32, 2) TTT_NORM(32, 4)
+  TTT_NORM(256, 1) TTT_NORM(256, 2) TTT_NORM(256, 4) TTT_NORM(256, 8)
+#undef TTT_NORM
+  return -1;
+}
+
+NormArgs args_of(const NormLaunch& L) {
+  NormArgs a{};
+  a.x = L.x; a.z = L.z; a.res = L.res; a.dout = L.dout; a.w = L.w;
+  a.out = L.out; a.dx = L.dx; a.dz = L.dz;
+  a.rows = L.rows; a.D = L.D; a.kind = L.kind; a.gate = L.gate; a.eps = L.eps; a.scale = L.scale;
+  return a;
+}
+
+}  // namespace
+
+int norm_bwd_parts(long long rows, int D, int bf16, int sms) {
+  return std::max(1, norm_grid(rows, norm_shape(D, bf16 ? 8 : 4).T, sms));
+}
+
+int launch_norm_fwd(const NormLaunch& L, int sms, cudaStream_t stream) {
+  const NormArgs a = args_of(L);
+  const int grid = norm_bwd_parts(L.rows, L.D, L.bf16, sms);
+  prof_before(K_NORM, stream);
+  const int r = L.bf16 ? launch_t<__nv_bfloat16, false>(a, grid, 0, stream)
+                       : launch_t<float, false>(a, grid, 0, stream);
+  prof_after(K_NORM, stream);
+  return r;
+}
+
+int launch_norm_bwd(const NormLaunch& L, int sms, cudaStream_t stream) {
+  NormArgs a = args_of(L);
+  const int T = norm_shape(L.D, L.bf16 ? 8 : 4).T;
+  const int grid = norm_bwd_parts(L.rows, L.D, L.bf16, sms);
+  a.part = L.dw != nullptr ? L.part : nullptr;
+  const size_t smem = a.part != nullptr ? (size_t)(THREADS / T) * L.D * sizeof(float) : 0;
+  prof_before(K_NORM_BWD, stream);
+  const int r = L.bf16 ? launch_t<__nv_bfloat16, true>(a, grid, smem, stream)
+                       : launch_t<float, true>(a, grid, smem, stream);
+  if (r == 0 && L.dw != nullptr)
+    norm_dw_kernel<<<(L.D + 31) / 32, 256, 0, stream>>>(a.part, grid, L.D, L.dw);
+  prof_after(K_NORM_BWD, stream);
+  return r == 0 && cudaGetLastError() == cudaSuccess ? 0 : -1;
+}
+
+}  // namespace ttt

@@ -21,6 +21,8 @@ Contents
                  differences).
   window_attention -- causal sliding-window softmax attention, and the LaCT
                  language layer (memory + window attention, outputs summed).
+  delta       -- the fast weight of ttt_linear on the squared loss: gated delta
+                 rule, its backward pass, and the row norm around it.
 
 Every function names the passage of the pages it follows.  Pins (checks
 against facts that are not this code) live in ``tests/test_oracle_*.py``.
@@ -30,3 +32,4 @@ from .ttt_linear import (ttt_linear_recurrent, ttt_linear_attention_sum,  # noqa
 from .lact import (lact_forward, lact_read, lact_chunk_gradients, newton_schulz,  # noqa: F401
                    silu, silu_prime, LaCTState)
 from .window_attention import sliding_window_attention, lact_layer_forward  # noqa: F401
+from .delta import delta_recurrent, delta_backward, row_norm, row_norm_backward  # noqa: F401

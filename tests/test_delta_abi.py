@@ -1,0 +1,179 @@
+"""Delta rule and row norm without a GPU: struct layouts, workspace sizes and
+the refusals that the host makes before anything is enqueued."""
+import ctypes
+import os
+import subprocess
+
+import pytest
+
+import learned_linear_attention_b200 as T
+from learned_linear_attention_b200 import _lib
+
+HEADER = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "include", "ttt.h")
+
+
+@pytest.fixture(scope="module", autouse=True)
+def lib():
+    if not os.path.exists(_lib.LIB_PATH):
+        from learned_linear_attention_b200 import build
+        build.build()
+    return T.load()
+
+
+def test_structs_match_c_layout(tmp_path):
+    lines = ['#include <stdio.h>', '#include <stddef.h>', f'#include "{HEADER}"', 'int main(void){']
+    for cls in (T.ttt_delta_desc, T.ttt_norm_desc):
+        s = cls.__name__
+        lines.append(f'printf("{s} %zu\\n", sizeof({s}));')
+        lines += [f'printf("{s}.{f[0]} %zu\\n", offsetof({s}, {f[0]}));' for f in cls._fields_]
+    (tmp_path / "l.c").write_text("\n".join(lines + ["return 0;}"]))
+    subprocess.run(["gcc", "-o", str(tmp_path / "l"), str(tmp_path / "l.c")], check=True)
+    out = subprocess.run([str(tmp_path / "l")], capture_output=True, text=True, check=True).stdout
+    got = dict(line.split() for line in out.splitlines())
+    for cls in (T.ttt_delta_desc, T.ttt_norm_desc):
+        assert int(got[cls.__name__]) == ctypes.sizeof(cls)
+        for f in cls._fields_:
+            assert int(got[f"{cls.__name__}.{f[0]}"]) == getattr(cls, f[0]).offset
+
+
+# addresses far apart, so that nothing overlaps; never dereferenced on the host
+def _far(**over):
+    names = ("q", "k", "v", "g", "beta", "S", "out", "ws", "dout", "dS_end", "dq", "dk", "dv", "dg",
+             "dbeta", "dS0", "slots", "x", "w", "z", "res", "dx", "dw", "dz")
+    p = {n: (i + 1) << 40 for i, n in enumerate(names)}
+    p.update(over)
+    return p
+
+
+def _fwd(d, ws_bytes=1 << 39, **over):
+    p = _far(**over)
+    return T.load().ttt_delta_fwd(ctypes.byref(d), *(p[n] for n in ("q", "k", "v", "g", "beta", "S", "out", "ws")),
+                                  ws_bytes, None)
+
+
+def _bwd(d, ws_bytes=1 << 39, **over):
+    p = _far(**over)
+    names = ("q", "k", "v", "g", "beta", "S", "dout", "dS_end", "dq", "dk", "dv", "dg", "dbeta", "dS0", "ws")
+    return T.load().ttt_delta_bwd(ctypes.byref(d), *(p[n] for n in names), ws_bytes, None)
+
+
+def _step(d, n_slots=64, **over):
+    p = _far(**over)
+    return T.load().ttt_delta_step(ctypes.byref(d), *(p[n] for n in ("q", "k", "v", "g", "beta", "slots")),
+                                   n_slots, p["S"], p["out"], None)
+
+
+def _norm(d, **over):
+    p = _far(**over)
+    return T.load().ttt_norm_fwd(ctypes.byref(d), *(p[n] for n in ("x", "w", "z", "res", "out")), None)
+
+
+def _norm_bwd(d, ws_bytes=1 << 39, **over):
+    p = _far(**over)
+    return T.load().ttt_norm_bwd(ctypes.byref(d), *(p[n] for n in ("x", "w", "z", "dout", "dx", "dw", "dz", "ws")),
+                                 ws_bytes, None)
+
+
+@pytest.mark.parametrize("call", [_fwd, _bwd, _step])
+def test_delta_descriptor_refusals(call):
+    N = 1 if call is _step else 8
+    mk = lambda **kw: T.make_delta_desc(**{**dict(B=2, H=2, N=N, dk=64, dv=64), **kw})  # noqa: E731
+    assert call(mk(B=0)) == T.TTT_ERR_SHAPE
+    assert call(mk(H=0)) == T.TTT_ERR_SHAPE
+    assert call(mk(N=-1)) == T.TTT_ERR_SHAPE
+    assert call(mk(dk=0)) == T.TTT_ERR_SHAPE
+    assert call(mk(dk=129)) == T.TTT_ERR_UNSUPPORTED
+    assert call(mk(dv=136)) == T.TTT_ERR_UNSUPPORTED
+    assert call(mk(B=1 << 16, H=1 << 15)) == T.TTT_ERR_SHAPE
+    assert call(mk(scale=float("nan"))) == T.TTT_ERR_ARG
+    for f in ("in_dtype", "out_dtype"):
+        d = mk()
+        setattr(d, f, 2)
+        assert call(d) == T.TTT_ERR_DTYPE
+    for n in ("q", "k", "v", "beta"):
+        assert call(mk(), **{n: 0}) == T.TTT_ERR_ARG, n
+        assert call(mk(), **{n: (9 << 44) + 8}) == T.TTT_ERR_ALIGN, n
+
+
+def test_delta_fwd_refusals():
+    d = T.make_delta_desc(1, 2, 8, 64, 64)
+    assert _fwd(d, ws_bytes=T.ttt_delta_workspace_bytes(d) - 1) == T.TTT_ERR_WORKSPACE
+    assert _fwd(d, S=0) == T.TTT_ERR_ARG
+    assert _fwd(d, ws=0) == T.TTT_ERR_ARG
+    assert _fwd(d, out=0) == T.TTT_ERR_ARG
+    # overlapping ranges: out on v, out in the middle of q, the state on the workspace
+    assert _fwd(d, out=3 << 40) == T.TTT_ERR_ARG
+    assert _fwd(d, out=(1 << 40) + 256) == T.TTT_ERR_ARG
+    assert _fwd(d, S=8 << 40) == T.TTT_ERR_ARG
+    # N = 0: nothing to do
+    assert _fwd(T.make_delta_desc(1, 2, 0, 64, 64)) == T.TTT_OK
+
+
+def test_delta_bwd_refusals():
+    d = T.make_delta_desc(1, 2, 8, 64, 64)
+    assert _bwd(d, ws_bytes=T.ttt_delta_bwd_workspace_bytes(d) - 1) == T.TTT_ERR_WORKSPACE
+    for n in ("dq", "dk", "dv", "dbeta", "dS0", "dout"):
+        assert _bwd(d, **{n: 0}) == T.TTT_ERR_ARG, n
+    assert _bwd(d, g=0) == T.TTT_ERR_ARG      # dg without g
+    assert _bwd(d, dg=0) == T.TTT_ERR_ARG     # g without dg
+    assert _bwd(d, dq=1 << 40) == T.TTT_ERR_ARG     # dq on q
+    assert _bwd(d, dq=12 << 40) == T.TTT_ERR_ARG    # dq on dk
+
+
+def test_delta_step_refusals():
+    d = T.make_delta_desc(4, 2, 1, 64, 64)
+    assert _step(T.make_delta_desc(4, 2, 2, 64, 64)) == T.TTT_ERR_SHAPE
+    assert _step(T.make_delta_desc(4, 2, 0, 64, 64)) == T.TTT_ERR_SHAPE
+    assert _step(d, n_slots=0) == T.TTT_ERR_SHAPE
+    assert _step(d, n_slots=3, slots=0) == T.TTT_ERR_SHAPE   # row 3 would have no state
+    assert _step(d, S=0) == T.TTT_ERR_ARG
+    assert _step(d, out=6 << 40) == T.TTT_ERR_ARG
+
+
+def test_norm_refusals():
+    mk = lambda **kw: T.make_norm_desc(**{**dict(rows=5, D=64, gate="silu"), **kw})  # noqa: E731
+    for call in (_norm, _norm_bwd):
+        assert call(mk(rows=-1)) == T.TTT_ERR_SHAPE
+        assert call(mk(D=0)) == T.TTT_ERR_SHAPE
+        assert call(mk(D=8200)) == T.TTT_ERR_UNSUPPORTED
+        assert call(mk(D=68)) == T.TTT_ERR_ALIGN
+        assert call(mk(rows=1 << 50)) == T.TTT_ERR_SHAPE
+        assert call(mk(eps=0.0)) == T.TTT_ERR_ARG
+        assert call(mk(eps=float("nan"))) == T.TTT_ERR_ARG
+        assert call(mk(scale=float("nan"))) == T.TTT_ERR_ARG
+        for f in ("kind", "gate"):
+            d = mk()
+            setattr(d, f, 3)
+            assert call(d) == T.TTT_ERR_ARG
+        d = mk()
+        d.dtype = 2
+        assert call(d) == T.TTT_ERR_DTYPE
+        assert call(mk(), x=0) == T.TTT_ERR_ARG
+        assert call(mk(), z=0) == T.TTT_ERR_ARG
+        assert call(mk(gate="none")) == T.TTT_ERR_ARG     # z without a gate
+        assert call(mk(), x=(9 << 44) + 4) == T.TTT_ERR_ALIGN
+    d = mk()
+    assert _norm(d, out=(18 << 40) + 128) == T.TTT_ERR_ARG   # out across x
+    assert _norm(mk(rows=0)) == T.TTT_OK
+    assert _norm_bwd(d, ws_bytes=T.ttt_norm_bwd_workspace_bytes(d) - 1) == T.TTT_ERR_WORKSPACE
+    assert _norm_bwd(d, dw=0) == T.TTT_ERR_ARG
+    assert _norm_bwd(d, w=0) == T.TTT_ERR_ARG
+    assert _norm_bwd(d, dz=0) == T.TTT_ERR_ARG
+    assert _norm_bwd(d, dx=24 << 40) == T.TTT_ERR_ARG        # dx on dz
+
+
+def test_layer_refusals():
+    def call(d, ws_bytes=1 << 39, eps=1e-6, **over):
+        p = _far(**over)
+        names = ("q", "k", "v", "g", "beta", "w", "z", "res", "S", "out", "ws")
+        return T.load().ttt_delta_layer_fwd(ctypes.byref(d), eps, 1.0, *(p[n] for n in names), ws_bytes, None)
+    d = T.make_delta_desc(1, 2, 8, 64, 64)
+    need = T.ttt_delta_layer_workspace_bytes(d)
+    assert need >= T.ttt_delta_workspace_bytes(d) + 3 * 2 * 8 * 64 * 2
+    assert call(d, ws_bytes=need - 1) == T.TTT_ERR_WORKSPACE
+    assert call(d, eps=0.0) == T.TTT_ERR_ARG
+    assert call(d, q=0) == T.TTT_ERR_ARG
+    assert call(d, out=3 << 40) == T.TTT_ERR_ARG
+    assert call(T.make_delta_desc(1, 2, 8, 60, 64)) == T.TTT_ERR_ALIGN
+    assert call(T.make_delta_desc(1, 2, 8, 64, 64, out_dtype="f32")) == T.TTT_ERR_DTYPE
+    assert call(T.make_delta_desc(1, 2, 0, 64, 64)) == T.TTT_OK

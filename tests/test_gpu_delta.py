@@ -1,0 +1,372 @@
+"""GPU parity of the gated delta rule (sequence, gradients, single tokens) with
+the float64 oracle, through the C ABI.
+
+Tolerances, |got - ref| <= r |ref| + s max|ref|:
+  r  half a step of the output's type (bf16 2^-8, float32 2^-24);
+  s  the sums.  Float32 path: a token's e and u are sums over dk products,
+     each rounded to 2^-24 of the running sum, and unit keys with
+     0 <= beta <= 1 make every step a contraction, so the errors of the N
+     tokens add up as independent ones at most: sqrt(dk N) 2^-24, times 8 for
+     the largest of many.  Tensor-core path: every derived operand is bf16 hi +
+     lo, off by at most 2^-17, of which a value's chain meets five (T, W, U, S,
+     and the partner's); dk or 128 products average them, and tokens add up
+     over the memory of the decay, so 8 * 5 * 2^-17 bounds the largest.
+"""
+import numpy as np
+import pytest
+import torch
+
+import learned_linear_attention_b200 as T
+from oracle import delta_backward, delta_recurrent
+
+pytestmark = pytest.mark.gpu
+TYPES = {"f32": torch.float32, "bf16": torch.bfloat16}
+HALF = {"f32": 2.0 ** -24, "bf16": 2.0 ** -8}
+
+
+def tensor_cores(dt, dk, dv):
+    return dt == "bf16" and dk == dv and dk in (64, 128)
+
+
+def tol(dt, dk, dv, N):
+    return 8 * 5 * 2.0 ** -17 if tensor_cores(dt, dk, dv) else 8 * np.sqrt(dk * max(N, 1)) * 2.0 ** -24
+
+
+def near(got, ref, r, s, what=""):
+    got = got.detach().double().cpu().numpy() if torch.is_tensor(got) else np.asarray(got)
+    ref = np.asarray(ref, dtype=np.float64)
+    assert got.shape == ref.shape, what
+    assert np.isfinite(got).all(), what
+    if ref.size == 0:
+        return
+    over = np.abs(got - ref) - (r * np.abs(ref) + s * np.abs(ref).max())
+    assert over.max() <= 0, f"{what}: {np.abs(got - ref).max():.3e} of {np.abs(ref).max():.3e}, over by {over.max():.3e}"
+
+
+class Problem:
+    """Inputs of one call: float64 copies hold the exact values given to the device."""
+
+    def __init__(self, B, H, N, dk, dv, dt, decay=True, start=True, seed=0, g_of=None, beta_of=None):
+        r = np.random.default_rng([B, H, N, dk, dv, seed])
+        self.shape, self.dt, self.decay = (B, H, N, dk, dv), dt, decay
+        k = r.standard_normal((2, B, H, N, dk))
+        k /= np.maximum(np.linalg.norm(k, axis=-1, keepdims=True), 1e-30)
+        g = -np.log1p(np.exp(1.5 * r.standard_normal((B, H, N)) - 4)) if g_of is None else g_of(r, (B, H, N))
+        beta = 1 / (1 + np.exp(-r.standard_normal((B, H, N)))) if beta_of is None else beta_of(r, (B, H, N))
+        raw = dict(q=k[0], k=k[1], v=r.standard_normal((B, H, N, dv)), g=g, beta=beta,
+                   dout=r.standard_normal((B, H, N, dv)))
+        self.dev = {n: torch.from_numpy(np.ascontiguousarray(x)).to(TYPES[dt]).cuda() for n, x in raw.items()}
+        self.S0 = torch.from_numpy(0.3 * r.standard_normal((B, H, dk, dv))).float().cuda() if start else None
+        self.dS = torch.from_numpy(0.3 * r.standard_normal((B, H, dk, dv))).float().cuda() if start else None
+        if not decay:
+            self.dev["g"] = None
+
+    def host(self, n):
+        x = self.dev.get(n) if n in self.dev else getattr(self, n)
+        return None if x is None else x.double().cpu().numpy()
+
+    def desc(self, out=None, N=None, scale=0.0):
+        B, H, n, dk, dv = self.shape
+        return T.make_delta_desc(B, H, n if N is None else N, dk, dv, scale=scale, in_dtype=self.dt,
+                                 out_dtype=out or self.dt)
+
+    def fwd(self, out=None, scale=0.0, stream=None, ws=None):
+        B, H, N, dk, dv = self.shape
+        d = self.desc(out, scale=scale)
+        S = torch.zeros(B, H, dk, dv, device="cuda") if self.S0 is None else self.S0.clone()
+        o = torch.full((B, H, N, dv), float("nan"), dtype=TYPES[out or self.dt], device="cuda")
+        ws = T.alloc_workspace(T.ttt_delta_workspace_bytes(d)) if ws is None else ws
+        x = self.dev
+        T.ttt_delta_fwd(d, x["q"], x["k"], x["v"], x["g"], x["beta"], S, o, ws, stream=stream)
+        assert T.ttt_check_device_status(ws, stream) == T.TTT_OK
+        return o, S
+
+    def new_grads(self):
+        B, H, N, dk, dv = self.shape
+        full = lambda *s, t=TYPES[self.dt]: torch.full(s, float("nan"), dtype=t, device="cuda")  # noqa: E731
+        return [full(B, H, N, dk), full(B, H, N, dk), full(B, H, N, dv), full(B, H, N) if self.decay else None,
+                full(B, H, N), full(B, H, dk, dv, t=torch.float32)]
+
+    def bwd(self, scale=0.0):
+        d, x, outs = self.desc(scale=scale), self.dev, self.new_grads()
+        ws = T.alloc_workspace(T.ttt_delta_bwd_workspace_bytes(d))
+        T.ttt_delta_bwd(d, x["q"], x["k"], x["v"], x["g"], x["beta"], self.S0, x["dout"], self.dS, *outs, ws)
+        assert T.ttt_check_device_status(ws) == T.TTT_OK
+        return outs
+
+    def check_fwd(self, got, out=None, scale=0.0):
+        B, H, N, dk, dv = self.shape
+        ref, S = delta_recurrent(*(self.host(n) for n in ("q", "k", "v", "g", "beta")), self.host("S0"), scale)
+        s = tol(self.dt, dk, dv, N)
+        near(got[0], ref, HALF[out or self.dt], s, "out")
+        near(got[1], S, HALF["f32"], s, "S")
+
+    def check_bwd(self, got, scale=0.0):
+        B, H, N, dk, dv = self.shape
+        ref = delta_backward(*(self.host(n) for n in ("q", "k", "v", "g", "beta", "dout", "S0", "dS")), scale)
+        # the gradients meet the forward's errors and the reverse pass's: twice s
+        s = 2 * tol(self.dt, dk, dv, N)
+        for name, a, b in zip(("dq", "dk", "dv", "dg", "dbeta", "dS0"), got, ref):
+            if b is None:
+                assert a is None
+            elif b.size:
+                near(a, b, HALF["f32" if name == "dS0" else self.dt], s, name)
+
+
+SHAPES = [(1, 1, 1, 64, 64), (1, 2, 1, 128, 128), (2, 3, 77, 24, 40), (1, 2, 130, 64, 64), (2, 1, 128, 128, 128),
+          (1, 1, 300, 128, 128), (1, 3, 257, 64, 64), (1, 1, 64, 1, 1), (1, 1, 33, 128, 3), (1, 2, 50, 5, 128)]
+
+
+@pytest.mark.parametrize("dt", ["f32", "bf16"])
+@pytest.mark.parametrize("shape", SHAPES, ids=str)
+def test_forward(cuda_device, shape, dt):
+    p = Problem(*shape, dt)
+    p.check_fwd(p.fwd())
+
+
+@pytest.mark.parametrize("dt", ["f32", "bf16"])
+@pytest.mark.parametrize("shape", SHAPES, ids=str)
+def test_backward(cuda_device, shape, dt):
+    p = Problem(*shape, dt)
+    p.check_bwd(p.bwd())
+
+
+@pytest.mark.parametrize("dt,dk,dv", [("f32", 16, 24), ("bf16", 64, 64), ("bf16", 128, 128)])
+@pytest.mark.parametrize("decay", [True, False])
+@pytest.mark.parametrize("start", [True, False])
+def test_without_decay_and_without_states(cuda_device, dt, dk, dv, decay, start):
+    p = Problem(1, 2, 200, dk, dv, dt, decay=decay, start=start)
+    p.check_fwd(p.fwd())
+    p.check_bwd(p.bwd())
+
+
+@pytest.mark.parametrize("dt,dk,dv", [("f32", 16, 24), ("bf16", 64, 64), ("bf16", 32, 48)])
+def test_other_output_type_and_scale(cuda_device, dt, dk, dv):
+    p = Problem(1, 2, 150, dk, dv, dt)
+    other = "f32" if dt == "bf16" else "bf16"
+    p.check_fwd(p.fwd(out=other, scale=0.5), out=other, scale=0.5)
+    p.check_bwd(p.bwd(scale=0.5), scale=0.5)
+
+
+GATES = {
+    # a state cleared in the middle of a tile, at its first token, and twice in a row
+    "cleared": dict(g_of=lambda r, s: np.where(np.isin(np.arange(s[-1]), [0, 40, 41, 128, 190]), -np.inf,
+                                               -0.1 * np.abs(r.standard_normal(s)))),
+    # decays so strong that products over a tile leave float32's range
+    "strong": dict(g_of=lambda r, s: -20 * np.abs(r.standard_normal(s))),
+    "full steps": dict(beta_of=lambda r, s: np.ones(s)),
+    # tokens that write nothing, and some with no decay either: padding
+    "no steps": dict(beta_of=lambda r, s: np.where(r.uniform(size=s) < 0.7, 0.0, r.uniform(size=s)),
+                     g_of=lambda r, s: np.where(r.uniform(size=s) < 0.5, 0.0, -0.05)),
+    "beta to two": dict(beta_of=lambda r, s: 2 * r.uniform(size=s) * 0.95),
+}
+
+
+@pytest.mark.parametrize("dt,dk,dv", [("f32", 16, 24), ("bf16", 64, 64), ("bf16", 128, 128)])
+@pytest.mark.parametrize("gates", sorted(GATES))
+def test_gates(cuda_device, gates, dt, dk, dv):
+    p = Problem(1, 2, 260, dk, dv, dt, **GATES[gates])
+    p.check_fwd(p.fwd())
+    p.check_bwd(p.bwd())
+
+
+@pytest.mark.parametrize("d", [64, 128])
+def test_equal_keys(cuda_device, d):
+    """Every key the same, full steps, no decay: (I + A) is the all-ones triangle,
+    whose inverse is bidiagonal; its powers are not bounded, its inverse is."""
+    p = Problem(1, 2, 256, d, d, "bf16", decay=False, beta_of=lambda r, s: np.ones(s))
+    k = torch.zeros(d)
+    k[: d // 16] = (16 / d) ** 0.5      # exact in bf16 for these sizes (0.5, and 2^-1.5 rounded)
+    p.dev["k"] = k.to(torch.bfloat16).cuda().expand(p.dev["k"].shape).contiguous()
+    p.check_fwd(p.fwd())
+    p.check_bwd(p.bwd())
+
+
+@pytest.mark.parametrize("dt,d,cut", [("bf16", 64, 100), ("bf16", 128, 128), ("f32", 40, 33)])
+def test_two_calls_continue_a_sequence(cuda_device, dt, d, cut):
+    p = Problem(2, 2, 300, d, d, dt)
+    ref, _ = delta_recurrent(*(p.host(n) for n in ("q", "k", "v", "g", "beta")), p.host("S0"))
+    S, outs = p.S0.clone(), []
+    for a, b in ((0, cut), (cut, 300)):
+        x = {n: p.dev[n][:, :, a:b].contiguous() for n in ("q", "k", "v", "g", "beta")}
+        o = torch.full((2, 2, b - a, d), float("nan"), dtype=TYPES[dt], device="cuda")
+        desc = p.desc(N=b - a)
+        ws = T.alloc_workspace(T.ttt_delta_workspace_bytes(desc))
+        T.ttt_delta_fwd(desc, x["q"], x["k"], x["v"], x["g"], x["beta"], S, o, ws)
+        assert T.ttt_check_device_status(ws) == T.TTT_OK
+        outs.append(o)
+    near(torch.cat(outs, 2), ref, HALF[dt], tol(dt, d, d, 300))
+
+
+@pytest.mark.parametrize("d", [64, 128])
+def test_long_sequence(cuda_device, d):
+    """Few heads over a long odd sequence (the form that splits it)."""
+    p = Problem(1, 2, 5003, d, d, "bf16")
+    p.check_fwd(p.fwd())
+    p.check_bwd(p.bwd())
+
+
+def test_empty_sequence(cuda_device):
+    for dt, d in (("f32", 24), ("bf16", 64)):
+        p = Problem(1, 2, 0, d, d, dt)
+        assert torch.equal(p.fwd()[1], p.S0)
+        assert torch.equal(p.bwd()[-1], p.dS)
+
+
+@pytest.mark.parametrize("d", [64, 128])
+def test_same_bits_twice_and_after_another_call(cuda_device, d):
+    p, other = Problem(2, 3, 333, d, d, "bf16"), Problem(1, 5, 700, d, d, "bf16", seed=3)
+    ws = T.alloc_workspace(max(T.ttt_delta_workspace_bytes(x.desc()) for x in (p, other)))
+    a = p.fwd(ws=ws)
+    other.fwd(ws=ws)
+    b = p.fwd(ws=ws)
+    assert all(torch.equal(x, y) for x, y in zip(a, b))
+    assert all(torch.equal(x, y) for x, y in zip(p.bwd(), p.bwd()))
+
+
+@pytest.mark.parametrize("dt,d", [("f32", 32), ("bf16", 64), ("bf16", 128)])
+def test_captured_calls_replay(cuda_device, dt, d):
+    """Forward, backward and step in one graph on another stream; replays on new
+    inputs in the same buffers."""
+    p = Problem(1, 2, 200, d, d, dt)
+    want_f, want_b = p.fwd(), p.bwd()
+    desc, x = p.desc(), p.dev
+    S, o, g = p.S0.clone(), torch.empty_like(x["v"]), p.new_grads()
+    ws = T.alloc_workspace(T.ttt_delta_workspace_bytes(desc))
+    wb = T.alloc_workspace(T.ttt_delta_bwd_workspace_bytes(desc))
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.stream(side):
+        graph.capture_begin()
+        S.copy_(p.S0)
+        T.ttt_delta_fwd(desc, x["q"], x["k"], x["v"], x["g"], x["beta"], S, o, ws)
+        T.ttt_delta_bwd(desc, x["q"], x["k"], x["v"], x["g"], x["beta"], p.S0, x["dout"], p.dS, *g, wb)
+        graph.capture_end()
+    torch.cuda.current_stream().wait_stream(side)
+    graph.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(o, want_f[0]) and torch.equal(S, want_f[1])
+    assert all(torch.equal(a, b) for a, b in zip(g, want_b))
+    new = Problem(1, 2, 200, d, d, dt, seed=9)
+    for n in x:
+        x[n].copy_(new.dev[n])
+    p.S0.copy_(new.S0)
+    p.dS.copy_(new.dS)
+    graph.replay()
+    torch.cuda.synchronize()
+    new.check_fwd((o, S))
+    new.check_bwd(g)
+
+
+def test_two_streams_at_once(cuda_device):
+    ps = [Problem(2, 4, 400, d, d, "bf16", seed=d) for d in (64, 128)]
+    want = [p.fwd() for p in ps]
+    streams, got = [torch.cuda.Stream() for _ in ps], []
+    torch.cuda.synchronize()
+    for _ in range(3):
+        got = []
+        for p, s in zip(ps, streams):
+            with torch.cuda.stream(s):
+                got.append(p.fwd())
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for w, g in zip(want, got) for a, b in zip(w, g))
+
+
+# ------------------------------------------------------------------ single tokens
+def step_ref(x, slots, S, n_slots):
+    """Rows in order on a float64 pool."""
+    S = S.copy()
+    B, H, dk = x["k"].shape
+    out = np.full(x["v"].shape, 7.0)
+    for b in range(B):
+        at = int(slots[b])
+        if 0 <= at < n_slots:
+            g = None if x["g"] is None else x["g"][b][None, :, None]
+            o, s = delta_recurrent(x["q"][b][None, :, None], x["k"][b][None, :, None], x["v"][b][None, :, None], g,
+                                   x["beta"][b][None, :, None], S[at][None])
+            S[at], out[b] = s[0], o[0, :, 0]
+    return out, S
+
+
+@pytest.mark.parametrize("dt,dk,dv,B,H", [("f32", 24, 40, 5, 3), ("bf16", 64, 64, 1, 1), ("bf16", 128, 128, 9, 4),
+                                          ("bf16", 128, 128, 70, 16), ("f32", 128, 128, 3, 2), ("bf16", 7, 5, 4, 2),
+                                          ("f32", 1, 1, 2, 1), ("bf16", 128, 67, 3, 2), ("bf16", 128, 36, 300, 2)])
+@pytest.mark.parametrize("kind", ["none", "spread", "idle and shared"])
+@pytest.mark.parametrize("decay", [True, False])
+def test_step(cuda_device, dt, dk, dv, B, H, kind, decay):
+    r = np.random.default_rng([dk, dv, B])
+    p = Problem(B, H, 1, dk, dv, dt, decay=decay)
+    x = {n: None if t is None else t[:, :, 0].contiguous() for n, t in p.dev.items()}
+    n_slots = B + 3
+    if kind == "none":
+        slots, idx = None, np.arange(B)
+    elif kind == "spread":
+        idx = r.permutation(n_slots)[:B]
+    else:   # negative and too large slots, and rows that share one
+        idx = r.integers(-2, max(2, B // 2), B)
+        idx[r.integers(B)] = n_slots
+    if kind != "none":
+        slots = torch.from_numpy(idx.astype(np.int32)).cuda()
+    pool = torch.from_numpy(0.3 * r.standard_normal((n_slots, H, dk, dv))).float().cuda()
+    want = step_ref({n: None if t is None else t.double().cpu().numpy() for n, t in x.items()}, idx,
+                    pool.double().cpu().numpy(), n_slots)
+    out = torch.full((B, H, dv), 7.0, dtype=TYPES[dt], device="cuda")
+    T.ttt_delta_step(p.desc(N=1), x["q"], x["k"], x["v"], x["g"], x["beta"], slots, n_slots, pool, out)
+    s = 8 * np.sqrt(dk * B) * 2.0 ** -24     # a state may take as many as B tokens
+    near(out, want[0], HALF[dt], s, "out")
+    near(pool, want[1], HALF["f32"], s, "S")
+    used = np.isin(np.arange(n_slots), idx)
+    assert np.array_equal(pool.cpu().numpy()[~used], want[1][~used].astype(np.float32))
+
+
+def test_large_pool_offsets(cuda_device):
+    """States beyond 2^32 bytes and 2^31 elements from the pool's start."""
+    H, d, n = 16, 128, 8400            # 8400 * 16 * 128 * 128 = 2.2e9 elements, 8.8 GB
+    pool = torch.empty(n, H, d, d, device="cuda")
+    p = Problem(2, H, 1, d, d, "bf16")
+    x = {m: t[:, :, 0].contiguous() for m, t in p.dev.items()}
+    idx = np.array([n - 1, 4200])
+    pool[torch.from_numpy(idx).cuda()] = 0.25
+    pool[0] = 5.0
+    host = np.full((2, H, d, d), 0.25)
+    want = step_ref({m: t.double().cpu().numpy() for m, t in x.items()}, np.array([0, 1]), host, 2)
+    out = torch.empty(2, H, d, dtype=torch.bfloat16, device="cuda")
+    T.ttt_delta_step(p.desc(N=1), x["q"], x["k"], x["v"], x["g"], x["beta"],
+                     torch.from_numpy(idx.astype(np.int32)).cuda(), n, pool, out)
+    near(out, want[0], HALF["bf16"], 8 * np.sqrt(d) * 2.0 ** -24)
+    near(pool[torch.from_numpy(idx).cuda()], want[1], HALF["f32"], 8 * np.sqrt(d) * 2.0 ** -24)
+    assert bool((pool[0] == 5.0).all())
+
+
+@pytest.mark.parametrize("dt,d", [("bf16", 64), ("bf16", 128), ("f32", 24)])
+def test_prefill_then_single_tokens(cuda_device, dt, d):
+    """A prompt through the sequence form, then tokens one by one on its state,
+    read as one sequence."""
+    p = Problem(2, 3, 150, d, d, dt)
+    ref, Sref = delta_recurrent(*(p.host(n) for n in ("q", "k", "v", "g", "beta")), p.host("S0"))
+    cut, S = 141, p.S0.clone()
+    x = {n: t[:, :, :cut].contiguous() for n, t in p.dev.items()}
+    out = torch.empty(2, 3, cut, d, dtype=TYPES[dt], device="cuda")
+    desc = p.desc(N=cut)
+    ws = T.alloc_workspace(T.ttt_delta_workspace_bytes(desc))
+    T.ttt_delta_fwd(desc, x["q"], x["k"], x["v"], x["g"], x["beta"], S, out, ws)
+    outs = [out]
+    for t in range(cut, 150):
+        x = {n: y[:, :, t].contiguous() for n, y in p.dev.items()}
+        o = torch.empty(2, 3, d, dtype=TYPES[dt], device="cuda")
+        T.ttt_delta_step(p.desc(N=1), x["q"], x["k"], x["v"], x["g"], x["beta"], None, 2, S, o)
+        outs.append(o[:, :, None])
+    s = tol(dt, d, d, 150)
+    near(torch.cat(outs, 2), ref, HALF[dt], s)
+    near(S, Sref, HALF["f32"], s)
+
+
+# ------------------------------------------------------------------ refusals with a device
+def test_memory_of_the_host_is_refused(cuda_device):
+    p = Problem(1, 1, 4, 16, 16, "f32")
+    d, x, S = p.desc(), p.dev, p.S0.clone()
+    ws, out = T.alloc_workspace(T.ttt_delta_workspace_bytes(d)), torch.empty_like(x["v"])
+    assert T.ttt_delta_fwd(d, x["q"].cpu(), x["k"], x["v"], x["g"], x["beta"], S, out, ws, check=False) == T.TTT_ERR_ARG
+    assert T.ttt_delta_fwd(d, x["q"], x["k"], x["v"], x["g"], x["beta"], S, x["v"], ws, check=False) == T.TTT_ERR_ARG
+    assert T.ttt_delta_fwd(d, x["q"], x["k"], x["v"], x["g"], x["beta"], S, out, ws, check=False) == T.TTT_OK
