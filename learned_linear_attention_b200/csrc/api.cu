@@ -312,7 +312,9 @@ int ttt_delta_workspace_bytes(const ttt_delta_desc* d, size_t* bytes) {
   int e = check_delta(d);
   if (e) return e;
   if (!bytes) return TTT_ERR_ARG;
-  *bytes = TTT_STATUS_BYTES;
+  *bytes = delta_uses_umma(d->in_dtype == TTT_BF16, d->dk, d->dv)
+               ? delta_umma_layout(d->B * d->H, d->N, d->dk).total
+               : TTT_STATUS_BYTES;
   return TTT_OK;
 }
 
@@ -336,7 +338,9 @@ int ttt_delta_fwd(const ttt_delta_desc* d, const void* q, const void* k, const v
   e = check_ranges(in, 5, o, 3);
   if (e) return e;
   const DeltaLaunch L = delta_launch(d, q, k, v, g, beta, S, out, ws);
-  return launch_delta_rec(L, as_stream(stream)) == 0 ? TTT_OK : TTT_ERR_CUDA;
+  const int r = delta_uses_umma(L.in_bf16, d->dk, d->dv) ? launch_delta_umma(L, as_stream(stream))
+                                                         : launch_delta_rec(L, as_stream(stream));
+  return r == 0 ? TTT_OK : TTT_ERR_CUDA;
 }
 
 int ttt_delta_bwd_workspace_bytes(const ttt_delta_desc* d, size_t* bytes) {

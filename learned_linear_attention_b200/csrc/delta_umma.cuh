@@ -1,0 +1,151 @@
+// delta_umma.cuh -- shared pieces of the tensor-core kernels of the gated
+// delta rule (bf16, dk = dv = 64 or 128, chunks of 128 tokens).
+//
+// Tiles: [rows][64] bf16 with 128-byte rows and 128-byte swizzle ("atoms");
+// a 128-row atom is 16 KB.  A derived matrix is a pair of atoms rows, hi =
+// bf16(x) and lo = bf16(x - hi): off by at most 2^-17 of the value, where one
+// bf16 alone would be off by 2^-9 and show in the float32 state.
+#pragma once
+
+#include "kernels.h"
+
+namespace ttt {
+namespace dl {
+
+constexpr int C = 128;                  // tokens of a chunk
+constexpr uint32_t ATOM = C * 128;      // bytes of a 128-row atom
+
+// ----------------------------------------------------------------- gates
+// Running sum G of the log decays of a chunk, as hi + lo: hi is a multiple of
+// 2^-9 that float32 holds exactly (|G| <= 128 * 200 < 2^15), so a difference
+// of two sums keeps the precision of its own size and not that of G.  A
+// single log decay is held to +-200 (exp(-200) is 0 in float32), which keeps
+// G finite where a state is cleared; NaN stays.
+struct Gates {
+  float hi[C], lo[C], beta[C];
+};
+template <typename T>
+TTT_DEVICE_INLINE double gate_clamp(T g) {
+  return g < T(-200) ? -200.0 : g > T(200) ? 200.0 : (double)g;
+}
+// by one whole warp; tokens behind n have beta = 0 and no decay
+TTT_DEVICE_INLINE void load_gates(Gates& s, const __nv_bfloat16* g, const __nv_bfloat16* beta, int n,
+                                  int lane) {
+  double x[4], run = 0;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int t = 4 * lane + i;
+    run += (t < n && g != nullptr) ? gate_clamp(__bfloat162float(g[t])) : 0.0;
+    x[i] = run;
+    s.beta[t] = t < n ? __bfloat162float(beta[t]) : 0.f;
+  }
+  double pre = run;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const double y = __shfl_up_sync(0xffffffffu, pre, o);
+    if (lane >= o) pre += y;
+  }
+  pre -= run;
+  // a NaN lane poisons its own difference too; later lanes hold NaN already
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const double G = pre + x[i], h = rint(G * 512.0) / 512.0;
+    s.hi[4 * lane + i] = (float)h;
+    s.lo[4 * lane + i] = (float)(G - h);
+  }
+}
+constexpr float LOG2E = 1.4426950408889634f;
+TTT_DEVICE_INLINE float gate_exp(float d) { return __expf(d); }
+// exp(G_i - G_j)
+TTT_DEVICE_INLINE float gate_ratio(const Gates& s, int i, int j) {
+  return gate_exp((s.hi[i] - s.hi[j]) + (s.lo[i] - s.lo[j]));
+}
+TTT_DEVICE_INLINE float gate_decay(const Gates& s, int i) { return gate_exp(s.hi[i] + s.lo[i]); }
+
+// ----------------------------------------------------------------- hi + lo
+TTT_DEVICE_INLINE void split2(float a, float b, uint32_t& hi, uint32_t& lo) {
+  hi = pack_bf16x2(a, b);
+  lo = pack_bf16x2(a - bf16lo(hi), b - bf16hi(hi));
+}
+// 8 columns (col a multiple of 8) of a row of two atoms
+TTT_DEVICE_INLINE void store8_split(uint32_t hi_atom, uint32_t lo_atom, int row, int col, const float* x) {
+  uint32_t h[4], l[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) split2(x[2 * i], x[2 * i + 1], h[i], l[i]);
+  const uint32_t o = sw128_offset(row, col);
+  st_shared_v4(hi_atom + o, h[0], h[1], h[2], h[3]);
+  st_shared_v4(lo_atom + o, l[0], l[1], l[2], l[3]);
+}
+TTT_DEVICE_INLINE void load8(uint32_t atom, int row, int col, float* x) {
+  uint32_t w[4];
+  ld_shared_v4(atom + sw128_offset(row, col), w[0], w[1], w[2], w[3]);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) { x[2 * i] = bf16lo(w[i]); x[2 * i + 1] = bf16hi(w[i]); }
+}
+TTT_DEVICE_INLINE void load8_split(uint32_t hi_atom, uint32_t lo_atom, int row, int col, float* x) {
+  float l[8];
+  load8(hi_atom, row, col, x);
+  load8(lo_atom, row, col, l);
+#pragma unroll
+  for (int i = 0; i < 8; ++i) x[i] += l[i];
+}
+
+// ----------------------------------------------------------------- products
+// Operands by shared address: K-major (rows are the M or N index, the 64
+// columns of an atom are K; further atoms of K `astride` bytes on) or MN-major
+// (rows are K, the columns M or N; further atoms of M or N `astride` on).
+struct Op {
+  uint32_t addr, astride;
+  bool mn;
+};
+TTT_DEVICE_INLINE uint64_t op_desc(const Op& o, int ks) {   // K step of 16
+  return o.mn ? make_sdesc(o.addr + ks * 2048, o.astride, 1024)
+              : make_sdesc(o.addr + (ks >> 2) * o.astride + (ks & 3) * 32, 16, 1024);
+}
+// D (+)= A B^T over K = 16 * steps; by one thread
+TTT_DEVICE_INLINE void product(uint32_t d, const Op& a, const Op& b, int M, int N, int steps, bool add) {
+  const uint32_t id = make_idesc(M, N, a.mn, b.mn);
+  for (int ks = 0; ks < steps; ++ks) mma_bf16(d, op_desc(a, ks), op_desc(b, ks), id, (add || ks > 0) ? 1u : 0u);
+}
+// the hi + lo pair of an operand: lo is `second` bytes after hi
+struct Pair {
+  Op hi;
+  uint32_t second;
+  TTT_DEVICE_INLINE Op lo() const { return Op{hi.addr + second, hi.astride, hi.mn}; }
+};
+// hi hi + hi lo + lo hi (lo lo is below 2^-17 of the product twice over)
+TTT_DEVICE_INLINE void product3(uint32_t d, const Pair& a, const Pair& b, int M, int N, int steps, bool add) {
+  product(d, a.hi, b.hi, M, N, steps, add);
+  product(d, a.hi, b.lo(), M, N, steps, true);
+  product(d, a.lo(), b.hi, M, N, steps, true);
+}
+
+// ----------------------------------------------------------------- phases
+// A CTA that works in phases: every thread waits for the same barrier and
+// learns whether all of them saw it complete; after a wait that ran out they
+// leave together.
+struct Phase {
+  Waiter W;
+  uint64_t* mma;       // completed by mma_commit, one phase per product group
+  uint32_t parity;
+  TTT_DEVICE_INLINE bool wait(uint64_t* bar, uint32_t par, uint32_t site) const {
+    const bool ok = W.wait(bar, par, site);
+    return __syncthreads_or(!ok) == 0;
+  }
+  TTT_DEVICE_INLINE bool mma_done(uint32_t site) {
+    const bool ok = wait(mma, parity, site);
+    parity ^= 1;
+    tc_fence_after();
+    return ok;
+  }
+  // generic writes of this phase become visible to the tensor cores
+  TTT_DEVICE_INLINE void publish() const {
+    fence_async_smem();
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+  }
+};
+
+}  // namespace dl
+}  // namespace ttt

@@ -299,7 +299,8 @@ __global__ void __launch_bounds__(GTHREADS) delta_chunk_grad_kernel(ChunkArgs<Ti
     double acc = 0;
     for (int i = 0; i < n; ++i) {
       // exp(-200) is 0 in float32: a cleared state keeps G finite
-      acc += p.g != nullptr ? fmax((double)to_f(p.g[tok + i]), -200.0) : 0.0;
+      const float gi = p.g != nullptr ? to_f(p.g[tok + i]) : 0.f;
+      acc += gi < -200.f ? -200.0 : (double)gi;   // NaN stays
       G[i] = acc;
     }
   }
