@@ -182,11 +182,11 @@ int ttt_linear_bwd(const ttt_linear_desc* desc, const void* q, const void* k, co
  * leaves the state as it is.  g, beta: [B, H, N] in the element type of q, k
  * and v.
  *
- * The sequence form with bf16 inputs and dk = dv = 64 or 128 runs on tensor
- * cores in chunks of 128 tokens; every derived operand there is carried as
- * bf16 hi + lo (about 17 significant bits) with float32 sums, and the state
- * stays float32.  Every other type and size, and the gradients, run in
- * float32 on CUDA cores, token by token.
+ * The sequence form and its gradients with bf16 inputs and dk = dv = 64 or
+ * 128 run on tensor cores in chunks of 128 tokens; every derived operand there
+ * is carried as bf16 hi + lo (about 17 significant bits) with float32 sums,
+ * and the state stays float32.  Every other type and size runs in float32 on
+ * CUDA cores, token by token.
  * ---------------------------------------------------------------------- */
 typedef struct {
   int B, H, N;          /* batch, heads, tokens (N >= 0)                     */

@@ -343,11 +343,17 @@ int ttt_delta_fwd(const ttt_delta_desc* d, const void* q, const void* k, const v
   return r == 0 ? TTT_OK : TTT_ERR_CUDA;
 }
 
+// an empty sequence takes the recurrent form, whose kernels hand the states on
+static bool delta_bwd_uses_umma(const ttt_delta_desc* d) {
+  return d->N > 0 && delta_uses_umma(d->in_dtype == TTT_BF16, d->dk, d->dv);
+}
+
 int ttt_delta_bwd_workspace_bytes(const ttt_delta_desc* d, size_t* bytes) {
   int e = check_delta(d);
   if (e) return e;
   if (!bytes) return TTT_ERR_ARG;
-  *bytes = delta_rec_bwd_layout(d->B * d->H, d->N, d->dk, d->dv).total;
+  *bytes = delta_bwd_uses_umma(d) ? delta_umma_bwd_layout(d->B * d->H, d->N, d->dk).total
+                                  : delta_rec_bwd_layout(d->B * d->H, d->N, d->dk, d->dv).total;
   return TTT_OK;
 }
 
@@ -376,8 +382,9 @@ int ttt_delta_bwd(const ttt_delta_desc* d, const void* q, const void* k, const v
   L.S0 = S0; L.dS_end = dS_end; L.dout = dout;
   L.dq = dq; L.dk = dk; L.dv = dv; L.dg = dg; L.dbeta = dbeta; L.dS0 = dS0;
   L.ws = static_cast<uint8_t*>(ws);
-  L.w = delta_rec_bwd_layout(d->B * d->H, d->N, d->dk, d->dv);
-  return launch_delta_rec_bwd(L, as_stream(stream)) == 0 ? TTT_OK : TTT_ERR_CUDA;
+  const int r = delta_bwd_uses_umma(d) ? launch_delta_umma_bwd(L, as_stream(stream))
+                                       : launch_delta_rec_bwd(L, as_stream(stream));
+  return r == 0 ? TTT_OK : TTT_ERR_CUDA;
 }
 
 int ttt_delta_step(const ttt_delta_desc* d, const void* q, const void* k, const void* v,

@@ -160,7 +160,7 @@ struct PrepArgs {
   float* gend;             // [BH nch] exp(G_last)
   float* H;                // [BH nch][D / 64][16][D][4]: columns in groups of four
   __nv_bfloat16* M;        // [BH nch][2][D][D] hi, lo
-  __nv_bfloat16* T;        // nullable: [BH nch][128][128]
+  __nv_bfloat16* T;        // nullable: [BH nch][2][128][128] hi, lo
   int N, nch;
   DevStatus st;
 };
@@ -275,11 +275,16 @@ __global__ void __launch_bounds__(256)
       t[j + 3] = c0 + 3 <= row ? x.w : 0.f;
     }
     if (a.T != nullptr) {
-      uint4* dst = reinterpret_cast<uint4*>(a.T + (ci * C + row) * C + hf * 64);
+      uint4* d0 = reinterpret_cast<uint4*>(a.T + (ci * 2 * C + row) * C + hf * 64);
+      uint4* d1 = reinterpret_cast<uint4*>(a.T + (ci * 2 * C + C + row) * C + hf * 64);
 #pragma unroll
-      for (int j = 0; j < 8; ++j)
-        dst[j] = make_uint4(pack_bf16x2(t[8 * j], t[8 * j + 1]), pack_bf16x2(t[8 * j + 2], t[8 * j + 3]),
-                            pack_bf16x2(t[8 * j + 4], t[8 * j + 5]), pack_bf16x2(t[8 * j + 6], t[8 * j + 7]));
+      for (int j = 0; j < 8; ++j) {
+        uint32_t h[4], l[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) split2(t[8 * j + 2 * i], t[8 * j + 2 * i + 1], h[i], l[i]);
+        d0[j] = make_uint4(h[0], h[1], h[2], h[3]);
+        d1[j] = make_uint4(l[0], l[1], l[2], l[3]);
+      }
     }
     __syncthreads();
     // operand tiles [hi atom 0, hi atom 1, lo atom 0, lo atom 1] of T with scaled columns
@@ -383,11 +388,7 @@ __global__ void __launch_bounds__(256)
       tmem_ld16(tmem + lanes + TM_H + c, h);
       tmem_ld16(tmem + lanes + TM_M + c, m);
       if (!own) continue;
-      float* dh = a.H + ci * D * D + (size_t)(c >> 6) * 64 * D;
-#pragma unroll
-      for (int i = 0; i < 16; i += 4)
-        *reinterpret_cast<float4*>(dh + ((size_t)(((c & 63) + i) >> 2) * D + r) * 4) =
-            make_float4(h[i], h[i + 1], h[i + 2], h[i + 3]);
+      store_h16(a.H + ci * D * D, D, r, c, h);
       uint32_t hi[8], lo[8];
 #pragma unroll
       for (int i = 0; i < 8; ++i) split2(-m[2 * i], -m[2 * i + 1], hi[i], lo[i]);
@@ -417,17 +418,14 @@ __global__ void __launch_bounds__(256)
 }
 
 // ------------------------------------------------------------------ chain
-// X <- e_c X + H_c + Mc X (forward) over the chunks of one head and 64 value
-// columns; X in float32 registers (16 values a thread), its hi + lo copy in
-// shared memory as the operand of the next chunk's product and in the
-// workspace as the chunk's border state.
+// X <- e_c X + H_c + Mc X over the chunks of one head and 64 value columns
+// (backward: Mc^T, from the last chunk); X in float32 registers (16 values a
+// thread), its hi + lo copy in shared memory as the operand of the next
+// chunk's product and in the workspace as the chunk's border state.
 struct ChainArgs {
   const float* gend;
-  const float* H;
-  const float* S_in;       // nullable: zeros
-  float* S_out;
-  __nv_bfloat16* X;        // [BH nch][2][D][D]: the state before each chunk
-  int nch;
+  DeltaChain dir[2];       // forward, backward
+  int nch, BH, first;      // the first CTAs take dir[first]
   DevStatus st;
 };
 
@@ -454,7 +452,10 @@ __global__ void __launch_bounds__(512, 1)
   uint32_t* abort_flag = tmem_slot + 1;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int slice = blockIdx.x % DA;
-  const size_t bh = blockIdx.x / DA, c0 = bh * a.nch;
+  const bool rev = a.first + blockIdx.x / (DA * a.BH) == 1;
+  const DeltaChain& dir = a.dir[rev ? 1 : 0];
+  const size_t bh = blockIdx.x / DA % a.BH, c0 = bh * a.nch;
+  auto chunk = [&](int i) { return c0 + (rev ? a.nch - 1 - i : i); };
 
   if (tid == 0) {
     for (int s = 0; s < STAGES; ++s) mbar_init(&full[s], 1);
@@ -484,7 +485,7 @@ __global__ void __launch_bounds__(512, 1)
     for (int h = 0; h < 2; ++h)
       for (int i = 0; i < DA; ++i)
         tma_load_3d(smem + s * SM::STAGE + (h * DA + i) * SM::SA, &mapM, &full[s], 64 * i, 0,
-                    (int)(2 * (c0 + issued) + h));
+                    (int)(2 * chunk(issued) + h));
     ++issued;
   };
   if (tid == 0)
@@ -493,7 +494,7 @@ __global__ void __launch_bounds__(512, 1)
 #pragma unroll
   for (int j = 0; j < 16; j += 4) {
     float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-    if (own && a.S_in != nullptr) v = *reinterpret_cast<const float4*>(a.S_in + (bh * D + r) * D + col + j);
+    if (own && dir.S_in != nullptr) v = *reinterpret_cast<const float4*>(dir.S_in + (bh * D + r) * D + col + j);
     x[j] = v.x; x[j + 1] = v.y; x[j + 2] = v.z; x[j + 3] = v.w;
   }
   // the operand copy, and the border state of chunk c
@@ -508,29 +509,29 @@ __global__ void __launch_bounds__(512, 1)
       st_shared_v4(sb + SM::X + o, h[i], h[i + 1], h[i + 2], h[i + 3]);
       st_shared_v4(sb + SM::X + SM::SA + o, l[i], l[i + 1], l[i + 2], l[i + 3]);
     }
-    uint4* g0 = reinterpret_cast<uint4*>(a.X + ((c0 + c) * 2 * D + r) * D + col);
-    uint4* g1 = reinterpret_cast<uint4*>(a.X + ((c0 + c) * 2 * D + D + r) * D + col);
+    uint4* g0 = reinterpret_cast<uint4*>(dir.X + (chunk(c) * 2 * D + r) * D + col);
+    uint4* g1 = reinterpret_cast<uint4*>(dir.X + (chunk(c) * 2 * D + D + r) * D + col);
     g0[0] = make_uint4(h[0], h[1], h[2], h[3]);
     g0[1] = make_uint4(h[4], h[5], h[6], h[7]);
     g1[0] = make_uint4(l[0], l[1], l[2], l[3]);
     g1[1] = make_uint4(l[4], l[5], l[6], l[7]);
   };
   auto load_h = [&](int c, float4 (&h)[4]) {
-    const float* p = a.H + (c0 + c) * D * D + (size_t)slice * 64 * D + ((size_t)cg * 4 * D + r) * 4;
+    const float* p = dir.H + chunk(c) * D * D + (size_t)slice * 64 * D + ((size_t)cg * 4 * D + r) * 4;
 #pragma unroll
     for (int j = 0; j < 4; ++j) h[j] = own ? *reinterpret_cast<const float4*>(p + (size_t)j * D * 4) : make_float4(0.f, 0.f, 0.f, 0.f);
   };
   float4 h[4];
   float e = 0.f;
   load_h(0, h);
-  e = a.gend[c0];
+  e = a.gend[chunk(0)];
   for (int c = 0; c < a.nch; ++c) {
     put_x(c);
     ph.publish();
     if (tid == 0) {
       const int s = c % STAGES;
       if (ph.W.wait(&full[s], (c / STAGES) & 1, 1)) {
-        const Pair A{{sb + s * SM::STAGE, SM::SA, false}, DA * SM::SA};
+        const Pair A{{sb + s * SM::STAGE, SM::SA, rev}, DA * SM::SA};
         const Pair B{{sb + SM::X, SM::SA, true}, SM::SA};
         product3(tmem, A, B, D, 64, D / 16, false);
         mma_commit(mma);
@@ -545,7 +546,7 @@ __global__ void __launch_bounds__(512, 1)
     }
     if (c + 1 < a.nch) {
       load_h(c + 1, h);
-      e = a.gend[c0 + c + 1];
+      e = a.gend[chunk(c + 1)];
     }
     if (!ph.mma_done(2)) break;
     float d[16];
@@ -554,8 +555,8 @@ __global__ void __launch_bounds__(512, 1)
     for (int j = 0; j < 16; ++j) x[j] += d[j];
     if (tid == 0) fetch();   // the stage that this chunk's product has read
   }
-  if (!ph.W.aborted() && own) {
-    float* dst = a.S_out + (bh * D + r) * D + col;
+  if (!ph.W.aborted() && own && dir.S_out != nullptr) {
+    float* dst = dir.S_out + (bh * D + r) * D + col;
 #pragma unroll
     for (int j = 0; j < 16; j += 4)
       *reinterpret_cast<float4*>(dst + j) = make_float4(x[j], x[j + 1], x[j + 2], x[j + 3]);
@@ -741,39 +742,65 @@ __global__ void __launch_bounds__(256)
 }
 
 template <int D>
-int launch_fwd(const DeltaLaunch& p, cudaStream_t stream) {
+int prep_launch(const DeltaLaunch& p, const DeltaPrepOut& o, cudaStream_t stream) {
+  const int BH = p.B * p.H, nch = (p.N + C - 1) / C;
+  const uint64_t nc = (uint64_t)BH * nch, rs = D * 2;
+  CUtensorMap mk, mv, mw, mu;
+  if (make_tmap_bf16_3d(&mk, p.k, D, p.N, BH, rs, p.N * rs, 64, C) ||
+      make_tmap_bf16_3d(&mv, p.v, D, p.N, BH, rs, p.N * rs, 64, C) ||
+      make_tmap_bf16_3d(&mw, o.W, D, C, 2 * nc, rs, C * rs, 64, C) ||
+      make_tmap_bf16_3d(&mu, o.U, D, C, 2 * nc, rs, C * rs, 64, C))
+    return -1;
+  static std::atomic<uint64_t> attr{0};
+  if (allow_dynamic_smem(delta_prep_kernel<D>, (int)PrepSmem<D>::TOTAL, attr)) return -1;
+  const PrepArgs a{(const __nv_bfloat16*)p.g, (const __nv_bfloat16*)p.beta, o.gend, o.H, o.M, o.T, p.N, nch, p.st};
+  prof_before(K_DELTA_PREP, stream);
+  delta_prep_kernel<D><<<(unsigned)nc, 256, PrepSmem<D>::TOTAL, stream>>>(mk, mv, mw, mu, a);
+  prof_after(K_DELTA_PREP, stream);
+  return cudaGetLastError() == cudaSuccess ? 0 : -1;
+}
+
+template <int D>
+int chain_launch(const DeltaLaunch& p, const float* gend, const __nv_bfloat16* M, const DeltaChain* fwd,
+                 const DeltaChain* rev, cudaStream_t stream) {
+  const int BH = p.B * p.H, nch = (p.N + C - 1) / C;
+  const uint64_t nc = (uint64_t)BH * nch, rs = D * 2;
+  CUtensorMap mm;
+  if (make_tmap_bf16_3d(&mm, M, D, D, 2 * nc, rs, D * rs, 64, D)) return -1;
+  static std::atomic<uint64_t> attr{0};
+  if (allow_dynamic_smem(delta_chain_kernel<D>, (int)ChainSmem<D>::TOTAL, attr)) return -1;
+  ChainArgs a{gend, {}, nch, BH, fwd ? 0 : 1, p.st};
+  if (fwd) a.dir[0] = *fwd;
+  if (rev) a.dir[1] = *rev;
+  const unsigned dirs = (fwd ? 1 : 0) + (rev ? 1 : 0);
+  prof_before(K_DELTA_CHAIN, stream);
+  delta_chain_kernel<D><<<dirs * (unsigned)(BH * (D / 64)), 512, ChainSmem<D>::TOTAL, stream>>>(mm, a);
+  prof_after(K_DELTA_CHAIN, stream);
+  return cudaGetLastError() == cudaSuccess ? 0 : -1;
+}
+
+template <int D>
+int fwd_launch(const DeltaLaunch& p, cudaStream_t stream) {
   const int BH = p.B * p.H, nch = (p.N + C - 1) / C;
   const DeltaUmmaWorkspace w = delta_umma_layout(BH, p.N, D);
-  const uint64_t nc = (uint64_t)BH * nch;
-  CUtensorMap mq, mk, mv, mw, mu, mm, ms;
-  const uint64_t rs = D * 2;
+  const uint64_t nc = (uint64_t)BH * nch, rs = D * 2;
+  auto bf = [&](size_t at) { return reinterpret_cast<__nv_bfloat16*>(p.ws + at); };
+  auto f32 = [&](size_t at) { return reinterpret_cast<float*>(p.ws + at); };
+  const DeltaPrepOut o{f32(w.gend), f32(w.H), bf(w.W), bf(w.U), bf(w.M), nullptr};
+  const DeltaChain chain{o.H, p.S, p.S, bf(w.X)};
+  if (prep_launch<D>(p, o, stream) || chain_launch<D>(p, o.gend, o.M, &chain, nullptr, stream)) return -1;
+  CUtensorMap mq, mk, mw, mu, ms;
   if (make_tmap_bf16_3d(&mq, p.q, D, p.N, BH, rs, p.N * rs, 64, C) ||
       make_tmap_bf16_3d(&mk, p.k, D, p.N, BH, rs, p.N * rs, 64, C) ||
-      make_tmap_bf16_3d(&mv, p.v, D, p.N, BH, rs, p.N * rs, 64, C) ||
-      make_tmap_bf16_3d(&mw, p.ws + w.W, D, C, 2 * nc, rs, C * rs, 64, C) ||
-      make_tmap_bf16_3d(&mu, p.ws + w.U, D, C, 2 * nc, rs, C * rs, 64, C) ||
-      make_tmap_bf16_3d(&mm, p.ws + w.M, D, D, 2 * nc, rs, D * rs, 64, D) ||
-      make_tmap_bf16_3d(&ms, p.ws + w.X, D, D, 2 * nc, rs, D * rs, 64, D))
+      make_tmap_bf16_3d(&mw, o.W, D, C, 2 * nc, rs, C * rs, 64, C) ||
+      make_tmap_bf16_3d(&mu, o.U, D, C, 2 * nc, rs, C * rs, 64, C) ||
+      make_tmap_bf16_3d(&ms, chain.X, D, D, 2 * nc, rs, D * rs, 64, D))
     return -1;
-  const __nv_bfloat16 *g = (const __nv_bfloat16*)p.g, *beta = (const __nv_bfloat16*)p.beta;
-  float* gend = reinterpret_cast<float*>(p.ws + w.gend);
-  float* H = reinterpret_cast<float*>(p.ws + w.H);
-  static std::atomic<uint64_t> a0{0}, a1{0}, a2{0};
-  if (allow_dynamic_smem(delta_prep_kernel<D>, (int)PrepSmem<D>::TOTAL, a0) ||
-      allow_dynamic_smem(delta_chain_kernel<D>, (int)ChainSmem<D>::TOTAL, a1) ||
-      allow_dynamic_smem(delta_out_kernel<D>, (int)OutSmem<D>::TOTAL, a2))
-    return -1;
-  const PrepArgs pa{g, beta, gend, H, reinterpret_cast<__nv_bfloat16*>(p.ws + w.M), nullptr, p.N, nch, p.st};
-  prof_before(K_DELTA_PREP, stream);
-  delta_prep_kernel<D><<<(unsigned)nc, 256, PrepSmem<D>::TOTAL, stream>>>(mk, mv, mw, mu, pa);
-  prof_after(K_DELTA_PREP, stream);
-  const ChainArgs ca{gend, H, p.S, p.S, reinterpret_cast<__nv_bfloat16*>(p.ws + w.X), nch, p.st};
-  prof_before(K_DELTA_CHAIN, stream);
-  delta_chain_kernel<D><<<(unsigned)(BH * (D / 64)), 512, ChainSmem<D>::TOTAL, stream>>>(mm, ca);
-  prof_after(K_DELTA_CHAIN, stream);
-  const OutArgs oa{g, beta, p.out, p.N, nch, p.out_bf16, p.scale, p.st};
+  static std::atomic<uint64_t> attr{0};
+  if (allow_dynamic_smem(delta_out_kernel<D>, (int)OutSmem<D>::TOTAL, attr)) return -1;
+  const OutArgs a{(const __nv_bfloat16*)p.g, (const __nv_bfloat16*)p.beta, p.out, p.N, nch, p.out_bf16, p.scale, p.st};
   prof_before(K_DELTA_OUT, stream);
-  delta_out_kernel<D><<<(unsigned)(nc * (D / 64)), 256, OutSmem<D>::TOTAL, stream>>>(mq, mk, mw, mu, ms, oa);
+  delta_out_kernel<D><<<(unsigned)(nc * (D / 64)), 256, OutSmem<D>::TOTAL, stream>>>(mq, mk, mw, mu, ms, a);
   prof_after(K_DELTA_OUT, stream);
   return cudaGetLastError() == cudaSuccess ? 0 : -1;
 }
@@ -788,7 +815,7 @@ DeltaUmmaWorkspace delta_umma_layout(int BH, int N, int D) {
   size_t at = 256;
   auto take = [&](size_t bytes) {
     const size_t o = at;
-    at += (bytes + 1023) / 1024 * 1024;
+    at += (bytes + 255) / 256 * 256;
     return o;
   };
   w.gend = take(nc * 4);
@@ -801,8 +828,16 @@ DeltaUmmaWorkspace delta_umma_layout(int BH, int N, int D) {
   return w;
 }
 
+int launch_delta_prep(const DeltaLaunch& p, const DeltaPrepOut& o, cudaStream_t stream) {
+  return p.dk == 64 ? prep_launch<64>(p, o, stream) : prep_launch<128>(p, o, stream);
+}
+int launch_delta_chain(const DeltaLaunch& p, const float* gend, const __nv_bfloat16* M, const DeltaChain* fwd,
+                       const DeltaChain* rev, cudaStream_t stream) {
+  return p.dk == 64 ? chain_launch<64>(p, gend, M, fwd, rev, stream)
+                    : chain_launch<128>(p, gend, M, fwd, rev, stream);
+}
 int launch_delta_umma(const DeltaLaunch& p, cudaStream_t stream) {
-  return p.dk == 64 ? launch_fwd<64>(p, stream) : launch_fwd<128>(p, stream);
+  return p.dk == 64 ? fwd_launch<64>(p, stream) : fwd_launch<128>(p, stream);
 }
 
 }  // namespace ttt

@@ -120,6 +120,19 @@ TTT_DEVICE_INLINE void product3(uint32_t d, const Pair& a, const Pair& b, int M,
   product(d, a.lo(), b.hi, M, N, steps, true);
 }
 
+// ----------------------------------------------------------------- chain layout
+// A [D][D] float32 matrix that the chain kernel adds (its H): 64-column
+// slices, columns in groups of four, so that a row's 16 columns are four
+// 16-byte loads, each whole across the rows of a warp.  Stores 16 columns
+// (c a multiple of 16) of row r.
+TTT_DEVICE_INLINE void store_h16(float* H, int D, int r, int c, const float* h) {
+  float* p = H + (size_t)(c >> 6) * 64 * D;
+#pragma unroll
+  for (int i = 0; i < 16; i += 4)
+    *reinterpret_cast<float4*>(p + ((size_t)(((c & 63) + i) >> 2) * D + r) * 4) =
+        make_float4(h[i], h[i + 1], h[i + 2], h[i + 3]);
+}
+
 // ----------------------------------------------------------------- phases
 // A CTA that works in phases: every thread waits for the same barrier and
 // learns whether all of them saw it complete; after a wait that ran out they
@@ -147,5 +160,63 @@ struct Phase {
   }
 };
 
+// ----------------------------------------------------------------- CTA
+struct Bars {
+  uint64_t load[2], mma;
+  uint32_t tmem, abort;
+};
+// Barriers and `cols` TMEM columns, before the first phase; returns the TMEM base.
+TTT_DEVICE_INLINE uint32_t cta_begin(Bars& b, uint32_t cols, int tid) {
+  if (tid == 0) {
+    mbar_init(&b.load[0], 1);
+    mbar_init(&b.load[1], 1);
+    mbar_init(&b.mma, 1);
+    b.abort = 0;
+    fence_barrier_init();
+  }
+  if (tid >> 5 == 1) {
+    tmem_alloc(&b.tmem, cols);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  return b.tmem;
+}
+// After the last phase, or an aborted one: nothing in flight outlives the CTA.
+// `loads` counts the load barriers in use (thread 0's).
+TTT_DEVICE_INLINE void cta_end(Bars& b, const Phase& ph, int loads, uint32_t tmem, uint32_t cols, int tid) {
+  if (tid == 0) {
+    if (ph.W.aborted()) {
+      for (int i = 0; i < loads; ++i) ph.W.drain(&b.load[i], 0);
+      mma_commit(&b.mma);
+      ph.W.drain(&b.mma, 0);
+      ph.W.drain(&b.mma, 1);
+    }
+    bulk_wait_all();
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (tid >> 5 == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem, cols);
+  }
+}
+
 }  // namespace dl
+
+// ----------------------------------------------------------------- launches shared by both passes
+struct DeltaPrepOut {       // device buffers, per chunk of all heads
+  float *gend, *H;
+  __nv_bfloat16 *W, *U, *M, *T;   // T nullable
+};
+struct DeltaChain {         // one direction of the state recurrence
+  const float *H, *S_in;    // S_in nullable (zeros)
+  float* S_out;             // nullable
+  __nv_bfloat16* X;         // [BH nch][2][D][D] hi, lo: the state at every chunk's start (its end, backward)
+};
+int launch_delta_prep(const DeltaLaunch& p, const DeltaPrepOut& o, cudaStream_t stream);
+// fwd nullable; rev nullable: X <- exp(G_last) X + M^T X + H, from the last chunk
+int launch_delta_chain(const DeltaLaunch& p, const float* gend, const __nv_bfloat16* M, const DeltaChain* fwd,
+                       const DeltaChain* rev, cudaStream_t stream);
 }  // namespace ttt

@@ -1,0 +1,725 @@
+// delta_umma_bwd.cu -- gradients of the gated delta rule on tensor cores:
+// bf16, dk = dv = D = 64 or 128, chunks of 128 tokens.
+//
+// With the chunk's matrices of the forward pass (delta_umma.cu; Gam, gam, rho,
+// T, W, Ut, U, S0 its start state), X1 = dL/dS at its end and P = Gam . Q K^T:
+//   dU = scale P^T dO + rho K X1,   Y = T^T dU          (of T's right-hand side)
+//   X0 = gam_last X1 + Q^T (scale gam dO) - W^T dU
+//      = (gam_last I + Mc^T) X1 + Hb,  Hb = Q^T (scale gam dO) - W^T (scale P^T dO)
+//   dV = beta Y
+//   Mq = Gam . scale dO U^T (j <= i),   Mk = -beta_i Gam . Y U^T (j < i)
+//   dQ = scale gam dO S0^T + Mq K
+//   dK = [Mk K - gam beta Y S0^T] + [Mq^T Q + Mk^T K] + [rho U X1^T]
+//   dbeta_i = Y_i . (V_i - gam_i S0^T k_i) - sum_j Gam_ij (Y_i . U_j) (k_i . k_j)
+// and, with r_i = q_i . dq_i + k_i . ([first] - [second part of dk_i]) and w_i
+// = k_i . [third part],
+//   dg_t = sum_{i >= t} r_i + sum_{i < t} w_i + gam_last <X1, S0>
+// (the last two terms are <X1, S1> less the w_i of i >= t, written so that no
+// large terms cancel).  So the reverse recurrence runs over the same Mc, side
+// by side with the forward one:
+//   delta_prep_kernel      K, V -> W, Ut, T, Mc, Hc
+//   delta_hb_kernel        Q, K, dO, W -> Hb, -scale P^T dO
+//   delta_chain_kernel     S0 and X1 of every chunk, dS0
+//   delta_vals_kernel      U, Y, dV, first part of dbeta; 64 value columns a CTA
+//   delta_keys_kernel      dQ, dK, r, w, second part of dbeta; 64 key columns a CTA
+//   delta_gate_grad_kernel dg, dbeta
+#include <algorithm>
+
+#include "delta_umma.cuh"
+
+namespace ttt {
+
+using namespace dl;
+
+namespace {
+
+constexpr int THREADS = 256;
+
+// Gam_ij m_ij of 16 columns of a row, lower triangle (with the diagonal or without)
+template <bool DIAG>
+TTT_DEVICE_INLINE void weigh16(const Gates& s, int row, int c0, float f, float* x) {
+  const float gh = s.hi[row], gl = s.lo[row];
+#pragma unroll
+  for (int j = 0; j < 16; ++j) {
+    const float d = (gh - s.hi[c0 + j]) + (gl - s.lo[c0 + j]);
+    x[j] = (DIAG ? c0 + j <= row : c0 + j < row) ? f * x[j] * gate_exp(d) : 0.f;
+  }
+}
+TTT_DEVICE_INLINE void zero16(float* x) {
+#pragma unroll
+  for (int j = 0; j < 16; ++j) x[j] = 0.f;
+}
+// 16 columns of a row into a matrix of two column atoms: [hi 0, hi 1, lo 0, lo 1]
+TTT_DEVICE_INLINE void store16_square(uint32_t base, int row, int c0, const float* x) {
+  const uint32_t hi = base + (uint32_t)(c0 >> 6) * ATOM, lo = hi + 2 * ATOM;
+  store8_split(hi, lo, row, c0 & 63, x);
+  store8_split(hi, lo, row, (c0 & 63) + 8, x + 8);
+}
+TTT_DEVICE_INLINE void store_bf16_row32(__nv_bfloat16* p, const float* x) {
+  uint4* dst = reinterpret_cast<uint4*>(p);
+#pragma unroll
+  for (int j = 0; j < 4; ++j)
+    dst[j] = make_uint4(pack_bf16x2(x[8 * j], x[8 * j + 1]), pack_bf16x2(x[8 * j + 2], x[8 * j + 3]),
+                        pack_bf16x2(x[8 * j + 4], x[8 * j + 5]), pack_bf16x2(x[8 * j + 6], x[8 * j + 7]));
+}
+
+struct ChunkId {
+  int slice, t0, n;
+  size_t ci, bh, tok;
+  TTT_DEVICE_INLINE ChunkId(int slices, int nch, int N) {
+    slice = blockIdx.x % slices;
+    ci = blockIdx.x / slices;
+    bh = ci / nch;
+    t0 = (int)(ci % nch) * C;
+    n = min(C, N - t0);
+    tok = bh * N + t0;
+  }
+};
+
+// ------------------------------------------------------------------ Hb
+struct HbArgs {
+  const __nv_bfloat16 *g, *beta;
+  float* H;
+  int N, nch;
+  float scale;
+  DevStatus st;
+};
+
+template <int D>
+struct HbSmem {
+  static constexpr int DA = D / 64;
+  static constexpr uint32_t Q = 0, P = DA * ATOM;             // P over K; then -scale P^T dO, scale gam dO
+  static constexpr uint32_t W = P + 4 * ATOM, DO = W + 2 * DA * ATOM;
+  static constexpr uint32_t GATES = DO + ATOM, BAR = GATES + sizeof(Gates), TOTAL = BAR + 64;
+};
+
+template <int D>
+__global__ void __launch_bounds__(THREADS)
+    delta_hb_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_constant__ CUtensorMap mapK,
+                    const __grid_constant__ CUtensorMap mapD, const __grid_constant__ CUtensorMap mapW,
+                    const __grid_constant__ CUtensorMap mapY, HbArgs a) {
+  using SM = HbSmem<D>;
+  constexpr int DA = D / 64;
+  constexpr uint32_t TM_P = 0, TM_U = 128, TM_H = 192, TM_COLS = 256;
+  extern __shared__ __align__(1024) uint8_t smem[];
+  Bars& bars = *reinterpret_cast<Bars*>(smem + SM::BAR);
+  Gates& gates = *reinterpret_cast<Gates*>(smem + SM::GATES);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const ChunkId id(DA, a.nch, a.N);
+  const uint32_t tmem = cta_begin(bars, TM_COLS, tid), sb = smem_u32(smem);
+  Phase ph{Waiter{&bars.abort, a.st, 1300}, &bars.mma, 0};
+  const int q4 = warp & 3, hf = warp >> 2, row = q4 * 32 + lane;
+  const uint32_t lanes = (uint32_t)(q4 * 32) << 16;
+  if (tid == 0) {
+    mbar_arrive_expect_tx(&bars.load[0], 4 * DA * ATOM + ATOM);
+    for (int i = 0; i < DA; ++i) {
+      tma_load_3d(smem + SM::Q + i * ATOM, &mapQ, &bars.load[0], 64 * i, id.t0, (int)id.bh);
+      tma_load_3d(smem + SM::P + i * ATOM, &mapK, &bars.load[0], 64 * i, id.t0, (int)id.bh);
+      for (int h = 0; h < 2; ++h)
+        tma_load_3d(smem + SM::W + (h * DA + i) * ATOM, &mapW, &bars.load[0], 64 * i, 0, (int)(2 * id.ci + h));
+    }
+    tma_load_3d(smem + SM::DO, &mapD, &bars.load[0], 64 * id.slice, id.t0, (int)id.bh);
+  }
+  if (warp == 2) load_gates(gates, a.g ? a.g + id.tok : nullptr, a.beta + id.tok, id.n, lane);
+  auto work = [&]() {
+    if (!ph.wait(&bars.load[0], 0, 1)) return;
+    const Op dOmn{sb + SM::DO, ATOM, true}, Qmn{sb + SM::Q, ATOM, true};
+    if (tid == 0) {
+      product(tmem + TM_P, Op{sb + SM::Q, ATOM, false}, Op{sb + SM::P, ATOM, false}, 128, 128, D / 16, false);
+      mma_commit(&bars.mma);
+    }
+    if (!ph.mma_done(2)) return;
+#pragma unroll
+    for (int b = 0; b < 4; ++b) {
+      const int c0 = hf * 64 + b * 16;
+      float x[16];
+      if (c0 <= q4 * 32 + 31) {
+        tmem_ld16(tmem + lanes + TM_P + c0, x);
+        weigh16<true>(gates, row, c0, 1.f, x);
+      } else {
+        zero16(x);
+      }
+      store16_square(sb + SM::P, row, c0, x);
+    }
+    ph.publish();
+    if (tid == 0) {
+      const Pair Pt{{sb + SM::P, ATOM, true}, 2 * ATOM};
+      product(tmem + TM_U, Pt.hi, dOmn, 128, 64, 8, false);
+      product(tmem + TM_U, Pt.lo(), dOmn, 128, 64, 8, true);
+      mma_commit(&bars.mma);
+    }
+    if (!ph.mma_done(3)) return;
+    {
+      float u[32];
+      tmem_ld32(tmem + lanes + TM_U + hf * 32, u);
+      const float f = a.scale * gate_decay(gates, row);
+#pragma unroll
+      for (int j = 0; j < 32; j += 8) {
+        float d[8];
+        load8(sb + SM::DO, row, hf * 32 + j, d);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          u[j + i] *= -a.scale;
+          d[i] *= f;
+        }
+        store8_split(sb + SM::P, sb + SM::P + ATOM, row, hf * 32 + j, u + j);
+        store8_split(sb + SM::P + 2 * ATOM, sb + SM::P + 3 * ATOM, row, hf * 32 + j, d);
+      }
+    }
+    ph.publish();
+    if (tid == 0) {
+      const Pair U{{sb + SM::P, ATOM, true}, ATOM}, G{{sb + SM::P + 2 * ATOM, ATOM, true}, ATOM};
+      const Pair Wt{{sb + SM::W, ATOM, true}, DA * ATOM};
+      product(tmem + TM_H, Qmn, G.hi, D, 64, 8, false);
+      product(tmem + TM_H, Qmn, G.lo(), D, 64, 8, true);
+      product3(tmem + TM_H, Wt, U, D, 64, 8, true);
+      mma_commit(&bars.mma);
+      for (int h = 0; h < 2; ++h)
+        tma_store_3d(&mapY, smem + SM::P + h * ATOM, 64 * id.slice, 0, (int)(2 * id.ci + h));
+      bulk_commit();
+    }
+    if (!ph.mma_done(4)) return;
+    const int r = D == 64 ? q4 * 16 + lane : row;
+#pragma unroll
+    for (int j = 0; j < 32; j += 16) {
+      float h[16];
+      tmem_ld16(tmem + lanes + TM_H + hf * 32 + j, h);
+      if (D == 128 || lane < 16) store_h16(a.H + id.ci * D * D, D, r, id.slice * 64 + hf * 32 + j, h);
+    }
+  };
+  work();
+  cta_end(bars, ph, 1, tmem, TM_COLS, tid);
+}
+
+// ------------------------------------------------------------------ values
+struct ValsArgs {
+  const __nv_bfloat16 *g, *beta, *v;
+  __nv_bfloat16* dv;
+  float* bpart;            // [D / 64][BH N]
+  int N, nch;
+  size_t tokens;
+  DevStatus st;
+};
+
+template <int D>
+struct ValsSmem {
+  static constexpr int DA = D / 64;
+  static constexpr uint32_t SA = D * 128;
+  static constexpr uint32_t T = 0;                            // W first
+  static constexpr uint32_t K = 4 * ATOM, S = K + DA * ATOM, X = S + 2 * SA, U = X + 2 * SA, Y = U + 2 * ATOM;
+  static constexpr uint32_t GATES = Y + 2 * ATOM, RED = GATES + sizeof(Gates), BAR = RED + C * 4, TOTAL = BAR + 64;
+};
+
+template <int D>
+__global__ void __launch_bounds__(THREADS)
+    delta_vals_kernel(const __grid_constant__ CUtensorMap mapK, const __grid_constant__ CUtensorMap mapW,
+                      const __grid_constant__ CUtensorMap mapU, const __grid_constant__ CUtensorMap mapY,
+                      const __grid_constant__ CUtensorMap mapT, const __grid_constant__ CUtensorMap mapS,
+                      const __grid_constant__ CUtensorMap mapX, ValsArgs a) {
+  using SM = ValsSmem<D>;
+  constexpr int DA = D / 64;
+  constexpr uint32_t TM_W = 0, TM_Z = 64, TM_X = 128, TM_Y = 192, TM_COLS = 256;
+  extern __shared__ __align__(1024) uint8_t smem[];
+  Bars& bars = *reinterpret_cast<Bars*>(smem + SM::BAR);
+  Gates& gates = *reinterpret_cast<Gates*>(smem + SM::GATES);
+  float* red = reinterpret_cast<float*>(smem + SM::RED);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const ChunkId id(DA, a.nch, a.N);
+  const uint32_t tmem = cta_begin(bars, TM_COLS, tid), sb = smem_u32(smem);
+  Phase ph{Waiter{&bars.abort, a.st, 1400}, &bars.mma, 0};
+  const int q4 = warp & 3, hf = warp >> 2, row = q4 * 32 + lane;
+  const uint32_t lanes = (uint32_t)(q4 * 32) << 16;
+  if (tid == 0) {
+    mbar_arrive_expect_tx(&bars.load[0], 3 * DA * ATOM + 4 * ATOM + 4 * SM::SA);
+    for (int i = 0; i < DA; ++i) {
+      tma_load_3d(smem + SM::K + i * ATOM, &mapK, &bars.load[0], 64 * i, id.t0, (int)id.bh);
+      for (int h = 0; h < 2; ++h)
+        tma_load_3d(smem + SM::T + (h * DA + i) * ATOM, &mapW, &bars.load[0], 64 * i, 0, (int)(2 * id.ci + h));
+    }
+    for (int h = 0; h < 2; ++h) {
+      const int z = (int)(2 * id.ci + h), x = 64 * id.slice;
+      tma_load_3d(smem + SM::S + h * SM::SA, &mapS, &bars.load[0], x, 0, z);
+      tma_load_3d(smem + SM::X + h * SM::SA, &mapX, &bars.load[0], x, 0, z);
+      tma_load_3d(smem + SM::U + h * ATOM, &mapU, &bars.load[0], x, 0, z);
+      tma_load_3d(smem + SM::Y + h * ATOM, &mapY, &bars.load[0], x, 0, z);
+    }
+  }
+  if (warp == 2) load_gates(gates, a.g ? a.g + id.tok : nullptr, a.beta + id.tok, id.n, lane);
+  int loads = 1;
+  auto work = [&]() {
+    if (!ph.wait(&bars.load[0], 0, 1)) return;
+    const Op K{sb + SM::K, ATOM, false};
+    const Pair W{{sb + SM::T, ATOM, false}, DA * ATOM};
+    const Pair S{{sb + SM::S, SM::SA, true}, SM::SA}, X{{sb + SM::X, SM::SA, true}, SM::SA};
+    if (tid == 0) {
+      product3(tmem + TM_W, W, S, 128, 64, D / 16, false);
+      product(tmem + TM_Z, K, S.hi, 128, 64, D / 16, false);
+      product(tmem + TM_Z, K, S.lo(), 128, 64, D / 16, true);
+      product(tmem + TM_X, K, X.hi, 128, 64, D / 16, false);
+      product(tmem + TM_X, K, X.lo(), 128, 64, D / 16, true);
+      mma_commit(&bars.mma);
+    }
+    if (!ph.mma_done(2)) return;
+    if (tid == 0) {   // T takes W's place
+      mbar_arrive_expect_tx(&bars.load[1], 4 * ATOM);
+      for (int h = 0; h < 2; ++h)
+        for (int i = 0; i < 2; ++i)
+          tma_load_3d(smem + SM::T + (2 * h + i) * ATOM, &mapT, &bars.load[1], 64 * i, 0, (int)(2 * id.ci + h));
+    }
+    loads = 2;
+    // U = Ut - W S0, dU = rho K X1 - (-scale P^T dO), both in place
+    {
+      const float rho = gate_ratio(gates, C - 1, row);
+#pragma unroll
+      for (int j = 0; j < 32; j += 16) {
+        const int c = hf * 32 + j;
+        float w[16], x[16], u[16], y[16];
+        tmem_ld16(tmem + lanes + TM_W + c, w);
+        tmem_ld16(tmem + lanes + TM_X + c, x);
+#pragma unroll
+        for (int b = 0; b < 16; b += 8) {
+          load8_split(sb + SM::U, sb + SM::U + ATOM, row, c + b, u + b);
+          load8_split(sb + SM::Y, sb + SM::Y + ATOM, row, c + b, y + b);
+        }
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+          u[i] -= w[i];
+          y[i] = fmaf(rho, x[i], -y[i]);
+        }
+#pragma unroll
+        for (int b = 0; b < 16; b += 8) {
+          store8_split(sb + SM::U, sb + SM::U + ATOM, row, c + b, u + b);
+          store8_split(sb + SM::Y, sb + SM::Y + ATOM, row, c + b, y + b);
+        }
+      }
+    }
+    ph.publish();
+    if (tid == 0) {
+      for (int h = 0; h < 2; ++h)
+        tma_store_3d(&mapU, smem + SM::U + h * ATOM, 64 * id.slice, 0, (int)(2 * id.ci + h));
+      bulk_commit();
+      if (ph.W.wait(&bars.load[1], 0, 3)) {
+        const Pair Tt{{sb + SM::T, ATOM, true}, 2 * ATOM}, dU{{sb + SM::Y, ATOM, true}, ATOM};
+        product3(tmem + TM_Y, Tt, dU, 128, 64, 8, false);
+        mma_commit(&bars.mma);
+      }
+    }
+    if (!ph.mma_done(4)) return;
+    float acc = 0.f;
+    {
+      const float beta = gates.beta[row], gam = gate_decay(gates, row);
+      const size_t at = (id.tok + row) * D + id.slice * 64 + hf * 32;
+      float y[32], z[32];
+      tmem_ld32(tmem + lanes + TM_Y + hf * 32, y);
+      tmem_ld32(tmem + lanes + TM_Z + hf * 32, z);
+#pragma unroll
+      for (int j = 0; j < 32; j += 8) store8_split(sb + SM::Y, sb + SM::Y + ATOM, row, hf * 32 + j, y + j);
+      if (row < id.n) {
+        const uint4* vp = reinterpret_cast<const uint4*>(a.v + at);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const uint4 t = vp[j];
+          const uint32_t w[4] = {t.x, t.y, t.z, t.w};
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            acc = fmaf(y[8 * j + 2 * i], bf16lo(w[i]) - gam * z[8 * j + 2 * i], acc);
+            acc = fmaf(y[8 * j + 2 * i + 1], bf16hi(w[i]) - gam * z[8 * j + 2 * i + 1], acc);
+          }
+        }
+#pragma unroll
+        for (int j = 0; j < 32; ++j) y[j] *= beta;
+        store_bf16_row32(a.dv + at, y);
+      }
+      if (hf == 1) red[row] = acc;
+    }
+    ph.publish();
+    if (tid == 0) {
+      for (int h = 0; h < 2; ++h)
+        tma_store_3d(&mapY, smem + SM::Y + h * ATOM, 64 * id.slice, 0, (int)(2 * id.ci + h));
+      bulk_commit();
+    }
+    if (hf == 0 && row < id.n) a.bpart[id.slice * a.tokens + id.tok + row] = acc + red[row];
+  };
+  work();
+  cta_end(bars, ph, loads, tmem, TM_COLS, tid);
+}
+
+// ------------------------------------------------------------------ keys
+struct KeysArgs {
+  const __nv_bfloat16 *g, *beta;
+  __nv_bfloat16 *dq, *dk;
+  float *rpart, *wpart;    // [D / 64][BH N]
+  float* xpart;            // [D / 64][BH nch]: <X1, S0>
+  float* bkey;             // [BH N]
+  int N, nch;
+  size_t tokens, chunks;
+  float scale;
+  DevStatus st;
+};
+
+template <int D>
+struct KeysSmem {
+  static constexpr int DA = D / 64;
+  static constexpr uint32_t HA = 64 * 128;                    // a [64][64] atom
+  static constexpr uint32_t DO = 0, MQ = DA * ATOM;           // MQ over S0 and X1 (rows of this slice)
+  static constexpr uint32_t S = MQ, X = S + 2 * DA * HA;
+  static constexpr uint32_t U = MQ + 4 * ATOM;                // then Mk
+  static constexpr uint32_t Y = U + 4 * ATOM;                 // then K, Q (this slice)
+  static constexpr uint32_t YB = 2 * DA * ATOM;
+  static constexpr uint32_t GATES = Y + YB, RED = GATES + sizeof(Gates), BAR = RED + 1024, TOTAL = BAR + 64;
+};
+
+template <int D>
+__global__ void __launch_bounds__(THREADS)
+    delta_keys_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_constant__ CUtensorMap mapK,
+                      const __grid_constant__ CUtensorMap mapD, const __grid_constant__ CUtensorMap mapU,
+                      const __grid_constant__ CUtensorMap mapY, const __grid_constant__ CUtensorMap mapS,
+                      const __grid_constant__ CUtensorMap mapX, KeysArgs a) {
+  using SM = KeysSmem<D>;
+  constexpr int DA = D / 64;
+  constexpr uint32_t TM_P = 0, TM_A = 128, TM_QS = 256, TM_YS = 320, TM_UX = 384, TM_KW = 448, TM_COLS = 512;
+  constexpr uint32_t TM_QK = TM_A, TM_KR = TM_A + 64;
+  extern __shared__ __align__(1024) uint8_t smem[];
+  Bars& bars = *reinterpret_cast<Bars*>(smem + SM::BAR);
+  Gates& gates = *reinterpret_cast<Gates*>(smem + SM::GATES);
+  float* red = reinterpret_cast<float*>(smem + SM::RED);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const ChunkId id(DA, a.nch, a.N);
+  const uint32_t tmem = cta_begin(bars, TM_COLS, tid), sb = smem_u32(smem);
+  Phase ph{Waiter{&bars.abort, a.st, 1500}, &bars.mma, 0};
+  const int q4 = warp & 3, hf = warp >> 2, row = q4 * 32 + lane;
+  const uint32_t lanes = (uint32_t)(q4 * 32) << 16;
+  if (tid == 0) {
+    mbar_arrive_expect_tx(&bars.load[0], 5 * DA * ATOM + 4 * DA * SM::HA);
+    for (int i = 0; i < DA; ++i) {
+      tma_load_3d(smem + SM::DO + i * ATOM, &mapD, &bars.load[0], 64 * i, id.t0, (int)id.bh);
+      for (int h = 0; h < 2; ++h) {
+        const int z = (int)(2 * id.ci + h);
+        tma_load_3d(smem + SM::U + (h * DA + i) * ATOM, &mapU, &bars.load[0], 64 * i, 0, z);
+        tma_load_3d(smem + SM::Y + (h * DA + i) * ATOM, &mapY, &bars.load[0], 64 * i, 0, z);
+        tma_load_3d(smem + SM::S + (h * DA + i) * SM::HA, &mapS, &bars.load[0], 64 * i, 64 * id.slice, z);
+        tma_load_3d(smem + SM::X + (h * DA + i) * SM::HA, &mapX, &bars.load[0], 64 * i, 64 * id.slice, z);
+      }
+    }
+  }
+  if (warp == 2) load_gates(gates, a.g ? a.g + id.tok : nullptr, a.beta + id.tok, id.n, lane);
+  int loads = 1;
+  auto work = [&]() {
+    if (!ph.wait(&bars.load[0], 0, 1)) return;
+    if (tid == 0) {
+      const Op dO{sb + SM::DO, ATOM, false};
+      const Pair U{{sb + SM::U, ATOM, false}, DA * ATOM}, Y{{sb + SM::Y, ATOM, false}, DA * ATOM};
+      const Pair S{{sb + SM::S, SM::HA, false}, DA * SM::HA}, X{{sb + SM::X, SM::HA, false}, DA * SM::HA};
+      product(tmem + TM_P, dO, U.hi, 128, 128, D / 16, false);
+      product(tmem + TM_P, dO, U.lo(), 128, 128, D / 16, true);
+      product3(tmem + TM_A, Y, U, 128, 128, D / 16, false);
+      product(tmem + TM_QS, dO, S.hi, 128, 64, D / 16, false);
+      product(tmem + TM_QS, dO, S.lo(), 128, 64, D / 16, true);
+      product3(tmem + TM_YS, Y, S, 128, 64, D / 16, false);
+      product3(tmem + TM_UX, U, X, 128, 64, D / 16, false);
+      mma_commit(&bars.mma);
+    }
+    {   // <X1, S0> of this slice's rows, while they are still here
+      float acc = 0.f;
+      for (int e = tid; e < 64 * D / 8; e += THREADS) {
+        const int r = e / (D / 8), c = e % (D / 8) * 8;
+        const uint32_t at = (uint32_t)(c >> 6) * SM::HA;
+        float s[8], x[8];
+        load8_split(sb + SM::S + at, sb + SM::S + DA * SM::HA + at, r, c & 63, s);
+        load8_split(sb + SM::X + at, sb + SM::X + DA * SM::HA + at, r, c & 63, x);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) acc = fmaf(s[i], x[i], acc);
+      }
+      for (int o = 16; o > 0; o >>= 1) acc += __shfl_xor_sync(0xffffffffu, acc, o);
+      if (lane == 0) red[warp] = acc;
+    }
+    if (!ph.mma_done(2)) return;
+    if (tid == 0) {   // K and Q take Y's place
+      mbar_arrive_expect_tx(&bars.load[1], (DA + 1) * ATOM);
+      for (int i = 0; i < DA; ++i)
+        tma_load_3d(smem + SM::Y + i * ATOM, &mapK, &bars.load[1], 64 * i, id.t0, (int)id.bh);
+      tma_load_3d(smem + SM::Y + DA * ATOM, &mapQ, &bars.load[1], 64 * id.slice, id.t0, (int)id.bh);
+      float acc = 0.f;
+      for (int w = 0; w < THREADS / 32; ++w) acc += red[w];
+      a.xpart[id.slice * a.chunks + id.ci] = acc;
+    }
+    loads = 2;
+#pragma unroll
+    for (int b = 0; b < 4; ++b) {
+      const int c0 = hf * 64 + b * 16;
+      float x[16];
+      if (c0 <= q4 * 32 + 31) {
+        tmem_ld16(tmem + lanes + TM_P + c0, x);
+        weigh16<true>(gates, row, c0, a.scale, x);
+      } else {
+        zero16(x);
+      }
+      store16_square(sb + SM::MQ, row, c0, x);
+    }
+    ph.publish();
+    const Op K{sb + SM::Y, ATOM, false};
+    if (tid == 0) {
+      if (ph.W.wait(&bars.load[1], 0, 3)) {
+        product(tmem + TM_P, K, K, 128, 128, D / 16, false);
+        mma_commit(&bars.mma);
+      }
+    }
+    if (!ph.mma_done(4)) return;
+    // Mk, and its row sums against k_i . k_j without beta
+    float db = 0.f;
+    const float beta = gates.beta[row];
+#pragma unroll
+    for (int b = 0; b < 4; ++b) {
+      const int c0 = hf * 64 + b * 16;
+      float x[16];
+      if (c0 <= q4 * 32 + 31) {
+        float kk[16];
+        tmem_ld16(tmem + lanes + TM_A + c0, x);
+        tmem_ld16(tmem + lanes + TM_P + c0, kk);
+        weigh16<false>(gates, row, c0, -1.f, x);
+#pragma unroll
+        for (int j = 0; j < 16; ++j) {
+          if (c0 + j < row) db = fmaf(x[j], kk[j], db);
+          x[j] *= beta;
+        }
+      } else {
+        zero16(x);
+      }
+      store16_square(sb + SM::U, row, c0, x);
+    }
+    if (hf == 1) red[row] = db;
+    ph.publish();
+    const Op Kmn{sb + SM::Y + id.slice * ATOM, ATOM, true}, Qmn{sb + SM::Y + DA * ATOM, ATOM, true};
+    if (tid == 0) {
+      const Pair Mq{{sb + SM::MQ, ATOM, false}, 2 * ATOM}, Mk{{sb + SM::U, ATOM, false}, 2 * ATOM};
+      const Pair Mqt{{sb + SM::MQ, ATOM, true}, 2 * ATOM}, Mkt{{sb + SM::U, ATOM, true}, 2 * ATOM};
+      product(tmem + TM_QK, Mq.hi, Kmn, 128, 64, 8, false);
+      product(tmem + TM_QK, Mq.lo(), Kmn, 128, 64, 8, true);
+      product(tmem + TM_KR, Mk.hi, Kmn, 128, 64, 8, false);
+      product(tmem + TM_KR, Mk.lo(), Kmn, 128, 64, 8, true);
+      product(tmem + TM_KW, Mqt.hi, Qmn, 128, 64, 8, false);
+      product(tmem + TM_KW, Mqt.lo(), Qmn, 128, 64, 8, true);
+      product(tmem + TM_KW, Mkt.hi, Kmn, 128, 64, 8, true);
+      product(tmem + TM_KW, Mkt.lo(), Kmn, 128, 64, 8, true);
+      mma_commit(&bars.mma);
+    }
+    if (hf == 0 && id.slice == 0 && row < id.n) a.bkey[id.tok + row] = db + red[row];
+    if (!ph.mma_done(5)) return;
+    const float gam = gate_decay(gates, row), rho = gate_ratio(gates, C - 1, row);
+    const float fq = a.scale * gam, fy = -gam * beta;
+    const size_t at = (id.tok + row) * D + id.slice * 64 + hf * 32;
+    float rs = 0.f, ws = 0.f;
+#pragma unroll
+    for (int j = 0; j < 32; j += 16) {
+      const int c = hf * 32 + j;
+      float x[16], y[16], t[16];
+      // dq
+      tmem_ld16(tmem + lanes + TM_QS + c, x);
+      tmem_ld16(tmem + lanes + TM_QK + c, y);
+      load8(sb + SM::Y + DA * ATOM, row, c, t);
+      load8(sb + SM::Y + DA * ATOM, row, c + 8, t + 8);
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        x[i] = fmaf(fq, x[i], y[i]);
+        rs = fmaf(t[i], x[i], rs);
+      }
+      if (row < id.n) {
+        uint4* d = reinterpret_cast<uint4*>(a.dq + at + j);
+        d[0] = make_uint4(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]), pack_bf16x2(x[4], x[5]), pack_bf16x2(x[6], x[7]));
+        d[1] = make_uint4(pack_bf16x2(x[8], x[9]), pack_bf16x2(x[10], x[11]), pack_bf16x2(x[12], x[13]), pack_bf16x2(x[14], x[15]));
+      }
+      // dk: read part less the second one for rs, third for ws
+      load8(sb + SM::Y + id.slice * ATOM, row, c, t);
+      load8(sb + SM::Y + id.slice * ATOM, row, c + 8, t + 8);
+      float z[16];
+      tmem_ld16(tmem + lanes + TM_KR + c, x);
+      tmem_ld16(tmem + lanes + TM_YS + c, y);
+      tmem_ld16(tmem + lanes + TM_KW + c, z);
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        x[i] = fmaf(fy, y[i], x[i]);
+        rs = fmaf(t[i], x[i] - z[i], rs);
+        x[i] += z[i];
+      }
+      tmem_ld16(tmem + lanes + TM_UX + c, y);
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        const float w = rho * y[i];
+        ws = fmaf(t[i], w, ws);
+        x[i] += w;
+      }
+      if (row < id.n) {
+        uint4* d = reinterpret_cast<uint4*>(a.dk + at + j);
+        d[0] = make_uint4(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]), pack_bf16x2(x[4], x[5]), pack_bf16x2(x[6], x[7]));
+        d[1] = make_uint4(pack_bf16x2(x[8], x[9]), pack_bf16x2(x[10], x[11]), pack_bf16x2(x[12], x[13]), pack_bf16x2(x[14], x[15]));
+      }
+    }
+    if (hf == 1) {
+      red[row] = rs;
+      red[C + row] = ws;
+    }
+    __syncthreads();
+    if (hf == 0 && row < id.n) {
+      const size_t o = id.slice * a.tokens + id.tok + row;
+      a.rpart[o] = rs + red[row];
+      a.wpart[o] = ws + red[C + row];
+    }
+  };
+  work();
+  cta_end(bars, ph, loads, tmem, TM_COLS, tid);
+}
+
+// ------------------------------------------------------------------ gates
+struct GateArgs {
+  const float *gend, *rpart, *wpart, *xpart, *bpart, *bkey;
+  __nv_bfloat16 *dg, *dbeta;   // dg nullable
+  int N, nch, slices;
+  size_t tokens, chunks;
+};
+
+TTT_DEVICE_INLINE float sum_below(float x, float* buf, int tid, float& total) {   // over threads 0..tid-1 of 128
+  float pre = x;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const float y = __shfl_up_sync(0xffffffffu, pre, o);
+    if ((tid & 31) >= o) pre += y;
+  }
+  if ((tid & 31) == 31) buf[tid >> 5] = pre;
+  __syncthreads();
+  float base = 0.f;
+  total = 0.f;
+#pragma unroll
+  for (int w = 0; w < C / 32; ++w) {
+    if (w < tid >> 5) base += buf[w];
+    total += buf[w];
+  }
+  __syncthreads();
+  // the shifted lane, not pre - x: that would cancel
+  const float y = __shfl_up_sync(0xffffffffu, pre, 1);
+  return base + ((tid & 31) ? y : 0.f);
+}
+
+__global__ void __launch_bounds__(C) delta_gate_grad_kernel(GateArgs a) {
+  __shared__ float buf[C / 32];
+  const int tid = threadIdx.x;
+  const size_t ci = blockIdx.x, bh = ci / a.nch;
+  const int t0 = (int)(ci % a.nch) * C, n = min(C, a.N - t0);
+  const size_t tok = bh * a.N + t0;
+  const bool live = tid < n;
+  float r = 0.f, w = 0.f, b = 0.f, x = 0.f;
+  for (int s = 0; s < a.slices; ++s) {
+    const size_t at = s * a.tokens + tok + tid;
+    if (live) {
+      r += a.rpart[at];
+      w += a.wpart[at];
+      b += a.bpart[at];
+    }
+    x += a.xpart[s * a.chunks + ci];
+  }
+  if (live) a.dbeta[tok + tid] = __float2bfloat16_rn(b + a.bkey[tok + tid]);
+  if (a.dg == nullptr) return;
+  // the sum over i >= t is a prefix sum of the reversed order
+  __shared__ float rev[C];
+  rev[C - 1 - tid] = r;
+  __syncthreads();
+  float total, wt;
+  const float below = sum_below(rev[tid], buf, tid, total) + rev[tid];
+  const float wpre = sum_below(w, buf, tid, wt);
+  rev[tid] = below;   // every thread has read its own entry
+  __syncthreads();
+  if (live) a.dg[tok + tid] = __float2bfloat16_rn(rev[C - 1 - tid] + wpre + a.gend[ci] * x);
+}
+
+template <int D>
+int bwd_launch(const DeltaBwdLaunch& L, cudaStream_t stream) {
+  const DeltaLaunch& p = L.f;
+  const int BH = p.B * p.H, nch = (p.N + C - 1) / C;
+  constexpr int DA = D / 64;
+  const DeltaUmmaBwdWorkspace w = delta_umma_bwd_layout(BH, p.N, D);
+  const uint64_t nc = (uint64_t)BH * nch, rs = D * 2;
+  const size_t tokens = (size_t)BH * p.N;
+  auto bf = [&](size_t at) { return reinterpret_cast<__nv_bfloat16*>(L.ws + at); };
+  auto f32 = [&](size_t at) { return reinterpret_cast<float*>(L.ws + at); };
+  const __nv_bfloat16 *g = (const __nv_bfloat16*)p.g, *beta = (const __nv_bfloat16*)p.beta;
+  const DeltaPrepOut o{f32(w.gend), f32(w.H), bf(w.W), bf(w.U), bf(w.M), bf(w.T)};
+  const DeltaChain fwd{o.H, L.S0, nullptr, bf(w.X)}, rev{f32(w.Hb), L.dS_end, L.dS0, bf(w.X1)};
+  CUtensorMap mq, mk, md, mw, mu, my, mt, ms, mx, ms64, mx64;
+  if (make_tmap_bf16_3d(&mq, p.q, D, p.N, BH, rs, p.N * rs, 64, C) ||
+      make_tmap_bf16_3d(&mk, p.k, D, p.N, BH, rs, p.N * rs, 64, C) ||
+      make_tmap_bf16_3d(&md, L.dout, D, p.N, BH, rs, p.N * rs, 64, C) ||
+      make_tmap_bf16_3d(&mw, o.W, D, C, 2 * nc, rs, C * rs, 64, C) ||
+      make_tmap_bf16_3d(&mu, o.U, D, C, 2 * nc, rs, C * rs, 64, C) ||
+      make_tmap_bf16_3d(&my, L.ws + w.Y, D, C, 2 * nc, rs, C * rs, 64, C) ||
+      make_tmap_bf16_3d(&mt, o.T, C, C, 2 * nc, 2 * C, 2 * C * C, 64, C) ||
+      make_tmap_bf16_3d(&ms, fwd.X, D, D, 2 * nc, rs, D * rs, 64, D) ||
+      make_tmap_bf16_3d(&mx, rev.X, D, D, 2 * nc, rs, D * rs, 64, D) ||
+      make_tmap_bf16_3d(&ms64, fwd.X, D, D, 2 * nc, rs, D * rs, 64, 64) ||
+      make_tmap_bf16_3d(&mx64, rev.X, D, D, 2 * nc, rs, D * rs, 64, 64))
+    return -1;
+  static std::atomic<uint64_t> a0{0}, a1{0}, a2{0};
+  if (allow_dynamic_smem(delta_hb_kernel<D>, (int)HbSmem<D>::TOTAL, a0) ||
+      allow_dynamic_smem(delta_vals_kernel<D>, (int)ValsSmem<D>::TOTAL, a1) ||
+      allow_dynamic_smem(delta_keys_kernel<D>, (int)KeysSmem<D>::TOTAL, a2))
+    return -1;
+  if (launch_delta_prep(p, o, stream)) return -1;
+  const unsigned grid = (unsigned)(nc * DA);
+  prof_before(K_DELTA_HB, stream);
+  delta_hb_kernel<D><<<grid, THREADS, HbSmem<D>::TOTAL, stream>>>(
+      mq, mk, md, mw, my, HbArgs{g, beta, f32(w.Hb), p.N, nch, p.scale, p.st});
+  prof_after(K_DELTA_HB, stream);
+  if (launch_delta_chain(p, o.gend, o.M, &fwd, &rev, stream)) return -1;
+  prof_before(K_DELTA_VALS, stream);
+  delta_vals_kernel<D><<<grid, THREADS, ValsSmem<D>::TOTAL, stream>>>(
+      mk, mw, mu, my, mt, ms, mx,
+      ValsArgs{g, beta, (const __nv_bfloat16*)p.v, (__nv_bfloat16*)L.dv, f32(w.bpart), p.N, nch, tokens, p.st});
+  prof_after(K_DELTA_VALS, stream);
+  prof_before(K_DELTA_KEYS, stream);
+  delta_keys_kernel<D><<<grid, THREADS, KeysSmem<D>::TOTAL, stream>>>(
+      mq, mk, md, mu, my, ms64, mx64,
+      KeysArgs{g, beta, (__nv_bfloat16*)L.dq, (__nv_bfloat16*)L.dk, f32(w.rpart), f32(w.wpart), f32(w.xpart),
+               f32(w.bkey), p.N, nch, tokens, nc, p.scale, p.st});
+  prof_after(K_DELTA_KEYS, stream);
+  prof_before(K_DELTA_GATES, stream);
+  delta_gate_grad_kernel<<<(unsigned)nc, C, 0, stream>>>(
+      GateArgs{o.gend, f32(w.rpart), f32(w.wpart), f32(w.xpart), f32(w.bpart), f32(w.bkey),
+               (__nv_bfloat16*)L.dg, (__nv_bfloat16*)L.dbeta, p.N, nch, DA, tokens, nc});
+  prof_after(K_DELTA_GATES, stream);
+  return cudaGetLastError() == cudaSuccess ? 0 : -1;
+}
+
+}  // namespace
+
+DeltaUmmaBwdWorkspace delta_umma_bwd_layout(int BH, int N, int D) {
+  DeltaUmmaBwdWorkspace w{};
+  const size_t nc = (size_t)BH * ((N + C - 1) / C), tokens = (size_t)BH * N, DA = D / 64;
+  size_t at = 256;
+  auto take = [&](size_t bytes) {
+    const size_t o = at;
+    at += (bytes + 255) / 256 * 256;
+    return o;
+  };
+  const size_t tile = nc * 2 * C * D * 2, mat = nc * 4 * D * D;
+  w.gend = take(nc * 4);
+  w.W = take(tile);
+  w.U = take(tile);
+  w.Y = take(tile);
+  w.T = take(nc * 2 * C * C * 2);
+  w.M = take(mat);
+  w.H = take(mat);
+  w.Hb = take(mat);
+  w.X = take(mat);
+  w.X1 = take(mat);
+  w.rpart = take(DA * tokens * 4);
+  w.wpart = take(DA * tokens * 4);
+  w.bpart = take(DA * tokens * 4);
+  w.bkey = take(tokens * 4);
+  w.xpart = take(DA * nc * 4);
+  w.total = at;
+  return w;
+}
+
+int launch_delta_umma_bwd(const DeltaBwdLaunch& L, cudaStream_t stream) {
+  return L.f.dk == 64 ? bwd_launch<64>(L, stream) : bwd_launch<128>(L, stream);
+}
+
+}  // namespace ttt

@@ -152,7 +152,6 @@ struct DeltaBwdLaunch {
   void *dq, *dk, *dv, *dg, *dbeta;
   float* dS0;
   uint8_t* ws;
-  DeltaBwdWorkspace w;
 };
 // CUDA cores, float32, any dims up to 128 (ttt_delta.cu)
 int launch_delta_rec(const DeltaLaunch& L, cudaStream_t stream);
@@ -165,6 +164,11 @@ struct DeltaUmmaWorkspace {           // byte offsets, per chunk of 128 tokens
 bool delta_uses_umma(int bf16, int dk, int dv);
 DeltaUmmaWorkspace delta_umma_layout(int BH, int N, int D);
 int launch_delta_umma(const DeltaLaunch& L, cudaStream_t stream);
+struct DeltaUmmaBwdWorkspace {
+  size_t gend, W, U, Y, T, M, H, Hb, X, X1, rpart, wpart, bpart, bkey, xpart, total;
+};
+DeltaUmmaBwdWorkspace delta_umma_bwd_layout(int BH, int N, int D);   // delta_umma_bwd.cu
+int launch_delta_umma_bwd(const DeltaBwdLaunch& L, cudaStream_t stream);
 int launch_delta_step(const DeltaLaunch& L, const int* slots, int n_slots, cudaStream_t stream);
 
 // ----------------------------------------------------------------- row norm
@@ -356,7 +360,7 @@ enum KernelKind {
   K_LIN_SIMT, K_LIN_UMMA, K_LACT_CAST, K_KEYPASS, K_GEMM_READ, K_GEMM_GRAD, K_UPDATE,
   K_MUON_MOM, K_NS_PREP, K_GEMM_NS, K_MUON_APPLY, K_KEYGRAD, K_LIN_SEG, K_LIN_BWD_EW, K_SWA, K_LOOP,
   K_BWD_FWD, K_BWD_GROUP, K_DELTA_REC, K_DELTA_REV, K_DELTA_GRAD, K_DELTA_STEP, K_NORM, K_NORM_BWD,
-  K_DELTA_PREP, K_DELTA_CHAIN, K_DELTA_OUT,
+  K_DELTA_PREP, K_DELTA_CHAIN, K_DELTA_OUT, K_DELTA_HB, K_DELTA_VALS, K_DELTA_KEYS, K_DELTA_GATES,
   K_NUM
 };
 void prof_before(int kind, cudaStream_t s);

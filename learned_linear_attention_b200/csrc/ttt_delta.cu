@@ -606,10 +606,11 @@ template <typename Tin>
 int bwd_launch(const DeltaBwdLaunch& L, cudaStream_t stream) {
   const DeltaLaunch& p = L.f;
   const int BH = p.B * p.H, nch = (p.N + CB - 1) / CB;
-  float* ev = reinterpret_cast<float*>(L.ws + L.w.ev);
-  float* du = reinterpret_cast<float*>(L.ws + L.w.du);
-  float* Sc = reinterpret_cast<float*>(L.ws + L.w.Sc);
-  float* Xc = reinterpret_cast<float*>(L.ws + L.w.Xc);
+  const DeltaBwdWorkspace w = delta_rec_bwd_layout(BH, p.N, p.dk, p.dv);
+  float* ev = reinterpret_cast<float*>(L.ws + w.ev);
+  float* du = reinterpret_cast<float*>(L.ws + w.du);
+  float* Sc = reinterpret_cast<float*>(L.ws + w.Sc);
+  float* Xc = reinterpret_cast<float*>(L.ws + w.Xc);
   if (rec_launch<Tin, float>(p, nullptr, L.S0, nullptr, ev, Sc, stream)) return -1;
   const dim3 grid((unsigned)BH, (unsigned)((p.dv + COLS - 1) / COLS));
   prof_before(K_DELTA_REV, stream);
