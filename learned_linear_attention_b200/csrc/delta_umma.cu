@@ -34,98 +34,85 @@ namespace {
 // end.
 constexpr int LDA = 132;
 
+// A thread of a join takes four columns and every 16th row, a warp two column
+// groups: what a column group skips (rows of T11 above it) its warp skips, and
+// what a row skips (T22 right of it) is known at compile time.
+TTT_DEVICE_INLINE void fma4(float2 (&acc)[2], float x, const float4& y) {
+  const float2 s = x2_splat(x);
+  acc[0] = x2_fma(s, make_float2(y.x, y.y), acc[0]);
+  acc[1] = x2_fma(s, make_float2(y.z, y.w), acc[1]);
+}
+
 template <int S>
 TTT_DEVICE_INLINE void join_blocks(float* A, int tid) {
-  constexpr int RT = S / 16, CG = S / 4;
-  const int p = tid / (4 * S), t = tid % (4 * S), cg = t % CG, r0 = t / CG * RT;
+  constexpr int RT = S / 16;
+  const int p = tid / (4 * S), t = tid % (4 * S), cg = t / 16, r0 = t % 16;
   float* T11 = A + p * 2 * S * (LDA + 1);
   float* A21 = T11 + S * LDA;
   float* T22 = A21 + S;
   float* Z = T11 + S;
-  float4 acc[RT];
+  float2 acc[RT][2];
+  auto zero = [&]() {
 #pragma unroll
-  for (int r = 0; r < RT; ++r) acc[r] = make_float4(0.f, 0.f, 0.f, 0.f);
-  auto step = [&](const float* X, const float* Y, int k, float sign) {
+    for (int r = 0; r < RT; ++r) acc[r][0] = acc[r][1] = make_float2(0.f, 0.f);
+  };
+  zero();
+  // Z = A21 T11; above T11's diagonal there may be anything
+  for (int k = 4 * (cg & ~1); k < S; k += 4) {
     float4 y[4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) y[i] = *reinterpret_cast<const float4*>(Y + (k + i) * LDA + 4 * cg);
-#pragma unroll
-    for (int r = 0; r < RT; ++r) {
-      const float4 x = *reinterpret_cast<const float4*>(X + (r0 + r) * LDA + k);
-      const float xs[4] = {sign * x.x, sign * x.y, sign * x.z, sign * x.w};
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        acc[r].x = fmaf(xs[i], y[i].x, acc[r].x);
-        acc[r].y = fmaf(xs[i], y[i].y, acc[r].y);
-        acc[r].z = fmaf(xs[i], y[i].z, acc[r].z);
-        acc[r].w = fmaf(xs[i], y[i].w, acc[r].w);
-      }
-    }
-  };
-  // rows of T11 above a column are zero (its own upper part was zeroed with
-  // its 16-blocks, or holds an earlier Z: skipped either way)
-  auto tri = [&](const float* X, int k, int row) {   // X[row][k..k+3] with what is above the diagonal as 0
-    float4 x = *reinterpret_cast<const float4*>(X + row * LDA + k);
-    if (k > row) x.x = 0.f;
-    if (k + 1 > row) x.y = 0.f;
-    if (k + 2 > row) x.z = 0.f;
-    if (k + 3 > row) x.w = 0.f;
-    return x;
-  };
-  // Z = A21 T11, k from the column group's first row on
-  for (int k = 4 * cg; k < S; k += 4) {
-    float4 y[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      y[i] = *reinterpret_cast<const float4*>(T11 + (k + i) * LDA + 4 * cg);
-      if (k == 4 * cg) {   // the diagonal's own 4 x 4: above it may be anything
-        if (i < 1) y[i].y = 0.f;
-        if (i < 2) y[i].z = 0.f;
-        if (i < 3) y[i].w = 0.f;
-      }
+    for (int i = 0; i < 4; ++i) y[i] = *reinterpret_cast<const float4*>(T11 + (k + i) * LDA + 4 * cg);
+    if (k <= 4 * cg) {
+      const bool diag = k == 4 * cg;
+      y[0] = make_float4(diag ? y[0].x : 0.f, 0.f, 0.f, 0.f);
+      y[1] = make_float4(diag ? y[1].x : 0.f, diag ? y[1].y : 0.f, 0.f, 0.f);
+      y[2] = make_float4(diag ? y[2].x : 0.f, diag ? y[2].y : 0.f, diag ? y[2].z : 0.f, 0.f);
+      if (!diag) y[3] = make_float4(0.f, 0.f, 0.f, 0.f);
     }
 #pragma unroll
     for (int r = 0; r < RT; ++r) {
-      const float4 x = *reinterpret_cast<const float4*>(A21 + (r0 + r) * LDA + k);
-      const float xs[4] = {x.x, x.y, x.z, x.w};
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        acc[r].x = fmaf(xs[i], y[i].x, acc[r].x);
-        acc[r].y = fmaf(xs[i], y[i].y, acc[r].y);
-        acc[r].z = fmaf(xs[i], y[i].z, acc[r].z);
-        acc[r].w = fmaf(xs[i], y[i].w, acc[r].w);
-      }
+      const float4 x = *reinterpret_cast<const float4*>(A21 + (r0 + 16 * r) * LDA + k);
+      fma4(acc[r], x.x, y[0]);
+      fma4(acc[r], x.y, y[1]);
+      fma4(acc[r], x.z, y[2]);
+      fma4(acc[r], x.w, y[3]);
     }
   }
 #pragma unroll
-  for (int r = 0; r < RT; ++r) {
-    *reinterpret_cast<float4*>(Z + (r0 + r) * LDA + 4 * cg) = acc[r];
-    acc[r] = make_float4(0.f, 0.f, 0.f, 0.f);
-  }
+  for (int r = 0; r < RT; ++r)
+    *reinterpret_cast<float4*>(Z + (r0 + 16 * r) * LDA + 4 * cg) =
+        make_float4(acc[r][0].x, acc[r][0].y, acc[r][1].x, acc[r][1].y);
+  zero();
   __syncthreads();
-  // T21 = -T22 Z, k up to the row group's last row; whole 4-steps below the
-  // group's first row need no mask
-  const int kd = r0 & ~3;
-  for (int k = 0; k < kd; k += 4) step(T22, Z, k, -1.f);
-  for (int k = kd; k < r0 + RT; k += 4) {
-    float4 y[4];
+  // T22 Z, 16 columns of T22 at a time: its rows above them have no part
 #pragma unroll
-    for (int i = 0; i < 4; ++i) y[i] = *reinterpret_cast<const float4*>(Z + (k + i) * LDA + 4 * cg);
+  for (int kb = 0; kb < RT; ++kb) {
 #pragma unroll
-    for (int r = 0; r < RT; ++r) {
-      const float4 x = tri(T22, k, r0 + r);
-      const float xs[4] = {-x.x, -x.y, -x.z, -x.w};
+    for (int k = 16 * kb; k < 16 * kb + 16; k += 4) {
+      float4 y[4];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        acc[r].x = fmaf(xs[i], y[i].x, acc[r].x);
-        acc[r].y = fmaf(xs[i], y[i].y, acc[r].y);
-        acc[r].z = fmaf(xs[i], y[i].z, acc[r].z);
-        acc[r].w = fmaf(xs[i], y[i].w, acc[r].w);
+      for (int i = 0; i < 4; ++i) y[i] = *reinterpret_cast<const float4*>(Z + (k + i) * LDA + 4 * cg);
+#pragma unroll
+      for (int r = kb; r < RT; ++r) {
+        float4 x = *reinterpret_cast<const float4*>(T22 + (r0 + 16 * r) * LDA + k);
+        if (r == kb) {
+          const int d = 16 * kb + r0 - k;   // columns behind the diagonal may hold anything
+          if (d < 0) x.x = 0.f;
+          if (d < 1) x.y = 0.f;
+          if (d < 2) x.z = 0.f;
+          if (d < 3) x.w = 0.f;
+        }
+        fma4(acc[r], x.x, y[0]);
+        fma4(acc[r], x.y, y[1]);
+        fma4(acc[r], x.z, y[2]);
+        fma4(acc[r], x.w, y[3]);
       }
     }
   }
 #pragma unroll
-  for (int r = 0; r < RT; ++r) *reinterpret_cast<float4*>(A21 + (r0 + r) * LDA + 4 * cg) = acc[r];
+  for (int r = 0; r < RT; ++r)
+    *reinterpret_cast<float4*>(A21 + (r0 + 16 * r) * LDA + 4 * cg) =
+        make_float4(-acc[r][0].x, -acc[r][0].y, -acc[r][1].x, -acc[r][1].y);
   __syncthreads();
 }
 
@@ -158,7 +145,9 @@ TTT_DEVICE_INLINE void invert(float* A, int tid) {
 struct PrepArgs {
   const __nv_bfloat16 *g, *beta;
   float* gend;             // [BH nch] exp(G_last)
-  float* H;                // [BH nch][D / 64][16][D][4]: columns in groups of four
+  float* H;                // [BH nch] float32 tiles [D][D]
+  float* U;                // [BH nch] float32 tiles [128][D]: Ut
+  __nv_bfloat16* W;        // [BH nch][2][128][D] hi, lo
   __nv_bfloat16* M;        // [BH nch][2][D][D] hi, lo
   __nv_bfloat16* T;        // nullable: [BH nch][2][128][128] hi, lo
   int N, nch;
@@ -168,17 +157,17 @@ struct PrepArgs {
 template <int D>
 struct PrepSmem {
   static constexpr uint32_t OP = D / 64 * ATOM;          // a [128][D] operand
-  static constexpr uint32_t K = 0, V = OP, T = 2 * OP;   // T: A in float32, then operand tiles
+  static constexpr uint32_t K = 0, V = OP, T = 2 * OP;   // T: A in float32, then T's operand tiles
   static constexpr uint32_t TBYTES = (C * LDA * 4 + 1023) / 1024 * 1024;
   static constexpr uint32_t GATES = T + TBYTES;
-  static constexpr uint32_t BAR = GATES + sizeof(Gates);
+  static constexpr uint32_t COL = GATES + sizeof(Gates);   // beta gam, rho
+  static constexpr uint32_t BAR = COL + 2 * C * 4;
   static constexpr uint32_t TOTAL = BAR + 64;
 };
 
 template <int D>
-__global__ void __launch_bounds__(256)
+__global__ void __launch_bounds__(256, D == 64 ? 2 : 1)
     delta_prep_kernel(const __grid_constant__ CUtensorMap mapK, const __grid_constant__ CUtensorMap mapV,
-                      const __grid_constant__ CUtensorMap mapW, const __grid_constant__ CUtensorMap mapU,
                       PrepArgs a) {
   using SM = PrepSmem<D>;
   constexpr int DA = D / 64;
@@ -186,75 +175,56 @@ __global__ void __launch_bounds__(256)
   // Hc takes the place of A; Mc follows it (D = 64) or takes the last columns
   constexpr uint32_t TM_H = 0, TM_M = D == 64 ? 64 : 384;
   extern __shared__ __align__(1024) uint8_t smem[];
-  uint64_t* load = reinterpret_cast<uint64_t*>(smem + SM::BAR);
-  uint64_t* mma = load + 1;
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(mma + 1);
-  uint32_t* abort_flag = tmem_slot + 1;
+  Bars& bars = *reinterpret_cast<Bars*>(smem + SM::BAR);
   Gates& gates = *reinterpret_cast<Gates*>(smem + SM::GATES);
+  float* bgam = reinterpret_cast<float*>(smem + SM::COL);
+  float* rhos = bgam + C;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int ch = blockIdx.x % a.nch;
   const size_t bh = blockIdx.x / a.nch, ci = blockIdx.x;
   const int t0 = ch * C, n = min(C, a.N - t0);
-
-  if (tid == 0) {
-    mbar_init(load, 1);
-    mbar_init(mma, 1);
-    *abort_flag = 0;
-    fence_barrier_init();
-  }
-  if (warp == 1) {
-    tmem_alloc(tmem_slot, TM_COLS);
-    tmem_relinquish();
-  }
-  tc_fence_before();
-  __syncthreads();
-  tc_fence_after();
-  const uint32_t tmem = *tmem_slot;
-  const uint32_t sb = smem_u32(smem);
-  Phase ph{Waiter{abort_flag, a.st, 1000}, mma, 0};
+  const uint32_t tmem = cta_begin(bars, TM_COLS, tid), sb = smem_u32(smem);
+  Phase ph{Waiter{&bars.abort, a.st, 1000}, &bars.mma, 0};
   const int q4 = warp & 3, hf = warp >> 2, row = q4 * 32 + lane;
   const uint32_t lanes = (uint32_t)(q4 * 32) << 16;
 
   if (tid == 0) {
-    mbar_arrive_expect_tx(load, 2 * SM::OP);
+    mbar_arrive_expect_tx(&bars.load[0], 2 * SM::OP);
     for (int i = 0; i < DA; ++i) {
-      tma_load_3d(smem + SM::K + i * ATOM, &mapK, load, 64 * i, t0, (int)bh);
-      tma_load_3d(smem + SM::V + i * ATOM, &mapV, load, 64 * i, t0, (int)bh);
+      tma_load_3d(smem + SM::K + i * ATOM, &mapK, &bars.load[0], 64 * i, t0, (int)bh);
+      tma_load_3d(smem + SM::V + i * ATOM, &mapV, &bars.load[0], 64 * i, t0, (int)bh);
     }
   }
   if (warp == 2) {
     const size_t tok = bh * a.N + t0;
     load_gates(gates, a.g ? a.g + tok : nullptr, a.beta + tok, n, lane);
+    __syncwarp();
+    for (int i = lane; i < C; i += 32) {
+      bgam[i] = gates.beta[i] * gate_decay(gates, i);
+      rhos[i] = gate_ratio(gates, C - 1, i);
+    }
     if (lane == 31) a.gend[ci] = gate_decay(gates, C - 1);
   }
   auto work = [&]() {
-    if (!ph.wait(load, 0, 1)) return;
+    if (!ph.wait(&bars.load[0], 0, 1)) return;
     const Op K{sb + SM::K, ATOM, false}, Kmn{sb + SM::K, ATOM, true}, Vmn{sb + SM::V, ATOM, true};
     if (tid == 0) {
       product(tmem + TM_A, K, K, 128, 128, D / 16, false);
-      mma_commit(mma);
+      mma_commit(&bars.mma);
     }
     if (!ph.mma_done(2)) return;
-    // A = beta_i Gam_ij k_i.k_j below the diagonal, float32
+    // A = beta_i Gam_ij k_i.k_j below the diagonal, float32; what lies in
+    // blocks of 16 above it is read by nobody
     float* A = reinterpret_cast<float*>(smem + SM::T);
     {
-      const float bi = gates.beta[row], gh = gates.hi[row], gl = gates.lo[row];
+      const float bi = gates.beta[row];
 #pragma unroll
       for (int b = 0; b < 4; ++b) {
         const int c0 = hf * 64 + b * 16;
+        if (c0 > q4 * 32 + 31) continue;
         float x[16];
-        const bool any = c0 <= q4 * 32 + 31;   // the warp's last row
-        if (any) {
-          tmem_ld16(tmem + lanes + TM_A + c0, x);
-#pragma unroll
-          for (int j = 0; j < 16; ++j) {
-            const float d = (gh - gates.hi[c0 + j]) + (gl - gates.lo[c0 + j]);
-            x[j] = c0 + j < row ? bi * x[j] * gate_exp(d) : 0.f;
-          }
-        } else {
-#pragma unroll
-          for (int j = 0; j < 16; ++j) x[j] = 0.f;
-        }
+        tmem_ld16(tmem + lanes + TM_A + c0, x);
+        weigh16<false>(gates, q4 * 32, row, c0, bi, x);
 #pragma unroll
         for (int j = 0; j < 16; j += 4)
           *reinterpret_cast<float4*>(A + row * LDA + c0 + j) = make_float4(x[j], x[j + 1], x[j + 2], x[j + 3]);
@@ -264,157 +234,139 @@ __global__ void __launch_bounds__(256)
     __syncthreads();
     invert(A, tid);
     // this thread's half row of T
+    const bool some = hf * 64 <= row;   // uniform in a warp
     float t[64];
 #pragma unroll
     for (int j = 0; j < 64; j += 4) {
       const int c0 = hf * 64 + j;
-      float4 x = *reinterpret_cast<const float4*>(A + row * LDA + c0);
+      float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (some) x = *reinterpret_cast<const float4*>(A + row * LDA + c0);
       t[j] = c0 <= row ? x.x : 0.f;
       t[j + 1] = c0 + 1 <= row ? x.y : 0.f;
       t[j + 2] = c0 + 2 <= row ? x.z : 0.f;
       t[j + 3] = c0 + 3 <= row ? x.w : 0.f;
     }
     if (a.T != nullptr) {
-      uint4* d0 = reinterpret_cast<uint4*>(a.T + (ci * 2 * C + row) * C + hf * 64);
-      uint4* d1 = reinterpret_cast<uint4*>(a.T + (ci * 2 * C + C + row) * C + hf * 64);
+      __nv_bfloat16* d = a.T + (ci * 2 * C + row) * C + hf * 64;
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        uint32_t h[4], l[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) split2(t[8 * j + 2 * i], t[8 * j + 2 * i + 1], h[i], l[i]);
-        d0[j] = make_uint4(h[0], h[1], h[2], h[3]);
-        d1[j] = make_uint4(l[0], l[1], l[2], l[3]);
-      }
+      for (int j = 0; j < 64; j += 16) store16_pair(d + j, d + C * C + j, t + j);
     }
     __syncthreads();
-    // operand tiles [hi atom 0, hi atom 1, lo atom 0, lo atom 1] of T with scaled columns
+    // operand tiles [hi atom 0, hi atom 1, lo atom 0, lo atom 1] of T with
+    // scaled columns; hi + lo is off by 2^-18 at most, and what T adds to the
+    // diagonal is a part of U and W only: 6e-7 of the state measured
     const uint32_t tb = sb + SM::T;
     const Pair Tp{{tb, ATOM, false}, 2 * ATOM};
-    auto put_t = [&](bool with_gam) {
+    auto put_t = [&](const float* col) {
 #pragma unroll
       for (int j = 0; j < 64; j += 8) {
-        float x[8];
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const int c = hf * 64 + j + i;
-          x[i] = t[j + i] * (with_gam ? gates.beta[c] * gate_decay(gates, c) : gates.beta[c]);
-        }
+        const float4 s0 = *reinterpret_cast<const float4*>(col + hf * 64 + j);
+        const float4 s1 = *reinterpret_cast<const float4*>(col + hf * 64 + j + 4);
+        const float x[8] = {t[j] * s0.x, t[j + 1] * s0.y, t[j + 2] * s0.z, t[j + 3] * s0.w,
+                            t[j + 4] * s1.x, t[j + 5] * s1.y, t[j + 6] * s1.z, t[j + 7] * s1.w};
         store8_split(tb + hf * ATOM, tb + (2 + hf) * ATOM, row, j, x);
       }
     };
-    put_t(false);
+    put_t(gates.beta);
     ph.publish();
     if (tid == 0) {
       product(tmem + TM_U, Tp.hi, Vmn, 128, D, 8, false);
       product(tmem + TM_U, Tp.lo(), Vmn, 128, D, 8, true);
-      mma_commit(mma);
+      mma_commit(&bars.mma);
     }
     if (!ph.mma_done(3)) return;
-    put_t(true);
+    if (some) put_t(bgam);
     ph.publish();
     if (tid == 0) {
       product(tmem + TM_W, Tp.hi, Kmn, 128, D, 8, false);
       product(tmem + TM_W, Tp.lo(), Kmn, 128, D, 8, true);
-      mma_commit(mma);
+      mma_commit(&bars.mma);
     }
-    if (!ph.mma_done(4)) return;
-    // rho K as hi (in K's place) and lo (in V's)
-    {
-      const float rho = gate_exp((gates.hi[C - 1] - gates.hi[row]) + (gates.lo[C - 1] - gates.lo[row]));
+    // Ut goes out in float32, W as hi + lo; rho Ut (three planes: Hc is the
+    // state's own term, and hi + lo alone would leave 4e-6 of it) and rho W
+    // (two: Mc multiplies what the decay left of the last state) are operands
+    // in the place of V and T, against the exact K
+    const float rho = rhos[row];
+    auto out_u = [&](int c) {   // 16 columns
+      float x[16];
+      tmem_ld16(tmem + lanes + TM_U + c, x);
+      store_tile16(a.U + ci * C * D, C, row, c, x);
 #pragma unroll
-      for (int j = 0; j < D / 2; j += 8) {
-        const int c = hf * (D / 2) + j;
-        const uint32_t at = (uint32_t)(c >> 6) * ATOM;
-        float x[8];
-        load8(sb + SM::K + at, row, c & 63, x);
+      for (int i = 0; i < 16; ++i) x[i] *= rho;
+      const uint32_t at = sb + SM::V + (uint32_t)(c >> 6) * ATOM;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) x[i] *= rho;
-        store8_split(sb + SM::K + at, sb + SM::V + at, row, c & 63, x);
-      }
-    }
-    // Ut and W as operand tiles, stored to the workspace and multiplied
-    auto put = [&](uint32_t tm, int col0, int cols, uint32_t hi, uint32_t lo) {
-      for (int j = 0; j < cols; j += 16) {
-        float x[16];
-        tmem_ld16(tmem + lanes + tm + col0 + j, x);
-        const int c = col0 + j;
-        const uint32_t at = (uint32_t)(c >> 6) * ATOM;
-        store8_split(hi + at, lo + at, row, c & 63, x);
-        store8_split(hi + at, lo + at, row, (c & 63) + 8, x + 8);
-      }
+      for (int i = 0; i < 16; i += 8)
+        store8_split3(at, at + SM::OP, at + 2 * SM::OP, row, (c & 63) + i, x + i);
     };
-    const Pair Kr{{sb + SM::K, ATOM, true}, SM::OP};
+    auto out_w = [&](int c, uint32_t hi, uint32_t second) {
+      float x[16];
+      tmem_ld16(tmem + lanes + TM_W + c, x);
+      __nv_bfloat16* d = a.W + (ci * 2 * C + row) * D + c;
+      store16_pair(d, d + C * D, x);
+#pragma unroll
+      for (int i = 0; i < 16; ++i) x[i] *= rho;
+      const uint32_t at = hi + (uint32_t)(c >> 6) * ATOM;
+#pragma unroll
+      for (int i = 0; i < 16; i += 8) store8_split(at, at + second, row, (c & 63) + i, x + i);
+    };
+    if (!ph.mma_done(4)) return;
+    const Op Kt{sb + SM::K, ATOM, true};
+    const uint32_t vb = sb + SM::V;
     if constexpr (D == 64) {
-      // [Ut hi, W hi, Ut lo, W lo]: a 128-column operand
-      if (hf == 0) put(TM_U, 0, 64, tb, tb + 2 * ATOM);
-      else put(TM_W, 0, 64, tb + ATOM, tb + 3 * ATOM);
+      // [Ut hi, lo, rest, W hi, lo] atoms
+      if (hf == 0) {
+#pragma unroll
+        for (int c = 0; c < 64; c += 16) out_u(c);
+      } else {
+#pragma unroll
+        for (int c = 0; c < 64; c += 16) out_w(c, vb + 3 * ATOM, ATOM);
+      }
       ph.publish();
       if (tid == 0) {
-        const Pair B{{tb, ATOM, true}, 2 * ATOM};
-        product3(tmem + TM_H, Kr, B, 64, 128, 8, false);
-        mma_commit(mma);
-        for (int h = 0; h < 2; ++h) {
-          tma_store_3d(&mapU, smem + SM::T + 2 * h * ATOM, 0, 0, (int)(2 * ci + h));
-          tma_store_3d(&mapW, smem + SM::T + (2 * h + 1) * ATOM, 0, 0, (int)(2 * ci + h));
-        }
-        bulk_commit();
+        for (int i = 0; i < 3; ++i) product(tmem + TM_H, Kt, Op{vb + i * ATOM, ATOM, true}, 64, 64, 8, i > 0);
+        for (int i = 0; i < 2; ++i) product(tmem + TM_M, Kt, Op{vb + (3 + i) * ATOM, ATOM, true}, 64, 64, 8, i > 0);
+        mma_commit(&bars.mma);
       }
       if (!ph.mma_done(5)) return;
     } else {
-      for (int m = 0; m < 2; ++m) {
-        put(m ? TM_W : TM_U, hf * 64, 64, tb, tb + 2 * ATOM);
-        ph.publish();
-        if (tid == 0) {
-          const Pair B{{tb, ATOM, true}, 2 * ATOM};
-          product3(tmem + (m ? TM_M : TM_H), Kr, B, 128, 128, 8, false);
-          mma_commit(mma);
-          for (int h = 0; h < 2; ++h)
-            for (int i = 0; i < 2; ++i)
-              tma_store_3d(m ? &mapW : &mapU, smem + SM::T + (2 * h + i) * ATOM, 64 * i, 0, (int)(2 * ci + h));
-          bulk_commit();
-          bulk_wait_read();
-        }
-        if (!ph.mma_done(5 + m)) return;
+#pragma unroll
+      for (int c = 0; c < 64; c += 16) out_u(hf * 64 + c);
+      ph.publish();
+      if (tid == 0) {
+        for (int i = 0; i < 3; ++i) product(tmem + TM_H, Kt, Op{vb + i * SM::OP, ATOM, true}, 128, 128, 8, i > 0);
+        mma_commit(&bars.mma);
       }
+      if (!ph.mma_done(5)) return;
+#pragma unroll
+      for (int c = 0; c < 64; c += 16) out_w(hf * 64 + c, vb, SM::OP);
+      ph.publish();
+      if (tid == 0) {
+        for (int i = 0; i < 2; ++i) product(tmem + TM_M, Kt, Op{vb + i * SM::OP, ATOM, true}, 128, 128, 8, i > 0);
+        mma_commit(&bars.mma);
+      }
+      if (!ph.mma_done(6)) return;
     }
-    // Hc in float32, Mc as hi and lo; for D = 64 the 64 rows sit in the first
-    // 16 lanes of each quadrant
+    // Hc in float32, Mc = -K^T rho W as hi and lo; for D = 64 the 64 rows sit
+    // in the first 16 lanes of each quadrant
     const int r = D == 64 ? q4 * 16 + lane : row;
     const bool own = D == 128 || lane < 16;
     const int cols = D / 2;   // of each, this half
+#pragma unroll
     for (int j = 0; j < cols; j += 16) {
       const int c = hf * cols + j;
       float h[16], m[16];
       tmem_ld16(tmem + lanes + TM_H + c, h);
       tmem_ld16(tmem + lanes + TM_M + c, m);
       if (!own) continue;
-      store_h16(a.H + ci * D * D, D, r, c, h);
-      uint32_t hi[8], lo[8];
+      store_tile16(a.H + ci * D * D, D, r, c, h);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) split2(-m[2 * i], -m[2 * i + 1], hi[i], lo[i]);
-      uint4* d0 = reinterpret_cast<uint4*>(a.M + (ci * 2 * D + r) * D + c);
-      uint4* d1 = reinterpret_cast<uint4*>(a.M + (ci * 2 * D + D + r) * D + c);
-      d0[0] = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-      d0[1] = make_uint4(hi[4], hi[5], hi[6], hi[7]);
-      d1[0] = make_uint4(lo[0], lo[1], lo[2], lo[3]);
-      d1[1] = make_uint4(lo[4], lo[5], lo[6], lo[7]);
+      for (int i = 0; i < 16; ++i) m[i] = -m[i];
+      __nv_bfloat16* d = a.M + (ci * 2 * D + r) * D + c;
+      store16_pair(d, d + D * D, m);
     }
-    if (tid == 0) bulk_wait_all();
   };
   work();
-  if (tid == 0 && ph.W.aborted()) {   // nothing in flight may outlive the CTA
-    ph.W.drain(load, 0);
-    bulk_wait_all();
-    mma_commit(mma);
-    ph.W.drain(mma, 0);
-    ph.W.drain(mma, 1);
-  }
-  tc_fence_before();
-  __syncthreads();
-  if (warp == 1) {
-    tc_fence_after();
-    tmem_dealloc(tmem, TM_COLS);
-  }
+  cta_end(bars, ph, 1, tmem, TM_COLS, tid);
 }
 
 // ------------------------------------------------------------------ chain
@@ -579,6 +531,7 @@ __global__ void __launch_bounds__(512, 1)
 // O = scale (gam Q S0 + (Gam . Q K^T) (Ut - W S0)) of one chunk and 64 value columns.
 struct OutArgs {
   const __nv_bfloat16 *g, *beta;
+  const float* U;
   void* out;
   int N, nch, out_bf16;
   float scale;
@@ -589,70 +542,53 @@ template <int D>
 struct OutSmem {
   static constexpr int DA = D / 64;
   static constexpr uint32_t OP = DA * ATOM, SA = D * 128;
-  static constexpr uint32_t Q = 0, K = OP, W = 2 * OP;             // W hi, lo
-  static constexpr uint32_t P = 0;                                  // 4 atoms, over Q, K (and W for D = 64)
-  static constexpr uint32_t U = 4 * OP;                             // Ut, then U: hi, lo
-  static constexpr uint32_t S = U + 2 * ATOM;                       // S0 hi, lo
-  static constexpr uint32_t GATES = S + 2 * SA;
-  static constexpr uint32_t BAR = GATES + sizeof(Gates);
-  static constexpr uint32_t TOTAL = BAR + 64;
+  static constexpr uint32_t Q = 0, K = OP, W = 2 * OP;              // W hi, lo
+  static constexpr uint32_t S = 4 * OP;                             // S0 hi, lo
+  static constexpr uint32_t P = 0, U = 4 * ATOM;                    // P: 4 atoms, U: 2, over all of these
+  static constexpr uint32_t OPS = S + 2 * SA > 6 * ATOM ? S + 2 * SA : 6 * ATOM;
+  static constexpr uint32_t GATES = OPS, BAR = GATES + sizeof(Gates), TOTAL = BAR + 64;
 };
 
 template <int D>
-__global__ void __launch_bounds__(256)
+__global__ void __launch_bounds__(256, D == 64 ? 2 : 1)
     delta_out_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_constant__ CUtensorMap mapK,
-                     const __grid_constant__ CUtensorMap mapW, const __grid_constant__ CUtensorMap mapU,
-                     const __grid_constant__ CUtensorMap mapS, OutArgs a) {
+                     const __grid_constant__ CUtensorMap mapW, const __grid_constant__ CUtensorMap mapS,
+                     OutArgs a) {
   using SM = OutSmem<D>;
   constexpr int DA = D / 64;
   constexpr uint32_t TM_P = 0, TM_W = 128, TM_Q = 192, TM_COLS = 256;   // P U takes W S0's place
   extern __shared__ __align__(1024) uint8_t smem[];
-  uint64_t* load = reinterpret_cast<uint64_t*>(smem + SM::BAR);
-  uint64_t* mma = load + 1;
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(mma + 1);
-  uint32_t* abort_flag = tmem_slot + 1;
+  Bars& bars = *reinterpret_cast<Bars*>(smem + SM::BAR);
   Gates& gates = *reinterpret_cast<Gates*>(smem + SM::GATES);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int slice = blockIdx.x % DA;
   const size_t ci = blockIdx.x / DA, bh = ci / a.nch;
   const int t0 = (int)(ci % a.nch) * C, n = min(C, a.N - t0);
-
-  if (tid == 0) {
-    mbar_init(load, 1);
-    mbar_init(mma, 1);
-    *abort_flag = 0;
-    fence_barrier_init();
-  }
-  if (warp == 1) {
-    tmem_alloc(tmem_slot, TM_COLS);
-    tmem_relinquish();
-  }
-  tc_fence_before();
-  __syncthreads();
-  tc_fence_after();
-  const uint32_t tmem = *tmem_slot, sb = smem_u32(smem);
-  Phase ph{Waiter{abort_flag, a.st, 1200}, mma, 0};
+  const uint32_t tmem = cta_begin(bars, TM_COLS, tid), sb = smem_u32(smem);
+  Phase ph{Waiter{&bars.abort, a.st, 1200}, &bars.mma, 0};
   const int q4 = warp & 3, hf = warp >> 2, row = q4 * 32 + lane;
   const uint32_t lanes = (uint32_t)(q4 * 32) << 16;
   if (tid == 0) {
-    mbar_arrive_expect_tx(load, 4 * SM::OP + 2 * ATOM + 2 * SM::SA);
+    mbar_arrive_expect_tx(&bars.load[0], 4 * SM::OP + 2 * SM::SA);
     for (int i = 0; i < DA; ++i) {
-      tma_load_3d(smem + SM::Q + i * ATOM, &mapQ, load, 64 * i, t0, (int)bh);
-      tma_load_3d(smem + SM::K + i * ATOM, &mapK, load, 64 * i, t0, (int)bh);
+      tma_load_3d(smem + SM::Q + i * ATOM, &mapQ, &bars.load[0], 64 * i, t0, (int)bh);
+      tma_load_3d(smem + SM::K + i * ATOM, &mapK, &bars.load[0], 64 * i, t0, (int)bh);
       for (int h = 0; h < 2; ++h)
-        tma_load_3d(smem + SM::W + (h * DA + i) * ATOM, &mapW, load, 64 * i, 0, (int)(2 * ci + h));
+        tma_load_3d(smem + SM::W + (h * DA + i) * ATOM, &mapW, &bars.load[0], 64 * i, 0, (int)(2 * ci + h));
     }
-    for (int h = 0; h < 2; ++h) {
-      tma_load_3d(smem + SM::U + h * ATOM, &mapU, load, 64 * slice, 0, (int)(2 * ci + h));
-      tma_load_3d(smem + SM::S + h * SM::SA, &mapS, load, 64 * slice, 0, (int)(2 * ci + h));
-    }
+    for (int h = 0; h < 2; ++h)
+      tma_load_3d(smem + SM::S + h * SM::SA, &mapS, &bars.load[0], 64 * slice, 0, (int)(2 * ci + h));
   }
   if (warp == 2) {
     const size_t tok = bh * a.N + t0;
     load_gates(gates, a.g ? a.g + tok : nullptr, a.beta + tok, n, lane);
   }
+  // this thread's 32 values of Ut, while the operands travel
+  float u[32];
+  load_tile16(a.U + ci * C * D, C, row, slice * 64 + hf * 32, u);
+  load_tile16(a.U + ci * C * D, C, row, slice * 64 + hf * 32 + 16, u + 16);
   auto work = [&]() {
-    if (!ph.wait(load, 0, 1)) return;
+    if (!ph.wait(&bars.load[0], 0, 1)) return;
     const Op Q{sb + SM::Q, ATOM, false}, K{sb + SM::K, ATOM, false};
     const Pair Wp{{sb + SM::W, ATOM, false}, SM::OP}, S{{sb + SM::S, SM::SA, true}, SM::SA};
     if (tid == 0) {
@@ -660,102 +596,84 @@ __global__ void __launch_bounds__(256)
       product3(tmem + TM_W, Wp, S, 128, 64, D / 16, false);
       product(tmem + TM_Q, Q, S.hi, 128, 64, D / 16, false);
       product(tmem + TM_Q, Q, S.lo(), 128, 64, D / 16, true);
-      mma_commit(mma);
+      mma_commit(&bars.mma);
     }
     if (!ph.mma_done(2)) return;
-    // U = Ut - W S0, in place; this half's 32 columns
-    {
-      float w[32];
-      tmem_ld32(tmem + lanes + TM_W + hf * 32, w);
+    // U = Ut - W S0; this half's 32 columns
 #pragma unroll
-      for (int j = 0; j < 32; j += 8) {
-        float u[8];
-        load8_split(sb + SM::U, sb + SM::U + ATOM, row, hf * 32 + j, u);
+    for (int j = 0; j < 32; j += 16) {
+      float w[16];
+      tmem_ld16(tmem + lanes + TM_W + hf * 32 + j, w);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) u[i] -= w[j + i];
-        store8_split(sb + SM::U, sb + SM::U + ATOM, row, hf * 32 + j, u);
-      }
+      for (int i = 0; i < 16; ++i) w[i] = u[j + i] - w[i];
+      store8_split(sb + SM::U, sb + SM::U + ATOM, row, hf * 32 + j, w);
+      store8_split(sb + SM::U, sb + SM::U + ATOM, row, hf * 32 + j + 8, w + 8);
     }
     // P = Gam . Q K^T on and below the diagonal: [hi 0, hi 1, lo 0, lo 1]
-    {
-      const float gh = gates.hi[row], gl = gates.lo[row];
 #pragma unroll
-      for (int b = 0; b < 4; ++b) {
-        const int c0 = hf * 64 + b * 16;
-        float x[16];
-        if (c0 <= q4 * 32 + 31) {
-          tmem_ld16(tmem + lanes + TM_P + c0, x);
+    for (int b = 0; b < 4; ++b) {
+      const int c0 = hf * 64 + b * 16;
+      float x[16];
+      if (c0 <= q4 * 32 + 31) {
+        tmem_ld16(tmem + lanes + TM_P + c0, x);
+        weigh16<true>(gates, q4 * 32, row, c0, 1.f, x);
+      } else {
 #pragma unroll
-          for (int j = 0; j < 16; ++j) {
-            const float d = (gh - gates.hi[c0 + j]) + (gl - gates.lo[c0 + j]);
-            x[j] = c0 + j <= row ? x[j] * gate_exp(d) : 0.f;
-          }
-        } else {
-#pragma unroll
-          for (int j = 0; j < 16; ++j) x[j] = 0.f;
-        }
-        store8_split(sb + SM::P + hf * ATOM, sb + SM::P + (2 + hf) * ATOM, row, b * 16, x);
-        store8_split(sb + SM::P + hf * ATOM, sb + SM::P + (2 + hf) * ATOM, row, b * 16 + 8, x + 8);
+        for (int j = 0; j < 16; ++j) x[j] = 0.f;
       }
+      store8_split(sb + SM::P + hf * ATOM, sb + SM::P + (2 + hf) * ATOM, row, b * 16, x);
+      store8_split(sb + SM::P + hf * ATOM, sb + SM::P + (2 + hf) * ATOM, row, b * 16 + 8, x + 8);
     }
     ph.publish();
     if (tid == 0) {
       const Pair P{{sb + SM::P, ATOM, false}, 2 * ATOM}, U{{sb + SM::U, ATOM, true}, ATOM};
       product3(tmem + TM_W, P, U, 128, 64, 8, false);
-      mma_commit(mma);
+      mma_commit(&bars.mma);
     }
     if (!ph.mma_done(3)) return;
-    float o[32], qs[32];
-    tmem_ld32(tmem + lanes + TM_W + hf * 32, o);
-    tmem_ld32(tmem + lanes + TM_Q + hf * 32, qs);
-    if (row < n) {
-      const float gam = a.scale * gate_decay(gates, row);
+    const float gam = a.scale * gate_decay(gates, row);
 #pragma unroll
-      for (int j = 0; j < 32; ++j) o[j] = fmaf(gam, qs[j], a.scale * o[j]);
-      const size_t at = (bh * a.N + t0 + row) * D + slice * 64 + hf * 32;
+    for (int j = 0; j < 32; j += 16) {
+      float o[16], qs[16];
+      tmem_ld16(tmem + lanes + TM_W + hf * 32 + j, o);
+      tmem_ld16(tmem + lanes + TM_Q + hf * 32 + j, qs);
+      if (row >= n) continue;
+#pragma unroll
+      for (int i = 0; i < 16; ++i) o[i] = fmaf(gam, qs[i], a.scale * o[i]);
+      const size_t at = (bh * a.N + t0 + row) * D + slice * 64 + hf * 32 + j;
       if (a.out_bf16) {
         uint4* dst = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.out) + at);
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
-          dst[j] = make_uint4(pack_bf16x2(o[8 * j], o[8 * j + 1]), pack_bf16x2(o[8 * j + 2], o[8 * j + 3]),
-                              pack_bf16x2(o[8 * j + 4], o[8 * j + 5]), pack_bf16x2(o[8 * j + 6], o[8 * j + 7]));
+        for (int i = 0; i < 2; ++i)
+          dst[i] = make_uint4(pack_bf16x2(o[8 * i], o[8 * i + 1]), pack_bf16x2(o[8 * i + 2], o[8 * i + 3]),
+                              pack_bf16x2(o[8 * i + 4], o[8 * i + 5]), pack_bf16x2(o[8 * i + 6], o[8 * i + 7]));
       } else {
         float4* dst = reinterpret_cast<float4*>(static_cast<float*>(a.out) + at);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) dst[j] = make_float4(o[4 * j], o[4 * j + 1], o[4 * j + 2], o[4 * j + 3]);
+        for (int i = 0; i < 4; ++i) dst[i] = make_float4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
       }
     }
   };
   work();
-  if (tid == 0 && ph.W.aborted()) {
-    ph.W.drain(load, 0);
-    mma_commit(mma);
-    ph.W.drain(mma, 0);
-    ph.W.drain(mma, 1);
-  }
-  tc_fence_before();
-  __syncthreads();
-  if (warp == 1) {
-    tc_fence_after();
-    tmem_dealloc(tmem, TM_COLS);
-  }
+  cta_end(bars, ph, 1, tmem, TM_COLS, tid);
 }
+
+static_assert(2 * (PrepSmem<64>::TOTAL + 1024) <= 233472 && 2 * (OutSmem<64>::TOTAL + 1024) <= 233472, "two CTAs an SM");
 
 template <int D>
 int prep_launch(const DeltaLaunch& p, const DeltaPrepOut& o, cudaStream_t stream) {
   const int BH = p.B * p.H, nch = (p.N + C - 1) / C;
   const uint64_t nc = (uint64_t)BH * nch, rs = D * 2;
-  CUtensorMap mk, mv, mw, mu;
+  CUtensorMap mk, mv;
   if (make_tmap_bf16_3d(&mk, p.k, D, p.N, BH, rs, p.N * rs, 64, C) ||
-      make_tmap_bf16_3d(&mv, p.v, D, p.N, BH, rs, p.N * rs, 64, C) ||
-      make_tmap_bf16_3d(&mw, o.W, D, C, 2 * nc, rs, C * rs, 64, C) ||
-      make_tmap_bf16_3d(&mu, o.U, D, C, 2 * nc, rs, C * rs, 64, C))
+      make_tmap_bf16_3d(&mv, p.v, D, p.N, BH, rs, p.N * rs, 64, C))
     return -1;
   static std::atomic<uint64_t> attr{0};
   if (allow_dynamic_smem(delta_prep_kernel<D>, (int)PrepSmem<D>::TOTAL, attr)) return -1;
-  const PrepArgs a{(const __nv_bfloat16*)p.g, (const __nv_bfloat16*)p.beta, o.gend, o.H, o.M, o.T, p.N, nch, p.st};
+  const PrepArgs a{(const __nv_bfloat16*)p.g, (const __nv_bfloat16*)p.beta, o.gend, o.H, o.U, o.W, o.M, o.T,
+                   p.N, nch, p.st};
   prof_before(K_DELTA_PREP, stream);
-  delta_prep_kernel<D><<<(unsigned)nc, 256, PrepSmem<D>::TOTAL, stream>>>(mk, mv, mw, mu, a);
+  delta_prep_kernel<D><<<(unsigned)nc, 256, PrepSmem<D>::TOTAL, stream>>>(mk, mv, a);
   prof_after(K_DELTA_PREP, stream);
   return cudaGetLastError() == cudaSuccess ? 0 : -1;
 }
@@ -786,21 +704,20 @@ int fwd_launch(const DeltaLaunch& p, cudaStream_t stream) {
   const uint64_t nc = (uint64_t)BH * nch, rs = D * 2;
   auto bf = [&](size_t at) { return reinterpret_cast<__nv_bfloat16*>(p.ws + at); };
   auto f32 = [&](size_t at) { return reinterpret_cast<float*>(p.ws + at); };
-  const DeltaPrepOut o{f32(w.gend), f32(w.H), bf(w.W), bf(w.U), bf(w.M), nullptr};
+  const DeltaPrepOut o{f32(w.gend), f32(w.H), f32(w.U), bf(w.W), bf(w.M), nullptr};
   const DeltaChain chain{o.H, p.S, p.S, bf(w.X)};
   if (prep_launch<D>(p, o, stream) || chain_launch<D>(p, o.gend, o.M, &chain, nullptr, stream)) return -1;
-  CUtensorMap mq, mk, mw, mu, ms;
+  CUtensorMap mq, mk, mw, ms;
   if (make_tmap_bf16_3d(&mq, p.q, D, p.N, BH, rs, p.N * rs, 64, C) ||
       make_tmap_bf16_3d(&mk, p.k, D, p.N, BH, rs, p.N * rs, 64, C) ||
       make_tmap_bf16_3d(&mw, o.W, D, C, 2 * nc, rs, C * rs, 64, C) ||
-      make_tmap_bf16_3d(&mu, o.U, D, C, 2 * nc, rs, C * rs, 64, C) ||
       make_tmap_bf16_3d(&ms, chain.X, D, D, 2 * nc, rs, D * rs, 64, D))
     return -1;
   static std::atomic<uint64_t> attr{0};
   if (allow_dynamic_smem(delta_out_kernel<D>, (int)OutSmem<D>::TOTAL, attr)) return -1;
-  const OutArgs a{(const __nv_bfloat16*)p.g, (const __nv_bfloat16*)p.beta, p.out, p.N, nch, p.out_bf16, p.scale, p.st};
+  const OutArgs a{(const __nv_bfloat16*)p.g, (const __nv_bfloat16*)p.beta, o.U, p.out, p.N, nch, p.out_bf16, p.scale, p.st};
   prof_before(K_DELTA_OUT, stream);
-  delta_out_kernel<D><<<(unsigned)(nc * (D / 64)), 256, OutSmem<D>::TOTAL, stream>>>(mq, mk, mw, mu, ms, a);
+  delta_out_kernel<D><<<(unsigned)(nc * (D / 64)), 256, OutSmem<D>::TOTAL, stream>>>(mq, mk, mw, ms, a);
   prof_after(K_DELTA_OUT, stream);
   return cudaGetLastError() == cudaSuccess ? 0 : -1;
 }
@@ -820,7 +737,7 @@ DeltaUmmaWorkspace delta_umma_layout(int BH, int N, int D) {
   };
   w.gend = take(nc * 4);
   w.W = take(nc * 2 * C * D * 2);
-  w.U = take(nc * 2 * C * D * 2);
+  w.U = take(nc * C * D * 4);
   w.M = take(nc * 2 * D * D * 2);
   w.H = take(nc * D * D * 4);
   w.X = take(nc * 2 * D * D * 2);

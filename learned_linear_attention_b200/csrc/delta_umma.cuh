@@ -23,7 +23,9 @@ constexpr uint32_t ATOM = C * 128;      // bytes of a 128-row atom
 // G finite where a state is cleared; NaN stays.
 struct Gates {
   float hi[C], lo[C], beta[C];
+  float down[C];           // exp(G_e - G_j), e the last token of j's block of 16
 };
+TTT_DEVICE_INLINE float gate_exp(float d) { return __expf(d); }
 template <typename T>
 TTT_DEVICE_INLINE double gate_clamp(T g) {
   return g < T(-200) ? -200.0 : g > T(200) ? 200.0 : (double)g;
@@ -53,14 +55,41 @@ TTT_DEVICE_INLINE void load_gates(Gates& s, const __nv_bfloat16* g, const __nv_b
     s.hi[4 * lane + i] = (float)h;
     s.lo[4 * lane + i] = (float)(G - h);
   }
+  const double last = __shfl_sync(0xffffffffu, pre + x[3], lane | 3);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) s.down[4 * lane + i] = gate_exp((float)(last - (pre + x[i])));
 }
-constexpr float LOG2E = 1.4426950408889634f;
-TTT_DEVICE_INLINE float gate_exp(float d) { return __expf(d); }
 // exp(G_i - G_j)
 TTT_DEVICE_INLINE float gate_ratio(const Gates& s, int i, int j) {
   return gate_exp((s.hi[i] - s.hi[j]) + (s.lo[i] - s.lo[j]));
 }
+// Gam_ij, i in the rows of this thread, j in 16 columns c0.. below the row's
+// own block of 16: exp(G_i - G_e) exp(G_e - G_j) with e the block's last token,
+// one exponential a block.  `down` holds exp(G_e - G_j) of every token.
+TTT_DEVICE_INLINE float gate_block(const Gates& s, int i, int c0) { return gate_ratio(s, i, c0 + 15); }
 TTT_DEVICE_INLINE float gate_decay(const Gates& s, int i) { return gate_exp(s.hi[i] + s.lo[i]); }
+
+// x_j <- f Gam_ij x_j of 16 columns of a row, lower triangle with the diagonal
+// or without.  `warp_row` is the first row of the warp (uniform branch): blocks
+// below all of its rows take one exponential, the others one an element.
+template <bool DIAG>
+TTT_DEVICE_INLINE void weigh16(const Gates& s, int warp_row, int row, int c0, float f, float* x) {
+  if (c0 < warp_row) {
+    const float a = f * gate_block(s, row, c0);
+#pragma unroll
+    for (int j = 0; j < 16; j += 4) {
+      const float4 d = *reinterpret_cast<const float4*>(s.down + c0 + j);
+      x[j] *= a * d.x; x[j + 1] *= a * d.y; x[j + 2] *= a * d.z; x[j + 3] *= a * d.w;
+    }
+  } else {
+    const float gh = s.hi[row], gl = s.lo[row];
+#pragma unroll
+    for (int j = 0; j < 16; ++j) {
+      const float d = (gh - s.hi[c0 + j]) + (gl - s.lo[c0 + j]);
+      x[j] = (DIAG ? c0 + j <= row : c0 + j < row) ? f * x[j] * gate_exp(d) : 0.f;
+    }
+  }
+}
 
 // ----------------------------------------------------------------- hi + lo
 TTT_DEVICE_INLINE void split2(float a, float b, uint32_t& hi, uint32_t& lo) {
@@ -120,17 +149,50 @@ TTT_DEVICE_INLINE void product3(uint32_t d, const Pair& a, const Pair& b, int M,
   product(d, a.lo(), b.hi, M, N, steps, true);
 }
 
-// ----------------------------------------------------------------- chain layout
-// A [D][D] float32 matrix that the chain kernel adds (its H): 64-column
-// slices, columns in groups of four, so that a row's 16 columns are four
-// 16-byte loads, each whole across the rows of a warp.  Stores 16 columns
-// (c a multiple of 16) of row r.
-TTT_DEVICE_INLINE void store_h16(float* H, int D, int r, int c, const float* h) {
-  float* p = H + (size_t)(c >> 6) * 64 * D;
+// three planes: what is left of 24 bits after hi and lo
+TTT_DEVICE_INLINE void store8_split3(uint32_t hi_atom, uint32_t lo_atom, uint32_t rest_atom, int row, int col,
+                                     const float* x) {
+  uint32_t h[4], l[4], r[4];
 #pragma unroll
-  for (int i = 0; i < 16; i += 4)
-    *reinterpret_cast<float4*>(p + ((size_t)(((c & 63) + i) >> 2) * D + r) * 4) =
-        make_float4(h[i], h[i + 1], h[i + 2], h[i + 3]);
+  for (int i = 0; i < 4; ++i) {
+    h[i] = pack_bf16x2(x[2 * i], x[2 * i + 1]);
+    const float a = x[2 * i] - bf16lo(h[i]), b = x[2 * i + 1] - bf16hi(h[i]);
+    split2(a, b, l[i], r[i]);
+  }
+  const uint32_t o = sw128_offset(row, col);
+  st_shared_v4(hi_atom + o, h[0], h[1], h[2], h[3]);
+  st_shared_v4(lo_atom + o, l[0], l[1], l[2], l[3]);
+  st_shared_v4(rest_atom + o, r[0], r[1], r[2], r[3]);
+}
+// 16 columns of a row as hi and lo rows of global memory (32-byte aligned)
+TTT_DEVICE_INLINE void store16_pair(__nv_bfloat16* hi, __nv_bfloat16* lo, const float* x) {
+  uint32_t h[8], l[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) split2(x[2 * i], x[2 * i + 1], h[i], l[i]);
+  st_global_v8(hi, h);
+  st_global_v8(lo, l);
+}
+
+// ----------------------------------------------------------------- float32 tiles in global memory
+// [rows][D] in 64-column slices, columns in groups of four: a row's 16 columns
+// (c a multiple of 16) are four 16-byte accesses, each whole across the rows
+// of a warp.
+TTT_DEVICE_INLINE float* tile_at(float* p, int rows, int r, int c) {
+  return p + (size_t)(c >> 6) * 64 * rows + ((size_t)((c & 63) >> 2) * rows + r) * 4;
+}
+TTT_DEVICE_INLINE void store_tile16(float* p, int rows, int r, int c, const float* x) {
+  float* t = tile_at(p, rows, r, c);
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    *reinterpret_cast<float4*>(t + (size_t)i * rows * 4) = make_float4(x[4 * i], x[4 * i + 1], x[4 * i + 2], x[4 * i + 3]);
+}
+TTT_DEVICE_INLINE void load_tile16(const float* p, int rows, int r, int c, float* x) {
+  const float* t = tile_at(const_cast<float*>(p), rows, r, c);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float4 v = *reinterpret_cast<const float4*>(t + (size_t)i * rows * 4);
+    x[4 * i] = v.x; x[4 * i + 1] = v.y; x[4 * i + 2] = v.z; x[4 * i + 3] = v.w;
+  }
 }
 
 // ----------------------------------------------------------------- phases
@@ -207,8 +269,8 @@ TTT_DEVICE_INLINE void cta_end(Bars& b, const Phase& ph, int loads, uint32_t tme
 
 // ----------------------------------------------------------------- launches shared by both passes
 struct DeltaPrepOut {       // device buffers, per chunk of all heads
-  float *gend, *H;
-  __nv_bfloat16 *W, *U, *M, *T;   // T nullable
+  float *gend, *H, *U;              // U: Ut, float32 tiles
+  __nv_bfloat16 *W, *M, *T;         // hi, lo; T nullable
 };
 struct DeltaChain {         // one direction of the state recurrence
   const float *H, *S_in;    // S_in nullable (zeros)

@@ -35,16 +35,6 @@ namespace {
 
 constexpr int THREADS = 256;
 
-// Gam_ij m_ij of 16 columns of a row, lower triangle (with the diagonal or without)
-template <bool DIAG>
-TTT_DEVICE_INLINE void weigh16(const Gates& s, int row, int c0, float f, float* x) {
-  const float gh = s.hi[row], gl = s.lo[row];
-#pragma unroll
-  for (int j = 0; j < 16; ++j) {
-    const float d = (gh - s.hi[c0 + j]) + (gl - s.lo[c0 + j]);
-    x[j] = (DIAG ? c0 + j <= row : c0 + j < row) ? f * x[j] * gate_exp(d) : 0.f;
-  }
-}
 TTT_DEVICE_INLINE void zero16(float* x) {
 #pragma unroll
   for (int j = 0; j < 16; ++j) x[j] = 0.f;
@@ -135,7 +125,7 @@ __global__ void __launch_bounds__(THREADS)
       float x[16];
       if (c0 <= q4 * 32 + 31) {
         tmem_ld16(tmem + lanes + TM_P + c0, x);
-        weigh16<true>(gates, row, c0, 1.f, x);
+        weigh16<true>(gates, q4 * 32, row, c0, 1.f, x);
       } else {
         zero16(x);
       }
@@ -184,7 +174,7 @@ __global__ void __launch_bounds__(THREADS)
     for (int j = 0; j < 32; j += 16) {
       float h[16];
       tmem_ld16(tmem + lanes + TM_H + hf * 32 + j, h);
-      if (D == 128 || lane < 16) store_h16(a.H + id.ci * D * D, D, r, id.slice * 64 + hf * 32 + j, h);
+      if (D == 128 || lane < 16) store_tile16(a.H + id.ci * D * D, D, r, id.slice * 64 + hf * 32 + j, h);
     }
   };
   work();
@@ -194,6 +184,7 @@ __global__ void __launch_bounds__(THREADS)
 // ------------------------------------------------------------------ values
 struct ValsArgs {
   const __nv_bfloat16 *g, *beta, *v;
+  const float* Ut;
   __nv_bfloat16* dv;
   float* bpart;            // [D / 64][BH N]
   int N, nch;
@@ -230,7 +221,7 @@ __global__ void __launch_bounds__(THREADS)
   const int q4 = warp & 3, hf = warp >> 2, row = q4 * 32 + lane;
   const uint32_t lanes = (uint32_t)(q4 * 32) << 16;
   if (tid == 0) {
-    mbar_arrive_expect_tx(&bars.load[0], 3 * DA * ATOM + 4 * ATOM + 4 * SM::SA);
+    mbar_arrive_expect_tx(&bars.load[0], 3 * DA * ATOM + 2 * ATOM + 4 * SM::SA);
     for (int i = 0; i < DA; ++i) {
       tma_load_3d(smem + SM::K + i * ATOM, &mapK, &bars.load[0], 64 * i, id.t0, (int)id.bh);
       for (int h = 0; h < 2; ++h)
@@ -240,7 +231,6 @@ __global__ void __launch_bounds__(THREADS)
       const int z = (int)(2 * id.ci + h), x = 64 * id.slice;
       tma_load_3d(smem + SM::S + h * SM::SA, &mapS, &bars.load[0], x, 0, z);
       tma_load_3d(smem + SM::X + h * SM::SA, &mapX, &bars.load[0], x, 0, z);
-      tma_load_3d(smem + SM::U + h * ATOM, &mapU, &bars.load[0], x, 0, z);
       tma_load_3d(smem + SM::Y + h * ATOM, &mapY, &bars.load[0], x, 0, z);
     }
   }
@@ -267,7 +257,7 @@ __global__ void __launch_bounds__(THREADS)
           tma_load_3d(smem + SM::T + (2 * h + i) * ATOM, &mapT, &bars.load[1], 64 * i, 0, (int)(2 * id.ci + h));
     }
     loads = 2;
-    // U = Ut - W S0, dU = rho K X1 - (-scale P^T dO), both in place
+    // U = Ut - W S0;  dU = rho K X1 - (-scale P^T dO), in place
     {
       const float rho = gate_ratio(gates, C - 1, row);
 #pragma unroll
@@ -276,9 +266,9 @@ __global__ void __launch_bounds__(THREADS)
         float w[16], x[16], u[16], y[16];
         tmem_ld16(tmem + lanes + TM_W + c, w);
         tmem_ld16(tmem + lanes + TM_X + c, x);
+        load_tile16(a.Ut + id.ci * C * D, C, row, id.slice * 64 + c, u);
 #pragma unroll
         for (int b = 0; b < 16; b += 8) {
-          load8_split(sb + SM::U, sb + SM::U + ATOM, row, c + b, u + b);
           load8_split(sb + SM::Y, sb + SM::Y + ATOM, row, c + b, y + b);
         }
 #pragma unroll
@@ -366,7 +356,7 @@ struct KeysSmem {
   static constexpr uint32_t U = MQ + 4 * ATOM;                // then Mk
   static constexpr uint32_t Y = U + 4 * ATOM;                 // then K, Q (this slice)
   static constexpr uint32_t YB = 2 * DA * ATOM;
-  static constexpr uint32_t GATES = Y + YB, RED = GATES + sizeof(Gates), BAR = RED + 1024, TOTAL = BAR + 64;
+  static constexpr uint32_t GATES = Y + YB, RED = GATES + sizeof(Gates), BAR = RED + C * 4, TOTAL = BAR + 64;
 };
 
 template <int D>
@@ -450,7 +440,7 @@ __global__ void __launch_bounds__(THREADS)
       float x[16];
       if (c0 <= q4 * 32 + 31) {
         tmem_ld16(tmem + lanes + TM_P + c0, x);
-        weigh16<true>(gates, row, c0, a.scale, x);
+        weigh16<true>(gates, q4 * 32, row, c0, a.scale, x);
       } else {
         zero16(x);
       }
@@ -476,7 +466,7 @@ __global__ void __launch_bounds__(THREADS)
         float kk[16];
         tmem_ld16(tmem + lanes + TM_A + c0, x);
         tmem_ld16(tmem + lanes + TM_P + c0, kk);
-        weigh16<false>(gates, row, c0, -1.f, x);
+        weigh16<false>(gates, q4 * 32, row, c0, -1.f, x);
 #pragma unroll
         for (int j = 0; j < 16; ++j) {
           if (c0 + j < row) db = fmaf(x[j], kk[j], db);
@@ -554,16 +544,14 @@ __global__ void __launch_bounds__(THREADS)
         d[1] = make_uint4(pack_bf16x2(x[8], x[9]), pack_bf16x2(x[10], x[11]), pack_bf16x2(x[12], x[13]), pack_bf16x2(x[14], x[15]));
       }
     }
-    if (hf == 1) {
-      red[row] = rs;
-      red[C + row] = ws;
-    }
+    if (hf == 1) red[row] = rs;
     __syncthreads();
-    if (hf == 0 && row < id.n) {
-      const size_t o = id.slice * a.tokens + id.tok + row;
-      a.rpart[o] = rs + red[row];
-      a.wpart[o] = ws + red[C + row];
-    }
+    const size_t o = id.slice * a.tokens + id.tok + row;
+    if (hf == 0 && row < id.n) a.rpart[o] = rs + red[row];
+    __syncthreads();
+    if (hf == 1) red[row] = ws;
+    __syncthreads();
+    if (hf == 0 && row < id.n) a.wpart[o] = ws + red[row];
   };
   work();
   cta_end(bars, ph, loads, tmem, TM_COLS, tid);
@@ -641,14 +629,14 @@ int bwd_launch(const DeltaBwdLaunch& L, cudaStream_t stream) {
   auto bf = [&](size_t at) { return reinterpret_cast<__nv_bfloat16*>(L.ws + at); };
   auto f32 = [&](size_t at) { return reinterpret_cast<float*>(L.ws + at); };
   const __nv_bfloat16 *g = (const __nv_bfloat16*)p.g, *beta = (const __nv_bfloat16*)p.beta;
-  const DeltaPrepOut o{f32(w.gend), f32(w.H), bf(w.W), bf(w.U), bf(w.M), bf(w.T)};
+  const DeltaPrepOut o{f32(w.gend), f32(w.H), f32(w.Ut), bf(w.W), bf(w.M), bf(w.T)};
   const DeltaChain fwd{o.H, L.S0, nullptr, bf(w.X)}, rev{f32(w.Hb), L.dS_end, L.dS0, bf(w.X1)};
   CUtensorMap mq, mk, md, mw, mu, my, mt, ms, mx, ms64, mx64;
   if (make_tmap_bf16_3d(&mq, p.q, D, p.N, BH, rs, p.N * rs, 64, C) ||
       make_tmap_bf16_3d(&mk, p.k, D, p.N, BH, rs, p.N * rs, 64, C) ||
       make_tmap_bf16_3d(&md, L.dout, D, p.N, BH, rs, p.N * rs, 64, C) ||
       make_tmap_bf16_3d(&mw, o.W, D, C, 2 * nc, rs, C * rs, 64, C) ||
-      make_tmap_bf16_3d(&mu, o.U, D, C, 2 * nc, rs, C * rs, 64, C) ||
+      make_tmap_bf16_3d(&mu, L.ws + w.U, D, C, 2 * nc, rs, C * rs, 64, C) ||
       make_tmap_bf16_3d(&my, L.ws + w.Y, D, C, 2 * nc, rs, C * rs, 64, C) ||
       make_tmap_bf16_3d(&mt, o.T, C, C, 2 * nc, 2 * C, 2 * C * C, 64, C) ||
       make_tmap_bf16_3d(&ms, fwd.X, D, D, 2 * nc, rs, D * rs, 64, D) ||
@@ -671,7 +659,7 @@ int bwd_launch(const DeltaBwdLaunch& L, cudaStream_t stream) {
   prof_before(K_DELTA_VALS, stream);
   delta_vals_kernel<D><<<grid, THREADS, ValsSmem<D>::TOTAL, stream>>>(
       mk, mw, mu, my, mt, ms, mx,
-      ValsArgs{g, beta, (const __nv_bfloat16*)p.v, (__nv_bfloat16*)L.dv, f32(w.bpart), p.N, nch, tokens, p.st});
+      ValsArgs{g, beta, (const __nv_bfloat16*)p.v, o.U, (__nv_bfloat16*)L.dv, f32(w.bpart), p.N, nch, tokens, p.st});
   prof_after(K_DELTA_VALS, stream);
   prof_before(K_DELTA_KEYS, stream);
   delta_keys_kernel<D><<<grid, THREADS, KeysSmem<D>::TOTAL, stream>>>(
@@ -702,6 +690,7 @@ DeltaUmmaBwdWorkspace delta_umma_bwd_layout(int BH, int N, int D) {
   w.gend = take(nc * 4);
   w.W = take(tile);
   w.U = take(tile);
+  w.Ut = take(tile);
   w.Y = take(tile);
   w.T = take(nc * 2 * C * C * 2);
   w.M = take(mat);
