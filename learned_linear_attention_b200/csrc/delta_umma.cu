@@ -393,7 +393,8 @@ struct ChainSmem {
 
 template <int D>
 __global__ void __launch_bounds__(512, 1)
-    delta_chain_kernel(const __grid_constant__ CUtensorMap mapM, ChainArgs a) {
+    delta_chain_kernel(const __grid_constant__ CUtensorMap mapM, const __grid_constant__ CUtensorMap mapXf,
+                       const __grid_constant__ CUtensorMap mapXr, ChainArgs a) {
   using SM = ChainSmem<D>;
   constexpr int DA = D / 64, STAGES = SM::STAGES;
   constexpr uint32_t TM_COLS = 64;
@@ -449,8 +450,7 @@ __global__ void __launch_bounds__(512, 1)
     if (own && dir.S_in != nullptr) v = *reinterpret_cast<const float4*>(dir.S_in + (bh * D + r) * D + col + j);
     x[j] = v.x; x[j + 1] = v.y; x[j + 2] = v.z; x[j + 3] = v.w;
   }
-  // the operand copy, and the border state of chunk c
-  auto put_x = [&](int c) {
+  auto put_x = [&]() {   // the operand copy
     if (!own) return;
     uint32_t h[8], l[8];
 #pragma unroll
@@ -461,12 +461,6 @@ __global__ void __launch_bounds__(512, 1)
       st_shared_v4(sb + SM::X + o, h[i], h[i + 1], h[i + 2], h[i + 3]);
       st_shared_v4(sb + SM::X + SM::SA + o, l[i], l[i + 1], l[i + 2], l[i + 3]);
     }
-    uint4* g0 = reinterpret_cast<uint4*>(dir.X + (chunk(c) * 2 * D + r) * D + col);
-    uint4* g1 = reinterpret_cast<uint4*>(dir.X + (chunk(c) * 2 * D + D + r) * D + col);
-    g0[0] = make_uint4(h[0], h[1], h[2], h[3]);
-    g0[1] = make_uint4(h[4], h[5], h[6], h[7]);
-    g1[0] = make_uint4(l[0], l[1], l[2], l[3]);
-    g1[1] = make_uint4(l[4], l[5], l[6], l[7]);
   };
   auto load_h = [&](int c, float4 (&h)[4]) {
     const float* p = dir.H + chunk(c) * D * D + (size_t)slice * 64 * D + ((size_t)cg * 4 * D + r) * 4;
@@ -478,7 +472,7 @@ __global__ void __launch_bounds__(512, 1)
   load_h(0, h);
   e = a.gend[chunk(0)];
   for (int c = 0; c < a.nch; ++c) {
-    put_x(c);
+    put_x();
     ph.publish();
     if (tid == 0) {
       const int s = c % STAGES;
@@ -488,6 +482,10 @@ __global__ void __launch_bounds__(512, 1)
         product3(tmem, A, B, D, 64, D / 16, false);
         mma_commit(mma);
       }
+      // the same copy is chunk c's border state
+      for (int h = 0; h < 2; ++h)
+        tma_store_3d(rev ? &mapXr : &mapXf, smem + SM::X + h * SM::SA, 64 * slice, 0, (int)(2 * chunk(c) + h));
+      bulk_commit();
     }
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
@@ -500,6 +498,7 @@ __global__ void __launch_bounds__(512, 1)
       load_h(c + 1, h);
       e = a.gend[chunk(c + 1)];
     }
+    if (tid == 0) bulk_wait_read();
     if (!ph.mma_done(2)) break;
     float d[16];
     tmem_ld16(tmem + lanes + cg * 16, d);
@@ -513,6 +512,7 @@ __global__ void __launch_bounds__(512, 1)
     for (int j = 0; j < 16; j += 4)
       *reinterpret_cast<float4*>(dst + j) = make_float4(x[j], x[j + 1], x[j + 2], x[j + 3]);
   }
+  if (tid == 0) bulk_wait_all();
   if (tid == 0 && ph.W.aborted()) {
     for (int i = max(0, issued - STAGES); i < issued; ++i) ph.W.drain(&full[i % STAGES], (i / STAGES) & 1);
     mma_commit(mma);
@@ -683,8 +683,11 @@ int chain_launch(const DeltaLaunch& p, const float* gend, const __nv_bfloat16* M
                  const DeltaChain* rev, cudaStream_t stream) {
   const int BH = p.B * p.H, nch = (p.N + C - 1) / C;
   const uint64_t nc = (uint64_t)BH * nch, rs = D * 2;
-  CUtensorMap mm;
-  if (make_tmap_bf16_3d(&mm, M, D, D, 2 * nc, rs, D * rs, 64, D)) return -1;
+  CUtensorMap mm, mf, mr;
+  if (make_tmap_bf16_3d(&mm, M, D, D, 2 * nc, rs, D * rs, 64, D) ||
+      make_tmap_bf16_3d(&mf, fwd ? fwd->X : rev->X, D, D, 2 * nc, rs, D * rs, 64, D) ||
+      make_tmap_bf16_3d(&mr, rev ? rev->X : fwd->X, D, D, 2 * nc, rs, D * rs, 64, D))
+    return -1;
   static std::atomic<uint64_t> attr{0};
   if (allow_dynamic_smem(delta_chain_kernel<D>, (int)ChainSmem<D>::TOTAL, attr)) return -1;
   ChainArgs a{gend, {}, nch, BH, fwd ? 0 : 1, p.st};
@@ -692,7 +695,7 @@ int chain_launch(const DeltaLaunch& p, const float* gend, const __nv_bfloat16* M
   if (rev) a.dir[1] = *rev;
   const unsigned dirs = (fwd ? 1 : 0) + (rev ? 1 : 0);
   prof_before(K_DELTA_CHAIN, stream);
-  delta_chain_kernel<D><<<dirs * (unsigned)(BH * (D / 64)), 512, ChainSmem<D>::TOTAL, stream>>>(mm, a);
+  delta_chain_kernel<D><<<dirs * (unsigned)(BH * (D / 64)), 512, ChainSmem<D>::TOTAL, stream>>>(mm, mf, mr, a);
   prof_after(K_DELTA_CHAIN, stream);
   return cudaGetLastError() == cudaSuccess ? 0 : -1;
 }

@@ -67,6 +67,8 @@ struct ChunkId {
 };
 
 // ------------------------------------------------------------------ Hb
+// Hb is what dS0 is made of, in float32: its operands are carried in three
+// planes (hi + lo alone left 3e-6 of dS0, mostly by scale gam dO).
 struct HbArgs {
   const __nv_bfloat16 *g, *beta;
   float* H;
@@ -78,8 +80,9 @@ struct HbArgs {
 template <int D>
 struct HbSmem {
   static constexpr int DA = D / 64;
-  static constexpr uint32_t Q = 0, P = DA * ATOM;             // P over K; then -scale P^T dO, scale gam dO
-  static constexpr uint32_t W = P + 4 * ATOM, DO = W + 2 * DA * ATOM;
+  // three planes of P over K; then three each of -scale P^T dO, scale gam dO
+  static constexpr uint32_t Q = 0, P = DA * ATOM;
+  static constexpr uint32_t W = P + 6 * ATOM, DO = W + 2 * DA * ATOM;
   static constexpr uint32_t GATES = DO + ATOM, BAR = GATES + sizeof(Gates), TOTAL = BAR + 64;
 };
 
@@ -129,13 +132,15 @@ __global__ void __launch_bounds__(THREADS)
       } else {
         zero16(x);
       }
-      store16_square(sb + SM::P, row, c0, x);
+      const uint32_t at = sb + SM::P + (uint32_t)hf * ATOM;   // [plane][column atom]
+#pragma unroll
+      for (int i = 0; i < 16; i += 8)
+        store8_split3(at, at + 2 * ATOM, at + 4 * ATOM, row, (c0 & 63) + i, x + i);
     }
     ph.publish();
     if (tid == 0) {
-      const Pair Pt{{sb + SM::P, ATOM, true}, 2 * ATOM};
-      product(tmem + TM_U, Pt.hi, dOmn, 128, 64, 8, false);
-      product(tmem + TM_U, Pt.lo(), dOmn, 128, 64, 8, true);
+      for (int i = 0; i < 3; ++i)
+        product(tmem + TM_U, Op{sb + SM::P + 2 * i * ATOM, ATOM, true}, dOmn, 128, 64, 8, i > 0);
       mma_commit(&bars.mma);
     }
     if (!ph.mma_done(3)) return;
@@ -152,17 +157,18 @@ __global__ void __launch_bounds__(THREADS)
           u[j + i] *= -a.scale;
           d[i] *= f;
         }
-        store8_split(sb + SM::P, sb + SM::P + ATOM, row, hf * 32 + j, u + j);
-        store8_split(sb + SM::P + 2 * ATOM, sb + SM::P + 3 * ATOM, row, hf * 32 + j, d);
+        const uint32_t at = sb + SM::P;
+        store8_split3(at, at + ATOM, at + 2 * ATOM, row, hf * 32 + j, u + j);
+        store8_split3(at + 3 * ATOM, at + 4 * ATOM, at + 5 * ATOM, row, hf * 32 + j, d);
       }
     }
     ph.publish();
     if (tid == 0) {
-      const Pair U{{sb + SM::P, ATOM, true}, ATOM}, G{{sb + SM::P + 2 * ATOM, ATOM, true}, ATOM};
+      auto plane = [&](int i) { return Op{sb + SM::P + i * ATOM, ATOM, true}; };
       const Pair Wt{{sb + SM::W, ATOM, true}, DA * ATOM};
-      product(tmem + TM_H, Qmn, G.hi, D, 64, 8, false);
-      product(tmem + TM_H, Qmn, G.lo(), D, 64, 8, true);
-      product3(tmem + TM_H, Wt, U, D, 64, 8, true);
+      for (int i = 0; i < 3; ++i) product(tmem + TM_H, Qmn, plane(3 + i), D, 64, 8, i > 0);
+      for (int i = 0; i < 3; ++i) product(tmem + TM_H, Wt.hi, plane(i), D, 64, 8, true);
+      for (int i = 0; i < 2; ++i) product(tmem + TM_H, Wt.lo(), plane(i), D, 64, 8, true);
       mma_commit(&bars.mma);
       for (int h = 0; h < 2; ++h)
         tma_store_3d(&mapY, smem + SM::P + h * ATOM, 64 * id.slice, 0, (int)(2 * id.ci + h));
