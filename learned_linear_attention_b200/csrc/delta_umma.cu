@@ -25,7 +25,7 @@ namespace {
 
 // ------------------------------------------------------------------ inverse
 // (I + A)^-1 in place, A strictly lower triangular [128][128] float32 in
-// shared memory (rows LDA floats apart), by 256 threads: 16 x 16 diagonal
+// shared memory (rows LDA floats apart), by 256 threads (barrier 1): 16 x 16 diagonal
 // blocks by substitution, one column a thread, then blocks of 16, 32 and 64
 // joined two by two, T21 = -T22 (A21 T11).  Every factor is itself an
 // inverse, so the intermediate values stay of the size of the result (the
@@ -58,6 +58,7 @@ TTT_DEVICE_INLINE void join_blocks(float* A, int tid) {
   };
   zero();
   // Z = A21 T11; above T11's diagonal there may be anything
+#pragma unroll 2
   for (int k = 4 * (cg & ~1); k < S; k += 4) {
     float4 y[4];
 #pragma unroll
@@ -83,7 +84,7 @@ TTT_DEVICE_INLINE void join_blocks(float* A, int tid) {
     *reinterpret_cast<float4*>(Z + (r0 + 16 * r) * LDA + 4 * cg) =
         make_float4(acc[r][0].x, acc[r][0].y, acc[r][1].x, acc[r][1].y);
   zero();
-  __syncthreads();
+  named_bar_sync(1, 256);
   // T22 Z, 16 columns of T22 at a time: its rows above them have no part
 #pragma unroll
   for (int kb = 0; kb < RT; ++kb) {
@@ -113,7 +114,7 @@ TTT_DEVICE_INLINE void join_blocks(float* A, int tid) {
   for (int r = 0; r < RT; ++r)
     *reinterpret_cast<float4*>(A21 + (r0 + 16 * r) * LDA + 4 * cg) =
         make_float4(-acc[r][0].x, -acc[r][0].y, -acc[r][1].x, -acc[r][1].y);
-  __syncthreads();
+  named_bar_sync(1, 256);
 }
 
 TTT_DEVICE_INLINE void invert(float* A, int tid) {
@@ -129,13 +130,13 @@ TTT_DEVICE_INLINE void invert(float* A, int tid) {
       x[i] = acc;
     }
   }
-  __syncthreads();
+  named_bar_sync(1, 256);
   if (tid < C) {
     float* B = A + (tid >> 4) * 16 * (LDA + 1);
 #pragma unroll
     for (int i = 0; i < 16; ++i) B[i * LDA + (tid & 15)] = x[i];
   }
-  __syncthreads();
+  named_bar_sync(1, 256);
   join_blocks<16>(A, tid);
   join_blocks<32>(A, tid);
   join_blocks<64>(A, tid);
@@ -165,8 +166,10 @@ struct PrepSmem {
   static constexpr uint32_t TOTAL = BAR + 64;
 };
 
+constexpr int PREP_THREADS = 512;
+
 template <int D>
-__global__ void __launch_bounds__(256, D == 64 ? 2 : 1)
+__global__ void __launch_bounds__(PREP_THREADS, D == 64 ? 2 : 1)
     delta_prep_kernel(const __grid_constant__ CUtensorMap mapK, const __grid_constant__ CUtensorMap mapV,
                       PrepArgs a) {
   using SM = PrepSmem<D>;
@@ -185,7 +188,7 @@ __global__ void __launch_bounds__(256, D == 64 ? 2 : 1)
   const int t0 = ch * C, n = min(C, a.N - t0);
   const uint32_t tmem = cta_begin(bars, TM_COLS, tid), sb = smem_u32(smem);
   Phase ph{Waiter{&bars.abort, a.st, 1000}, &bars.mma, 0};
-  const int q4 = warp & 3, hf = warp >> 2, row = q4 * 32 + lane;
+  const int q4 = warp & 3, cg = warp >> 2, row = q4 * 32 + lane;
   const uint32_t lanes = (uint32_t)(q4 * 32) << 16;
 
   if (tid == 0) {
@@ -219,8 +222,8 @@ __global__ void __launch_bounds__(256, D == 64 ? 2 : 1)
     {
       const float bi = gates.beta[row];
 #pragma unroll
-      for (int b = 0; b < 4; ++b) {
-        const int c0 = hf * 64 + b * 16;
+      for (int b = 0; b < 2; ++b) {
+        const int c0 = cg * 32 + b * 16;
         if (c0 > q4 * 32 + 31) continue;
         float x[16];
         tmem_ld16(tmem + lanes + TM_A + c0, x);
@@ -232,13 +235,14 @@ __global__ void __launch_bounds__(256, D == 64 ? 2 : 1)
     }
     tc_fence_before();
     __syncthreads();
-    invert(A, tid);
-    // this thread's half row of T
-    const bool some = hf * 64 <= row;   // uniform in a warp
-    float t[64];
+    if (tid < 256) invert(A, tid);
+    __syncthreads();
+    // this thread's 32 columns of a row of T
+    const bool some = cg <= q4;   // the others lie above the diagonal
+    float t[32];
 #pragma unroll
-    for (int j = 0; j < 64; j += 4) {
-      const int c0 = hf * 64 + j;
+    for (int j = 0; j < 32; j += 4) {
+      const int c0 = cg * 32 + j;
       float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
       if (some) x = *reinterpret_cast<const float4*>(A + row * LDA + c0);
       t[j] = c0 <= row ? x.x : 0.f;
@@ -247,9 +251,9 @@ __global__ void __launch_bounds__(256, D == 64 ? 2 : 1)
       t[j + 3] = c0 + 3 <= row ? x.w : 0.f;
     }
     if (a.T != nullptr) {
-      __nv_bfloat16* d = a.T + (ci * 2 * C + row) * C + hf * 64;
+      __nv_bfloat16* d = a.T + (ci * 2 * C + row) * C + cg * 32;
 #pragma unroll
-      for (int j = 0; j < 64; j += 16) store16_pair(d + j, d + C * C + j, t + j);
+      for (int j = 0; j < 32; j += 16) store16_pair(d + j, d + C * C + j, t + j);
     }
     __syncthreads();
     // operand tiles [hi atom 0, hi atom 1, lo atom 0, lo atom 1] of T with
@@ -259,27 +263,27 @@ __global__ void __launch_bounds__(256, D == 64 ? 2 : 1)
     const Pair Tp{{tb, ATOM, false}, 2 * ATOM};
     auto put_t = [&](const float* col) {
 #pragma unroll
-      for (int j = 0; j < 64; j += 8) {
-        const float4 s0 = *reinterpret_cast<const float4*>(col + hf * 64 + j);
-        const float4 s1 = *reinterpret_cast<const float4*>(col + hf * 64 + j + 4);
+      for (int j = 0; j < 32; j += 8) {
+        const float4 s0 = *reinterpret_cast<const float4*>(col + cg * 32 + j);
+        const float4 s1 = *reinterpret_cast<const float4*>(col + cg * 32 + j + 4);
         const float x[8] = {t[j] * s0.x, t[j + 1] * s0.y, t[j + 2] * s0.z, t[j + 3] * s0.w,
                             t[j + 4] * s1.x, t[j + 5] * s1.y, t[j + 6] * s1.z, t[j + 7] * s1.w};
-        store8_split(tb + hf * ATOM, tb + (2 + hf) * ATOM, row, j, x);
+        store8_split(tb + (cg >> 1) * ATOM, tb + (2 + (cg >> 1)) * ATOM, row, (cg & 1) * 32 + j, x);
       }
     };
     put_t(gates.beta);
     ph.publish();
     if (tid == 0) {
-      product(tmem + TM_U, Tp.hi, Vmn, 128, D, 8, false);
-      product(tmem + TM_U, Tp.lo(), Vmn, 128, D, 8, true);
+      product(tmem + TM_U, Tp.lo(), Vmn, 128, D, 8, false);
+      product(tmem + TM_U, Tp.hi, Vmn, 128, D, 8, true);
       mma_commit(&bars.mma);
     }
     if (!ph.mma_done(3)) return;
     if (some) put_t(bgam);
     ph.publish();
     if (tid == 0) {
-      product(tmem + TM_W, Tp.hi, Kmn, 128, D, 8, false);
-      product(tmem + TM_W, Tp.lo(), Kmn, 128, D, 8, true);
+      product(tmem + TM_W, Tp.lo(), Kmn, 128, D, 8, false);
+      product(tmem + TM_W, Tp.hi, Kmn, 128, D, 8, true);
       mma_commit(&bars.mma);
     }
     // Ut goes out in float32, W as hi + lo; rho Ut (three planes: Hc is the
@@ -287,7 +291,8 @@ __global__ void __launch_bounds__(256, D == 64 ? 2 : 1)
     // (two: Mc multiplies what the decay left of the last state) are operands
     // in the place of V and T, against the exact K
     const float rho = rhos[row];
-    auto out_u = [&](int c) {   // 16 columns
+    // (planes `second` bytes apart)
+    auto out_u = [&](int c, uint32_t second) {   // 16 columns
       float x[16];
       tmem_ld16(tmem + lanes + TM_U + c, x);
       store_tile16(a.U + ci * C * D, C, row, c, x);
@@ -296,7 +301,7 @@ __global__ void __launch_bounds__(256, D == 64 ? 2 : 1)
       const uint32_t at = sb + SM::V + (uint32_t)(c >> 6) * ATOM;
 #pragma unroll
       for (int i = 0; i < 16; i += 8)
-        store8_split3(at, at + SM::OP, at + 2 * SM::OP, row, (c & 63) + i, x + i);
+        store8_split3(at, at + second, at + 2 * second, row, (c & 63) + i, x + i);
     };
     auto out_w = [&](int c, uint32_t hi, uint32_t second) {
       float x[16];
@@ -313,35 +318,34 @@ __global__ void __launch_bounds__(256, D == 64 ? 2 : 1)
     const Op Kt{sb + SM::K, ATOM, true};
     const uint32_t vb = sb + SM::V;
     if constexpr (D == 64) {
-      // [Ut hi, lo, rest, W hi, lo] atoms
-      if (hf == 0) {
+      // atoms [Ut hi, W hi, Ut lo, W lo, Ut rest]: Ut and W are one operand of 128 columns
 #pragma unroll
-        for (int c = 0; c < 64; c += 16) out_u(c);
-      } else {
-#pragma unroll
-        for (int c = 0; c < 64; c += 16) out_w(c, vb + 3 * ATOM, ATOM);
+      for (int c = 0; c < 32; c += 16) {
+        if (cg < 2) out_u(cg * 32 + c, 2 * ATOM);
+        else out_w((cg - 2) * 32 + c, vb + ATOM, 2 * ATOM);
       }
       ph.publish();
       if (tid == 0) {
-        for (int i = 0; i < 3; ++i) product(tmem + TM_H, Kt, Op{vb + i * ATOM, ATOM, true}, 64, 64, 8, i > 0);
-        for (int i = 0; i < 2; ++i) product(tmem + TM_M, Kt, Op{vb + (3 + i) * ATOM, ATOM, true}, 64, 64, 8, i > 0);
+        product(tmem + TM_H, Kt, Op{vb + 2 * ATOM, ATOM, true}, 64, 128, 8, false);
+        product(tmem + TM_H, Kt, Op{vb + 4 * ATOM, ATOM, true}, 64, 64, 8, true);
+        product(tmem + TM_H, Kt, Op{vb, ATOM, true}, 64, 128, 8, true);
         mma_commit(&bars.mma);
       }
       if (!ph.mma_done(5)) return;
     } else {
 #pragma unroll
-      for (int c = 0; c < 64; c += 16) out_u(hf * 64 + c);
+      for (int c = 0; c < 32; c += 16) out_u(cg * 32 + c, SM::OP);
       ph.publish();
       if (tid == 0) {
-        for (int i = 0; i < 3; ++i) product(tmem + TM_H, Kt, Op{vb + i * SM::OP, ATOM, true}, 128, 128, 8, i > 0);
+        product_planes(tmem + TM_H, Kt, Op{vb, ATOM, true}, SM::OP, 3, 128, 128, 8, false);
         mma_commit(&bars.mma);
       }
       if (!ph.mma_done(5)) return;
 #pragma unroll
-      for (int c = 0; c < 64; c += 16) out_w(hf * 64 + c, vb, SM::OP);
+      for (int c = 0; c < 32; c += 16) out_w(cg * 32 + c, vb, SM::OP);
       ph.publish();
       if (tid == 0) {
-        for (int i = 0; i < 2; ++i) product(tmem + TM_M, Kt, Op{vb + i * SM::OP, ATOM, true}, 128, 128, 8, i > 0);
+        product_planes(tmem + TM_M, Kt, Op{vb, ATOM, true}, SM::OP, 2, 128, 128, 8, false);
         mma_commit(&bars.mma);
       }
       if (!ph.mma_done(6)) return;
@@ -350,10 +354,10 @@ __global__ void __launch_bounds__(256, D == 64 ? 2 : 1)
     // in the first 16 lanes of each quadrant
     const int r = D == 64 ? q4 * 16 + lane : row;
     const bool own = D == 128 || lane < 16;
-    const int cols = D / 2;   // of each, this half
+    constexpr int cols = D / 4;   // of each, this group
 #pragma unroll
     for (int j = 0; j < cols; j += 16) {
-      const int c = hf * cols + j;
+      const int c = cg * cols + j;
       float h[16], m[16];
       tmem_ld16(tmem + lanes + TM_H + c, h);
       tmem_ld16(tmem + lanes + TM_M + c, m);
@@ -594,8 +598,7 @@ __global__ void __launch_bounds__(256, D == 64 ? 2 : 1)
     if (tid == 0) {
       product(tmem + TM_P, Q, K, 128, 128, D / 16, false);
       product3(tmem + TM_W, Wp, S, 128, 64, D / 16, false);
-      product(tmem + TM_Q, Q, S.hi, 128, 64, D / 16, false);
-      product(tmem + TM_Q, Q, S.lo(), 128, 64, D / 16, true);
+      product_planes(tmem + TM_Q, Q, S.hi, SM::SA, 2, 128, 64, D / 16, false);
       mma_commit(&bars.mma);
     }
     if (!ph.mma_done(2)) return;
@@ -673,7 +676,7 @@ int prep_launch(const DeltaLaunch& p, const DeltaPrepOut& o, cudaStream_t stream
   const PrepArgs a{(const __nv_bfloat16*)p.g, (const __nv_bfloat16*)p.beta, o.gend, o.H, o.U, o.W, o.M, o.T,
                    p.N, nch, p.st};
   prof_before(K_DELTA_PREP, stream);
-  delta_prep_kernel<D><<<(unsigned)nc, 256, PrepSmem<D>::TOTAL, stream>>>(mk, mv, a);
+  delta_prep_kernel<D><<<(unsigned)nc, PREP_THREADS, PrepSmem<D>::TOTAL, stream>>>(mk, mv, a);
   prof_after(K_DELTA_PREP, stream);
   return cudaGetLastError() == cudaSuccess ? 0 : -1;
 }

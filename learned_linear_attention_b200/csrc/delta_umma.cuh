@@ -33,13 +33,21 @@ TTT_DEVICE_INLINE double gate_clamp(T g) {
 // by one whole warp; tokens behind n have beta = 0 and no decay
 TTT_DEVICE_INLINE void load_gates(Gates& s, const __nv_bfloat16* g, const __nv_bfloat16* beta, int n,
                                   int lane) {
+  // every load is issued before the first one is used
+  __nv_bfloat16 gv[4], bv[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int t = min(4 * lane + i, n - 1);
+    bv[i] = beta[t];
+    gv[i] = g != nullptr ? g[t] : __float2bfloat16_rn(0.f);
+  }
   double x[4], run = 0;
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    const int t = 4 * lane + i;
-    run += (t < n && g != nullptr) ? gate_clamp(__bfloat162float(g[t])) : 0.0;
+    const bool in = 4 * lane + i < n;
+    run += in ? gate_clamp(__bfloat162float(gv[i])) : 0.0;
     x[i] = run;
-    s.beta[t] = t < n ? __bfloat162float(beta[t]) : 0.f;
+    s.beta[4 * lane + i] = in ? __bfloat162float(bv[i]) : 0.f;
   }
   double pre = run;
 #pragma unroll
@@ -84,9 +92,16 @@ TTT_DEVICE_INLINE void weigh16(const Gates& s, int warp_row, int row, int c0, fl
   } else {
     const float gh = s.hi[row], gl = s.lo[row];
 #pragma unroll
-    for (int j = 0; j < 16; ++j) {
-      const float d = (gh - s.hi[c0 + j]) + (gl - s.lo[c0 + j]);
-      x[j] = (DIAG ? c0 + j <= row : c0 + j < row) ? f * x[j] * gate_exp(d) : 0.f;
+    for (int j = 0; j < 16; j += 4) {
+      const float4 h = *reinterpret_cast<const float4*>(s.hi + c0 + j);
+      const float4 l = *reinterpret_cast<const float4*>(s.lo + c0 + j);
+      const float d[4] = {(gh - h.x) + (gl - l.x), (gh - h.y) + (gl - l.y), (gh - h.z) + (gl - l.z),
+                          (gh - h.w) + (gl - l.w)};
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int c = c0 + j + i;
+        x[j + i] = (DIAG ? c <= row : c < row) ? f * x[j + i] * gate_exp(d[i]) : 0.f;
+      }
     }
   }
 }
@@ -136,17 +151,25 @@ TTT_DEVICE_INLINE void product(uint32_t d, const Op& a, const Op& b, int M, int 
   const uint32_t id = make_idesc(M, N, a.mn, b.mn);
   for (int ks = 0; ks < steps; ++ks) mma_bf16(d, op_desc(a, ks), op_desc(b, ks), id, (add || ks > 0) ? 1u : 0u);
 }
+// D (+)= A (lo + hi), planes of B `second` bytes apart, the last plane first
+TTT_DEVICE_INLINE void product_planes(uint32_t d, const Op& a, const Op& b, uint32_t second, int planes, int M,
+                                      int N, int steps, bool add) {
+  for (int i = planes - 1; i >= 0; --i)
+    product(d, a, Op{b.addr + i * second, b.astride, b.mn}, M, N, steps, add || i < planes - 1);
+}
 // the hi + lo pair of an operand: lo is `second` bytes after hi
 struct Pair {
   Op hi;
   uint32_t second;
   TTT_DEVICE_INLINE Op lo() const { return Op{hi.addr + second, hi.astride, hi.mn}; }
 };
-// hi hi + hi lo + lo hi (lo lo is below 2^-17 of the product twice over)
+// lo hi + hi lo + hi hi (lo lo is below 2^-17 of the product twice over).  The
+// tensor core truncates its running sum, so small terms go first: only the
+// last 8 or so additions round at the size of the result.
 TTT_DEVICE_INLINE void product3(uint32_t d, const Pair& a, const Pair& b, int M, int N, int steps, bool add) {
-  product(d, a.hi, b.hi, M, N, steps, add);
+  product(d, a.lo(), b.hi, M, N, steps, add);
   product(d, a.hi, b.lo(), M, N, steps, true);
-  product(d, a.lo(), b.hi, M, N, steps, true);
+  product(d, a.hi, b.hi, M, N, steps, true);
 }
 
 // three planes: what is left of 24 bits after hi and lo

@@ -139,8 +139,8 @@ __global__ void __launch_bounds__(THREADS)
     }
     ph.publish();
     if (tid == 0) {
-      for (int i = 0; i < 3; ++i)
-        product(tmem + TM_U, Op{sb + SM::P + 2 * i * ATOM, ATOM, true}, dOmn, 128, 64, 8, i > 0);
+      for (int i = 2; i >= 0; --i)
+        product(tmem + TM_U, Op{sb + SM::P + 2 * i * ATOM, ATOM, true}, dOmn, 128, 64, 8, i < 2);
       mma_commit(&bars.mma);
     }
     if (!ph.mma_done(3)) return;
@@ -166,9 +166,11 @@ __global__ void __launch_bounds__(THREADS)
     if (tid == 0) {
       auto plane = [&](int i) { return Op{sb + SM::P + i * ATOM, ATOM, true}; };
       const Pair Wt{{sb + SM::W, ATOM, true}, DA * ATOM};
-      for (int i = 0; i < 3; ++i) product(tmem + TM_H, Qmn, plane(3 + i), D, 64, 8, i > 0);
-      for (int i = 0; i < 3; ++i) product(tmem + TM_H, Wt.hi, plane(i), D, 64, 8, true);
-      for (int i = 0; i < 2; ++i) product(tmem + TM_H, Wt.lo(), plane(i), D, 64, 8, true);
+      // small terms first (see product3)
+      for (int i = 2; i >= 1; --i) product(tmem + TM_H, Qmn, plane(3 + i), D, 64, 8, i < 2);
+      for (int i = 1; i >= 0; --i) product(tmem + TM_H, Wt.lo(), plane(i), D, 64, 8, true);
+      for (int i = 2; i >= 0; --i) product(tmem + TM_H, Wt.hi, plane(i), D, 64, 8, true);
+      product(tmem + TM_H, Qmn, plane(3), D, 64, 8, true);
       mma_commit(&bars.mma);
       for (int h = 0; h < 2; ++h)
         tma_store_3d(&mapY, smem + SM::P + h * ATOM, 64 * id.slice, 0, (int)(2 * id.ci + h));
@@ -249,10 +251,8 @@ __global__ void __launch_bounds__(THREADS)
     const Pair S{{sb + SM::S, SM::SA, true}, SM::SA}, X{{sb + SM::X, SM::SA, true}, SM::SA};
     if (tid == 0) {
       product3(tmem + TM_W, W, S, 128, 64, D / 16, false);
-      product(tmem + TM_Z, K, S.hi, 128, 64, D / 16, false);
-      product(tmem + TM_Z, K, S.lo(), 128, 64, D / 16, true);
-      product(tmem + TM_X, K, X.hi, 128, 64, D / 16, false);
-      product(tmem + TM_X, K, X.lo(), 128, 64, D / 16, true);
+      product_planes(tmem + TM_Z, K, S.hi, S.second, 2, 128, 64, D / 16, false);
+      product_planes(tmem + TM_X, K, X.hi, X.second, 2, 128, 64, D / 16, false);
       mma_commit(&bars.mma);
     }
     if (!ph.mma_done(2)) return;
@@ -406,11 +406,9 @@ __global__ void __launch_bounds__(THREADS)
       const Op dO{sb + SM::DO, ATOM, false};
       const Pair U{{sb + SM::U, ATOM, false}, DA * ATOM}, Y{{sb + SM::Y, ATOM, false}, DA * ATOM};
       const Pair S{{sb + SM::S, SM::HA, false}, DA * SM::HA}, X{{sb + SM::X, SM::HA, false}, DA * SM::HA};
-      product(tmem + TM_P, dO, U.hi, 128, 128, D / 16, false);
-      product(tmem + TM_P, dO, U.lo(), 128, 128, D / 16, true);
+      product_planes(tmem + TM_P, dO, U.hi, U.second, 2, 128, 128, D / 16, false);
       product3(tmem + TM_A, Y, U, 128, 128, D / 16, false);
-      product(tmem + TM_QS, dO, S.hi, 128, 64, D / 16, false);
-      product(tmem + TM_QS, dO, S.lo(), 128, 64, D / 16, true);
+      product_planes(tmem + TM_QS, dO, S.hi, S.second, 2, 128, 64, D / 16, false);
       product3(tmem + TM_YS, Y, S, 128, 64, D / 16, false);
       product3(tmem + TM_UX, U, X, 128, 64, D / 16, false);
       mma_commit(&bars.mma);
@@ -489,14 +487,14 @@ __global__ void __launch_bounds__(THREADS)
     if (tid == 0) {
       const Pair Mq{{sb + SM::MQ, ATOM, false}, 2 * ATOM}, Mk{{sb + SM::U, ATOM, false}, 2 * ATOM};
       const Pair Mqt{{sb + SM::MQ, ATOM, true}, 2 * ATOM}, Mkt{{sb + SM::U, ATOM, true}, 2 * ATOM};
-      product(tmem + TM_QK, Mq.hi, Kmn, 128, 64, 8, false);
-      product(tmem + TM_QK, Mq.lo(), Kmn, 128, 64, 8, true);
-      product(tmem + TM_KR, Mk.hi, Kmn, 128, 64, 8, false);
-      product(tmem + TM_KR, Mk.lo(), Kmn, 128, 64, 8, true);
-      product(tmem + TM_KW, Mqt.hi, Qmn, 128, 64, 8, false);
-      product(tmem + TM_KW, Mqt.lo(), Qmn, 128, 64, 8, true);
-      product(tmem + TM_KW, Mkt.hi, Kmn, 128, 64, 8, true);
+      product(tmem + TM_QK, Mq.lo(), Kmn, 128, 64, 8, false);
+      product(tmem + TM_QK, Mq.hi, Kmn, 128, 64, 8, true);
+      product(tmem + TM_KR, Mk.lo(), Kmn, 128, 64, 8, false);
+      product(tmem + TM_KR, Mk.hi, Kmn, 128, 64, 8, true);
+      product(tmem + TM_KW, Mqt.lo(), Qmn, 128, 64, 8, false);
+      product(tmem + TM_KW, Mqt.hi, Qmn, 128, 64, 8, true);
       product(tmem + TM_KW, Mkt.lo(), Kmn, 128, 64, 8, true);
+      product(tmem + TM_KW, Mkt.hi, Kmn, 128, 64, 8, true);
       mma_commit(&bars.mma);
     }
     if (hf == 0 && id.slice == 0 && row < id.n) a.bkey[id.tok + row] = db + red[row];
