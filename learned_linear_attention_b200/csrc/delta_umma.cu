@@ -158,10 +158,10 @@ struct PrepArgs {
 template <int D>
 struct PrepSmem {
   static constexpr uint32_t OP = D / 64 * ATOM;          // a [128][D] operand
-  static constexpr uint32_t K = 0, V = OP, T = 2 * OP;   // T: A in float32, then T's operand tiles
+  static constexpr uint32_t K = 0, V = OP, T = 2 * OP;   // T: A in float32, then gam K
   static constexpr uint32_t TBYTES = (C * LDA * 4 + 1023) / 1024 * 1024;
   static constexpr uint32_t GATES = T + TBYTES;
-  static constexpr uint32_t COL = GATES + sizeof(Gates);   // beta gam, rho
+  static constexpr uint32_t COL = GATES + sizeof(Gates);   // gam, rho
   static constexpr uint32_t BAR = COL + 2 * C * 4;
   static constexpr uint32_t TOTAL = BAR + 64;
 };
@@ -174,14 +174,14 @@ __global__ void __launch_bounds__(PREP_THREADS, D == 64 ? 2 : 1)
                       PrepArgs a) {
   using SM = PrepSmem<D>;
   constexpr int DA = D / 64;
-  constexpr uint32_t TM_A = 0, TM_U = 128, TM_W = 128 + D, TM_COLS = D == 64 ? 256 : 512;
-  // Hc takes the place of A; Mc follows it (D = 64) or takes the last columns
+  constexpr uint32_t TM_A = 0, TM_T = 0, TM_U = 128, TM_W = 128 + D, TM_COLS = D == 64 ? 256 : 512;
+  // Hc takes the place of T; Mc follows it (D = 64) or takes the last columns
   constexpr uint32_t TM_H = 0, TM_M = D == 64 ? 64 : 384;
   extern __shared__ __align__(1024) uint8_t smem[];
   Bars& bars = *reinterpret_cast<Bars*>(smem + SM::BAR);
   Gates& gates = *reinterpret_cast<Gates*>(smem + SM::GATES);
-  float* bgam = reinterpret_cast<float*>(smem + SM::COL);
-  float* rhos = bgam + C;
+  float* gams = reinterpret_cast<float*>(smem + SM::COL);
+  float* rhos = gams + C;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int ch = blockIdx.x % a.nch;
   const size_t bh = blockIdx.x / a.nch, ci = blockIdx.x;
@@ -198,19 +198,14 @@ __global__ void __launch_bounds__(PREP_THREADS, D == 64 ? 2 : 1)
       tma_load_3d(smem + SM::V + i * ATOM, &mapV, &bars.load[0], 64 * i, t0, (int)bh);
     }
   }
-  if (warp == 2) {
+  if (cg == 1) {
     const size_t tok = bh * a.N + t0;
-    load_gates(gates, a.g ? a.g + tok : nullptr, a.beta + tok, n, lane);
-    __syncwarp();
-    for (int i = lane; i < C; i += 32) {
-      bgam[i] = gates.beta[i] * gate_decay(gates, i);
-      rhos[i] = gate_ratio(gates, C - 1, i);
-    }
-    if (lane == 31) a.gend[ci] = gate_decay(gates, C - 1);
+    load_gates(gates, a.g ? a.g + tok : nullptr, a.beta + tok, n, row, gams[row], rhos[row]);
+    if (row == C - 1) a.gend[ci] = gams[row];
   }
   auto work = [&]() {
     if (!ph.wait(&bars.load[0], 0, 1)) return;
-    const Op K{sb + SM::K, ATOM, false}, Kmn{sb + SM::K, ATOM, true}, Vmn{sb + SM::V, ATOM, true};
+    const Op K{sb + SM::K, ATOM, false}, Vmn{sb + SM::V, ATOM, true};
     if (tid == 0) {
       product(tmem + TM_A, K, K, 128, 128, D / 16, false);
       mma_commit(&bars.mma);
@@ -255,35 +250,46 @@ __global__ void __launch_bounds__(PREP_THREADS, D == 64 ? 2 : 1)
 #pragma unroll
       for (int j = 0; j < 32; j += 16) store16_pair(d + j, d + C * C + j, t + j);
     }
-    __syncthreads();
-    // operand tiles [hi atom 0, hi atom 1, lo atom 0, lo atom 1] of T with
-    // scaled columns; hi + lo is off by 2^-18 at most, and what T adds to the
-    // diagonal is a part of U and W only: 6e-7 of the state measured
-    const uint32_t tb = sb + SM::T;
-    const Pair Tp{{tb, ATOM, false}, 2 * ATOM};
-    auto put_t = [&](const float* col) {
+    // T diag(beta), hi and lo, becomes an operand in TMEM in A's place; hi + lo
+    // is off by 2^-18 at most, and what T adds to the diagonal is a part of U
+    // and W only: 6e-7 of the state measured
+    {
+      uint32_t h[16], l[16];
 #pragma unroll
-      for (int j = 0; j < 32; j += 8) {
-        const float4 s0 = *reinterpret_cast<const float4*>(col + cg * 32 + j);
-        const float4 s1 = *reinterpret_cast<const float4*>(col + cg * 32 + j + 4);
-        const float x[8] = {t[j] * s0.x, t[j + 1] * s0.y, t[j + 2] * s0.z, t[j + 3] * s0.w,
-                            t[j + 4] * s1.x, t[j + 5] * s1.y, t[j + 6] * s1.z, t[j + 7] * s1.w};
-        store8_split(tb + (cg >> 1) * ATOM, tb + (2 + (cg >> 1)) * ATOM, row, (cg & 1) * 32 + j, x);
+      for (int j = 0; j < 32; j += 4) {
+        const float4 b = *reinterpret_cast<const float4*>(gates.beta + cg * 32 + j);
+        split2(t[j] * b.x, t[j + 1] * b.y, h[j / 2], l[j / 2]);
+        split2(t[j + 2] * b.z, t[j + 3] * b.w, h[j / 2 + 1], l[j / 2 + 1]);
       }
-    };
-    put_t(gates.beta);
-    ph.publish();
-    if (tid == 0) {
-      product(tmem + TM_U, Tp.lo(), Vmn, 128, D, 8, false);
-      product(tmem + TM_U, Tp.hi, Vmn, 128, D, 8, true);
-      mma_commit(&bars.mma);
+      tmem_st16_issue(tmem + lanes + TM_T + cg * 16, h);
+      tmem_st16_issue(tmem + lanes + TM_T + 64 + cg * 16, l);
     }
-    if (!ph.mma_done(3)) return;
-    if (some) put_t(bgam);
+    __syncthreads();   // all of A has been read
+    // gam K, hi and lo, in A's place
+    const uint32_t tb = sb + SM::T;
+    {
+      const float gam = gams[row];
+      constexpr int cols = D / 4;
+#pragma unroll
+      for (int j = 0; j < cols; j += 8) {
+        const int c = cg * cols + j;
+        const uint32_t at = (uint32_t)(c >> 6) * ATOM;
+        float x[8];
+        load8(sb + SM::K + at, row, c & 63, x);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) x[i] *= gam;
+        store8_split(tb + at, tb + SM::OP + at, row, c & 63, x);
+      }
+    }
+    tmem_wait_st();
     ph.publish();
     if (tid == 0) {
-      product(tmem + TM_W, Tp.lo(), Kmn, 128, D, 8, false);
-      product(tmem + TM_W, Tp.hi, Kmn, 128, D, 8, true);
+      const Op gK{tb, ATOM, true}, gKlo{tb + SM::OP, ATOM, true};
+      product_ts(tmem + TM_W, tmem + TM_T, gKlo, D, 8, false);
+      product_ts(tmem + TM_W, tmem + TM_T + 64, gK, D, 8, true);
+      product_ts(tmem + TM_W, tmem + TM_T, gK, D, 8, true);
+      product_ts(tmem + TM_U, tmem + TM_T + 64, Vmn, D, 8, false);
+      product_ts(tmem + TM_U, tmem + TM_T, Vmn, D, 8, true);
       mma_commit(&bars.mma);
     }
     // Ut goes out in float32, W as hi + lo; rho Ut (three planes: Hc is the
@@ -314,7 +320,7 @@ __global__ void __launch_bounds__(PREP_THREADS, D == 64 ? 2 : 1)
 #pragma unroll
       for (int i = 0; i < 16; i += 8) store8_split(at, at + second, row, (c & 63) + i, x + i);
     };
-    if (!ph.mma_done(4)) return;
+    if (!ph.mma_done(3)) return;
     const Op Kt{sb + SM::K, ATOM, true};
     const uint32_t vb = sb + SM::V;
     if constexpr (D == 64) {
@@ -583,9 +589,9 @@ __global__ void __launch_bounds__(256, D == 64 ? 2 : 1)
     for (int h = 0; h < 2; ++h)
       tma_load_3d(smem + SM::S + h * SM::SA, &mapS, &bars.load[0], 64 * slice, 0, (int)(2 * ci + h));
   }
-  if (warp == 2) {
+  if (hf == 1) {
     const size_t tok = bh * a.N + t0;
-    load_gates(gates, a.g ? a.g + tok : nullptr, a.beta + tok, n, lane);
+    load_gates(gates, a.g ? a.g + tok : nullptr, a.beta + tok, n, row);
   }
   // this thread's 32 values of Ut, while the operands travel
   float u[32];

@@ -16,74 +16,68 @@ constexpr int C = 128;                  // tokens of a chunk
 constexpr uint32_t ATOM = C * 128;      // bytes of a 128-row atom
 
 // ----------------------------------------------------------------- gates
-// Running sum G of the log decays of a chunk, as hi + lo: hi is a multiple of
-// 2^-9 that float32 holds exactly (|G| <= 128 * 200 < 2^15), so a difference
-// of two sums keeps the precision of its own size and not that of G.  A
-// single log decay is held to +-200 (exp(-200) is 0 in float32), which keeps
-// G finite where a state is cleared; NaN stays.
+// Running sum G of the log decays of a chunk, as hi + lo: hi sums multiples of
+// 2^-9 that float32 holds exactly (|G| <= 128 * 200 < 2^15), lo the rests
+// (below 2^-10 each), so a difference of two sums keeps the precision of its
+// own size and not that of G.  A single log decay is held to +-200 (exp(-200)
+// is 0 in float32), which keeps G finite where a state is cleared; NaN stays.
 struct Gates {
   float hi[C], lo[C], beta[C];
   float down[C];           // exp(G_e - G_j), e the last token of j's block of 16
+  float part[8];
 };
 TTT_DEVICE_INLINE float gate_exp(float d) { return __expf(d); }
-template <typename T>
-TTT_DEVICE_INLINE double gate_clamp(T g) {
-  return g < T(-200) ? -200.0 : g > T(200) ? 200.0 : (double)g;
-}
-// by one whole warp; tokens behind n have beta = 0 and no decay
-TTT_DEVICE_INLINE void load_gates(Gates& s, const __nv_bfloat16* g, const __nv_bfloat16* beta, int n,
-                                  int lane) {
-  // every load is issued before the first one is used
-  __nv_bfloat16 gv[4], bv[4];
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int t = min(4 * lane + i, n - 1);
-    bv[i] = beta[t];
-    gv[i] = g != nullptr ? g[t] : __float2bfloat16_rn(0.f);
-  }
-  double x[4], run = 0;
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const bool in = 4 * lane + i < n;
-    run += in ? gate_clamp(__bfloat162float(gv[i])) : 0.0;
-    x[i] = run;
-    s.beta[4 * lane + i] = in ? __bfloat162float(bv[i]) : 0.f;
-  }
-  double pre = run;
+TTT_DEVICE_INLINE float gate_clamp(float g) { return g < -200.f ? -200.f : g > 200.f ? 200.f : g; }
+
+// By the 128 threads t = 0..127 of four whole warps (barrier 2); tokens behind
+// n have beta = 0 and no decay.  gam = exp(G_t), rho = exp(G_last - G_t).
+TTT_DEVICE_INLINE void load_gates(Gates& s, const __nv_bfloat16* g, const __nv_bfloat16* beta, int n, int t,
+                                  float& gam, float& rho) {
+  const int lane = t & 31, w = t >> 5, at = min(t, n - 1);
+  const __nv_bfloat16 bv = beta[at];
+  float x = g != nullptr ? gate_clamp(__bfloat162float(g[at])) : 0.f;
+  if (t >= n) x = 0.f;
+  float hi = rintf(x * 512.f) * (1.f / 512.f), lo = x - hi;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
-    const double y = __shfl_up_sync(0xffffffffu, pre, o);
-    if (lane >= o) pre += y;
+    const float h = __shfl_up_sync(0xffffffffu, hi, o), l = __shfl_up_sync(0xffffffffu, lo, o);
+    if (lane >= o) { hi += h; lo += l; }
   }
-  pre -= run;
-  // a NaN lane poisons its own difference too; later lanes hold NaN already
+  if (lane == 31) { s.part[w] = hi; s.part[4 + w] = lo; }
+  named_bar_sync(2, C);
+  float hl = 0.f, ll = 0.f;
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    const double G = pre + x[i], h = rint(G * 512.0) / 512.0;
-    s.hi[4 * lane + i] = (float)h;
-    s.lo[4 * lane + i] = (float)(G - h);
+    if (i == w) { hi += hl; lo += ll; }
+    hl += s.part[i];
+    ll += s.part[4 + i];
   }
-  const double last = __shfl_sync(0xffffffffu, pre + x[3], lane | 3);
-#pragma unroll
-  for (int i = 0; i < 4; ++i) s.down[4 * lane + i] = gate_exp((float)(last - (pre + x[i])));
+  const float he = __shfl_sync(0xffffffffu, hi, lane | 15), le = __shfl_sync(0xffffffffu, lo, lane | 15);
+  s.hi[t] = hi;
+  s.lo[t] = lo;
+  s.beta[t] = t < n ? __bfloat162float(bv) : 0.f;
+  s.down[t] = gate_exp((he - hi) + (le - lo));
+  gam = gate_exp(hi + lo);
+  rho = gate_exp((hl - hi) + (ll - lo));
+}
+TTT_DEVICE_INLINE void load_gates(Gates& s, const __nv_bfloat16* g, const __nv_bfloat16* beta, int n, int t) {
+  float gam, rho;
+  load_gates(s, g, beta, n, t, gam, rho);
 }
 // exp(G_i - G_j)
 TTT_DEVICE_INLINE float gate_ratio(const Gates& s, int i, int j) {
   return gate_exp((s.hi[i] - s.hi[j]) + (s.lo[i] - s.lo[j]));
 }
-// Gam_ij, i in the rows of this thread, j in 16 columns c0.. below the row's
-// own block of 16: exp(G_i - G_e) exp(G_e - G_j) with e the block's last token,
-// one exponential a block.  `down` holds exp(G_e - G_j) of every token.
-TTT_DEVICE_INLINE float gate_block(const Gates& s, int i, int c0) { return gate_ratio(s, i, c0 + 15); }
 TTT_DEVICE_INLINE float gate_decay(const Gates& s, int i) { return gate_exp(s.hi[i] + s.lo[i]); }
 
 // x_j <- f Gam_ij x_j of 16 columns of a row, lower triangle with the diagonal
 // or without.  `warp_row` is the first row of the warp (uniform branch): blocks
-// below all of its rows take one exponential, the others one an element.
+// below all of its rows take one exponential, exp(G_i - G_e) exp(G_e - G_j) with
+// e the block's last token, the others one an element.
 template <bool DIAG>
 TTT_DEVICE_INLINE void weigh16(const Gates& s, int warp_row, int row, int c0, float f, float* x) {
   if (c0 < warp_row) {
-    const float a = f * gate_block(s, row, c0);
+    const float a = f * gate_ratio(s, row, c0 + 15);
 #pragma unroll
     for (int j = 0; j < 16; j += 4) {
       const float4 d = *reinterpret_cast<const float4*>(s.down + c0 + j);
@@ -156,6 +150,12 @@ TTT_DEVICE_INLINE void product_planes(uint32_t d, const Op& a, const Op& b, uint
                                       int N, int steps, bool add) {
   for (int i = planes - 1; i >= 0; --i)
     product(d, a, Op{b.addr + i * second, b.astride, b.mn}, M, N, steps, add || i < planes - 1);
+}
+// The same with A in TMEM: lane = row, two bf16 of K to a column.
+TTT_DEVICE_INLINE void product_ts(uint32_t d, uint32_t a_tmem, const Op& b, int N, int steps, bool add) {
+  const uint32_t id = make_idesc(128, N, false, b.mn);
+  for (int ks = 0; ks < steps; ++ks)
+    mma_bf16_ts(d, a_tmem + 8 * ks, op_desc(b, ks), id, (add || ks > 0) ? 1u : 0u);
 }
 // the hi + lo pair of an operand: lo is `second` bytes after hi
 struct Pair {

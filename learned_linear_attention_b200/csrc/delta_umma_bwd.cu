@@ -113,7 +113,7 @@ __global__ void __launch_bounds__(THREADS)
     }
     tma_load_3d(smem + SM::DO, &mapD, &bars.load[0], 64 * id.slice, id.t0, (int)id.bh);
   }
-  if (warp == 2) load_gates(gates, a.g ? a.g + id.tok : nullptr, a.beta + id.tok, id.n, lane);
+  if (hf == 1) load_gates(gates, a.g ? a.g + id.tok : nullptr, a.beta + id.tok, id.n, row);
   auto work = [&]() {
     if (!ph.wait(&bars.load[0], 0, 1)) return;
     const Op dOmn{sb + SM::DO, ATOM, true}, Qmn{sb + SM::Q, ATOM, true};
@@ -242,7 +242,7 @@ __global__ void __launch_bounds__(THREADS)
       tma_load_3d(smem + SM::Y + h * ATOM, &mapY, &bars.load[0], x, 0, z);
     }
   }
-  if (warp == 2) load_gates(gates, a.g ? a.g + id.tok : nullptr, a.beta + id.tok, id.n, lane);
+  if (hf == 1) load_gates(gates, a.g ? a.g + id.tok : nullptr, a.beta + id.tok, id.n, row);
   int loads = 1;
   auto work = [&]() {
     if (!ph.wait(&bars.load[0], 0, 1)) return;
@@ -398,7 +398,7 @@ __global__ void __launch_bounds__(THREADS)
       }
     }
   }
-  if (warp == 2) load_gates(gates, a.g ? a.g + id.tok : nullptr, a.beta + id.tok, id.n, lane);
+  if (hf == 1) load_gates(gates, a.g ? a.g + id.tok : nullptr, a.beta + id.tok, id.n, row);
   int loads = 1;
   auto work = [&]() {
     if (!ph.wait(&bars.load[0], 0, 1)) return;
