@@ -559,8 +559,10 @@ struct OutSmem {
   static constexpr uint32_t GATES = OPS, BAR = GATES + sizeof(Gates), TOTAL = BAR + 64;
 };
 
+constexpr int OUT_THREADS = 512;
+
 template <int D>
-__global__ void __launch_bounds__(256, D == 64 ? 2 : 1)
+__global__ void __launch_bounds__(OUT_THREADS, D == 64 ? 2 : 1)
     delta_out_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_constant__ CUtensorMap mapK,
                      const __grid_constant__ CUtensorMap mapW, const __grid_constant__ CUtensorMap mapS,
                      OutArgs a) {
@@ -576,7 +578,7 @@ __global__ void __launch_bounds__(256, D == 64 ? 2 : 1)
   const int t0 = (int)(ci % a.nch) * C, n = min(C, a.N - t0);
   const uint32_t tmem = cta_begin(bars, TM_COLS, tid), sb = smem_u32(smem);
   Phase ph{Waiter{&bars.abort, a.st, 1200}, &bars.mma, 0};
-  const int q4 = warp & 3, hf = warp >> 2, row = q4 * 32 + lane;
+  const int q4 = warp & 3, cg = warp >> 2, row = q4 * 32 + lane;
   const uint32_t lanes = (uint32_t)(q4 * 32) << 16;
   if (tid == 0) {
     mbar_arrive_expect_tx(&bars.load[0], 4 * SM::OP + 2 * SM::SA);
@@ -589,14 +591,13 @@ __global__ void __launch_bounds__(256, D == 64 ? 2 : 1)
     for (int h = 0; h < 2; ++h)
       tma_load_3d(smem + SM::S + h * SM::SA, &mapS, &bars.load[0], 64 * slice, 0, (int)(2 * ci + h));
   }
-  if (hf == 1) {
+  if (cg == 1) {
     const size_t tok = bh * a.N + t0;
     load_gates(gates, a.g ? a.g + tok : nullptr, a.beta + tok, n, row);
   }
-  // this thread's 32 values of Ut, while the operands travel
-  float u[32];
-  load_tile16(a.U + ci * C * D, C, row, slice * 64 + hf * 32, u);
-  load_tile16(a.U + ci * C * D, C, row, slice * 64 + hf * 32 + 16, u + 16);
+  // this thread's 16 values of Ut, while the operands travel
+  float u[16];
+  load_tile16(a.U + ci * C * D, C, row, slice * 64 + cg * 16, u);
   auto work = [&]() {
     if (!ph.wait(&bars.load[0], 0, 1)) return;
     const Op Q{sb + SM::Q, ATOM, false}, K{sb + SM::K, ATOM, false};
@@ -608,20 +609,19 @@ __global__ void __launch_bounds__(256, D == 64 ? 2 : 1)
       mma_commit(&bars.mma);
     }
     if (!ph.mma_done(2)) return;
-    // U = Ut - W S0; this half's 32 columns
-#pragma unroll
-    for (int j = 0; j < 32; j += 16) {
+    // U = Ut - W S0
+    {
       float w[16];
-      tmem_ld16(tmem + lanes + TM_W + hf * 32 + j, w);
+      tmem_ld16(tmem + lanes + TM_W + cg * 16, w);
 #pragma unroll
-      for (int i = 0; i < 16; ++i) w[i] = u[j + i] - w[i];
-      store8_split(sb + SM::U, sb + SM::U + ATOM, row, hf * 32 + j, w);
-      store8_split(sb + SM::U, sb + SM::U + ATOM, row, hf * 32 + j + 8, w + 8);
+      for (int i = 0; i < 16; ++i) u[i] -= w[i];
+      store8_split(sb + SM::U, sb + SM::U + ATOM, row, cg * 16, u);
+      store8_split(sb + SM::U, sb + SM::U + ATOM, row, cg * 16 + 8, u + 8);
     }
     // P = Gam . Q K^T on and below the diagonal: [hi 0, hi 1, lo 0, lo 1]
 #pragma unroll
-    for (int b = 0; b < 4; ++b) {
-      const int c0 = hf * 64 + b * 16;
+    for (int b = 0; b < 2; ++b) {
+      const int c0 = cg * 32 + b * 16;
       float x[16];
       if (c0 <= q4 * 32 + 31) {
         tmem_ld16(tmem + lanes + TM_P + c0, x);
@@ -630,8 +630,9 @@ __global__ void __launch_bounds__(256, D == 64 ? 2 : 1)
 #pragma unroll
         for (int j = 0; j < 16; ++j) x[j] = 0.f;
       }
-      store8_split(sb + SM::P + hf * ATOM, sb + SM::P + (2 + hf) * ATOM, row, b * 16, x);
-      store8_split(sb + SM::P + hf * ATOM, sb + SM::P + (2 + hf) * ATOM, row, b * 16 + 8, x + 8);
+      const uint32_t hi = sb + SM::P + (uint32_t)(c0 >> 6) * ATOM;
+      store8_split(hi, hi + 2 * ATOM, row, c0 & 63, x);
+      store8_split(hi, hi + 2 * ATOM, row, (c0 & 63) + 8, x + 8);
     }
     ph.publish();
     if (tid == 0) {
@@ -641,26 +642,19 @@ __global__ void __launch_bounds__(256, D == 64 ? 2 : 1)
     }
     if (!ph.mma_done(3)) return;
     const float gam = a.scale * gate_decay(gates, row);
+    float o[16], qs[16];
+    tmem_ld16(tmem + lanes + TM_W + cg * 16, o);
+    tmem_ld16(tmem + lanes + TM_Q + cg * 16, qs);
+    if (row >= n) return;
 #pragma unroll
-    for (int j = 0; j < 32; j += 16) {
-      float o[16], qs[16];
-      tmem_ld16(tmem + lanes + TM_W + hf * 32 + j, o);
-      tmem_ld16(tmem + lanes + TM_Q + hf * 32 + j, qs);
-      if (row >= n) continue;
+    for (int i = 0; i < 16; ++i) o[i] = fmaf(gam, qs[i], a.scale * o[i]);
+    const size_t at = (bh * a.N + t0 + row) * D + slice * 64 + cg * 16;
+    if (a.out_bf16) {
+      store_bf16_row16(static_cast<__nv_bfloat16*>(a.out) + at, o);
+    } else {
+      float4* dst = reinterpret_cast<float4*>(static_cast<float*>(a.out) + at);
 #pragma unroll
-      for (int i = 0; i < 16; ++i) o[i] = fmaf(gam, qs[i], a.scale * o[i]);
-      const size_t at = (bh * a.N + t0 + row) * D + slice * 64 + hf * 32 + j;
-      if (a.out_bf16) {
-        uint4* dst = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.out) + at);
-#pragma unroll
-        for (int i = 0; i < 2; ++i)
-          dst[i] = make_uint4(pack_bf16x2(o[8 * i], o[8 * i + 1]), pack_bf16x2(o[8 * i + 2], o[8 * i + 3]),
-                              pack_bf16x2(o[8 * i + 4], o[8 * i + 5]), pack_bf16x2(o[8 * i + 6], o[8 * i + 7]));
-      } else {
-        float4* dst = reinterpret_cast<float4*>(static_cast<float*>(a.out) + at);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) dst[i] = make_float4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
-      }
+      for (int i = 0; i < 4; ++i) dst[i] = make_float4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
     }
   };
   work();
@@ -714,8 +708,9 @@ int fwd_launch(const DeltaLaunch& p, cudaStream_t stream) {
   const int BH = p.B * p.H, nch = (p.N + C - 1) / C;
   const DeltaUmmaWorkspace w = delta_umma_layout(BH, p.N, D);
   const uint64_t nc = (uint64_t)BH * nch, rs = D * 2;
-  auto bf = [&](size_t at) { return reinterpret_cast<__nv_bfloat16*>(p.ws + at); };
-  auto f32 = [&](size_t at) { return reinterpret_cast<float*>(p.ws + at); };
+  uint8_t* ws = delta_ws_base(p.ws);
+  auto bf = [&](size_t at) { return reinterpret_cast<__nv_bfloat16*>(ws + at); };
+  auto f32 = [&](size_t at) { return reinterpret_cast<float*>(ws + at); };
   const DeltaPrepOut o{f32(w.gend), f32(w.H), f32(w.U), bf(w.W), bf(w.M), nullptr};
   const DeltaChain chain{o.H, p.S, p.S, bf(w.X)};
   if (prep_launch<D>(p, o, stream) || chain_launch<D>(p, o.gend, o.M, &chain, nullptr, stream)) return -1;
@@ -729,7 +724,7 @@ int fwd_launch(const DeltaLaunch& p, cudaStream_t stream) {
   if (allow_dynamic_smem(delta_out_kernel<D>, (int)OutSmem<D>::TOTAL, attr)) return -1;
   const OutArgs a{(const __nv_bfloat16*)p.g, (const __nv_bfloat16*)p.beta, o.U, p.out, p.N, nch, p.out_bf16, p.scale, p.st};
   prof_before(K_DELTA_OUT, stream);
-  delta_out_kernel<D><<<(unsigned)(nc * (D / 64)), 256, OutSmem<D>::TOTAL, stream>>>(mq, mk, mw, ms, a);
+  delta_out_kernel<D><<<(unsigned)(nc * (D / 64)), OUT_THREADS, OutSmem<D>::TOTAL, stream>>>(mq, mk, mw, ms, a);
   prof_after(K_DELTA_OUT, stream);
   return cudaGetLastError() == cudaSuccess ? 0 : -1;
 }
@@ -741,7 +736,7 @@ bool delta_uses_umma(int bf16, int dk, int dv) { return bf16 && dk == dv && (dk 
 DeltaUmmaWorkspace delta_umma_layout(int BH, int N, int D) {
   DeltaUmmaWorkspace w{};
   const size_t nc = (size_t)BH * ((N + C - 1) / C);
-  size_t at = 256;
+  size_t at = 512;   // see delta_ws_base
   auto take = [&](size_t bytes) {
     const size_t o = at;
     at += (bytes + 255) / 256 * 256;

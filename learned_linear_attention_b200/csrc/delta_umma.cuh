@@ -187,7 +187,15 @@ TTT_DEVICE_INLINE void store8_split3(uint32_t hi_atom, uint32_t lo_atom, uint32_
   st_shared_v4(lo_atom + o, l[0], l[1], l[2], l[3]);
   st_shared_v4(rest_atom + o, r[0], r[1], r[2], r[3]);
 }
-// 16 columns of a row as hi and lo rows of global memory (32-byte aligned)
+// 16 columns of a row of the caller's (16-byte aligned) bf16 tensor
+TTT_DEVICE_INLINE void store_bf16_row16(__nv_bfloat16* p, const float* x) {
+  uint4* d = reinterpret_cast<uint4*>(p);
+#pragma unroll
+  for (int i = 0; i < 2; ++i)
+    d[i] = make_uint4(pack_bf16x2(x[8 * i], x[8 * i + 1]), pack_bf16x2(x[8 * i + 2], x[8 * i + 3]),
+                      pack_bf16x2(x[8 * i + 4], x[8 * i + 5]), pack_bf16x2(x[8 * i + 6], x[8 * i + 7]));
+}
+// 16 columns of a row as hi and lo rows of the workspace (32-byte aligned)
 TTT_DEVICE_INLINE void store16_pair(__nv_bfloat16* hi, __nv_bfloat16* lo, const float* x) {
   uint32_t h[8], l[8];
 #pragma unroll
@@ -291,6 +299,12 @@ TTT_DEVICE_INLINE void cta_end(Bars& b, const Phase& ph, int loads, uint32_t tme
 }  // namespace dl
 
 // ----------------------------------------------------------------- launches shared by both passes
+// Offsets of the workspace layouts count from here: 256-byte aligned and less
+// than 256 bytes before the caller's 16-byte aligned pointer, so offset 512 is
+// behind its status block.
+inline uint8_t* delta_ws_base(uint8_t* ws) {
+  return reinterpret_cast<uint8_t*>(reinterpret_cast<uintptr_t>(ws) & ~uintptr_t(255));
+}
 struct DeltaPrepOut {       // device buffers, per chunk of all heads
   float *gend, *H, *U;              // U: Ut, float32 tiles
   __nv_bfloat16 *W, *M, *T;         // hi, lo; T nullable

@@ -33,7 +33,7 @@ using namespace dl;
 
 namespace {
 
-constexpr int THREADS = 256;
+constexpr int THREADS = 512;        // four column groups of 128 rows
 
 TTT_DEVICE_INLINE void zero16(float* x) {
 #pragma unroll
@@ -45,12 +45,9 @@ TTT_DEVICE_INLINE void store16_square(uint32_t base, int row, int c0, const floa
   store8_split(hi, lo, row, c0 & 63, x);
   store8_split(hi, lo, row, (c0 & 63) + 8, x + 8);
 }
-TTT_DEVICE_INLINE void store_bf16_row32(__nv_bfloat16* p, const float* x) {
-  uint4* dst = reinterpret_cast<uint4*>(p);
-#pragma unroll
-  for (int j = 0; j < 4; ++j)
-    dst[j] = make_uint4(pack_bf16x2(x[8 * j], x[8 * j + 1]), pack_bf16x2(x[8 * j + 2], x[8 * j + 3]),
-                        pack_bf16x2(x[8 * j + 4], x[8 * j + 5]), pack_bf16x2(x[8 * j + 6], x[8 * j + 7]));
+// the column groups' sums of a row, [group][row]
+TTT_DEVICE_INLINE float row_total(const float* red, int row) {
+  return (red[row] + red[C + row]) + (red[2 * C + row] + red[3 * C + row]);
 }
 
 struct ChunkId {
@@ -87,7 +84,7 @@ struct HbSmem {
 };
 
 template <int D>
-__global__ void __launch_bounds__(THREADS)
+__global__ void __launch_bounds__(THREADS, 1)
     delta_hb_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_constant__ CUtensorMap mapK,
                     const __grid_constant__ CUtensorMap mapD, const __grid_constant__ CUtensorMap mapW,
                     const __grid_constant__ CUtensorMap mapY, HbArgs a) {
@@ -101,7 +98,7 @@ __global__ void __launch_bounds__(THREADS)
   const ChunkId id(DA, a.nch, a.N);
   const uint32_t tmem = cta_begin(bars, TM_COLS, tid), sb = smem_u32(smem);
   Phase ph{Waiter{&bars.abort, a.st, 1300}, &bars.mma, 0};
-  const int q4 = warp & 3, hf = warp >> 2, row = q4 * 32 + lane;
+  const int q4 = warp & 3, cg = warp >> 2, row = q4 * 32 + lane;
   const uint32_t lanes = (uint32_t)(q4 * 32) << 16;
   if (tid == 0) {
     mbar_arrive_expect_tx(&bars.load[0], 4 * DA * ATOM + ATOM);
@@ -113,7 +110,7 @@ __global__ void __launch_bounds__(THREADS)
     }
     tma_load_3d(smem + SM::DO, &mapD, &bars.load[0], 64 * id.slice, id.t0, (int)id.bh);
   }
-  if (hf == 1) load_gates(gates, a.g ? a.g + id.tok : nullptr, a.beta + id.tok, id.n, row);
+  if (cg == 1) load_gates(gates, a.g ? a.g + id.tok : nullptr, a.beta + id.tok, id.n, row);
   auto work = [&]() {
     if (!ph.wait(&bars.load[0], 0, 1)) return;
     const Op dOmn{sb + SM::DO, ATOM, true}, Qmn{sb + SM::Q, ATOM, true};
@@ -123,8 +120,8 @@ __global__ void __launch_bounds__(THREADS)
     }
     if (!ph.mma_done(2)) return;
 #pragma unroll
-    for (int b = 0; b < 4; ++b) {
-      const int c0 = hf * 64 + b * 16;
+    for (int b = 0; b < 2; ++b) {
+      const int c0 = cg * 32 + b * 16;
       float x[16];
       if (c0 <= q4 * 32 + 31) {
         tmem_ld16(tmem + lanes + TM_P + c0, x);
@@ -132,7 +129,7 @@ __global__ void __launch_bounds__(THREADS)
       } else {
         zero16(x);
       }
-      const uint32_t at = sb + SM::P + (uint32_t)hf * ATOM;   // [plane][column atom]
+      const uint32_t at = sb + SM::P + (uint32_t)(cg >> 1) * ATOM;   // [plane][column atom]
 #pragma unroll
       for (int i = 0; i < 16; i += 8)
         store8_split3(at, at + 2 * ATOM, at + 4 * ATOM, row, (c0 & 63) + i, x + i);
@@ -145,21 +142,21 @@ __global__ void __launch_bounds__(THREADS)
     }
     if (!ph.mma_done(3)) return;
     {
-      float u[32];
-      tmem_ld32(tmem + lanes + TM_U + hf * 32, u);
+      float u[16];
+      tmem_ld16(tmem + lanes + TM_U + cg * 16, u);
       const float f = a.scale * gate_decay(gates, row);
 #pragma unroll
-      for (int j = 0; j < 32; j += 8) {
+      for (int j = 0; j < 16; j += 8) {
         float d[8];
-        load8(sb + SM::DO, row, hf * 32 + j, d);
+        load8(sb + SM::DO, row, cg * 16 + j, d);
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
           u[j + i] *= -a.scale;
           d[i] *= f;
         }
         const uint32_t at = sb + SM::P;
-        store8_split3(at, at + ATOM, at + 2 * ATOM, row, hf * 32 + j, u + j);
-        store8_split3(at + 3 * ATOM, at + 4 * ATOM, at + 5 * ATOM, row, hf * 32 + j, d);
+        store8_split3(at, at + ATOM, at + 2 * ATOM, row, cg * 16 + j, u + j);
+        store8_split3(at + 3 * ATOM, at + 4 * ATOM, at + 5 * ATOM, row, cg * 16 + j, d);
       }
     }
     ph.publish();
@@ -178,12 +175,9 @@ __global__ void __launch_bounds__(THREADS)
     }
     if (!ph.mma_done(4)) return;
     const int r = D == 64 ? q4 * 16 + lane : row;
-#pragma unroll
-    for (int j = 0; j < 32; j += 16) {
-      float h[16];
-      tmem_ld16(tmem + lanes + TM_H + hf * 32 + j, h);
-      if (D == 128 || lane < 16) store_tile16(a.H + id.ci * D * D, D, r, id.slice * 64 + hf * 32 + j, h);
-    }
+    float h[16];
+    tmem_ld16(tmem + lanes + TM_H + cg * 16, h);
+    if (D == 128 || lane < 16) store_tile16(a.H + id.ci * D * D, D, r, id.slice * 64 + cg * 16, h);
   };
   work();
   cta_end(bars, ph, 1, tmem, TM_COLS, tid);
@@ -206,11 +200,12 @@ struct ValsSmem {
   static constexpr uint32_t SA = D * 128;
   static constexpr uint32_t T = 0;                            // W first
   static constexpr uint32_t K = 4 * ATOM, S = K + DA * ATOM, X = S + 2 * SA, U = X + 2 * SA, Y = U + 2 * ATOM;
-  static constexpr uint32_t GATES = Y + 2 * ATOM, RED = GATES + sizeof(Gates), BAR = RED + C * 4, TOTAL = BAR + 64;
+  static constexpr uint32_t RED = K;                          // behind the first products
+  static constexpr uint32_t GATES = Y + 2 * ATOM, BAR = GATES + sizeof(Gates), TOTAL = BAR + 64;
 };
 
 template <int D>
-__global__ void __launch_bounds__(THREADS)
+__global__ void __launch_bounds__(THREADS, 1)
     delta_vals_kernel(const __grid_constant__ CUtensorMap mapK, const __grid_constant__ CUtensorMap mapW,
                       const __grid_constant__ CUtensorMap mapU, const __grid_constant__ CUtensorMap mapY,
                       const __grid_constant__ CUtensorMap mapT, const __grid_constant__ CUtensorMap mapS,
@@ -226,7 +221,7 @@ __global__ void __launch_bounds__(THREADS)
   const ChunkId id(DA, a.nch, a.N);
   const uint32_t tmem = cta_begin(bars, TM_COLS, tid), sb = smem_u32(smem);
   Phase ph{Waiter{&bars.abort, a.st, 1400}, &bars.mma, 0};
-  const int q4 = warp & 3, hf = warp >> 2, row = q4 * 32 + lane;
+  const int q4 = warp & 3, cg = warp >> 2, row = q4 * 32 + lane;
   const uint32_t lanes = (uint32_t)(q4 * 32) << 16;
   if (tid == 0) {
     mbar_arrive_expect_tx(&bars.load[0], 3 * DA * ATOM + 2 * ATOM + 4 * SM::SA);
@@ -242,7 +237,7 @@ __global__ void __launch_bounds__(THREADS)
       tma_load_3d(smem + SM::Y + h * ATOM, &mapY, &bars.load[0], x, 0, z);
     }
   }
-  if (hf == 1) load_gates(gates, a.g ? a.g + id.tok : nullptr, a.beta + id.tok, id.n, row);
+  if (cg == 1) load_gates(gates, a.g ? a.g + id.tok : nullptr, a.beta + id.tok, id.n, row);
   int loads = 1;
   auto work = [&]() {
     if (!ph.wait(&bars.load[0], 0, 1)) return;
@@ -266,27 +261,22 @@ __global__ void __launch_bounds__(THREADS)
     // U = Ut - W S0;  dU = rho K X1 - (-scale P^T dO), in place
     {
       const float rho = gate_ratio(gates, C - 1, row);
+      const int c = cg * 16;
+      float w[16], x[16], u[16], y[16];
+      load_tile16(a.Ut + id.ci * C * D, C, row, id.slice * 64 + c, u);
+      tmem_ld16(tmem + lanes + TM_W + c, w);
+      tmem_ld16(tmem + lanes + TM_X + c, x);
 #pragma unroll
-      for (int j = 0; j < 32; j += 16) {
-        const int c = hf * 32 + j;
-        float w[16], x[16], u[16], y[16];
-        tmem_ld16(tmem + lanes + TM_W + c, w);
-        tmem_ld16(tmem + lanes + TM_X + c, x);
-        load_tile16(a.Ut + id.ci * C * D, C, row, id.slice * 64 + c, u);
+      for (int b = 0; b < 16; b += 8) load8_split(sb + SM::Y, sb + SM::Y + ATOM, row, c + b, y + b);
 #pragma unroll
-        for (int b = 0; b < 16; b += 8) {
-          load8_split(sb + SM::Y, sb + SM::Y + ATOM, row, c + b, y + b);
-        }
+      for (int i = 0; i < 16; ++i) {
+        u[i] -= w[i];
+        y[i] = fmaf(rho, x[i], -y[i]);
+      }
 #pragma unroll
-        for (int i = 0; i < 16; ++i) {
-          u[i] -= w[i];
-          y[i] = fmaf(rho, x[i], -y[i]);
-        }
-#pragma unroll
-        for (int b = 0; b < 16; b += 8) {
-          store8_split(sb + SM::U, sb + SM::U + ATOM, row, c + b, u + b);
-          store8_split(sb + SM::Y, sb + SM::Y + ATOM, row, c + b, y + b);
-        }
+      for (int b = 0; b < 16; b += 8) {
+        store8_split(sb + SM::U, sb + SM::U + ATOM, row, c + b, u + b);
+        store8_split(sb + SM::Y, sb + SM::Y + ATOM, row, c + b, y + b);
       }
     }
     ph.publish();
@@ -301,19 +291,19 @@ __global__ void __launch_bounds__(THREADS)
       }
     }
     if (!ph.mma_done(4)) return;
-    float acc = 0.f;
     {
+      float acc = 0.f;
       const float beta = gates.beta[row], gam = gate_decay(gates, row);
-      const size_t at = (id.tok + row) * D + id.slice * 64 + hf * 32;
-      float y[32], z[32];
-      tmem_ld32(tmem + lanes + TM_Y + hf * 32, y);
-      tmem_ld32(tmem + lanes + TM_Z + hf * 32, z);
+      const size_t at = (id.tok + row) * D + id.slice * 64 + cg * 16;
+      float y[16], z[16];
+      tmem_ld16(tmem + lanes + TM_Y + cg * 16, y);
+      tmem_ld16(tmem + lanes + TM_Z + cg * 16, z);
 #pragma unroll
-      for (int j = 0; j < 32; j += 8) store8_split(sb + SM::Y, sb + SM::Y + ATOM, row, hf * 32 + j, y + j);
+      for (int j = 0; j < 16; j += 8) store8_split(sb + SM::Y, sb + SM::Y + ATOM, row, cg * 16 + j, y + j);
       if (row < id.n) {
         const uint4* vp = reinterpret_cast<const uint4*>(a.v + at);
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
+        for (int j = 0; j < 2; ++j) {
           const uint4 t = vp[j];
           const uint32_t w[4] = {t.x, t.y, t.z, t.w};
 #pragma unroll
@@ -323,10 +313,10 @@ __global__ void __launch_bounds__(THREADS)
           }
         }
 #pragma unroll
-        for (int j = 0; j < 32; ++j) y[j] *= beta;
-        store_bf16_row32(a.dv + at, y);
+        for (int j = 0; j < 16; ++j) y[j] *= beta;
+        store_bf16_row16(a.dv + at, y);
       }
-      if (hf == 1) red[row] = acc;
+      red[cg * C + row] = acc;
     }
     ph.publish();
     if (tid == 0) {
@@ -334,7 +324,7 @@ __global__ void __launch_bounds__(THREADS)
         tma_store_3d(&mapY, smem + SM::Y + h * ATOM, 64 * id.slice, 0, (int)(2 * id.ci + h));
       bulk_commit();
     }
-    if (hf == 0 && row < id.n) a.bpart[id.slice * a.tokens + id.tok + row] = acc + red[row];
+    if (cg == 0 && row < id.n) a.bpart[id.slice * a.tokens + id.tok + row] = row_total(red, row);
   };
   work();
   cta_end(bars, ph, loads, tmem, TM_COLS, tid);
@@ -362,11 +352,12 @@ struct KeysSmem {
   static constexpr uint32_t U = MQ + 4 * ATOM;                // then Mk
   static constexpr uint32_t Y = U + 4 * ATOM;                 // then K, Q (this slice)
   static constexpr uint32_t YB = 2 * DA * ATOM;
-  static constexpr uint32_t GATES = Y + YB, RED = GATES + sizeof(Gates), BAR = RED + C * 4, TOTAL = BAR + 64;
+  static constexpr uint32_t RED = DO;                         // behind the first products
+  static constexpr uint32_t GATES = Y + YB, XS = GATES + sizeof(Gates), BAR = XS + 64, TOTAL = BAR + 64;
 };
 
 template <int D>
-__global__ void __launch_bounds__(THREADS)
+__global__ void __launch_bounds__(THREADS, 1)
     delta_keys_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_constant__ CUtensorMap mapK,
                       const __grid_constant__ CUtensorMap mapD, const __grid_constant__ CUtensorMap mapU,
                       const __grid_constant__ CUtensorMap mapY, const __grid_constant__ CUtensorMap mapS,
@@ -378,12 +369,12 @@ __global__ void __launch_bounds__(THREADS)
   extern __shared__ __align__(1024) uint8_t smem[];
   Bars& bars = *reinterpret_cast<Bars*>(smem + SM::BAR);
   Gates& gates = *reinterpret_cast<Gates*>(smem + SM::GATES);
-  float* red = reinterpret_cast<float*>(smem + SM::RED);
+  float *red = reinterpret_cast<float*>(smem + SM::RED), *xs = reinterpret_cast<float*>(smem + SM::XS);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const ChunkId id(DA, a.nch, a.N);
   const uint32_t tmem = cta_begin(bars, TM_COLS, tid), sb = smem_u32(smem);
   Phase ph{Waiter{&bars.abort, a.st, 1500}, &bars.mma, 0};
-  const int q4 = warp & 3, hf = warp >> 2, row = q4 * 32 + lane;
+  const int q4 = warp & 3, cg = warp >> 2, row = q4 * 32 + lane;
   const uint32_t lanes = (uint32_t)(q4 * 32) << 16;
   if (tid == 0) {
     mbar_arrive_expect_tx(&bars.load[0], 5 * DA * ATOM + 4 * DA * SM::HA);
@@ -398,7 +389,7 @@ __global__ void __launch_bounds__(THREADS)
       }
     }
   }
-  if (hf == 1) load_gates(gates, a.g ? a.g + id.tok : nullptr, a.beta + id.tok, id.n, row);
+  if (cg == 1) load_gates(gates, a.g ? a.g + id.tok : nullptr, a.beta + id.tok, id.n, row);
   int loads = 1;
   auto work = [&]() {
     if (!ph.wait(&bars.load[0], 0, 1)) return;
@@ -425,7 +416,7 @@ __global__ void __launch_bounds__(THREADS)
         for (int i = 0; i < 8; ++i) acc = fmaf(s[i], x[i], acc);
       }
       for (int o = 16; o > 0; o >>= 1) acc += __shfl_xor_sync(0xffffffffu, acc, o);
-      if (lane == 0) red[warp] = acc;
+      if (lane == 0) xs[warp] = acc;
     }
     if (!ph.mma_done(2)) return;
     if (tid == 0) {   // K and Q take Y's place
@@ -434,13 +425,13 @@ __global__ void __launch_bounds__(THREADS)
         tma_load_3d(smem + SM::Y + i * ATOM, &mapK, &bars.load[1], 64 * i, id.t0, (int)id.bh);
       tma_load_3d(smem + SM::Y + DA * ATOM, &mapQ, &bars.load[1], 64 * id.slice, id.t0, (int)id.bh);
       float acc = 0.f;
-      for (int w = 0; w < THREADS / 32; ++w) acc += red[w];
+      for (int w = 0; w < THREADS / 32; ++w) acc += xs[w];
       a.xpart[id.slice * a.chunks + id.ci] = acc;
     }
     loads = 2;
 #pragma unroll
-    for (int b = 0; b < 4; ++b) {
-      const int c0 = hf * 64 + b * 16;
+    for (int b = 0; b < 2; ++b) {
+      const int c0 = cg * 32 + b * 16;
       float x[16];
       if (c0 <= q4 * 32 + 31) {
         tmem_ld16(tmem + lanes + TM_P + c0, x);
@@ -463,8 +454,8 @@ __global__ void __launch_bounds__(THREADS)
     float db = 0.f;
     const float beta = gates.beta[row];
 #pragma unroll
-    for (int b = 0; b < 4; ++b) {
-      const int c0 = hf * 64 + b * 16;
+    for (int b = 0; b < 2; ++b) {
+      const int c0 = cg * 32 + b * 16;
       float x[16];
       if (c0 <= q4 * 32 + 31) {
         float kk[16];
@@ -481,7 +472,7 @@ __global__ void __launch_bounds__(THREADS)
       }
       store16_square(sb + SM::U, row, c0, x);
     }
-    if (hf == 1) red[row] = db;
+    red[cg * C + row] = db;
     ph.publish();
     const Op Kmn{sb + SM::Y + id.slice * ATOM, ATOM, true}, Qmn{sb + SM::Y + DA * ATOM, ATOM, true};
     if (tid == 0) {
@@ -497,65 +488,54 @@ __global__ void __launch_bounds__(THREADS)
       product(tmem + TM_KW, Mkt.hi, Kmn, 128, 64, 8, true);
       mma_commit(&bars.mma);
     }
-    if (hf == 0 && id.slice == 0 && row < id.n) a.bkey[id.tok + row] = db + red[row];
+    if (cg == 0 && id.slice == 0 && row < id.n) a.bkey[id.tok + row] = row_total(red, row);
     if (!ph.mma_done(5)) return;
     const float gam = gate_decay(gates, row), rho = gate_ratio(gates, C - 1, row);
     const float fq = a.scale * gam, fy = -gam * beta;
-    const size_t at = (id.tok + row) * D + id.slice * 64 + hf * 32;
+    const int c = cg * 16;
+    const size_t at = (id.tok + row) * D + id.slice * 64 + c;
     float rs = 0.f, ws = 0.f;
+    float x[16], y[16], z[16], t[16];
+    // dq
+    tmem_ld16(tmem + lanes + TM_QS + c, x);
+    tmem_ld16(tmem + lanes + TM_QK + c, y);
+    load8(sb + SM::Y + DA * ATOM, row, c, t);
+    load8(sb + SM::Y + DA * ATOM, row, c + 8, t + 8);
 #pragma unroll
-    for (int j = 0; j < 32; j += 16) {
-      const int c = hf * 32 + j;
-      float x[16], y[16], t[16];
-      // dq
-      tmem_ld16(tmem + lanes + TM_QS + c, x);
-      tmem_ld16(tmem + lanes + TM_QK + c, y);
-      load8(sb + SM::Y + DA * ATOM, row, c, t);
-      load8(sb + SM::Y + DA * ATOM, row, c + 8, t + 8);
-#pragma unroll
-      for (int i = 0; i < 16; ++i) {
-        x[i] = fmaf(fq, x[i], y[i]);
-        rs = fmaf(t[i], x[i], rs);
-      }
-      if (row < id.n) {
-        uint4* d = reinterpret_cast<uint4*>(a.dq + at + j);
-        d[0] = make_uint4(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]), pack_bf16x2(x[4], x[5]), pack_bf16x2(x[6], x[7]));
-        d[1] = make_uint4(pack_bf16x2(x[8], x[9]), pack_bf16x2(x[10], x[11]), pack_bf16x2(x[12], x[13]), pack_bf16x2(x[14], x[15]));
-      }
-      // dk: read part less the second one for rs, third for ws
-      load8(sb + SM::Y + id.slice * ATOM, row, c, t);
-      load8(sb + SM::Y + id.slice * ATOM, row, c + 8, t + 8);
-      float z[16];
-      tmem_ld16(tmem + lanes + TM_KR + c, x);
-      tmem_ld16(tmem + lanes + TM_YS + c, y);
-      tmem_ld16(tmem + lanes + TM_KW + c, z);
-#pragma unroll
-      for (int i = 0; i < 16; ++i) {
-        x[i] = fmaf(fy, y[i], x[i]);
-        rs = fmaf(t[i], x[i] - z[i], rs);
-        x[i] += z[i];
-      }
-      tmem_ld16(tmem + lanes + TM_UX + c, y);
-#pragma unroll
-      for (int i = 0; i < 16; ++i) {
-        const float w = rho * y[i];
-        ws = fmaf(t[i], w, ws);
-        x[i] += w;
-      }
-      if (row < id.n) {
-        uint4* d = reinterpret_cast<uint4*>(a.dk + at + j);
-        d[0] = make_uint4(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]), pack_bf16x2(x[4], x[5]), pack_bf16x2(x[6], x[7]));
-        d[1] = make_uint4(pack_bf16x2(x[8], x[9]), pack_bf16x2(x[10], x[11]), pack_bf16x2(x[12], x[13]), pack_bf16x2(x[14], x[15]));
-      }
+    for (int i = 0; i < 16; ++i) {
+      x[i] = fmaf(fq, x[i], y[i]);
+      rs = fmaf(t[i], x[i], rs);
     }
-    if (hf == 1) red[row] = rs;
+    if (row < id.n) store_bf16_row16(a.dq + at, x);
+    // dk: read part less the second one for rs, third for ws
+    load8(sb + SM::Y + id.slice * ATOM, row, c, t);
+    load8(sb + SM::Y + id.slice * ATOM, row, c + 8, t + 8);
+    tmem_ld16(tmem + lanes + TM_KR + c, x);
+    tmem_ld16(tmem + lanes + TM_YS + c, y);
+    tmem_ld16(tmem + lanes + TM_KW + c, z);
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      x[i] = fmaf(fy, y[i], x[i]);
+      rs = fmaf(t[i], x[i] - z[i], rs);
+      x[i] += z[i];
+    }
+    tmem_ld16(tmem + lanes + TM_UX + c, y);
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      const float w = rho * y[i];
+      ws = fmaf(t[i], w, ws);
+      x[i] += w;
+    }
+    if (row < id.n) store_bf16_row16(a.dk + at, x);
+    float* wred = red + 4 * C;
+    red[cg * C + row] = rs;
+    wred[cg * C + row] = ws;
     __syncthreads();
-    const size_t o = id.slice * a.tokens + id.tok + row;
-    if (hf == 0 && row < id.n) a.rpart[o] = rs + red[row];
-    __syncthreads();
-    if (hf == 1) red[row] = ws;
-    __syncthreads();
-    if (hf == 0 && row < id.n) a.wpart[o] = ws + red[row];
+    if (cg == 0 && row < id.n) {
+      const size_t o = id.slice * a.tokens + id.tok + row;
+      a.rpart[o] = row_total(red, row);
+      a.wpart[o] = row_total(wred, row);
+    }
   };
   work();
   cta_end(bars, ph, loads, tmem, TM_COLS, tid);
@@ -630,8 +610,9 @@ int bwd_launch(const DeltaBwdLaunch& L, cudaStream_t stream) {
   const DeltaUmmaBwdWorkspace w = delta_umma_bwd_layout(BH, p.N, D);
   const uint64_t nc = (uint64_t)BH * nch, rs = D * 2;
   const size_t tokens = (size_t)BH * p.N;
-  auto bf = [&](size_t at) { return reinterpret_cast<__nv_bfloat16*>(L.ws + at); };
-  auto f32 = [&](size_t at) { return reinterpret_cast<float*>(L.ws + at); };
+  uint8_t* ws = delta_ws_base(L.ws);
+  auto bf = [&](size_t at) { return reinterpret_cast<__nv_bfloat16*>(ws + at); };
+  auto f32 = [&](size_t at) { return reinterpret_cast<float*>(ws + at); };
   const __nv_bfloat16 *g = (const __nv_bfloat16*)p.g, *beta = (const __nv_bfloat16*)p.beta;
   const DeltaPrepOut o{f32(w.gend), f32(w.H), f32(w.Ut), bf(w.W), bf(w.M), bf(w.T)};
   const DeltaChain fwd{o.H, L.S0, nullptr, bf(w.X)}, rev{f32(w.Hb), L.dS_end, L.dS0, bf(w.X1)};
@@ -640,8 +621,8 @@ int bwd_launch(const DeltaBwdLaunch& L, cudaStream_t stream) {
       make_tmap_bf16_3d(&mk, p.k, D, p.N, BH, rs, p.N * rs, 64, C) ||
       make_tmap_bf16_3d(&md, L.dout, D, p.N, BH, rs, p.N * rs, 64, C) ||
       make_tmap_bf16_3d(&mw, o.W, D, C, 2 * nc, rs, C * rs, 64, C) ||
-      make_tmap_bf16_3d(&mu, L.ws + w.U, D, C, 2 * nc, rs, C * rs, 64, C) ||
-      make_tmap_bf16_3d(&my, L.ws + w.Y, D, C, 2 * nc, rs, C * rs, 64, C) ||
+      make_tmap_bf16_3d(&mu, ws + w.U, D, C, 2 * nc, rs, C * rs, 64, C) ||
+      make_tmap_bf16_3d(&my, ws + w.Y, D, C, 2 * nc, rs, C * rs, 64, C) ||
       make_tmap_bf16_3d(&mt, o.T, C, C, 2 * nc, 2 * C, 2 * C * C, 64, C) ||
       make_tmap_bf16_3d(&ms, fwd.X, D, D, 2 * nc, rs, D * rs, 64, D) ||
       make_tmap_bf16_3d(&mx, rev.X, D, D, 2 * nc, rs, D * rs, 64, D) ||
@@ -684,7 +665,7 @@ int bwd_launch(const DeltaBwdLaunch& L, cudaStream_t stream) {
 DeltaUmmaBwdWorkspace delta_umma_bwd_layout(int BH, int N, int D) {
   DeltaUmmaBwdWorkspace w{};
   const size_t nc = (size_t)BH * ((N + C - 1) / C), tokens = (size_t)BH * N, DA = D / 64;
-  size_t at = 256;
+  size_t at = 512;
   auto take = [&](size_t bytes) {
     const size_t o = at;
     at += (bytes + 255) / 256 * 256;

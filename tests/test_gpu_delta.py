@@ -224,6 +224,32 @@ def test_same_bits_twice_and_after_another_call(cuda_device, d):
     assert all(torch.equal(x, y) for x, y in zip(p.bwd(), p.bwd()))
 
 
+@pytest.mark.parametrize("dt,d", [("bf16", 64), ("bf16", 128), ("bf16", 40), ("f32", 24)])
+def test_tensors_aligned_to_16_bytes_only(cuda_device, dt, d):
+    """Every tensor and the workspace 16 bytes behind a 256-byte boundary: the same bits."""
+    p = Problem(1, 2, 200, d, d, dt)
+    want_f, want_b = p.fwd(), p.bwd()
+
+    def shifted(t):
+        n = t.numel() * t.element_size()
+        raw = torch.zeros(n + 512, dtype=torch.uint8, device="cuda")
+        off = -raw.data_ptr() % 256 + 16
+        out = raw[off:off + n].view(t.dtype).view(t.shape)
+        out.copy_(t)
+        return out
+
+    desc, x = p.desc(), {n: shifted(t) for n, t in p.dev.items()}
+    S, S0, dS, o = shifted(p.S0), shifted(p.S0), shifted(p.dS), shifted(torch.zeros_like(p.dev["v"]))
+    g = [shifted(t) for t in p.new_grads()]
+    nf, nb = T.ttt_delta_workspace_bytes(desc), T.ttt_delta_bwd_workspace_bytes(desc)
+    wf, wb = (shifted(torch.zeros(n, dtype=torch.uint8, device="cuda")) for n in (nf, nb))
+    T.ttt_delta_fwd(desc, x["q"], x["k"], x["v"], x["g"], x["beta"], S, o, wf)
+    T.ttt_delta_bwd(desc, x["q"], x["k"], x["v"], x["g"], x["beta"], S0, x["dout"], dS, *g, wb)
+    assert T.ttt_check_device_status(wf) == T.TTT_OK and T.ttt_check_device_status(wb) == T.TTT_OK
+    assert torch.equal(o, want_f[0]) and torch.equal(S, want_f[1])
+    assert all(torch.equal(a, b) for a, b in zip(g, want_b))
+
+
 @pytest.mark.parametrize("dt,d", [("f32", 32), ("bf16", 64), ("bf16", 128)])
 def test_captured_calls_replay(cuda_device, dt, d):
     """Forward, backward and step in one graph on another stream; replays on new
