@@ -5,11 +5,16 @@
 //   a_t = exp(g_t);  e_t = v_t - a_t S^T k_t;  S <- a_t S + beta_t k_t e_t^T;  o_t = scale S^T q_t
 //
 // The value columns of S never mix, so a column of S and its entry of e, v
-// and o live in 8 neighbouring lanes (16 rows each, in registers) for the
-// whole sequence, and a CTA of 16 columns needs no other CTA.  Per token the
-// chain is one dot product over dk (16 FMA and 3 shuffles), so the kernels
-// are bound by that latency (about 0.08 us a token at dk = 128), not by
-// memory; the chunked tensor-core kernels take the sizes where it matters.
+// and o live in 8 neighbouring lanes (up to 16 rows each, in registers) for
+// the whole sequence, and a CTA of 16 columns needs no other CTA.  Tokens go
+// four at a time: with s the state before them, A_t the product of the decays
+// up to t and R_ti that of the decays behind i up to t,
+//   u_t = beta_t (v_t - A_t k_t.s - sum_{i<t} R_ti (k_t.k_i) u_i)
+//   o_t = scale (A_t q_t.s + sum_{i<=t} R_ti (q_t.k_i) u_i),  s <- A_3 s + sum_i R_3i k_i u_i
+// so one reduction over the lanes serves eight dot products, and the products
+// of tokens with one another are shared by the CTA's columns.  Bound by the
+// latency of that chain; the chunked tensor-core kernels (delta_umma.cu) take
+// the sizes where it matters.
 #include <algorithm>
 #include <type_traits>
 
@@ -22,9 +27,9 @@ namespace {
 constexpr int L = 8;            // lanes of one column
 constexpr int COLS = 16;        // columns of a CTA
 constexpr int THREADS = L * COLS;
-constexpr int TT = 16;          // tokens staged at a time
+constexpr int TT = 32;          // tokens staged at a time, and between kept states
+constexpr int NB = TT / 4;      // blocks of four tokens
 constexpr int DMAX = 128;
-constexpr int RV = DMAX / (4 * L);   // float4 row groups of a lane: rows 4 (lane + L i) + 0..3
 
 TTT_DEVICE_INLINE float to_f(float x) { return x; }
 TTT_DEVICE_INLINE float to_f(__nv_bfloat16 x) { return __bfloat162float(x); }
@@ -34,144 +39,234 @@ TTT_DEVICE_INLINE T from_f(float x) {
   else return __float2bfloat16_rn(x);
 }
 
-TTT_DEVICE_INLINE float sum8(float x) {
-  x += __shfl_xor_sync(0xffffffffu, x, 1);
-  x += __shfl_xor_sync(0xffffffffu, x, 2);
-  x += __shfl_xor_sync(0xffffffffu, x, 4);
-  return x;
-}
-
-// rows of this lane in a zero-padded row of DMAX floats
-TTT_DEVICE_INLINE void load_rows(const float* row, int l, float (&x)[4 * RV]) {
-#pragma unroll
-  for (int i = 0; i < RV; ++i) {
-    const float4 t = *reinterpret_cast<const float4*>(row + 4 * (l + L * i));
-    x[4 * i] = t.x; x[4 * i + 1] = t.y; x[4 * i + 2] = t.z; x[4 * i + 3] = t.w;
-  }
-}
-TTT_DEVICE_INLINE float dot_rows(const float (&x)[4 * RV], const float (&y)[4 * RV]) {
-  float a = 0.f, b = 0.f, c = 0.f, d = 0.f;
-#pragma unroll
-  for (int i = 0; i < RV; ++i) {
-    a = fmaf(x[4 * i], y[4 * i], a);
-    b = fmaf(x[4 * i + 1], y[4 * i + 1], b);
-    c = fmaf(x[4 * i + 2], y[4 * i + 2], c);
-    d = fmaf(x[4 * i + 3], y[4 * i + 3], d);
-  }
-  return sum8((a + b) + (c + d));
-}
-
-struct Column {   // this thread's column of a [dk][dv] matrix
+// This thread's rows 4 (lane + 8 i) + 0..3, i < R4, of a column of a [dk][dv] matrix.
+template <int R4>
+struct Column {
   int l, c, dk, dv;
   bool live;
-  // row of register 4 i + j
   TTT_DEVICE_INLINE int row(int i, int j) const { return 4 * (l + L * i) + j; }
-  TTT_DEVICE_INLINE void load(const float* S, float (&s)[4 * RV]) const {
+  TTT_DEVICE_INLINE void load(const float* S, float (&s)[4 * R4]) const {
 #pragma unroll
-    for (int i = 0; i < RV; ++i)
+    for (int i = 0; i < R4; ++i)
 #pragma unroll
       for (int j = 0; j < 4; ++j)
         s[4 * i + j] = (live && row(i, j) < dk) ? S[(size_t)row(i, j) * dv + c] : 0.f;
   }
-  TTT_DEVICE_INLINE void store(float* S, const float (&s)[4 * RV]) const {
+  TTT_DEVICE_INLINE void store(float* S, const float (&s)[4 * R4]) const {
 #pragma unroll
-    for (int i = 0; i < RV; ++i)
+    for (int i = 0; i < R4; ++i)
 #pragma unroll
       for (int j = 0; j < 4; ++j)
         if (live && row(i, j) < dk) S[(size_t)row(i, j) * dv + c] = s[4 * i + j];
   }
 };
 
-// Tokens [t0, t0 + TT) of two [N][D] tensors staged as zero-padded float rows
-// (xs, ys), of a value tensor (this CTA's columns) and of the gates.
-template <typename Tin>
+// Tokens [t0, t0 + TT) as zero-padded float rows (k, q), the CTA's columns of
+// a value tensor (w), the gates, and the coefficients of every block of four
+// tokens; rows 4 floats longer than the dims, so that a column of rows lies in
+// different banks.
+template <int R4>
 struct Stage {
-  float x[TT][DMAX], y[TT][DMAX], w[TT][COLS], a[TT], b[TT];
+  static constexpr int PITCH = 32 * R4 + 4;
+  float k[TT][PITCH], q[TT][PITCH], w[TT][COLS], a[TT], b[TT];
+  float A[TT], R[TT];            // A_t, R_3t
+  float kk[TT][4], qk[TT][4];    // R_ti k_t.k_i (i < t), R_ti q_t.k_i (i <= t); else 0
+  float os[TT][COLS];
 };
+
+// The next tile's tokens wait in registers while this one is worked on.
+template <typename Tin, int R4>
+struct Fetch {
+  static constexpr int NX = TT * 32 * R4 / THREADS, NW = TT * COLS / THREADS;
+  Tin k[NX], q[NX], w[NW], g, b;
+  int t0;
+  TTT_DEVICE_INLINE void load(const Tin* kp, const Tin* qp, const Tin* wp, const Tin* gp, const Tin* bp,
+                              size_t bh, int t0_, int N, int dk, int dv, int c0, int tid) {
+    t0 = t0_;
+#pragma unroll
+    for (int i = 0; i < NX; ++i) {
+      const int e = i * THREADS + tid, t = t0 + e / (32 * R4), r = e % (32 * R4);
+      const bool in = t >= 0 && t < N && r < dk;
+      const size_t at = (bh * N + t) * dk + r;
+      k[i] = in ? kp[at] : from_f<Tin>(0.f);
+      q[i] = in && qp != nullptr ? qp[at] : from_f<Tin>(0.f);
+    }
+#pragma unroll
+    for (int i = 0; i < NW; ++i) {
+      const int e = i * THREADS + tid, t = t0 + e / COLS, c = c0 + e % COLS;
+      w[i] = t >= 0 && t < N && c < dv ? wp[(bh * N + t) * dv + c] : from_f<Tin>(0.f);
+    }
+    g = b = from_f<Tin>(0.f);   // no decay, no step: a padding token
+    const int t = t0 + tid;
+    if (tid < TT && t >= 0 && t < N) {
+      if (gp != nullptr) g = gp[bh * N + t];
+      b = bp[bh * N + t];
+    }
+  }
+  TTT_DEVICE_INLINE void put(Stage<R4>& st, float wscale, int tid) const {
+#pragma unroll
+    for (int i = 0; i < NX; ++i) {
+      const int e = i * THREADS + tid;
+      st.k[e / (32 * R4)][e % (32 * R4)] = to_f(k[i]);
+      st.q[e / (32 * R4)][e % (32 * R4)] = to_f(q[i]);
+    }
+#pragma unroll
+    for (int i = 0; i < NW; ++i) (&st.w[0][0])[i * THREADS + tid] = wscale * to_f(w[i]);
+    if (tid < TT) {
+      st.a[tid] = expf(to_f(g));
+      st.b[tid] = to_f(b);
+    }
+  }
+};
+
+// Coefficients of the staged tokens: thread 16 b + d takes one of the 16
+// products within block b.
+template <int R4>
+TTT_DEVICE_INLINE void coefficients(Stage<R4>& st, int tid) {
+  const int base = tid / 16 * 4, d = tid % 16;
+  // d: 0..9 q.k with (t, i) in lower-triangle order, 10..15 k.k below the diagonal
+  constexpr unsigned long long TS = 0x3332213333222110ull, IS = 0x2101003210210100ull;
+  const int t = (int)(TS >> (4 * d) & 15), i = (int)(IS >> (4 * d) & 15);
+  const float* x = d < 10 ? st.q[base + t] : st.k[base + t];
+  const float* y = st.k[base + i];
+  float a0 = 0.f, a1 = 0.f, a2 = 0.f, a3 = 0.f;
+#pragma unroll
+  for (int r = 0; r < 32 * R4; r += 4) {
+    const float4 u = *reinterpret_cast<const float4*>(x + r), v = *reinterpret_cast<const float4*>(y + r);
+    a0 = fmaf(u.x, v.x, a0);
+    a1 = fmaf(u.y, v.y, a1);
+    a2 = fmaf(u.z, v.z, a2);
+    a3 = fmaf(u.w, v.w, a3);
+  }
+  float f = (a0 + a1) + (a2 + a3);
+  for (int m = i + 1; m <= t; ++m) f *= st.a[base + m];
+  if (d < 10) st.qk[base + t][i] = f;
+  else st.kk[base + t][i] = f;
+  if (tid < TT) {
+    const int b0 = tid & ~3;
+    float A = 1.f, R = 1.f;
+    for (int m = b0; m < b0 + 4; ++m) {
+      if (m <= tid) A *= st.a[m];
+      else R *= st.a[m];
+    }
+    st.A[tid] = A;
+    st.R[tid] = R;
+#pragma unroll
+    for (int m = 0; m < 4; ++m) {
+      if (m > (tid & 3)) st.qk[tid][m] = 0.f;
+      if (m >= (tid & 3)) st.kk[tid][m] = 0.f;
+    }
+  }
+}
+
+template <int R4>
+TTT_DEVICE_INLINE void load_rows(const float* row, int l, float (&x)[4 * R4]) {
+#pragma unroll
+  for (int i = 0; i < R4; ++i) {
+    const float4 t = *reinterpret_cast<const float4*>(row + 4 * (l + L * i));
+    x[4 * i] = t.x; x[4 * i + 1] = t.y; x[4 * i + 2] = t.z; x[4 * i + 3] = t.w;
+  }
+}
+template <int R4>
+TTT_DEVICE_INLINE float part_dot(const float (&x)[4 * R4], const float (&y)[4 * R4]) {
+  float a = 0.f, b = 0.f;
+#pragma unroll
+  for (int i = 0; i < 4 * R4; i += 2) {
+    a = fmaf(x[i], y[i], a);
+    b = fmaf(x[i + 1], y[i + 1], b);
+  }
+  return a + b;
+}
 
 // ------------------------------------------------------------------ forward
 // out may be null (the backward pass's replay); then e and the state at every
-// chunk border are kept: ev [BH][N][dv], Sc [BH][nch + 1][dk][dv].
-template <typename Tin, typename Tout>
+// chunk border (TT tokens) are kept: ev [BH][N][dv], Sc [BH][nch + 1][dk][dv].
+template <typename Tin, typename Tout, int R4>
 __global__ void __launch_bounds__(THREADS)
     delta_rec_kernel(const Tin* __restrict__ q, const Tin* __restrict__ k, const Tin* __restrict__ v,
                      const Tin* __restrict__ g, const Tin* __restrict__ beta, const float* S_in,
                      float* S_out, Tout* __restrict__ out, float* __restrict__ ev,
-                     float* __restrict__ Sc, int N, int dk, int dv, float scale, int border) {
-  __shared__ Stage<Tin> st;
-  __shared__ float os[TT][COLS];
+                     float* __restrict__ Sc, int N, int dk, int dv, float scale) {
+  __shared__ __align__(16) Stage<R4> st;
   const size_t bh = blockIdx.x;
-  const int c0 = blockIdx.y * COLS, tid = threadIdx.x;
-  const int cl = tid / L;
-  const Column col{tid % L, c0 + cl, dk, dv, c0 + cl < dv};
+  const int c0 = blockIdx.y * COLS, tid = threadIdx.x, cl = tid / L;
+  const Column<R4> col{tid % L, c0 + cl, dk, dv, c0 + cl < dv};
+  const int l = col.l, lt = l & 3;
   const size_t mat = (size_t)dk * dv;
-  float s[4 * RV];
+  float s[4 * R4];
   if (S_in != nullptr) {
     col.load(S_in + bh * mat, s);
   } else {
 #pragma unroll
-    for (int i = 0; i < 4 * RV; ++i) s[i] = 0.f;
+    for (int i = 0; i < 4 * R4; ++i) s[i] = 0.f;
   }
-  const int nch = Sc ? (N + border - 1) / border : 0;
-  // the next tile's tokens wait in registers while this one is worked on
-  constexpr int NX = TT * DMAX / THREADS, NW = TT * COLS / THREADS;
-  float rx[NX], ry[NX], rw[NW], ra = 0.f, rb = 0.f;
-  auto fetch = [&](int t0) {
-#pragma unroll
-    for (int i = 0; i < NX; ++i) {
-      const int t = t0 + (i * THREADS + tid) / DMAX, r = (i * THREADS + tid) % DMAX;
-      const bool in = t < N && r < dk;
-      const size_t at = (bh * N + t) * dk + r;
-      rx[i] = in ? to_f(k[at]) : 0.f;
-      ry[i] = in && out != nullptr ? to_f(q[at]) : 0.f;
-    }
-#pragma unroll
-    for (int i = 0; i < NW; ++i) {
-      const int t = t0 + (i * THREADS + tid) / COLS, c = c0 + (i * THREADS + tid) % COLS;
-      rw[i] = t < N && c < dv ? to_f(v[(bh * N + t) * dv + c]) : 0.f;
-    }
-    if (tid < TT && t0 + tid < N) {
-      ra = g != nullptr ? expf(to_f(g[bh * N + t0 + tid])) : 1.f;
-      rb = to_f(beta[bh * N + t0 + tid]);
-    }
-  };
-  fetch(0);
+  const int nch = (N + TT - 1) / TT;
+  Fetch<Tin, R4> f;
+  const Tin* qp = out != nullptr ? q : nullptr;
+  f.load(k, qp, v, g, beta, bh, 0, N, dk, dv, c0, tid);
   for (int t0 = 0; t0 < N; t0 += TT) {
-#pragma unroll
-    for (int i = 0; i < NX; ++i) {
-      (&st.x[0][0])[i * THREADS + tid] = rx[i];
-      (&st.y[0][0])[i * THREADS + tid] = ry[i];
-    }
-#pragma unroll
-    for (int i = 0; i < NW; ++i) (&st.w[0][0])[i * THREADS + tid] = rw[i];
-    if (tid < TT) { st.a[tid] = ra; st.b[tid] = rb; }
+    f.put(st, 1.f, tid);
     __syncthreads();
-    fetch(t0 + TT);
-    const int n = min(TT, N - t0);
-    for (int t = 0; t < n; ++t) {
-      if (Sc != nullptr && (t0 + t) % border == 0)
-        col.store(Sc + (bh * (nch + 1) + (t0 + t) / border) * mat, s);
-      float kk[4 * RV];
-      load_rows(st.x[t], col.l, kk);
-      const float a = st.a[t], e = st.w[t][cl] - a * dot_rows(kk, s), u = st.b[t] * e;
+    f.load(k, qp, v, g, beta, bh, t0 + TT, N, dk, dv, c0, tid);
+    coefficients(st, tid);
+    if (Sc != nullptr) col.store(Sc + (bh * (nch + 1) + t0 / TT) * mat, s);
+    __syncthreads();
+    const int n = min(TT, N - t0), nb = (n + 3) / 4;
+    for (int b = 0; b < nb; ++b) {
+      float kv[4][4 * R4], d[8];
 #pragma unroll
-      for (int i = 0; i < 4 * RV; ++i) s[i] = fmaf(kk[i], u, a * s[i]);
-      if (out != nullptr) {
-        float qq[4 * RV];
-        load_rows(st.y[t], col.l, qq);
-        const float o = dot_rows(qq, s);
-        if (col.l == 0) os[t][cl] = scale * o;
-      } else if (col.l == 0) {
-        os[t][cl] = e;
+      for (int t = 0; t < 4; ++t) {
+        load_rows<R4>(st.k[4 * b + t], l, kv[t]);
+        d[t] = part_dot<R4>(kv[t], s);
       }
+#pragma unroll
+      for (int t = 0; t < 4; ++t) {
+        float qv[4 * R4];
+        load_rows<R4>(st.q[4 * b + t], l, qv);
+        d[4 + t] = part_dot<R4>(qv, s);
+      }
+      // eight sums over eight lanes, halving the values a lane holds: k_t.s
+      // ends in lane t, q_t.s in lane 4 + t
+      float h[4], p2[2], mine;
+#pragma unroll
+      for (int t = 0; t < 4; ++t)
+        h[t] = ((l & 4) ? d[4 + t] : d[t]) + __shfl_xor_sync(0xffffffffu, (l & 4) ? d[t] : d[4 + t], 4);
+#pragma unroll
+      for (int t = 0; t < 2; ++t)
+        p2[t] = ((l & 2) ? h[2 + t] : h[t]) + __shfl_xor_sync(0xffffffffu, (l & 2) ? h[t] : h[2 + t], 2);
+      mine = ((l & 1) ? p2[1] : p2[0]) + __shfl_xor_sync(0xffffffffu, (l & 1) ? p2[0] : p2[1], 1);
+      float p[4], e[4], u[4];
+#pragma unroll
+      for (int t = 0; t < 4; ++t) p[t] = __shfl_sync(0xffffffffu, mine, t, 8);
+#pragma unroll
+      for (int t = 0; t < 4; ++t) e[t] = fmaf(-st.A[4 * b + t], p[t], st.w[4 * b + t][cl]);
+#pragma unroll
+      for (int t = 0; t < 4; ++t) {
+#pragma unroll
+        for (int i = 0; i < t; ++i) e[t] = fmaf(-st.kk[4 * b + t][i], u[i], e[t]);
+        u[t] = st.b[4 * b + t] * e[t];
+      }
+      if (out != nullptr) {
+        const float4 c = *reinterpret_cast<const float4*>(st.qk[4 * b + lt]);
+        const float o = fmaf(c.x, u[0], fmaf(c.y, u[1], fmaf(c.z, u[2], fmaf(c.w, u[3], st.A[4 * b + lt] * mine))));
+        if (l & 4) st.os[4 * b + lt][cl] = scale * o;
+      } else if (l < 4) {
+        st.os[4 * b + l][cl] = l == 0 ? e[0] : l == 1 ? e[1] : l == 2 ? e[2] : e[3];
+      }
+      const float A3 = st.A[4 * b + 3];
+#pragma unroll
+      for (int t = 0; t < 4; ++t) u[t] *= st.R[4 * b + t];
+#pragma unroll
+      for (int i = 0; i < 4 * R4; ++i)
+        s[i] = fmaf(kv[3][i], u[3], fmaf(kv[2][i], u[2], fmaf(kv[1][i], u[1], fmaf(kv[0][i], u[0], A3 * s[i]))));
     }
     __syncthreads();
     for (int i = tid; i < n * COLS; i += THREADS) {
       const int t = t0 + i / COLS, c = c0 + i % COLS;
       if (c >= dv) continue;
       const size_t at = (bh * N + t) * dv + c;
-      if (out != nullptr) out[at] = from_f<Tout>(os[i / COLS][i % COLS]);
-      else ev[at] = os[i / COLS][i % COLS];
+      if (out != nullptr) out[at] = from_f<Tout>(st.os[i / COLS][i % COLS]);
+      else ev[at] = st.os[i / COLS][i % COLS];
     }
   }
   if (Sc != nullptr) col.store(Sc + (bh * (nch + 1) + nch) * mat, s);
@@ -180,70 +275,89 @@ __global__ void __launch_bounds__(THREADS)
 
 // ------------------------------------------------------------------ reverse
 // X = dL/dS from the last token back:  X += scale q do^T;  du = X^T k;
-// X <- a (X - beta k du^T).  Kept: du [BH][N][dv], and X at the end of every
-// chunk of `border` tokens, Xc [BH][nch][dk][dv].
-template <typename Tin>
+// X <- a (X - beta k du^T).  Four tokens at a time, with X the value behind
+// them and f = beta du:
+//   du_t = R_3t k_t.X + sum_{s>=t} R_st (q_s.k_t) do_s - sum_{s>t} R_st (k_s.k_t) f_s
+//   X <- A_3 X + sum_s A_s (q_s do_s - k_s f_s)
+// Kept: du [BH][N][dv], and X at the end of every chunk of TT tokens, Xc
+// [BH][nch][dk][dv].
+template <typename Tin, int R4>
 __global__ void __launch_bounds__(THREADS)
     delta_rev_kernel(const Tin* __restrict__ q, const Tin* __restrict__ k,
                      const Tin* __restrict__ dout, const Tin* __restrict__ g,
                      const Tin* __restrict__ beta, const float* __restrict__ dS_end,
                      float* __restrict__ dS0, float* __restrict__ duv, float* __restrict__ Xc, int N,
-                     int dk, int dv, float scale, int border) {
-  __shared__ Stage<Tin> st;
-  __shared__ float os[TT][COLS];
+                     int dk, int dv, float scale) {
+  __shared__ __align__(16) Stage<R4> st;
   const size_t bh = blockIdx.x;
-  const int c0 = blockIdx.y * COLS, tid = threadIdx.x;
-  const int cl = tid / L;
-  const Column col{tid % L, c0 + cl, dk, dv, c0 + cl < dv};
+  const int c0 = blockIdx.y * COLS, tid = threadIdx.x, cl = tid / L;
+  const Column<R4> col{tid % L, c0 + cl, dk, dv, c0 + cl < dv};
+  const int l = col.l;
   const size_t mat = (size_t)dk * dv;
-  float x[4 * RV];
+  float x[4 * R4];
   if (dS_end != nullptr) {
     col.load(dS_end + bh * mat, x);
   } else {
 #pragma unroll
-    for (int i = 0; i < 4 * RV; ++i) x[i] = 0.f;
+    for (int i = 0; i < 4 * R4; ++i) x[i] = 0.f;
   }
-  const int nch = (N + border - 1) / border;
-  constexpr int NX = TT * DMAX / THREADS, NW = TT * COLS / THREADS;
-  for (int t0 = (N - 1) / TT * TT; t0 >= 0 && N > 0; t0 -= TT) {
-    const int n = min(TT, N - t0);
-#pragma unroll
-    for (int i = 0; i < NX; ++i) {
-      const int t = t0 + (i * THREADS + tid) / DMAX, r = (i * THREADS + tid) % DMAX;
-      const bool in = t < N && r < dk;
-      const size_t at = (bh * N + t) * dk + r;
-      (&st.x[0][0])[i * THREADS + tid] = in ? to_f(k[at]) : 0.f;
-      (&st.y[0][0])[i * THREADS + tid] = in ? to_f(q[at]) : 0.f;
-    }
-#pragma unroll
-    for (int i = 0; i < NW; ++i) {
-      const int t = t0 + (i * THREADS + tid) / COLS, c = c0 + (i * THREADS + tid) % COLS;
-      (&st.w[0][0])[i * THREADS + tid] = t < N && c < dv ? scale * to_f(dout[(bh * N + t) * dv + c]) : 0.f;
-    }
-    if (tid < n) {
-      st.a[tid] = g != nullptr ? expf(to_f(g[bh * N + t0 + tid])) : 1.f;
-      st.b[tid] = to_f(beta[bh * N + t0 + tid]);
-    }
+  const int nch = (N + TT - 1) / TT;
+  Fetch<Tin, R4> f;
+  f.load(k, q, dout, g, beta, bh, (nch - 1) * TT, N, dk, dv, c0, tid);
+  for (int ch = nch - 1; ch >= 0; --ch) {
+    const int t0 = ch * TT;
+    f.put(st, scale, tid);
     __syncthreads();
-    for (int t = n - 1; t >= 0; --t) {
-      const int tt = t0 + t;
-      if (tt == N - 1 || (tt + 1) % border == 0) col.store(Xc + (bh * nch + tt / border) * mat, x);
-      float kk[4 * RV], qq[4 * RV];
-      load_rows(st.x[t], col.l, kk);
-      load_rows(st.y[t], col.l, qq);
-      const float dov = st.w[t][cl], a = st.a[t];
+    f.load(k, q, dout, g, beta, bh, t0 - TT, N, dk, dv, c0, tid);
+    coefficients(st, tid);
+    col.store(Xc + (bh * nch + ch) * mat, x);
+    __syncthreads();
+    const int n = min(TT, N - t0);
+    for (int b = (n + 3) / 4 - 1; b >= 0; --b) {
+      float kv[4][4 * R4], d[4];
 #pragma unroll
-      for (int i = 0; i < 4 * RV; ++i) x[i] = fmaf(qq[i], dov, x[i]);
-      const float du = dot_rows(kk, x);
-      const float f = st.b[t] * du;
+      for (int t = 0; t < 4; ++t) {
+        load_rows<R4>(st.k[4 * b + t], l, kv[t]);
+        d[t] = part_dot<R4>(kv[t], x);
+      }
+      float h[2], mine;
 #pragma unroll
-      for (int i = 0; i < 4 * RV; ++i) x[i] = a * fmaf(-kk[i], f, x[i]);
-      if (col.l == 0) os[t][cl] = du;
+      for (int t = 0; t < 2; ++t)
+        h[t] = ((l & 2) ? d[2 + t] : d[t]) + __shfl_xor_sync(0xffffffffu, (l & 2) ? d[t] : d[2 + t], 2);
+      mine = ((l & 1) ? h[1] : h[0]) + __shfl_xor_sync(0xffffffffu, (l & 1) ? h[0] : h[1], 1);
+      mine += __shfl_xor_sync(0xffffffffu, mine, 4);
+      float du[4], w[4], fu[4];
+#pragma unroll
+      for (int t = 0; t < 4; ++t) w[t] = st.w[4 * b + t][cl];
+#pragma unroll
+      for (int t = 0; t < 4; ++t) {
+        du[t] = st.R[4 * b + t] * __shfl_sync(0xffffffffu, mine, t, 8);
+#pragma unroll
+        for (int s = t; s < 4; ++s) du[t] = fmaf(st.qk[4 * b + s][t], w[s], du[t]);
+      }
+#pragma unroll
+      for (int t = 3; t >= 0; --t) {
+#pragma unroll
+        for (int s = 3; s > t; --s) du[t] = fmaf(-st.kk[4 * b + s][t], fu[s], du[t]);
+        fu[t] = st.b[4 * b + t] * du[t];
+      }
+      if (l < 4) st.os[4 * b + l][cl] = l == 0 ? du[0] : l == 1 ? du[1] : l == 2 ? du[2] : du[3];
+      const float A3 = st.A[4 * b + 3];
+#pragma unroll
+      for (int i = 0; i < 4 * R4; ++i) x[i] *= A3;
+#pragma unroll
+      for (int t = 0; t < 4; ++t) {
+        const float A = st.A[4 * b + t], wt = A * w[t], ft = -A * fu[t];
+        float qv[4 * R4];
+        load_rows<R4>(st.q[4 * b + t], l, qv);
+#pragma unroll
+        for (int i = 0; i < 4 * R4; ++i) x[i] = fmaf(qv[i], wt, fmaf(kv[t][i], ft, x[i]));
+      }
     }
     __syncthreads();
     for (int i = tid; i < n * COLS; i += THREADS) {
       const int c = c0 + i % COLS;
-      if (c < dv) duv[(bh * N + t0 + i / COLS) * dv + c] = os[i / COLS][i % COLS];
+      if (c < dv) duv[(bh * N + t0 + i / COLS) * dv + c] = st.os[i / COLS][i % COLS];
     }
   }
   col.store(dS0 + bh * mat, x);
@@ -260,7 +374,7 @@ __global__ void __launch_bounds__(THREADS)
 //   dv_i = R_i,  dbeta_i = du_i . e_i
 //   dg_t = sum_{i >= t} (q_i . dq_i + k_i . [read part of dk_i] - k_i . [write part]) + <X1, S1>
 // One CTA per chunk and head, every matrix in shared memory.
-constexpr int CB = 32;          // tokens of a chunk
+constexpr int CB = TT;          // tokens of a chunk
 constexpr int GTHREADS = 256;
 
 template <typename Tin>
@@ -590,14 +704,25 @@ __global__ void __launch_bounds__(STHREADS)
   }
 }
 
+#define TTT_BY_ROWS(CALL)                     \
+  switch ((p.dk + 31) / 32) {                 \
+    case 1: CALL(1); break;                   \
+    case 2: CALL(2); break;                   \
+    case 3: CALL(3); break;                   \
+    default: CALL(4); break;                  \
+  }
+
 template <typename Tin, typename Tout>
 int rec_launch(const DeltaLaunch& p, float* S_out, const float* S_in, Tout* out, float* ev, float* Sc,
                cudaStream_t stream) {
   const dim3 grid((unsigned)(p.B * p.H), (unsigned)((p.dv + COLS - 1) / COLS));
   prof_before(K_DELTA_REC, stream);
-  delta_rec_kernel<Tin, Tout><<<grid, THREADS, 0, stream>>>(
-      (const Tin*)p.q, (const Tin*)p.k, (const Tin*)p.v, (const Tin*)p.g, (const Tin*)p.beta, S_in,
-      S_out, out, ev, Sc, p.N, p.dk, p.dv, p.scale, CB);
+#define TTT_REC(R4)                                                                            \
+  delta_rec_kernel<Tin, Tout, R4><<<grid, THREADS, 0, stream>>>(                               \
+      (const Tin*)p.q, (const Tin*)p.k, (const Tin*)p.v, (const Tin*)p.g, (const Tin*)p.beta,  \
+      S_in, S_out, out, ev, Sc, p.N, p.dk, p.dv, p.scale)
+  TTT_BY_ROWS(TTT_REC)
+#undef TTT_REC
   prof_after(K_DELTA_REC, stream);
   return cudaGetLastError() == cudaSuccess ? 0 : -1;
 }
@@ -614,9 +739,12 @@ int bwd_launch(const DeltaBwdLaunch& L, cudaStream_t stream) {
   if (rec_launch<Tin, float>(p, nullptr, L.S0, nullptr, ev, Sc, stream)) return -1;
   const dim3 grid((unsigned)BH, (unsigned)((p.dv + COLS - 1) / COLS));
   prof_before(K_DELTA_REV, stream);
-  delta_rev_kernel<Tin><<<grid, THREADS, 0, stream>>>(
-      (const Tin*)p.q, (const Tin*)p.k, (const Tin*)L.dout, (const Tin*)p.g, (const Tin*)p.beta,
-      L.dS_end, L.dS0, du, Xc, p.N, p.dk, p.dv, p.scale, CB);
+#define TTT_REV(R4)                                                                               \
+  delta_rev_kernel<Tin, R4><<<grid, THREADS, 0, stream>>>(                                        \
+      (const Tin*)p.q, (const Tin*)p.k, (const Tin*)L.dout, (const Tin*)p.g, (const Tin*)p.beta,  \
+      L.dS_end, L.dS0, du, Xc, p.N, p.dk, p.dv, p.scale)
+  TTT_BY_ROWS(TTT_REV)
+#undef TTT_REV
   prof_after(K_DELTA_REV, stream);
   if (cudaGetLastError() != cudaSuccess) return -1;
   const size_t smem = chunk_grad_smem(p.dk, p.dv);
