@@ -183,10 +183,11 @@ int ttt_linear_bwd(const ttt_linear_desc* desc, const void* q, const void* k, co
  * and v.
  *
  * The sequence form and its gradients with bf16 inputs and dk = dv = 64 or
- * 128 run on tensor cores in chunks of 128 tokens; every derived operand there
- * is carried as bf16 hi + lo (about 17 significant bits) with float32 sums,
- * and the state stays float32.  Every other type and size runs in float32 on
- * CUDA cores, token by token.
+ * 128 run on tensor cores in chunks of 128 tokens once they hold more than
+ * some 100 tokens: every derived operand there is carried as bf16 hi + lo
+ * (about 17 significant bits; three planes in what S and dS0 are made of) with
+ * float32 sums, and the state stays float32.  Every other type and size runs
+ * in float32 on CUDA cores, four tokens at a time.
  * ---------------------------------------------------------------------- */
 typedef struct {
   int B, H, N;          /* batch, heads, tokens (N >= 0)                     */
@@ -196,7 +197,7 @@ typedef struct {
   ttt_dtype out_dtype;  /* out                                               */
 } ttt_delta_desc;
 
-/* Workspace bytes of ttt_delta_fwd.  Errors: TTT_ERR_ARG (null pointers), the
+/* Workspace bytes of ttt_delta_fwd (they depend on the device's SM count).  Errors: TTT_ERR_ARG (null pointers), the
  * shape and dtype errors of ttt_delta_fwd. */
 int ttt_delta_workspace_bytes(const ttt_delta_desc* desc, size_t* bytes);
 

@@ -308,11 +308,16 @@ static DeltaLaunch delta_launch(const ttt_delta_desc* d, const void* q, const vo
   return L;
 }
 
+static bool delta_umma(const ttt_delta_desc* d, bool backward) {
+  return delta_uses_umma(d->in_dtype == TTT_BF16, d->dk, d->dv, (long long)d->B * d->H, d->N, device_sms(),
+                         backward);
+}
+
 int ttt_delta_workspace_bytes(const ttt_delta_desc* d, size_t* bytes) {
   int e = check_delta(d);
   if (e) return e;
   if (!bytes) return TTT_ERR_ARG;
-  *bytes = delta_uses_umma(d->in_dtype == TTT_BF16, d->dk, d->dv)
+  *bytes = delta_umma(d, false)
                ? delta_umma_layout(d->B * d->H, d->N, d->dk).total
                : TTT_STATUS_BYTES;
   return TTT_OK;
@@ -338,22 +343,17 @@ int ttt_delta_fwd(const ttt_delta_desc* d, const void* q, const void* k, const v
   e = check_ranges(in, 5, o, 3);
   if (e) return e;
   const DeltaLaunch L = delta_launch(d, q, k, v, g, beta, S, out, ws);
-  const int r = delta_uses_umma(L.in_bf16, d->dk, d->dv) ? launch_delta_umma(L, as_stream(stream))
-                                                         : launch_delta_rec(L, as_stream(stream));
+  const int r = delta_umma(d, false) ? launch_delta_umma(L, as_stream(stream))
+                                     : launch_delta_rec(L, as_stream(stream));
   return r == 0 ? TTT_OK : TTT_ERR_CUDA;
-}
-
-// an empty sequence takes the recurrent form, whose kernels hand the states on
-static bool delta_bwd_uses_umma(const ttt_delta_desc* d) {
-  return d->N > 0 && delta_uses_umma(d->in_dtype == TTT_BF16, d->dk, d->dv);
 }
 
 int ttt_delta_bwd_workspace_bytes(const ttt_delta_desc* d, size_t* bytes) {
   int e = check_delta(d);
   if (e) return e;
   if (!bytes) return TTT_ERR_ARG;
-  *bytes = delta_bwd_uses_umma(d) ? delta_umma_bwd_layout(d->B * d->H, d->N, d->dk).total
-                                  : delta_rec_bwd_layout(d->B * d->H, d->N, d->dk, d->dv).total;
+  *bytes = delta_umma(d, true) ? delta_umma_bwd_layout(d->B * d->H, d->N, d->dk).total
+                               : delta_rec_bwd_layout(d->B * d->H, d->N, d->dk, d->dv).total;
   return TTT_OK;
 }
 
@@ -382,8 +382,8 @@ int ttt_delta_bwd(const ttt_delta_desc* d, const void* q, const void* k, const v
   L.S0 = S0; L.dS_end = dS_end; L.dout = dout;
   L.dq = dq; L.dk = dk; L.dv = dv; L.dg = dg; L.dbeta = dbeta; L.dS0 = dS0;
   L.ws = static_cast<uint8_t*>(ws);
-  const int r = delta_bwd_uses_umma(d) ? launch_delta_umma_bwd(L, as_stream(stream))
-                                       : launch_delta_rec_bwd(L, as_stream(stream));
+  const int r = delta_umma(d, true) ? launch_delta_umma_bwd(L, as_stream(stream))
+                                    : launch_delta_rec_bwd(L, as_stream(stream));
   return r == 0 ? TTT_OK : TTT_ERR_CUDA;
 }
 

@@ -731,7 +731,18 @@ int fwd_launch(const DeltaLaunch& p, cudaStream_t stream) {
 
 }  // namespace
 
-bool delta_uses_umma(int bf16, int dk, int dv) { return bf16 && dk == dv && (dk == 64 || dk == 128); }
+// Short sequences go token by token: the chunk kernels' latency is that of a
+// whole chunk and of three launches (29 us forward, 56 us backward at D = 64;
+// 36 and 67 at 128), the recurrent ones' 0.12 us a token at D = 64 and 0.19 at
+// 128 (backward 0.24 and 0.37, behind 21 and 40), times the rounds that their
+// CTAs of 16 value columns take.  Forward at D = 64, 1 to 32 heads: 128 tokens
+// 18 against 30 us, 256 tokens 33 against 31.  Backward at D = 64: 128 tokens 51
+// against 57, at 128: 64 tokens 61 against 67.
+bool delta_uses_umma(int bf16, int dk, int dv, long long BH, int N, int sms, bool backward) {
+  if (!bf16 || dk != dv || (dk != 64 && dk != 128)) return false;
+  const double rounds = std::max(1.0, (double)BH * (dv / 16) / (1.25 * sms));
+  return N * rounds > (backward ? (dk == 64 ? 128 : 64) : 160);
+}
 
 DeltaUmmaWorkspace delta_umma_layout(int BH, int N, int D) {
   DeltaUmmaWorkspace w{};

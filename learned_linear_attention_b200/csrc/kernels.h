@@ -161,7 +161,7 @@ int launch_delta_rec_bwd(const DeltaBwdLaunch& L, cudaStream_t stream);
 struct DeltaUmmaWorkspace {           // byte offsets, per chunk of 128 tokens
   size_t gend, W, U, M, H, X, total;
 };
-bool delta_uses_umma(int bf16, int dk, int dv);
+bool delta_uses_umma(int bf16, int dk, int dv, long long BH, int N, int sms, bool backward);
 DeltaUmmaWorkspace delta_umma_layout(int BH, int N, int D);
 int launch_delta_umma(const DeltaLaunch& L, cudaStream_t stream);
 struct DeltaUmmaBwdWorkspace {

@@ -74,50 +74,73 @@ struct Stage {
   float os[TT][COLS];
 };
 
-// The next tile's tokens wait in registers while this one is worked on.
+// The next tile's tokens wait in registers while this one is worked on.  A
+// thread keeps its row of k and q and its column of the value tensor.
 template <typename Tin, int R4>
 struct Fetch {
-  static constexpr int NX = TT * 32 * R4 / THREADS, NW = TT * COLS / THREADS;
+  static constexpr int RW = R4 == 3 ? 128 : 32 * R4;      // threads of a token's row
+  static constexpr int TS = THREADS / RW, NX = TT / TS;   // tokens side by side, and of a thread
+  static constexpr int WS = THREADS / COLS, NW = TT / WS;
   Tin k[NX], q[NX], w[NW], g, b;
-  int t0;
-  TTT_DEVICE_INLINE void load(const Tin* kp, const Tin* qp, const Tin* wp, const Tin* gp, const Tin* bp,
-                              size_t bh, int t0_, int N, int dk, int dv, int c0, int tid) {
-    t0 = t0_;
+  const Tin *kp, *qp, *wp, *gp, *bp;
+  int N, dk, dv, r, tr, tw, tid;
+  bool row, col;
+  TTT_DEVICE_INLINE Fetch(const Tin* k_, const Tin* q_, const Tin* w_, const Tin* g_, const Tin* b_, size_t bh,
+                          int N_, int dk_, int dv_, int c0, int tid_)
+      : N(N_), dk(dk_), dv(dv_), r(tid_ % RW), tr(tid_ / RW), tw(tid_ / COLS), tid(tid_) {
+    row = r < dk;
+    col = c0 + tid % COLS < dv;
+    const size_t tok = bh * N;
+    kp = k_ + tok * dk + r;
+    qp = q_ != nullptr ? q_ + tok * dk + r : nullptr;
+    wp = w_ + tok * dv + c0 + tid % COLS;
+    gp = g_ != nullptr ? g_ + tok : nullptr;
+    bp = b_ + tok;
+  }
+  TTT_DEVICE_INLINE void load(int t0) {   // t0 may lie before the first or behind the last token
+    const Tin zero = from_f<Tin>(0.f);
+    const int n = t0 < 0 ? 0 : N - t0;
+    const size_t x0 = ((size_t)t0 + tr) * dk, w0 = ((size_t)t0 + tw) * dv;
 #pragma unroll
     for (int i = 0; i < NX; ++i) {
-      const int e = i * THREADS + tid, t = t0 + e / (32 * R4), r = e % (32 * R4);
-      const bool in = t >= 0 && t < N && r < dk;
-      const size_t at = (bh * N + t) * dk + r;
-      k[i] = in ? kp[at] : from_f<Tin>(0.f);
-      q[i] = in && qp != nullptr ? qp[at] : from_f<Tin>(0.f);
+      const bool in = row && tr + i * TS < n;
+      k[i] = in ? kp[x0 + (size_t)(i * TS * dk)] : zero;
+      q[i] = in && qp != nullptr ? qp[x0 + (size_t)(i * TS * dk)] : zero;
     }
 #pragma unroll
-    for (int i = 0; i < NW; ++i) {
-      const int e = i * THREADS + tid, t = t0 + e / COLS, c = c0 + e % COLS;
-      w[i] = t >= 0 && t < N && c < dv ? wp[(bh * N + t) * dv + c] : from_f<Tin>(0.f);
-    }
-    g = b = from_f<Tin>(0.f);   // no decay, no step: a padding token
-    const int t = t0 + tid;
-    if (tid < TT && t >= 0 && t < N) {
-      if (gp != nullptr) g = gp[bh * N + t];
-      b = bp[bh * N + t];
+    for (int i = 0; i < NW; ++i) w[i] = col && tw + i * WS < n ? wp[w0 + (size_t)(i * WS * dv)] : zero;
+    g = b = zero;   // no decay, no step: a padding token
+    if (tid < TT && tid < n) {
+      if (gp != nullptr) g = gp[t0 + tid];
+      b = bp[t0 + tid];
     }
   }
-  TTT_DEVICE_INLINE void put(Stage<R4>& st, float wscale, int tid) const {
+  TTT_DEVICE_INLINE void put(Stage<R4>& st, float wscale) const {
+    if (R4 != 3 || r < 96) {
 #pragma unroll
-    for (int i = 0; i < NX; ++i) {
-      const int e = i * THREADS + tid;
-      st.k[e / (32 * R4)][e % (32 * R4)] = to_f(k[i]);
-      st.q[e / (32 * R4)][e % (32 * R4)] = to_f(q[i]);
+      for (int i = 0; i < NX; ++i) {
+        st.k[tr + i * TS][r] = to_f(k[i]);
+        st.q[tr + i * TS][r] = to_f(q[i]);
+      }
     }
 #pragma unroll
-    for (int i = 0; i < NW; ++i) (&st.w[0][0])[i * THREADS + tid] = wscale * to_f(w[i]);
+    for (int i = 0; i < NW; ++i) st.w[tw + i * WS][tid % COLS] = wscale * to_f(w[i]);
     if (tid < TT) {
       st.a[tid] = expf(to_f(g));
       st.b[tid] = to_f(b);
     }
   }
 };
+// st.os to global memory, n tokens of 16 columns
+template <typename T, int R4>
+TTT_DEVICE_INLINE void write_os(const Stage<R4>& st, T* dst, int n, int dv, int c0, int tid) {
+  const int c = tid % COLS, t = tid / COLS;
+  constexpr int WS = THREADS / COLS;
+  T* p = dst + (size_t)t * dv + c0 + c;
+#pragma unroll
+  for (int i = 0; i < TT / WS; ++i)
+    if (c0 + c < dv && t + i * WS < n) p[(size_t)(i * WS * dv)] = from_f<T>(st.os[t + i * WS][c]);
+}
 
 // Coefficients of the staged tokens: thread 16 b + d takes one of the 16
 // products within block b.
@@ -139,25 +162,41 @@ TTT_DEVICE_INLINE void coefficients(Stage<R4>& st, int tid) {
     a3 = fmaf(u.w, v.w, a3);
   }
   float f = (a0 + a1) + (a2 + a3);
-  for (int m = i + 1; m <= t; ++m) f *= st.a[base + m];
+  const float4 av = *reinterpret_cast<const float4*>(st.a + base);
+  if (i < 1 && t >= 1) f *= av.y;
+  if (i < 2 && t >= 2) f *= av.z;
+  if (i < 3 && t >= 3) f *= av.w;
   if (d < 10) st.qk[base + t][i] = f;
   else st.kk[base + t][i] = f;
-  if (tid < TT) {
-    const int b0 = tid & ~3;
-    float A = 1.f, R = 1.f;
-    for (int m = b0; m < b0 + 4; ++m) {
-      if (m <= tid) A *= st.a[m];
-      else R *= st.a[m];
-    }
-    st.A[tid] = A;
-    st.R[tid] = R;
+  if (d < 4) {   // token d of the block
+    st.A[base + d] = av.x * (d >= 1 ? av.y : 1.f) * (d >= 2 ? av.z : 1.f) * (d >= 3 ? av.w : 1.f);
+    st.R[base + d] = (d < 1 ? av.y : 1.f) * (d < 2 ? av.z : 1.f) * (d < 3 ? av.w : 1.f);
 #pragma unroll
     for (int m = 0; m < 4; ++m) {
-      if (m > (tid & 3)) st.qk[tid][m] = 0.f;
-      if (m >= (tid & 3)) st.kk[tid][m] = 0.f;
+      if (m > d) st.qk[base + d][m] = 0.f;
+      if (m >= d) st.kk[base + d][m] = 0.f;
     }
   }
 }
+
+// A block's coefficients in registers, read ahead of its chain.
+struct BlockCoef {
+  float A[4], R[4], b[4], w[4], kk[4][4];
+  template <int R4>
+  TTT_DEVICE_INLINE BlockCoef(const Stage<R4>& st, int blk, int cl) {
+    auto get = [](const float* p, float (&x)[4]) {
+      const float4 v = *reinterpret_cast<const float4*>(p);
+      x[0] = v.x; x[1] = v.y; x[2] = v.z; x[3] = v.w;
+    };
+    get(st.A + 4 * blk, A);
+    get(st.R + 4 * blk, R);
+    get(st.b + 4 * blk, b);
+#pragma unroll
+    for (int t = 0; t < 4; ++t) w[t] = st.w[4 * blk + t][cl];
+#pragma unroll
+    for (int t = 1; t < 4; ++t) get(st.kk[4 * blk + t], kk[t]);
+  }
+};
 
 template <int R4>
 TTT_DEVICE_INLINE void load_rows(const float* row, int l, float (&x)[4 * R4]) {
@@ -191,6 +230,7 @@ __global__ void __launch_bounds__(THREADS)
   const size_t bh = blockIdx.x;
   const int c0 = blockIdx.y * COLS, tid = threadIdx.x, cl = tid / L;
   const Column<R4> col{tid % L, c0 + cl, dk, dv, c0 + cl < dv};
+  constexpr int U = R4 == 1 ? 4 : 2;
   const int l = col.l, lt = l & 3;
   const size_t mat = (size_t)dk * dv;
   float s[4 * R4];
@@ -201,73 +241,79 @@ __global__ void __launch_bounds__(THREADS)
     for (int i = 0; i < 4 * R4; ++i) s[i] = 0.f;
   }
   const int nch = (N + TT - 1) / TT;
-  Fetch<Tin, R4> f;
-  const Tin* qp = out != nullptr ? q : nullptr;
-  f.load(k, qp, v, g, beta, bh, 0, N, dk, dv, c0, tid);
+  Fetch<Tin, R4> f(k, out != nullptr ? q : nullptr, v, g, beta, bh, N, dk, dv, c0, tid);
+  f.load(0);
   for (int t0 = 0; t0 < N; t0 += TT) {
-    f.put(st, 1.f, tid);
+    f.put(st, 1.f);
     __syncthreads();
-    f.load(k, qp, v, g, beta, bh, t0 + TT, N, dk, dv, c0, tid);
+    f.load(t0 + TT);
     coefficients(st, tid);
     if (Sc != nullptr) col.store(Sc + (bh * (nch + 1) + t0 / TT) * mat, s);
     __syncthreads();
     const int n = min(TT, N - t0), nb = (n + 3) / 4;
-    for (int b = 0; b < nb; ++b) {
-      float kv[4][4 * R4], d[8];
+    // U blocks to a turn, so that one block's loads pass under the chain of
+    // the one before (results are kept back, as a store would stop the loads);
+    // padding tokens change nothing
+    for (int b0 = 0; b0 < nb; b0 += U) {
+      float keep[U];
 #pragma unroll
-      for (int t = 0; t < 4; ++t) {
-        load_rows<R4>(st.k[4 * b + t], l, kv[t]);
-        d[t] = part_dot<R4>(kv[t], s);
+      for (int ub = 0; ub < U; ++ub) {
+        const int b = b0 + ub;
+        const BlockCoef c4(st, b, cl);
+        float kv[4][4 * R4], d[8];
+#pragma unroll
+        for (int t = 0; t < 4; ++t) {
+          load_rows<R4>(st.k[4 * b + t], l, kv[t]);
+          d[t] = part_dot<R4>(kv[t], s);
+        }
+#pragma unroll
+        for (int t = 0; t < 4; ++t) {
+          float qv[4 * R4];
+          load_rows<R4>(st.q[4 * b + t], l, qv);
+          d[4 + t] = part_dot<R4>(qv, s);
+        }
+        // eight sums over eight lanes, halving the values a lane holds: k_t.s
+        // ends in lane t, q_t.s in lane 4 + t
+        float h[4], p2[2], mine;
+#pragma unroll
+        for (int t = 0; t < 4; ++t)
+          h[t] = ((l & 4) ? d[4 + t] : d[t]) + __shfl_xor_sync(0xffffffffu, (l & 4) ? d[t] : d[4 + t], 4);
+#pragma unroll
+        for (int t = 0; t < 2; ++t)
+          p2[t] = ((l & 2) ? h[2 + t] : h[t]) + __shfl_xor_sync(0xffffffffu, (l & 2) ? h[t] : h[2 + t], 2);
+        mine = ((l & 1) ? p2[1] : p2[0]) + __shfl_xor_sync(0xffffffffu, (l & 1) ? p2[0] : p2[1], 1);
+        float p[4], e[4], u[4];
+#pragma unroll
+        for (int t = 0; t < 4; ++t) p[t] = __shfl_sync(0xffffffffu, mine, t, 8);
+#pragma unroll
+        for (int t = 0; t < 4; ++t) e[t] = fmaf(-c4.A[t], p[t], c4.w[t]);
+#pragma unroll
+        for (int t = 0; t < 4; ++t) {
+#pragma unroll
+          for (int i = 0; i < t; ++i) e[t] = fmaf(-c4.kk[t][i], u[i], e[t]);
+          u[t] = c4.b[t] * e[t];
+        }
+        if (out != nullptr) {
+          const float4 c = *reinterpret_cast<const float4*>(st.qk[4 * b + lt]);
+          const float o = fmaf(c.x, u[0], fmaf(c.y, u[1], fmaf(c.z, u[2], fmaf(c.w, u[3], st.A[4 * b + lt] * mine))));
+          keep[ub] = scale * o;
+        } else {
+          keep[ub] = lt == 0 ? e[0] : lt == 1 ? e[1] : lt == 2 ? e[2] : e[3];
+        }
+        const float A3 = c4.A[3];
+#pragma unroll
+        for (int t = 0; t < 4; ++t) u[t] *= c4.R[t];
+#pragma unroll
+        for (int i = 0; i < 4 * R4; ++i)
+          s[i] = fmaf(kv[3][i], u[3], fmaf(kv[2][i], u[2], fmaf(kv[1][i], u[1], fmaf(kv[0][i], u[0], A3 * s[i]))));
       }
+      if (l & 4)
 #pragma unroll
-      for (int t = 0; t < 4; ++t) {
-        float qv[4 * R4];
-        load_rows<R4>(st.q[4 * b + t], l, qv);
-        d[4 + t] = part_dot<R4>(qv, s);
-      }
-      // eight sums over eight lanes, halving the values a lane holds: k_t.s
-      // ends in lane t, q_t.s in lane 4 + t
-      float h[4], p2[2], mine;
-#pragma unroll
-      for (int t = 0; t < 4; ++t)
-        h[t] = ((l & 4) ? d[4 + t] : d[t]) + __shfl_xor_sync(0xffffffffu, (l & 4) ? d[t] : d[4 + t], 4);
-#pragma unroll
-      for (int t = 0; t < 2; ++t)
-        p2[t] = ((l & 2) ? h[2 + t] : h[t]) + __shfl_xor_sync(0xffffffffu, (l & 2) ? h[t] : h[2 + t], 2);
-      mine = ((l & 1) ? p2[1] : p2[0]) + __shfl_xor_sync(0xffffffffu, (l & 1) ? p2[0] : p2[1], 1);
-      float p[4], e[4], u[4];
-#pragma unroll
-      for (int t = 0; t < 4; ++t) p[t] = __shfl_sync(0xffffffffu, mine, t, 8);
-#pragma unroll
-      for (int t = 0; t < 4; ++t) e[t] = fmaf(-st.A[4 * b + t], p[t], st.w[4 * b + t][cl]);
-#pragma unroll
-      for (int t = 0; t < 4; ++t) {
-#pragma unroll
-        for (int i = 0; i < t; ++i) e[t] = fmaf(-st.kk[4 * b + t][i], u[i], e[t]);
-        u[t] = st.b[4 * b + t] * e[t];
-      }
-      if (out != nullptr) {
-        const float4 c = *reinterpret_cast<const float4*>(st.qk[4 * b + lt]);
-        const float o = fmaf(c.x, u[0], fmaf(c.y, u[1], fmaf(c.z, u[2], fmaf(c.w, u[3], st.A[4 * b + lt] * mine))));
-        if (l & 4) st.os[4 * b + lt][cl] = scale * o;
-      } else if (l < 4) {
-        st.os[4 * b + l][cl] = l == 0 ? e[0] : l == 1 ? e[1] : l == 2 ? e[2] : e[3];
-      }
-      const float A3 = st.A[4 * b + 3];
-#pragma unroll
-      for (int t = 0; t < 4; ++t) u[t] *= st.R[4 * b + t];
-#pragma unroll
-      for (int i = 0; i < 4 * R4; ++i)
-        s[i] = fmaf(kv[3][i], u[3], fmaf(kv[2][i], u[2], fmaf(kv[1][i], u[1], fmaf(kv[0][i], u[0], A3 * s[i]))));
+        for (int ub = 0; ub < U; ++ub) st.os[4 * (b0 + ub) + lt][cl] = keep[ub];
     }
     __syncthreads();
-    for (int i = tid; i < n * COLS; i += THREADS) {
-      const int t = t0 + i / COLS, c = c0 + i % COLS;
-      if (c >= dv) continue;
-      const size_t at = (bh * N + t) * dv + c;
-      if (out != nullptr) out[at] = from_f<Tout>(st.os[i / COLS][i % COLS]);
-      else ev[at] = st.os[i / COLS][i % COLS];
-    }
+    if (out != nullptr) write_os(st, out + (bh * N + t0) * dv, n, dv, c0, tid);
+    else write_os(st, ev + (bh * N + t0) * dv, n, dv, c0, tid);
   }
   if (Sc != nullptr) col.store(Sc + (bh * (nch + 1) + nch) * mat, s);
   if (S_out != nullptr) col.store(S_out + bh * mat, s);
@@ -292,6 +338,7 @@ __global__ void __launch_bounds__(THREADS)
   const size_t bh = blockIdx.x;
   const int c0 = blockIdx.y * COLS, tid = threadIdx.x, cl = tid / L;
   const Column<R4> col{tid % L, c0 + cl, dk, dv, c0 + cl < dv};
+  constexpr int U = R4 == 1 ? 4 : 2;
   const int l = col.l;
   const size_t mat = (size_t)dk * dv;
   float x[4 * R4];
@@ -302,63 +349,69 @@ __global__ void __launch_bounds__(THREADS)
     for (int i = 0; i < 4 * R4; ++i) x[i] = 0.f;
   }
   const int nch = (N + TT - 1) / TT;
-  Fetch<Tin, R4> f;
-  f.load(k, q, dout, g, beta, bh, (nch - 1) * TT, N, dk, dv, c0, tid);
+  Fetch<Tin, R4> f(k, q, dout, g, beta, bh, N, dk, dv, c0, tid);
+  f.load((nch - 1) * TT);
   for (int ch = nch - 1; ch >= 0; --ch) {
     const int t0 = ch * TT;
-    f.put(st, scale, tid);
+    f.put(st, scale);
     __syncthreads();
-    f.load(k, q, dout, g, beta, bh, t0 - TT, N, dk, dv, c0, tid);
+    f.load(t0 - TT);
     coefficients(st, tid);
     col.store(Xc + (bh * nch + ch) * mat, x);
     __syncthreads();
     const int n = min(TT, N - t0);
-    for (int b = (n + 3) / 4 - 1; b >= 0; --b) {
-      float kv[4][4 * R4], d[4];
+    for (int b0 = (n + 4 * U - 1) / (4 * U) * U - 1; b0 >= 0; b0 -= U) {
+      float keep[U];
 #pragma unroll
-      for (int t = 0; t < 4; ++t) {
-        load_rows<R4>(st.k[4 * b + t], l, kv[t]);
-        d[t] = part_dot<R4>(kv[t], x);
+      for (int ub = 0; ub < U; ++ub) {
+        const int b = b0 - ub;
+        const BlockCoef c4(st, b, cl);
+        float kv[4][4 * R4], d[4];
+#pragma unroll
+        for (int t = 0; t < 4; ++t) {
+          load_rows<R4>(st.k[4 * b + t], l, kv[t]);
+          d[t] = part_dot<R4>(kv[t], x);
+        }
+        float h[2], mine;
+#pragma unroll
+        for (int t = 0; t < 2; ++t)
+          h[t] = ((l & 2) ? d[2 + t] : d[t]) + __shfl_xor_sync(0xffffffffu, (l & 2) ? d[t] : d[2 + t], 2);
+        mine = ((l & 1) ? h[1] : h[0]) + __shfl_xor_sync(0xffffffffu, (l & 1) ? h[0] : h[1], 1);
+        mine += __shfl_xor_sync(0xffffffffu, mine, 4);
+        float du[4], w[4], fu[4];
+#pragma unroll
+        for (int t = 0; t < 4; ++t) w[t] = c4.w[t];
+#pragma unroll
+        for (int t = 0; t < 4; ++t) {
+          du[t] = c4.R[t] * __shfl_sync(0xffffffffu, mine, t, 8);
+#pragma unroll
+          for (int s = t; s < 4; ++s) du[t] = fmaf(st.qk[4 * b + s][t], w[s], du[t]);
+        }
+#pragma unroll
+        for (int t = 3; t >= 0; --t) {
+#pragma unroll
+          for (int s = 3; s > t; --s) du[t] = fmaf(-c4.kk[s][t], fu[s], du[t]);
+          fu[t] = c4.b[t] * du[t];
+        }
+        keep[ub] = (l & 3) == 0 ? du[0] : (l & 3) == 1 ? du[1] : (l & 3) == 2 ? du[2] : du[3];
+        const float A3 = c4.A[3];
+#pragma unroll
+        for (int i = 0; i < 4 * R4; ++i) x[i] *= A3;
+#pragma unroll
+        for (int t = 0; t < 4; ++t) {
+          const float A = c4.A[t], wt = A * w[t], ft = -A * fu[t];
+          float qv[4 * R4];
+          load_rows<R4>(st.q[4 * b + t], l, qv);
+#pragma unroll
+          for (int i = 0; i < 4 * R4; ++i) x[i] = fmaf(qv[i], wt, fmaf(kv[t][i], ft, x[i]));
+        }
       }
-      float h[2], mine;
+      if (l & 4)
 #pragma unroll
-      for (int t = 0; t < 2; ++t)
-        h[t] = ((l & 2) ? d[2 + t] : d[t]) + __shfl_xor_sync(0xffffffffu, (l & 2) ? d[t] : d[2 + t], 2);
-      mine = ((l & 1) ? h[1] : h[0]) + __shfl_xor_sync(0xffffffffu, (l & 1) ? h[0] : h[1], 1);
-      mine += __shfl_xor_sync(0xffffffffu, mine, 4);
-      float du[4], w[4], fu[4];
-#pragma unroll
-      for (int t = 0; t < 4; ++t) w[t] = st.w[4 * b + t][cl];
-#pragma unroll
-      for (int t = 0; t < 4; ++t) {
-        du[t] = st.R[4 * b + t] * __shfl_sync(0xffffffffu, mine, t, 8);
-#pragma unroll
-        for (int s = t; s < 4; ++s) du[t] = fmaf(st.qk[4 * b + s][t], w[s], du[t]);
-      }
-#pragma unroll
-      for (int t = 3; t >= 0; --t) {
-#pragma unroll
-        for (int s = 3; s > t; --s) du[t] = fmaf(-st.kk[4 * b + s][t], fu[s], du[t]);
-        fu[t] = st.b[4 * b + t] * du[t];
-      }
-      if (l < 4) st.os[4 * b + l][cl] = l == 0 ? du[0] : l == 1 ? du[1] : l == 2 ? du[2] : du[3];
-      const float A3 = st.A[4 * b + 3];
-#pragma unroll
-      for (int i = 0; i < 4 * R4; ++i) x[i] *= A3;
-#pragma unroll
-      for (int t = 0; t < 4; ++t) {
-        const float A = st.A[4 * b + t], wt = A * w[t], ft = -A * fu[t];
-        float qv[4 * R4];
-        load_rows<R4>(st.q[4 * b + t], l, qv);
-#pragma unroll
-        for (int i = 0; i < 4 * R4; ++i) x[i] = fmaf(qv[i], wt, fmaf(kv[t][i], ft, x[i]));
-      }
+        for (int ub = 0; ub < U; ++ub) st.os[4 * (b0 - ub) + (l & 3)][cl] = keep[ub];
     }
     __syncthreads();
-    for (int i = tid; i < n * COLS; i += THREADS) {
-      const int c = c0 + i % COLS;
-      if (c < dv) duv[(bh * N + t0 + i / COLS) * dv + c] = st.os[i / COLS][i % COLS];
-    }
+    write_os(st, duv + (bh * N + t0) * dv, n, dv, c0, tid);
   }
   col.store(dS0 + bh * mat, x);
 }
@@ -386,22 +439,46 @@ struct ChunkArgs {
   float scale;
 };
 
-template <typename Tin>
+// Shared memory: pitches are 4 (mod 8) floats, so that 16-byte reads down a
+// column of rows meet different banks; everything behind dv in a row is zero.
+struct GradSmem {
+  int ms;                                  // pitch of a value row
+  size_t S0, X1, Q, K, D, U, R, Mq, Mk, floats;
+  __host__ __device__ GradSmem(int dk, int dv) {
+    ms = (dv + 7) / 8 * 8 + 4;
+    S0 = 0;
+    X1 = S0 + (size_t)dk * ms;
+    D = X1 + (size_t)dk * ms;
+    U = D + CB * ms;
+    R = U + CB * ms;
+    Mq = R + CB * ms;
+    Mk = Mq + CB * MP;
+    Q = Mk + CB * MP;
+    K = Q + CB * dk;
+    floats = K + CB * dk;
+  }
+  static constexpr int MP = CB + 4;        // pitch of Mq, Mk
+};
+
+TTT_DEVICE_INLINE void copy_async4(float* dst, const float* src) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
+}
+TTT_DEVICE_INLINE float dot4(const float4& a, const float4& b, float acc) {
+  return fmaf(a.w, b.w, fmaf(a.z, b.z, fmaf(a.y, b.y, fmaf(a.x, b.x, acc))));
+}
+
+template <typename Tin, int R4>   // R4: groups of 32 rows of dk and columns of dv
 __global__ void __launch_bounds__(GTHREADS) delta_chunk_grad_kernel(ChunkArgs<Tin> p) {
-  extern __shared__ float sm[];
-  const int dk = p.dk_, dv = p.dv_, N = p.N, tid = threadIdx.x;
-  float* M = sm;                    // [dk][dv + 1]: S0, then X1
-  const int ms = dv + 1;
-  float* Q = M + dk * ms;           // [CB][dk]
-  float* K = Q + CB * dk;
-  float* D = K + CB * dk;           // [CB][dv] scale * dout
-  float* U = D + CB * dv;           // beta e
-  float* R = U + CB * dv;           // beta du
-  float* Mq = R + CB * dv;          // [CB][CB + 1]
-  float* Mk = Mq + CB * (CB + 1);
-  float* dKr = Mk + CB * (CB + 1);  // [CB]: row sums for dg
+  extern __shared__ __align__(16) float sm[];
+  constexpr int WARPS = GTHREADS / 32, MP = GradSmem::MP;
+  static_assert(CB == 4 * WARPS && CB == 32, "a warp takes four tokens, the gates are one warp's");
+  const int dk = p.dk_, dv = p.dv_, N = p.N, tid = threadIdx.x, warp = tid / 32, lane = tid & 31;
+  const GradSmem L_(dk, dv);
+  const int ms = L_.ms;
+  float *S0s = sm + L_.S0, *X1s = sm + L_.X1, *Q = sm + L_.Q, *K = sm + L_.K;
+  float *D = sm + L_.D, *U = sm + L_.U, *R = sm + L_.R, *Mq = sm + L_.Mq, *Mk = sm + L_.Mk;
   __shared__ double G[CB];
-  __shared__ float red[GTHREADS / 32];
+  __shared__ float red[WARPS], row_s[CB];
   const size_t bh = blockIdx.y;
   const int ch = blockIdx.x, t0 = ch * CB, n = min(CB, N - t0), nch = gridDim.x;
   const size_t mat = (size_t)dk * dv, tok = bh * N + t0;
@@ -409,130 +486,159 @@ __global__ void __launch_bounds__(GTHREADS) delta_chunk_grad_kernel(ChunkArgs<Ti
   const float* S1 = S0 + mat;
   const float* X1 = p.Xc + (bh * nch + ch) * mat;
 
-  if (tid == 0) {
-    double acc = 0;
-    for (int i = 0; i < n; ++i) {
-      // exp(-200) is 0 in float32: a cleared state keeps G finite
-      const float gi = p.g != nullptr ? to_f(p.g[tok + i]) : 0.f;
-      acc += gi < -200.f ? -200.0 : (double)gi;   // NaN stays
-      G[i] = acc;
+  for (int r = warp; r < dk; r += WARPS)
+    for (int c = lane; c < ms; c += 32) {
+      if (c < dv) {
+        copy_async4(S0s + r * ms + c, S0 + (size_t)r * dv + c);
+        copy_async4(X1s + r * ms + c, X1 + (size_t)r * dv + c);
+      } else {
+        S0s[r * ms + c] = X1s[r * ms + c] = 0.f;
+      }
+    }
+  // tokens warp + 8 i: every load before the first use
+  Tin qv[4][R4], kv[4][R4], dov[4][R4], bv[4];
+  float evv[4][R4], duv[4][R4];
+  const Tin zero = from_f<Tin>(0.f);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int t = warp + WARPS * i;
+    const bool in = t < n;
+    bv[i] = in ? p.beta[tok + t] : zero;
+#pragma unroll
+    for (int b = 0; b < R4; ++b) {
+      const int r = lane + 32 * b;
+      const size_t ak = (tok + t) * dk + r, av = (tok + t) * dv + r;
+      qv[i][b] = in && r < dk ? p.q[ak] : zero;
+      kv[i][b] = in && r < dk ? p.k[ak] : zero;
+      dov[i][b] = in && r < dv ? p.dout[av] : zero;
+      evv[i][b] = in && r < dv ? p.ev[av] : 0.f;
+      duv[i][b] = in && r < dv ? p.duv[av] : 0.f;
     }
   }
-  if (tid < CB) dKr[tid] = 0.f;
-  for (int i = tid; i < n * dk; i += GTHREADS) {
-    Q[i] = to_f(p.q[tok * dk + i]);
-    K[i] = to_f(p.k[tok * dk + i]);
-  }
-  for (int i = tid; i < n * dv; i += GTHREADS) {
-    const float b = to_f(p.beta[tok + i / dv]);
-    const float r = b * p.duv[tok * dv + i];
-    D[i] = p.scale * to_f(p.dout[tok * dv + i]);
-    U[i] = b * p.ev[tok * dv + i];
-    R[i] = r;
-    p.dv[tok * dv + i] = from_f<Tin>(r);
+  if (warp == 0) {
+    // exp(-200) is 0 in float32: a cleared state keeps G finite
+    const float gi = p.g != nullptr && lane < n ? to_f(p.g[tok + lane]) : 0.f;
+    double acc = gi < -200.f ? -200.0 : (double)gi;   // NaN stays
+    for (int o = 1; o < 32; o <<= 1) {
+      const double y = __shfl_up_sync(0xffffffffu, acc, o);
+      if (lane >= o) acc += y;
+    }
+    G[lane] = acc;
   }
   float xs = 0.f;   // <X1, S1>
-  for (int i = tid; i < dk * dv; i += GTHREADS) {
-    M[i / dv * ms + i % dv] = S0[i];
-    xs = fmaf(X1[i], S1[i], xs);
+#pragma unroll 4
+  for (int r = warp; r < dk; r += WARPS)
+#pragma unroll
+    for (int b = 0; b < R4; ++b)
+      if (lane + 32 * b < dv) {
+        const size_t at = (size_t)r * dv + lane + 32 * b;
+        xs = fmaf(X1[at], S1[at], xs);
+      }
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int t = warp + WARPS * i;
+    const float bt = to_f(bv[i]);
+    float db = 0.f;
+#pragma unroll
+    for (int b = 0; b < R4; ++b) {
+      const int r = lane + 32 * b;
+      if (r < dk) {
+        Q[t * dk + r] = to_f(qv[i][b]);
+        K[t * dk + r] = to_f(kv[i][b]);
+      }
+      if (r < ms) {
+        const float rv = bt * duv[i][b];
+        D[t * ms + r] = p.scale * to_f(dov[i][b]);
+        U[t * ms + r] = bt * evv[i][b];
+        R[t * ms + r] = rv;
+        if (t < n && r < dv) p.dv[(tok + t) * dv + r] = from_f<Tin>(rv);
+      }
+      db = fmaf(duv[i][b], evv[i][b], db);
+    }
+    for (int o = 16; o > 0; o >>= 1) db += __shfl_xor_sync(0xffffffffu, db, o);
+    if (lane == 0 && t < n) p.dbeta[tok + t] = from_f<Tin>(db);
+    // a full last group leaves the row's last four floats to this
+    if (32 * R4 + lane < ms) D[t * ms + 32 * R4 + lane] = U[t * ms + 32 * R4 + lane] = R[t * ms + 32 * R4 + lane] = 0.f;
   }
   for (int o = 16; o > 0; o >>= 1) xs += __shfl_xor_sync(0xffffffffu, xs, o);
-  if ((tid & 31) == 0) red[tid / 32] = xs;
+  if (lane == 0) red[warp] = xs;
+  asm volatile("cp.async.wait_all;" ::: "memory");
   __syncthreads();
-  // dbeta, Mq, Mk
-  for (int i = tid / 32; i < n; i += GTHREADS / 32) {
-    float acc = 0.f;
-    for (int c = tid & 31; c < dv; c += 32)
-      acc = fmaf(p.duv[(tok + i) * dv + c], p.ev[(tok + i) * dv + c], acc);
-    for (int o = 16; o > 0; o >>= 1) acc += __shfl_xor_sync(0xffffffffu, acc, o);
-    if ((tid & 31) == 0) p.dbeta[tok + i] = from_f<Tin>(acc);
-  }
-  for (int e = tid; e < CB * CB; e += GTHREADS) {
-    const int i = e / CB, j = e % CB;
-    float mq = 0.f, mk = 0.f;
-    if (i < n && j <= i) {
-      for (int c = 0; c < dv; ++c) {
-        mq = fmaf(D[i * dv + c], U[j * dv + c], mq);
-        mk = fmaf(R[i * dv + c], U[j * dv + c], mk);
+  auto at4 = [](const float* x) { return *reinterpret_cast<const float4*>(x); };
+  {   // Mq, Mk: column j = lane, rows i = warp + 8 a
+    const int j = lane;
+    float mq[4] = {0.f, 0.f, 0.f, 0.f}, mk[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 2
+    for (int c = 0; c < dv; c += 4) {
+      const float4 u = at4(U + j * ms + c);
+#pragma unroll
+      for (int a = 0; a < 4; ++a) {
+        const int i = warp + WARPS * a;
+        mq[a] = dot4(at4(D + i * ms + c), u, mq[a]);
+        mk[a] = dot4(at4(R + i * ms + c), u, mk[a]);
       }
-      const float f = expf((float)(G[i] - G[j]));
-      mq *= f;
-      mk = j < i ? -mk * f : 0.f;
     }
-    Mq[i * (CB + 1) + j] = mq;
-    Mk[i * (CB + 1) + j] = mk;
+#pragma unroll
+    for (int a = 0; a < 4; ++a) {
+      const int i = warp + WARPS * a;
+      const float f = j <= i ? expf((float)(G[i] - G[j])) : 0.f;
+      Mq[i * MP + j] = j <= i ? mq[a] * f : 0.f;
+      Mk[i * MP + j] = j < i ? -mk[a] * f : 0.f;
+    }
   }
   __syncthreads();
-  // a thread holds row r of four tokens' dq and dk at a time; lanes of a warp
-  // share the tokens, so the sums for dg are warp sums
-  const int warp = tid / 32, lane = tid & 31;
-  constexpr int ROWS = DMAX / 32;
-  static_assert(CB == 4 * (GTHREADS / 32), "a warp takes four tokens");
+  // a lane holds rows lane + 32 b of four tokens' gradients
   const int i0 = warp * 4;
-  float dqv[4][ROWS], dkr[4][ROWS];
+  float dqv[4][R4], dkr[4][R4], dkw[4][R4];
 #pragma unroll
   for (int a = 0; a < 4; ++a)
 #pragma unroll
-    for (int b = 0; b < ROWS; ++b) { dqv[a][b] = 0.f; dkr[a][b] = 0.f; }
-  for (int c = 0; c < dv; ++c) {
-    float m[ROWS];
+    for (int b = 0; b < R4; ++b) dqv[a][b] = dkr[a][b] = dkw[a][b] = 0.f;
+#pragma unroll 2
+  for (int c = 0; c < dv; c += 4) {
+    float4 m[R4], x[R4];
 #pragma unroll
-    for (int b = 0; b < ROWS; ++b) m[b] = lane + 32 * b < dk ? M[(lane + 32 * b) * ms + c] : 0.f;
-#pragma unroll
-    for (int a = 0; a < 4; ++a) {
-      const int i = i0 + a;
-      const float d = i < n ? D[i * dv + c] : 0.f, r = i < n ? R[i * dv + c] : 0.f;
-#pragma unroll
-      for (int b = 0; b < ROWS; ++b) {
-        dqv[a][b] = fmaf(d, m[b], dqv[a][b]);
-        dkr[a][b] = fmaf(-r, m[b], dkr[a][b]);
-      }
+    for (int b = 0; b < R4; ++b) {
+      const int r = min(lane + 32 * b, dk - 1);   // rows behind dk are not stored
+      m[b] = at4(S0s + r * ms + c);
+      x[b] = at4(X1s + r * ms + c);
     }
-  }
-  __syncthreads();
-  for (int i = tid; i < dk * dv; i += GTHREADS) M[i / dv * ms + i % dv] = X1[i];
-  __syncthreads();
-  float dkw[4][ROWS];
-#pragma unroll
-  for (int a = 0; a < 4; ++a)
-#pragma unroll
-    for (int b = 0; b < ROWS; ++b) dkw[a][b] = 0.f;
-  for (int c = 0; c < dv; ++c) {
-    float m[ROWS];
-#pragma unroll
-    for (int b = 0; b < ROWS; ++b) m[b] = lane + 32 * b < dk ? M[(lane + 32 * b) * ms + c] : 0.f;
 #pragma unroll
     for (int a = 0; a < 4; ++a) {
-      const float u = i0 + a < n ? U[(i0 + a) * dv + c] : 0.f;
+      const float4 d = at4(D + (i0 + a) * ms + c), r = at4(R + (i0 + a) * ms + c), u = at4(U + (i0 + a) * ms + c);
 #pragma unroll
-      for (int b = 0; b < ROWS; ++b) dkw[a][b] = fmaf(u, m[b], dkw[a][b]);
+      for (int b = 0; b < R4; ++b) {
+        dqv[a][b] = dot4(d, m[b], dqv[a][b]);
+        dkr[a][b] = dot4(r, m[b], dkr[a][b]);
+        dkw[a][b] = dot4(u, x[b], dkw[a][b]);
+      }
     }
   }
 #pragma unroll
   for (int a = 0; a < 4; ++a) {
-    const int i = i0 + a;
-    const float gam = i < n ? expf((float)G[i]) : 0.f;
-    const float rho = i < n ? expf((float)(G[n - 1] - G[i])) : 0.f;
+    const float gam = expf((float)G[i0 + a]), rho = expf((float)(G[CB - 1] - G[i0 + a]));
 #pragma unroll
-    for (int b = 0; b < ROWS; ++b) { dqv[a][b] *= gam; dkr[a][b] *= gam; dkw[a][b] *= rho; }
+    for (int b = 0; b < R4; ++b) { dqv[a][b] *= gam; dkr[a][b] *= -gam; dkw[a][b] *= rho; }
   }
-  for (int j = 0; j < n; ++j) {
-    float kj[ROWS], qj[ROWS];
+#pragma unroll 2
+  for (int j = 0; j < n; ++j) {   // rows and columns of Mq and Mk behind n are zero
+    float kj[R4], qj[R4];
 #pragma unroll
-    for (int b = 0; b < ROWS; ++b) {
-      kj[b] = lane + 32 * b < dk ? K[j * dk + lane + 32 * b] : 0.f;
-      qj[b] = lane + 32 * b < dk ? Q[j * dk + lane + 32 * b] : 0.f;
+    for (int b = 0; b < R4; ++b) {
+      const int r = min(lane + 32 * b, dk - 1);
+      kj[b] = K[j * dk + r];
+      qj[b] = Q[j * dk + r];
     }
+    const float4 wq4 = at4(Mq + j * MP + i0), wk4 = at4(Mk + j * MP + i0);
+    const float wq[4] = {wq4.x, wq4.y, wq4.z, wq4.w}, wk[4] = {wk4.x, wk4.y, wk4.z, wk4.w};
 #pragma unroll
     for (int a = 0; a < 4; ++a) {
-      const int i = i0 + a;   // rows behind n read zeros written above
-      const float mq = Mq[i * (CB + 1) + j], mk = Mk[i * (CB + 1) + j];
-      const float wq = Mq[j * (CB + 1) + i], wk = Mk[j * (CB + 1) + i];
+      const float mq = Mq[(i0 + a) * MP + j], mk = Mk[(i0 + a) * MP + j];
 #pragma unroll
-      for (int b = 0; b < ROWS; ++b) {
+      for (int b = 0; b < R4; ++b) {
         dqv[a][b] = fmaf(mq, kj[b], dqv[a][b]);
         dkr[a][b] = fmaf(mk, kj[b], dkr[a][b]);
-        dkw[a][b] = fmaf(wq, qj[b], fmaf(wk, kj[b], dkw[a][b]));
+        dkw[a][b] = fmaf(wq[a], qj[b], fmaf(wk[a], kj[b], dkw[a][b]));
       }
     }
   }
@@ -540,33 +646,32 @@ __global__ void __launch_bounds__(GTHREADS) delta_chunk_grad_kernel(ChunkArgs<Ti
   for (int a = 0; a < 4; ++a) {
     const int i = i0 + a;
     float acc = 0.f;
-    if (i < n) {
 #pragma unroll
-      for (int b = 0; b < ROWS; ++b) {
-        const int r = lane + 32 * b;
-        if (r >= dk) continue;
-        p.dq[(tok + i) * dk + r] = from_f<Tin>(dqv[a][b]);
-        p.dk[(tok + i) * dk + r] = from_f<Tin>(dkr[a][b] + dkw[a][b]);
-        acc = fmaf(Q[i * dk + r], dqv[a][b], fmaf(K[i * dk + r], dkr[a][b] - dkw[a][b], acc));
-      }
+    for (int b = 0; b < R4; ++b) {
+      const int r = lane + 32 * b;
+      if (r >= dk || i >= n) continue;
+      p.dq[(tok + i) * dk + r] = from_f<Tin>(dqv[a][b]);
+      p.dk[(tok + i) * dk + r] = from_f<Tin>(dkr[a][b] + dkw[a][b]);
+      acc = fmaf(Q[i * dk + r], dqv[a][b], fmaf(K[i * dk + r], dkr[a][b] - dkw[a][b], acc));
     }
     for (int o = 16; o > 0; o >>= 1) acc += __shfl_xor_sync(0xffffffffu, acc, o);
-    if (lane == 0) dKr[i] = acc;
+    if (lane == 0) row_s[i] = acc;
   }
   __syncthreads();
-  if (tid == 0 && p.dg != nullptr) {
-    float acc = 0.f;
-    for (int w = 0; w < GTHREADS / 32; ++w) acc += red[w];
-    for (int i = n - 1; i >= 0; --i) {
-      acc += dKr[i];
-      p.dg[tok + i] = from_f<Tin>(acc);
+  if (warp == 0 && p.dg != nullptr) {
+    float x1s1 = 0.f;
+    for (int w = 0; w < WARPS; ++w) x1s1 += red[w];
+    // the sum over the tokens from this one on
+    float acc = row_s[lane];
+    for (int o = 1; o < 32; o <<= 1) {
+      const float y = __shfl_down_sync(0xffffffffu, acc, o);
+      if (lane + o < 32) acc += y;
     }
+    if (lane < n) p.dg[tok + lane] = from_f<Tin>(acc + x1s1);
   }
 }
 
-size_t chunk_grad_smem(int dk, int dv) {
-  return sizeof(float) * ((size_t)dk * (dv + 1) + 2 * CB * dk + 3 * CB * dv + 2 * CB * (CB + 1) + CB);
-}
+size_t chunk_grad_smem(int dk, int dv) { return sizeof(float) * GradSmem(dk, dv).floats; }
 
 // ------------------------------------------------------------------ single tokens
 // One token per row; a CTA takes `vc` columns of one row's head: lanes cover
@@ -704,8 +809,8 @@ __global__ void __launch_bounds__(STHREADS)
   }
 }
 
-#define TTT_BY_ROWS(CALL)                     \
-  switch ((p.dk + 31) / 32) {                 \
+#define TTT_BY_ROWS(ROWS, CALL)               \
+  switch (((ROWS) + 31) / 32) {               \
     case 1: CALL(1); break;                   \
     case 2: CALL(2); break;                   \
     case 3: CALL(3); break;                   \
@@ -721,7 +826,7 @@ int rec_launch(const DeltaLaunch& p, float* S_out, const float* S_in, Tout* out,
   delta_rec_kernel<Tin, Tout, R4><<<grid, THREADS, 0, stream>>>(                               \
       (const Tin*)p.q, (const Tin*)p.k, (const Tin*)p.v, (const Tin*)p.g, (const Tin*)p.beta,  \
       S_in, S_out, out, ev, Sc, p.N, p.dk, p.dv, p.scale)
-  TTT_BY_ROWS(TTT_REC)
+  TTT_BY_ROWS(p.dk, TTT_REC)
 #undef TTT_REC
   prof_after(K_DELTA_REC, stream);
   return cudaGetLastError() == cudaSuccess ? 0 : -1;
@@ -743,14 +848,18 @@ int bwd_launch(const DeltaBwdLaunch& L, cudaStream_t stream) {
   delta_rev_kernel<Tin, R4><<<grid, THREADS, 0, stream>>>(                                        \
       (const Tin*)p.q, (const Tin*)p.k, (const Tin*)L.dout, (const Tin*)p.g, (const Tin*)p.beta,  \
       L.dS_end, L.dS0, du, Xc, p.N, p.dk, p.dv, p.scale)
-  TTT_BY_ROWS(TTT_REV)
+  TTT_BY_ROWS(p.dk, TTT_REV)
 #undef TTT_REV
   prof_after(K_DELTA_REV, stream);
   if (cudaGetLastError() != cudaSuccess) return -1;
   const size_t smem = chunk_grad_smem(p.dk, p.dv);
-  auto kfn = delta_chunk_grad_kernel<Tin>;
-  static std::atomic<uint64_t> attr{0};
-  if (allow_dynamic_smem(kfn, (int)chunk_grad_smem(DMAX, DMAX), attr)) return -1;
+  void (*kfn)(ChunkArgs<Tin>) = nullptr;
+  static std::atomic<uint64_t> attr[4] = {};
+  const int widest = std::max(p.dk, p.dv);
+#define TTT_GRAD(R4) kfn = delta_chunk_grad_kernel<Tin, R4>
+  TTT_BY_ROWS(widest, TTT_GRAD)
+#undef TTT_GRAD
+  if (allow_dynamic_smem(kfn, (int)chunk_grad_smem(DMAX, DMAX), attr[(widest - 1) / 32])) return -1;
   ChunkArgs<Tin> a{(const Tin*)p.q, (const Tin*)p.k, (const Tin*)L.dout, (const Tin*)p.g,
                    (const Tin*)p.beta, ev, du, Sc, Xc, (Tin*)L.dq, (Tin*)L.dk, (Tin*)L.dv,
                    (Tin*)L.dg, (Tin*)L.dbeta, p.N, p.dk, p.dv, p.scale};
