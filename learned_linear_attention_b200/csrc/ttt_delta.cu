@@ -674,36 +674,44 @@ __global__ void __launch_bounds__(GTHREADS) delta_chunk_grad_kernel(ChunkArgs<Ti
 size_t chunk_grad_smem(int dk, int dv) { return sizeof(float) * GradSmem(dk, dv).floats; }
 
 // ------------------------------------------------------------------ single tokens
-// One token per row; a CTA takes `vc` columns of one row's head: lanes cover
-// the columns four at a time, the other threads split dk.  The state slice is
+// One token per row; a CTA takes VC columns of one row's head: lanes cover the
+// columns four at a time, the other threads split dk.  The state slice is
 // read into registers in one sweep, the two dot products over dk (S^T k, and
 // q.S' from q.S and q.k) are joined through shared memory in one exchange,
 // and the slice is written back: bound by the state's bytes.
 constexpr int STHREADS = 128;
-constexpr int SROWS = 32;       // most rows of dk a thread holds
 
-template <typename Tin, typename Tout>
-__global__ void __launch_bounds__(STHREADS)
+template <typename Tin, typename Tout, int VC>
+__global__ void __launch_bounds__(STHREADS, 7)
     delta_step_kernel(const Tin* __restrict__ q, const Tin* __restrict__ k, const Tin* __restrict__ v,
                       const Tin* __restrict__ g, const Tin* __restrict__ beta,
                       const int* __restrict__ slots, int n_slots, float* __restrict__ S,
-                      Tout* __restrict__ out, int B, int H, int dk, int dv, int vc, float scale) {
+                      Tout* __restrict__ out, int B, int H, int dk, int dv, float scale) {
+  constexpr int lanes = VC / 4, groups = STHREADS / lanes, SROWS = DMAX / groups;   // SROWS: rows of a thread
   __shared__ float ks[DMAX], qs[DMAX];
   __shared__ float part[2][STHREADS][4];   // partial S^T k and S^T q of four columns
   __shared__ float qk_s;
-  __shared__ int again;
-  const int h = blockIdx.y, c0 = blockIdx.z * vc, tid = threadIdx.x;
+  __shared__ int next_s;
+  static_assert(DMAX == STHREADS, "a thread brings one row of k and q");
+  const int h = blockIdx.y, c0 = blockIdx.z * VC, tid = threadIdx.x;
   int b = blockIdx.x;
   const int slot = slots != nullptr ? slots[b] : b;
   if (slot < 0 || slot >= n_slots) return;
-  if (slots != nullptr) {   // a sequence's first row takes all of its rows, in order
-    int dup = 0;
-    for (int j = tid; j < b; j += STHREADS) dup |= slots[j] == slot;
-    if (__syncthreads_or(dup)) return;
-  }
-  const int lanes = vc / 4, groups = STHREADS / lanes;
   const int cl = tid % lanes, gr = tid / lanes, c = c0 + 4 * cl;
   const bool vec = (dv & 3) == 0;
+  // every load of the row before the first wait
+  Tin kr_, qr_, vr_[4], gr_, br_;
+  const Tin zero = from_f<Tin>(0.f);
+  auto fetch = [&]() {
+    const size_t tok = (size_t)b * H + h;
+    kr_ = tid < dk ? k[tok * dk + tid] : zero;
+    qr_ = tid < dk ? q[tok * dk + tid] : zero;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) vr_[j] = c + j < dv ? v[tok * dv + c + j] : zero;
+    gr_ = g != nullptr ? g[tok] : zero;
+    br_ = beta[tok];
+  };
+  fetch();
   float* Sm = S + ((size_t)slot * H + h) * dk * dv;
   float4 s[SROWS];
 #pragma unroll
@@ -722,14 +730,26 @@ __global__ void __launch_bounds__(STHREADS)
       }
     }
   }
+  int next = B;
+  if (slots != nullptr) {   // a sequence's first row takes all of its rows, in order
+    if (tid == 0) next_s = B;
+    __syncthreads();
+    int before = 0, after = B;
+    for (int j = tid; j < B; j += STHREADS) {
+      if (slots[j] != slot) continue;
+      if (j < b) before = 1;
+      else if (j > b) after = min(after, j);
+    }
+    if (after < B) atomicMin(&next_s, after);
+    if (__syncthreads_or(before)) return;
+    next = next_s;
+  }
   for (;;) {
     const size_t tok = (size_t)b * H + h;
-    for (int i = tid; i < DMAX; i += STHREADS) {
-      ks[i] = i < dk ? to_f(k[tok * dk + i]) : 0.f;
-      qs[i] = i < dk ? to_f(q[tok * dk + i]) : 0.f;
-    }
+    ks[tid] = to_f(kr_);
+    qs[tid] = to_f(qr_);
     __syncthreads();
-    const float a = g != nullptr ? expf(to_f(g[tok])) : 1.f, bt = to_f(beta[tok]);
+    const float a = expf(to_f(gr_)), bt = to_f(br_);
     float4 pk = make_float4(0.f, 0.f, 0.f, 0.f), pq = pk;
 #pragma unroll
     for (int i = 0; i < SROWS; ++i) {
@@ -765,7 +785,7 @@ __global__ void __launch_bounds__(STHREADS)
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
       if (c + j < dv) {
-        u[j] = bt * (to_f(v[tok * dv + c + j]) - a * pks[j]);
+        u[j] = bt * (to_f(vr_[j]) - a * pks[j]);
         // S'^T q = a S^T q + (q.k) u
         if (gr == 0) out[tok * dv + c + j] = from_f<Tout>(scale * fmaf(qk_s, u[j], a * pqs[j]));
       }
@@ -779,18 +799,18 @@ __global__ void __launch_bounds__(STHREADS)
         s[i].z = fmaf(kr, u[2], a * s[i].z); s[i].w = fmaf(kr, u[3], a * s[i].w);
       }
     }
-    if (slots == nullptr) break;
+    if (next >= B) break;
     // the next row of the same sequence
-    if (tid == 0) again = B;
+    b = next;
+    fetch();
+    if (tid == 0) next_s = B;
+    __syncthreads();   // every thread is behind its reads of ks, qs and next_s
+    int after = B;
+    for (int j = b + 1 + tid; j < B && after == B; j += STHREADS)
+      if (slots[j] == slot) after = j;
+    if (after < B) atomicMin(&next_s, after);
     __syncthreads();
-    int next = B;
-    for (int j = b + 1 + tid; j < B; j += STHREADS)
-      if (slots[j] == slot) { next = j; break; }
-    if (next < B) atomicMin(&again, next);
-    __syncthreads();
-    if (again >= B) break;
-    b = again;
-    __syncthreads();   // `again`, ks and qs are written again above
+    next = next_s;
   }
 #pragma unroll
   for (int i = 0; i < SROWS; ++i) {
@@ -915,16 +935,20 @@ int launch_delta_rec_bwd(const DeltaBwdLaunch& L, cudaStream_t stream) {
 }
 
 int launch_delta_step(const DeltaLaunch& p, const int* slots, int n_slots, cudaStream_t stream) {
-  // columns of a CTA: all of them where rows and heads fill the device, fewer
-  // where they do not (a slice of 16 columns is 64 bytes of every state row)
-  int vc = 16;
-  while (vc < 128 && vc < p.dv) vc *= 2;
-  while (vc > 16 && (long long)p.B * p.H * ((p.dv + vc - 1) / vc) < 4 * 148) vc /= 2;
+  // columns of a CTA: a slice of 32 is one 128-byte line of every state row and
+  // 16 KB in all, so that a dozen CTAs of an SM keep loads and stores mixed;
+  // half of it where rows and heads do not fill the device
+  const int vc = (long long)p.B * p.H * ((p.dv + 31) / 32) < 4 * 148 ? 16 : 32;
   const dim3 grid((unsigned)p.B, (unsigned)p.H, (unsigned)((p.dv + vc - 1) / vc));
-#define TTT_STEP(TI, TO)                                                                          \
-  delta_step_kernel<TI, TO><<<grid, STHREADS, 0, stream>>>(                                        \
+#define TTT_STEP_VC(TI, TO, VC)                                                                    \
+  delta_step_kernel<TI, TO, VC><<<grid, STHREADS, 0, stream>>>(                                    \
       (const TI*)p.q, (const TI*)p.k, (const TI*)p.v, (const TI*)p.g, (const TI*)p.beta, slots,    \
-      n_slots, p.S, (TO*)p.out, p.B, p.H, p.dk, p.dv, vc, p.scale)
+      n_slots, p.S, (TO*)p.out, p.B, p.H, p.dk, p.dv, p.scale)
+#define TTT_STEP(TI, TO)                     \
+  do {                                       \
+    if (vc == 16) TTT_STEP_VC(TI, TO, 16);   \
+    else TTT_STEP_VC(TI, TO, 32);            \
+  } while (0)
   prof_before(K_DELTA_STEP, stream);
   if (p.in_bf16) {
     if (p.out_bf16) TTT_STEP(__nv_bfloat16, __nv_bfloat16);
@@ -934,6 +958,7 @@ int launch_delta_step(const DeltaLaunch& p, const int* slots, int n_slots, cudaS
     else TTT_STEP(float, float);
   }
 #undef TTT_STEP
+#undef TTT_STEP_VC
   prof_after(K_DELTA_STEP, stream);
   return cudaGetLastError() == cudaSuccess ? 0 : -1;
 }

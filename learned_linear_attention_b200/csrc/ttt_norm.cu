@@ -18,13 +18,12 @@ namespace {
 constexpr int THREADS = 256;
 
 template <typename T>
-struct Vec;   // 16 bytes of T as floats
+struct Vec;   // 16 bytes of T; kept as they are until they are worked on
 template <>
 struct Vec<float> {
   static constexpr int N = 4;
-  static TTT_DEVICE_INLINE void load(const float* p, float* x) {
-    const float4 t = *reinterpret_cast<const float4*>(p);
-    x[0] = t.x; x[1] = t.y; x[2] = t.z; x[3] = t.w;
+  static TTT_DEVICE_INLINE void get(const uint4& t, float* x) {
+    x[0] = __uint_as_float(t.x); x[1] = __uint_as_float(t.y); x[2] = __uint_as_float(t.z); x[3] = __uint_as_float(t.w);
   }
   static TTT_DEVICE_INLINE void store(float* p, const float* x) {
     *reinterpret_cast<float4*>(p) = make_float4(x[0], x[1], x[2], x[3]);
@@ -33,8 +32,7 @@ struct Vec<float> {
 template <>
 struct Vec<__nv_bfloat16> {
   static constexpr int N = 8;
-  static TTT_DEVICE_INLINE void load(const __nv_bfloat16* p, float* x) {
-    const uint4 t = *reinterpret_cast<const uint4*>(p);
+  static TTT_DEVICE_INLINE void get(const uint4& t, float* x) {
     const uint32_t w[4] = {t.x, t.y, t.z, t.w};
 #pragma unroll
     for (int i = 0; i < 4; ++i) { x[2 * i] = bf16lo(w[i]); x[2 * i + 1] = bf16hi(w[i]); }
@@ -44,6 +42,10 @@ struct Vec<__nv_bfloat16> {
                                               pack_bf16x2(x[4], x[5]), pack_bf16x2(x[6], x[7]));
   }
 };
+template <typename E>
+TTT_DEVICE_INLINE uint4 raw(const void* p, size_t at) {
+  return *reinterpret_cast<const uint4*>(static_cast<const E*>(p) + at);
+}
 
 // Sum over the T threads of a row (T = 256: the CTA, through shared memory).
 template <int T>
@@ -61,7 +63,9 @@ TTT_DEVICE_INLINE float row_sum(float x, float* red) {
   return x;
 }
 
-TTT_DEVICE_INLINE float sigmoidf(float z) { return 1.f / (1.f + __expf(-z)); }
+// __fdividef(1, y) is 0 for y > 2^126, where sigmoid is below float32's normal
+// range; z = -inf gives 0 and NaN stays
+TTT_DEVICE_INLINE float sigmoidf(float z) { return __fdividef(1.f, 1.f + __expf(-z)); }
 
 struct NormArgs {
   const void *x, *z, *res, *dout;
@@ -70,22 +74,75 @@ struct NormArgs {
   float* part;   // partial sums of dw [gridDim.x][D]
   long long rows;
   int D, kind, gate;
-  float eps, scale;
+  float eps, scale, inv_d;
 };
 
-// r of a row with sum of squares ss; dr = 0 where r does not depend on x
+// r of a row with sum of squares ss; `fixed` where r does not depend on x
 TTT_DEVICE_INLINE float row_r(const NormArgs& a, float ss, bool& fixed) {
-  if (a.kind == 0) { fixed = false; return 1.f / sqrtf(ss / a.D + a.eps); }
+  if (a.kind == 0) {
+    fixed = false;
+    // rsqrtf with one Newton step, which an infinite sum would make NaN
+    const float m = fmaf(ss, a.inv_d, a.eps), y = rsqrtf(m);
+    return m < 3e38f ? fmaf(0.5f * y, fmaf(-m * y, y, 1.f), y) : y;
+  }
   const float len = sqrtf(ss);
   fixed = !(len > a.eps);
   return 1.f / (fixed && len == len ? a.eps : len);
 }
 
+// A thread's vectors of a row of up to three tensors.  Where it holds one or
+// two, the next row's are on their way while this one is worked on: the work
+// (two or three transcendental functions an element) takes as long as the
+// loads, and four CTAs an SM alone would leave the memory idle meanwhile.
 template <typename E, int T, int V>
-__global__ void __launch_bounds__(THREADS) norm_fwd_kernel(NormArgs a) {
-  constexpr int N = Vec<E>::N, GROUPS = THREADS / T;
-  __shared__ float red[THREADS / 32];
+struct Row {
+  uint4 v[3][V];
+  TTT_DEVICE_INLINE void load(const NormArgs& a, const void* p0, const void* p1, const void* p2, long long row,
+                              int t) {
+    constexpr int N = Vec<E>::N;
+    const size_t at = (size_t)row * a.D;
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      const int c = (i * T + t) * N;
+      v[0][i] = v[1][i] = v[2][i] = make_uint4(0, 0, 0, 0);
+      if (row >= a.rows || c >= a.D) continue;
+      v[0][i] = raw<E>(p0, at + c);
+      if (p1 != nullptr) v[1][i] = raw<E>(p1, at + c);
+      if (p2 != nullptr) v[2][i] = raw<E>(p2, at + c);
+    }
+  }
+};
+template <typename E, int T, int V, typename F>
+TTT_DEVICE_INLINE void for_rows(const NormArgs& a, const void* p0, const void* p1, const void* p2, F work) {
+  constexpr int GROUPS = THREADS / T;
   const int t = threadIdx.x % T, gr = threadIdx.x / T;
+  // a warp's groups leave the loop together: the bound is on the CTA's first row
+  const long long step = (long long)gridDim.x * GROUPS;
+  long long r0 = (long long)blockIdx.x * GROUPS;
+  Row<E, T, V> cur;
+  if constexpr (V <= 2) {
+    if (r0 < a.rows) cur.load(a, p0, p1, p2, r0 + gr, t);
+    for (; r0 < a.rows; r0 += step) {
+      Row<E, T, V> next;
+      next.load(a, p0, p1, p2, r0 + step + gr, t);
+      work(cur, r0 + gr);
+      cur = next;
+    }
+  } else {
+    for (; r0 < a.rows; r0 += step) {
+      cur.load(a, p0, p1, p2, r0 + gr, t);
+      work(cur, r0 + gr);
+    }
+  }
+}
+template <int V>
+constexpr int ctas() { return V == 1 ? 4 : 1; }
+
+template <typename E, int T, int V>
+__global__ void __launch_bounds__(THREADS, ctas<V>()) norm_fwd_kernel(NormArgs a) {
+  constexpr int N = Vec<E>::N;
+  __shared__ float red[THREADS / 32];
+  const int t = threadIdx.x % T;
   float w[V][N];
 #pragma unroll
   for (int v = 0; v < V; ++v) {
@@ -93,124 +150,107 @@ __global__ void __launch_bounds__(THREADS) norm_fwd_kernel(NormArgs a) {
 #pragma unroll
     for (int i = 0; i < N; ++i) w[v][i] = a.scale * (a.w != nullptr && c < a.D ? a.w[c + i] : 1.f);
   }
-  // a warp's groups leave the loop together: its rows are adjacent, and the
-  // bound is on the warp's first row
-  const long long step = (long long)gridDim.x * GROUPS;
-  for (long long r0 = (long long)blockIdx.x * GROUPS; r0 < a.rows; r0 += step) {
-    const long long row = r0 + gr;
-    const bool live = row < a.rows;
-    const E* xp = static_cast<const E*>(a.x) + row * a.D;
-    float x[V][N], ss = 0.f;
+  for_rows<E, T, V>(a, a.x, a.gate != 0 ? a.z : nullptr, a.res, [&](const Row<E, T, V>& in, long long row) {
+    float ss = 0.f;
 #pragma unroll
     for (int v = 0; v < V; ++v) {
-      const int c = (v * T + t) * N;
-      if (live && c < a.D) {
-        Vec<E>::load(xp + c, x[v]);
-      } else {
+      float x[N];
+      Vec<E>::get(in.v[0][v], x);
 #pragma unroll
-        for (int i = 0; i < N; ++i) x[v][i] = 0.f;
-      }
-#pragma unroll
-      for (int i = 0; i < N; ++i) ss = fmaf(x[v][i], x[v][i], ss);
+      for (int i = 0; i < N; ++i) ss = fmaf(x[i], x[i], ss);
     }
-    float z[V][N], rs[V][N];
-#pragma unroll
-    for (int v = 0; v < V; ++v) {
-      const int c = (v * T + t) * N;
-      if (live && c < a.D && a.gate != 0) Vec<E>::load(static_cast<const E*>(a.z) + row * a.D + c, z[v]);
-      if (live && c < a.D && a.res != nullptr) Vec<E>::load(static_cast<const E*>(a.res) + row * a.D + c, rs[v]);
-    }
-    ss = row_sum<T>(ss, red);
     bool fixed;
-    const float r = row_r(a, ss, fixed);
+    const float r = row_r(a, row_sum<T>(ss, red), fixed);
 #pragma unroll
     for (int v = 0; v < V; ++v) {
       const int c = (v * T + t) * N;
-      if (!live || c >= a.D) continue;
+      if (row >= a.rows || c >= a.D) continue;
+      float x[N], z[N], rs[N];
+      Vec<E>::get(in.v[0][v], x);
+      Vec<E>::get(in.v[1][v], z);
+      Vec<E>::get(in.v[2][v], rs);
 #pragma unroll
       for (int i = 0; i < N; ++i) {
-        float y = x[v][i] * r * w[v][i];
+        float y = x[i] * r * w[v][i];
         if (a.gate != 0) {
-          const float s = sigmoidf(z[v][i]);
-          y *= a.gate == 1 ? z[v][i] * s : s;
+          const float s = sigmoidf(z[i]);
+          y *= a.gate == 1 ? z[i] * s : s;
         }
-        x[v][i] = a.res != nullptr ? y + rs[v][i] : y;
+        x[i] = a.res != nullptr ? y + rs[i] : y;
       }
-      Vec<E>::store(static_cast<E*>(a.out) + row * a.D + c, x[v]);
+      Vec<E>::store(static_cast<E*>(a.out) + (size_t)row * a.D + c, x);
     }
-  }
+  });
 }
 
 // With n = x r, p = scale dout:  dz = p n w act'(z),  dw = sum p act(z) n,
 // dn = p w act(z),  dx = r (dn - n mean(dn n))  (RMS; for L2 the sum instead
 // of the mean, and no such term where r is 1 / eps).
 template <typename E, int T, int V>
-__global__ void __launch_bounds__(THREADS) norm_bwd_kernel(NormArgs a) {
+__global__ void __launch_bounds__(THREADS, V == 1 ? 3 : 1) norm_bwd_kernel(NormArgs a) {
   constexpr int N = Vec<E>::N, GROUPS = THREADS / T;
   __shared__ float red[THREADS / 32];
   extern __shared__ float acc_s[];   // [GROUPS][D] where dw is wanted
   const int t = threadIdx.x % T, gr = threadIdx.x / T;
-  float dw[V][N];
+  float dw[V][N], w[V][N];
 #pragma unroll
-  for (int v = 0; v < V; ++v)
+  for (int v = 0; v < V; ++v) {
+    const int c = (v * T + t) * N;
 #pragma unroll
-    for (int i = 0; i < N; ++i) dw[v][i] = 0.f;
-  const long long step = (long long)gridDim.x * GROUPS;
-  for (long long r0 = (long long)blockIdx.x * GROUPS; r0 < a.rows; r0 += step) {
-    const long long row = r0 + gr;
-    const bool live = row < a.rows;
-    float x[V][N], d[V][N], z[V][N], ss = 0.f;
-#pragma unroll
-    for (int v = 0; v < V; ++v) {
-      const int c = (v * T + t) * N;
-      const bool in = live && c < a.D;
-#pragma unroll
-      for (int i = 0; i < N; ++i) x[v][i] = d[v][i] = z[v][i] = 0.f;
-      if (in) {
-        Vec<E>::load(static_cast<const E*>(a.x) + row * a.D + c, x[v]);
-        Vec<E>::load(static_cast<const E*>(a.dout) + row * a.D + c, d[v]);
-        if (a.gate != 0) Vec<E>::load(static_cast<const E*>(a.z) + row * a.D + c, z[v]);
-      }
-#pragma unroll
-      for (int i = 0; i < N; ++i) ss = fmaf(x[v][i], x[v][i], ss);
+    for (int i = 0; i < N; ++i) {
+      dw[v][i] = 0.f;
+      w[v][i] = a.w != nullptr && c < a.D ? a.w[c + i] : 1.f;
     }
-    ss = row_sum<T>(ss, red);
+  }
+  for_rows<E, T, V>(a, a.x, a.dout, a.gate != 0 ? a.z : nullptr, [&](const Row<E, T, V>& in, long long row) {
+    float ss = 0.f, dot = 0.f, dn[V][N];
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      float x[N];
+      Vec<E>::get(in.v[0][v], x);
+#pragma unroll
+      for (int i = 0; i < N; ++i) ss = fmaf(x[i], x[i], ss);
+    }
     bool fixed;
-    const float r = row_r(a, ss, fixed);
-    float dot = 0.f;
+    const float r = row_r(a, row_sum<T>(ss, red), fixed);
 #pragma unroll
     for (int v = 0; v < V; ++v) {
       const int c = (v * T + t) * N;
-      const bool in = live && c < a.D;
+      float x[N], z[N], d[N];
+      Vec<E>::get(in.v[0][v], x);
+      Vec<E>::get(in.v[1][v], d);
+      Vec<E>::get(in.v[2][v], z);
 #pragma unroll
       for (int i = 0; i < N; ++i) {
-        const float n = x[v][i] * r;
-        float p = a.scale * d[v][i];
-        const float w = in && a.w != nullptr ? a.w[c + i] : 1.f;
+        const float n = x[i] * r;
+        float p = a.scale * d[i];
         if (a.gate != 0) {
-          const float s = sigmoidf(z[v][i]);
-          const float act = a.gate == 1 ? z[v][i] * s : s;
-          const float dact = a.gate == 1 ? s * (1.f + z[v][i] * (1.f - s)) : s * (1.f - s);
-          z[v][i] = p * n * w * dact;
+          const float s = sigmoidf(z[i]);
+          // act' is s (1 + z (1 - s)) for silu, s (1 - s) for the sigmoid
+          const float act = a.gate == 1 ? z[i] * s : s;
+          const float dact = a.gate == 1 ? fmaf(act, 1.f - s, s) : fmaf(-s, s, s);
+          z[i] = p * n * w[v][i] * dact;
           p *= act;
         }
         dw[v][i] = fmaf(p, n, dw[v][i]);
-        d[v][i] = p * w;
-        dot = fmaf(d[v][i], n, dot);
+        dn[v][i] = p * w[v][i];
+        dot = fmaf(dn[v][i], n, dot);
       }
-      if (in && a.gate != 0) Vec<E>::store(static_cast<E*>(a.dz) + row * a.D + c, z[v]);
+      if (a.gate != 0 && row < a.rows && c < a.D) Vec<E>::store(static_cast<E*>(a.dz) + (size_t)row * a.D + c, z);
     }
     dot = row_sum<T>(dot, red);
-    const float m = fixed ? 0.f : a.kind == 0 ? dot / a.D : dot;
+    const float m = fixed ? 0.f : a.kind == 0 ? dot * a.inv_d : dot;
 #pragma unroll
     for (int v = 0; v < V; ++v) {
       const int c = (v * T + t) * N;
-      if (!live || c >= a.D) continue;
+      if (row >= a.rows || c >= a.D) continue;
+      float x[N];
+      Vec<E>::get(in.v[0][v], x);
 #pragma unroll
-      for (int i = 0; i < N; ++i) x[v][i] = r * (d[v][i] - x[v][i] * r * m);
-      Vec<E>::store(static_cast<E*>(a.dx) + row * a.D + c, x[v]);
+      for (int i = 0; i < N; ++i) x[i] = r * fmaf(-m, x[i] * r, dn[v][i]);
+      Vec<E>::store(static_cast<E*>(a.dx) + (size_t)row * a.D + c, x);
     }
-  }
+  });
   if (a.part == nullptr) return;
 #pragma unroll
   for (int v = 0; v < V; ++v) {
@@ -282,6 +322,7 @@ NormArgs args_of(const NormLaunch& L) {
   a.x = L.x; a.z = L.z; a.res = L.res; a.dout = L.dout; a.w = L.w;
   a.out = L.out; a.dx = L.dx; a.dz = L.dz;
   a.rows = L.rows; a.D = L.D; a.kind = L.kind; a.gate = L.gate; a.eps = L.eps; a.scale = L.scale;
+  a.inv_d = 1.f / (float)L.D;
   return a;
 }
 
