@@ -47,7 +47,8 @@ TTT_DEVICE_INLINE uint4 raw(const void* p, size_t at) {
   return *reinterpret_cast<const uint4*>(static_cast<const E*>(p) + at);
 }
 
-// Sum over the T threads of a row (T = 256: the CTA, through shared memory).
+// Sum over the T threads of a row (several warps: through shared memory, by
+// the whole CTA together).
 template <int T>
 TTT_DEVICE_INLINE float row_sum(float x, float* red) {
 #pragma unroll
@@ -57,8 +58,9 @@ TTT_DEVICE_INLINE float row_sum(float x, float* red) {
     if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = x;
     __syncthreads();
     x = 0.f;
+    const float* mine = red + threadIdx.x / T * (T / 32);
 #pragma unroll
-    for (int w = 0; w < T / 32; ++w) x += red[w];
+    for (int w = 0; w < T / 32; ++w) x += mine[w];
   }
   return x;
 }
@@ -267,39 +269,46 @@ __global__ void __launch_bounds__(THREADS, V == 1 ? 3 : 1) norm_bwd_kernel(NormA
   }
 }
 
-// dw[c] = sum of the CTAs' partial sums, in their order: 32 columns and 8
+// dw[c] = sum of the CTAs' partial sums, in their order: 32 columns and 32
 // interleaved runs of partial sums to a CTA.
-__global__ void __launch_bounds__(256) norm_dw_kernel(const float* __restrict__ part, int n, int D,
-                                                      float* __restrict__ dw) {
-  __shared__ float s[8][33];
-  const int c = blockIdx.x * 32 + threadIdx.x % 32, j0 = threadIdx.x / 32;
+__global__ void __launch_bounds__(1024) norm_dw_kernel(const float* __restrict__ part, int n, int D,
+                                                       float* __restrict__ dw) {
+  __shared__ float s[32][33];
+  const int l = threadIdx.x % 32, j0 = threadIdx.x / 32, c = blockIdx.x * 32 + l;
   float acc = 0.f;
   if (c < D)
-    for (int j = j0; j < n; j += 8) acc += part[(size_t)j * D + c];
-  s[j0][threadIdx.x % 32] = acc;
+#pragma unroll 8
+    for (int j = j0; j < n; j += 32) acc += part[(size_t)j * D + c];
+  s[j0][l] = acc;
   __syncthreads();
   if (j0 == 0 && c < D) {
-    for (int j = 1; j < 8; ++j) acc += s[j][threadIdx.x];
+#pragma unroll
+    for (int j = 1; j < 32; ++j) acc += s[j][l];
     dw[c] = acc;
   }
 }
 
 struct Shape { int T, V; };
-// threads of a row and vectors of a thread: few threads keep several rows'
-// loads in flight in a warp, one vector per thread keeps accesses whole
+// Threads of a row and vectors of a thread: few threads keep several rows'
+// loads in flight in a warp, one vector a thread keeps accesses whole and the
+// next row in registers.  A warp takes a row of up to four float32 vectors a
+// thread (512 of them: 79 us against 96 for a whole CTA a row, 134 MB in and
+// out); bf16 vectors hold twice the values, and rows of more than two a thread go
+// to several warps (512 values: 46 us against 57; 1024 values: 67 against 44).
 Shape norm_shape(int D, int per_vec) {
-  const int nv = (D + per_vec - 1) / per_vec;
+  const int nv = (D + per_vec - 1) / per_vec, most = per_vec == 4 ? 128 : 64;
   int T = 4;
   while (T < 32 && T < nv) T *= 2;
-  if (nv > 128) T = 256;
+  while (T < 256 && nv > most && T < nv) T *= 2;
   int V = 1;
   while (T * V < nv) V *= 2;
   return {T, V};
 }
 
-int norm_grid(long long rows, int T, int sms) {
+// `per_sm` CTAs an SM: as many as are resident (see __launch_bounds__), so that all take the same number of rows
+int norm_grid(long long rows, int T, int sms, int per_sm) {
   const long long groups = THREADS / T;
-  return (int)std::min<long long>((rows + groups - 1) / groups, (long long)sms * 8);
+  return (int)std::max<long long>(1, std::min<long long>((rows + groups - 1) / groups, (long long)sms * per_sm));
 }
 
 template <typename E, bool BWD>
@@ -312,6 +321,7 @@ int launch_t(const NormArgs& a, int grid, size_t smem, cudaStream_t stream) {
     return cudaGetLastError() == cudaSuccess ? 0 : -1;                                 \
   }
   TTT_NORM(4, 1) TTT_NORM(8, 1) TTT_NORM(16, 1) TTT_NORM(32, 1) TTT_NORM(32, 2) TTT_NORM(32, 4)
+  TTT_NORM(64, 1) TTT_NORM(128, 1)
   TTT_NORM(256, 1) TTT_NORM(256, 2) TTT_NORM(256, 4) TTT_NORM(256, 8)
 #undef TTT_NORM
   return -1;
@@ -329,12 +339,12 @@ NormArgs args_of(const NormLaunch& L) {
 }  // namespace
 
 int norm_bwd_parts(long long rows, int D, int bf16, int sms) {
-  return std::max(1, norm_grid(rows, norm_shape(D, bf16 ? 8 : 4).T, sms));
+  return norm_grid(rows, norm_shape(D, bf16 ? 8 : 4).T, sms, 3);
 }
 
 int launch_norm_fwd(const NormLaunch& L, int sms, cudaStream_t stream) {
   const NormArgs a = args_of(L);
-  const int grid = norm_bwd_parts(L.rows, L.D, L.bf16, sms);
+  const int grid = norm_grid(L.rows, norm_shape(L.D, L.bf16 ? 8 : 4).T, sms, 4);
   prof_before(K_NORM, stream);
   const int r = L.bf16 ? launch_t<__nv_bfloat16, false>(a, grid, 0, stream)
                        : launch_t<float, false>(a, grid, 0, stream);
@@ -352,7 +362,7 @@ int launch_norm_bwd(const NormLaunch& L, int sms, cudaStream_t stream) {
   const int r = L.bf16 ? launch_t<__nv_bfloat16, true>(a, grid, smem, stream)
                        : launch_t<float, true>(a, grid, smem, stream);
   if (r == 0 && L.dw != nullptr)
-    norm_dw_kernel<<<(L.D + 31) / 32, 256, 0, stream>>>(a.part, grid, L.D, L.dw);
+    norm_dw_kernel<<<(L.D + 31) / 32, 1024, 0, stream>>>(a.part, grid, L.D, L.dw);
   prof_after(K_NORM_BWD, stream);
   return r == 0 && cudaGetLastError() == cudaSuccess ? 0 : -1;
 }
