@@ -396,13 +396,15 @@ struct ChainSmem {
   static constexpr int STAGES = D == 64 ? 4 : 2;
   static constexpr uint32_t SA = D * 128;                 // bytes of a [D][64] atom
   static constexpr uint32_t STAGE = 2 * (D / 64) * SA;    // Mc hi, lo
-  static constexpr uint32_t X = STAGES * STAGE;           // [hi, lo]
-  static constexpr uint32_t BAR = X + 2 * SA;
+  static constexpr uint32_t X = STAGES * STAGE;           // two of [hi, lo], in turn
+  static constexpr uint32_t BAR = X + 4 * SA;
   static constexpr uint32_t TOTAL = BAR + 128;
 };
 
+constexpr int CHAIN_THREADS = 512;
+
 template <int D>
-__global__ void __launch_bounds__(512, 1)
+__global__ void __launch_bounds__(CHAIN_THREADS, 1)
     delta_chain_kernel(const __grid_constant__ CUtensorMap mapM, const __grid_constant__ CUtensorMap mapXf,
                        const __grid_constant__ CUtensorMap mapXr, ChainArgs a) {
   using SM = ChainSmem<D>;
@@ -441,7 +443,8 @@ __global__ void __launch_bounds__(512, 1)
   const uint32_t lanes = (uint32_t)(q4 * 32) << 16;
   const int col = slice * 64 + cg * 16;
   int issued = 0;
-  auto fetch = [&]() {   // by thread 0: the next chunk's Mc
+  // one thread each issues the products, the loads and the stores
+  auto fetch = [&]() {   // by thread 32: the next chunk's Mc
     if (issued >= a.nch) return;
     const int s = issued % STAGES;
     mbar_arrive_expect_tx(&full[s], SM::STAGE);
@@ -451,7 +454,7 @@ __global__ void __launch_bounds__(512, 1)
                     (int)(2 * chunk(issued) + h));
     ++issued;
   };
-  if (tid == 0)
+  if (tid == 32)
     for (int s = 0; s < STAGES; ++s) fetch();
   float x[16];
 #pragma unroll
@@ -460,7 +463,7 @@ __global__ void __launch_bounds__(512, 1)
     if (own && dir.S_in != nullptr) v = *reinterpret_cast<const float4*>(dir.S_in + (bh * D + r) * D + col + j);
     x[j] = v.x; x[j + 1] = v.y; x[j + 2] = v.z; x[j + 3] = v.w;
   }
-  auto put_x = [&]() {   // the operand copy
+  auto put_x = [&](uint32_t xb) {   // the operand copy
     if (!own) return;
     uint32_t h[8], l[8];
 #pragma unroll
@@ -468,8 +471,8 @@ __global__ void __launch_bounds__(512, 1)
 #pragma unroll
     for (int i = 0; i < 8; i += 4) {
       const uint32_t o = sw128_offset(r, cg * 16 + 2 * i);
-      st_shared_v4(sb + SM::X + o, h[i], h[i + 1], h[i + 2], h[i + 3]);
-      st_shared_v4(sb + SM::X + SM::SA + o, l[i], l[i + 1], l[i + 2], l[i + 3]);
+      st_shared_v4(xb + o, h[i], h[i + 1], h[i + 2], h[i + 3]);
+      st_shared_v4(xb + SM::SA + o, l[i], l[i + 1], l[i + 2], l[i + 3]);
     }
   };
   auto load_h = [&](int c, float4 (&h)[4]) {
@@ -481,20 +484,38 @@ __global__ void __launch_bounds__(512, 1)
   float e = 0.f;
   load_h(0, h);
   e = a.gend[chunk(0)];
+  // One CTA barrier a chunk: it publishes X and tells whether every thread saw
+  // the last product complete.
+  bool ok = true;
   for (int c = 0; c < a.nch; ++c) {
-    put_x();
-    ph.publish();
+    const uint32_t xo = SM::X + (c & 1) * 2 * SM::SA, xb = sb + xo;
+    put_x(xb);
+    fence_async_smem();
+    tc_fence_before();
+    if (tid == 64) bulk_wait_read();   // behind this barrier the other copy may be written again
+    if (!named_bar_all(1, CHAIN_THREADS, ok)) break;
+    tc_fence_after();
     if (tid == 0) {
       const int s = c % STAGES;
       if (ph.W.wait(&full[s], (c / STAGES) & 1, 1)) {
-        const Pair A{{sb + s * SM::STAGE, SM::SA, rev}, DA * SM::SA};
-        const Pair B{{sb + SM::X, SM::SA, true}, SM::SA};
-        product3(tmem, A, B, D, 64, D / 16, false);
+        const Op X{xb, SM::SA, true}, Xlo{xb + SM::SA, SM::SA, true};
+        const uint32_t m = sb + s * SM::STAGE, mlo = m + DA * SM::SA;
+        if (rev) {
+          product(tmem, Op{mlo, SM::SA, true}, X, D, 64, D / 16, false);
+          product(tmem, Op{m, SM::SA, true}, Xlo, D, 64, D / 16, true);
+          product(tmem, Op{m, SM::SA, true}, X, D, 64, D / 16, true);
+        } else {
+          product(tmem, Op{mlo, SM::SA, false}, X, D, 64, D / 16, false);
+          product(tmem, Op{m, SM::SA, false}, Xlo, D, 64, D / 16, true);
+          product(tmem, Op{m, SM::SA, false}, X, D, 64, D / 16, true);
+        }
         mma_commit(mma);
       }
-      // the same copy is chunk c's border state
+    } else if (tid == 32) {
+      if (c > 0) fetch();   // into the stage that the last chunk's product has read
+    } else if (tid == 64) {   // the same copy is chunk c's border state
       for (int h = 0; h < 2; ++h)
-        tma_store_3d(rev ? &mapXr : &mapXf, smem + SM::X + h * SM::SA, 64 * slice, 0, (int)(2 * chunk(c) + h));
+        tma_store_3d(rev ? &mapXr : &mapXf, smem + xo + h * SM::SA, 64 * slice, 0, (int)(2 * chunk(c) + h));
       bulk_commit();
     }
 #pragma unroll
@@ -508,23 +529,25 @@ __global__ void __launch_bounds__(512, 1)
       load_h(c + 1, h);
       e = a.gend[chunk(c + 1)];
     }
-    if (tid == 0) bulk_wait_read();
-    if (!ph.mma_done(2)) break;
+    ok = ph.W.wait(mma, (uint32_t)c & 1u, 2);
+    __syncwarp();
+    tc_fence_after();
     float d[16];
     tmem_ld16(tmem + lanes + cg * 16, d);
 #pragma unroll
     for (int j = 0; j < 16; ++j) x[j] += d[j];
-    if (tid == 0) fetch();   // the stage that this chunk's product has read
   }
+  __syncthreads();
   if (!ph.W.aborted() && own && dir.S_out != nullptr) {
     float* dst = dir.S_out + (bh * D + r) * D + col;
 #pragma unroll
     for (int j = 0; j < 16; j += 4)
       *reinterpret_cast<float4*>(dst + j) = make_float4(x[j], x[j + 1], x[j + 2], x[j + 3]);
   }
-  if (tid == 0) bulk_wait_all();
-  if (tid == 0 && ph.W.aborted()) {
+  if (tid == 64) bulk_wait_all();
+  if (tid == 32 && ph.W.aborted())
     for (int i = max(0, issued - STAGES); i < issued; ++i) ph.W.drain(&full[i % STAGES], (i / STAGES) & 1);
+  if (tid == 0 && ph.W.aborted()) {
     mma_commit(mma);
     ph.W.drain(mma, 0);
     ph.W.drain(mma, 1);
@@ -698,7 +721,7 @@ int chain_launch(const DeltaLaunch& p, const float* gend, const __nv_bfloat16* M
   if (rev) a.dir[1] = *rev;
   const unsigned dirs = (fwd ? 1 : 0) + (rev ? 1 : 0);
   prof_before(K_DELTA_CHAIN, stream);
-  delta_chain_kernel<D><<<dirs * (unsigned)(BH * (D / 64)), 512, ChainSmem<D>::TOTAL, stream>>>(mm, mf, mr, a);
+  delta_chain_kernel<D><<<dirs * (unsigned)(BH * (D / 64)), CHAIN_THREADS, ChainSmem<D>::TOTAL, stream>>>(mm, mf, mr, a);
   prof_after(K_DELTA_CHAIN, stream);
   return cudaGetLastError() == cudaSuccess ? 0 : -1;
 }

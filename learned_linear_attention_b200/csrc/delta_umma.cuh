@@ -136,14 +136,22 @@ struct Op {
   uint32_t addr, astride;
   bool mn;
 };
-TTT_DEVICE_INLINE uint64_t op_desc(const Op& o, int ks) {   // K step of 16
-  return o.mn ? make_sdesc(o.addr + ks * 2048, o.astride, 1024)
-              : make_sdesc(o.addr + (ks >> 2) * o.astride + (ks & 3) * 32, 16, 1024);
+TTT_DEVICE_INLINE uint64_t op_desc(const Op& o) {
+  return o.mn ? make_sdesc(o.addr, o.astride, 1024) : make_sdesc(o.addr, 16, 1024);
 }
-// D (+)= A B^T over K = 16 * steps; by one thread
+// bytes from the operand's start to K step ks of 16
+TTT_DEVICE_INLINE uint32_t op_step(const Op& o, int ks) {
+  return o.mn ? ks * 2048 : (ks >> 2) * o.astride + (ks & 3) * 32;
+}
+// D (+)= A B^T over K = 16 * steps; by one thread.  One descriptor an operand,
+// an addition a step: the issuing thread must keep ahead of the tensor core,
+// which takes 16 to 64 cycles a step.
 TTT_DEVICE_INLINE void product(uint32_t d, const Op& a, const Op& b, int M, int N, int steps, bool add) {
   const uint32_t id = make_idesc(M, N, a.mn, b.mn);
-  for (int ks = 0; ks < steps; ++ks) mma_bf16(d, op_desc(a, ks), op_desc(b, ks), id, (add || ks > 0) ? 1u : 0u);
+  const uint64_t da = op_desc(a), db = op_desc(b);
+#pragma unroll
+  for (int ks = 0; ks < steps; ++ks)
+    mma_bf16(d, sdesc_add(da, op_step(a, ks)), sdesc_add(db, op_step(b, ks)), id, (add || ks > 0) ? 1u : 0u);
 }
 // D (+)= A (lo + hi), planes of B `second` bytes apart, the last plane first
 TTT_DEVICE_INLINE void product_planes(uint32_t d, const Op& a, const Op& b, uint32_t second, int planes, int M,
@@ -154,8 +162,10 @@ TTT_DEVICE_INLINE void product_planes(uint32_t d, const Op& a, const Op& b, uint
 // The same with A in TMEM: lane = row, two bf16 of K to a column.
 TTT_DEVICE_INLINE void product_ts(uint32_t d, uint32_t a_tmem, const Op& b, int N, int steps, bool add) {
   const uint32_t id = make_idesc(128, N, false, b.mn);
+  const uint64_t db = op_desc(b);
+#pragma unroll
   for (int ks = 0; ks < steps; ++ks)
-    mma_bf16_ts(d, a_tmem + 8 * ks, op_desc(b, ks), id, (add || ks > 0) ? 1u : 0u);
+    mma_bf16_ts(d, a_tmem + 8 * ks, sdesc_add(db, op_step(b, ks)), id, (add || ks > 0) ? 1u : 0u);
 }
 // the hi + lo pair of an operand: lo is `second` bytes after hi
 struct Pair {
