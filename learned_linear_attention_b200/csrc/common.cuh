@@ -296,6 +296,20 @@ TTT_DEVICE_INLINE void mma_commit(uint64_t* bar) {
       : "memory");
 }
 
+// True in one lane of a converged warp.  Code behind it is known to be one
+// thread's, so operands that are the same in the whole warp stay in uniform
+// registers, which tcgen05.mma reads (behind a test of threadIdx they are moved
+// there one by one, about 90 cycles an instruction).
+TTT_DEVICE_INLINE bool elect_one() {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(r)::"memory");
+  return r != 0;
+}
+// The warp's index, known to be the same in all of its lanes.
+TTT_DEVICE_INLINE int warp_index() { return __shfl_sync(0xffffffffu, (int)(threadIdx.x >> 5), 0); }
+
 // Instruction descriptor, kind::f16 / kind::tf32 with fp32 accumulation.
 // bits: [4,6) D fmt (1=f32), [7,10) A fmt, [10,13) B fmt (bf16=1, tf32=2),
 // 15 A major (1 = MN), 16 B major, [17,23) N>>3, [24,29) M>>4.

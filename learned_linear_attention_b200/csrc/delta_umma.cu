@@ -182,7 +182,7 @@ __global__ void __launch_bounds__(PREP_THREADS, D == 64 ? 2 : 1)
   Gates& gates = *reinterpret_cast<Gates*>(smem + SM::GATES);
   float* gams = reinterpret_cast<float*>(smem + SM::COL);
   float* rhos = gams + C;
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int tid = threadIdx.x, warp = warp_index(), lane = tid & 31;
   const int ch = blockIdx.x % a.nch;
   const size_t bh = blockIdx.x / a.nch, ci = blockIdx.x;
   const int t0 = ch * C, n = min(C, a.N - t0);
@@ -206,8 +206,8 @@ __global__ void __launch_bounds__(PREP_THREADS, D == 64 ? 2 : 1)
   auto work = [&]() {
     if (!ph.wait(&bars.load[0], 0, 1)) return;
     const Op K{sb + SM::K, ATOM, false}, Vmn{sb + SM::V, ATOM, true};
-    if (tid == 0) {
-      product(tmem + TM_A, K, K, 128, 128, D / 16, false);
+    if (warp == 0 && elect_one()) {
+      products<D / 16>(Prod(tmem + TM_A, K, K, 128, 128, false));
       mma_commit(&bars.mma);
     }
     if (!ph.mma_done(2)) return;
@@ -283,13 +283,12 @@ __global__ void __launch_bounds__(PREP_THREADS, D == 64 ? 2 : 1)
     }
     tmem_wait_st();
     ph.publish();
-    if (tid == 0) {
+    if (warp == 0 && elect_one()) {
       const Op gK{tb, ATOM, true}, gKlo{tb + SM::OP, ATOM, true};
-      product_ts(tmem + TM_W, tmem + TM_T, gKlo, D, 8, false);
-      product_ts(tmem + TM_W, tmem + TM_T + 64, gK, D, 8, true);
-      product_ts(tmem + TM_W, tmem + TM_T, gK, D, 8, true);
-      product_ts(tmem + TM_U, tmem + TM_T + 64, Vmn, D, 8, false);
-      product_ts(tmem + TM_U, tmem + TM_T, Vmn, D, 8, true);
+      const uint32_t hi = tmem + TM_T, lo = hi + 64;
+      products<8>(Prod(tmem + TM_W, hi, gKlo, D, false), Prod(tmem + TM_U, lo, Vmn, D, false));
+      products<8>(Prod(tmem + TM_W, lo, gK, D, true), Prod(tmem + TM_U, hi, Vmn, D, true));
+      products<8>(Prod(tmem + TM_W, hi, gK, D, true));
       mma_commit(&bars.mma);
     }
     // Ut goes out in float32, W as hi + lo; rho Ut (three planes: Hc is the
@@ -331,10 +330,10 @@ __global__ void __launch_bounds__(PREP_THREADS, D == 64 ? 2 : 1)
         else out_w((cg - 2) * 32 + c, vb + ATOM, 2 * ATOM);
       }
       ph.publish();
-      if (tid == 0) {
-        product(tmem + TM_H, Kt, Op{vb + 2 * ATOM, ATOM, true}, 64, 128, 8, false);
-        product(tmem + TM_H, Kt, Op{vb + 4 * ATOM, ATOM, true}, 64, 64, 8, true);
-        product(tmem + TM_H, Kt, Op{vb, ATOM, true}, 64, 128, 8, true);
+      if (warp == 0 && elect_one()) {
+        products<8>(Prod(tmem + TM_H, Kt, Op{vb + 2 * ATOM, ATOM, true}, 64, 128, false));
+        products<8>(Prod(tmem + TM_H, Kt, Op{vb + 4 * ATOM, ATOM, true}, 64, 64, true));
+        products<8>(Prod(tmem + TM_H, Kt, Op{vb, ATOM, true}, 64, 128, true));
         mma_commit(&bars.mma);
       }
       if (!ph.mma_done(5)) return;
@@ -342,16 +341,19 @@ __global__ void __launch_bounds__(PREP_THREADS, D == 64 ? 2 : 1)
 #pragma unroll
       for (int c = 0; c < 32; c += 16) out_u(cg * 32 + c, SM::OP);
       ph.publish();
-      if (tid == 0) {
-        product_planes(tmem + TM_H, Kt, Op{vb, ATOM, true}, SM::OP, 3, 128, 128, 8, false);
+      if (warp == 0 && elect_one()) {
+        const Pair U{{vb, ATOM, true}, SM::OP};
+        for (int i = 2; i >= 0; --i) products<8>(Prod(tmem + TM_H, Kt, U.plane(i), 128, 128, i < 2));
         mma_commit(&bars.mma);
       }
       if (!ph.mma_done(5)) return;
 #pragma unroll
       for (int c = 0; c < 32; c += 16) out_w(cg * 32 + c, vb, SM::OP);
       ph.publish();
-      if (tid == 0) {
-        product_planes(tmem + TM_M, Kt, Op{vb, ATOM, true}, SM::OP, 2, 128, 128, 8, false);
+      if (warp == 0 && elect_one()) {
+        const Pair W{{vb, ATOM, true}, SM::OP};
+        products<8>(Prod(tmem + TM_M, Kt, W.lo(), 128, 128, false));
+        products<8>(Prod(tmem + TM_M, Kt, W.hi, 128, 128, true));
         mma_commit(&bars.mma);
       }
       if (!ph.mma_done(6)) return;
@@ -415,7 +417,7 @@ __global__ void __launch_bounds__(CHAIN_THREADS, 1)
   uint64_t* mma = full + STAGES;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(mma + 1);
   uint32_t* abort_flag = tmem_slot + 1;
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int tid = threadIdx.x, warp = warp_index(), lane = tid & 31;
   const int slice = blockIdx.x % DA;
   const bool rev = a.first + blockIdx.x / (DA * a.BH) == 1;
   const DeltaChain& dir = a.dir[rev ? 1 : 0];
@@ -435,7 +437,7 @@ __global__ void __launch_bounds__(CHAIN_THREADS, 1)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = *tmem_slot, sb = smem_u32(smem);
+  const uint32_t tmem = __shfl_sync(0xffffffffu, *tmem_slot, 0), sb = smem_u32(smem);
   Phase ph{Waiter{abort_flag, a.st, 1100}, mma, 0};
   const int q4 = warp & 3, cg = warp >> 2;    // 16 columns of the slice
   const int r = D == 64 ? q4 * 16 + lane : q4 * 32 + lane;
@@ -495,22 +497,17 @@ __global__ void __launch_bounds__(CHAIN_THREADS, 1)
     if (tid == 64) bulk_wait_read();   // behind this barrier the other copy may be written again
     if (!named_bar_all(1, CHAIN_THREADS, ok)) break;
     tc_fence_after();
-    if (tid == 0) {
+    if (warp == 0) {
       const int s = c % STAGES;
-      if (ph.W.wait(&full[s], (c / STAGES) & 1, 1)) {
+      if (ph.W.wait(&full[s], (c / STAGES) & 1, 1) && elect_one()) {
         const Op X{xb, SM::SA, true}, Xlo{xb + SM::SA, SM::SA, true};
         const uint32_t m = sb + s * SM::STAGE, mlo = m + DA * SM::SA;
-        if (rev) {
-          product(tmem, Op{mlo, SM::SA, true}, X, D, 64, D / 16, false);
-          product(tmem, Op{m, SM::SA, true}, Xlo, D, 64, D / 16, true);
-          product(tmem, Op{m, SM::SA, true}, X, D, 64, D / 16, true);
-        } else {
-          product(tmem, Op{mlo, SM::SA, false}, X, D, 64, D / 16, false);
-          product(tmem, Op{m, SM::SA, false}, Xlo, D, 64, D / 16, true);
-          product(tmem, Op{m, SM::SA, false}, X, D, 64, D / 16, true);
-        }
+        products<D / 16>(Prod(tmem, Op{mlo, SM::SA, rev}, X, D, 64, false));
+        products<D / 16>(Prod(tmem, Op{m, SM::SA, rev}, Xlo, D, 64, true));
+        products<D / 16>(Prod(tmem, Op{m, SM::SA, rev}, X, D, 64, true));
         mma_commit(mma);
       }
+      __syncwarp();
     } else if (tid == 32) {
       if (c > 0) fetch();   // into the stage that the last chunk's product has read
     } else if (tid == 64) {   // the same copy is chunk c's border state
@@ -595,7 +592,7 @@ __global__ void __launch_bounds__(OUT_THREADS, D == 64 ? 2 : 1)
   extern __shared__ __align__(1024) uint8_t smem[];
   Bars& bars = *reinterpret_cast<Bars*>(smem + SM::BAR);
   Gates& gates = *reinterpret_cast<Gates*>(smem + SM::GATES);
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int tid = threadIdx.x, warp = warp_index(), lane = tid & 31;
   const int slice = blockIdx.x % DA;
   const size_t ci = blockIdx.x / DA, bh = ci / a.nch;
   const int t0 = (int)(ci % a.nch) * C, n = min(C, a.N - t0);
@@ -625,10 +622,11 @@ __global__ void __launch_bounds__(OUT_THREADS, D == 64 ? 2 : 1)
     if (!ph.wait(&bars.load[0], 0, 1)) return;
     const Op Q{sb + SM::Q, ATOM, false}, K{sb + SM::K, ATOM, false};
     const Pair Wp{{sb + SM::W, ATOM, false}, SM::OP}, S{{sb + SM::S, SM::SA, true}, SM::SA};
-    if (tid == 0) {
-      product(tmem + TM_P, Q, K, 128, 128, D / 16, false);
-      product3(tmem + TM_W, Wp, S, 128, 64, D / 16, false);
-      product_planes(tmem + TM_Q, Q, S.hi, SM::SA, 2, 128, 64, D / 16, false);
+    if (warp == 0 && elect_one()) {
+      products<D / 16>(Prod(tmem + TM_W, Wp.lo(), S.hi, 128, 64, false), Prod(tmem + TM_P, Q, K, 128, 128, false),
+                       Prod(tmem + TM_Q, Q, S.lo(), 128, 64, false));
+      products<D / 16>(Prod(tmem + TM_W, Wp.hi, S.lo(), 128, 64, true), Prod(tmem + TM_Q, Q, S.hi, 128, 64, true));
+      products<D / 16>(Prod(tmem + TM_W, Wp.hi, S.hi, 128, 64, true));
       mma_commit(&bars.mma);
     }
     if (!ph.mma_done(2)) return;
@@ -658,9 +656,11 @@ __global__ void __launch_bounds__(OUT_THREADS, D == 64 ? 2 : 1)
       store8_split(hi, hi + 2 * ATOM, row, (c0 & 63) + 8, x + 8);
     }
     ph.publish();
-    if (tid == 0) {
+    if (warp == 0 && elect_one()) {
       const Pair P{{sb + SM::P, ATOM, false}, 2 * ATOM}, U{{sb + SM::U, ATOM, true}, ATOM};
-      product3(tmem + TM_W, P, U, 128, 64, 8, false);
+      products<8>(Prod(tmem + TM_W, P.lo(), U.hi, 128, 64, false));
+      products<8>(Prod(tmem + TM_W, P.hi, U.lo(), 128, 64, true));
+      products<8>(Prod(tmem + TM_W, P.hi, U.hi, 128, 64, true));
       mma_commit(&bars.mma);
     }
     if (!ph.mma_done(3)) return;

@@ -128,60 +128,6 @@ TTT_DEVICE_INLINE void load8_split(uint32_t hi_atom, uint32_t lo_atom, int row, 
   for (int i = 0; i < 8; ++i) x[i] += l[i];
 }
 
-// ----------------------------------------------------------------- products
-// Operands by shared address: K-major (rows are the M or N index, the 64
-// columns of an atom are K; further atoms of K `astride` bytes on) or MN-major
-// (rows are K, the columns M or N; further atoms of M or N `astride` on).
-struct Op {
-  uint32_t addr, astride;
-  bool mn;
-};
-TTT_DEVICE_INLINE uint64_t op_desc(const Op& o) {
-  return o.mn ? make_sdesc(o.addr, o.astride, 1024) : make_sdesc(o.addr, 16, 1024);
-}
-// bytes from the operand's start to K step ks of 16
-TTT_DEVICE_INLINE uint32_t op_step(const Op& o, int ks) {
-  return o.mn ? ks * 2048 : (ks >> 2) * o.astride + (ks & 3) * 32;
-}
-// D (+)= A B^T over K = 16 * steps; by one thread.  One descriptor an operand,
-// an addition a step: the issuing thread must keep ahead of the tensor core,
-// which takes 16 to 64 cycles a step.
-TTT_DEVICE_INLINE void product(uint32_t d, const Op& a, const Op& b, int M, int N, int steps, bool add) {
-  const uint32_t id = make_idesc(M, N, a.mn, b.mn);
-  const uint64_t da = op_desc(a), db = op_desc(b);
-#pragma unroll
-  for (int ks = 0; ks < steps; ++ks)
-    mma_bf16(d, sdesc_add(da, op_step(a, ks)), sdesc_add(db, op_step(b, ks)), id, (add || ks > 0) ? 1u : 0u);
-}
-// D (+)= A (lo + hi), planes of B `second` bytes apart, the last plane first
-TTT_DEVICE_INLINE void product_planes(uint32_t d, const Op& a, const Op& b, uint32_t second, int planes, int M,
-                                      int N, int steps, bool add) {
-  for (int i = planes - 1; i >= 0; --i)
-    product(d, a, Op{b.addr + i * second, b.astride, b.mn}, M, N, steps, add || i < planes - 1);
-}
-// The same with A in TMEM: lane = row, two bf16 of K to a column.
-TTT_DEVICE_INLINE void product_ts(uint32_t d, uint32_t a_tmem, const Op& b, int N, int steps, bool add) {
-  const uint32_t id = make_idesc(128, N, false, b.mn);
-  const uint64_t db = op_desc(b);
-#pragma unroll
-  for (int ks = 0; ks < steps; ++ks)
-    mma_bf16_ts(d, a_tmem + 8 * ks, sdesc_add(db, op_step(b, ks)), id, (add || ks > 0) ? 1u : 0u);
-}
-// the hi + lo pair of an operand: lo is `second` bytes after hi
-struct Pair {
-  Op hi;
-  uint32_t second;
-  TTT_DEVICE_INLINE Op lo() const { return Op{hi.addr + second, hi.astride, hi.mn}; }
-};
-// lo hi + hi lo + hi hi (lo lo is below 2^-17 of the product twice over).  The
-// tensor core truncates its running sum, so small terms go first: only the
-// last 8 or so additions round at the size of the result.
-TTT_DEVICE_INLINE void product3(uint32_t d, const Pair& a, const Pair& b, int M, int N, int steps, bool add) {
-  product(d, a.lo(), b.hi, M, N, steps, add);
-  product(d, a.hi, b.lo(), M, N, steps, true);
-  product(d, a.hi, b.hi, M, N, steps, true);
-}
-
 // three planes: what is left of 24 bits after hi and lo
 TTT_DEVICE_INLINE void store8_split3(uint32_t hi_atom, uint32_t lo_atom, uint32_t rest_atom, int row, int col,
                                      const float* x) {
@@ -213,6 +159,57 @@ TTT_DEVICE_INLINE void store16_pair(__nv_bfloat16* hi, __nv_bfloat16* lo, const 
   st_global_v8(hi, h);
   st_global_v8(lo, l);
 }
+
+// ----------------------------------------------------------------- products
+// Operands by shared address: K-major (rows are the M or N index, the 64
+// columns of an atom are K; further atoms of K `astride` bytes on) or MN-major
+// (rows are K, the columns M or N; further atoms of M or N `astride` on).
+struct Op {
+  uint32_t addr, astride;
+  bool mn;
+};
+TTT_DEVICE_INLINE uint64_t op_desc(const Op& o) {
+  return o.mn ? make_sdesc(o.addr, o.astride, 1024) : make_sdesc(o.addr, 16, 1024);
+}
+// D (+)= A B^T over K, 16 at a step, by one elected thread (see elect_one): one
+// descriptor an operand, an addition a step.  A step of M = 128, N = 64 takes
+// about 50 cycles, what its 6 KB of operands take to leave shared memory.
+// products() takes a step of each of several products in turn.  The tensor core
+// truncates its running sum, so small terms go first.
+struct Prod {
+  uint32_t d, id, a_stride, b_stride, ta;
+  uint64_t da, db;
+  bool add, a_mn, b_mn, ts;
+  TTT_DEVICE_INLINE Prod(uint32_t d_, const Op& a, const Op& b, int M, int N, bool add_)
+      : d(d_), id(make_idesc(M, N, a.mn, b.mn)), a_stride(a.astride), b_stride(b.astride), ta(0),
+        da(op_desc(a)), db(op_desc(b)), add(add_), a_mn(a.mn), b_mn(b.mn), ts(false) {}
+  // A in TMEM: lane = row, two bf16 of K to a column
+  TTT_DEVICE_INLINE Prod(uint32_t d_, uint32_t a_tmem, const Op& b, int N, bool add_)
+      : d(d_), id(make_idesc(128, N, false, b.mn)), a_stride(0), b_stride(b.astride), ta(a_tmem), da(0),
+        db(op_desc(b)), add(add_), a_mn(false), b_mn(b.mn), ts(true) {}
+  TTT_DEVICE_INLINE static uint32_t at(bool mn, uint32_t stride, int ks) {   // bytes to K step ks
+    return mn ? ks * 2048 : (ks >> 2) * stride + (ks & 3) * 32;
+  }
+  TTT_DEVICE_INLINE void step(int ks) const {
+    const uint32_t acc = add || ks > 0;
+    const uint64_t b = sdesc_add(db, at(b_mn, b_stride, ks));
+    if (ts) mma_bf16_ts(d, ta + 8 * ks, b, id, acc);
+    else mma_bf16(d, sdesc_add(da, at(a_mn, a_stride, ks)), b, id, acc);
+  }
+};
+template <int STEPS, typename... P>
+TTT_DEVICE_INLINE void products(const P&... p) {
+#pragma unroll
+  for (int ks = 0; ks < STEPS; ++ks) (p.step(ks), ...);
+}
+// The hi + lo pair of an operand: lo is `second` bytes after hi.  A product of
+// two pairs is lo hi + hi lo + hi hi (lo lo is below 2^-17 of it twice over).
+struct Pair {
+  Op hi;
+  uint32_t second;
+  TTT_DEVICE_INLINE Op lo() const { return plane(1); }
+  TTT_DEVICE_INLINE Op plane(int i) const { return Op{hi.addr + i * second, hi.astride, hi.mn}; }
+};
 
 // ----------------------------------------------------------------- float32 tiles in global memory
 // [rows][D] in 64-column slices, columns in groups of four: a row's 16 columns
@@ -284,7 +281,7 @@ TTT_DEVICE_INLINE uint32_t cta_begin(Bars& b, uint32_t cols, int tid) {
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  return b.tmem;
+  return __shfl_sync(0xffffffffu, b.tmem, 0);
 }
 // After the last phase, or an aborted one: nothing in flight outlives the CTA.
 // `loads` counts the load barriers in use (thread 0's).

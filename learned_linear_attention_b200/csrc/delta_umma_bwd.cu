@@ -94,7 +94,7 @@ __global__ void __launch_bounds__(THREADS, 1)
   extern __shared__ __align__(1024) uint8_t smem[];
   Bars& bars = *reinterpret_cast<Bars*>(smem + SM::BAR);
   Gates& gates = *reinterpret_cast<Gates*>(smem + SM::GATES);
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int tid = threadIdx.x, warp = warp_index(), lane = tid & 31;
   const ChunkId id(DA, a.nch, a.N);
   const uint32_t tmem = cta_begin(bars, TM_COLS, tid), sb = smem_u32(smem);
   Phase ph{Waiter{&bars.abort, a.st, 1300}, &bars.mma, 0};
@@ -114,8 +114,8 @@ __global__ void __launch_bounds__(THREADS, 1)
   auto work = [&]() {
     if (!ph.wait(&bars.load[0], 0, 1)) return;
     const Op dOmn{sb + SM::DO, ATOM, true}, Qmn{sb + SM::Q, ATOM, true};
-    if (tid == 0) {
-      product(tmem + TM_P, Op{sb + SM::Q, ATOM, false}, Op{sb + SM::P, ATOM, false}, 128, 128, D / 16, false);
+    if (warp == 0 && elect_one()) {
+      products<D / 16>(Prod(tmem + TM_P, Op{sb + SM::Q, ATOM, false}, Op{sb + SM::P, ATOM, false}, 128, 128, false));
       mma_commit(&bars.mma);
     }
     if (!ph.mma_done(2)) return;
@@ -135,9 +135,9 @@ __global__ void __launch_bounds__(THREADS, 1)
         store8_split3(at, at + 2 * ATOM, at + 4 * ATOM, row, (c0 & 63) + i, x + i);
     }
     ph.publish();
-    if (tid == 0) {
-      for (int i = 2; i >= 0; --i)
-        product(tmem + TM_U, Op{sb + SM::P + 2 * i * ATOM, ATOM, true}, dOmn, 128, 64, 8, i < 2);
+    if (warp == 0 && elect_one()) {
+      const Pair Pt{{sb + SM::P, ATOM, true}, 2 * ATOM};
+      for (int i = 2; i >= 0; --i) products<8>(Prod(tmem + TM_U, Pt.plane(i), dOmn, 128, 64, i < 2));
       mma_commit(&bars.mma);
     }
     if (!ph.mma_done(3)) return;
@@ -160,15 +160,21 @@ __global__ void __launch_bounds__(THREADS, 1)
       }
     }
     ph.publish();
-    if (tid == 0) {
-      auto plane = [&](int i) { return Op{sb + SM::P + i * ATOM, ATOM, true}; };
+    if (warp == 0 && elect_one()) {
+      const Pair U{{sb + SM::P, ATOM, true}, ATOM}, G{{sb + SM::P + 3 * ATOM, ATOM, true}, ATOM};
       const Pair Wt{{sb + SM::W, ATOM, true}, DA * ATOM};
-      // small terms first (see product3)
-      for (int i = 2; i >= 1; --i) product(tmem + TM_H, Qmn, plane(3 + i), D, 64, 8, i < 2);
-      for (int i = 1; i >= 0; --i) product(tmem + TM_H, Wt.lo(), plane(i), D, 64, 8, true);
-      for (int i = 2; i >= 0; --i) product(tmem + TM_H, Wt.hi, plane(i), D, 64, 8, true);
-      product(tmem + TM_H, Qmn, plane(3), D, 64, 8, true);
+      const uint32_t t = tmem + TM_H;   // small terms first
+      products<8>(Prod(t, Qmn, G.plane(2), D, 64, false));
+      products<8>(Prod(t, Wt.lo(), U.lo(), D, 64, true));
+      products<8>(Prod(t, Wt.hi, U.plane(2), D, 64, true));
+      products<8>(Prod(t, Qmn, G.lo(), D, 64, true));
+      products<8>(Prod(t, Wt.lo(), U.hi, D, 64, true));
+      products<8>(Prod(t, Wt.hi, U.lo(), D, 64, true));
+      products<8>(Prod(t, Wt.hi, U.hi, D, 64, true));
+      products<8>(Prod(t, Qmn, G.hi, D, 64, true));
       mma_commit(&bars.mma);
+    }
+    if (tid == 0) {
       for (int h = 0; h < 2; ++h)
         tma_store_3d(&mapY, smem + SM::P + h * ATOM, 64 * id.slice, 0, (int)(2 * id.ci + h));
       bulk_commit();
@@ -217,7 +223,7 @@ __global__ void __launch_bounds__(THREADS, 1)
   Bars& bars = *reinterpret_cast<Bars*>(smem + SM::BAR);
   Gates& gates = *reinterpret_cast<Gates*>(smem + SM::GATES);
   float* red = reinterpret_cast<float*>(smem + SM::RED);
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int tid = threadIdx.x, warp = warp_index(), lane = tid & 31;
   const ChunkId id(DA, a.nch, a.N);
   const uint32_t tmem = cta_begin(bars, TM_COLS, tid), sb = smem_u32(smem);
   Phase ph{Waiter{&bars.abort, a.st, 1400}, &bars.mma, 0};
@@ -244,10 +250,12 @@ __global__ void __launch_bounds__(THREADS, 1)
     const Op K{sb + SM::K, ATOM, false};
     const Pair W{{sb + SM::T, ATOM, false}, DA * ATOM};
     const Pair S{{sb + SM::S, SM::SA, true}, SM::SA}, X{{sb + SM::X, SM::SA, true}, SM::SA};
-    if (tid == 0) {
-      product3(tmem + TM_W, W, S, 128, 64, D / 16, false);
-      product_planes(tmem + TM_Z, K, S.hi, S.second, 2, 128, 64, D / 16, false);
-      product_planes(tmem + TM_X, K, X.hi, X.second, 2, 128, 64, D / 16, false);
+    if (warp == 0 && elect_one()) {
+      products<D / 16>(Prod(tmem + TM_W, W.lo(), S.hi, 128, 64, false), Prod(tmem + TM_Z, K, S.lo(), 128, 64, false),
+                       Prod(tmem + TM_X, K, X.lo(), 128, 64, false));
+      products<D / 16>(Prod(tmem + TM_W, W.hi, S.lo(), 128, 64, true), Prod(tmem + TM_Z, K, S.hi, 128, 64, true),
+                       Prod(tmem + TM_X, K, X.hi, 128, 64, true));
+      products<D / 16>(Prod(tmem + TM_W, W.hi, S.hi, 128, 64, true));
       mma_commit(&bars.mma);
     }
     if (!ph.mma_done(2)) return;
@@ -284,11 +292,13 @@ __global__ void __launch_bounds__(THREADS, 1)
       for (int h = 0; h < 2; ++h)
         tma_store_3d(&mapU, smem + SM::U + h * ATOM, 64 * id.slice, 0, (int)(2 * id.ci + h));
       bulk_commit();
-      if (ph.W.wait(&bars.load[1], 0, 3)) {
-        const Pair Tt{{sb + SM::T, ATOM, true}, 2 * ATOM}, dU{{sb + SM::Y, ATOM, true}, ATOM};
-        product3(tmem + TM_Y, Tt, dU, 128, 64, 8, false);
-        mma_commit(&bars.mma);
-      }
+    }
+    if (warp == 0 && ph.W.wait(&bars.load[1], 0, 3) && elect_one()) {
+      const Pair Tt{{sb + SM::T, ATOM, true}, 2 * ATOM}, dU{{sb + SM::Y, ATOM, true}, ATOM};
+      products<8>(Prod(tmem + TM_Y, Tt.lo(), dU.hi, 128, 64, false));
+      products<8>(Prod(tmem + TM_Y, Tt.hi, dU.lo(), 128, 64, true));
+      products<8>(Prod(tmem + TM_Y, Tt.hi, dU.hi, 128, 64, true));
+      mma_commit(&bars.mma);
     }
     if (!ph.mma_done(4)) return;
     {
@@ -370,7 +380,7 @@ __global__ void __launch_bounds__(THREADS, 1)
   Bars& bars = *reinterpret_cast<Bars*>(smem + SM::BAR);
   Gates& gates = *reinterpret_cast<Gates*>(smem + SM::GATES);
   float *red = reinterpret_cast<float*>(smem + SM::RED), *xs = reinterpret_cast<float*>(smem + SM::XS);
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int tid = threadIdx.x, warp = warp_index(), lane = tid & 31;
   const ChunkId id(DA, a.nch, a.N);
   const uint32_t tmem = cta_begin(bars, TM_COLS, tid), sb = smem_u32(smem);
   Phase ph{Waiter{&bars.abort, a.st, 1500}, &bars.mma, 0};
@@ -393,15 +403,19 @@ __global__ void __launch_bounds__(THREADS, 1)
   int loads = 1;
   auto work = [&]() {
     if (!ph.wait(&bars.load[0], 0, 1)) return;
-    if (tid == 0) {
+    if (warp == 0 && elect_one()) {
       const Op dO{sb + SM::DO, ATOM, false};
       const Pair U{{sb + SM::U, ATOM, false}, DA * ATOM}, Y{{sb + SM::Y, ATOM, false}, DA * ATOM};
       const Pair S{{sb + SM::S, SM::HA, false}, DA * SM::HA}, X{{sb + SM::X, SM::HA, false}, DA * SM::HA};
-      product_planes(tmem + TM_P, dO, U.hi, U.second, 2, 128, 128, D / 16, false);
-      product3(tmem + TM_A, Y, U, 128, 128, D / 16, false);
-      product_planes(tmem + TM_QS, dO, S.hi, S.second, 2, 128, 64, D / 16, false);
-      product3(tmem + TM_YS, Y, S, 128, 64, D / 16, false);
-      product3(tmem + TM_UX, U, X, 128, 64, D / 16, false);
+      auto prod = [&](uint32_t d, const Op& x, const Op& y, int N, bool add) { return Prod(tmem + d, x, y, 128, N, add); };
+      products<D / 16>(prod(TM_A, Y.lo(), U.hi, 128, false), prod(TM_YS, Y.lo(), S.hi, 64, false),
+                       prod(TM_UX, U.lo(), X.hi, 64, false), prod(TM_P, dO, U.lo(), 128, false),
+                       prod(TM_QS, dO, S.lo(), 64, false));
+      products<D / 16>(prod(TM_A, Y.hi, U.lo(), 128, true), prod(TM_YS, Y.hi, S.lo(), 64, true),
+                       prod(TM_UX, U.hi, X.lo(), 64, true), prod(TM_P, dO, U.hi, 128, true),
+                       prod(TM_QS, dO, S.hi, 64, true));
+      products<D / 16>(prod(TM_A, Y.hi, U.hi, 128, true), prod(TM_YS, Y.hi, S.hi, 64, true),
+                       prod(TM_UX, U.hi, X.hi, 64, true));
       mma_commit(&bars.mma);
     }
     {   // <X1, S0> of this slice's rows, while they are still here
@@ -443,11 +457,9 @@ __global__ void __launch_bounds__(THREADS, 1)
     }
     ph.publish();
     const Op K{sb + SM::Y, ATOM, false};
-    if (tid == 0) {
-      if (ph.W.wait(&bars.load[1], 0, 3)) {
-        product(tmem + TM_P, K, K, 128, 128, D / 16, false);
-        mma_commit(&bars.mma);
-      }
+    if (warp == 0 && ph.W.wait(&bars.load[1], 0, 3) && elect_one()) {
+      products<D / 16>(Prod(tmem + TM_P, K, K, 128, 128, false));
+      mma_commit(&bars.mma);
     }
     if (!ph.mma_done(4)) return;
     // Mk, and its row sums against k_i . k_j without beta
@@ -475,17 +487,15 @@ __global__ void __launch_bounds__(THREADS, 1)
     red[cg * C + row] = db;
     ph.publish();
     const Op Kmn{sb + SM::Y + id.slice * ATOM, ATOM, true}, Qmn{sb + SM::Y + DA * ATOM, ATOM, true};
-    if (tid == 0) {
+    if (warp == 0 && elect_one()) {
       const Pair Mq{{sb + SM::MQ, ATOM, false}, 2 * ATOM}, Mk{{sb + SM::U, ATOM, false}, 2 * ATOM};
       const Pair Mqt{{sb + SM::MQ, ATOM, true}, 2 * ATOM}, Mkt{{sb + SM::U, ATOM, true}, 2 * ATOM};
-      product(tmem + TM_QK, Mq.lo(), Kmn, 128, 64, 8, false);
-      product(tmem + TM_QK, Mq.hi, Kmn, 128, 64, 8, true);
-      product(tmem + TM_KR, Mk.lo(), Kmn, 128, 64, 8, false);
-      product(tmem + TM_KR, Mk.hi, Kmn, 128, 64, 8, true);
-      product(tmem + TM_KW, Mqt.lo(), Qmn, 128, 64, 8, false);
-      product(tmem + TM_KW, Mqt.hi, Qmn, 128, 64, 8, true);
-      product(tmem + TM_KW, Mkt.lo(), Kmn, 128, 64, 8, true);
-      product(tmem + TM_KW, Mkt.hi, Kmn, 128, 64, 8, true);
+      products<8>(Prod(tmem + TM_QK, Mq.lo(), Kmn, 128, 64, false), Prod(tmem + TM_KR, Mk.lo(), Kmn, 128, 64, false),
+                  Prod(tmem + TM_KW, Mqt.lo(), Qmn, 128, 64, false));
+      products<8>(Prod(tmem + TM_KW, Mkt.lo(), Kmn, 128, 64, true));
+      products<8>(Prod(tmem + TM_QK, Mq.hi, Kmn, 128, 64, true), Prod(tmem + TM_KR, Mk.hi, Kmn, 128, 64, true),
+                  Prod(tmem + TM_KW, Mqt.hi, Qmn, 128, 64, true));
+      products<8>(Prod(tmem + TM_KW, Mkt.hi, Kmn, 128, 64, true));
       mma_commit(&bars.mma);
     }
     if (cg == 0 && id.slice == 0 && row < id.n) a.bkey[id.tok + row] = row_total(red, row);

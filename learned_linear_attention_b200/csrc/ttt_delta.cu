@@ -28,7 +28,6 @@ constexpr int L = 8;            // lanes of one column
 constexpr int COLS = 16;        // columns of a CTA
 constexpr int THREADS = L * COLS;
 constexpr int TT = 32;          // tokens staged at a time, and between kept states
-constexpr int NB = TT / 4;      // blocks of four tokens
 constexpr int DMAX = 128;
 
 TTT_DEVICE_INLINE float to_f(float x) { return x; }
