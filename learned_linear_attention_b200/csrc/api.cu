@@ -298,7 +298,7 @@ static DeltaLaunch delta_launch(const ttt_delta_desc* d, const void* q, const vo
                                 const void* v, const void* g, const void* beta, float* S,
                                 void* out, void* ws) {
   DeltaLaunch L{};
-  L.B = d->B; L.H = d->H; L.N = d->N; L.dk = d->dk; L.dv = d->dv;
+  L.B = d->B; L.H = d->H; L.N = d->N; L.dk = d->dk; L.dv = d->dv; L.sms = device_sms();
   L.scale = d->scale > 0.f ? d->scale : 1.f / sqrtf((float)d->dk);
   L.in_bf16 = d->in_dtype == TTT_BF16;
   L.out_bf16 = d->out_dtype == TTT_BF16;

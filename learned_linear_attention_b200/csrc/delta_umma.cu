@@ -151,7 +151,7 @@ struct PrepArgs {
   __nv_bfloat16* W;        // [BH nch][2][128][D] hi, lo
   __nv_bfloat16* M;        // [BH nch][2][D][D] hi, lo
   __nv_bfloat16* T;        // nullable: [BH nch][2][128][128] hi, lo
-  int N, nch;
+  int N, nch, ahead;
   DevStatus st;
 };
 
@@ -183,24 +183,28 @@ __global__ void __launch_bounds__(PREP_THREADS, D == 64 ? 2 : 1)
   float* gams = reinterpret_cast<float*>(smem + SM::COL);
   float* rhos = gams + C;
   const int tid = threadIdx.x, warp = warp_index(), lane = tid & 31;
-  const int ch = blockIdx.x % a.nch;
-  const size_t bh = blockIdx.x / a.nch, ci = blockIdx.x;
-  const int t0 = ch * C, n = min(C, a.N - t0);
-  const uint32_t tmem = cta_begin(bars, TM_COLS, tid), sb = smem_u32(smem);
+  const ChunkId id(blockIdx.x, 1, a.nch, a.N);
+  const size_t ci = id.ci;
+  const uint32_t sb = smem_u32(smem);
+  const uint32_t tmem = cta_begin(bars, TM_COLS, tid, [&]() {
+    mbar_arrive_expect_tx(&bars.load[0], 2 * SM::OP);
+    for (int i = 0; i < DA; ++i) {
+      tma_load_3d(smem + SM::K + i * ATOM, &mapK, &bars.load[0], 64 * i, id.t0, (int)id.bh);
+      tma_load_3d(smem + SM::V + i * ATOM, &mapV, &bars.load[0], 64 * i, id.t0, (int)id.bh);
+    }
+  });
   Phase ph{Waiter{&bars.abort, a.st, 1000}, &bars.mma, 0};
   const int q4 = warp & 3, cg = warp >> 2, row = q4 * 32 + lane;
   const uint32_t lanes = (uint32_t)(q4 * 32) << 16;
 
-  if (tid == 0) {
-    mbar_arrive_expect_tx(&bars.load[0], 2 * SM::OP);
+  prefetch_next(a.ahead, 1, a.nch, a.N, [&](const ChunkId& next) {
     for (int i = 0; i < DA; ++i) {
-      tma_load_3d(smem + SM::K + i * ATOM, &mapK, &bars.load[0], 64 * i, t0, (int)bh);
-      tma_load_3d(smem + SM::V + i * ATOM, &mapV, &bars.load[0], 64 * i, t0, (int)bh);
+      tma_prefetch_3d(&mapK, 64 * i, next.t0, (int)next.bh);
+      tma_prefetch_3d(&mapV, 64 * i, next.t0, (int)next.bh);
     }
-  }
+  });
   if (cg == 1) {
-    const size_t tok = bh * a.N + t0;
-    load_gates(gates, a.g ? a.g + tok : nullptr, a.beta + tok, n, row, gams[row], rhos[row]);
+    load_gates(gates, a.g ? a.g + id.tok : nullptr, a.beta + id.tok, id.n, row, gams[row], rhos[row]);
     if (row == C - 1) a.gend[ci] = gams[row];
   }
   auto work = [&]() {
@@ -563,7 +567,7 @@ struct OutArgs {
   const __nv_bfloat16 *g, *beta;
   const float* U;
   void* out;
-  int N, nch, out_bf16;
+  int N, nch, ahead, out_bf16;
   float scale;
   DevStatus st;
 };
@@ -593,27 +597,35 @@ __global__ void __launch_bounds__(OUT_THREADS, D == 64 ? 2 : 1)
   Bars& bars = *reinterpret_cast<Bars*>(smem + SM::BAR);
   Gates& gates = *reinterpret_cast<Gates*>(smem + SM::GATES);
   const int tid = threadIdx.x, warp = warp_index(), lane = tid & 31;
-  const int slice = blockIdx.x % DA;
-  const size_t ci = blockIdx.x / DA, bh = ci / a.nch;
-  const int t0 = (int)(ci % a.nch) * C, n = min(C, a.N - t0);
-  const uint32_t tmem = cta_begin(bars, TM_COLS, tid), sb = smem_u32(smem);
-  Phase ph{Waiter{&bars.abort, a.st, 1200}, &bars.mma, 0};
-  const int q4 = warp & 3, cg = warp >> 2, row = q4 * 32 + lane;
-  const uint32_t lanes = (uint32_t)(q4 * 32) << 16;
-  if (tid == 0) {
+  const ChunkId id(blockIdx.x, DA, a.nch, a.N);
+  const int slice = id.slice;
+  const size_t ci = id.ci;
+  const uint32_t sb = smem_u32(smem);
+  const uint32_t tmem = cta_begin(bars, TM_COLS, tid, [&]() {
     mbar_arrive_expect_tx(&bars.load[0], 4 * SM::OP + 2 * SM::SA);
     for (int i = 0; i < DA; ++i) {
-      tma_load_3d(smem + SM::Q + i * ATOM, &mapQ, &bars.load[0], 64 * i, t0, (int)bh);
-      tma_load_3d(smem + SM::K + i * ATOM, &mapK, &bars.load[0], 64 * i, t0, (int)bh);
+      tma_load_3d(smem + SM::Q + i * ATOM, &mapQ, &bars.load[0], 64 * i, id.t0, (int)id.bh);
+      tma_load_3d(smem + SM::K + i * ATOM, &mapK, &bars.load[0], 64 * i, id.t0, (int)id.bh);
       for (int h = 0; h < 2; ++h)
         tma_load_3d(smem + SM::W + (h * DA + i) * ATOM, &mapW, &bars.load[0], 64 * i, 0, (int)(2 * ci + h));
     }
     for (int h = 0; h < 2; ++h)
       tma_load_3d(smem + SM::S + h * SM::SA, &mapS, &bars.load[0], 64 * slice, 0, (int)(2 * ci + h));
-  }
+  });
+  Phase ph{Waiter{&bars.abort, a.st, 1200}, &bars.mma, 0};
+  const int q4 = warp & 3, cg = warp >> 2, row = q4 * 32 + lane;
+  const uint32_t lanes = (uint32_t)(q4 * 32) << 16;
+  prefetch_next(a.ahead, DA, a.nch, a.N, [&](const ChunkId& next) {
+    for (int i = 0; i < DA; ++i) {
+      tma_prefetch_3d(&mapQ, 64 * i, next.t0, (int)next.bh);
+      tma_prefetch_3d(&mapK, 64 * i, next.t0, (int)next.bh);
+      for (int h = 0; h < 2; ++h) tma_prefetch_3d(&mapW, 64 * i, 0, (int)(2 * next.ci + h));
+    }
+    for (int h = 0; h < 2; ++h) tma_prefetch_3d(&mapS, 64 * next.slice, 0, (int)(2 * next.ci + h));
+    bulk_prefetch(a.U + next.ci * C * D + next.slice * 64 * C, 64 * C * 4);
+  });
   if (cg == 1) {
-    const size_t tok = bh * a.N + t0;
-    load_gates(gates, a.g ? a.g + tok : nullptr, a.beta + tok, n, row);
+    load_gates(gates, a.g ? a.g + id.tok : nullptr, a.beta + id.tok, id.n, row);
   }
   // this thread's 16 values of Ut, while the operands travel
   float u[16];
@@ -668,10 +680,10 @@ __global__ void __launch_bounds__(OUT_THREADS, D == 64 ? 2 : 1)
     float o[16], qs[16];
     tmem_ld16(tmem + lanes + TM_W + cg * 16, o);
     tmem_ld16(tmem + lanes + TM_Q + cg * 16, qs);
-    if (row >= n) return;
+    if (row >= id.n) return;
 #pragma unroll
     for (int i = 0; i < 16; ++i) o[i] = fmaf(gam, qs[i], a.scale * o[i]);
-    const size_t at = (bh * a.N + t0 + row) * D + slice * 64 + cg * 16;
+    const size_t at = (id.tok + row) * D + slice * 64 + cg * 16;
     if (a.out_bf16) {
       store_bf16_row16(static_cast<__nv_bfloat16*>(a.out) + at, o);
     } else {
@@ -697,7 +709,7 @@ int prep_launch(const DeltaLaunch& p, const DeltaPrepOut& o, cudaStream_t stream
   static std::atomic<uint64_t> attr{0};
   if (allow_dynamic_smem(delta_prep_kernel<D>, (int)PrepSmem<D>::TOTAL, attr)) return -1;
   const PrepArgs a{(const __nv_bfloat16*)p.g, (const __nv_bfloat16*)p.beta, o.gend, o.H, o.U, o.W, o.M, o.T,
-                   p.N, nch, p.st};
+                   p.N, nch, p.sms * (D == 64 ? 2 : 1), p.st};
   prof_before(K_DELTA_PREP, stream);
   delta_prep_kernel<D><<<(unsigned)nc, PREP_THREADS, PrepSmem<D>::TOTAL, stream>>>(mk, mv, a);
   prof_after(K_DELTA_PREP, stream);
@@ -745,7 +757,8 @@ int fwd_launch(const DeltaLaunch& p, cudaStream_t stream) {
     return -1;
   static std::atomic<uint64_t> attr{0};
   if (allow_dynamic_smem(delta_out_kernel<D>, (int)OutSmem<D>::TOTAL, attr)) return -1;
-  const OutArgs a{(const __nv_bfloat16*)p.g, (const __nv_bfloat16*)p.beta, o.U, p.out, p.N, nch, p.out_bf16, p.scale, p.st};
+  const OutArgs a{(const __nv_bfloat16*)p.g, (const __nv_bfloat16*)p.beta, o.U, p.out, p.N, nch,
+                  p.sms * (D == 64 ? 2 : 1), p.out_bf16, p.scale, p.st};
   prof_before(K_DELTA_OUT, stream);
   delta_out_kernel<D><<<(unsigned)(nc * (D / 64)), OUT_THREADS, OutSmem<D>::TOTAL, stream>>>(mq, mk, mw, ms, a);
   prof_after(K_DELTA_OUT, stream);

@@ -261,18 +261,43 @@ struct Phase {
 };
 
 // ----------------------------------------------------------------- CTA
+// The chunk (and 64-column slice) of a CTA.
+struct ChunkId {
+  int slice, t0, n;
+  size_t ci, bh, tok;
+  TTT_DEVICE_INLINE ChunkId(unsigned block, int slices, int nch, int N) {
+    slice = block % slices;
+    ci = block / slices;
+    bh = ci / nch;
+    t0 = (int)(ci % nch) * C;
+    n = min(C, N - t0);
+    tok = bh * N + t0;
+  }
+};
+// One thread brings the operands of the CTA that will follow this one on its SM
+// (`ahead` CTAs on) into L2: a CTA lasts 5 to 20 us, of which a wait for DRAM
+// would be 1.
+template <typename F>
+TTT_DEVICE_INLINE void prefetch_next(int ahead, int slices, int nch, int N, F f) {
+  const unsigned next = blockIdx.x + ahead;
+  if (threadIdx.x == 64 && next < gridDim.x) f(ChunkId(next, slices, nch, N));
+}
 struct Bars {
   uint64_t load[2], mma;
   uint32_t tmem, abort;
 };
-// Barriers and `cols` TMEM columns, before the first phase; returns the TMEM base.
-TTT_DEVICE_INLINE uint32_t cta_begin(Bars& b, uint32_t cols, int tid) {
+// Barriers and `cols` TMEM columns, before the first phase; returns the TMEM
+// base.  Thread 0 issues the first loads (on load[0]) as soon as the barriers
+// stand.
+template <typename F>
+TTT_DEVICE_INLINE uint32_t cta_begin(Bars& b, uint32_t cols, int tid, F loads) {
   if (tid == 0) {
     mbar_init(&b.load[0], 1);
     mbar_init(&b.load[1], 1);
     mbar_init(&b.mma, 1);
     b.abort = 0;
     fence_barrier_init();
+    loads();
   }
   if (tid >> 5 == 1) {
     tmem_alloc(&b.tmem, cols);

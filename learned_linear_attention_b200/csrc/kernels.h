@@ -133,7 +133,7 @@ int launch_ttt_linear_bwd(const LinearBwdLaunch& L, cudaStream_t stream);
 
 // ----------------------------------------------------------------- delta rule
 struct DeltaLaunch {
-  int B, H, N, dk, dv;
+  int B, H, N, dk, dv, sms;
   float scale;
   int in_bf16, out_bf16;
   const void *q, *k, *v, *g, *beta;   // g nullable: no decay
