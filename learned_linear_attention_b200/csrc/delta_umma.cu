@@ -578,9 +578,8 @@ struct OutSmem {
   static constexpr uint32_t OP = DA * ATOM, SA = D * 128;
   static constexpr uint32_t Q = 0, K = OP, W = 2 * OP;              // W hi, lo
   static constexpr uint32_t S = 4 * OP;                             // S0 hi, lo
-  static constexpr uint32_t P = 0, U = 4 * ATOM;                    // P: 4 atoms, U: 2, over all of these
-  static constexpr uint32_t OPS = S + 2 * SA > 6 * ATOM ? S + 2 * SA : 6 * ATOM;
-  static constexpr uint32_t GATES = OPS, BAR = GATES + sizeof(Gates), TOTAL = BAR + 64;
+  static constexpr uint32_t U = 0;                                  // hi, lo, over Q and K
+  static constexpr uint32_t GATES = S + 2 * SA, BAR = GATES + sizeof(Gates), TOTAL = BAR + 64;
 };
 
 constexpr int OUT_THREADS = 512;
@@ -651,7 +650,9 @@ __global__ void __launch_bounds__(OUT_THREADS, D == 64 ? 2 : 1)
       store8_split(sb + SM::U, sb + SM::U + ATOM, row, cg * 16, u);
       store8_split(sb + SM::U, sb + SM::U + ATOM, row, cg * 16 + 8, u + 8);
     }
-    // P = Gam . Q K^T on and below the diagonal: [hi 0, hi 1, lo 0, lo 1]
+    // P = Gam . Q K^T on and below the diagonal, hi and lo, becomes an operand in
+    // tensor memory in the place of Q K^T
+    uint32_t ph_[16], pl[16];
 #pragma unroll
     for (int b = 0; b < 2; ++b) {
       const int c0 = cg * 32 + b * 16;
@@ -663,16 +664,22 @@ __global__ void __launch_bounds__(OUT_THREADS, D == 64 ? 2 : 1)
 #pragma unroll
         for (int j = 0; j < 16; ++j) x[j] = 0.f;
       }
-      const uint32_t hi = sb + SM::P + (uint32_t)(c0 >> 6) * ATOM;
-      store8_split(hi, hi + 2 * ATOM, row, c0 & 63, x);
-      store8_split(hi, hi + 2 * ATOM, row, (c0 & 63) + 8, x + 8);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) split2(x[2 * j], x[2 * j + 1], ph_[8 * b + j], pl[8 * b + j]);
     }
+    tc_fence_before();
+    __syncthreads();   // all of Q K^T has been read
+    tc_fence_after();
+    tmem_st16_issue(tmem + lanes + TM_P + cg * 16, ph_);
+    tmem_st16_issue(tmem + lanes + TM_P + 64 + cg * 16, pl);
+    tmem_wait_st();
     ph.publish();
     if (warp == 0 && elect_one()) {
-      const Pair P{{sb + SM::P, ATOM, false}, 2 * ATOM}, U{{sb + SM::U, ATOM, true}, ATOM};
-      products<8>(Prod(tmem + TM_W, P.lo(), U.hi, 128, 64, false));
-      products<8>(Prod(tmem + TM_W, P.hi, U.lo(), 128, 64, true));
-      products<8>(Prod(tmem + TM_W, P.hi, U.hi, 128, 64, true));
+      const Pair U{{sb + SM::U, ATOM, true}, ATOM};
+      const uint32_t hi = tmem + TM_P, lo = hi + 64;
+      products<8>(Prod(tmem + TM_W, lo, U.hi, 64, false));
+      products<8>(Prod(tmem + TM_W, hi, U.lo(), 64, true));
+      products<8>(Prod(tmem + TM_W, hi, U.hi, 64, true));
       mma_commit(&bars.mma);
     }
     if (!ph.mma_done(3)) return;
