@@ -318,7 +318,7 @@ int ttt_delta_workspace_bytes(const ttt_delta_desc* d, size_t* bytes) {
   if (e) return e;
   if (!bytes) return TTT_ERR_ARG;
   *bytes = delta_umma(d, false)
-               ? delta_umma_layout(d->B * d->H, d->N, d->dk).total
+               ? delta_umma_layout(d->B * d->H, d->N, d->dk, device_sms()).total
                : TTT_STATUS_BYTES;
   return TTT_OK;
 }

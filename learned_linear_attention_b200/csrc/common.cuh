@@ -190,17 +190,6 @@ TTT_DEVICE_INLINE void tma_load_3d(void* dst, const CUtensorMap* m, uint64_t* ba
       : "memory");
 }
 
-// The same tile, or `bytes` (a multiple of 16) from a 16-byte aligned address, into L2 only.
-TTT_DEVICE_INLINE void tma_prefetch_3d(const CUtensorMap* m, int x, int y, int z) {
-  asm volatile("cp.async.bulk.prefetch.tensor.3d.L2.global.tile [%0, {%1, %2, %3}];" ::"l"(
-                   reinterpret_cast<uint64_t>(m)),
-               "r"(x), "r"(y), "r"(z)
-               : "memory");
-}
-TTT_DEVICE_INLINE void bulk_prefetch(const void* p, uint32_t bytes) {
-  asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(p), "r"(bytes) : "memory");
-}
-
 TTT_DEVICE_INLINE void tma_load_4d(void* dst, const CUtensorMap* m, uint64_t* bar, int x, int y,
                                    int z, int w) {
   asm volatile(

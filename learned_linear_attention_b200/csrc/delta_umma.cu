@@ -10,9 +10,9 @@
 //   Mc = -(rho K)^T W [D, D],  Hc = (rho K)^T Ut [D, D]
 // so only the D x D recurrence S1 = gam_last S0 + Mc S0 + Hc runs in order
 // (one product a chunk), and everything else is parallel over the chunks:
-//   delta_prep_kernel   K, V -> W, Ut, Mc, Hc
-//   delta_chain_kernel  Mc, Hc -> every chunk's start state, end state
-//   delta_out_kernel    Q, K, W, Ut, start states -> O
+//   prep_cta   K, V -> W, Ut, Mc, Hc
+//   chain_cta  Mc, Hc -> every chunk's start state, end state
+//   out_cta    Q, K, W, Ut, start states -> O
 #include <algorithm>
 
 #include "delta_umma.cuh"
@@ -22,6 +22,8 @@ namespace ttt {
 using namespace dl;
 
 namespace {
+
+constexpr int THREADS = 512;   // of every CTA: four column groups of 128 rows
 
 // ------------------------------------------------------------------ inverse
 // (I + A)^-1 in place, A strictly lower triangular [128][128] float32 in
@@ -151,7 +153,8 @@ struct PrepArgs {
   __nv_bfloat16* W;        // [BH nch][2][128][D] hi, lo
   __nv_bfloat16* M;        // [BH nch][2][D][D] hi, lo
   __nv_bfloat16* T;        // nullable: [BH nch][2][128][128] hi, lo
-  int N, nch, ahead;
+  int N;
+  Slab slab;
   DevStatus st;
 };
 
@@ -166,24 +169,20 @@ struct PrepSmem {
   static constexpr uint32_t TOTAL = BAR + 64;
 };
 
-constexpr int PREP_THREADS = 512;
-
 template <int D>
-__global__ void __launch_bounds__(PREP_THREADS, D == 64 ? 2 : 1)
-    delta_prep_kernel(const __grid_constant__ CUtensorMap mapK, const __grid_constant__ CUtensorMap mapV,
-                      PrepArgs a) {
+TTT_DEVICE_INLINE void prep_cta(uint8_t* smem, const CUtensorMap& mapK, const CUtensorMap& mapV,
+                                const PrepArgs& a, unsigned block) {
   using SM = PrepSmem<D>;
   constexpr int DA = D / 64;
   constexpr uint32_t TM_A = 0, TM_T = 0, TM_U = 128, TM_W = 128 + D, TM_COLS = D == 64 ? 256 : 512;
   // Hc takes the place of T; Mc follows it (D = 64) or takes the last columns
   constexpr uint32_t TM_H = 0, TM_M = D == 64 ? 64 : 384;
-  extern __shared__ __align__(1024) uint8_t smem[];
   Bars& bars = *reinterpret_cast<Bars*>(smem + SM::BAR);
   Gates& gates = *reinterpret_cast<Gates*>(smem + SM::GATES);
   float* gams = reinterpret_cast<float*>(smem + SM::COL);
   float* rhos = gams + C;
   const int tid = threadIdx.x, warp = warp_index(), lane = tid & 31;
-  const ChunkId id(blockIdx.x, 1, a.nch, a.N);
+  const ChunkId id(block, 1, a.slab, a.N);
   const size_t ci = id.ci;
   const uint32_t sb = smem_u32(smem);
   const uint32_t tmem = cta_begin(bars, TM_COLS, tid, [&]() {
@@ -197,12 +196,6 @@ __global__ void __launch_bounds__(PREP_THREADS, D == 64 ? 2 : 1)
   const int q4 = warp & 3, cg = warp >> 2, row = q4 * 32 + lane;
   const uint32_t lanes = (uint32_t)(q4 * 32) << 16;
 
-  prefetch_next(a.ahead, 1, a.nch, a.N, [&](const ChunkId& next) {
-    for (int i = 0; i < DA; ++i) {
-      tma_prefetch_3d(&mapK, 64 * i, next.t0, (int)next.bh);
-      tma_prefetch_3d(&mapV, 64 * i, next.t0, (int)next.bh);
-    }
-  });
   if (cg == 1) {
     load_gates(gates, a.g ? a.g + id.tok : nullptr, a.beta + id.tok, id.n, row, gams[row], rhos[row]);
     if (row == C - 1) a.gend[ci] = gams[row];
@@ -393,7 +386,8 @@ __global__ void __launch_bounds__(PREP_THREADS, D == 64 ? 2 : 1)
 struct ChainArgs {
   const float* gend;
   DeltaChain dir[2];       // forward, backward
-  int nch, BH, first;      // the first CTAs take dir[first]
+  int BH, first;           // the first CTAs take dir[first]
+  Slab slab;
   DevStatus st;
 };
 
@@ -407,26 +401,24 @@ struct ChainSmem {
   static constexpr uint32_t TOTAL = BAR + 128;
 };
 
-constexpr int CHAIN_THREADS = 512;
-
 template <int D>
-__global__ void __launch_bounds__(CHAIN_THREADS, 1)
-    delta_chain_kernel(const __grid_constant__ CUtensorMap mapM, const __grid_constant__ CUtensorMap mapXf,
-                       const __grid_constant__ CUtensorMap mapXr, ChainArgs a) {
+TTT_DEVICE_INLINE void chain_cta(uint8_t* smem, const CUtensorMap& mapM, const CUtensorMap& mapXf,
+                                 const CUtensorMap& mapXr, const ChainArgs& a, unsigned block) {
   using SM = ChainSmem<D>;
   constexpr int DA = D / 64, STAGES = SM::STAGES;
   constexpr uint32_t TM_COLS = 64;
-  extern __shared__ __align__(1024) uint8_t smem[];
   uint64_t* full = reinterpret_cast<uint64_t*>(smem + SM::BAR);
   uint64_t* mma = full + STAGES;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(mma + 1);
   uint32_t* abort_flag = tmem_slot + 1;
   const int tid = threadIdx.x, warp = warp_index(), lane = tid & 31;
-  const int slice = blockIdx.x % DA;
-  const bool rev = a.first + blockIdx.x / (DA * a.BH) == 1;
-  const DeltaChain& dir = a.dir[rev ? 1 : 0];
-  const size_t bh = blockIdx.x / DA % a.BH, c0 = bh * a.nch;
-  auto chunk = [&](int i) { return c0 + (rev ? a.nch - 1 - i : i); };
+  const int slice = block % DA, nch = a.slab.len;
+  const bool rev = a.first + block / (DA * a.BH) == 1;
+  const float* H = rev ? a.dir[1].H : a.dir[0].H;
+  const float* S_in = rev ? a.dir[1].S_in : a.dir[0].S_in;
+  float* S_out = rev ? a.dir[1].S_out : a.dir[0].S_out;
+  const size_t bh = block / DA % a.BH, c0 = a.slab.w0 + bh * nch;
+  auto chunk = [&](int i) { return c0 + (rev ? nch - 1 - i : i); };
 
   if (tid == 0) {
     for (int s = 0; s < STAGES; ++s) mbar_init(&full[s], 1);
@@ -451,7 +443,7 @@ __global__ void __launch_bounds__(CHAIN_THREADS, 1)
   int issued = 0;
   // one thread each issues the products, the loads and the stores
   auto fetch = [&]() {   // by thread 32: the next chunk's Mc
-    if (issued >= a.nch) return;
+    if (issued >= nch) return;
     const int s = issued % STAGES;
     mbar_arrive_expect_tx(&full[s], SM::STAGE);
     for (int h = 0; h < 2; ++h)
@@ -466,7 +458,7 @@ __global__ void __launch_bounds__(CHAIN_THREADS, 1)
 #pragma unroll
   for (int j = 0; j < 16; j += 4) {
     float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-    if (own && dir.S_in != nullptr) v = *reinterpret_cast<const float4*>(dir.S_in + (bh * D + r) * D + col + j);
+    if (own && S_in != nullptr) v = *reinterpret_cast<const float4*>(S_in + (bh * D + r) * D + col + j);
     x[j] = v.x; x[j + 1] = v.y; x[j + 2] = v.z; x[j + 3] = v.w;
   }
   auto put_x = [&](uint32_t xb) {   // the operand copy
@@ -482,7 +474,7 @@ __global__ void __launch_bounds__(CHAIN_THREADS, 1)
     }
   };
   auto load_h = [&](int c, float4 (&h)[4]) {
-    const float* p = dir.H + chunk(c) * D * D + (size_t)slice * 64 * D + ((size_t)cg * 4 * D + r) * 4;
+    const float* p = H + chunk(c) * D * D + (size_t)slice * 64 * D + ((size_t)cg * 4 * D + r) * 4;
 #pragma unroll
     for (int j = 0; j < 4; ++j) h[j] = own ? *reinterpret_cast<const float4*>(p + (size_t)j * D * 4) : make_float4(0.f, 0.f, 0.f, 0.f);
   };
@@ -493,13 +485,13 @@ __global__ void __launch_bounds__(CHAIN_THREADS, 1)
   // One CTA barrier a chunk: it publishes X and tells whether every thread saw
   // the last product complete.
   bool ok = true;
-  for (int c = 0; c < a.nch; ++c) {
+  for (int c = 0; c < nch; ++c) {
     const uint32_t xo = SM::X + (c & 1) * 2 * SM::SA, xb = sb + xo;
     put_x(xb);
     fence_async_smem();
     tc_fence_before();
     if (tid == 64) bulk_wait_read();   // behind this barrier the other copy may be written again
-    if (!named_bar_all(1, CHAIN_THREADS, ok)) break;
+    if (!named_bar_all(1, THREADS, ok)) break;
     tc_fence_after();
     if (warp == 0) {
       const int s = c % STAGES;
@@ -526,7 +518,7 @@ __global__ void __launch_bounds__(CHAIN_THREADS, 1)
       x[4 * j + 2] = fmaf(e, x[4 * j + 2], h[j].z);
       x[4 * j + 3] = fmaf(e, x[4 * j + 3], h[j].w);
     }
-    if (c + 1 < a.nch) {
+    if (c + 1 < nch) {
       load_h(c + 1, h);
       e = a.gend[chunk(c + 1)];
     }
@@ -539,8 +531,8 @@ __global__ void __launch_bounds__(CHAIN_THREADS, 1)
     for (int j = 0; j < 16; ++j) x[j] += d[j];
   }
   __syncthreads();
-  if (!ph.W.aborted() && own && dir.S_out != nullptr) {
-    float* dst = dir.S_out + (bh * D + r) * D + col;
+  if (!ph.W.aborted() && own && S_out != nullptr) {
+    float* dst = S_out + (bh * D + r) * D + col;
 #pragma unroll
     for (int j = 0; j < 16; j += 4)
       *reinterpret_cast<float4*>(dst + j) = make_float4(x[j], x[j + 1], x[j + 2], x[j + 3]);
@@ -567,7 +559,8 @@ struct OutArgs {
   const __nv_bfloat16 *g, *beta;
   const float* U;
   void* out;
-  int N, nch, ahead, out_bf16;
+  int N, out_bf16;
+  Slab slab;
   float scale;
   DevStatus st;
 };
@@ -582,21 +575,17 @@ struct OutSmem {
   static constexpr uint32_t GATES = S + 2 * SA, BAR = GATES + sizeof(Gates), TOTAL = BAR + 64;
 };
 
-constexpr int OUT_THREADS = 512;
-
 template <int D>
-__global__ void __launch_bounds__(OUT_THREADS, D == 64 ? 2 : 1)
-    delta_out_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_constant__ CUtensorMap mapK,
-                     const __grid_constant__ CUtensorMap mapW, const __grid_constant__ CUtensorMap mapS,
-                     OutArgs a) {
+TTT_DEVICE_INLINE void out_cta(uint8_t* smem, const CUtensorMap& mapQ, const CUtensorMap& mapK,
+                               const CUtensorMap& mapW, const CUtensorMap& mapS, const OutArgs& a,
+                               unsigned block) {
   using SM = OutSmem<D>;
   constexpr int DA = D / 64;
   constexpr uint32_t TM_P = 0, TM_W = 128, TM_Q = 192, TM_COLS = 256;   // P U takes W S0's place
-  extern __shared__ __align__(1024) uint8_t smem[];
   Bars& bars = *reinterpret_cast<Bars*>(smem + SM::BAR);
   Gates& gates = *reinterpret_cast<Gates*>(smem + SM::GATES);
   const int tid = threadIdx.x, warp = warp_index(), lane = tid & 31;
-  const ChunkId id(blockIdx.x, DA, a.nch, a.N);
+  const ChunkId id(block, DA, a.slab, a.N);
   const int slice = id.slice;
   const size_t ci = id.ci;
   const uint32_t sb = smem_u32(smem);
@@ -614,15 +603,6 @@ __global__ void __launch_bounds__(OUT_THREADS, D == 64 ? 2 : 1)
   Phase ph{Waiter{&bars.abort, a.st, 1200}, &bars.mma, 0};
   const int q4 = warp & 3, cg = warp >> 2, row = q4 * 32 + lane;
   const uint32_t lanes = (uint32_t)(q4 * 32) << 16;
-  prefetch_next(a.ahead, DA, a.nch, a.N, [&](const ChunkId& next) {
-    for (int i = 0; i < DA; ++i) {
-      tma_prefetch_3d(&mapQ, 64 * i, next.t0, (int)next.bh);
-      tma_prefetch_3d(&mapK, 64 * i, next.t0, (int)next.bh);
-      for (int h = 0; h < 2; ++h) tma_prefetch_3d(&mapW, 64 * i, 0, (int)(2 * next.ci + h));
-    }
-    for (int h = 0; h < 2; ++h) tma_prefetch_3d(&mapS, 64 * next.slice, 0, (int)(2 * next.ci + h));
-    bulk_prefetch(a.U + next.ci * C * D + next.slice * 64 * C, 64 * C * 4);
-  });
   if (cg == 1) {
     load_gates(gates, a.g ? a.g + id.tok : nullptr, a.beta + id.tok, id.n, row);
   }
@@ -703,7 +683,52 @@ __global__ void __launch_bounds__(OUT_THREADS, D == 64 ? 2 : 1)
   cta_end(bars, ph, 1, tmem, TM_COLS, tid);
 }
 
-static_assert(2 * (PrepSmem<64>::TOTAL + 1024) <= 233472 && 2 * (OutSmem<64>::TOTAL + 1024) <= 233472, "two CTAs an SM");
+// ------------------------------------------------------------------ kernels
+template <int D>
+__global__ void __launch_bounds__(THREADS, D == 64 ? 2 : 1)
+    delta_prep_kernel(const __grid_constant__ CUtensorMap mapK, const __grid_constant__ CUtensorMap mapV,
+                      PrepArgs a) {
+  extern __shared__ __align__(1024) uint8_t smem[];
+  prep_cta<D>(smem, mapK, mapV, a, blockIdx.x);
+}
+template <int D>
+__global__ void __launch_bounds__(THREADS, 1)
+    delta_chain_kernel(const __grid_constant__ CUtensorMap mapM, const __grid_constant__ CUtensorMap mapXf,
+                       const __grid_constant__ CUtensorMap mapXr, ChainArgs a) {
+  extern __shared__ __align__(1024) uint8_t smem[];
+  chain_cta<D>(smem, mapM, mapXf, mapXr, a, blockIdx.x);
+}
+
+// The forward pass goes over the sequence in slabs, one launch after another:
+// the recurrence over slab i, the outputs of slab i - 1 and the preparation of
+// slab i + 1 share a launch, so the recurrence, which keeps a CTA a head and
+// 64 columns busy with latency, costs next to nothing, and the workspace is
+// that of three slabs.  No CTA waits for another one of its launch.
+struct FwdMaps {
+  CUtensorMap q, k, v, w, m, x;   // x as the chain stores it and the outputs read it
+};
+struct FwdArgs {
+  ChainArgs chain;
+  OutArgs out;
+  PrepArgs prep;
+  unsigned n_chain, n_out;        // CTAs of these roles, first in the grid; the others prepare
+};
+template <int D>
+struct FwdSmem {
+  static constexpr uint32_t most(uint32_t a, uint32_t b) { return a > b ? a : b; }
+  static constexpr uint32_t TOTAL = most(PrepSmem<D>::TOTAL, most(ChainSmem<D>::TOTAL, OutSmem<D>::TOTAL));
+};
+static_assert(2 * (FwdSmem<64>::TOTAL + 1024) <= 233472, "two CTAs an SM");
+
+template <int D>
+__global__ void __launch_bounds__(THREADS, D == 64 ? 2 : 1)
+    delta_fwd_kernel(const __grid_constant__ FwdMaps maps, const __grid_constant__ FwdArgs a) {
+  extern __shared__ __align__(1024) uint8_t smem[];
+  const unsigned b = blockIdx.x;
+  if (b < a.n_chain) chain_cta<D>(smem, maps.m, maps.x, maps.x, a.chain, b);
+  else if (b < a.n_chain + a.n_out) out_cta<D>(smem, maps.q, maps.k, maps.w, maps.x, a.out, b - a.n_chain);
+  else prep_cta<D>(smem, maps.k, maps.v, a.prep, b - a.n_chain - a.n_out);
+}
 
 template <int D>
 int prep_launch(const DeltaLaunch& p, const DeltaPrepOut& o, cudaStream_t stream) {
@@ -716,9 +741,9 @@ int prep_launch(const DeltaLaunch& p, const DeltaPrepOut& o, cudaStream_t stream
   static std::atomic<uint64_t> attr{0};
   if (allow_dynamic_smem(delta_prep_kernel<D>, (int)PrepSmem<D>::TOTAL, attr)) return -1;
   const PrepArgs a{(const __nv_bfloat16*)p.g, (const __nv_bfloat16*)p.beta, o.gend, o.H, o.U, o.W, o.M, o.T,
-                   p.N, nch, p.sms * (D == 64 ? 2 : 1), p.st};
+                   p.N, Slab{0, nch, 0}, p.st};
   prof_before(K_DELTA_PREP, stream);
-  delta_prep_kernel<D><<<(unsigned)nc, PREP_THREADS, PrepSmem<D>::TOTAL, stream>>>(mk, mv, a);
+  delta_prep_kernel<D><<<(unsigned)nc, THREADS, PrepSmem<D>::TOTAL, stream>>>(mk, mv, a);
   prof_after(K_DELTA_PREP, stream);
   return cudaGetLastError() == cudaSuccess ? 0 : -1;
 }
@@ -735,41 +760,69 @@ int chain_launch(const DeltaLaunch& p, const float* gend, const __nv_bfloat16* M
     return -1;
   static std::atomic<uint64_t> attr{0};
   if (allow_dynamic_smem(delta_chain_kernel<D>, (int)ChainSmem<D>::TOTAL, attr)) return -1;
-  ChainArgs a{gend, {}, nch, BH, fwd ? 0 : 1, p.st};
+  ChainArgs a{gend, {}, BH, fwd ? 0 : 1, Slab{0, nch, 0}, p.st};
   if (fwd) a.dir[0] = *fwd;
   if (rev) a.dir[1] = *rev;
   const unsigned dirs = (fwd ? 1 : 0) + (rev ? 1 : 0);
   prof_before(K_DELTA_CHAIN, stream);
-  delta_chain_kernel<D><<<dirs * (unsigned)(BH * (D / 64)), CHAIN_THREADS, ChainSmem<D>::TOTAL, stream>>>(mm, mf, mr, a);
+  delta_chain_kernel<D><<<dirs * (unsigned)(BH * (D / 64)), THREADS, ChainSmem<D>::TOTAL, stream>>>(mm, mf, mr, a);
   prof_after(K_DELTA_CHAIN, stream);
   return cudaGetLastError() == cudaSuccess ? 0 : -1;
 }
 
+// Chunks of a slab: an eighth of the sequence, or what gives the preparing
+// CTAs two rounds on the device, if that is more; at least four chunks.
+int slab_chunks(int BH, int nch, int D, int sms) {
+  const int rounds2 = (2 * sms * (D == 64 ? 2 : 1) + BH - 1) / BH;
+  return std::min(nch, std::max({(nch + 7) / 8, rounds2, 4}));
+}
+
 template <int D>
 int fwd_launch(const DeltaLaunch& p, cudaStream_t stream) {
-  const int BH = p.B * p.H, nch = (p.N + C - 1) / C;
-  const DeltaUmmaWorkspace w = delta_umma_layout(BH, p.N, D);
-  const uint64_t nc = (uint64_t)BH * nch, rs = D * 2;
+  const int BH = p.B * p.H, nch = (p.N + C - 1) / C, len = slab_chunks(BH, nch, D, p.sms);
+  const int slabs = (nch + len - 1) / len;
+  const DeltaUmmaWorkspace w = delta_umma_layout(BH, p.N, D, p.sms);
+  const uint64_t nc = w.chunks, rs = D * 2;
   uint8_t* ws = delta_ws_base(p.ws);
   auto bf = [&](size_t at) { return reinterpret_cast<__nv_bfloat16*>(ws + at); };
   auto f32 = [&](size_t at) { return reinterpret_cast<float*>(ws + at); };
-  const DeltaPrepOut o{f32(w.gend), f32(w.H), f32(w.U), bf(w.W), bf(w.M), nullptr};
-  const DeltaChain chain{o.H, p.S, p.S, bf(w.X)};
-  if (prep_launch<D>(p, o, stream) || chain_launch<D>(p, o.gend, o.M, &chain, nullptr, stream)) return -1;
-  CUtensorMap mq, mk, mw, ms;
-  if (make_tmap_bf16_3d(&mq, p.q, D, p.N, BH, rs, p.N * rs, 64, C) ||
-      make_tmap_bf16_3d(&mk, p.k, D, p.N, BH, rs, p.N * rs, 64, C) ||
-      make_tmap_bf16_3d(&mw, o.W, D, C, 2 * nc, rs, C * rs, 64, C) ||
-      make_tmap_bf16_3d(&ms, chain.X, D, D, 2 * nc, rs, D * rs, 64, D))
+  FwdMaps maps;
+  if (make_tmap_bf16_3d(&maps.q, p.q, D, p.N, BH, rs, p.N * rs, 64, C) ||
+      make_tmap_bf16_3d(&maps.k, p.k, D, p.N, BH, rs, p.N * rs, 64, C) ||
+      make_tmap_bf16_3d(&maps.v, p.v, D, p.N, BH, rs, p.N * rs, 64, C) ||
+      make_tmap_bf16_3d(&maps.w, bf(w.W), D, C, 2 * nc, rs, C * rs, 64, C) ||
+      make_tmap_bf16_3d(&maps.m, bf(w.M), D, D, 2 * nc, rs, D * rs, 64, D) ||
+      make_tmap_bf16_3d(&maps.x, bf(w.X), D, D, 2 * nc, rs, D * rs, 64, D))
     return -1;
   static std::atomic<uint64_t> attr{0};
-  if (allow_dynamic_smem(delta_out_kernel<D>, (int)OutSmem<D>::TOTAL, attr)) return -1;
-  const OutArgs a{(const __nv_bfloat16*)p.g, (const __nv_bfloat16*)p.beta, o.U, p.out, p.N, nch,
-                  p.sms * (D == 64 ? 2 : 1), p.out_bf16, p.scale, p.st};
-  prof_before(K_DELTA_OUT, stream);
-  delta_out_kernel<D><<<(unsigned)(nc * (D / 64)), OUT_THREADS, OutSmem<D>::TOTAL, stream>>>(mq, mk, mw, ms, a);
-  prof_after(K_DELTA_OUT, stream);
-  return cudaGetLastError() == cudaSuccess ? 0 : -1;
+  if (allow_dynamic_smem(delta_fwd_kernel<D>, (int)FwdSmem<D>::TOTAL, attr)) return -1;
+  const __nv_bfloat16 *g = (const __nv_bfloat16*)p.g, *beta = (const __nv_bfloat16*)p.beta;
+  auto slab = [&](int i) {
+    return Slab{i * len, std::min(len, nch - i * len), (size_t)(i % 3) * BH * len};
+  };
+  for (int j = 0; j < slabs + 2; ++j) {   // prepare slab j, recur over j - 1, outputs of j - 2
+    FwdArgs a{};
+    unsigned n_prep = 0;
+    if (j < slabs) {
+      a.prep = PrepArgs{g, beta, f32(w.gend), f32(w.H), f32(w.U), bf(w.W), bf(w.M), nullptr, p.N, slab(j), p.st};
+      n_prep = (unsigned)BH * a.prep.slab.len;
+    }
+    if (j >= 1 && j <= slabs) {
+      // every slab's recurrence starts from S and leaves its end there
+      const DeltaChain dir{f32(w.H), p.S, p.S, nullptr};
+      a.chain = ChainArgs{f32(w.gend), {dir, {}}, BH, 0, slab(j - 1), p.st};
+      a.n_chain = (unsigned)(BH * (D / 64));
+    }
+    if (j >= 2) {
+      a.out = OutArgs{g, beta, f32(w.U), p.out, p.N, p.out_bf16, slab(j - 2), p.scale, p.st};
+      a.n_out = (unsigned)(BH * (D / 64)) * a.out.slab.len;
+    }
+    prof_before(K_DELTA_FWD, stream);
+    delta_fwd_kernel<D><<<a.n_chain + a.n_out + n_prep, THREADS, FwdSmem<D>::TOTAL, stream>>>(maps, a);
+    prof_after(K_DELTA_FWD, stream);
+    if (cudaGetLastError() != cudaSuccess) return -1;
+  }
+  return 0;
 }
 
 }  // namespace
@@ -787,9 +840,11 @@ bool delta_uses_umma(int bf16, int dk, int dv, long long BH, int N, int sms, boo
   return N * rounds > (backward ? (dk == 64 ? 128 : 64) : 160);
 }
 
-DeltaUmmaWorkspace delta_umma_layout(int BH, int N, int D) {
+DeltaUmmaWorkspace delta_umma_layout(int BH, int N, int D, int sms) {
   DeltaUmmaWorkspace w{};
-  const size_t nc = (size_t)BH * ((N + C - 1) / C);
+  const int nch = (N + C - 1) / C, len = slab_chunks(BH, nch, D, sms);
+  const size_t nc = (size_t)BH * std::min(nch, 3 * len);
+  w.chunks = nc;
   size_t at = 512;   // see delta_ws_base
   auto take = [&](size_t bytes) {
     const size_t o = at;

@@ -261,27 +261,26 @@ struct Phase {
 };
 
 // ----------------------------------------------------------------- CTA
-// The chunk (and 64-column slice) of a CTA.
+// Chunks [c0, c0 + len) of every head; their buffers in the workspace are those
+// from w0 on, head by head.
+struct Slab {
+  int c0, len;
+  size_t w0;
+};
+// The chunk (and 64-column slice) of a CTA; ci counts in the workspace.
 struct ChunkId {
   int slice, t0, n;
   size_t ci, bh, tok;
-  TTT_DEVICE_INLINE ChunkId(unsigned block, int slices, int nch, int N) {
+  TTT_DEVICE_INLINE ChunkId(unsigned block, int slices, const Slab& s, int N) {
     slice = block % slices;
-    ci = block / slices;
-    bh = ci / nch;
-    t0 = (int)(ci % nch) * C;
+    const unsigned r = block / slices;
+    ci = s.w0 + r;
+    bh = r / s.len;
+    t0 = (s.c0 + (int)(r % s.len)) * C;
     n = min(C, N - t0);
     tok = bh * N + t0;
   }
 };
-// One thread brings the operands of the CTA that will follow this one on its SM
-// (`ahead` CTAs on) into L2: a CTA lasts 5 to 20 us, of which a wait for DRAM
-// would be 1.
-template <typename F>
-TTT_DEVICE_INLINE void prefetch_next(int ahead, int slices, int nch, int N, F f) {
-  const unsigned next = blockIdx.x + ahead;
-  if (threadIdx.x == 64 && next < gridDim.x) f(ChunkId(next, slices, nch, N));
-}
 struct Bars {
   uint64_t load[2], mma;
   uint32_t tmem, abort;
@@ -346,6 +345,7 @@ struct DeltaChain {         // one direction of the state recurrence
   float* S_out;             // nullable
   __nv_bfloat16* X;         // [BH nch][2][D][D] hi, lo: the state at every chunk's start (its end, backward)
 };
+// All chunks at once, each with buffers of its own.
 int launch_delta_prep(const DeltaLaunch& p, const DeltaPrepOut& o, cudaStream_t stream);
 // fwd nullable; rev nullable: X <- exp(G_last) X + M^T X + H, from the last chunk
 int launch_delta_chain(const DeltaLaunch& p, const float* gend, const __nv_bfloat16* M, const DeltaChain* fwd,

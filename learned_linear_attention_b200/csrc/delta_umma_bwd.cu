@@ -56,7 +56,7 @@ TTT_DEVICE_INLINE float row_total(const float* red, int row) {
 struct HbArgs {
   const __nv_bfloat16 *g, *beta;
   float* H;
-  int N, nch, ahead;
+  int N, nch;
   float scale;
   DevStatus st;
 };
@@ -82,7 +82,7 @@ __global__ void __launch_bounds__(THREADS, 1)
   Bars& bars = *reinterpret_cast<Bars*>(smem + SM::BAR);
   Gates& gates = *reinterpret_cast<Gates*>(smem + SM::GATES);
   const int tid = threadIdx.x, warp = warp_index(), lane = tid & 31;
-  const ChunkId id(blockIdx.x, DA, a.nch, a.N);
+  const ChunkId id(blockIdx.x, DA, Slab{0, a.nch, 0}, a.N);
   const uint32_t sb = smem_u32(smem);
   const uint32_t tmem = cta_begin(bars, TM_COLS, tid, [&]() {
     mbar_arrive_expect_tx(&bars.load[0], 4 * DA * ATOM + ATOM);
@@ -97,14 +97,6 @@ __global__ void __launch_bounds__(THREADS, 1)
   Phase ph{Waiter{&bars.abort, a.st, 1300}, &bars.mma, 0};
   const int q4 = warp & 3, cg = warp >> 2, row = q4 * 32 + lane;
   const uint32_t lanes = (uint32_t)(q4 * 32) << 16;
-  prefetch_next(a.ahead, DA, a.nch, a.N, [&](const ChunkId& next) {
-    for (int i = 0; i < DA; ++i) {
-      tma_prefetch_3d(&mapQ, 64 * i, next.t0, (int)next.bh);
-      tma_prefetch_3d(&mapK, 64 * i, next.t0, (int)next.bh);
-      for (int h = 0; h < 2; ++h) tma_prefetch_3d(&mapW, 64 * i, 0, (int)(2 * next.ci + h));
-    }
-    tma_prefetch_3d(&mapD, 64 * next.slice, next.t0, (int)next.bh);
-  });
   if (cg == 1) load_gates(gates, a.g ? a.g + id.tok : nullptr, a.beta + id.tok, id.n, row);
   auto work = [&]() {
     if (!ph.wait(&bars.load[0], 0, 1)) return;
@@ -190,7 +182,7 @@ struct ValsArgs {
   const float* Ut;
   __nv_bfloat16* dv;
   float* bpart;            // [D / 64][BH N]
-  int N, nch, ahead;
+  int N, nch;
   size_t tokens;
   DevStatus st;
 };
@@ -219,7 +211,7 @@ __global__ void __launch_bounds__(THREADS, 1)
   Gates& gates = *reinterpret_cast<Gates*>(smem + SM::GATES);
   float* red = reinterpret_cast<float*>(smem + SM::RED);
   const int tid = threadIdx.x, warp = warp_index(), lane = tid & 31;
-  const ChunkId id(blockIdx.x, DA, a.nch, a.N);
+  const ChunkId id(blockIdx.x, DA, Slab{0, a.nch, 0}, a.N);
   const uint32_t sb = smem_u32(smem);
   const uint32_t tmem = cta_begin(bars, TM_COLS, tid, [&]() {
     mbar_arrive_expect_tx(&bars.load[0], 3 * DA * ATOM + 2 * ATOM + 4 * SM::SA);
@@ -238,18 +230,6 @@ __global__ void __launch_bounds__(THREADS, 1)
   Phase ph{Waiter{&bars.abort, a.st, 1400}, &bars.mma, 0};
   const int q4 = warp & 3, cg = warp >> 2, row = q4 * 32 + lane;
   const uint32_t lanes = (uint32_t)(q4 * 32) << 16;
-  prefetch_next(a.ahead, DA, a.nch, a.N, [&](const ChunkId& next) {
-    for (int h = 0; h < 2; ++h) {
-      const int z = (int)(2 * next.ci + h), x = 64 * next.slice;
-      for (int i = 0; i < DA; ++i) tma_prefetch_3d(&mapW, 64 * i, 0, z);
-      for (int i = 0; i < 2; ++i) tma_prefetch_3d(&mapT, 64 * i, 0, z);
-      tma_prefetch_3d(&mapS, x, 0, z);
-      tma_prefetch_3d(&mapX, x, 0, z);
-      tma_prefetch_3d(&mapY, x, 0, z);
-    }
-    for (int i = 0; i < DA; ++i) tma_prefetch_3d(&mapK, 64 * i, next.t0, (int)next.bh);
-    bulk_prefetch(a.Ut + next.ci * C * D + next.slice * 64 * C, 64 * C * 4);
-  });
   if (cg == 1) load_gates(gates, a.g ? a.g + id.tok : nullptr, a.beta + id.tok, id.n, row);
   int loads = 1;
   auto work = [&]() {
@@ -354,7 +334,7 @@ struct KeysArgs {
   float *rpart, *wpart;    // [D / 64][BH N]
   float* xpart;            // [D / 64][BH nch]: <X1, S0>
   float* bkey;             // [BH N]
-  int N, nch, ahead;
+  int N, nch;
   size_t tokens, chunks;
   float scale;
   DevStatus st;
@@ -388,7 +368,7 @@ __global__ void __launch_bounds__(THREADS, 1)
   Gates& gates = *reinterpret_cast<Gates*>(smem + SM::GATES);
   float *red = reinterpret_cast<float*>(smem + SM::RED), *xs = reinterpret_cast<float*>(smem + SM::XS);
   const int tid = threadIdx.x, warp = warp_index(), lane = tid & 31;
-  const ChunkId id(blockIdx.x, DA, a.nch, a.N);
+  const ChunkId id(blockIdx.x, DA, Slab{0, a.nch, 0}, a.N);
   const uint32_t sb = smem_u32(smem);
   const uint32_t tmem = cta_begin(bars, TM_COLS, tid, [&]() {
     mbar_arrive_expect_tx(&bars.load[0], 5 * DA * ATOM + 4 * DA * SM::HA);
@@ -406,20 +386,6 @@ __global__ void __launch_bounds__(THREADS, 1)
   Phase ph{Waiter{&bars.abort, a.st, 1500}, &bars.mma, 0};
   const int q4 = warp & 3, cg = warp >> 2, row = q4 * 32 + lane;
   const uint32_t lanes = (uint32_t)(q4 * 32) << 16;
-  prefetch_next(a.ahead, DA, a.nch, a.N, [&](const ChunkId& next) {
-    for (int i = 0; i < DA; ++i) {
-      tma_prefetch_3d(&mapD, 64 * i, next.t0, (int)next.bh);
-      tma_prefetch_3d(&mapK, 64 * i, next.t0, (int)next.bh);
-      for (int h = 0; h < 2; ++h) {
-        const int z = (int)(2 * next.ci + h);
-        tma_prefetch_3d(&mapU, 64 * i, 0, z);
-        tma_prefetch_3d(&mapY, 64 * i, 0, z);
-        tma_prefetch_3d(&mapS, 64 * i, 64 * next.slice, z);
-        tma_prefetch_3d(&mapX, 64 * i, 64 * next.slice, z);
-      }
-    }
-    tma_prefetch_3d(&mapQ, 64 * next.slice, next.t0, (int)next.bh);
-  });
   if (cg == 1) load_gates(gates, a.g ? a.g + id.tok : nullptr, a.beta + id.tok, id.n, row);
   int loads = 1;
   auto work = [&]() {
@@ -669,19 +635,19 @@ int bwd_launch(const DeltaBwdLaunch& L, cudaStream_t stream) {
   const unsigned grid = (unsigned)(nc * DA);
   prof_before(K_DELTA_HB, stream);
   delta_hb_kernel<D><<<grid, THREADS, HbSmem<D>::TOTAL, stream>>>(
-      mq, mk, md, mw, my, HbArgs{g, beta, f32(w.Hb), p.N, nch, p.sms, p.scale, p.st});
+      mq, mk, md, mw, my, HbArgs{g, beta, f32(w.Hb), p.N, nch, p.scale, p.st});
   prof_after(K_DELTA_HB, stream);
   if (launch_delta_chain(p, o.gend, o.M, &fwd, &rev, stream)) return -1;
   prof_before(K_DELTA_VALS, stream);
   delta_vals_kernel<D><<<grid, THREADS, ValsSmem<D>::TOTAL, stream>>>(
       mk, mw, mu, my, mt, ms, mx,
-      ValsArgs{g, beta, (const __nv_bfloat16*)p.v, o.U, (__nv_bfloat16*)L.dv, f32(w.bpart), p.N, nch, p.sms, tokens, p.st});
+      ValsArgs{g, beta, (const __nv_bfloat16*)p.v, o.U, (__nv_bfloat16*)L.dv, f32(w.bpart), p.N, nch, tokens, p.st});
   prof_after(K_DELTA_VALS, stream);
   prof_before(K_DELTA_KEYS, stream);
   delta_keys_kernel<D><<<grid, THREADS, KeysSmem<D>::TOTAL, stream>>>(
       mq, mk, md, mu, my, ms64, mx64,
       KeysArgs{g, beta, (__nv_bfloat16*)L.dq, (__nv_bfloat16*)L.dk, f32(w.rpart), f32(w.wpart), f32(w.xpart),
-               f32(w.bkey), p.N, nch, p.sms, tokens, nc, p.scale, p.st});
+               f32(w.bkey), p.N, nch, tokens, nc, p.scale, p.st});
   prof_after(K_DELTA_KEYS, stream);
   prof_before(K_DELTA_GATES, stream);
   delta_gate_grad_kernel<<<(unsigned)nc, C, 0, stream>>>(

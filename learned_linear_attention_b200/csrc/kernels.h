@@ -158,11 +158,11 @@ int launch_delta_rec(const DeltaLaunch& L, cudaStream_t stream);
 DeltaBwdWorkspace delta_rec_bwd_layout(int BH, int N, int dk, int dv);
 int launch_delta_rec_bwd(const DeltaBwdLaunch& L, cudaStream_t stream);
 // tensor cores, bf16, dk = dv = 64 or 128 (delta_umma.cu)
-struct DeltaUmmaWorkspace {           // byte offsets, per chunk of 128 tokens
-  size_t gend, W, U, M, H, X, total;
+struct DeltaUmmaWorkspace {           // byte offsets, of `chunks` chunks of 128 tokens
+  size_t gend, W, U, M, H, X, total, chunks;
 };
 bool delta_uses_umma(int bf16, int dk, int dv, long long BH, int N, int sms, bool backward);
-DeltaUmmaWorkspace delta_umma_layout(int BH, int N, int D);
+DeltaUmmaWorkspace delta_umma_layout(int BH, int N, int D, int sms);
 int launch_delta_umma(const DeltaLaunch& L, cudaStream_t stream);
 struct DeltaUmmaBwdWorkspace {
   size_t gend, W, U, Ut, Y, T, M, H, Hb, X, X1, rpart, wpart, bpart, bkey, xpart, total;
@@ -360,7 +360,7 @@ enum KernelKind {
   K_LIN_SIMT, K_LIN_UMMA, K_LACT_CAST, K_KEYPASS, K_GEMM_READ, K_GEMM_GRAD, K_UPDATE,
   K_MUON_MOM, K_NS_PREP, K_GEMM_NS, K_MUON_APPLY, K_KEYGRAD, K_LIN_SEG, K_LIN_BWD_EW, K_SWA, K_LOOP,
   K_BWD_FWD, K_BWD_GROUP, K_DELTA_REC, K_DELTA_REV, K_DELTA_GRAD, K_DELTA_STEP, K_NORM, K_NORM_BWD,
-  K_DELTA_PREP, K_DELTA_CHAIN, K_DELTA_OUT, K_DELTA_HB, K_DELTA_VALS, K_DELTA_KEYS, K_DELTA_GATES,
+  K_DELTA_PREP, K_DELTA_CHAIN, K_DELTA_FWD, K_DELTA_HB, K_DELTA_VALS, K_DELTA_KEYS, K_DELTA_GATES,
   K_NUM
 };
 void prof_before(int kind, cudaStream_t s);
