@@ -27,99 +27,106 @@ constexpr int THREADS = 512;   // of every CTA: four column groups of 128 rows
 
 // ------------------------------------------------------------------ inverse
 // (I + A)^-1 in place, A strictly lower triangular [128][128] float32 in
-// shared memory (rows LDA floats apart), by 256 threads (barrier 1): 16 x 16 diagonal
-// blocks by substitution, one column a thread, then blocks of 16, 32 and 64
-// joined two by two, T21 = -T22 (A21 T11).  Every factor is itself an
-// inverse, so the intermediate values stay of the size of the result (the
-// powers of A of a Neumann product do not).  A21 T11 waits in the unused
-// block above the diagonal, so what is above the diagonal is not zero at the
-// end.
+// shared memory (rows LDA floats apart): 16 x 16 diagonal blocks by
+// substitution, one column a thread, then blocks of 16, 32 and 64 joined two
+// by two, T21 = -T22 (A21 T11).  Every factor is itself an inverse, so the
+// intermediate values stay of the size of the result (the powers of A of a
+// Neumann product do not).  A21 T11 waits in the unused block above the
+// diagonal, so what is above the diagonal may be anything, before and after.
+//
+// The joins are warp-level tensor products, a tile of 16 x 16 a warp, with
+// every float32 value as a sum of two tf32 ones (three products; 2^-22).  With
+// FFMA, what the register tiles read from shared memory bound them: 4 x 4 a
+// thread took 8100 cycles for blocks of 64, two CTAs an SM.  (The blocks are
+// too small for tcgen05: its operands would have to be split into planes and
+// stored first.)
 constexpr int LDA = 132;
 
-// A thread of a join takes four columns and every 16th row, a warp two column
-// groups: what a column group skips (rows of T11 above it) its warp skips, and
-// what a row skips (T22 right of it) is known at compile time.
-TTT_DEVICE_INLINE void fma4(float2 (&acc)[2], float x, const float4& y) {
-  const float2 s = x2_splat(x);
-  acc[0] = x2_fma(s, make_float2(y.x, y.y), acc[0]);
-  acc[1] = x2_fma(s, make_float2(y.z, y.w), acc[1]);
+struct Tf32 {
+  uint32_t hi, lo;
+  TTT_DEVICE_INLINE explicit Tf32(float x) {
+    hi = __float_as_uint(x) & 0xffffe000u;
+    lo = __float_as_uint(x - __uint_as_float(hi));   // its own lowest bits are not read
+  }
+};
+TTT_DEVICE_INLINE void mma_16x8x8(float (&c)[4], const uint32_t (&a)[4], const uint32_t (&b)[2]) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k8.row.col.f32.tf32.tf32.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b[0]), "r"(b[1]));
+}
+
+// acc = X Y of a 16 x 16 tile: X at its first row, Y at its first column, k in
+// [k0, k1).  xd, yd: the tile's first row or column where X or Y is lower
+// triangular (what lies above the diagonal counts as zero), -1 where not.
+TTT_DEVICE_INLINE void tile_product(const float* X, const float* Y, int k0, int k1, int xd, int yd, int lane,
+                                    float (&acc)[2][4]) {
+  const int g = lane >> 2, t = lane & 3;
+#pragma unroll
+  for (int n = 0; n < 2; ++n)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) acc[n][i] = 0.f;
+#pragma unroll 2
+  for (int k = k0; k < k1; k += 8) {
+    uint32_t ah[4], al[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int r = g + (i & 1) * 8, c = k + t + (i >> 1) * 4;
+      const float x = X[r * LDA + c];
+      const Tf32 v(xd >= 0 && c > xd + r ? 0.f : x);
+      ah[i] = v.hi;
+      al[i] = v.lo;
+    }
+#pragma unroll
+    for (int n = 0; n < 2; ++n) {
+      uint32_t bh[2], bl[2];
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const int r = k + t + i * 4, c = 8 * n + g;
+        const float y = Y[r * LDA + c];
+        const Tf32 v(yd >= 0 && r < yd + c ? 0.f : y);
+        bh[i] = v.hi;
+        bl[i] = v.lo;
+      }
+      mma_16x8x8(acc[n], al, bh);
+      mma_16x8x8(acc[n], ah, bl);
+      mma_16x8x8(acc[n], ah, bh);
+    }
+  }
+}
+TTT_DEVICE_INLINE void store_tile(float* C_, float sign, int lane, const float (&acc)[2][4]) {
+  const int g = lane >> 2, t = lane & 3;
+#pragma unroll
+  for (int n = 0; n < 2; ++n) {
+    *reinterpret_cast<float2*>(C_ + g * LDA + 8 * n + 2 * t) = make_float2(sign * acc[n][0], sign * acc[n][1]);
+    *reinterpret_cast<float2*>(C_ + (g + 8) * LDA + 8 * n + 2 * t) = make_float2(sign * acc[n][2], sign * acc[n][3]);
+  }
 }
 
 template <int S>
-TTT_DEVICE_INLINE void join_blocks(float* A, int tid) {
-  constexpr int RT = S / 16;
-  const int p = tid / (4 * S), t = tid % (4 * S), cg = t / 16, r0 = t % 16;
+TTT_DEVICE_INLINE void join_blocks(float* A, int warp, int lane) {
+  constexpr int TILES = S / 16, WARPS = TILES * TILES * (C / (2 * S));
+  static_assert(WARPS <= THREADS / 32, "a tile a warp");
+  const int p = warp / (TILES * TILES), r0 = warp / TILES % TILES * 16, n0 = warp % TILES * 16;
   float* T11 = A + p * 2 * S * (LDA + 1);
   float* A21 = T11 + S * LDA;
   float* T22 = A21 + S;
   float* Z = T11 + S;
-  float2 acc[RT][2];
-  auto zero = [&]() {
-#pragma unroll
-    for (int r = 0; r < RT; ++r) acc[r][0] = acc[r][1] = make_float2(0.f, 0.f);
-  };
-  zero();
-  // Z = A21 T11; above T11's diagonal there may be anything
-#pragma unroll 2
-  for (int k = 4 * (cg & ~1); k < S; k += 4) {
-    float4 y[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) y[i] = *reinterpret_cast<const float4*>(T11 + (k + i) * LDA + 4 * cg);
-    if (k <= 4 * cg) {
-      const bool diag = k == 4 * cg;
-      y[0] = make_float4(diag ? y[0].x : 0.f, 0.f, 0.f, 0.f);
-      y[1] = make_float4(diag ? y[1].x : 0.f, diag ? y[1].y : 0.f, 0.f, 0.f);
-      y[2] = make_float4(diag ? y[2].x : 0.f, diag ? y[2].y : 0.f, diag ? y[2].z : 0.f, 0.f);
-      if (!diag) y[3] = make_float4(0.f, 0.f, 0.f, 0.f);
-    }
-#pragma unroll
-    for (int r = 0; r < RT; ++r) {
-      const float4 x = *reinterpret_cast<const float4*>(A21 + (r0 + 16 * r) * LDA + k);
-      fma4(acc[r], x.x, y[0]);
-      fma4(acc[r], x.y, y[1]);
-      fma4(acc[r], x.z, y[2]);
-      fma4(acc[r], x.w, y[3]);
-    }
+  float acc[2][4];
+  if (warp < WARPS) {   // Z = A21 T11: nothing above T11's columns
+    tile_product(A21 + r0 * LDA, T11 + n0, n0, S, -1, n0, lane, acc);
+    store_tile(Z + r0 * LDA + n0, 1.f, lane, acc);
   }
-#pragma unroll
-  for (int r = 0; r < RT; ++r)
-    *reinterpret_cast<float4*>(Z + (r0 + 16 * r) * LDA + 4 * cg) =
-        make_float4(acc[r][0].x, acc[r][0].y, acc[r][1].x, acc[r][1].y);
-  zero();
-  named_bar_sync(1, 256);
-  // T22 Z, 16 columns of T22 at a time: its rows above them have no part
-#pragma unroll
-  for (int kb = 0; kb < RT; ++kb) {
-#pragma unroll
-    for (int k = 16 * kb; k < 16 * kb + 16; k += 4) {
-      float4 y[4];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) y[i] = *reinterpret_cast<const float4*>(Z + (k + i) * LDA + 4 * cg);
-#pragma unroll
-      for (int r = kb; r < RT; ++r) {
-        float4 x = *reinterpret_cast<const float4*>(T22 + (r0 + 16 * r) * LDA + k);
-        if (r == kb) {
-          const int d = 16 * kb + r0 - k;   // columns behind the diagonal may hold anything
-          if (d < 0) x.x = 0.f;
-          if (d < 1) x.y = 0.f;
-          if (d < 2) x.z = 0.f;
-          if (d < 3) x.w = 0.f;
-        }
-        fma4(acc[r], x.x, y[0]);
-        fma4(acc[r], x.y, y[1]);
-        fma4(acc[r], x.z, y[2]);
-        fma4(acc[r], x.w, y[3]);
-      }
-    }
+  __syncthreads();
+  if (warp < WARPS) {   // -T22 Z: nothing right of T22's rows
+    tile_product(T22 + r0 * LDA, Z + n0, 0, r0 + 16, r0, -1, lane, acc);
+    store_tile(A21 + r0 * LDA + n0, -1.f, lane, acc);
   }
-#pragma unroll
-  for (int r = 0; r < RT; ++r)
-    *reinterpret_cast<float4*>(A21 + (r0 + 16 * r) * LDA + 4 * cg) =
-        make_float4(-acc[r][0].x, -acc[r][0].y, -acc[r][1].x, -acc[r][1].y);
-  named_bar_sync(1, 256);
+  __syncthreads();
 }
 
-TTT_DEVICE_INLINE void invert(float* A, int tid) {
+TTT_DEVICE_INLINE void invert(float* A, int warp, int lane) {
+  const int tid = warp * 32 + lane;
   float x[16];
   if (tid < C) {
     const float* B = A + (tid >> 4) * 16 * (LDA + 1);
@@ -131,17 +138,15 @@ TTT_DEVICE_INLINE void invert(float* A, int tid) {
       for (int k = 0; k < i; ++k) acc = fmaf(-B[i * LDA + k], x[k], acc);
       x[i] = acc;
     }
-  }
-  named_bar_sync(1, 256);
-  if (tid < C) {
-    float* B = A + (tid >> 4) * 16 * (LDA + 1);
+    __syncwarp();   // a block's 16 threads are in one warp
+    float* W = A + (tid >> 4) * 16 * (LDA + 1);
 #pragma unroll
-    for (int i = 0; i < 16; ++i) B[i * LDA + (tid & 15)] = x[i];
+    for (int i = 0; i < 16; ++i) W[i * LDA + (tid & 15)] = x[i];
   }
-  named_bar_sync(1, 256);
-  join_blocks<16>(A, tid);
-  join_blocks<32>(A, tid);
-  join_blocks<64>(A, tid);
+  __syncthreads();
+  join_blocks<16>(A, warp, lane);
+  join_blocks<32>(A, warp, lane);
+  join_blocks<64>(A, warp, lane);
 }
 
 // ------------------------------------------------------------------ prep
@@ -227,8 +232,7 @@ TTT_DEVICE_INLINE void prep_cta(uint8_t* smem, const CUtensorMap& mapK, const CU
     }
     tc_fence_before();
     __syncthreads();
-    if (tid < 256) invert(A, tid);
-    __syncthreads();
+    invert(A, warp, lane);
     // this thread's 32 columns of a row of T
     const bool some = cg <= q4;   // the others lie above the diagonal
     float t[32];
