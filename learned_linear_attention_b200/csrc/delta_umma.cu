@@ -58,14 +58,16 @@ TTT_DEVICE_INLINE void mma_16x8x8(float (&c)[4], const uint32_t (&a)[4], const u
 
 // acc = X Y of a 16 x 16 tile: X at its first row, Y at its first column, k in
 // [k0, k1).  xd, yd: the tile's first row or column where X or Y is lower
-// triangular (what lies above the diagonal counts as zero), -1 where not.
+// triangular (what lies above the diagonal counts as zero), -1 where not.  The
+// three products have sums of their own, so that a step waits for one of them.
 TTT_DEVICE_INLINE void tile_product(const float* X, const float* Y, int k0, int k1, int xd, int yd, int lane,
                                     float (&acc)[2][4]) {
   const int g = lane >> 2, t = lane & 3;
+  float s1[2][4], s2[2][4];
 #pragma unroll
   for (int n = 0; n < 2; ++n)
 #pragma unroll
-    for (int i = 0; i < 4; ++i) acc[n][i] = 0.f;
+    for (int i = 0; i < 4; ++i) acc[n][i] = s1[n][i] = s2[n][i] = 0.f;
 #pragma unroll 2
   for (int k = k0; k < k1; k += 8) {
     uint32_t ah[4], al[4];
@@ -88,11 +90,15 @@ TTT_DEVICE_INLINE void tile_product(const float* X, const float* Y, int k0, int 
         bh[i] = v.hi;
         bl[i] = v.lo;
       }
-      mma_16x8x8(acc[n], al, bh);
-      mma_16x8x8(acc[n], ah, bl);
+      mma_16x8x8(s1[n], al, bh);
+      mma_16x8x8(s2[n], ah, bl);
       mma_16x8x8(acc[n], ah, bh);
     }
   }
+#pragma unroll
+  for (int n = 0; n < 2; ++n)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) acc[n][i] += s1[n][i] + s2[n][i];
 }
 TTT_DEVICE_INLINE void store_tile(float* C_, float sign, int lane, const float (&acc)[2][4]) {
   const int g = lane >> 2, t = lane & 3;
@@ -206,9 +212,8 @@ TTT_DEVICE_INLINE void prep_cta(uint8_t* smem, const CUtensorMap& mapK, const CU
     if (row == C - 1) a.gend[ci] = gams[row];
   }
   auto work = [&]() {
-    if (!ph.wait(&bars.load[0], 0, 1)) return;
-    const Op K{sb + SM::K, ATOM, false}, Vmn{sb + SM::V, ATOM, true};
-    if (warp == 0 && elect_one()) {
+    const Op K{sb + SM::K, ATOM, false};
+    if (warp == 0 && ph.W.wait(&bars.load[0], 0, 1) && elect_one()) {
       products<D / 16>(Prod(tmem + TM_A, K, K, 128, 128, false));
       mma_commit(&bars.mma);
     }
@@ -285,11 +290,12 @@ TTT_DEVICE_INLINE void prep_cta(uint8_t* smem, const CUtensorMap& mapK, const CU
     tmem_wait_st();
     ph.publish();
     if (warp == 0 && elect_one()) {
-      const Op gK{tb, ATOM, true}, gKlo{tb + SM::OP, ATOM, true};
+      // V and the hi plane of gam K lie side by side, as Ut and W do: one operand
+      const Op VK{sb + SM::V, ATOM, true}, gKlo{tb + SM::OP, ATOM, true};
       const uint32_t hi = tmem + TM_T, lo = hi + 64;
-      products<8>(Prod(tmem + TM_W, hi, gKlo, D, false), Prod(tmem + TM_U, lo, Vmn, D, false));
-      products<8>(Prod(tmem + TM_W, lo, gK, D, true), Prod(tmem + TM_U, hi, Vmn, D, true));
-      products<8>(Prod(tmem + TM_W, hi, gK, D, true));
+      products<8>(Prod(tmem + TM_U, lo, VK, 2 * D, false));
+      products<8>(Prod(tmem + TM_W, hi, gKlo, D, true));
+      products<8>(Prod(tmem + TM_U, hi, VK, 2 * D, true));
       mma_commit(&bars.mma);
     }
     // Ut goes out in float32, W as hi + lo; rho Ut (three planes: Hc is the
@@ -614,10 +620,9 @@ TTT_DEVICE_INLINE void out_cta(uint8_t* smem, const CUtensorMap& mapQ, const CUt
   float u[16];
   load_tile16(a.U + ci * C * D, C, row, slice * 64 + cg * 16, u);
   auto work = [&]() {
-    if (!ph.wait(&bars.load[0], 0, 1)) return;
     const Op Q{sb + SM::Q, ATOM, false}, K{sb + SM::K, ATOM, false};
     const Pair Wp{{sb + SM::W, ATOM, false}, SM::OP}, S{{sb + SM::S, SM::SA, true}, SM::SA};
-    if (warp == 0 && elect_one()) {
+    if (warp == 0 && ph.W.wait(&bars.load[0], 0, 1) && elect_one()) {
       products<D / 16>(Prod(tmem + TM_W, Wp.lo(), S.hi, 128, 64, false), Prod(tmem + TM_P, Q, K, 128, 128, false),
                        Prod(tmem + TM_Q, Q, S.lo(), 128, 64, false));
       products<D / 16>(Prod(tmem + TM_W, Wp.hi, S.lo(), 128, 64, true), Prod(tmem + TM_Q, Q, S.hi, 128, 64, true));

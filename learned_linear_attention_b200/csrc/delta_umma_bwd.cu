@@ -99,9 +99,8 @@ __global__ void __launch_bounds__(THREADS, 1)
   const uint32_t lanes = (uint32_t)(q4 * 32) << 16;
   if (cg == 1) load_gates(gates, a.g ? a.g + id.tok : nullptr, a.beta + id.tok, id.n, row);
   auto work = [&]() {
-    if (!ph.wait(&bars.load[0], 0, 1)) return;
     const Op dOmn{sb + SM::DO, ATOM, true}, Qmn{sb + SM::Q, ATOM, true};
-    if (warp == 0 && elect_one()) {
+    if (warp == 0 && ph.W.wait(&bars.load[0], 0, 1) && elect_one()) {
       products<D / 16>(Prod(tmem + TM_P, Op{sb + SM::Q, ATOM, false}, Op{sb + SM::P, ATOM, false}, 128, 128, false));
       mma_commit(&bars.mma);
     }
@@ -233,11 +232,10 @@ __global__ void __launch_bounds__(THREADS, 1)
   if (cg == 1) load_gates(gates, a.g ? a.g + id.tok : nullptr, a.beta + id.tok, id.n, row);
   int loads = 1;
   auto work = [&]() {
-    if (!ph.wait(&bars.load[0], 0, 1)) return;
     const Op K{sb + SM::K, ATOM, false};
     const Pair W{{sb + SM::T, ATOM, false}, DA * ATOM};
     const Pair S{{sb + SM::S, SM::SA, true}, SM::SA}, X{{sb + SM::X, SM::SA, true}, SM::SA};
-    if (warp == 0 && elect_one()) {
+    if (warp == 0 && ph.W.wait(&bars.load[0], 0, 1) && elect_one()) {
       products<D / 16>(Prod(tmem + TM_W, W.lo(), S.hi, 128, 64, false), Prod(tmem + TM_Z, K, S.lo(), 128, 64, false),
                        Prod(tmem + TM_X, K, X.lo(), 128, 64, false));
       products<D / 16>(Prod(tmem + TM_W, W.hi, S.lo(), 128, 64, true), Prod(tmem + TM_Z, K, S.hi, 128, 64, true),
@@ -389,8 +387,7 @@ __global__ void __launch_bounds__(THREADS, 1)
   if (cg == 1) load_gates(gates, a.g ? a.g + id.tok : nullptr, a.beta + id.tok, id.n, row);
   int loads = 1;
   auto work = [&]() {
-    if (!ph.wait(&bars.load[0], 0, 1)) return;
-    if (warp == 0 && elect_one()) {
+    if (warp == 0 && ph.W.wait(&bars.load[0], 0, 1) && elect_one()) {
       const Op dO{sb + SM::DO, ATOM, false};
       const Pair U{{sb + SM::U, ATOM, false}, DA * ATOM}, Y{{sb + SM::Y, ATOM, false}, DA * ATOM};
       const Pair S{{sb + SM::S, SM::HA, false}, DA * SM::HA}, X{{sb + SM::X, SM::HA, false}, DA * SM::HA};
@@ -405,7 +402,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                        prod(TM_UX, U.hi, X.hi, 64, true));
       mma_commit(&bars.mma);
     }
-    {   // <X1, S0> of this slice's rows, while they are still here
+    if (ph.W.wait(&bars.load[0], 0, 1)) {   // <X1, S0> of this slice's rows, while they are still here
       float acc = 0.f;
       for (int e = tid; e < 64 * D / 8; e += THREADS) {
         const int r = e / (D / 8), c = e % (D / 8) * 8;
