@@ -450,20 +450,17 @@ TTT_DEVICE_INLINE void chain_cta(uint8_t* smem, const CUtensorMap& mapM, const C
   const bool own = D == 128 || lane < 16;
   const uint32_t lanes = (uint32_t)(q4 * 32) << 16;
   const int col = slice * 64 + cg * 16;
-  int issued = 0;
-  // one thread each issues the products, the loads and the stores
-  auto fetch = [&]() {   // by thread 32: the next chunk's Mc
-    if (issued >= nch) return;
-    const int s = issued % STAGES;
+  // one elected thread each issues the products (warp 0), the loads (1) and the stores (2)
+  auto fetch = [&](int i) {   // Mc of the i-th chunk
+    if (i >= nch) return;
+    const int s = i % STAGES, z = (int)(2 * chunk(i));
     mbar_arrive_expect_tx(&full[s], SM::STAGE);
     for (int h = 0; h < 2; ++h)
-      for (int i = 0; i < DA; ++i)
-        tma_load_3d(smem + s * SM::STAGE + (h * DA + i) * SM::SA, &mapM, &full[s], 64 * i, 0,
-                    (int)(2 * chunk(issued) + h));
-    ++issued;
+      for (int k = 0; k < DA; ++k)
+        tma_load_3d(smem + s * SM::STAGE + (h * DA + k) * SM::SA, &mapM, &full[s], 64 * k, 0, z + h);
   };
-  if (tid == 32)
-    for (int s = 0; s < STAGES; ++s) fetch();
+  if (warp == 1 && elect_one())
+    for (int i = 0; i < STAGES; ++i) fetch(i);
   float x[16];
 #pragma unroll
   for (int j = 0; j < 16; j += 4) {
@@ -494,29 +491,27 @@ TTT_DEVICE_INLINE void chain_cta(uint8_t* smem, const CUtensorMap& mapM, const C
   e = a.gend[chunk(0)];
   // One CTA barrier a chunk: it publishes X and tells whether every thread saw
   // the last product complete.
-  bool ok = true;
+  bool ok = warp != 0 || ph.W.wait(&full[0], 0, 1);
+  int fetched = STAGES;   // loads issued, no more than nch
   for (int c = 0; c < nch; ++c) {
     const uint32_t xo = SM::X + (c & 1) * 2 * SM::SA, xb = sb + xo;
     put_x(xb);
     fence_async_smem();
     tc_fence_before();
-    if (tid == 64) bulk_wait_read();   // behind this barrier the other copy may be written again
+    if (warp == 2 && elect_one()) bulk_wait_read();   // behind this barrier the other copy may be written again
     if (!named_bar_all(1, THREADS, ok)) break;
     tc_fence_after();
     if (warp == 0) {
-      const int s = c % STAGES;
-      if (ph.W.wait(&full[s], (c / STAGES) & 1, 1) && elect_one()) {
+      if (ok && elect_one()) {
         const Op X{xb, SM::SA, true}, Xlo{xb + SM::SA, SM::SA, true};
-        const uint32_t m = sb + s * SM::STAGE, mlo = m + DA * SM::SA;
+        const uint32_t m = sb + c % STAGES * SM::STAGE, mlo = m + DA * SM::SA;
         products<D / 16>(Prod(tmem, Op{mlo, SM::SA, rev}, X, D, 64, false));
         products<D / 16>(Prod(tmem, Op{m, SM::SA, rev}, Xlo, D, 64, true));
         products<D / 16>(Prod(tmem, Op{m, SM::SA, rev}, X, D, 64, true));
         mma_commit(mma);
       }
       __syncwarp();
-    } else if (tid == 32) {
-      if (c > 0) fetch();   // into the stage that the last chunk's product has read
-    } else if (tid == 64) {   // the same copy is chunk c's border state
+    } else if (warp == 2 && elect_one()) {   // the same copy is chunk c's border state
       for (int h = 0; h < 2; ++h)
         tma_store_3d(rev ? &mapXr : &mapXf, smem + xo + h * SM::SA, 64 * slice, 0, (int)(2 * chunk(c) + h));
       bulk_commit();
@@ -532,7 +527,11 @@ TTT_DEVICE_INLINE void chain_cta(uint8_t* smem, const CUtensorMap& mapM, const C
       load_h(c + 1, h);
       e = a.gend[chunk(c + 1)];
     }
-    ok = ph.W.wait(mma, (uint32_t)c & 1u, 2);
+    // the next chunk's Mc, under this one's product
+    if (warp == 0 && c + 1 < nch) ok = ph.W.wait(&full[(c + 1) % STAGES], ((c + 1) / STAGES) & 1, 1);
+    ok = ph.W.wait(mma, (uint32_t)c & 1u, 2) && ok;
+    if (warp == 1 && ok && elect_one()) fetch(c + STAGES);   // into the stage that this product has read
+    if (ok) ++fetched;
     __syncwarp();
     tc_fence_after();
     float d[16];
@@ -547,9 +546,10 @@ TTT_DEVICE_INLINE void chain_cta(uint8_t* smem, const CUtensorMap& mapM, const C
     for (int j = 0; j < 16; j += 4)
       *reinterpret_cast<float4*>(dst + j) = make_float4(x[j], x[j + 1], x[j + 2], x[j + 3]);
   }
-  if (tid == 64) bulk_wait_all();
-  if (tid == 32 && ph.W.aborted())
-    for (int i = max(0, issued - STAGES); i < issued; ++i) ph.W.drain(&full[i % STAGES], (i / STAGES) & 1);
+  if (warp == 2 && elect_one()) bulk_wait_all();   // the same thread: an election has one outcome
+  if (warp == 1 && ph.W.aborted())
+    for (int i = max(0, fetched - STAGES); i < min(fetched, nch); ++i)
+      ph.W.drain(&full[i % STAGES], (i / STAGES) & 1);
   if (tid == 0 && ph.W.aborted()) {
     mma_commit(mma);
     ph.W.drain(mma, 0);
@@ -779,11 +779,13 @@ int chain_launch(const DeltaLaunch& p, const float* gend, const __nv_bfloat16* M
   return cudaGetLastError() == cudaSuccess ? 0 : -1;
 }
 
-// Chunks of a slab: an eighth of the sequence, or what gives the preparing
-// CTAs two rounds on the device, if that is more; at least four chunks.
+// Chunks of a slab: a sixth of the sequence, or what gives the preparing CTAs
+// two rounds on the device, if that is more; at least four chunks.  (64 heads of
+// 64, 32K tokens: 4 slabs 1755 us, 6 1784, 8 1828, 16 1914; the workspace is
+// three slabs.)
 int slab_chunks(int BH, int nch, int D, int sms) {
   const int rounds2 = (2 * sms * (D == 64 ? 2 : 1) + BH - 1) / BH;
-  return std::min(nch, std::max({(nch + 7) / 8, rounds2, 4}));
+  return std::min(nch, std::max({(nch + 5) / 6, rounds2, 4}));
 }
 
 template <int D>
