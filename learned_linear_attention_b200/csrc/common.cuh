@@ -101,6 +101,11 @@ struct Waiter {
       }
     }
   }
+  // The same for a whole warp, whose lanes get one answer (a lane that gave up
+  // alone would be missed by the warp's next collective instruction).
+  TTT_DEVICE_INLINE bool wait_warp(uint64_t* bar, uint32_t parity, uint32_t site) const {
+    return __all_sync(0xffffffffu, wait(bar, parity, site)) != 0;
+  }
   // Wait that ignores the abort flag (used while draining copies in flight);
   // still bounded by the timeout.
   TTT_DEVICE_INLINE bool drain(uint64_t* bar, uint32_t parity) const {
@@ -187,6 +192,15 @@ TTT_DEVICE_INLINE void tma_load_3d(void* dst, const CUtensorMap* m, uint64_t* ba
       "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
       " [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(smem_u32(dst)),
       "l"(reinterpret_cast<uint64_t>(m)), "r"(smem_u32(bar)), "r"(x), "r"(y), "r"(z)
+      : "memory");
+}
+
+// `bytes` contiguous bytes (a multiple of 16, both sides 16-byte aligned).
+TTT_DEVICE_INLINE void bulk_load_1d(void* dst, const void* src, uint32_t bytes, uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+          smem_u32(dst)),
+      "l"(src), "r"(bytes), "r"(smem_u32(bar))
       : "memory");
 }
 

@@ -213,7 +213,7 @@ TTT_DEVICE_INLINE void prep_cta(uint8_t* smem, const CUtensorMap& mapK, const CU
   }
   auto work = [&]() {
     const Op K{sb + SM::K, ATOM, false};
-    if (warp == 0 && ph.W.wait(&bars.load[0], 0, 1) && elect_one()) {
+    if (warp == 0 && ph.W.wait_warp(&bars.load[0], 0, 1) && elect_one()) {
       products<D / 16>(Prod(tmem + TM_A, K, K, 128, 128, false));
       mma_commit(&bars.mma);
     }
@@ -390,9 +390,16 @@ TTT_DEVICE_INLINE void prep_cta(uint8_t* smem, const CUtensorMap& mapK, const CU
 
 // ------------------------------------------------------------------ chain
 // X <- e_c X + H_c + Mc X over the chunks of one head and 64 value columns
-// (backward: Mc^T, from the last chunk); X in float32 registers (16 values a
-// thread), its hi + lo copy in shared memory as the operand of the next
-// chunk's product and in the workspace as the chunk's border state.
+// (backward: Mc^T, from the last chunk); X in float32 registers, its hi + lo
+// copy in shared memory as the operand of the chunk's product and, by TMA, in
+// the workspace as its border state.
+//
+// Bound by latency, a chunk after another, so the work is split by warps that
+// meet at mbarriers and nowhere else: 0 issues the products, 1 the loads, 2
+// the stores, 4 to 11 hold X (32 columns of a row a thread; the others rest).
+// While the tensor core works, those add e X + H.  With sixteen warps that did
+// everything between two CTA barriers, the warps beside the issuing ones
+// were last to every barrier.
 struct ChainArgs {
   const float* gend;
   DeltaChain dir[2];       // forward, backward
@@ -403,24 +410,28 @@ struct ChainArgs {
 
 template <int D>
 struct ChainSmem {
-  static constexpr int STAGES = D == 64 ? 4 : 2;
+  static constexpr int MS = 2, HS = D == 64 ? 2 : 1;      // slots of Mc and of H
   static constexpr uint32_t SA = D * 128;                 // bytes of a [D][64] atom
-  static constexpr uint32_t STAGE = 2 * (D / 64) * SA;    // Mc hi, lo
-  static constexpr uint32_t X = STAGES * STAGE;           // two of [hi, lo], in turn
+  static constexpr uint32_t M = 0, MB = 2 * (D / 64) * SA;   // Mc hi, lo
+  static constexpr uint32_t H = MS * MB, HB = D * 64 * 4;
+  static constexpr uint32_t X = H + HS * HB;              // two of [hi, lo], in turn
   static constexpr uint32_t BAR = X + 4 * SA;
-  static constexpr uint32_t TOTAL = BAR + 128;
+  static constexpr uint32_t TOTAL = BAR + 256;
+};
+// Every barrier belongs to a slot, which is filled again only behind the wait
+// of its reader: nobody can be a phase behind without being noticed.
+struct ChainBars {
+  uint64_t m_full[2], m_free[2], h_full[2], h_free[2], x_ready[2], x_free[2], mma, fin;
+  uint32_t tmem, abort;
 };
 
 template <int D>
 TTT_DEVICE_INLINE void chain_cta(uint8_t* smem, const CUtensorMap& mapM, const CUtensorMap& mapXf,
                                  const CUtensorMap& mapXr, const ChainArgs& a, unsigned block) {
   using SM = ChainSmem<D>;
-  constexpr int DA = D / 64, STAGES = SM::STAGES;
+  constexpr int DA = D / 64, MS = SM::MS, HS = SM::HS, XWARPS = 8;
   constexpr uint32_t TM_COLS = 64;
-  uint64_t* full = reinterpret_cast<uint64_t*>(smem + SM::BAR);
-  uint64_t* mma = full + STAGES;
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(mma + 1);
-  uint32_t* abort_flag = tmem_slot + 1;
+  ChainBars& bars = *reinterpret_cast<ChainBars*>(smem + SM::BAR);
   const int tid = threadIdx.x, warp = warp_index(), lane = tid & 31;
   const int slice = block % DA, nch = a.slab.len;
   const bool rev = a.first + block / (DA * a.BH) == 1;
@@ -431,129 +442,148 @@ TTT_DEVICE_INLINE void chain_cta(uint8_t* smem, const CUtensorMap& mapM, const C
   auto chunk = [&](int i) { return c0 + (rev ? nch - 1 - i : i); };
 
   if (tid == 0) {
-    for (int s = 0; s < STAGES; ++s) mbar_init(&full[s], 1);
-    mbar_init(mma, 1);
-    *abort_flag = 0;
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&bars.m_full[i], 1);
+      mbar_init(&bars.m_free[i], 1);
+      mbar_init(&bars.h_full[i], 1);
+      mbar_init(&bars.h_free[i], XWARPS);
+      mbar_init(&bars.x_ready[i], XWARPS);
+      mbar_init(&bars.x_free[i], 1);
+    }
+    mbar_init(&bars.mma, 1);
+    mbar_init(&bars.fin, 1);
+    bars.abort = 0;
     fence_barrier_init();
   }
   if (warp == 1) {
-    tmem_alloc(tmem_slot, TM_COLS);
+    tmem_alloc(&bars.tmem, TM_COLS);
     tmem_relinquish();
   }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = __shfl_sync(0xffffffffu, *tmem_slot, 0), sb = smem_u32(smem);
-  Phase ph{Waiter{abort_flag, a.st, 1100}, mma, 0};
-  const int q4 = warp & 3, cg = warp >> 2;    // 16 columns of the slice
-  const int r = D == 64 ? q4 * 16 + lane : q4 * 32 + lane;
-  const bool own = D == 128 || lane < 16;
-  const uint32_t lanes = (uint32_t)(q4 * 32) << 16;
-  const int col = slice * 64 + cg * 16;
-  // one elected thread each issues the products (warp 0), the loads (1) and the stores (2)
-  auto fetch = [&](int i) {   // Mc of the i-th chunk
-    if (i >= nch) return;
-    const int s = i % STAGES, z = (int)(2 * chunk(i));
-    mbar_arrive_expect_tx(&full[s], SM::STAGE);
-    for (int h = 0; h < 2; ++h)
-      for (int k = 0; k < DA; ++k)
-        tma_load_3d(smem + s * SM::STAGE + (h * DA + k) * SM::SA, &mapM, &full[s], 64 * k, 0, z + h);
-  };
-  if (warp == 1 && elect_one())
-    for (int i = 0; i < STAGES; ++i) fetch(i);
-  float x[16];
-#pragma unroll
-  for (int j = 0; j < 16; j += 4) {
-    float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-    if (own && S_in != nullptr) v = *reinterpret_cast<const float4*>(S_in + (bh * D + r) * D + col + j);
-    x[j] = v.x; x[j + 1] = v.y; x[j + 2] = v.z; x[j + 3] = v.w;
-  }
-  auto put_x = [&](uint32_t xb) {   // the operand copy
-    if (!own) return;
-    uint32_t h[8], l[8];
-#pragma unroll
-    for (int i = 0; i < 8; ++i) split2(x[2 * i], x[2 * i + 1], h[i], l[i]);
-#pragma unroll
-    for (int i = 0; i < 8; i += 4) {
-      const uint32_t o = sw128_offset(r, cg * 16 + 2 * i);
-      st_shared_v4(xb + o, h[i], h[i + 1], h[i + 2], h[i + 3]);
-      st_shared_v4(xb + SM::SA + o, l[i], l[i + 1], l[i + 2], l[i + 3]);
-    }
-  };
-  auto load_h = [&](int c, float4 (&h)[4]) {
-    const float* p = H + chunk(c) * D * D + (size_t)slice * 64 * D + ((size_t)cg * 4 * D + r) * 4;
-#pragma unroll
-    for (int j = 0; j < 4; ++j) h[j] = own ? *reinterpret_cast<const float4*>(p + (size_t)j * D * 4) : make_float4(0.f, 0.f, 0.f, 0.f);
-  };
-  float4 h[4];
-  float e = 0.f;
-  load_h(0, h);
-  e = a.gend[chunk(0)];
-  // One CTA barrier a chunk: it publishes X and tells whether every thread saw
-  // the last product complete.
-  bool ok = warp != 0 || ph.W.wait(&full[0], 0, 1);
-  int fetched = STAGES;   // loads issued, no more than nch
-  for (int c = 0; c < nch; ++c) {
-    const uint32_t xo = SM::X + (c & 1) * 2 * SM::SA, xb = sb + xo;
-    put_x(xb);
-    fence_async_smem();
-    tc_fence_before();
-    if (warp == 2 && elect_one()) bulk_wait_read();   // behind this barrier the other copy may be written again
-    if (!named_bar_all(1, THREADS, ok)) break;
-    tc_fence_after();
-    if (warp == 0) {
-      if (ok && elect_one()) {
+  const uint32_t tmem = __shfl_sync(0xffffffffu, bars.tmem, 0), sb = smem_u32(smem);
+  const Waiter W{&bars.abort, a.st, 1100};
+
+  if (warp == 0) {
+    for (int c = 0; c < nch; ++c) {
+      const int s = c % MS, b = c & 1;
+      if (!W.wait_warp(&bars.m_full[s], (c / MS) & 1, 1) || !W.wait_warp(&bars.x_ready[b], (c >> 1) & 1, 2)) break;
+      tc_fence_after();
+      if (elect_one()) {
+        const uint32_t xb = sb + SM::X + b * 2 * SM::SA, m = sb + SM::M + s * SM::MB, mlo = m + DA * SM::SA;
         const Op X{xb, SM::SA, true}, Xlo{xb + SM::SA, SM::SA, true};
-        const uint32_t m = sb + c % STAGES * SM::STAGE, mlo = m + DA * SM::SA;
         products<D / 16>(Prod(tmem, Op{mlo, SM::SA, rev}, X, D, 64, false));
         products<D / 16>(Prod(tmem, Op{m, SM::SA, rev}, Xlo, D, 64, true));
         products<D / 16>(Prod(tmem, Op{m, SM::SA, rev}, X, D, 64, true));
-        mma_commit(mma);
+        mma_commit(&bars.mma);
+        mma_commit(&bars.m_free[s]);
       }
       __syncwarp();
-    } else if (warp == 2 && elect_one()) {   // the same copy is chunk c's border state
-      for (int h = 0; h < 2; ++h)
-        tma_store_3d(rev ? &mapXr : &mapXf, smem + xo + h * SM::SA, 64 * slice, 0, (int)(2 * chunk(c) + h));
-      bulk_commit();
     }
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      x[4 * j] = fmaf(e, x[4 * j], h[j].x);
-      x[4 * j + 1] = fmaf(e, x[4 * j + 1], h[j].y);
-      x[4 * j + 2] = fmaf(e, x[4 * j + 2], h[j].z);
-      x[4 * j + 3] = fmaf(e, x[4 * j + 3], h[j].w);
-    }
-    if (c + 1 < nch) {
-      load_h(c + 1, h);
-      e = a.gend[chunk(c + 1)];
-    }
-    // the next chunk's Mc, under this one's product
-    if (warp == 0 && c + 1 < nch) ok = ph.W.wait(&full[(c + 1) % STAGES], ((c + 1) / STAGES) & 1, 1);
-    ok = ph.W.wait(mma, (uint32_t)c & 1u, 2) && ok;
-    if (warp == 1 && ok && elect_one()) fetch(c + STAGES);   // into the stage that this product has read
-    if (ok) ++fetched;
+    if (elect_one()) mma_commit(&bars.fin);   // nothing in flight outlives the CTA
     __syncwarp();
-    tc_fence_after();
-    float d[16];
-    tmem_ld16(tmem + lanes + cg * 16, d);
+    W.drain(&bars.fin, 0);
+  } else if (warp == 1) {
+    int c = 0;
+    for (; c < nch; ++c) {
+      const int s = c % MS, hs = c % HS;
+      if (c >= MS && !W.wait_warp(&bars.m_free[s], (c / MS - 1) & 1, 3)) break;
+      if (elect_one()) {
+        const int z = (int)(2 * chunk(c));
+        mbar_arrive_expect_tx(&bars.m_full[s], SM::MB);
+        for (int h = 0; h < 2; ++h)
+          for (int k = 0; k < DA; ++k)
+            tma_load_3d(smem + SM::M + s * SM::MB + (h * DA + k) * SM::SA, &mapM, &bars.m_full[s], 64 * k, 0, z + h);
+      }
+      __syncwarp();
+      if (c >= HS && !W.wait_warp(&bars.h_free[hs], (c / HS - 1) & 1, 4)) break;
+      if (elect_one()) {
+        mbar_arrive_expect_tx(&bars.h_full[hs], SM::HB);
+        bulk_load_1d(smem + SM::H + hs * SM::HB, H + chunk(c) * D * D + (size_t)slice * 64 * D, SM::HB, &bars.h_full[hs]);
+      }
+      __syncwarp();
+    }
+    if (W.aborted()) {   // the loads of the last rounds, if they were issued
+      for (int i = max(0, c - MS); i <= min(c, nch - 1); ++i) W.drain(&bars.m_full[i % MS], (i / MS) & 1);
+      for (int i = max(0, c - HS); i < c; ++i) W.drain(&bars.h_full[i % HS], (i / HS) & 1);
+    }
+  } else if (warp == 2) {
+    for (int c = 0; c < nch; ++c) {
+      const int b = c & 1;
+      if (!W.wait_warp(&bars.x_ready[b], (c >> 1) & 1, 5)) break;
+      if (elect_one()) {   // chunk c's border state
+        for (int h = 0; h < 2; ++h)
+          tma_store_3d(rev ? &mapXr : &mapXf, smem + SM::X + (2 * b + h) * SM::SA, 64 * slice, 0,
+                       (int)(2 * chunk(c) + h));
+        bulk_commit();
+        bulk_wait_read();
+        mbar_arrive(&bars.x_free[b]);
+      }
+      __syncwarp();
+    }
+    if (elect_one()) bulk_wait_all();   // the same thread: an election has one outcome
+    __syncwarp();
+  } else if (warp >= 4 && warp < 4 + XWARPS) {
+    const int q4 = warp & 3, cg = (warp - 4) >> 2;    // 32 columns of the slice
+    const int r = D == 64 ? q4 * 16 + lane : q4 * 32 + lane;
+    const bool own = D == 128 || lane < 16;
+    const uint32_t lanes = (uint32_t)(q4 * 32) << 16;
+    const size_t at = (bh * D + r) * D + slice * 64 + cg * 32;
+    float x[32];
 #pragma unroll
-    for (int j = 0; j < 16; ++j) x[j] += d[j];
-  }
-  __syncthreads();
-  if (!ph.W.aborted() && own && S_out != nullptr) {
-    float* dst = S_out + (bh * D + r) * D + col;
+    for (int j = 0; j < 32; j += 4) {
+      float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (own && S_in != nullptr) v = *reinterpret_cast<const float4*>(S_in + at + j);
+      x[j] = v.x; x[j + 1] = v.y; x[j + 2] = v.z; x[j + 3] = v.w;
+    }
+    float e = a.gend[chunk(0)];
+    bool ok = true;
+    for (int c = 0; c < nch; ++c) {
+      const int b = c & 1, hs = c % HS;
+      ok = c < 2 || W.wait_warp(&bars.x_free[b], ((c >> 1) - 1) & 1, 6);
+      if (!ok) break;
+      if (own) {
+        const uint32_t xb = sb + SM::X + b * 2 * SM::SA;
 #pragma unroll
-    for (int j = 0; j < 16; j += 4)
-      *reinterpret_cast<float4*>(dst + j) = make_float4(x[j], x[j + 1], x[j + 2], x[j + 3]);
-  }
-  if (warp == 2 && elect_one()) bulk_wait_all();   // the same thread: an election has one outcome
-  if (warp == 1 && ph.W.aborted())
-    for (int i = max(0, fetched - STAGES); i < min(fetched, nch); ++i)
-      ph.W.drain(&full[i % STAGES], (i / STAGES) & 1);
-  if (tid == 0 && ph.W.aborted()) {
-    mma_commit(mma);
-    ph.W.drain(mma, 0);
-    ph.W.drain(mma, 1);
+        for (int j = 0; j < 32; j += 8) store8_split(xb, xb + SM::SA, r, cg * 32 + j, x + j);
+      }
+      fence_async_smem();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&bars.x_ready[b]);
+      ok = W.wait_warp(&bars.h_full[hs], (c / HS) & 1, 7);
+      if (!ok) break;
+      if (own) {
+        const float4* h = reinterpret_cast<const float4*>(smem + SM::H + hs * SM::HB) + cg * 8 * D + r;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          const float4 v = h[j * D];
+          x[4 * j] = fmaf(e, x[4 * j], v.x);
+          x[4 * j + 1] = fmaf(e, x[4 * j + 1], v.y);
+          x[4 * j + 2] = fmaf(e, x[4 * j + 2], v.z);
+          x[4 * j + 3] = fmaf(e, x[4 * j + 3], v.w);
+        }
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&bars.h_free[hs]);
+      if (c + 1 < nch) e = a.gend[chunk(c + 1)];
+      ok = W.wait_warp(&bars.mma, c & 1, 8);
+      if (!ok) break;
+      tc_fence_after();
+#pragma unroll
+      for (int j = 0; j < 32; j += 16) {
+        float d[16];
+        tmem_ld16(tmem + lanes + cg * 32 + j, d);
+#pragma unroll
+        for (int i = 0; i < 16; ++i) x[j + i] += d[i];
+      }
+    }
+    if (ok && own && S_out != nullptr) {
+#pragma unroll
+      for (int j = 0; j < 32; j += 4)
+        *reinterpret_cast<float4*>(S_out + at + j) = make_float4(x[j], x[j + 1], x[j + 2], x[j + 3]);
+    }
   }
   tc_fence_before();
   __syncthreads();
@@ -622,7 +652,7 @@ TTT_DEVICE_INLINE void out_cta(uint8_t* smem, const CUtensorMap& mapQ, const CUt
   auto work = [&]() {
     const Op Q{sb + SM::Q, ATOM, false}, K{sb + SM::K, ATOM, false};
     const Pair Wp{{sb + SM::W, ATOM, false}, SM::OP}, S{{sb + SM::S, SM::SA, true}, SM::SA};
-    if (warp == 0 && ph.W.wait(&bars.load[0], 0, 1) && elect_one()) {
+    if (warp == 0 && ph.W.wait_warp(&bars.load[0], 0, 1) && elect_one()) {
       products<D / 16>(Prod(tmem + TM_W, Wp.lo(), S.hi, 128, 64, false), Prod(tmem + TM_P, Q, K, 128, 128, false),
                        Prod(tmem + TM_Q, Q, S.lo(), 128, 64, false));
       products<D / 16>(Prod(tmem + TM_W, Wp.hi, S.lo(), 128, 64, true), Prod(tmem + TM_Q, Q, S.hi, 128, 64, true));

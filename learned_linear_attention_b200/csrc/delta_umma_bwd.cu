@@ -100,7 +100,7 @@ __global__ void __launch_bounds__(THREADS, 1)
   if (cg == 1) load_gates(gates, a.g ? a.g + id.tok : nullptr, a.beta + id.tok, id.n, row);
   auto work = [&]() {
     const Op dOmn{sb + SM::DO, ATOM, true}, Qmn{sb + SM::Q, ATOM, true};
-    if (warp == 0 && ph.W.wait(&bars.load[0], 0, 1) && elect_one()) {
+    if (warp == 0 && ph.W.wait_warp(&bars.load[0], 0, 1) && elect_one()) {
       products<D / 16>(Prod(tmem + TM_P, Op{sb + SM::Q, ATOM, false}, Op{sb + SM::P, ATOM, false}, 128, 128, false));
       mma_commit(&bars.mma);
     }
@@ -235,7 +235,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     const Op K{sb + SM::K, ATOM, false};
     const Pair W{{sb + SM::T, ATOM, false}, DA * ATOM};
     const Pair S{{sb + SM::S, SM::SA, true}, SM::SA}, X{{sb + SM::X, SM::SA, true}, SM::SA};
-    if (warp == 0 && ph.W.wait(&bars.load[0], 0, 1) && elect_one()) {
+    if (warp == 0 && ph.W.wait_warp(&bars.load[0], 0, 1) && elect_one()) {
       products<D / 16>(Prod(tmem + TM_W, W.lo(), S.hi, 128, 64, false), Prod(tmem + TM_Z, K, S.lo(), 128, 64, false),
                        Prod(tmem + TM_X, K, X.lo(), 128, 64, false));
       products<D / 16>(Prod(tmem + TM_W, W.hi, S.lo(), 128, 64, true), Prod(tmem + TM_Z, K, S.hi, 128, 64, true),
@@ -278,7 +278,7 @@ __global__ void __launch_bounds__(THREADS, 1)
         tma_store_3d(&mapU, smem + SM::U + h * ATOM, 64 * id.slice, 0, (int)(2 * id.ci + h));
       bulk_commit();
     }
-    if (warp == 0 && ph.W.wait(&bars.load[1], 0, 3) && elect_one()) {
+    if (warp == 0 && ph.W.wait_warp(&bars.load[1], 0, 3) && elect_one()) {
       const Pair Tt{{sb + SM::T, ATOM, true}, 2 * ATOM}, dU{{sb + SM::Y, ATOM, true}, ATOM};
       products<8>(Prod(tmem + TM_Y, Tt.lo(), dU.hi, 128, 64, false));
       products<8>(Prod(tmem + TM_Y, Tt.hi, dU.lo(), 128, 64, true));
@@ -387,7 +387,7 @@ __global__ void __launch_bounds__(THREADS, 1)
   if (cg == 1) load_gates(gates, a.g ? a.g + id.tok : nullptr, a.beta + id.tok, id.n, row);
   int loads = 1;
   auto work = [&]() {
-    if (warp == 0 && ph.W.wait(&bars.load[0], 0, 1) && elect_one()) {
+    if (warp == 0 && ph.W.wait_warp(&bars.load[0], 0, 1) && elect_one()) {
       const Op dO{sb + SM::DO, ATOM, false};
       const Pair U{{sb + SM::U, ATOM, false}, DA * ATOM}, Y{{sb + SM::Y, ATOM, false}, DA * ATOM};
       const Pair S{{sb + SM::S, SM::HA, false}, DA * SM::HA}, X{{sb + SM::X, SM::HA, false}, DA * SM::HA};
@@ -402,7 +402,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                        prod(TM_UX, U.hi, X.hi, 64, true));
       mma_commit(&bars.mma);
     }
-    if (ph.W.wait(&bars.load[0], 0, 1)) {   // <X1, S0> of this slice's rows, while they are still here
+    if (ph.W.wait_warp(&bars.load[0], 0, 1)) {   // <X1, S0> of this slice's rows, while they are still here
       float acc = 0.f;
       for (int e = tid; e < 64 * D / 8; e += THREADS) {
         const int r = e / (D / 8), c = e % (D / 8) * 8;
@@ -441,7 +441,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     }
     ph.publish();
     const Op K{sb + SM::Y, ATOM, false};
-    if (warp == 0 && ph.W.wait(&bars.load[1], 0, 3) && elect_one()) {
+    if (warp == 0 && ph.W.wait_warp(&bars.load[1], 0, 3) && elect_one()) {
       products<D / 16>(Prod(tmem + TM_P, K, K, 128, 128, false));
       mma_commit(&bars.mma);
     }
