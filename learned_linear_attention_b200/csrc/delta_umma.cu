@@ -196,7 +196,7 @@ TTT_DEVICE_INLINE void prep_cta(uint8_t* smem, const CUtensorMap& mapK, const CU
   const ChunkId id(block, 1, a.slab, a.N);
   const size_t ci = id.ci;
   const uint32_t sb = smem_u32(smem);
-  const uint32_t tmem = cta_begin(bars, TM_COLS, tid, [&]() {
+  const uint32_t tmem = cta_begin(bars, TM_COLS, warp, [&]() {
     mbar_arrive_expect_tx(&bars.load[0], 2 * SM::OP);
     for (int i = 0; i < DA; ++i) {
       tma_load_3d(smem + SM::K + i * ATOM, &mapK, &bars.load[0], 64 * i, id.t0, (int)id.bh);
@@ -385,7 +385,7 @@ TTT_DEVICE_INLINE void prep_cta(uint8_t* smem, const CUtensorMap& mapK, const CU
     }
   };
   work();
-  cta_end(bars, ph, 1, tmem, TM_COLS, tid);
+  cta_end(bars, ph, 1, tmem, TM_COLS, warp);
 }
 
 // ------------------------------------------------------------------ chain
@@ -629,7 +629,7 @@ TTT_DEVICE_INLINE void out_cta(uint8_t* smem, const CUtensorMap& mapQ, const CUt
   const int slice = id.slice;
   const size_t ci = id.ci;
   const uint32_t sb = smem_u32(smem);
-  const uint32_t tmem = cta_begin(bars, TM_COLS, tid, [&]() {
+  const uint32_t tmem = cta_begin(bars, TM_COLS, warp, [&]() {
     mbar_arrive_expect_tx(&bars.load[0], 4 * SM::OP + 2 * SM::SA);
     for (int i = 0; i < DA; ++i) {
       tma_load_3d(smem + SM::Q + i * ATOM, &mapQ, &bars.load[0], 64 * i, id.t0, (int)id.bh);
@@ -719,7 +719,7 @@ TTT_DEVICE_INLINE void out_cta(uint8_t* smem, const CUtensorMap& mapQ, const CUt
     }
   };
   work();
-  cta_end(bars, ph, 1, tmem, TM_COLS, tid);
+  cta_end(bars, ph, 1, tmem, TM_COLS, warp);
 }
 
 // ------------------------------------------------------------------ kernels

@@ -286,11 +286,12 @@ struct Bars {
   uint32_t tmem, abort;
 };
 // Barriers and `cols` TMEM columns, before the first phase; returns the TMEM
-// base.  Thread 0 issues the first loads (on load[0]) as soon as the barriers
-// stand.
+// base.  An elected thread of warp 0 issues the first loads (on load[0]) as
+// soon as the barriers stand (elected: an address that the whole warp knows
+// costs a TMA instruction a few cycles, one in a thread's registers about 100).
 template <typename F>
-TTT_DEVICE_INLINE uint32_t cta_begin(Bars& b, uint32_t cols, int tid, F loads) {
-  if (tid == 0) {
+TTT_DEVICE_INLINE uint32_t cta_begin(Bars& b, uint32_t cols, int warp, F loads) {
+  if (warp == 0 && elect_one()) {
     mbar_init(&b.load[0], 1);
     mbar_init(&b.load[1], 1);
     mbar_init(&b.mma, 1);
@@ -298,7 +299,7 @@ TTT_DEVICE_INLINE uint32_t cta_begin(Bars& b, uint32_t cols, int tid, F loads) {
     fence_barrier_init();
     loads();
   }
-  if (tid >> 5 == 1) {
+  if (warp == 1) {
     tmem_alloc(&b.tmem, cols);
     tmem_relinquish();
   }
@@ -308,20 +309,20 @@ TTT_DEVICE_INLINE uint32_t cta_begin(Bars& b, uint32_t cols, int tid, F loads) {
   return __shfl_sync(0xffffffffu, b.tmem, 0);
 }
 // After the last phase, or an aborted one: nothing in flight outlives the CTA.
-// `loads` counts the load barriers in use (thread 0's).
-TTT_DEVICE_INLINE void cta_end(Bars& b, const Phase& ph, int loads, uint32_t tmem, uint32_t cols, int tid) {
-  if (tid == 0) {
-    if (ph.W.aborted()) {
-      for (int i = 0; i < loads; ++i) ph.W.drain(&b.load[i], 0);
-      mma_commit(&b.mma);
-      ph.W.drain(&b.mma, 0);
-      ph.W.drain(&b.mma, 1);
-    }
-    bulk_wait_all();
+// `loads` counts the load barriers in use.  Warp 0's elected thread issues the
+// products, warp 1's the stores: an election has one outcome, so the threads
+// that wait here are the same ones.
+TTT_DEVICE_INLINE void cta_end(Bars& b, const Phase& ph, int loads, uint32_t tmem, uint32_t cols, int warp) {
+  if (warp == 0 && ph.W.aborted() && elect_one()) {
+    for (int i = 0; i < loads; ++i) ph.W.drain(&b.load[i], 0);
+    mma_commit(&b.mma);
+    ph.W.drain(&b.mma, 0);
+    ph.W.drain(&b.mma, 1);
   }
+  if (warp == 1 && elect_one()) bulk_wait_all();
   tc_fence_before();
   __syncthreads();
-  if (tid >> 5 == 1) {
+  if (warp == 1) {
     tc_fence_after();
     tmem_dealloc(tmem, cols);
   }

@@ -84,7 +84,7 @@ __global__ void __launch_bounds__(THREADS, 1)
   const int tid = threadIdx.x, warp = warp_index(), lane = tid & 31;
   const ChunkId id(blockIdx.x, DA, Slab{0, a.nch, 0}, a.N);
   const uint32_t sb = smem_u32(smem);
-  const uint32_t tmem = cta_begin(bars, TM_COLS, tid, [&]() {
+  const uint32_t tmem = cta_begin(bars, TM_COLS, warp, [&]() {
     mbar_arrive_expect_tx(&bars.load[0], 4 * DA * ATOM + ATOM);
     for (int i = 0; i < DA; ++i) {
       tma_load_3d(smem + SM::Q + i * ATOM, &mapQ, &bars.load[0], 64 * i, id.t0, (int)id.bh);
@@ -160,7 +160,7 @@ __global__ void __launch_bounds__(THREADS, 1)
       products<8>(Prod(t, Qmn, G.hi, D, 64, true));
       mma_commit(&bars.mma);
     }
-    if (tid == 0) {
+    if (warp == 1 && elect_one()) {
       for (int h = 0; h < 2; ++h)
         tma_store_3d(&mapY, smem + SM::P + h * ATOM, 64 * id.slice, 0, (int)(2 * id.ci + h));
       bulk_commit();
@@ -172,7 +172,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     if (D == 128 || lane < 16) store_tile16(a.H + id.ci * D * D, D, r, id.slice * 64 + cg * 16, h);
   };
   work();
-  cta_end(bars, ph, 1, tmem, TM_COLS, tid);
+  cta_end(bars, ph, 1, tmem, TM_COLS, warp);
 }
 
 // ------------------------------------------------------------------ values
@@ -212,7 +212,7 @@ __global__ void __launch_bounds__(THREADS, 1)
   const int tid = threadIdx.x, warp = warp_index(), lane = tid & 31;
   const ChunkId id(blockIdx.x, DA, Slab{0, a.nch, 0}, a.N);
   const uint32_t sb = smem_u32(smem);
-  const uint32_t tmem = cta_begin(bars, TM_COLS, tid, [&]() {
+  const uint32_t tmem = cta_begin(bars, TM_COLS, warp, [&]() {
     mbar_arrive_expect_tx(&bars.load[0], 3 * DA * ATOM + 2 * ATOM + 4 * SM::SA);
     for (int i = 0; i < DA; ++i) {
       tma_load_3d(smem + SM::K + i * ATOM, &mapK, &bars.load[0], 64 * i, id.t0, (int)id.bh);
@@ -244,7 +244,7 @@ __global__ void __launch_bounds__(THREADS, 1)
       mma_commit(&bars.mma);
     }
     if (!ph.mma_done(2)) return;
-    if (tid == 0) {   // T takes W's place
+    if (warp == 2 && elect_one()) {   // T takes W's place
       mbar_arrive_expect_tx(&bars.load[1], 4 * ATOM);
       for (int h = 0; h < 2; ++h)
         for (int i = 0; i < 2; ++i)
@@ -273,7 +273,7 @@ __global__ void __launch_bounds__(THREADS, 1)
       }
     }
     ph.publish();
-    if (tid == 0) {
+    if (warp == 1 && elect_one()) {
       for (int h = 0; h < 2; ++h)
         tma_store_3d(&mapU, smem + SM::U + h * ATOM, 64 * id.slice, 0, (int)(2 * id.ci + h));
       bulk_commit();
@@ -314,7 +314,7 @@ __global__ void __launch_bounds__(THREADS, 1)
       red[cg * C + row] = acc;
     }
     ph.publish();
-    if (tid == 0) {
+    if (warp == 1 && elect_one()) {
       for (int h = 0; h < 2; ++h)
         tma_store_3d(&mapY, smem + SM::Y + h * ATOM, 64 * id.slice, 0, (int)(2 * id.ci + h));
       bulk_commit();
@@ -322,7 +322,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     if (cg == 0 && row < id.n) a.bpart[id.slice * a.tokens + id.tok + row] = row_total(red, row);
   };
   work();
-  cta_end(bars, ph, loads, tmem, TM_COLS, tid);
+  cta_end(bars, ph, loads, tmem, TM_COLS, warp);
 }
 
 // ------------------------------------------------------------------ keys
@@ -368,7 +368,7 @@ __global__ void __launch_bounds__(THREADS, 1)
   const int tid = threadIdx.x, warp = warp_index(), lane = tid & 31;
   const ChunkId id(blockIdx.x, DA, Slab{0, a.nch, 0}, a.N);
   const uint32_t sb = smem_u32(smem);
-  const uint32_t tmem = cta_begin(bars, TM_COLS, tid, [&]() {
+  const uint32_t tmem = cta_begin(bars, TM_COLS, warp, [&]() {
     mbar_arrive_expect_tx(&bars.load[0], 5 * DA * ATOM + 4 * DA * SM::HA);
     for (int i = 0; i < DA; ++i) {
       tma_load_3d(smem + SM::DO + i * ATOM, &mapD, &bars.load[0], 64 * i, id.t0, (int)id.bh);
@@ -417,11 +417,13 @@ __global__ void __launch_bounds__(THREADS, 1)
       if (lane == 0) xs[warp] = acc;
     }
     if (!ph.mma_done(2)) return;
-    if (tid == 0) {   // K and Q take Y's place
+    if (warp == 2 && elect_one()) {   // K and Q take Y's place
       mbar_arrive_expect_tx(&bars.load[1], (DA + 1) * ATOM);
       for (int i = 0; i < DA; ++i)
         tma_load_3d(smem + SM::Y + i * ATOM, &mapK, &bars.load[1], 64 * i, id.t0, (int)id.bh);
       tma_load_3d(smem + SM::Y + DA * ATOM, &mapQ, &bars.load[1], 64 * id.slice, id.t0, (int)id.bh);
+    }
+    if (tid == 96) {
       float acc = 0.f;
       for (int w = 0; w < THREADS / 32; ++w) acc += xs[w];
       a.xpart[id.slice * a.chunks + id.ci] = acc;
@@ -532,7 +534,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     }
   };
   work();
-  cta_end(bars, ph, loads, tmem, TM_COLS, tid);
+  cta_end(bars, ph, loads, tmem, TM_COLS, warp);
 }
 
 // ------------------------------------------------------------------ gates
