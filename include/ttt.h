@@ -187,7 +187,8 @@ int ttt_linear_bwd(const ttt_linear_desc* desc, const void* q, const void* k, co
  * some 100 tokens: every derived operand there is carried as bf16 hi + lo
  * (about 17 significant bits; three planes in what S and dS0 are made of) with
  * float32 sums, and the state stays float32.  Every other type and size runs
- * in float32 on CUDA cores, four tokens at a time.
+ * in float32 on CUDA cores, four tokens at a time.  An infinity or NaN in a
+ * token reaches the tokens behind it, and on tensor cores all of its chunk.
  * ---------------------------------------------------------------------- */
 typedef struct {
   int B, H, N;          /* batch, heads, tokens (N >= 0)                     */

@@ -294,7 +294,11 @@ __global__ void __launch_bounds__(THREADS)
         }
         if (out != nullptr) {
           const float4 c = *reinterpret_cast<const float4*>(st.qk[4 * b + lt]);
-          const float o = fmaf(c.x, u[0], fmaf(c.y, u[1], fmaf(c.z, u[2], fmaf(c.w, u[3], st.A[4 * b + lt] * mine))));
+          // (selected, not multiplied by zero: a later token may hold NaN)
+          float o = fmaf(c.x, u[0], st.A[4 * b + lt] * mine);
+          o = lt >= 1 ? fmaf(c.y, u[1], o) : o;
+          o = lt >= 2 ? fmaf(c.z, u[2], o) : o;
+          o = lt >= 3 ? fmaf(c.w, u[3], o) : o;
           keep[ub] = scale * o;
         } else {
           keep[ub] = lt == 0 ? e[0] : lt == 1 ? e[1] : lt == 2 ? e[2] : e[3];

@@ -299,7 +299,7 @@ Shape norm_shape(int D, int per_vec) {
   const int nv = (D + per_vec - 1) / per_vec, most = per_vec == 4 ? 128 : 64;
   int T = 4;
   while (T < 32 && T < nv) T *= 2;
-  while (T < 256 && nv > most && T < nv) T *= 2;
+  while (T < 256 && nv > most && T < nv) T *= T == 32 ? 4 : 2;
   int V = 1;
   while (T * V < nv) V *= 2;
   return {T, V};
@@ -321,7 +321,7 @@ int launch_t(const NormArgs& a, int grid, size_t smem, cudaStream_t stream) {
     return cudaGetLastError() == cudaSuccess ? 0 : -1;                                 \
   }
   TTT_NORM(4, 1) TTT_NORM(8, 1) TTT_NORM(16, 1) TTT_NORM(32, 1) TTT_NORM(32, 2) TTT_NORM(32, 4)
-  TTT_NORM(64, 1) TTT_NORM(128, 1)
+  TTT_NORM(128, 1)
   TTT_NORM(256, 1) TTT_NORM(256, 2) TTT_NORM(256, 4) TTT_NORM(256, 8)
 #undef TTT_NORM
   return -1;

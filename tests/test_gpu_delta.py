@@ -206,6 +206,46 @@ def test_long_sequence(cuda_device, d):
     p.check_bwd(p.bwd())
 
 
+@pytest.mark.parametrize("d,N", [(64, 2700), (128, 2600)])
+def test_many_heads_are_the_heads_one_by_one(cuda_device, d, N):
+    """64 heads go over the sequence in several slabs that share the workspace in
+    turn (their lengths go by the number of heads), one head in one: the same bits."""
+    p = Problem(1, 1, N, d, d, "bf16", seed=5)
+    B, H = 2, 32
+    r = torch.Generator(device="cuda").manual_seed(7)
+    shift = torch.randint(0, N, (B * H,), generator=r, device="cuda").tolist()
+    many = {n: torch.stack([t[0, 0].roll(s, 0) for s in shift]).view(B, H, *t.shape[2:]) for n, t in p.dev.items()}
+    S = torch.randn(B, H, d, d, generator=r, device="cuda")
+    one = [0, 31, 63]
+    S_one = [S.view(-1, d, d)[i].clone() for i in one]
+    o = torch.full_like(many["v"], float("nan"))
+    desc = T.make_delta_desc(B, H, N, d, d)
+    ws = T.alloc_workspace(T.ttt_delta_workspace_bytes(desc))
+    T.ttt_delta_fwd(desc, many["q"], many["k"], many["v"], many["g"], many["beta"], S, o, ws)
+    assert T.ttt_check_device_status(ws) == T.TTT_OK
+    desc = T.make_delta_desc(1, 1, N, d, d)
+    ws = T.alloc_workspace(T.ttt_delta_workspace_bytes(desc))
+    for i, s in zip(one, S_one):
+        x = {n: t.flatten(0, 1)[i].clone() for n, t in many.items()}   # (aligned)
+        got = torch.empty_like(x["v"])
+        T.ttt_delta_fwd(desc, x["q"], x["k"], x["v"], x["g"], x["beta"], s, got, ws)
+        assert torch.equal(got, o.flatten(0, 1)[i]) and torch.equal(s, S.view(-1, d, d)[i])
+
+
+@pytest.mark.parametrize("dt,d,first", [("f32", 24, 189), ("bf16", 40, 189), ("bf16", 64, 128), ("bf16", 128, 128)])
+@pytest.mark.parametrize("bad", [float("nan"), float("inf")])
+def test_a_bad_value_stays_behind(cuda_device, dt, d, first, bad):
+    """NaN or infinity in token 189 of one head: nothing before it changes (on
+    tensor cores, nothing before its chunk), nor any other head."""
+    p = Problem(1, 2, 300, d, d, dt)
+    want = p.fwd()
+    p.dev["v"][0, 1, 189, 3] = bad
+    got = p.fwd()
+    assert torch.equal(got[0][0, 0], want[0][0, 0]) and torch.equal(got[1][0, 0], want[1][0, 0])
+    assert torch.equal(got[0][0, 1, :first], want[0][0, 1, :first])
+    assert not torch.isfinite(got[0][0, 1, 189:]).all() and not torch.isfinite(got[1][0, 1]).all()
+
+
 def test_empty_sequence(cuda_device):
     for dt, d in (("f32", 24), ("bf16", 64)):
         p = Problem(1, 2, 0, d, d, dt)

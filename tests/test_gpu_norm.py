@@ -59,6 +59,12 @@ def test_against_oracle(cuda_device, rows, D, dt, kind, gate, w, res):
     check(make(rows, D, dt, w, gate, res), rows, D, dt, kind, gate)
 
 
+@pytest.mark.parametrize("dt", ["f32", "bf16"])
+@pytest.mark.parametrize("D", [248, 256, 264, 504, 512, 520, 1016, 1032, 2056, 4104])
+def test_widths_around_the_borders_of_a_rows_threads(cuda_device, D, dt):
+    check(make(301, D, dt, True, "silu", True), 301, D, dt, "rms", "silu")
+
+
 def test_many_rows(cuda_device):
     check(make(20011, 128, "bf16", True, "silu", True), 20011, 128, "bf16", "rms", "silu")
 
