@@ -281,6 +281,14 @@ static int check_ranges(const Range* in, int n_in, const Range* out, int n_out) 
   return TTT_OK;
 }
 
+// A refused launch leaves the runtime's last error set; the caller's next check
+// must not find it.
+static int launched(int r) {
+  if (r == 0) return TTT_OK;
+  cudaGetLastError();
+  return TTT_ERR_CUDA;
+}
+
 static bool dtype_ok(int t) { return t == TTT_F32 || t == TTT_BF16; }
 static size_t dtype_bytes(int t) { return t == TTT_BF16 ? 2 : 4; }
 
@@ -345,7 +353,7 @@ int ttt_delta_fwd(const ttt_delta_desc* d, const void* q, const void* k, const v
   const DeltaLaunch L = delta_launch(d, q, k, v, g, beta, S, out, ws);
   const int r = delta_umma(d, false) ? launch_delta_umma(L, as_stream(stream))
                                      : launch_delta_rec(L, as_stream(stream));
-  return r == 0 ? TTT_OK : TTT_ERR_CUDA;
+  return launched(r);
 }
 
 int ttt_delta_bwd_workspace_bytes(const ttt_delta_desc* d, size_t* bytes) {
@@ -384,7 +392,7 @@ int ttt_delta_bwd(const ttt_delta_desc* d, const void* q, const void* k, const v
   L.ws = static_cast<uint8_t*>(ws);
   const int r = delta_umma(d, true) ? launch_delta_umma_bwd(L, as_stream(stream))
                                     : launch_delta_rec_bwd(L, as_stream(stream));
-  return r == 0 ? TTT_OK : TTT_ERR_CUDA;
+  return launched(r);
 }
 
 int ttt_delta_step(const ttt_delta_desc* d, const void* q, const void* k, const void* v,
@@ -402,7 +410,7 @@ int ttt_delta_step(const ttt_delta_desc* d, const void* q, const void* k, const 
   e = check_ranges(in, 6, o, 2);
   if (e) return e;
   const DeltaLaunch L = delta_launch(d, q, k, v, g, beta, S, out, nullptr);
-  return launch_delta_step(L, slots, n_slots, as_stream(stream)) == 0 ? TTT_OK : TTT_ERR_CUDA;
+  return launched(launch_delta_step(L, slots, n_slots, as_stream(stream)));
 }
 
 // ------------------------------------------------------------------ row norm
@@ -444,7 +452,7 @@ int ttt_norm_fwd(const ttt_norm_desc* d, const void* x, const float* w, const vo
   NormLaunch L = norm_launch(d, x, w, z);
   L.res = res;
   L.out = out;
-  return launch_norm_fwd(L, device_sms(), as_stream(stream)) == 0 ? TTT_OK : TTT_ERR_CUDA;
+  return launched(launch_norm_fwd(L, device_sms(), as_stream(stream)));
 }
 
 int ttt_norm_bwd_workspace_bytes(const ttt_norm_desc* d, size_t* bytes) {
@@ -482,7 +490,7 @@ int ttt_norm_bwd(const ttt_norm_desc* d, const void* x, const float* w, const vo
   NormLaunch L = norm_launch(d, x, w, z);
   L.dout = dout; L.dx = dx; L.dz = dz; L.dw = dw;
   L.part = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + TTT_STATUS_BYTES);
-  return launch_norm_bwd(L, device_sms(), as_stream(stream)) == 0 ? TTT_OK : TTT_ERR_CUDA;
+  return launched(launch_norm_bwd(L, device_sms(), as_stream(stream)));
 }
 
 // ------------------------------------------------------------------ delta layer

@@ -462,6 +462,8 @@ TTT_DEVICE_INLINE void chain_cta(uint8_t* smem, const CUtensorMap& mapM, const C
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
+  pdl_wait();
+  pdl_launch_dependents();
   const uint32_t tmem = __shfl_sync(0xffffffffu, bars.tmem, 0), sb = smem_u32(smem);
   const Waiter W{&bars.abort, a.st, 1100};
 
@@ -782,9 +784,11 @@ int prep_launch(const DeltaLaunch& p, const DeltaPrepOut& o, cudaStream_t stream
   const PrepArgs a{(const __nv_bfloat16*)p.g, (const __nv_bfloat16*)p.beta, o.gend, o.H, o.U, o.W, o.M, o.T,
                    p.N, Slab{0, nch, 0}, p.st};
   prof_before(K_DELTA_PREP, stream);
-  delta_prep_kernel<D><<<(unsigned)nc, THREADS, PrepSmem<D>::TOTAL, stream>>>(mk, mv, a);
+  const cudaError_t err = launch_pdl(
+      delta_prep_kernel<D>, dim3((unsigned)nc), dim3(THREADS), PrepSmem<D>::TOTAL, stream,
+      mk, mv, a);
   prof_after(K_DELTA_PREP, stream);
-  return cudaGetLastError() == cudaSuccess ? 0 : -1;
+  return err == cudaSuccess ? 0 : -1;
 }
 
 template <int D>
@@ -804,9 +808,11 @@ int chain_launch(const DeltaLaunch& p, const float* gend, const __nv_bfloat16* M
   if (rev) a.dir[1] = *rev;
   const unsigned dirs = (fwd ? 1 : 0) + (rev ? 1 : 0);
   prof_before(K_DELTA_CHAIN, stream);
-  delta_chain_kernel<D><<<dirs * (unsigned)(BH * (D / 64)), THREADS, ChainSmem<D>::TOTAL, stream>>>(mm, mf, mr, a);
+  const cudaError_t err = launch_pdl(
+      delta_chain_kernel<D>, dim3(dirs * (unsigned)(BH * (D / 64))), dim3(THREADS), ChainSmem<D>::TOTAL, stream,
+      mm, mf, mr, a);
   prof_after(K_DELTA_CHAIN, stream);
-  return cudaGetLastError() == cudaSuccess ? 0 : -1;
+  return err == cudaSuccess ? 0 : -1;
 }
 
 // Chunks of a slab: a sixth of the sequence, or what gives the preparing CTAs
@@ -859,9 +865,11 @@ int fwd_launch(const DeltaLaunch& p, cudaStream_t stream) {
       a.n_out = (unsigned)(BH * (D / 64)) * a.out.slab.len;
     }
     prof_before(K_DELTA_FWD, stream);
-    delta_fwd_kernel<D><<<a.n_chain + a.n_out + n_prep, THREADS, FwdSmem<D>::TOTAL, stream>>>(maps, a);
+    const cudaError_t err = launch_pdl(
+      delta_fwd_kernel<D>, dim3(a.n_chain + a.n_out + n_prep), dim3(THREADS), FwdSmem<D>::TOTAL, stream,
+      maps, a);
     prof_after(K_DELTA_FWD, stream);
-    if (cudaGetLastError() != cudaSuccess) return -1;
+    if (err != cudaSuccess) return -1;
   }
   return 0;
 }
@@ -869,16 +877,16 @@ int fwd_launch(const DeltaLaunch& p, cudaStream_t stream) {
 }  // namespace
 
 // Short sequences go token by token: the chunk kernels' latency is that of a
-// whole chunk and of three launches (29 us forward, 56 us backward at D = 64;
-// 36 and 67 at 128), the recurrent ones' 0.12 us a token at D = 64 and 0.19 at
-// 128 (backward 0.24 and 0.37, behind 21 and 40), times the rounds that their
+// whole chunk and of three launches (24 us forward, 48 us backward at D = 64;
+// 33 and 61 at 128), the recurrent ones' 0.12 us a token at D = 64 and 0.19 at
+// 128 (backward 0.24 and 0.37, behind 21 and 41), times the rounds that their
 // CTAs of 16 value columns take.  Forward at D = 64, 1 to 32 heads: 128 tokens
-// 18 against 30 us, 256 tokens 33 against 31.  Backward at D = 64: 128 tokens 51
-// against 57, at 128: 64 tokens 61 against 67.
+// 18 against 24 us, 256 tokens 33 against 24.  Backward at D = 64: 64 tokens 35
+// against 48, 128 tokens 51 against 48; at 128: 32 tokens 52 against 60.
 bool delta_uses_umma(int bf16, int dk, int dv, long long BH, int N, int sms, bool backward) {
   if (!bf16 || dk != dv || (dk != 64 && dk != 128)) return false;
   const double rounds = std::max(1.0, (double)BH * (dv / 16) / (1.25 * sms));
-  return N * rounds > (backward ? (dk == 64 ? 128 : 64) : 160);
+  return N * rounds > (backward ? (dk == 64 ? 112 : 48) : 160);
 }
 
 DeltaUmmaWorkspace delta_umma_layout(int BH, int N, int D, int sms) {

@@ -287,7 +287,9 @@ struct Bars {
 };
 // Barriers and `cols` TMEM columns, before the first phase; returns the TMEM
 // base.  An elected thread of warp 0 issues the first loads (on load[0]) as
-// soon as the barriers stand (elected: an address that the whole warp knows
+// soon as the barriers stand and the launch before this one is complete (every
+// kernel here is launched to start while its predecessor drains, and waits
+// before it touches global memory) (elected: an address that the whole warp knows
 // costs a TMA instruction a few cycles, one in a thread's registers about 100).
 template <typename F>
 TTT_DEVICE_INLINE uint32_t cta_begin(Bars& b, uint32_t cols, int warp, F loads) {
@@ -297,6 +299,7 @@ TTT_DEVICE_INLINE uint32_t cta_begin(Bars& b, uint32_t cols, int warp, F loads) 
     mbar_init(&b.mma, 1);
     b.abort = 0;
     fence_barrier_init();
+    pdl_wait();
     loads();
   }
   if (warp == 1) {
@@ -306,6 +309,8 @@ TTT_DEVICE_INLINE uint32_t cta_begin(Bars& b, uint32_t cols, int warp, F loads) 
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
+  pdl_wait();
+  pdl_launch_dependents();   // every CTA has its tensor memory by then
   return __shfl_sync(0xffffffffu, b.tmem, 0);
 }
 // After the last phase, or an aborted one: nothing in flight outlives the CTA.

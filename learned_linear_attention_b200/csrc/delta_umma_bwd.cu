@@ -574,6 +574,8 @@ __global__ void __launch_bounds__(C) delta_gate_grad_kernel(GateArgs a) {
   const int t0 = (int)(ci % a.nch) * C, n = min(C, a.N - t0);
   const size_t tok = bh * a.N + t0;
   const bool live = tid < n;
+  pdl_wait();
+  pdl_launch_dependents();
   float r = 0.f, w = 0.f, b = 0.f, x = 0.f;
   for (int s = 0; s < a.slices; ++s) {
     const size_t at = s * a.tokens + tok + tid;
@@ -633,27 +635,32 @@ int bwd_launch(const DeltaBwdLaunch& L, cudaStream_t stream) {
   if (launch_delta_prep(p, o, stream)) return -1;
   const unsigned grid = (unsigned)(nc * DA);
   prof_before(K_DELTA_HB, stream);
-  delta_hb_kernel<D><<<grid, THREADS, HbSmem<D>::TOTAL, stream>>>(
+  const cudaError_t e_hb = launch_pdl(
+      delta_hb_kernel<D>, dim3(grid), dim3(THREADS), HbSmem<D>::TOTAL, stream,
       mq, mk, md, mw, my, HbArgs{g, beta, f32(w.Hb), p.N, nch, p.scale, p.st});
   prof_after(K_DELTA_HB, stream);
   if (launch_delta_chain(p, o.gend, o.M, &fwd, &rev, stream)) return -1;
   prof_before(K_DELTA_VALS, stream);
-  delta_vals_kernel<D><<<grid, THREADS, ValsSmem<D>::TOTAL, stream>>>(
+  const cudaError_t e_vals = launch_pdl(
+      delta_vals_kernel<D>, dim3(grid), dim3(THREADS), ValsSmem<D>::TOTAL, stream,
       mk, mw, mu, my, mt, ms, mx,
       ValsArgs{g, beta, (const __nv_bfloat16*)p.v, o.U, (__nv_bfloat16*)L.dv, f32(w.bpart), p.N, nch, tokens, p.st});
   prof_after(K_DELTA_VALS, stream);
   prof_before(K_DELTA_KEYS, stream);
-  delta_keys_kernel<D><<<grid, THREADS, KeysSmem<D>::TOTAL, stream>>>(
+  const cudaError_t e_keys = launch_pdl(
+      delta_keys_kernel<D>, dim3(grid), dim3(THREADS), KeysSmem<D>::TOTAL, stream,
       mq, mk, md, mu, my, ms64, mx64,
       KeysArgs{g, beta, (__nv_bfloat16*)L.dq, (__nv_bfloat16*)L.dk, f32(w.rpart), f32(w.wpart), f32(w.xpart),
                f32(w.bkey), p.N, nch, tokens, nc, p.scale, p.st});
   prof_after(K_DELTA_KEYS, stream);
   prof_before(K_DELTA_GATES, stream);
-  delta_gate_grad_kernel<<<(unsigned)nc, C, 0, stream>>>(
+  const cudaError_t e_gates = launch_pdl(
+      delta_gate_grad_kernel, dim3((unsigned)nc), dim3(C), 0, stream,
       GateArgs{o.gend, f32(w.rpart), f32(w.wpart), f32(w.xpart), f32(w.bpart), f32(w.bkey),
                (__nv_bfloat16*)L.dg, (__nv_bfloat16*)L.dbeta, p.N, nch, DA, tokens, nc});
   prof_after(K_DELTA_GATES, stream);
-  return cudaGetLastError() == cudaSuccess ? 0 : -1;
+  const bool ok = e_hb == cudaSuccess && e_vals == cudaSuccess && e_keys == cudaSuccess && e_gates == cudaSuccess;
+  return ok ? 0 : -1;
 }
 
 }  // namespace
