@@ -68,14 +68,13 @@ TTT_DEVICE_INLINE void tile_product(const float* X, const float* Y, int k0, int 
   for (int n = 0; n < 2; ++n)
 #pragma unroll
     for (int i = 0; i < 4; ++i) acc[n][i] = s1[n][i] = s2[n][i] = 0.f;
-#pragma unroll 2
-  for (int k = k0; k < k1; k += 8) {
+  auto step = [&](int k, bool diag) {
     uint32_t ah[4], al[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const int r = g + (i & 1) * 8, c = k + t + (i >> 1) * 4;
       const float x = X[r * LDA + c];
-      const Tf32 v(xd >= 0 && c > xd + r ? 0.f : x);
+      const Tf32 v(diag && xd >= 0 && c > xd + r ? 0.f : x);
       ah[i] = v.hi;
       al[i] = v.lo;
     }
@@ -86,7 +85,7 @@ TTT_DEVICE_INLINE void tile_product(const float* X, const float* Y, int k0, int 
       for (int i = 0; i < 2; ++i) {
         const int r = k + t + i * 4, c = 8 * n + g;
         const float y = Y[r * LDA + c];
-        const Tf32 v(yd >= 0 && r < yd + c ? 0.f : y);
+        const Tf32 v(diag && yd >= 0 && r < yd + c ? 0.f : y);
         bh[i] = v.hi;
         bl[i] = v.lo;
       }
@@ -94,7 +93,14 @@ TTT_DEVICE_INLINE void tile_product(const float* X, const float* Y, int k0, int 
       mma_16x8x8(s2[n], ah, bl);
       mma_16x8x8(acc[n], ah, bh);
     }
-  }
+  };
+  // the 16 columns (rows) on the diagonal, then the others: at most 48
+  const int d0 = xd >= 0 ? xd : yd;
+  step(d0, true);
+  step(d0 + 8, true);
+  const int e0 = xd >= 0 ? k0 : k0 + 16, e1 = xd >= 0 ? k1 - 16 : k1;
+#pragma unroll 2
+  for (int k = e0; k < e1; k += 8) step(k, false);
 #pragma unroll
   for (int n = 0; n < 2; ++n)
 #pragma unroll
@@ -815,13 +821,16 @@ int chain_launch(const DeltaLaunch& p, const float* gend, const __nv_bfloat16* M
   return err == cudaSuccess ? 0 : -1;
 }
 
-// Chunks of a slab: a sixth of the sequence, or what gives the preparing CTAs
-// two rounds on the device, if that is more; at least four chunks.  (64 heads of
-// 64, 32K tokens: 4 slabs 1755 us, 6 1784, 8 1828, 16 1914; the workspace is
-// three slabs.)
+// Chunks of a slab: about a sixth of the sequence, and whole rounds of preparing
+// CTAs on the device (two at least; where the recurrence keeps few SMs, on the
+// others), but four chunks at least.  64 heads of 64, 32K tokens: 4 slabs 1755
+// us, 6 1784, 8 1828, 16 1914; the workspace is three slabs.  8 heads of 128,
+// 32749 tokens: slabs of 2.6 rounds 650 us, of whole ones 614.
 int slab_chunks(int BH, int nch, int D, int sms) {
-  const int rounds2 = (2 * sms * (D == 64 ? 2 : 1) + BH - 1) / BH;
-  return std::min(nch, std::max({(nch + 5) / 6, rounds2, 4}));
+  const int all = sms * (D == 64 ? 2 : 1), chain = BH * (D / 64);
+  const int free = chain <= all / 4 ? all - chain : all;
+  const long long rounds = std::max(2ll, ((long long)BH * ((nch + 5) / 6) + free - 1) / free);
+  return std::min(nch, std::max((int)(rounds * free / BH), 4));
 }
 
 template <int D>
