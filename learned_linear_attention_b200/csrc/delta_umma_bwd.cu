@@ -77,7 +77,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                     const __grid_constant__ CUtensorMap mapY, HbArgs a) {
   using SM = HbSmem<D>;
   constexpr int DA = D / 64;
-  constexpr uint32_t TM_P = 0, TM_U = 128, TM_H = 192, TM_COLS = 256;
+  constexpr uint32_t TM_P = 0, TM_U = 128, TM_COLS = 256;   // Hb's accumulators take their places
   extern __shared__ __align__(1024) uint8_t smem[];
   Bars& bars = *reinterpret_cast<Bars*>(smem + SM::BAR);
   Gates& gates = *reinterpret_cast<Gates*>(smem + SM::GATES);
@@ -149,15 +149,11 @@ __global__ void __launch_bounds__(THREADS, 1)
     if (warp == 0 && elect_one()) {
       const Pair U{{sb + SM::P, ATOM, true}, ATOM}, G{{sb + SM::P + 3 * ATOM, ATOM, true}, ATOM};
       const Pair Wt{{sb + SM::W, ATOM, true}, DA * ATOM};
-      const uint32_t t = tmem + TM_H;   // small terms first
-      products<8>(Prod(t, Qmn, G.plane(2), D, 64, false));
-      products<8>(Prod(t, Wt.lo(), U.lo(), D, 64, true));
-      products<8>(Prod(t, Wt.hi, U.plane(2), D, 64, true));
-      products<8>(Prod(t, Qmn, G.lo(), D, 64, true));
-      products<8>(Prod(t, Wt.lo(), U.hi, D, 64, true));
-      products<8>(Prod(t, Wt.hi, U.lo(), D, 64, true));
-      products<8>(Prod(t, Wt.hi, U.hi, D, 64, true));
-      products<8>(Prod(t, Qmn, G.hi, D, 64, true));
+      // the three planes side by side are one operand of 192 columns: an
+      // accumulator each, of which the first holds the large terms
+      products<8>(Prod(tmem, Wt.hi, U.hi, D, 192, false));
+      products<8>(Prod(tmem + 64, Wt.lo(), U.hi, D, 128, true));
+      products<8>(Prod(tmem, Qmn, G.hi, D, 192, true));
       mma_commit(&bars.mma);
     }
     if (warp == 1 && elect_one()) {
@@ -168,7 +164,14 @@ __global__ void __launch_bounds__(THREADS, 1)
     if (!ph.mma_done(4)) return;
     const int r = D == 64 ? q4 * 16 + lane : row;
     float h[16];
-    tmem_ld16(tmem + lanes + TM_H + cg * 16, h);
+    tmem_ld16(tmem + lanes + 128 + cg * 16, h);
+#pragma unroll
+    for (int p = 1; p >= 0; --p) {
+      float y[16];
+      tmem_ld16(tmem + lanes + 64 * p + cg * 16, y);
+#pragma unroll
+      for (int i = 0; i < 16; ++i) h[i] += y[i];
+    }
     if (D == 128 || lane < 16) store_tile16(a.H + id.ci * D * D, D, r, id.slice * 64 + cg * 16, h);
   };
   work();
