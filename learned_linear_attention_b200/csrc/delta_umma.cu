@@ -886,12 +886,13 @@ int fwd_launch(const DeltaLaunch& p, cudaStream_t stream) {
 }  // namespace
 
 // Short sequences go token by token: the chunk kernels' latency is that of a
-// whole chunk and of three launches (24 us forward, 48 us backward at D = 64;
-// 33 and 61 at 128), the recurrent ones' 0.12 us a token at D = 64 and 0.19 at
-// 128 (backward 0.24 and 0.37, behind 21 and 41), times the rounds that their
-// CTAs of 16 value columns take.  Forward at D = 64, 1 to 32 heads: 128 tokens
-// 18 against 24 us, 256 tokens 33 against 24.  Backward at D = 64: 64 tokens 35
-// against 48, 128 tokens 51 against 48; at 128: 32 tokens 52 against 60.
+// whole chunk and of three launches (23 us forward, 47 us backward at D = 64;
+// 33 and 60 at 128), the recurrent ones' 0.10 us a token at D = 64 and 0.15 at
+// 128 (backward 0.20 and 0.32, behind 21 and 40), times the rounds that their
+// CTAs of 16 value columns take.  Forward at D = 64, up to 32 heads: 128 tokens
+// 16 against 19 us (one chunk), 256 tokens 28 against 23.  Backward at D = 64:
+// 77 tokens 38 against 46, 128 tokens 47 against 46; at 128: 33 tokens 55
+// against 59.
 bool delta_uses_umma(int bf16, int dk, int dv, long long BH, int N, int sms, bool backward) {
   if (!bf16 || dk != dv || (dk != 64 && dk != 128)) return false;
   const double rounds = std::max(1.0, (double)BH * (dv / 16) / (1.25 * sms));

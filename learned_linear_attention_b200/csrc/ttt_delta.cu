@@ -216,108 +216,175 @@ TTT_DEVICE_INLINE float part_dot(const float (&x)[4 * R4], const float (&y)[4 * 
   return a + b;
 }
 
+// ------------------------------------------------------------------ tiles
+// A CTA's 128 state threads walk tiles of TT tokens.  With HELP, 128 more
+// threads stage the next tile, form its coefficients and write the last one's
+// values meanwhile, in two buffers: what is left between tiles is one barrier.
+template <typename Tin, int R4, bool HELP, typename K, typename W, typename F>
+TTT_DEVICE_INLINE void walk_tiles(Stage<R4>* st, Fetch<Tin, R4>& f, int nch, bool down, float wscale, int tid,
+                                  K keep, W work, F write) {
+  if (nch == 0) return;
+  // the i-th tile of the walk starts at token t0(i)
+  auto t0 = [&](int i) { return (down ? nch - 1 - i : i) * TT; };
+  if constexpr (HELP) {
+    const bool helper = tid >= THREADS;
+    const int h = tid - THREADS;
+    auto stage = [&](int i) {   // by the helpers: tile i, whose values they hold
+      Stage<R4>& s = st[i & 1];
+      f.put(s, wscale);
+      named_bar_sync(1, THREADS);
+      if (i + 1 < nch) f.load(t0(i + 1));
+      coefficients(s, h);
+    };
+    if (helper) {
+      f.load(t0(0));
+      stage(0);
+    }
+    __syncthreads();
+    for (int i = 0; i < nch; ++i) {
+      if (!helper) {
+        keep(t0(i));
+        work(st[i & 1], t0(i));
+      } else {
+        if (i > 0) write(st[(i - 1) & 1], t0(i - 1), h);
+        if (i + 1 < nch) stage(i + 1);
+      }
+      __syncthreads();
+    }
+    if (helper) write(st[(nch - 1) & 1], t0(nch - 1), h);
+  } else {
+    f.load(t0(0));
+    for (int i = 0; i < nch; ++i) {
+      f.put(st[0], wscale);
+      __syncthreads();
+      if (i + 1 < nch) f.load(t0(i + 1));
+      coefficients(st[0], tid);
+      keep(t0(i));
+      __syncthreads();
+      work(st[0], t0(i));
+      __syncthreads();
+      write(st[0], t0(i), tid);
+    }
+  }
+}
+template <int R4, bool HELP>
+constexpr size_t stage_bytes() { return (HELP ? 2 : 1) * sizeof(Stage<R4>); }
+
 // ------------------------------------------------------------------ forward
+// The state over one tile of n tokens; READS: out of every token into st.os,
+// else e.
+template <int R4, bool READS>
+TTT_DEVICE_INLINE void rec_tile(Stage<R4>& st, float (&s)[4 * R4], int n, float scale, int l, int cl) {
+  constexpr int U = R4 == 1 ? 4 : 2;
+  const int lt = l & 3, nb = (n + 3) / 4;
+  // U blocks to a turn, so that one block's loads pass under the chain of
+  // the one before (results are kept back, as a store would stop the loads);
+  // padding tokens change nothing
+  for (int b0 = 0; b0 < nb; b0 += U) {
+    float keep[U];
+#pragma unroll
+    for (int ub = 0; ub < U; ++ub) {
+      const int b = b0 + ub;
+      const BlockCoef c4(st, b, cl);
+      float kv[4][4 * R4], d[4], dq[4];
+#pragma unroll
+      for (int t = 0; t < 4; ++t) {
+        load_rows<R4>(st.k[4 * b + t], l, kv[t]);
+        d[t] = part_dot<R4>(kv[t], s);
+      }
+      // eight sums over eight lanes, halving the values a lane holds: k_t.s
+      // ends in lane t, q_t.s in lane 4 + t
+      if constexpr (READS) {
+#pragma unroll
+        for (int t = 0; t < 4; ++t) {
+          float qv[4 * R4];
+          load_rows<R4>(st.q[4 * b + t], l, qv);
+          dq[t] = part_dot<R4>(qv, s);
+        }
+#pragma unroll
+        for (int t = 0; t < 4; ++t)
+          d[t] = ((l & 4) ? dq[t] : d[t]) + __shfl_xor_sync(0xffffffffu, (l & 4) ? d[t] : dq[t], 4);
+      }
+      float p2[2], mine;
+#pragma unroll
+      for (int t = 0; t < 2; ++t)
+        p2[t] = ((l & 2) ? d[2 + t] : d[t]) + __shfl_xor_sync(0xffffffffu, (l & 2) ? d[t] : d[2 + t], 2);
+      mine = ((l & 1) ? p2[1] : p2[0]) + __shfl_xor_sync(0xffffffffu, (l & 1) ? p2[0] : p2[1], 1);
+      if constexpr (!READS) mine += __shfl_xor_sync(0xffffffffu, mine, 4);
+      float p[4], e[4], u[4];
+#pragma unroll
+      for (int t = 0; t < 4; ++t) p[t] = __shfl_sync(0xffffffffu, mine, t, 8);
+#pragma unroll
+      for (int t = 0; t < 4; ++t) e[t] = fmaf(-c4.A[t], p[t], c4.w[t]);
+#pragma unroll
+      for (int t = 0; t < 4; ++t) {
+#pragma unroll
+        for (int i = 0; i < t; ++i) e[t] = fmaf(-c4.kk[t][i], u[i], e[t]);
+        u[t] = c4.b[t] * e[t];
+      }
+      if constexpr (READS) {
+        const float4 c = *reinterpret_cast<const float4*>(st.qk[4 * b + lt]);
+        // (selected, not multiplied by zero: a later token may hold NaN)
+        float o = fmaf(c.x, u[0], st.A[4 * b + lt] * mine);
+        o = lt >= 1 ? fmaf(c.y, u[1], o) : o;
+        o = lt >= 2 ? fmaf(c.z, u[2], o) : o;
+        o = lt >= 3 ? fmaf(c.w, u[3], o) : o;
+        keep[ub] = scale * o;
+      } else {
+        keep[ub] = lt == 0 ? e[0] : lt == 1 ? e[1] : lt == 2 ? e[2] : e[3];
+      }
+      const float A3 = c4.A[3];
+#pragma unroll
+      for (int t = 0; t < 4; ++t) u[t] *= c4.R[t];
+#pragma unroll
+      for (int i = 0; i < 4 * R4; ++i)
+        s[i] = fmaf(kv[3][i], u[3], fmaf(kv[2][i], u[2], fmaf(kv[1][i], u[1], fmaf(kv[0][i], u[0], A3 * s[i]))));
+    }
+    if (l & 4)
+#pragma unroll
+      for (int ub = 0; ub < U; ++ub) st.os[4 * (b0 + ub) + lt][cl] = keep[ub];
+  }
+}
+
 // out may be null (the backward pass's replay); then e and the state at every
 // chunk border (TT tokens) are kept: ev [BH][N][dv], Sc [BH][nch + 1][dk][dv].
-template <typename Tin, typename Tout, int R4>
-__global__ void __launch_bounds__(THREADS)
+template <typename Tin, typename Tout, int R4, bool HELP>
+__global__ void __launch_bounds__(HELP ? 2 * THREADS : THREADS)
     delta_rec_kernel(const Tin* __restrict__ q, const Tin* __restrict__ k, const Tin* __restrict__ v,
                      const Tin* __restrict__ g, const Tin* __restrict__ beta, const float* S_in,
                      float* S_out, Tout* __restrict__ out, float* __restrict__ ev,
                      float* __restrict__ Sc, int N, int dk, int dv, float scale) {
-  __shared__ __align__(16) Stage<R4> st;
+  extern __shared__ __align__(16) uint8_t smem_raw[];
+  Stage<R4>* st = reinterpret_cast<Stage<R4>*>(smem_raw);
   const size_t bh = blockIdx.x;
-  const int c0 = blockIdx.y * COLS, tid = threadIdx.x, cl = tid / L;
+  const int c0 = blockIdx.y * COLS, tid = threadIdx.x, cl = tid % THREADS / L;
   const Column<R4> col{tid % L, c0 + cl, dk, dv, c0 + cl < dv};
-  constexpr int U = R4 == 1 ? 4 : 2;
-  const int l = col.l, lt = l & 3;
+  const bool state = tid < THREADS, reads = out != nullptr;
   const size_t mat = (size_t)dk * dv;
   float s[4 * R4];
-  if (S_in != nullptr) {
+  if (state && S_in != nullptr) {
     col.load(S_in + bh * mat, s);
   } else {
 #pragma unroll
     for (int i = 0; i < 4 * R4; ++i) s[i] = 0.f;
   }
   const int nch = (N + TT - 1) / TT;
-  Fetch<Tin, R4> f(k, out != nullptr ? q : nullptr, v, g, beta, bh, N, dk, dv, c0, tid);
-  f.load(0);
-  for (int t0 = 0; t0 < N; t0 += TT) {
-    f.put(st, 1.f);
-    __syncthreads();
-    f.load(t0 + TT);
-    coefficients(st, tid);
-    if (Sc != nullptr) col.store(Sc + (bh * (nch + 1) + t0 / TT) * mat, s);
-    __syncthreads();
-    const int n = min(TT, N - t0), nb = (n + 3) / 4;
-    // U blocks to a turn, so that one block's loads pass under the chain of
-    // the one before (results are kept back, as a store would stop the loads);
-    // padding tokens change nothing
-    for (int b0 = 0; b0 < nb; b0 += U) {
-      float keep[U];
-#pragma unroll
-      for (int ub = 0; ub < U; ++ub) {
-        const int b = b0 + ub;
-        const BlockCoef c4(st, b, cl);
-        float kv[4][4 * R4], d[8];
-#pragma unroll
-        for (int t = 0; t < 4; ++t) {
-          load_rows<R4>(st.k[4 * b + t], l, kv[t]);
-          d[t] = part_dot<R4>(kv[t], s);
-        }
-#pragma unroll
-        for (int t = 0; t < 4; ++t) {
-          float qv[4 * R4];
-          load_rows<R4>(st.q[4 * b + t], l, qv);
-          d[4 + t] = part_dot<R4>(qv, s);
-        }
-        // eight sums over eight lanes, halving the values a lane holds: k_t.s
-        // ends in lane t, q_t.s in lane 4 + t
-        float h[4], p2[2], mine;
-#pragma unroll
-        for (int t = 0; t < 4; ++t)
-          h[t] = ((l & 4) ? d[4 + t] : d[t]) + __shfl_xor_sync(0xffffffffu, (l & 4) ? d[t] : d[4 + t], 4);
-#pragma unroll
-        for (int t = 0; t < 2; ++t)
-          p2[t] = ((l & 2) ? h[2 + t] : h[t]) + __shfl_xor_sync(0xffffffffu, (l & 2) ? h[t] : h[2 + t], 2);
-        mine = ((l & 1) ? p2[1] : p2[0]) + __shfl_xor_sync(0xffffffffu, (l & 1) ? p2[0] : p2[1], 1);
-        float p[4], e[4], u[4];
-#pragma unroll
-        for (int t = 0; t < 4; ++t) p[t] = __shfl_sync(0xffffffffu, mine, t, 8);
-#pragma unroll
-        for (int t = 0; t < 4; ++t) e[t] = fmaf(-c4.A[t], p[t], c4.w[t]);
-#pragma unroll
-        for (int t = 0; t < 4; ++t) {
-#pragma unroll
-          for (int i = 0; i < t; ++i) e[t] = fmaf(-c4.kk[t][i], u[i], e[t]);
-          u[t] = c4.b[t] * e[t];
-        }
-        if (out != nullptr) {
-          const float4 c = *reinterpret_cast<const float4*>(st.qk[4 * b + lt]);
-          // (selected, not multiplied by zero: a later token may hold NaN)
-          float o = fmaf(c.x, u[0], st.A[4 * b + lt] * mine);
-          o = lt >= 1 ? fmaf(c.y, u[1], o) : o;
-          o = lt >= 2 ? fmaf(c.z, u[2], o) : o;
-          o = lt >= 3 ? fmaf(c.w, u[3], o) : o;
-          keep[ub] = scale * o;
-        } else {
-          keep[ub] = lt == 0 ? e[0] : lt == 1 ? e[1] : lt == 2 ? e[2] : e[3];
-        }
-        const float A3 = c4.A[3];
-#pragma unroll
-        for (int t = 0; t < 4; ++t) u[t] *= c4.R[t];
-#pragma unroll
-        for (int i = 0; i < 4 * R4; ++i)
-          s[i] = fmaf(kv[3][i], u[3], fmaf(kv[2][i], u[2], fmaf(kv[1][i], u[1], fmaf(kv[0][i], u[0], A3 * s[i]))));
-      }
-      if (l & 4)
-#pragma unroll
-        for (int ub = 0; ub < U; ++ub) st.os[4 * (b0 + ub) + lt][cl] = keep[ub];
-    }
-    __syncthreads();
-    if (out != nullptr) write_os(st, out + (bh * N + t0) * dv, n, dv, c0, tid);
-    else write_os(st, ev + (bh * N + t0) * dv, n, dv, c0, tid);
-  }
+  Fetch<Tin, R4> f(k, reads ? q : nullptr, v, g, beta, bh, N, dk, dv, c0, tid % THREADS);
+  walk_tiles<Tin, R4, HELP>(
+      st, f, nch, false, 1.f, tid,
+      [&](int t0) {
+        if (Sc != nullptr) col.store(Sc + (bh * (nch + 1) + t0 / TT) * mat, s);
+      },
+      [&](Stage<R4>& t, int t0) {
+        if (reads) rec_tile<R4, true>(t, s, min(TT, N - t0), scale, col.l, cl);
+        else rec_tile<R4, false>(t, s, min(TT, N - t0), scale, col.l, cl);
+      },
+      [&](const Stage<R4>& t, int t0, int h) {
+        const int n = min(TT, N - t0);
+        if (reads) write_os(t, out + (bh * N + t0) * dv, n, dv, c0, h);
+        else write_os(t, ev + (bh * N + t0) * dv, n, dv, c0, h);
+      });
+  if (!state) return;
   if (Sc != nullptr) col.store(Sc + (bh * (nch + 1) + nch) * mat, s);
   if (S_out != nullptr) col.store(S_out + bh * mat, s);
 }
@@ -328,95 +395,94 @@ __global__ void __launch_bounds__(THREADS)
 // them and f = beta du:
 //   du_t = R_3t k_t.X + sum_{s>=t} R_st (q_s.k_t) do_s - sum_{s>t} R_st (k_s.k_t) f_s
 //   X <- A_3 X + sum_s A_s (q_s do_s - k_s f_s)
+template <int R4>
+TTT_DEVICE_INLINE void rev_tile(Stage<R4>& st, float (&x)[4 * R4], int n, int l, int cl) {
+  constexpr int U = R4 == 1 ? 4 : 2;
+  for (int b0 = (n + 4 * U - 1) / (4 * U) * U - 1; b0 >= 0; b0 -= U) {
+    float keep[U];
+#pragma unroll
+    for (int ub = 0; ub < U; ++ub) {
+      const int b = b0 - ub;
+      const BlockCoef c4(st, b, cl);
+      float kv[4][4 * R4], d[4];
+#pragma unroll
+      for (int t = 0; t < 4; ++t) {
+        load_rows<R4>(st.k[4 * b + t], l, kv[t]);
+        d[t] = part_dot<R4>(kv[t], x);
+      }
+      float h[2], mine;
+#pragma unroll
+      for (int t = 0; t < 2; ++t)
+        h[t] = ((l & 2) ? d[2 + t] : d[t]) + __shfl_xor_sync(0xffffffffu, (l & 2) ? d[t] : d[2 + t], 2);
+      mine = ((l & 1) ? h[1] : h[0]) + __shfl_xor_sync(0xffffffffu, (l & 1) ? h[0] : h[1], 1);
+      mine += __shfl_xor_sync(0xffffffffu, mine, 4);
+      float du[4], w[4], fu[4];
+#pragma unroll
+      for (int t = 0; t < 4; ++t) w[t] = c4.w[t];
+#pragma unroll
+      for (int t = 0; t < 4; ++t) {
+        du[t] = c4.R[t] * __shfl_sync(0xffffffffu, mine, t, 8);
+#pragma unroll
+        for (int s = t; s < 4; ++s) du[t] = fmaf(st.qk[4 * b + s][t], w[s], du[t]);
+      }
+#pragma unroll
+      for (int t = 3; t >= 0; --t) {
+#pragma unroll
+        for (int s = 3; s > t; --s) du[t] = fmaf(-c4.kk[s][t], fu[s], du[t]);
+        fu[t] = c4.b[t] * du[t];
+      }
+      keep[ub] = (l & 3) == 0 ? du[0] : (l & 3) == 1 ? du[1] : (l & 3) == 2 ? du[2] : du[3];
+      const float A3 = c4.A[3];
+#pragma unroll
+      for (int i = 0; i < 4 * R4; ++i) x[i] *= A3;
+#pragma unroll
+      for (int t = 0; t < 4; ++t) {
+        const float A = c4.A[t], wt = A * w[t], ft = -A * fu[t];
+        float qv[4 * R4];
+        load_rows<R4>(st.q[4 * b + t], l, qv);
+#pragma unroll
+        for (int i = 0; i < 4 * R4; ++i) x[i] = fmaf(qv[i], wt, fmaf(kv[t][i], ft, x[i]));
+      }
+    }
+    if (l & 4)
+#pragma unroll
+      for (int ub = 0; ub < U; ++ub) st.os[4 * (b0 - ub) + (l & 3)][cl] = keep[ub];
+  }
+}
+
 // Kept: du [BH][N][dv], and X at the end of every chunk of TT tokens, Xc
 // [BH][nch][dk][dv].
-template <typename Tin, int R4>
-__global__ void __launch_bounds__(THREADS)
+template <typename Tin, int R4, bool HELP>
+__global__ void __launch_bounds__(HELP ? 2 * THREADS : THREADS)
     delta_rev_kernel(const Tin* __restrict__ q, const Tin* __restrict__ k,
                      const Tin* __restrict__ dout, const Tin* __restrict__ g,
                      const Tin* __restrict__ beta, const float* __restrict__ dS_end,
                      float* __restrict__ dS0, float* __restrict__ duv, float* __restrict__ Xc, int N,
                      int dk, int dv, float scale) {
-  __shared__ __align__(16) Stage<R4> st;
+  extern __shared__ __align__(16) uint8_t smem_raw[];
+  Stage<R4>* st = reinterpret_cast<Stage<R4>*>(smem_raw);
   const size_t bh = blockIdx.x;
-  const int c0 = blockIdx.y * COLS, tid = threadIdx.x, cl = tid / L;
+  const int c0 = blockIdx.y * COLS, tid = threadIdx.x, cl = tid % THREADS / L;
   const Column<R4> col{tid % L, c0 + cl, dk, dv, c0 + cl < dv};
-  constexpr int U = R4 == 1 ? 4 : 2;
-  const int l = col.l;
+  const bool state = tid < THREADS;
   const size_t mat = (size_t)dk * dv;
   float x[4 * R4];
-  if (dS_end != nullptr) {
+  if (state && dS_end != nullptr) {
     col.load(dS_end + bh * mat, x);
   } else {
 #pragma unroll
     for (int i = 0; i < 4 * R4; ++i) x[i] = 0.f;
   }
   const int nch = (N + TT - 1) / TT;
-  Fetch<Tin, R4> f(k, q, dout, g, beta, bh, N, dk, dv, c0, tid);
-  f.load((nch - 1) * TT);
-  for (int ch = nch - 1; ch >= 0; --ch) {
-    const int t0 = ch * TT;
-    f.put(st, scale);
-    __syncthreads();
-    f.load(t0 - TT);
-    coefficients(st, tid);
-    col.store(Xc + (bh * nch + ch) * mat, x);
-    __syncthreads();
-    const int n = min(TT, N - t0);
-    for (int b0 = (n + 4 * U - 1) / (4 * U) * U - 1; b0 >= 0; b0 -= U) {
-      float keep[U];
-#pragma unroll
-      for (int ub = 0; ub < U; ++ub) {
-        const int b = b0 - ub;
-        const BlockCoef c4(st, b, cl);
-        float kv[4][4 * R4], d[4];
-#pragma unroll
-        for (int t = 0; t < 4; ++t) {
-          load_rows<R4>(st.k[4 * b + t], l, kv[t]);
-          d[t] = part_dot<R4>(kv[t], x);
-        }
-        float h[2], mine;
-#pragma unroll
-        for (int t = 0; t < 2; ++t)
-          h[t] = ((l & 2) ? d[2 + t] : d[t]) + __shfl_xor_sync(0xffffffffu, (l & 2) ? d[t] : d[2 + t], 2);
-        mine = ((l & 1) ? h[1] : h[0]) + __shfl_xor_sync(0xffffffffu, (l & 1) ? h[0] : h[1], 1);
-        mine += __shfl_xor_sync(0xffffffffu, mine, 4);
-        float du[4], w[4], fu[4];
-#pragma unroll
-        for (int t = 0; t < 4; ++t) w[t] = c4.w[t];
-#pragma unroll
-        for (int t = 0; t < 4; ++t) {
-          du[t] = c4.R[t] * __shfl_sync(0xffffffffu, mine, t, 8);
-#pragma unroll
-          for (int s = t; s < 4; ++s) du[t] = fmaf(st.qk[4 * b + s][t], w[s], du[t]);
-        }
-#pragma unroll
-        for (int t = 3; t >= 0; --t) {
-#pragma unroll
-          for (int s = 3; s > t; --s) du[t] = fmaf(-c4.kk[s][t], fu[s], du[t]);
-          fu[t] = c4.b[t] * du[t];
-        }
-        keep[ub] = (l & 3) == 0 ? du[0] : (l & 3) == 1 ? du[1] : (l & 3) == 2 ? du[2] : du[3];
-        const float A3 = c4.A[3];
-#pragma unroll
-        for (int i = 0; i < 4 * R4; ++i) x[i] *= A3;
-#pragma unroll
-        for (int t = 0; t < 4; ++t) {
-          const float A = c4.A[t], wt = A * w[t], ft = -A * fu[t];
-          float qv[4 * R4];
-          load_rows<R4>(st.q[4 * b + t], l, qv);
-#pragma unroll
-          for (int i = 0; i < 4 * R4; ++i) x[i] = fmaf(qv[i], wt, fmaf(kv[t][i], ft, x[i]));
-        }
-      }
-      if (l & 4)
-#pragma unroll
-        for (int ub = 0; ub < U; ++ub) st.os[4 * (b0 - ub) + (l & 3)][cl] = keep[ub];
-    }
-    __syncthreads();
-    write_os(st, duv + (bh * N + t0) * dv, n, dv, c0, tid);
-  }
-  col.store(dS0 + bh * mat, x);
+  Fetch<Tin, R4> f(k, q, dout, g, beta, bh, N, dk, dv, c0, tid % THREADS);
+  walk_tiles<Tin, R4, HELP>(
+      st, f, nch, true, scale, tid,
+      [&](int t0) { col.store(Xc + (bh * nch + t0 / TT) * mat, x); },
+      [&](Stage<R4>& t, int t0) { rev_tile<R4>(t, x, min(TT, N - t0), col.l, cl); },
+      [&](const Stage<R4>& t, int t0, int h) {
+        write_os(t, duv + (bh * N + t0) * dv, min(TT, N - t0), dv, c0, h);
+      });
+  if (state) col.store(dS0 + bh * mat, x);
 }
 
 // ------------------------------------------------------------------ a chunk's gradients
@@ -840,19 +906,43 @@ __global__ void __launch_bounds__(STHREADS, 7)
     default: CALL(4); break;                  \
   }
 
+// Helpers pay while every CTA has an SM for itself: forward over 1,024 float32
+// tokens, 8 heads of 32 / 64 / 128: 97 / 130 / 201 us alone, 75 / 102 / 159
+// helped.  Beyond that they take issue slots from the second CTA: 64 heads of
+// 64 / 128: 177 / 575 us alone, 203 / 631 helped (64 heads of 32 are 128 CTAs).
+bool rec_helped(const DeltaLaunch& p) {
+  return (long long)p.B * p.H * ((p.dv + COLS - 1) / COLS) <= p.sms;
+}
+template <int R4, bool HELP, typename... KArgs, typename... Args>
+int launch_rec(void (*kernel)(KArgs...), dim3 grid, cudaStream_t stream, Args... args) {
+  if (stage_bytes<R4, HELP>() > 48 * 1024 &&
+      cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)stage_bytes<R4, HELP>()) !=
+          cudaSuccess)
+    return -1;
+  kernel<<<grid, HELP ? 2 * THREADS : THREADS, stage_bytes<R4, HELP>(), stream>>>(args...);
+  return cudaGetLastError() == cudaSuccess ? 0 : -1;
+}
+
 template <typename Tin, typename Tout>
 int rec_launch(const DeltaLaunch& p, float* S_out, const float* S_in, Tout* out, float* ev, float* Sc,
                cudaStream_t stream) {
   const dim3 grid((unsigned)(p.B * p.H), (unsigned)((p.dv + COLS - 1) / COLS));
   prof_before(K_DELTA_REC, stream);
-#define TTT_REC(R4)                                                                            \
-  delta_rec_kernel<Tin, Tout, R4><<<grid, THREADS, 0, stream>>>(                               \
-      (const Tin*)p.q, (const Tin*)p.k, (const Tin*)p.v, (const Tin*)p.g, (const Tin*)p.beta,  \
-      S_in, S_out, out, ev, Sc, p.N, p.dk, p.dv, p.scale)
+  const bool help = rec_helped(p);
+  int err = 0;
+#define TTT_REC(R4)                                                                              \
+  err = help ? launch_rec<R4, true>(delta_rec_kernel<Tin, Tout, R4, true>, grid, stream,         \
+                                    TTT_REC_ARGS)                                                \
+             : launch_rec<R4, false>(delta_rec_kernel<Tin, Tout, R4, false>, grid, stream,       \
+                                     TTT_REC_ARGS)
+#define TTT_REC_ARGS                                                                              \
+  (const Tin*)p.q, (const Tin*)p.k, (const Tin*)p.v, (const Tin*)p.g, (const Tin*)p.beta, S_in,  \
+      S_out, out, ev, Sc, p.N, p.dk, p.dv, p.scale
   TTT_BY_ROWS(p.dk, TTT_REC)
+#undef TTT_REC_ARGS
 #undef TTT_REC
   prof_after(K_DELTA_REC, stream);
-  return cudaGetLastError() == cudaSuccess ? 0 : -1;
+  return err;
 }
 
 template <typename Tin>
@@ -867,14 +957,19 @@ int bwd_launch(const DeltaBwdLaunch& L, cudaStream_t stream) {
   if (rec_launch<Tin, float>(p, nullptr, L.S0, nullptr, ev, Sc, stream)) return -1;
   const dim3 grid((unsigned)BH, (unsigned)((p.dv + COLS - 1) / COLS));
   prof_before(K_DELTA_REV, stream);
+  const bool help = rec_helped(p);
+  int err = 0;
 #define TTT_REV(R4)                                                                               \
-  delta_rev_kernel<Tin, R4><<<grid, THREADS, 0, stream>>>(                                        \
-      (const Tin*)p.q, (const Tin*)p.k, (const Tin*)L.dout, (const Tin*)p.g, (const Tin*)p.beta,  \
-      L.dS_end, L.dS0, du, Xc, p.N, p.dk, p.dv, p.scale)
+  err = help ? launch_rec<R4, true>(delta_rev_kernel<Tin, R4, true>, grid, stream, TTT_REV_ARGS)  \
+             : launch_rec<R4, false>(delta_rev_kernel<Tin, R4, false>, grid, stream, TTT_REV_ARGS)
+#define TTT_REV_ARGS                                                                              \
+  (const Tin*)p.q, (const Tin*)p.k, (const Tin*)L.dout, (const Tin*)p.g, (const Tin*)p.beta,      \
+      L.dS_end, L.dS0, du, Xc, p.N, p.dk, p.dv, p.scale
   TTT_BY_ROWS(p.dk, TTT_REV)
+#undef TTT_REV_ARGS
 #undef TTT_REV
   prof_after(K_DELTA_REV, stream);
-  if (cudaGetLastError() != cudaSuccess) return -1;
+  if (err) return -1;
   const size_t smem = chunk_grad_smem(p.dk, p.dv);
   void (*kfn)(ChunkArgs<Tin>) = nullptr;
   static std::atomic<uint64_t> attr[4] = {};

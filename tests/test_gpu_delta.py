@@ -232,6 +232,14 @@ def test_many_heads_are_the_heads_one_by_one(cuda_device, d, N):
         assert torch.equal(got, o.flatten(0, 1)[i]) and torch.equal(s, S.view(-1, d, d)[i])
 
 
+@pytest.mark.parametrize("d,N", [(64, 70), (128, 33), (64, 1)])
+def test_many_short_sequences(cuda_device, d, N):
+    """So many heads that less than one chunk of each goes to the tensor cores (one token does not)."""
+    p = Problem(8, 20, N, d, d, "bf16")
+    p.check_fwd(p.fwd())
+    p.check_bwd(p.bwd())
+
+
 @pytest.mark.parametrize("dt,d,first", [("f32", 24, 189), ("bf16", 40, 189), ("bf16", 64, 128), ("bf16", 128, 128)])
 @pytest.mark.parametrize("bad", [float("nan"), float("inf")])
 def test_a_bad_value_stays_behind(cuda_device, dt, d, first, bad):
