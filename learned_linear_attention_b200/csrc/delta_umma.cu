@@ -60,9 +60,12 @@ TTT_DEVICE_INLINE void mma_16x8x8(float (&c)[4], const uint32_t (&a)[4], const u
 // [k0, k1).  xd, yd: the tile's first row or column where X or Y is lower
 // triangular (what lies above the diagonal counts as zero), -1 where not.  The
 // three products have sums of their own, so that a step waits for one of them.
+// Lane (g, t) holds columns 2t and 2t + 1 of X's rows tile_row(g) and 8 below,
+// and those rows of Y: with LDA = 4 (mod 32) no two lanes meet in a bank.
+TTT_DEVICE_INLINE int tile_row(int g) { return 2 * (g & 3) + (g >> 2); }
 TTT_DEVICE_INLINE void tile_product(const float* X, const float* Y, int k0, int k1, int xd, int yd, int lane,
                                     float (&acc)[2][4]) {
-  const int g = lane >> 2, t = lane & 3;
+  const int g = lane >> 2, t = lane & 3, gr = tile_row(g);
   float s1[2][4], s2[2][4];
 #pragma unroll
   for (int n = 0; n < 2; ++n)
@@ -71,19 +74,21 @@ TTT_DEVICE_INLINE void tile_product(const float* X, const float* Y, int k0, int 
   auto step = [&](int k, bool diag) {
     uint32_t ah[4], al[4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int r = g + (i & 1) * 8, c = k + t + (i >> 1) * 4;
-      const float x = X[r * LDA + c];
-      const Tf32 v(diag && xd >= 0 && c > xd + r ? 0.f : x);
+    for (int i = 0; i < 2; ++i) {
+      const int r = gr + i * 8, c = k + 2 * t;
+      const float2 x = *reinterpret_cast<const float2*>(X + r * LDA + c);
+      const Tf32 v(diag && xd >= 0 && c > xd + r ? 0.f : x.x), w(diag && xd >= 0 && c + 1 > xd + r ? 0.f : x.y);
       ah[i] = v.hi;
       al[i] = v.lo;
+      ah[i + 2] = w.hi;
+      al[i + 2] = w.lo;
     }
 #pragma unroll
     for (int n = 0; n < 2; ++n) {
       uint32_t bh[2], bl[2];
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
-        const int r = k + t + i * 4, c = 8 * n + g;
+        const int r = k + 2 * t + i, c = 8 * n + g;
         const float y = Y[r * LDA + c];
         const Tf32 v(diag && yd >= 0 && r < yd + c ? 0.f : y);
         bh[i] = v.hi;
@@ -107,7 +112,7 @@ TTT_DEVICE_INLINE void tile_product(const float* X, const float* Y, int k0, int 
     for (int i = 0; i < 4; ++i) acc[n][i] += s1[n][i] + s2[n][i];
 }
 TTT_DEVICE_INLINE void store_tile(float* C_, float sign, int lane, const float (&acc)[2][4]) {
-  const int g = lane >> 2, t = lane & 3;
+  const int g = tile_row(lane >> 2), t = lane & 3;
 #pragma unroll
   for (int n = 0; n < 2; ++n) {
     *reinterpret_cast<float2*>(C_ + g * LDA + 8 * n + 2 * t) = make_float2(sign * acc[n][0], sign * acc[n][1]);
@@ -119,7 +124,10 @@ template <int S>
 TTT_DEVICE_INLINE void join_blocks(float* A, int warp, int lane) {
   constexpr int TILES = S / 16, WARPS = TILES * TILES * (C / (2 * S));
   static_assert(WARPS <= THREADS / 32, "a tile a warp");
-  const int p = warp / (TILES * TILES), r0 = warp / TILES % TILES * 16, n0 = warp % TILES * 16;
+  // (the columns turn from row to row, and rows from pair to pair, as a tile's
+  // depth goes with them and an SM's quarter runs every fourth warp)
+  const int p = warp / (TILES * TILES), r0 = (warp / TILES + p) % TILES * 16;
+  const int n0 = (warp + warp / 4) % TILES * 16;
   float* T11 = A + p * 2 * S * (LDA + 1);
   float* A21 = T11 + S * LDA;
   float* T22 = A21 + S;
@@ -145,9 +153,11 @@ TTT_DEVICE_INLINE void invert(float* A, int warp, int lane) {
     const int j = tid & 15;
 #pragma unroll
     for (int i = 0; i < 16; ++i) {
-      float acc = i == j ? 1.f : 0.f;
+      float b[16], acc = i == j ? 1.f : 0.f;
 #pragma unroll
-      for (int k = 0; k < i; ++k) acc = fmaf(-B[i * LDA + k], x[k], acc);
+      for (int k = 0; k < i; k += 4) *reinterpret_cast<float4*>(b + k) = *reinterpret_cast<const float4*>(B + i * LDA + k);
+#pragma unroll
+      for (int k = 0; k < i; ++k) acc = fmaf(-b[k], x[k], acc);
       x[i] = acc;
     }
     __syncwarp();   // a block's 16 threads are in one warp
