@@ -296,6 +296,7 @@ static int check_delta(const ttt_delta_desc* d) {
   if (!d) return TTT_ERR_ARG;
   if (d->B < 1 || d->H < 1 || d->N < 0 || d->dk < 1 || d->dv < 1) return TTT_ERR_SHAPE;
   if ((long long)d->B * d->H > (1ll << 31) - 1) return TTT_ERR_SHAPE;
+  if ((long long)d->B * d->H * d->N > 1ll << 46) return TTT_ERR_SHAPE;   // sizes in bytes stay below 2^64
   if (!dtype_ok(d->in_dtype) || !dtype_ok(d->out_dtype)) return TTT_ERR_DTYPE;
   if (d->scale != d->scale) return TTT_ERR_ARG;
   if (d->dk > 128 || d->dv > 128) return TTT_ERR_UNSUPPORTED;
@@ -557,16 +558,18 @@ int ttt_delta_layer_fwd(const ttt_delta_desc* d, float eps, float out_scale, con
   cudaStream_t s = as_stream(stream);
   NormLaunch n = norm_launch(&nk, q, nullptr, nullptr);
   n.out = base + lay.q;
-  if (launch_norm_fwd(n, device_sms(), s)) return TTT_ERR_CUDA;
+  e = launched(launch_norm_fwd(n, device_sms(), s));
+  if (e) return e;
   n.x = k;
   n.out = base + lay.k;
-  if (launch_norm_fwd(n, device_sms(), s)) return TTT_ERR_CUDA;
+  e = launched(launch_norm_fwd(n, device_sms(), s));
+  if (e) return e;
   e = ttt_delta_fwd(d, base + lay.q, base + lay.k, v, g, beta, S, base + lay.o, ws, lay.q, stream);
   if (e) return e;
   n = norm_launch(&no, base + lay.o, w, z);
   n.res = res;
   n.out = out;
-  return launch_norm_fwd(n, device_sms(), s) ? TTT_ERR_CUDA : TTT_OK;
+  return launched(launch_norm_fwd(n, device_sms(), s));
 }
 
 // ------------------------------------------------------------------ window attention

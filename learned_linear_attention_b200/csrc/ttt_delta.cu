@@ -915,11 +915,10 @@ bool rec_helped(const DeltaLaunch& p) {
 }
 template <int R4, bool HELP, typename... KArgs, typename... Args>
 int launch_rec(void (*kernel)(KArgs...), dim3 grid, cudaStream_t stream, Args... args) {
-  if (stage_bytes<R4, HELP>() > 48 * 1024 &&
-      cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)stage_bytes<R4, HELP>()) !=
-          cudaSuccess)
-    return -1;
-  kernel<<<grid, HELP ? 2 * THREADS : THREADS, stage_bytes<R4, HELP>(), stream>>>(args...);
+  constexpr size_t smem = stage_bytes<R4, HELP>();
+  static std::atomic<uint64_t> attr{};
+  if (smem > 48 * 1024 && allow_dynamic_smem(kernel, (int)smem, attr)) return -1;
+  kernel<<<grid, HELP ? 2 * THREADS : THREADS, smem, stream>>>(args...);
   return cudaGetLastError() == cudaSuccess ? 0 : -1;
 }
 

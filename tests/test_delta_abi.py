@@ -74,6 +74,20 @@ def _norm_bwd(d, ws_bytes=1 << 39, **over):
                                  ws_bytes, None)
 
 
+def test_delta_refuses_sizes_that_wrap():
+    """Tokens whose byte counts would pass 64 bits are refused, not wrapped to a small workspace."""
+    d = T.make_delta_desc(1 << 16, (1 << 15) - 1, (1 << 31) - 1, 128, 128)
+    n = ctypes.c_size_t(0)
+    for fn in ("ttt_delta_workspace_bytes", "ttt_delta_bwd_workspace_bytes", "ttt_delta_layer_workspace_bytes"):
+        assert getattr(T.load(), fn)(ctypes.byref(d), ctypes.byref(n)) == T.TTT_ERR_SHAPE, fn
+    assert _fwd(d) == _bwd(d) == T.TTT_ERR_SHAPE
+    # the largest that pass: 64-bit sizes, larger than their tensors
+    d = T.make_delta_desc(1, 1, (1 << 31) - 1, 128, 128)
+    for fn in ("ttt_delta_bwd_workspace_bytes", "ttt_delta_layer_workspace_bytes"):
+        assert getattr(T.load(), fn)(ctypes.byref(d), ctypes.byref(n)) == T.TTT_OK
+        assert n.value > ((1 << 31) - 1) * 128 * 2
+
+
 @pytest.mark.parametrize("call", [_fwd, _bwd, _step])
 def test_delta_descriptor_refusals(call):
     N = 1 if call is _step else 8
