@@ -183,9 +183,9 @@ int ttt_linear_bwd(const ttt_linear_desc* desc, const void* q, const void* k, co
  * and v.
  *
  * The sequence form and its gradients with bf16 inputs and dk = dv = 64 or
- * 128 run on tensor cores in chunks of 128 tokens once they hold more than
- * some 100 tokens: every derived operand there is carried as bf16 hi + lo
- * (about 17 significant bits; three planes in what S and dS0 are made of) with
+ * 128 run on tensor cores in chunks of 128 tokens once they hold some 200
+ * tokens (some 40 where there are many heads): every derived operand there is
+ * carried as bf16 hi + lo (about 17 significant bits; three planes in what S and dS0 are made of) with
  * float32 sums, and the state stays float32.  Every other type and size runs
  * in float32 on CUDA cores, four tokens at a time.  An infinity or NaN in a
  * token reaches the tokens behind it, and on tensor cores all of its chunk.

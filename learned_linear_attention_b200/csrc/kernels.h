@@ -359,7 +359,7 @@ int launch_lact_keygrad(const KeyGradLaunch& L, cudaStream_t stream);
 enum KernelKind {
   K_LIN_SIMT, K_LIN_UMMA, K_LACT_CAST, K_KEYPASS, K_GEMM_READ, K_GEMM_GRAD, K_UPDATE,
   K_MUON_MOM, K_NS_PREP, K_GEMM_NS, K_MUON_APPLY, K_KEYGRAD, K_LIN_SEG, K_LIN_BWD_EW, K_SWA, K_LOOP,
-  K_BWD_FWD, K_BWD_GROUP, K_DELTA_REC, K_DELTA_REV, K_DELTA_GRAD, K_DELTA_STEP, K_NORM, K_NORM_BWD,
+  K_BWD_FWD, K_BWD_GROUP, K_DELTA_REC, K_DELTA_STATES, K_DELTA_GRAD, K_DELTA_STEP, K_NORM, K_NORM_BWD,
   K_DELTA_PREP, K_DELTA_CHAIN, K_DELTA_FWD, K_DELTA_HB, K_DELTA_VALS, K_DELTA_KEYS, K_DELTA_GATES,
   K_NUM
 };

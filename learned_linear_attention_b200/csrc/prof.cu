@@ -13,7 +13,7 @@ static const char* kKindNames[K_NUM] = {
     "gemm_read",       "gemm_grad",       "lact_update",   "muon_momentum",
     "ns_prep",         "gemm_ns",         "muon_apply",    "lact_keygrad",
     "ttt_linear_segstate", "ttt_linear_bwd_ew", "window_attention", "lact_loop", "lact_bwd_fwd",
-    "lact_bwd_gemm", "delta_rec", "delta_rev", "delta_grad", "delta_step", "norm", "norm_bwd",
+    "lact_bwd_gemm", "delta_rec", "delta_states", "delta_grad", "delta_step", "norm", "norm_bwd",
     "delta_prep", "delta_chain", "delta_fwd", "delta_hb", "delta_vals", "delta_keys", "delta_gates"};
 
 struct ProfRec {

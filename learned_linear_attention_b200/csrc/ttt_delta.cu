@@ -346,20 +346,19 @@ TTT_DEVICE_INLINE void rec_tile(Stage<R4>& st, float (&s)[4 * R4], int n, float 
   }
 }
 
-// out may be null (the backward pass's replay); then e and the state at every
-// chunk border (TT tokens) are kept: ev [BH][N][dv], Sc [BH][nch + 1][dk][dv].
-template <typename Tin, typename Tout, int R4, bool HELP>
-__global__ void __launch_bounds__(HELP ? 2 * THREADS : THREADS)
-    delta_rec_kernel(const Tin* __restrict__ q, const Tin* __restrict__ k, const Tin* __restrict__ v,
-                     const Tin* __restrict__ g, const Tin* __restrict__ beta, const float* S_in,
-                     float* S_out, Tout* __restrict__ out, float* __restrict__ ev,
-                     float* __restrict__ Sc, int N, int dk, int dv, float scale) {
-  extern __shared__ __align__(16) uint8_t smem_raw[];
-  Stage<R4>* st = reinterpret_cast<Stage<R4>*>(smem_raw);
+// One CTA's 16 columns over the whole sequence.  KEEP: the backward pass's
+// replay, whose rows are e (ev [BH][N][dv]) in place of out, and which keeps
+// the state at every chunk border (TT tokens), Sc [BH][nch + 1][dk][dv].
+template <typename Tin, typename Tout, int R4, bool HELP, bool KEEP>
+TTT_DEVICE_INLINE void rec_cta(Stage<R4>* st, const Tin* __restrict__ q, const Tin* __restrict__ k,
+                               const Tin* __restrict__ v, const Tin* __restrict__ g,
+                               const Tin* __restrict__ beta, const float* S_in, float* S_out,
+                               Tout* __restrict__ rows, float* __restrict__ Sc, int N, int dk, int dv,
+                               float scale) {
   const size_t bh = blockIdx.x;
   const int c0 = blockIdx.y * COLS, tid = threadIdx.x, cl = tid % THREADS / L;
   const Column<R4> col{tid % L, c0 + cl, dk, dv, c0 + cl < dv};
-  const bool state = tid < THREADS, reads = out != nullptr;
+  const bool state = tid < THREADS;
   const size_t mat = (size_t)dk * dv;
   float s[4 * R4];
   if (state && S_in != nullptr) {
@@ -369,24 +368,28 @@ __global__ void __launch_bounds__(HELP ? 2 * THREADS : THREADS)
     for (int i = 0; i < 4 * R4; ++i) s[i] = 0.f;
   }
   const int nch = (N + TT - 1) / TT;
-  Fetch<Tin, R4> f(k, reads ? q : nullptr, v, g, beta, bh, N, dk, dv, c0, tid % THREADS);
+  Fetch<Tin, R4> f(k, KEEP ? nullptr : q, v, g, beta, bh, N, dk, dv, c0, tid % THREADS);
   walk_tiles<Tin, R4, HELP>(
       st, f, nch, false, 1.f, tid,
       [&](int t0) {
-        if (Sc != nullptr) col.store(Sc + (bh * (nch + 1) + t0 / TT) * mat, s);
+        if constexpr (KEEP) col.store(Sc + (bh * (nch + 1) + t0 / TT) * mat, s);
       },
-      [&](Stage<R4>& t, int t0) {
-        if (reads) rec_tile<R4, true>(t, s, min(TT, N - t0), scale, col.l, cl);
-        else rec_tile<R4, false>(t, s, min(TT, N - t0), scale, col.l, cl);
-      },
+      [&](Stage<R4>& t, int t0) { rec_tile<R4, !KEEP>(t, s, min(TT, N - t0), scale, col.l, cl); },
       [&](const Stage<R4>& t, int t0, int h) {
-        const int n = min(TT, N - t0);
-        if (reads) write_os(t, out + (bh * N + t0) * dv, n, dv, c0, h);
-        else write_os(t, ev + (bh * N + t0) * dv, n, dv, c0, h);
+        write_os(t, rows + (bh * N + t0) * dv, min(TT, N - t0), dv, c0, h);
       });
   if (!state) return;
-  if (Sc != nullptr) col.store(Sc + (bh * (nch + 1) + nch) * mat, s);
-  if (S_out != nullptr) col.store(S_out + bh * mat, s);
+  if constexpr (KEEP) col.store(Sc + (bh * (nch + 1) + nch) * mat, s);
+  else col.store(S_out + bh * mat, s);
+}
+template <typename Tin, typename Tout, int R4, bool HELP>
+__global__ void __launch_bounds__(HELP ? 2 * THREADS : THREADS)
+    delta_rec_kernel(const Tin* __restrict__ q, const Tin* __restrict__ k, const Tin* __restrict__ v,
+                     const Tin* __restrict__ g, const Tin* __restrict__ beta, float* S,
+                     Tout* __restrict__ out, int N, int dk, int dv, float scale) {
+  extern __shared__ __align__(16) uint8_t smem_raw[];
+  rec_cta<Tin, Tout, R4, HELP, false>(reinterpret_cast<Stage<R4>*>(smem_raw), q, k, v, g, beta, S, S, out,
+                                      nullptr, N, dk, dv, scale);
 }
 
 // ------------------------------------------------------------------ reverse
@@ -453,14 +456,11 @@ TTT_DEVICE_INLINE void rev_tile(Stage<R4>& st, float (&x)[4 * R4], int n, int l,
 // Kept: du [BH][N][dv], and X at the end of every chunk of TT tokens, Xc
 // [BH][nch][dk][dv].
 template <typename Tin, int R4, bool HELP>
-__global__ void __launch_bounds__(HELP ? 2 * THREADS : THREADS)
-    delta_rev_kernel(const Tin* __restrict__ q, const Tin* __restrict__ k,
-                     const Tin* __restrict__ dout, const Tin* __restrict__ g,
-                     const Tin* __restrict__ beta, const float* __restrict__ dS_end,
-                     float* __restrict__ dS0, float* __restrict__ duv, float* __restrict__ Xc, int N,
-                     int dk, int dv, float scale) {
-  extern __shared__ __align__(16) uint8_t smem_raw[];
-  Stage<R4>* st = reinterpret_cast<Stage<R4>*>(smem_raw);
+TTT_DEVICE_INLINE void rev_cta(Stage<R4>* st, const Tin* __restrict__ q, const Tin* __restrict__ k,
+                               const Tin* __restrict__ dout, const Tin* __restrict__ g,
+                               const Tin* __restrict__ beta, const float* __restrict__ dS_end,
+                               float* __restrict__ dS0, float* __restrict__ duv, float* __restrict__ Xc,
+                               int N, int dk, int dv, float scale) {
   const size_t bh = blockIdx.x;
   const int c0 = blockIdx.y * COLS, tid = threadIdx.x, cl = tid % THREADS / L;
   const Column<R4> col{tid % L, c0 + cl, dk, dv, c0 + cl < dv};
@@ -483,6 +483,28 @@ __global__ void __launch_bounds__(HELP ? 2 * THREADS : THREADS)
         write_os(t, duv + (bh * N + t0) * dv, min(TT, N - t0), dv, c0, h);
       });
   if (state) col.store(dS0 + bh * mat, x);
+}
+
+// Neither direction needs the other: the forward replay (z = 0) and the
+// reverse (z = 1) are CTAs of one launch.
+template <typename Tin>
+struct StatesArgs {
+  const Tin *q, *k, *v, *dout, *g, *beta;
+  const float *S0, *dS_end;
+  float *dS0, *ev, *du, *Sc, *Xc;
+  int N, dk, dv;
+  float scale;
+};
+template <typename Tin, int R4, bool HELP>
+__global__ void __launch_bounds__(HELP ? 2 * THREADS : THREADS) delta_states_kernel(const StatesArgs<Tin> a) {
+  extern __shared__ __align__(16) uint8_t smem_raw[];
+  Stage<R4>* st = reinterpret_cast<Stage<R4>*>(smem_raw);
+  if (blockIdx.z == 0)
+    rec_cta<Tin, float, R4, HELP, true>(st, a.q, a.k, a.v, a.g, a.beta, a.S0, nullptr, a.ev, a.Sc, a.N, a.dk,
+                                        a.dv, a.scale);
+  else
+    rev_cta<Tin, R4, HELP>(st, a.q, a.k, a.dout, a.g, a.beta, a.dS_end, a.dS0, a.du, a.Xc, a.N, a.dk, a.dv,
+                           a.scale);
 }
 
 // ------------------------------------------------------------------ a chunk's gradients
@@ -910,33 +932,34 @@ __global__ void __launch_bounds__(STHREADS, 7)
 // tokens, 8 heads of 32 / 64 / 128: 97 / 130 / 201 us alone, 75 / 102 / 159
 // helped.  Beyond that they take issue slots from the second CTA: 64 heads of
 // 64 / 128: 177 / 575 us alone, 203 / 631 helped (64 heads of 32 are 128 CTAs).
-bool rec_helped(const DeltaLaunch& p) {
-  return (long long)p.B * p.H * ((p.dv + COLS - 1) / COLS) <= p.sms;
-}
 template <int R4, bool HELP, typename... KArgs, typename... Args>
-int launch_rec(void (*kernel)(KArgs...), dim3 grid, cudaStream_t stream, Args... args) {
+int launch_cols(void (*kernel)(KArgs...), dim3 grid, cudaStream_t stream, Args... args) {
   constexpr size_t smem = stage_bytes<R4, HELP>();
   static std::atomic<uint64_t> attr{};
   if (smem > 48 * 1024 && allow_dynamic_smem(kernel, (int)smem, attr)) return -1;
   kernel<<<grid, HELP ? 2 * THREADS : THREADS, smem, stream>>>(args...);
   return cudaGetLastError() == cudaSuccess ? 0 : -1;
 }
+// heads x slices of columns x directions
+dim3 cols_grid(const DeltaLaunch& p, int directions) {
+  return dim3((unsigned)(p.B * p.H), (unsigned)((p.dv + COLS - 1) / COLS), (unsigned)directions);
+}
+bool helped(const DeltaLaunch& p, const dim3& g) { return (long long)g.x * g.y * g.z <= p.sms; }
 
 template <typename Tin, typename Tout>
-int rec_launch(const DeltaLaunch& p, float* S_out, const float* S_in, Tout* out, float* ev, float* Sc,
-               cudaStream_t stream) {
-  const dim3 grid((unsigned)(p.B * p.H), (unsigned)((p.dv + COLS - 1) / COLS));
-  prof_before(K_DELTA_REC, stream);
-  const bool help = rec_helped(p);
+int rec_launch(const DeltaLaunch& p, cudaStream_t stream) {
+  const dim3 grid = cols_grid(p, 1);
+  const bool help = helped(p, grid);
   int err = 0;
-#define TTT_REC(R4)                                                                              \
-  err = help ? launch_rec<R4, true>(delta_rec_kernel<Tin, Tout, R4, true>, grid, stream,         \
-                                    TTT_REC_ARGS)                                                \
-             : launch_rec<R4, false>(delta_rec_kernel<Tin, Tout, R4, false>, grid, stream,       \
-                                     TTT_REC_ARGS)
-#define TTT_REC_ARGS                                                                              \
-  (const Tin*)p.q, (const Tin*)p.k, (const Tin*)p.v, (const Tin*)p.g, (const Tin*)p.beta, S_in,  \
-      S_out, out, ev, Sc, p.N, p.dk, p.dv, p.scale
+  prof_before(K_DELTA_REC, stream);
+#define TTT_REC(R4)                                                                                \
+  err = help ? launch_cols<R4, true>(delta_rec_kernel<Tin, Tout, R4, true>, grid, stream,          \
+                                     TTT_REC_ARGS)                                                 \
+             : launch_cols<R4, false>(delta_rec_kernel<Tin, Tout, R4, false>, grid, stream,        \
+                                      TTT_REC_ARGS)
+#define TTT_REC_ARGS                                                                               \
+  (const Tin*)p.q, (const Tin*)p.k, (const Tin*)p.v, (const Tin*)p.g, (const Tin*)p.beta, p.S,     \
+      (Tout*)p.out, p.N, p.dk, p.dv, p.scale
   TTT_BY_ROWS(p.dk, TTT_REC)
 #undef TTT_REC_ARGS
 #undef TTT_REC
@@ -953,21 +976,19 @@ int bwd_launch(const DeltaBwdLaunch& L, cudaStream_t stream) {
   float* du = reinterpret_cast<float*>(L.ws + w.du);
   float* Sc = reinterpret_cast<float*>(L.ws + w.Sc);
   float* Xc = reinterpret_cast<float*>(L.ws + w.Xc);
-  if (rec_launch<Tin, float>(p, nullptr, L.S0, nullptr, ev, Sc, stream)) return -1;
-  const dim3 grid((unsigned)BH, (unsigned)((p.dv + COLS - 1) / COLS));
-  prof_before(K_DELTA_REV, stream);
-  const bool help = rec_helped(p);
+  const StatesArgs<Tin> states{(const Tin*)p.q, (const Tin*)p.k, (const Tin*)p.v, (const Tin*)L.dout,
+                               (const Tin*)p.g, (const Tin*)p.beta, L.S0, L.dS_end, L.dS0, ev, du, Sc, Xc,
+                               p.N, p.dk, p.dv, p.scale};
+  const dim3 grid = cols_grid(p, 2);
+  const bool help = helped(p, grid);
   int err = 0;
-#define TTT_REV(R4)                                                                               \
-  err = help ? launch_rec<R4, true>(delta_rev_kernel<Tin, R4, true>, grid, stream, TTT_REV_ARGS)  \
-             : launch_rec<R4, false>(delta_rev_kernel<Tin, R4, false>, grid, stream, TTT_REV_ARGS)
-#define TTT_REV_ARGS                                                                              \
-  (const Tin*)p.q, (const Tin*)p.k, (const Tin*)L.dout, (const Tin*)p.g, (const Tin*)p.beta,      \
-      L.dS_end, L.dS0, du, Xc, p.N, p.dk, p.dv, p.scale
-  TTT_BY_ROWS(p.dk, TTT_REV)
-#undef TTT_REV_ARGS
-#undef TTT_REV
-  prof_after(K_DELTA_REV, stream);
+  prof_before(K_DELTA_STATES, stream);
+#define TTT_STATES(R4)                                                                             \
+  err = help ? launch_cols<R4, true>(delta_states_kernel<Tin, R4, true>, grid, stream, states)     \
+             : launch_cols<R4, false>(delta_states_kernel<Tin, R4, false>, grid, stream, states)
+  TTT_BY_ROWS(p.dk, TTT_STATES)
+#undef TTT_STATES
+  prof_after(K_DELTA_STATES, stream);
   if (err) return -1;
   const size_t smem = chunk_grad_smem(p.dk, p.dv);
   void (*kfn)(ChunkArgs<Tin>) = nullptr;
@@ -1003,11 +1024,11 @@ int bwd_launch(const DeltaBwdLaunch& L, cudaStream_t stream) {
 
 int launch_delta_rec(const DeltaLaunch& p, cudaStream_t stream) {
   if (p.in_bf16) {
-    if (p.out_bf16) return rec_launch<__nv_bfloat16, __nv_bfloat16>(p, p.S, p.S, (__nv_bfloat16*)p.out, nullptr, nullptr, stream);
-    return rec_launch<__nv_bfloat16, float>(p, p.S, p.S, (float*)p.out, nullptr, nullptr, stream);
+    if (p.out_bf16) return rec_launch<__nv_bfloat16, __nv_bfloat16>(p, stream);
+    return rec_launch<__nv_bfloat16, float>(p, stream);
   }
-  if (p.out_bf16) return rec_launch<float, __nv_bfloat16>(p, p.S, p.S, (__nv_bfloat16*)p.out, nullptr, nullptr, stream);
-  return rec_launch<float, float>(p, p.S, p.S, (float*)p.out, nullptr, nullptr, stream);
+  if (p.out_bf16) return rec_launch<float, __nv_bfloat16>(p, stream);
+  return rec_launch<float, float>(p, stream);
 }
 
 DeltaBwdWorkspace delta_rec_bwd_layout(int BH, int N, int dk, int dv) {
@@ -1035,7 +1056,7 @@ int launch_delta_step(const DeltaLaunch& p, const int* slots, int n_slots, cudaS
   // columns of a CTA: a slice of 32 is one 128-byte line of every state row and
   // 16 KB in all, so that a dozen CTAs of an SM keep loads and stores mixed;
   // half of it where rows and heads do not fill the device
-  const int vc = (long long)p.B * p.H * ((p.dv + 31) / 32) < 4 * 148 ? 16 : 32;
+  const int vc = (long long)p.B * p.H * ((p.dv + 31) / 32) < 4 * p.sms ? 16 : 32;
   const dim3 grid((unsigned)p.B, (unsigned)p.H, (unsigned)((p.dv + vc - 1) / vc));
 #define TTT_STEP_VC(TI, TO, VC)                                                                    \
   delta_step_kernel<TI, TO, VC><<<grid, STHREADS, 0, stream>>>(                                    \

@@ -170,6 +170,25 @@ def test_gates(cuda_device, gates, dt, dk, dv):
     p.check_bwd(p.bwd())
 
 
+@pytest.mark.parametrize("d,N", [(64, 65), (64, 128), (64, 130), (64, 200), (128, 45), (128, 129)])
+@pytest.mark.parametrize("gates", [None] + sorted(GATES))
+def test_short_sequences_of_many_heads(cuda_device, gates, d, N):
+    """Enough heads for the chunk form at every one of these lengths."""
+    p = Problem(2, 10240 // d // 2, N, d, d, "bf16", **GATES.get(gates, {}))
+    p.check_fwd(p.fwd())
+    p.check_bwd(p.bwd())
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("N", [283, 385, 500])
+def test_gates_in_the_chunk_form(cuda_device, d, N):
+    """One head: longer sequences than the token form takes."""
+    for gates in sorted(GATES):
+        p = Problem(1, 1, N, d, d, "bf16", **GATES[gates])
+        p.check_fwd(p.fwd())
+        p.check_bwd(p.bwd())
+
+
 @pytest.mark.parametrize("d", [64, 128])
 def test_equal_keys(cuda_device, d):
     """Every key the same, full steps, no decay: (I + A) is the all-ones triangle,
