@@ -898,17 +898,17 @@ int fwd_launch(const DeltaLaunch& p, cudaStream_t stream) {
 // Short sequences go token by token: the chunk kernels' latency is that of a
 // whole chunk and of three launches (23 us forward, 47 us backward at D = 64;
 // 32 and 60 at 128), the recurrent ones' 0.09 us a token at D = 64 and 0.14 at
-// 128 (backward 0.11 and 0.16, behind 17 and 36), times the rounds that their
+// 128 (backward 0.11 and 0.16, behind 17 and 31), times the rounds that their
 // CTAs of 16 value columns take on the device.  Both grow alike with the heads
 // once the chunks too fill it, so rounds count up to 5.  Token by token against
 // chunks, us: forward 8 heads of 64, 128 tokens 16 / 17, 256 tokens 28 / 23;
 // 128 heads, 32 tokens 15 / 23, 64 tokens 25 / 23.  Backward 8 heads of 64, 256
-// tokens 44 / 48, 512 tokens 69 / 50; of 128, 64 tokens 50 / 59, 256 tokens 79 /
+// tokens 44 / 48, 512 tokens 69 / 50; of 128, 128 tokens 57 / 60, 256 tokens 75 /
 // 62; 128 heads of 64, 32 tokens 41 / 52, 64 tokens 63 / 52.
 bool delta_uses_umma(int bf16, int dk, int dv, long long BH, int N, int sms, bool backward) {
   if (!bf16 || dk != dv || (dk != 64 && dk != 128)) return false;
   const double rounds = (double)BH * (dv / 16) * (backward ? 2 : 1) / sms;
-  return N * std::min(std::max(rounds, 1.0), 5.0) > (!backward ? 190 : dk == 64 ? 270 : 130);
+  return N * std::min(std::max(rounds, 1.0), 5.0) > (!backward ? 190 : dk == 64 ? 270 : 150);
 }
 
 DeltaUmmaWorkspace delta_umma_layout(int BH, int N, int D, int sms) {
