@@ -172,6 +172,9 @@ TTT_DEVICE_INLINE void invert(float* A, int warp, int lane) {
 }
 
 // ------------------------------------------------------------------ prep
+// A chunk takes about 22 us with two CTAs an SM (heads of 64), a third of it
+// the inverse, the rest the latency of two rounds of products, splits and
+// stores: 2048 chunks 164 us, and no unit is more than half busy.
 struct PrepArgs {
   const __nv_bfloat16 *g, *beta;
   float* gend;             // [BH nch] exp(G_last)
@@ -415,7 +418,8 @@ TTT_DEVICE_INLINE void prep_cta(uint8_t* smem, const CUtensorMap& mapK, const CU
 // the stores, 4 to 11 hold X (32 columns of a row a thread; the others rest).
 // While the tensor core works, those add e X + H.  With sixteen warps that did
 // everything between two CTA barriers, the warps beside the issuing ones
-// were last to every barrier.
+// were last to every barrier.  A chunk takes 1.0 us at D = 64 and 1.7 at 128
+// (that form: 1.5 and 2.1).
 struct ChainArgs {
   const float* gend;
   DeltaChain dir[2];       // forward, backward

@@ -52,7 +52,9 @@ TTT_DEVICE_INLINE float row_total(const float* red, int row) {
 
 // ------------------------------------------------------------------ Hb
 // Hb is what dS0 is made of, in float32: its operands are carried in three
-// planes (hi + lo alone left 3e-6 of dS0, mostly by scale gam dO).
+// planes (hi + lo alone left 3e-6 of dS0, mostly by scale gam dO).  Its shared
+// memory leaves one CTA an SM, whose phases' latency bounds it: 2048 chunks of
+// heads of 64 116 us.
 struct HbArgs {
   const __nv_bfloat16 *g, *beta;
   float* H;
@@ -179,6 +181,8 @@ __global__ void __launch_bounds__(THREADS, 1)
 }
 
 // ------------------------------------------------------------------ values
+// Bound by HBM, which it reads T, W, Ut, the border states and what Hb left
+// from: 2048 chunks of heads of 64 134 us, 4.6 TB/s.
 struct ValsArgs {
   const __nv_bfloat16 *g, *beta, *v;
   const float* Ut;
@@ -329,6 +333,8 @@ __global__ void __launch_bounds__(THREADS, 1)
 }
 
 // ------------------------------------------------------------------ keys
+// One CTA an SM, by its shared memory; bound by the latency of its four rounds
+// of products: 2048 chunks of heads of 64 187 us.
 struct KeysArgs {
   const __nv_bfloat16 *g, *beta;
   __nv_bfloat16 *dq, *dk;
