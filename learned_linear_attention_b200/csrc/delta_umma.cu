@@ -902,7 +902,7 @@ int fwd_launch(const DeltaLaunch& p, cudaStream_t stream) {
 // Short sequences go token by token: the chunk kernels' latency is that of a
 // whole chunk and of three launches (23 us forward, 47 us backward at D = 64;
 // 32 and 60 at 128), the recurrent ones' 0.09 us a token at D = 64 and 0.14 at
-// 128 (backward 0.11 and 0.16, behind 17 and 31), times the rounds that their
+// 128 (backward 0.11 and 0.16, behind 15 and 31), times the rounds that their
 // CTAs of 16 value columns take on the device.  Both grow alike with the heads
 // once the chunks too fill it, so rounds count up to 5.  Token by token against
 // chunks, us: forward 8 heads of 64, 128 tokens 16 / 17, 256 tokens 28 / 23;

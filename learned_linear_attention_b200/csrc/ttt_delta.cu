@@ -519,7 +519,7 @@ __global__ void __launch_bounds__(HELP ? 2 * THREADS : THREADS) delta_states_ker
 //   dv_i = R_i,  dbeta_i = du_i . e_i
 //   dg_t = sum_{i >= t} (q_i . dq_i + k_i . [read part of dk_i] - k_i . [write part]) + <X1, S1>
 // One CTA per chunk and head, every matrix in shared memory, whose reads and
-// the latency of the phases bound it: 12 us for one chunk of heads of 64.
+// the latency of the phases bound it: 10 us for one chunk of heads of 64.
 constexpr int CB = TT;          // tokens of a chunk
 constexpr int GTHREADS = 256;
 
@@ -625,9 +625,20 @@ __global__ void __launch_bounds__(GTHREADS) delta_chunk_grad_kernel(ChunkArgs<Ti
       duv[i][b] = in && r < dv ? p.duv[av] : 0.f;
     }
   }
+  const Tin gv = p.g != nullptr && lane < n ? p.g[tok + lane] : zero;
+  constexpr int UX = R4 == 4 ? 4 : 8;   // loads in flight, beside the rows in registers
+  float xs = 0.f;   // <X1, S1>
+  if (mat % 4 == 0) {
+#pragma unroll UX
+    for (int e = 4 * tid; e < (int)mat; e += 4 * GTHREADS)
+      xs = dot4(*reinterpret_cast<const float4*>(X1 + e), *reinterpret_cast<const float4*>(S1 + e), xs);
+  } else {
+#pragma unroll 8
+    for (int e = tid; e < (int)mat; e += GTHREADS) xs = fmaf(X1[e], S1[e], xs);
+  }
   if (warp == 0) {
     // exp(-200) is 0 in float32: a cleared state keeps G finite
-    const float gi = p.g != nullptr && lane < n ? to_f(p.g[tok + lane]) : 0.f;
+    const float gi = to_f(gv);
     double acc = gi < -200.f ? -200.0 : (double)gi;   // NaN stays
     for (int o = 1; o < 32; o <<= 1) {
       const double y = __shfl_up_sync(0xffffffffu, acc, o);
@@ -635,15 +646,6 @@ __global__ void __launch_bounds__(GTHREADS) delta_chunk_grad_kernel(ChunkArgs<Ti
     }
     G[lane] = acc;
   }
-  float xs = 0.f;   // <X1, S1>
-#pragma unroll 4
-  for (int r = warp; r < dk; r += WARPS)
-#pragma unroll
-    for (int b = 0; b < R4; ++b)
-      if (lane + 32 * b < dv) {
-        const size_t at = (size_t)r * dv + lane + 32 * b;
-        xs = fmaf(X1[at], S1[at], xs);
-      }
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     const int t = warp + WARPS * i;
