@@ -793,7 +793,7 @@ __global__ void __launch_bounds__(THREADS, D == 64 ? 2 : 1)
 
 template <int D>
 int prep_launch(const DeltaLaunch& p, const DeltaPrepOut& o, cudaStream_t stream) {
-  const int BH = p.B * p.H, nch = (p.N + C - 1) / C;
+  const int BH = p.B * p.H, nch = tiles_of(p.N, C);
   const uint64_t nc = (uint64_t)BH * nch, rs = D * 2;
   CUtensorMap mk, mv;
   if (make_tmap_bf16_3d(&mk, p.k, D, p.N, BH, rs, p.N * rs, 64, C) ||
@@ -814,7 +814,7 @@ int prep_launch(const DeltaLaunch& p, const DeltaPrepOut& o, cudaStream_t stream
 template <int D>
 int chain_launch(const DeltaLaunch& p, const float* gend, const __nv_bfloat16* M, const DeltaChain* fwd,
                  const DeltaChain* rev, cudaStream_t stream) {
-  const int BH = p.B * p.H, nch = (p.N + C - 1) / C;
+  const int BH = p.B * p.H, nch = tiles_of(p.N, C);
   const uint64_t nc = (uint64_t)BH * nch, rs = D * 2;
   CUtensorMap mm, mf, mr;
   if (make_tmap_bf16_3d(&mm, M, D, D, 2 * nc, rs, D * rs, 64, D) ||
@@ -849,7 +849,7 @@ int slab_chunks(int BH, int nch, int D, int sms) {
 
 template <int D>
 int fwd_launch(const DeltaLaunch& p, cudaStream_t stream) {
-  const int BH = p.B * p.H, nch = (p.N + C - 1) / C, len = slab_chunks(BH, nch, D, p.sms);
+  const int BH = p.B * p.H, nch = tiles_of(p.N, C), len = slab_chunks(BH, nch, D, p.sms);
   const int slabs = (nch + len - 1) / len;
   const DeltaUmmaWorkspace w = delta_umma_layout(BH, p.N, D, p.sms);
   const uint64_t nc = w.chunks, rs = D * 2;
@@ -917,7 +917,7 @@ bool delta_uses_umma(int bf16, int dk, int dv, long long BH, int N, int sms, boo
 
 DeltaUmmaWorkspace delta_umma_layout(int BH, int N, int D, int sms) {
   DeltaUmmaWorkspace w{};
-  const int nch = (N + C - 1) / C, len = slab_chunks(BH, nch, D, sms);
+  const int nch = tiles_of(N, C), len = slab_chunks(BH, nch, D, sms);
   const size_t nc = (size_t)BH * std::min(nch, 3 * len);
   w.chunks = nc;
   size_t at = 512;   // see delta_ws_base

@@ -612,7 +612,7 @@ __global__ void __launch_bounds__(C) delta_gate_grad_kernel(GateArgs a) {
 template <int D>
 int bwd_launch(const DeltaBwdLaunch& L, cudaStream_t stream) {
   const DeltaLaunch& p = L.f;
-  const int BH = p.B * p.H, nch = (p.N + C - 1) / C;
+  const int BH = p.B * p.H, nch = tiles_of(p.N, C);
   constexpr int DA = D / 64;
   const DeltaUmmaBwdWorkspace w = delta_umma_bwd_layout(BH, p.N, D);
   const uint64_t nc = (uint64_t)BH * nch, rs = D * 2;
@@ -676,7 +676,7 @@ int bwd_launch(const DeltaBwdLaunch& L, cudaStream_t stream) {
 
 DeltaUmmaBwdWorkspace delta_umma_bwd_layout(int BH, int N, int D) {
   DeltaUmmaBwdWorkspace w{};
-  const size_t nc = (size_t)BH * ((N + C - 1) / C), tokens = (size_t)BH * N, DA = D / 64;
+  const size_t nc = (size_t)BH * tiles_of(N, C), tokens = (size_t)BH * N, DA = D / 64;
   size_t at = 512;
   auto take = [&](size_t bytes) {
     const size_t o = at;

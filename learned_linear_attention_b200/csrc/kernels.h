@@ -132,6 +132,10 @@ struct LinearBwdLaunch {
 int launch_ttt_linear_bwd(const LinearBwdLaunch& L, cudaStream_t stream);
 
 // ----------------------------------------------------------------- delta rule
+// Tiles of `size` tokens that n >= 0 tokens take; n may be as large as 2^31 - 1,
+// where n + size - 1 would overflow.
+__host__ __device__ inline int tiles_of(int n, int size) { return n / size + (n % size != 0); }
+
 struct DeltaLaunch {
   int B, H, N, dk, dv, sms;
   float scale;

@@ -368,7 +368,7 @@ TTT_DEVICE_INLINE void rec_cta(Stage<R4>* st, const Tin* __restrict__ q, const T
 #pragma unroll
     for (int i = 0; i < 4 * R4; ++i) s[i] = 0.f;
   }
-  const int nch = (N + TT - 1) / TT;
+  const int nch = tiles_of(N, TT);
   Fetch<Tin, R4> f(k, KEEP ? nullptr : q, v, g, beta, bh, N, dk, dv, c0, tid % THREADS);
   walk_tiles<Tin, R4, HELP>(
       st, f, nch, false, 1.f, tid,
@@ -474,7 +474,7 @@ TTT_DEVICE_INLINE void rev_cta(Stage<R4>* st, const Tin* __restrict__ q, const T
 #pragma unroll
     for (int i = 0; i < 4 * R4; ++i) x[i] = 0.f;
   }
-  const int nch = (N + TT - 1) / TT;
+  const int nch = tiles_of(N, TT);
   Fetch<Tin, R4> f(k, q, dout, g, beta, bh, N, dk, dv, c0, tid % THREADS);
   walk_tiles<Tin, R4, HELP>(
       st, f, nch, true, scale, tid,
@@ -992,7 +992,7 @@ int rec_launch(const DeltaLaunch& p, cudaStream_t stream) {
 template <typename Tin>
 int bwd_launch(const DeltaBwdLaunch& L, cudaStream_t stream) {
   const DeltaLaunch& p = L.f;
-  const int BH = p.B * p.H, nch = (p.N + CB - 1) / CB;
+  const int BH = p.B * p.H, nch = tiles_of(p.N, CB);
   const DeltaBwdWorkspace w = delta_rec_bwd_layout(BH, p.N, p.dk, p.dv);
   float* ev = reinterpret_cast<float*>(L.ws + w.ev);
   float* du = reinterpret_cast<float*>(L.ws + w.du);
@@ -1061,7 +1061,7 @@ DeltaBwdWorkspace delta_rec_bwd_layout(int BH, int N, int dk, int dv) {
     at += (floats * sizeof(float) + 255) / 256 * 256;
     return o;
   };
-  const size_t nch = (N + CB - 1) / CB, mat = (size_t)dk * dv;
+  const size_t nch = tiles_of(N, CB), mat = (size_t)dk * dv;
   w.ev = take((size_t)BH * N * dv);
   w.du = take((size_t)BH * N * dv);
   w.Sc = take((size_t)BH * (nch + 1) * mat);

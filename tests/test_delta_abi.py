@@ -191,3 +191,32 @@ def test_layer_refusals():
     assert call(T.make_delta_desc(1, 2, 8, 60, 64)) == T.TTT_ERR_ALIGN
     assert call(T.make_delta_desc(1, 2, 8, 64, 64, out_dtype="f32")) == T.TTT_ERR_DTYPE
     assert call(T.make_delta_desc(1, 2, 0, 64, 64)) == T.TTT_OK
+
+
+def _bytes(fn, d):
+    n = ctypes.c_size_t(0)
+    assert getattr(T.load(), fn)(ctypes.byref(d), ctypes.byref(n)) == T.TTT_OK
+    return n.value
+
+
+def test_workspace_of_the_longest_sequences():
+    """Tiles of 32 and chunks of 128 tokens are counted without a sum that passes
+    2^31: the sizes follow the layouts' formulas up to the largest N."""
+    up = lambda n: -(-n // 256) * 256  # noqa: E731
+    for N in [(1 << 31) - i for i in (1, 2, 31, 32, 33, 100, 127, 128, 129, 200)]:
+        # token by token: e and du of every token, states at the borders of tiles
+        tiles = -(-N // 32)
+        for dk, dv in ((1, 1), (3, 2)):
+            want = 256 + 2 * up(4 * N * dv) + up(4 * (tiles + 1) * dk * dv) + up(4 * tiles * dk * dv)
+            assert _bytes("ttt_delta_bwd_workspace_bytes", T.make_delta_desc(1, 1, N, dk, dv)) == want
+        for D in (64, 128):
+            d, chunks, slices = T.make_delta_desc(1, 1, N, D, D), -(-N // 128), D // 64
+            pair, mat = 2 * 128 * D * 2, 4 * D * D
+            # W, U, Ut, Y; T; M, H, Hb and two border states; sums of tokens and chunks
+            want = 512 + up(4 * chunks) + 4 * up(pair * chunks) + up(chunks * 2 * 128 * 128 * 2) + 5 * up(mat * chunks)
+            want += 3 * up(4 * slices * N) + up(4 * N) + up(4 * slices * chunks)
+            assert _bytes("ttt_delta_bwd_workspace_bytes", d) == want
+            # forward: at most three slabs, at least one chunk in six
+            one = 4 + 2 * pair + 3 * mat
+            assert chunks / 6 * one <= _bytes("ttt_delta_workspace_bytes", d) <= (chunks + 8) * one + 4096
+            assert _bytes("ttt_delta_layer_workspace_bytes", d) >= _bytes("ttt_delta_workspace_bytes", d) + 3 * N * D * 2
