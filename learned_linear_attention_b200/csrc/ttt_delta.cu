@@ -349,7 +349,7 @@ TTT_DEVICE_INLINE void rec_tile(Stage<R4>& st, float (&s)[4 * R4], int n, float 
 
 // One CTA's 16 columns over the whole sequence.  KEEP: the backward pass's
 // replay, whose rows are e (ev [BH][N][dv]) in place of out, and which keeps
-// the state at every chunk border (TT tokens), Sc [BH][nch + 1][dk][dv].
+// the state at the start of every chunk (TT tokens), Sc [BH][nch][dk][dv].
 template <typename Tin, typename Tout, int R4, bool HELP, bool KEEP>
 TTT_DEVICE_INLINE void rec_cta(Stage<R4>* st, const Tin* __restrict__ q, const Tin* __restrict__ k,
                                const Tin* __restrict__ v, const Tin* __restrict__ g,
@@ -373,15 +373,14 @@ TTT_DEVICE_INLINE void rec_cta(Stage<R4>* st, const Tin* __restrict__ q, const T
   walk_tiles<Tin, R4, HELP>(
       st, f, nch, false, 1.f, tid,
       [&](int t0) {
-        if constexpr (KEEP) col.store(Sc + (bh * (nch + 1) + t0 / TT) * mat, s);
+        if constexpr (KEEP) col.store(Sc + (bh * nch + t0 / TT) * mat, s);
       },
       [&](Stage<R4>& t, int t0) { rec_tile<R4, !KEEP>(t, s, min(TT, N - t0), scale, col.l, cl); },
       [&](const Stage<R4>& t, int t0, int h) {
         write_os(t, rows + (bh * N + t0) * dv, min(TT, N - t0), dv, c0, h);
       });
-  if (!state) return;
-  if constexpr (KEEP) col.store(Sc + (bh * (nch + 1) + nch) * mat, s);
-  else col.store(S_out + bh * mat, s);
+  if constexpr (!KEEP)
+    if (state) col.store(S_out + bh * mat, s);
 }
 template <typename Tin, typename Tout, int R4, bool HELP>
 __global__ void __launch_bounds__(HELP ? 2 * THREADS : THREADS)
@@ -509,15 +508,20 @@ __global__ void __launch_bounds__(HELP ? 2 * THREADS : THREADS) delta_states_ker
 }
 
 // ------------------------------------------------------------------ a chunk's gradients
-// With the states S0 at the chunk's start and S1 at its end, X1 = dL/dS at
-// its end, and every token's e and du, the chunk's gradients need no
-// recurrence.  G: the decay's running sum in the chunk, Gam_ij = exp(G_i -
+// With the state S0 at the chunk's start, X1 = dL/dS at its end, and every
+// token's e and du, the chunk's gradients need no recurrence.  G: the decay's running sum in the chunk, Gam_ij = exp(G_i -
 // G_j), gam_i = exp(G_i), rho_j = exp(G_end - G_j), U = beta e, R = beta du:
 //   Mq_ij = (scale do_i . U_j) Gam_ij (j <= i),  Mk_ij = -(R_i . U_j) Gam_ij (j < i)
 //   dq_i = gam_i S0 (scale do_i) + sum_j Mq_ij k_j
 //   dk_i = [-gam_i S0 R_i + sum_j Mk_ij k_j] + [sum_j (Mq_ji q_j + Mk_ji k_j) + rho_i X1 U_i]
 //   dv_i = R_i,  dbeta_i = du_i . e_i
-//   dg_t = sum_{i >= t} (q_i . dq_i + k_i . [read part of dk_i] - k_i . [write part]) + <X1, S1>
+//   dg_t = sum_{i >= t} gam_i (q_i . S0 (scale do_i) - k_i . S0 R_i)
+//          + sum_{i >= t > j} (Mq_ij q_i . k_j + Mk_ij k_i . k_j)
+//          + sum_{i < t} rho_i k_i . X1 U_i + gam_end <X1, S0>
+// (every term of dg_t holds the decay of token t.  The sums over dq and dk of
+// the tokens i >= t less those of dk as a written key are the same, but pairs of
+// tokens behind t then enter with both signs, and where the decays are strong
+// what is left of them is larger than dg_t.)
 // One CTA per chunk and head, every matrix in shared memory, whose reads and
 // the latency of the phases bound it: 10 us for one chunk of heads of 64.
 constexpr int CB = TT;          // tokens of a chunk
@@ -533,12 +537,14 @@ struct ChunkArgs {
 };
 
 // Shared memory: pitches are 4 (mod 8) floats, so that 16-byte reads down a
-// column of rows meet different banks; everything behind dv in a row is zero.
+// column of rows meet different banks; everything behind dv or dk in a row is zero.
 struct GradSmem {
   int ms;                                  // pitch of a value row
+  int ks;                                  // pitch of a key row
   size_t S0, X1, Q, K, D, U, R, Mq, Mk, floats;
   __host__ __device__ GradSmem(int dk, int dv) {
     ms = (dv + 7) / 8 * 8 + 4;
+    ks = (dk + 7) / 8 * 8 + 4;
     S0 = 0;
     X1 = S0 + (size_t)dk * ms;
     D = X1 + (size_t)dk * ms;
@@ -547,8 +553,8 @@ struct GradSmem {
     Mq = R + CB * ms;
     Mk = Mq + CB * MP;
     Q = Mk + CB * MP;
-    K = Q + CB * dk;
-    floats = K + CB * dk;
+    K = Q + CB * ks;
+    floats = K + CB * ks;
   }
   static constexpr int MP = CB + 4;        // pitch of Mq, Mk
 };
@@ -570,16 +576,15 @@ __global__ void __launch_bounds__(GTHREADS) delta_chunk_grad_kernel(ChunkArgs<Ti
   static_assert(CB == 4 * WARPS && CB == 32, "a warp takes four tokens, the gates are one warp's");
   const int dk = p.dk_, dv = p.dv_, N = p.N, tid = threadIdx.x, warp = tid / 32, lane = tid & 31;
   const GradSmem L_(dk, dv);
-  const int ms = L_.ms;
+  const int ms = L_.ms, ks = L_.ks;
   float *S0s = sm + L_.S0, *X1s = sm + L_.X1, *Q = sm + L_.Q, *K = sm + L_.K;
   float *D = sm + L_.D, *U = sm + L_.U, *R = sm + L_.R, *Mq = sm + L_.Mq, *Mk = sm + L_.Mk;
   __shared__ double G[CB];
-  __shared__ float red[WARPS], row_s[CB];
+  __shared__ float red[WARPS], row_s[CB], row_w[CB], corner[WARPS][CB];
   const size_t bh = blockIdx.y;
   const int ch = blockIdx.x, t0 = ch * CB, n = min(CB, N - t0), nch = gridDim.x;
   const size_t mat = (size_t)dk * dv, tok = bh * N + t0;
-  const float* S0 = p.Sc + (bh * (nch + 1) + ch) * mat;
-  const float* S1 = S0 + mat;
+  const float* S0 = p.Sc + (bh * nch + ch) * mat;
   const float* X1 = p.Xc + (bh * nch + ch) * mat;
 
   if (dv % 4 == 0) {   // (four floats at a time: 128 x 128 alone take 33,000 copies of one)
@@ -627,14 +632,14 @@ __global__ void __launch_bounds__(GTHREADS) delta_chunk_grad_kernel(ChunkArgs<Ti
   }
   const Tin gv = p.g != nullptr && lane < n ? p.g[tok + lane] : zero;
   constexpr int UX = R4 == 4 ? 4 : 8;   // loads in flight, beside the rows in registers
-  float xs = 0.f;   // <X1, S1>
+  float xs = 0.f;   // <X1, S0>
   if (mat % 4 == 0) {
 #pragma unroll UX
     for (int e = 4 * tid; e < (int)mat; e += 4 * GTHREADS)
-      xs = dot4(*reinterpret_cast<const float4*>(X1 + e), *reinterpret_cast<const float4*>(S1 + e), xs);
+      xs = dot4(*reinterpret_cast<const float4*>(X1 + e), *reinterpret_cast<const float4*>(S0 + e), xs);
   } else {
 #pragma unroll 8
-    for (int e = tid; e < (int)mat; e += GTHREADS) xs = fmaf(X1[e], S1[e], xs);
+    for (int e = tid; e < (int)mat; e += GTHREADS) xs = fmaf(X1[e], S0[e], xs);
   }
   if (warp == 0) {
     // exp(-200) is 0 in float32: a cleared state keeps G finite
@@ -654,9 +659,9 @@ __global__ void __launch_bounds__(GTHREADS) delta_chunk_grad_kernel(ChunkArgs<Ti
 #pragma unroll
     for (int b = 0; b < R4; ++b) {
       const int r = lane + 32 * b;
-      if (r < dk) {
-        Q[t * dk + r] = to_f(qv[i][b]);
-        K[t * dk + r] = to_f(kv[i][b]);
+      if (r < ks) {
+        Q[t * ks + r] = to_f(qv[i][b]);
+        K[t * ks + r] = to_f(kv[i][b]);
       }
       if (r < ms) {
         const float rv = bt * duv[i][b];
@@ -670,6 +675,7 @@ __global__ void __launch_bounds__(GTHREADS) delta_chunk_grad_kernel(ChunkArgs<Ti
     for (int o = 16; o > 0; o >>= 1) db += __shfl_xor_sync(0xffffffffu, db, o);
     if (lane == 0 && t < n) p.dbeta[tok + t] = from_f<Tin>(db);
     // a full last group leaves the row's last four floats to this
+    if (32 * R4 + lane < ks) Q[t * ks + 32 * R4 + lane] = K[t * ks + 32 * R4 + lane] = 0.f;
     if (32 * R4 + lane < ms) D[t * ms + 32 * R4 + lane] = U[t * ms + 32 * R4 + lane] = R[t * ms + 32 * R4 + lane] = 0.f;
   }
   for (int o = 16; o > 0; o >>= 1) xs += __shfl_xor_sync(0xffffffffu, xs, o);
@@ -694,8 +700,34 @@ __global__ void __launch_bounds__(GTHREADS) delta_chunk_grad_kernel(ChunkArgs<Ti
     for (int a = 0; a < 4; ++a) {
       const int i = warp + WARPS * a;
       const float f = j <= i ? expf((float)(G[i] - G[j])) : 0.f;
-      Mq[i * MP + j] = j <= i ? mq[a] * f : 0.f;
-      Mk[i * MP + j] = j < i ? -mk[a] * f : 0.f;
+      Mq[i * MP + j] = mq[a] = j <= i ? mq[a] * f : 0.f;
+      Mk[i * MP + j] = mk[a] = j < i ? -mk[a] * f : 0.f;
+    }
+    if (p.dg != nullptr) {   // the pairs' part of dg
+      float qk[4] = {0.f, 0.f, 0.f, 0.f}, kk[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 2
+      for (int c = 0; c < dk; c += 4) {
+        const float4 k = at4(K + j * ks + c);
+#pragma unroll
+        for (int a = 0; a < 4; ++a) {
+          const int i = warp + WARPS * a;
+          qk[a] = dot4(at4(Q + i * ks + c), k, qk[a]);
+          kk[a] = dot4(at4(K + i * ks + c), k, kk[a]);
+        }
+      }
+      float sum = 0.f;
+#pragma unroll
+      for (int a = 0; a < 4; ++a) {
+        const int i = warp + WARPS * a;
+        float v = j < i ? fmaf(mq[a], qk[a], mk[a] * kk[a]) : 0.f;
+        for (int o = 1; o < 32; o <<= 1) {
+          const float y = __shfl_up_sync(0xffffffffu, v, o);
+          if (lane >= o) v += y;
+        }
+        v = __shfl_up_sync(0xffffffffu, v, 1);   // lane t: the sum over j < t
+        if (lane > 0 && lane <= i) sum += v;
+      }
+      corner[warp][lane] = sum;
     }
   }
   __syncthreads();
@@ -731,6 +763,24 @@ __global__ void __launch_bounds__(GTHREADS) delta_chunk_grad_kernel(ChunkArgs<Ti
     const float gam = expf((float)G[i0 + a]), rho = expf((float)(G[CB - 1] - G[i0 + a]));
 #pragma unroll
     for (int b = 0; b < R4; ++b) { dqv[a][b] *= gam; dkr[a][b] *= -gam; dkw[a][b] *= rho; }
+    if (p.dg != nullptr) {   // the states' part of dg
+      float s = 0.f, w = 0.f;
+#pragma unroll
+      for (int b = 0; b < R4; ++b) {
+        const int r = lane + 32 * b;
+        if (r >= dk) continue;
+        s = fmaf(Q[(i0 + a) * ks + r], dqv[a][b], fmaf(K[(i0 + a) * ks + r], dkr[a][b], s));
+        w = fmaf(K[(i0 + a) * ks + r], dkw[a][b], w);
+      }
+      for (int o = 16; o > 0; o >>= 1) {
+        s += __shfl_xor_sync(0xffffffffu, s, o);
+        w += __shfl_xor_sync(0xffffffffu, w, o);
+      }
+      if (lane == 0) {
+        row_s[i0 + a] = s;
+        row_w[i0 + a] = w;
+      }
+    }
   }
 #pragma unroll 2
   for (int j = 0; j < n; ++j) {   // rows and columns of Mq and Mk behind n are zero
@@ -738,8 +788,8 @@ __global__ void __launch_bounds__(GTHREADS) delta_chunk_grad_kernel(ChunkArgs<Ti
 #pragma unroll
     for (int b = 0; b < R4; ++b) {
       const int r = min(lane + 32 * b, dk - 1);
-      kj[b] = K[j * dk + r];
-      qj[b] = Q[j * dk + r];
+      kj[b] = K[j * ks + r];
+      qj[b] = Q[j * ks + r];
     }
     const float4 wq4 = at4(Mq + j * MP + i0), wk4 = at4(Mk + j * MP + i0);
     const float wq[4] = {wq4.x, wq4.y, wq4.z, wq4.w}, wk[4] = {wk4.x, wk4.y, wk4.z, wk4.w};
@@ -757,29 +807,31 @@ __global__ void __launch_bounds__(GTHREADS) delta_chunk_grad_kernel(ChunkArgs<Ti
 #pragma unroll
   for (int a = 0; a < 4; ++a) {
     const int i = i0 + a;
-    float acc = 0.f;
 #pragma unroll
     for (int b = 0; b < R4; ++b) {
       const int r = lane + 32 * b;
       if (r >= dk || i >= n) continue;
       p.dq[(tok + i) * dk + r] = from_f<Tin>(dqv[a][b]);
       p.dk[(tok + i) * dk + r] = from_f<Tin>(dkr[a][b] + dkw[a][b]);
-      acc = fmaf(Q[i * dk + r], dqv[a][b], fmaf(K[i * dk + r], dkr[a][b] - dkw[a][b], acc));
     }
-    for (int o = 16; o > 0; o >>= 1) acc += __shfl_xor_sync(0xffffffffu, acc, o);
-    if (lane == 0) row_s[i] = acc;
   }
   __syncthreads();
   if (warp == 0 && p.dg != nullptr) {
-    float x1s1 = 0.f;
-    for (int w = 0; w < WARPS; ++w) x1s1 += red[w];
-    // the sum over the tokens from this one on
-    float acc = row_s[lane];
-    for (int o = 1; o < 32; o <<= 1) {
-      const float y = __shfl_down_sync(0xffffffffu, acc, o);
-      if (lane + o < 32) acc += y;
+    float x1s0 = 0.f, pairs = 0.f;
+    for (int w = 0; w < WARPS; ++w) {
+      x1s0 += red[w];
+      pairs += corner[w][lane];
     }
-    if (lane < n) p.dg[tok + lane] = from_f<Tin>(acc + x1s1);
+    // reads of the tokens from this one on, writes of those before it
+    float reads = row_s[lane], writes = row_w[lane];
+    for (int o = 1; o < 32; o <<= 1) {
+      const float x = __shfl_down_sync(0xffffffffu, reads, o), y = __shfl_up_sync(0xffffffffu, writes, o);
+      if (lane + o < 32) reads += x;
+      if (lane >= o) writes += y;
+    }
+    writes = __shfl_up_sync(0xffffffffu, writes, 1);
+    if (lane == 0) writes = 0.f;
+    if (lane < n) p.dg[tok + lane] = from_f<Tin>((reads + pairs) + fmaf(expf((float)G[CB - 1]), x1s0, writes));
   }
 }
 
@@ -1033,7 +1085,7 @@ int bwd_launch(const DeltaBwdLaunch& L, cudaStream_t stream) {
     s.dout += t * p.dv; s.dv += t * p.dv; s.ev += t * p.dv; s.duv += t * p.dv;
     s.beta += t; s.dbeta += t;
     if (s.g != nullptr) { s.g += t; s.dg += t; }
-    s.Sc += (size_t)b0 * (nch + 1) * mat;
+    s.Sc += (size_t)b0 * nch * mat;
     s.Xc += (size_t)b0 * nch * mat;
     prof_before(K_DELTA_GRAD, stream);
     kfn<<<dim3((unsigned)nch, (unsigned)nb), GTHREADS, smem, stream>>>(s);
@@ -1064,7 +1116,7 @@ DeltaBwdWorkspace delta_rec_bwd_layout(int BH, int N, int dk, int dv) {
   const size_t nch = tiles_of(N, CB), mat = (size_t)dk * dv;
   w.ev = take((size_t)BH * N * dv);
   w.du = take((size_t)BH * N * dv);
-  w.Sc = take((size_t)BH * (nch + 1) * mat);
+  w.Sc = take((size_t)BH * nch * mat);
   w.Xc = take((size_t)BH * nch * mat);
   w.total = at;
   return w;

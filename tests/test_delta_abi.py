@@ -204,10 +204,10 @@ def test_workspace_of_the_longest_sequences():
     2^31: the sizes follow the layouts' formulas up to the largest N."""
     up = lambda n: -(-n // 256) * 256  # noqa: E731
     for N in [(1 << 31) - i for i in (1, 2, 31, 32, 33, 100, 127, 128, 129, 200)]:
-        # token by token: e and du of every token, states at the borders of tiles
+        # token by token: e and du of every token, two states a tile
         tiles = -(-N // 32)
         for dk, dv in ((1, 1), (3, 2)):
-            want = 256 + 2 * up(4 * N * dv) + up(4 * (tiles + 1) * dk * dv) + up(4 * tiles * dk * dv)
+            want = 256 + 2 * up(4 * N * dv) + 2 * up(4 * tiles * dk * dv)
             assert _bytes("ttt_delta_bwd_workspace_bytes", T.make_delta_desc(1, 1, N, dk, dv)) == want
         for D in (64, 128):
             d, chunks, slices = T.make_delta_desc(1, 1, N, D, D), -(-N // 128), D // 64

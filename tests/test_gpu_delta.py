@@ -463,3 +463,33 @@ def test_memory_of_the_host_is_refused(cuda_device):
     assert T.ttt_delta_fwd(d, x["q"].cpu(), x["k"], x["v"], x["g"], x["beta"], S, out, ws, check=False) == T.TTT_ERR_ARG
     assert T.ttt_delta_fwd(d, x["q"], x["k"], x["v"], x["g"], x["beta"], S, x["v"], ws, check=False) == T.TTT_ERR_ARG
     assert T.ttt_delta_fwd(d, x["q"], x["k"], x["v"], x["g"], x["beta"], S, out, ws, check=False) == T.TTT_OK
+
+
+# ------------------------------------------------------------------ gradients of strong decays
+DECAYS = {"-4": -4.0, "-8": -8.0, "-12": -12.0, "-16": -16.0, "-30": -30.0,
+          # strong decays among weak ones, where terms of the weak ones are e^30 times larger
+          "mixed": np.array([-0.02, -0.02, -0.02, -4, -8, -12, -16, -30])}
+
+
+def check_decay_gradient(p, got):
+    """dg_t = a_t <Y, S_{t-1}> is as small as its own decay a_t = exp(g_t), so it
+    is compared as dg_t / a_t: no term of another token's size may enter it.
+    Tolerance: the gradients' one of check_bwd, r for the type's rounding."""
+    B, H, N, dk, dv = p.shape
+    ref = delta_backward(*(p.host(n) for n in ("q", "k", "v", "g", "beta", "dout", "S0", "dS")))[3]
+    a = np.exp(p.host("g"))
+    near(got[3].double().cpu().numpy() / a, ref / a, HALF[p.dt], 2 * tol(p.dt, dk, dv, N), "dg / a")
+
+
+def strong(dt, N, d, decay, B=1, H=2):
+    return Problem(B, H, N, *d, dt, g_of=lambda r, s: r.choice(np.atleast_1d(DECAYS[decay]), s))
+
+
+@pytest.mark.parametrize("dt,N,d", [("f32", 32, (64, 64)), ("f32", 75, (24, 40)), ("bf16", 100, (128, 128)),
+                                    ("f32", 150, (5, 3))])
+@pytest.mark.parametrize("decay", list(DECAYS))
+def test_gradients_of_strong_decays_token_form(cuda_device, dt, N, d, decay):
+    p = strong(dt, N, d, decay)
+    got = p.bwd()
+    p.check_bwd(got)
+    check_decay_gradient(p, got)
