@@ -241,12 +241,9 @@ struct Phase {
   Waiter W;
   uint64_t* mma;       // completed by mma_commit, one phase per product group
   uint32_t parity;
-  TTT_DEVICE_INLINE bool wait(uint64_t* bar, uint32_t par, uint32_t site) const {
-    const bool ok = W.wait(bar, par, site);
-    return __syncthreads_or(!ok) == 0;
-  }
-  TTT_DEVICE_INLINE bool mma_done(uint32_t site) {
-    const bool ok = wait(mma, parity, site);
+  TTT_DEVICE_INLINE bool mma_done(uint32_t site, bool before = true) {   // before: this thread's waits so far
+    const bool done = W.wait(mma, parity, site);
+    const bool ok = __syncthreads_or(!done || !before) == 0;
     parity ^= 1;
     tc_fence_after();
     return ok;
@@ -282,7 +279,7 @@ struct ChunkId {
   }
 };
 struct Bars {
-  uint64_t load[2], mma;
+  uint64_t load[2], mma, aux, fin;   // aux, fin: of product groups waited for beside those of mma
   uint32_t tmem, abort;
 };
 // Barriers and `cols` TMEM columns, before the first phase; returns the TMEM
@@ -297,6 +294,8 @@ TTT_DEVICE_INLINE uint32_t cta_begin(Bars& b, uint32_t cols, int warp, F loads) 
     mbar_init(&b.load[0], 1);
     mbar_init(&b.load[1], 1);
     mbar_init(&b.mma, 1);
+    mbar_init(&b.aux, 1);
+    mbar_init(&b.fin, 1);
     b.abort = 0;
     fence_barrier_init();
     pdl_wait();

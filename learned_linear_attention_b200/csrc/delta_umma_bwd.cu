@@ -11,17 +11,19 @@
 //   dQ = scale gam dO S0^T + Mq K
 //   dK = [Mk K - gam beta Y S0^T] + [Mq^T Q + Mk^T K] + [rho U X1^T]
 //   dbeta_i = Y_i . (V_i - gam_i S0^T k_i) - sum_j Gam_ij (Y_i . U_j) (k_i . k_j)
-// and, with r_i = q_i . dq_i + k_i . ([first] - [second part of dk_i]) and w_i
-// = k_i . [third part],
-//   dg_t = sum_{i >= t} r_i + sum_{i < t} w_i + gam_last <X1, S0>
-// (the last two terms are <X1, S1> less the w_i of i >= t, written so that no
-// large terms cancel).  So the reverse recurrence runs over the same Mc, side
+// and, with r_i = gam_i (q_i . scale S0 dO_i - beta_i k_i . S0 Y_i), V_ij = Mq_ij
+// q_i . k_j + Mk_ij k_i . k_j (j < i) and w_i = k_i . [third part of dk_i],
+//   dg_t = sum_{i >= t} r_i + sum_{i >= t > j} V_ij + sum_{i < t} w_i + gam_last <X1, S0>
+// where every term holds the decay of token t (sums of q_i . dq_i and k_i . dk_i
+// over i >= t would hold the V_ij of i, j >= t with both signs, and where the
+// decays are strong what rounding leaves of them is larger than dg_t).  So the
+// reverse recurrence runs over the same Mc, side
 // by side with the forward one:
 //   delta_prep_kernel      K, V -> W, Ut, T, Mc, Hc
 //   delta_hb_kernel        Q, K, dO, W -> Hb, -scale P^T dO
 //   delta_chain_kernel     S0 and X1 of every chunk, dS0
 //   delta_vals_kernel      U, Y, dV, first part of dbeta; 64 value columns a CTA
-//   delta_keys_kernel      dQ, dK, r, w, second part of dbeta; 64 key columns a CTA
+//   delta_keys_kernel      dQ, dK, r, w, sums of V, second part of dbeta; 64 key columns a CTA
 //   delta_gate_grad_kernel dg, dbeta
 #include <algorithm>
 
@@ -339,6 +341,7 @@ struct KeysArgs {
   const __nv_bfloat16 *g, *beta;
   __nv_bfloat16 *dq, *dk;
   float *rpart, *wpart;    // [D / 64][BH N]
+  float* cpart;            // [D / 64][BH N]: sum_{i >= t > j} V_ij; nullable: dg not wanted
   float* xpart;            // [D / 64][BH nch]: <X1, S0>
   float* bkey;             // [BH N]
   int N, nch;
@@ -457,8 +460,8 @@ __global__ void __launch_bounds__(THREADS, 1)
       mma_commit(&bars.mma);
     }
     if (!ph.mma_done(4)) return;
-    // Mk, and its row sums against k_i . k_j without beta
-    float db = 0.f;
+    // Mk, and its row sums against k_i . k_j without beta; v: those terms
+    float db = 0.f, v[32];
     const float beta = gates.beta[row];
 #pragma unroll
     for (int b = 0; b < 2; ++b) {
@@ -471,20 +474,30 @@ __global__ void __launch_bounds__(THREADS, 1)
         weigh16<false>(gates, q4 * 32, row, c0, -1.f, x);
 #pragma unroll
         for (int j = 0; j < 16; ++j) {
-          if (c0 + j < row) db = fmaf(x[j], kk[j], db);
+          v[16 * b + j] = c0 + j < row ? x[j] * kk[j] : 0.f;
+          db += v[16 * b + j];
           x[j] *= beta;
         }
       } else {
         zero16(x);
+        zero16(v + 16 * b);
       }
       store16_square(sb + SM::U, row, c0, x);
     }
     red[cg * C + row] = db;
     ph.publish();
     const Op Kmn{sb + SM::Y + id.slice * ATOM, ATOM, true}, Qmn{sb + SM::Y + DA * ATOM, ATOM, true};
-    if (warp == 0 && elect_one()) {
+    // (by a warp whose pairs all lie above the diagonal: issuing takes as long as
+    // the products, and the other warps' sums go on meanwhile)
+    constexpr int ISSUER = 4;
+    if (warp == ISSUER && elect_one()) {
       const Pair Mq{{sb + SM::MQ, ATOM, false}, 2 * ATOM}, Mk{{sb + SM::U, ATOM, false}, 2 * ATOM};
       const Pair Mqt{{sb + SM::MQ, ATOM, true}, 2 * ATOM}, Mkt{{sb + SM::U, ATOM, true}, 2 * ATOM};
+      if (a.cpart != nullptr) {   // q_i . k_j over this slice's columns, first: it is waited for alone
+        products<4>(Prod(tmem + TM_P, Op{sb + SM::Y + DA * ATOM, ATOM, false},
+                         Op{sb + SM::Y + id.slice * ATOM, ATOM, false}, 128, 128, false));
+        mma_commit(&bars.aux);
+      }
       products<8>(Prod(tmem + TM_QK, Mq.lo(), Kmn, 128, 64, false), Prod(tmem + TM_KR, Mk.lo(), Kmn, 128, 64, false),
                   Prod(tmem + TM_KW, Mqt.lo(), Qmn, 128, 64, false));
       products<8>(Prod(tmem + TM_KW, Mkt.lo(), Kmn, 128, 64, true));
@@ -494,7 +507,57 @@ __global__ void __launch_bounds__(THREADS, 1)
       mma_commit(&bars.mma);
     }
     if (cg == 0 && id.slice == 0 && row < id.n) a.bkey[id.tok + row] = row_total(red, row);
-    if (!ph.mma_done(5)) return;
+    // c_t = sum_{i >= t > j} V_ij while the other products run: the sums over j < t
+    // of a row, then over the rows from t on
+    float *vsum = red + 8 * C, *csum = red + 12 * C;   // [column group][row], [32 rows][column]
+    bool ok = true;
+    if (a.cpart != nullptr && cg > q4) {
+      csum[q4 * C + cg * 32 + lane] = 0.f;
+    } else if (a.cpart != nullptr) {
+      ok = ph.W.wait_warp(&bars.aux, 0, 6);
+      tc_fence_after();
+      const float fk = id.slice == 0 ? beta : 0.f;   // k_i . k_j is whole in every slice
+      float total = 0.f;
+#pragma unroll
+      for (int b = 0; b < 2; ++b) {
+        const int c0 = cg * 32 + b * 16;
+        float qk[16], mq[16];
+        tmem_ld16(tmem + lanes + TM_P + c0, qk);
+        const uint32_t at = sb + SM::MQ + (uint32_t)(c0 >> 6) * ATOM;
+        load8_split(at, at + 2 * ATOM, row, c0 & 63, mq);
+        load8_split(at, at + 2 * ATOM, row, (c0 & 63) + 8, mq + 8);
+#pragma unroll
+        for (int j = 0; j < 16; ++j) {
+          float& x = v[16 * b + j];
+          x = c0 + j < row ? fmaf(mq[j], qk[j], fk * x) : 0.f;
+          total += x;
+        }
+      }
+      vsum[cg * C + row] = total;
+      named_bar_sync(3, 10 * 32);   // the warps on and below the diagonal
+      float below = 0.f;
+      for (int g = 0; g < cg; ++g) below += vsum[g * C + row];
+#pragma unroll
+      for (int j = 0; j < 32; ++j) {   // t = 32 cg + j
+        const float x = v[j];
+        v[j] = row >= cg * 32 + j ? below : 0.f;
+        below += x;
+      }
+      // 32 sums over 32 lanes, halving the values a lane holds: column j ends in lane j
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1)
+#pragma unroll
+        for (int j = 0; j < o; ++j)
+          v[j] = ((lane & o) ? v[j + o] : v[j]) + __shfl_xor_sync(0xffffffffu, (lane & o) ? v[j] : v[j + o], o);
+      csum[q4 * C + cg * 32 + lane] = v[0];
+    }
+    if (!ph.mma_done(5, ok)) {
+      if (warp == ISSUER && elect_one()) {   // nothing in flight outlives the CTA (cta_end knows warp 0's)
+        mma_commit(&bars.fin);
+        ph.W.drain(&bars.fin, 0);
+      }
+      return;
+    }
     const float gam = gate_decay(gates, row), rho = gate_ratio(gates, C - 1, row);
     const float fq = a.scale * gam, fy = -gam * beta;
     const int c = cg * 16;
@@ -508,11 +571,12 @@ __global__ void __launch_bounds__(THREADS, 1)
     load8(sb + SM::Y + DA * ATOM, row, c + 8, t + 8);
 #pragma unroll
     for (int i = 0; i < 16; ++i) {
-      x[i] = fmaf(fq, x[i], y[i]);
+      x[i] *= fq;
       rs = fmaf(t[i], x[i], rs);
+      x[i] += y[i];
     }
     if (row < id.n) store_bf16_row16(a.dq + at, x);
-    // dk: read part less the second one for rs, third for ws
+    // dk: the state's part of the first for rs, third for ws
     load8(sb + SM::Y + id.slice * ATOM, row, c, t);
     load8(sb + SM::Y + id.slice * ATOM, row, c + 8, t + 8);
     tmem_ld16(tmem + lanes + TM_KR + c, x);
@@ -520,9 +584,9 @@ __global__ void __launch_bounds__(THREADS, 1)
     tmem_ld16(tmem + lanes + TM_KW + c, z);
 #pragma unroll
     for (int i = 0; i < 16; ++i) {
-      x[i] = fmaf(fy, y[i], x[i]);
-      rs = fmaf(t[i], x[i] - z[i], rs);
-      x[i] += z[i];
+      y[i] *= fy;
+      rs = fmaf(t[i], y[i], rs);
+      x[i] += y[i] + z[i];
     }
     tmem_ld16(tmem + lanes + TM_UX + c, y);
 #pragma unroll
@@ -540,6 +604,7 @@ __global__ void __launch_bounds__(THREADS, 1)
       const size_t o = id.slice * a.tokens + id.tok + row;
       a.rpart[o] = row_total(red, row);
       a.wpart[o] = row_total(wred, row);
+      if (a.cpart != nullptr) a.cpart[o] = row_total(csum, row);
     }
   };
   work();
@@ -548,7 +613,7 @@ __global__ void __launch_bounds__(THREADS, 1)
 
 // ------------------------------------------------------------------ gates
 struct GateArgs {
-  const float *gend, *rpart, *wpart, *xpart, *bpart, *bkey;
+  const float *gend, *rpart, *wpart, *cpart, *xpart, *bpart, *bkey;
   __nv_bfloat16 *dg, *dbeta;   // dg nullable
   int N, nch, slices;
   size_t tokens, chunks;
@@ -585,12 +650,13 @@ __global__ void __launch_bounds__(C) delta_gate_grad_kernel(GateArgs a) {
   const bool live = tid < n;
   pdl_wait();
   pdl_launch_dependents();
-  float r = 0.f, w = 0.f, b = 0.f, x = 0.f;
+  float r = 0.f, w = 0.f, c = 0.f, b = 0.f, x = 0.f;
   for (int s = 0; s < a.slices; ++s) {
     const size_t at = s * a.tokens + tok + tid;
     if (live) {
       r += a.rpart[at];
       w += a.wpart[at];
+      if (a.dg != nullptr) c += a.cpart[at];
       b += a.bpart[at];
     }
     x += a.xpart[s * a.chunks + ci];
@@ -606,7 +672,7 @@ __global__ void __launch_bounds__(C) delta_gate_grad_kernel(GateArgs a) {
   const float wpre = sum_below(w, buf, tid, wt);
   rev[tid] = below;   // every thread has read its own entry
   __syncthreads();
-  if (live) a.dg[tok + tid] = __float2bfloat16_rn(rev[C - 1 - tid] + wpre + a.gend[ci] * x);
+  if (live) a.dg[tok + tid] = __float2bfloat16_rn((rev[C - 1 - tid] + c) + fmaf(a.gend[ci], x, wpre));
 }
 
 template <int D>
@@ -659,13 +725,13 @@ int bwd_launch(const DeltaBwdLaunch& L, cudaStream_t stream) {
   const cudaError_t e_keys = launch_pdl(
       delta_keys_kernel<D>, dim3(grid), dim3(THREADS), KeysSmem<D>::TOTAL, stream,
       mq, mk, md, mu, my, ms64, mx64,
-      KeysArgs{g, beta, (__nv_bfloat16*)L.dq, (__nv_bfloat16*)L.dk, f32(w.rpart), f32(w.wpart), f32(w.xpart),
-               f32(w.bkey), p.N, nch, tokens, nc, p.scale, p.st});
+      KeysArgs{g, beta, (__nv_bfloat16*)L.dq, (__nv_bfloat16*)L.dk, f32(w.rpart), f32(w.wpart),
+               L.dg != nullptr ? f32(w.cpart) : nullptr, f32(w.xpart), f32(w.bkey), p.N, nch, tokens, nc, p.scale, p.st});
   prof_after(K_DELTA_KEYS, stream);
   prof_before(K_DELTA_GATES, stream);
   const cudaError_t e_gates = launch_pdl(
       delta_gate_grad_kernel, dim3((unsigned)nc), dim3(C), 0, stream,
-      GateArgs{o.gend, f32(w.rpart), f32(w.wpart), f32(w.xpart), f32(w.bpart), f32(w.bkey),
+      GateArgs{o.gend, f32(w.rpart), f32(w.wpart), f32(w.cpart), f32(w.xpart), f32(w.bpart), f32(w.bkey),
                (__nv_bfloat16*)L.dg, (__nv_bfloat16*)L.dbeta, p.N, nch, DA, tokens, nc});
   prof_after(K_DELTA_GATES, stream);
   const bool ok = e_hb == cudaSuccess && e_vals == cudaSuccess && e_keys == cudaSuccess && e_gates == cudaSuccess;
@@ -697,6 +763,7 @@ DeltaUmmaBwdWorkspace delta_umma_bwd_layout(int BH, int N, int D) {
   w.X1 = take(mat);
   w.rpart = take(DA * tokens * 4);
   w.wpart = take(DA * tokens * 4);
+  w.cpart = take(DA * tokens * 4);
   w.bpart = take(DA * tokens * 4);
   w.bkey = take(tokens * 4);
   w.xpart = take(DA * nc * 4);

@@ -169,7 +169,7 @@ bool delta_uses_umma(int bf16, int dk, int dv, long long BH, int N, int sms, boo
 DeltaUmmaWorkspace delta_umma_layout(int BH, int N, int D, int sms);
 int launch_delta_umma(const DeltaLaunch& L, cudaStream_t stream);
 struct DeltaUmmaBwdWorkspace {
-  size_t gend, W, U, Ut, Y, T, M, H, Hb, X, X1, rpart, wpart, bpart, bkey, xpart, total;
+  size_t gend, W, U, Ut, Y, T, M, H, Hb, X, X1, rpart, wpart, cpart, bpart, bkey, xpart, total;
 };
 DeltaUmmaBwdWorkspace delta_umma_bwd_layout(int BH, int N, int D);   // delta_umma_bwd.cu
 int launch_delta_umma_bwd(const DeltaBwdLaunch& L, cudaStream_t stream);

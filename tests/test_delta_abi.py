@@ -214,7 +214,7 @@ def test_workspace_of_the_longest_sequences():
             pair, mat = 2 * 128 * D * 2, 4 * D * D
             # W, U, Ut, Y; T; M, H, Hb and two border states; sums of tokens and chunks
             want = 512 + up(4 * chunks) + 4 * up(pair * chunks) + up(chunks * 2 * 128 * 128 * 2) + 5 * up(mat * chunks)
-            want += 3 * up(4 * slices * N) + up(4 * N) + up(4 * slices * chunks)
+            want += 4 * up(4 * slices * N) + up(4 * N) + up(4 * slices * chunks)
             assert _bytes("ttt_delta_bwd_workspace_bytes", d) == want
             # forward: at most three slabs, at least one chunk in six
             one = 4 + 2 * pair + 3 * mat

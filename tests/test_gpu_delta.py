@@ -493,3 +493,12 @@ def test_gradients_of_strong_decays_token_form(cuda_device, dt, N, d, decay):
     got = p.bwd()
     p.check_bwd(got)
     check_decay_gradient(p, got)
+
+
+@pytest.mark.parametrize("d,N,B,H", [(64, 400, 1, 2), (128, 300, 1, 2), (64, 130, 4, 40), (128, 45, 4, 20)])
+@pytest.mark.parametrize("decay", list(DECAYS))
+def test_gradients_of_strong_decays_chunk_form(cuda_device, d, N, B, H, decay):
+    p = strong("bf16", N, (d, d), decay, B, H)
+    got = p.bwd()
+    p.check_bwd(got)
+    check_decay_gradient(p, got)
