@@ -569,6 +569,22 @@ TTT_DEVICE_INLINE float dot4(const float4& a, const float4& b, float acc) {
   return fmaf(a.w, b.w, fmaf(a.z, b.z, fmaf(a.y, b.y, fmaf(a.x, b.x, acc))));
 }
 
+// n values' sums over the warp, halving the values a lane holds: value v ends in
+// x[0] of the 32 / n lanes from v 32 / n on.
+template <int n>
+TTT_DEVICE_INLINE void lane_sums(float (&x)[n], int lane) {
+#pragma unroll
+  for (int o = 16, h = n / 2; o > 0; o >>= 1, h >>= 1) {
+    if (h > 0) {
+#pragma unroll
+      for (int v = 0; v < h; ++v)
+        x[v] = ((lane & o) ? x[v + h] : x[v]) + __shfl_xor_sync(0xffffffffu, (lane & o) ? x[v] : x[v + h], o);
+    } else {
+      x[0] += __shfl_xor_sync(0xffffffffu, x[0], o);
+    }
+  }
+}
+
 template <typename Tin, int R4>   // R4: groups of 32 rows of dk and columns of dv
 __global__ void __launch_bounds__(GTHREADS) delta_chunk_grad_kernel(ChunkArgs<Tin> p) {
   extern __shared__ __align__(16) float sm[];
@@ -580,7 +596,7 @@ __global__ void __launch_bounds__(GTHREADS) delta_chunk_grad_kernel(ChunkArgs<Ti
   float *S0s = sm + L_.S0, *X1s = sm + L_.X1, *Q = sm + L_.Q, *K = sm + L_.K;
   float *D = sm + L_.D, *U = sm + L_.U, *R = sm + L_.R, *Mq = sm + L_.Mq, *Mk = sm + L_.Mk;
   __shared__ double G[CB];
-  __shared__ float red[WARPS], row_s[CB], row_w[CB], corner[WARPS][CB];
+  __shared__ float red[WARPS], rows[2][CB], psum[WARPS][CB], corner[CB];
   const size_t bh = blockIdx.y;
   const int ch = blockIdx.x, t0 = ch * CB, n = min(CB, N - t0), nch = gridDim.x;
   const size_t mat = (size_t)dk * dv, tok = bh * N + t0;
@@ -683,56 +699,61 @@ __global__ void __launch_bounds__(GTHREADS) delta_chunk_grad_kernel(ChunkArgs<Ti
   asm volatile("cp.async.wait_all;" ::: "memory");
   __syncthreads();
   auto at4 = [](const float* x) { return *reinterpret_cast<const float4*>(x); };
-  {   // Mq, Mk: column j = lane, rows i = warp + 8 a
-    const int j = lane;
+  const int i0 = warp * 4;
+  float pairs[4];   // the pairs' terms of dg
+  {   // Mq, Mk: row i = lane, columns j = i0 + a; all zero where those lie behind n
+    const int i = lane, dv_in = i0 < n ? dv : 0, dk_in = i0 < n ? dk : 0;
     float mq[4] = {0.f, 0.f, 0.f, 0.f}, mk[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll 2
-    for (int c = 0; c < dv; c += 4) {
-      const float4 u = at4(U + j * ms + c);
+    for (int c = 0; c < dv_in; c += 4) {
+      const float4 d = at4(D + i * ms + c), r = at4(R + i * ms + c);
 #pragma unroll
       for (int a = 0; a < 4; ++a) {
-        const int i = warp + WARPS * a;
-        mq[a] = dot4(at4(D + i * ms + c), u, mq[a]);
-        mk[a] = dot4(at4(R + i * ms + c), u, mk[a]);
+        const float4 u = at4(U + (i0 + a) * ms + c);
+        mq[a] = dot4(d, u, mq[a]);
+        mk[a] = dot4(r, u, mk[a]);
       }
     }
 #pragma unroll
     for (int a = 0; a < 4; ++a) {
-      const int i = warp + WARPS * a;
+      const int j = i0 + a;
       const float f = j <= i ? expf((float)(G[i] - G[j])) : 0.f;
-      Mq[i * MP + j] = mq[a] = j <= i ? mq[a] * f : 0.f;
-      Mk[i * MP + j] = mk[a] = j < i ? -mk[a] * f : 0.f;
+      mq[a] = j <= i ? mq[a] * f : 0.f;
+      mk[a] = j < i ? -mk[a] * f : 0.f;
     }
-    if (p.dg != nullptr) {   // the pairs' part of dg
+    *reinterpret_cast<float4*>(Mq + i * MP + i0) = make_float4(mq[0], mq[1], mq[2], mq[3]);
+    *reinterpret_cast<float4*>(Mk + i * MP + i0) = make_float4(mk[0], mk[1], mk[2], mk[3]);
+    if (p.dg != nullptr) {
       float qk[4] = {0.f, 0.f, 0.f, 0.f}, kk[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll 2
-      for (int c = 0; c < dk; c += 4) {
-        const float4 k = at4(K + j * ks + c);
+      for (int c = 0; c < dk_in; c += 4) {
+        const float4 x = at4(Q + i * ks + c), y = at4(K + i * ks + c);
 #pragma unroll
         for (int a = 0; a < 4; ++a) {
-          const int i = warp + WARPS * a;
-          qk[a] = dot4(at4(Q + i * ks + c), k, qk[a]);
-          kk[a] = dot4(at4(K + i * ks + c), k, kk[a]);
+          const float4 k = at4(K + (i0 + a) * ks + c);
+          qk[a] = dot4(x, k, qk[a]);
+          kk[a] = dot4(y, k, kk[a]);
         }
       }
-      float sum = 0.f;
 #pragma unroll
-      for (int a = 0; a < 4; ++a) {
-        const int i = warp + WARPS * a;
-        float v = j < i ? fmaf(mq[a], qk[a], mk[a] * kk[a]) : 0.f;
-        for (int o = 1; o < 32; o <<= 1) {
-          const float y = __shfl_up_sync(0xffffffffu, v, o);
-          if (lane >= o) v += y;
-        }
-        v = __shfl_up_sync(0xffffffffu, v, 1);   // lane t: the sum over j < t
-        if (lane > 0 && lane <= i) sum += v;
-      }
-      corner[warp][lane] = sum;
+      for (int a = 0; a < 4; ++a) pairs[a] = i0 + a < i ? fmaf(mq[a], qk[a], mk[a] * kk[a]) : 0.f;
+      psum[warp][i] = (pairs[0] + pairs[1]) + (pairs[2] + pairs[3]);
     }
   }
   __syncthreads();
+  if (p.dg != nullptr) {   // the sums over j < t = i0 + a of row i = lane, then over the rows from t on
+    float below = 0.f;
+    for (int w = 0; w < warp; ++w) below += psum[w][lane];
+#pragma unroll
+    for (int a = 0; a < 4; ++a) {
+      const float x = pairs[a];
+      pairs[a] = lane >= i0 + a ? below : 0.f;
+      below += x;
+    }
+    lane_sums<4>(pairs, lane);
+    if ((lane & 7) == 0) corner[i0 + lane / 8] = pairs[0];
+  }
   // a lane holds rows lane + 32 b of four tokens' gradients
-  const int i0 = warp * 4;
   float dqv[4][R4], dkr[4][R4], dkw[4][R4];
 #pragma unroll
   for (int a = 0; a < 4; ++a)
@@ -763,24 +784,23 @@ __global__ void __launch_bounds__(GTHREADS) delta_chunk_grad_kernel(ChunkArgs<Ti
     const float gam = expf((float)G[i0 + a]), rho = expf((float)(G[CB - 1] - G[i0 + a]));
 #pragma unroll
     for (int b = 0; b < R4; ++b) { dqv[a][b] *= gam; dkr[a][b] *= -gam; dkw[a][b] *= rho; }
-    if (p.dg != nullptr) {   // the states' part of dg
-      float s = 0.f, w = 0.f;
+  }
+  if (p.dg != nullptr) {   // the states' part of dg: reads of the four tokens, then their writes
+    float x[8];
+#pragma unroll
+    for (int a = 0; a < 4; ++a) {
+      x[a] = x[4 + a] = 0.f;
 #pragma unroll
       for (int b = 0; b < R4; ++b) {
         const int r = lane + 32 * b;
         if (r >= dk) continue;
-        s = fmaf(Q[(i0 + a) * ks + r], dqv[a][b], fmaf(K[(i0 + a) * ks + r], dkr[a][b], s));
-        w = fmaf(K[(i0 + a) * ks + r], dkw[a][b], w);
-      }
-      for (int o = 16; o > 0; o >>= 1) {
-        s += __shfl_xor_sync(0xffffffffu, s, o);
-        w += __shfl_xor_sync(0xffffffffu, w, o);
-      }
-      if (lane == 0) {
-        row_s[i0 + a] = s;
-        row_w[i0 + a] = w;
+        const float k = K[(i0 + a) * ks + r];
+        x[a] = fmaf(Q[(i0 + a) * ks + r], dqv[a][b], fmaf(k, dkr[a][b], x[a]));
+        x[4 + a] = fmaf(k, dkw[a][b], x[4 + a]);
       }
     }
+    lane_sums<8>(x, lane);
+    if ((lane & 3) == 0) rows[lane / 16][i0 + (lane >> 2 & 3)] = x[0];
   }
 #pragma unroll 2
   for (int j = 0; j < n; ++j) {   // rows and columns of Mq and Mk behind n are zero
@@ -817,13 +837,10 @@ __global__ void __launch_bounds__(GTHREADS) delta_chunk_grad_kernel(ChunkArgs<Ti
   }
   __syncthreads();
   if (warp == 0 && p.dg != nullptr) {
-    float x1s0 = 0.f, pairs = 0.f;
-    for (int w = 0; w < WARPS; ++w) {
-      x1s0 += red[w];
-      pairs += corner[w][lane];
-    }
+    float x1s0 = 0.f;
+    for (int w = 0; w < WARPS; ++w) x1s0 += red[w];
     // reads of the tokens from this one on, writes of those before it
-    float reads = row_s[lane], writes = row_w[lane];
+    float reads = rows[0][lane], writes = rows[1][lane];
     for (int o = 1; o < 32; o <<= 1) {
       const float x = __shfl_down_sync(0xffffffffu, reads, o), y = __shfl_up_sync(0xffffffffu, writes, o);
       if (lane + o < 32) reads += x;
@@ -831,7 +848,7 @@ __global__ void __launch_bounds__(GTHREADS) delta_chunk_grad_kernel(ChunkArgs<Ti
     }
     writes = __shfl_up_sync(0xffffffffu, writes, 1);
     if (lane == 0) writes = 0.f;
-    if (lane < n) p.dg[tok + lane] = from_f<Tin>((reads + pairs) + fmaf(expf((float)G[CB - 1]), x1s0, writes));
+    if (lane < n) p.dg[tok + lane] = from_f<Tin>((reads + corner[lane]) + fmaf(expf((float)G[CB - 1]), x1s0, writes));
   }
 }
 
