@@ -1028,8 +1028,7 @@ int launch_cols(void (*kernel)(KArgs...), dim3 grid, cudaStream_t stream, Args..
   constexpr size_t smem = stage_bytes<R4, HELP>();
   static std::atomic<uint64_t> attr{};
   if (smem > 48 * 1024 && allow_dynamic_smem(kernel, (int)smem, attr)) return -1;
-  kernel<<<grid, HELP ? 2 * THREADS : THREADS, smem, stream>>>(args...);
-  return cudaGetLastError() == cudaSuccess ? 0 : -1;
+  return launch_plain(kernel, grid, dim3(HELP ? 2 * THREADS : THREADS), smem, stream, args...) == cudaSuccess ? 0 : -1;
 }
 // heads x slices of columns x directions
 dim3 cols_grid(const DeltaLaunch& p, int directions) {
@@ -1105,10 +1104,11 @@ int bwd_launch(const DeltaBwdLaunch& L, cudaStream_t stream) {
     s.Sc += (size_t)b0 * nch * mat;
     s.Xc += (size_t)b0 * nch * mat;
     prof_before(K_DELTA_GRAD, stream);
-    kfn<<<dim3((unsigned)nch, (unsigned)nb), GTHREADS, smem, stream>>>(s);
+    const cudaError_t e = launch_plain(kfn, dim3((unsigned)nch, (unsigned)nb), dim3(GTHREADS), smem, stream, s);
     prof_after(K_DELTA_GRAD, stream);
+    if (e != cudaSuccess) return -1;
   }
-  return cudaGetLastError() == cudaSuccess ? 0 : -1;
+  return 0;
 }
 
 }  // namespace
@@ -1150,14 +1150,15 @@ int launch_delta_step(const DeltaLaunch& p, const int* slots, int n_slots, cudaS
   const int vc = (long long)p.B * p.H * ((p.dv + 31) / 32) < 4 * p.sms ? 16 : 32;
   const dim3 grid((unsigned)p.B, (unsigned)p.H, (unsigned)((p.dv + vc - 1) / vc));
 #define TTT_STEP_VC(TI, TO, VC)                                                                    \
-  delta_step_kernel<TI, TO, VC><<<grid, STHREADS, 0, stream>>>(                                    \
-      (const TI*)p.q, (const TI*)p.k, (const TI*)p.v, (const TI*)p.g, (const TI*)p.beta, slots,    \
-      n_slots, p.S, (TO*)p.out, p.B, p.H, p.dk, p.dv, p.scale)
+  e = launch_plain(delta_step_kernel<TI, TO, VC>, grid, dim3(STHREADS), 0, stream, (const TI*)p.q,  \
+                   (const TI*)p.k, (const TI*)p.v, (const TI*)p.g, (const TI*)p.beta, slots,        \
+                   n_slots, p.S, (TO*)p.out, p.B, p.H, p.dk, p.dv, p.scale)
 #define TTT_STEP(TI, TO)                     \
   do {                                       \
     if (vc == 16) TTT_STEP_VC(TI, TO, 16);   \
     else TTT_STEP_VC(TI, TO, 32);            \
   } while (0)
+  cudaError_t e = cudaSuccess;
   prof_before(K_DELTA_STEP, stream);
   if (p.in_bf16) {
     if (p.out_bf16) TTT_STEP(__nv_bfloat16, __nv_bfloat16);
@@ -1169,7 +1170,7 @@ int launch_delta_step(const DeltaLaunch& p, const int* slots, int n_slots, cudaS
 #undef TTT_STEP
 #undef TTT_STEP_VC
   prof_after(K_DELTA_STEP, stream);
-  return cudaGetLastError() == cudaSuccess ? 0 : -1;
+  return e == cudaSuccess ? 0 : -1;
 }
 
 }  // namespace ttt

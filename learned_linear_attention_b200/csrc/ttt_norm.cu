@@ -317,9 +317,8 @@ int launch_t(const NormArgs& a, int grid, size_t smem, cudaStream_t stream) {
   const Shape s = norm_shape(a.D, Vec<E>::N);
 #define TTT_NORM(T_, V_)                                                              \
   if (s.T == T_ && s.V == V_) {                                                       \
-    if constexpr (BWD) norm_bwd_kernel<E, T_, V_><<<grid, THREADS, smem, stream>>>(a); \
-    else norm_fwd_kernel<E, T_, V_><<<grid, THREADS, 0, stream>>>(a);                  \
-    return cudaGetLastError() == cudaSuccess ? 0 : -1;                                 \
+    const auto kernel = BWD ? norm_bwd_kernel<E, T_, V_> : norm_fwd_kernel<E, T_, V_>; \
+    return launch_plain(kernel, dim3(grid), dim3(THREADS), smem, stream, a) == cudaSuccess ? 0 : -1; \
   }
   TTT_NORM(4, 1) TTT_NORM(8, 1) TTT_NORM(16, 1) TTT_NORM(32, 1) TTT_NORM(32, 2) TTT_NORM(32, 4)
   TTT_NORM(128, 1)
@@ -360,12 +359,12 @@ int launch_norm_bwd(const NormLaunch& L, int sms, cudaStream_t stream) {
   a.part = L.dw != nullptr ? L.part : nullptr;
   const size_t smem = a.part != nullptr ? (size_t)(THREADS / T) * L.D * sizeof(float) : 0;
   prof_before(K_NORM_BWD, stream);
-  const int r = L.bf16 ? launch_t<__nv_bfloat16, true>(a, grid, smem, stream)
-                       : launch_t<float, true>(a, grid, smem, stream);
-  if (r == 0 && L.dw != nullptr)
-    norm_dw_kernel<<<(L.D + 31) / 32, 1024, 0, stream>>>(a.part, grid, L.D, L.dw);
+  int r = L.bf16 ? launch_t<__nv_bfloat16, true>(a, grid, smem, stream) : launch_t<float, true>(a, grid, smem, stream);
+  if (r == 0 && L.dw != nullptr &&
+      launch_plain(norm_dw_kernel, dim3((L.D + 31) / 32), dim3(1024), 0, stream, a.part, grid, L.D, L.dw) != cudaSuccess)
+    r = -1;
   prof_after(K_NORM_BWD, stream);
-  return r == 0 && cudaGetLastError() == cudaSuccess ? 0 : -1;
+  return r;
 }
 
 }  // namespace ttt

@@ -12,6 +12,8 @@ Tolerances, |got - ref| <= r |ref| + s max|ref|:
      and the partner's); dk or 128 products average them, and tokens add up
      over the memory of the decay, so 8 * 5 * 2^-17 bounds the largest.
 """
+import ctypes
+
 import numpy as np
 import pytest
 import torch
@@ -502,3 +504,31 @@ def test_gradients_of_strong_decays_chunk_form(cuda_device, d, N, B, H, decay):
     got = p.bwd()
     p.check_bwd(got)
     check_decay_gradient(p, got)
+
+
+# ------------------------------------------------------------------ errors of earlier calls
+def leave_an_error():
+    """A refused memset of an earlier call stays the library runtime's last
+    error (the state is host memory)."""
+    d = T.make_linear_desc(1, 1, 4, 8, 8, 4, in_dtype="f32", out_dtype="f32")
+    T.load().ttt_linear_state_init(ctypes.byref(d), None, torch.zeros(1, 1, 8, 8).data_ptr(), None)
+
+
+@pytest.mark.parametrize("dt,d", [("f32", 24), ("bf16", 64)])
+def test_an_earlier_error_is_not_this_calls(cuda_device, dt, d):
+    """A pending error of another call: the work is done once and reported as done."""
+    p = Problem(2, 2, 200, d, d, dt)
+    want_f, want_b = p.fwd(), p.bwd()
+    leave_an_error()
+    got = p.fwd()
+    leave_an_error()
+    grads = p.bwd()
+    assert all(torch.equal(a, b) for a, b in zip(want_f + tuple(want_b), got + tuple(grads)))
+    x = {n: t[:, :, 0].contiguous() for n, t in p.dev.items()}
+    pools, outs = [p.S0.clone(), p.S0.clone()], []
+    for S, error in zip(pools, (False, True)):
+        if error:
+            leave_an_error()
+        outs.append(torch.empty_like(x["v"]))
+        T.ttt_delta_step(p.desc(N=1), x["q"], x["k"], x["v"], x["g"], x["beta"], None, 2, S, outs[-1])
+    assert torch.equal(*pools) and torch.equal(*outs)

@@ -13,7 +13,7 @@ import torch
 
 import learned_linear_attention_b200 as T
 from oracle import delta_recurrent, row_norm, row_norm_backward
-from test_gpu_delta import HALF, TYPES, Problem, near, tol
+from test_gpu_delta import HALF, TYPES, Problem, leave_an_error, near, tol
 
 pytestmark = pytest.mark.gpu
 U = 2.0 ** -24
@@ -196,3 +196,19 @@ def test_training_step_of_the_layer(cuda_device):
         diff = (loss(hi) - loss(lo)) / (2 * h)
         # the sum of |d_i g_i| over n entries, each off by the float32 chain's 2e-5 at most
         assert abs(diff - (host(got) * dirn).sum()) <= 2e-5 * np.abs(host(got) * dirn).sum() + 1e-7, n
+
+
+def test_an_earlier_error_is_not_this_calls(cuda_device):
+    p = make(50, 64, "f32", True, "silu", False)
+    d = T.make_norm_desc(50, 64, gate="silu", dtype="f32")
+    ws, outs = T.alloc_workspace(T.ttt_norm_bwd_workspace_bytes(d)), []
+    for error in (False, True):
+        g = [torch.empty_like(p[n]) for n in ("x", "x", "w", "z")]
+        if error:
+            leave_an_error()
+        T.ttt_norm_fwd(d, p["x"], p["w"], p["z"], None, g[0])
+        if error:
+            leave_an_error()
+        T.ttt_norm_bwd(d, p["x"], p["w"], p["z"], p["dout"], *g[1:], ws)
+        outs.append(g)
+    assert all(torch.equal(a, b) for a, b in zip(*outs))
