@@ -1092,9 +1092,10 @@ int bwd_launch(const DeltaBwdLaunch& L, cudaStream_t stream) {
                    (const Tin*)p.beta, ev, du, Sc, Xc, (Tin*)L.dq, (Tin*)L.dk, (Tin*)L.dv,
                    (Tin*)L.dg, (Tin*)L.dbeta, p.N, p.dk, p.dv, p.scale};
   if (nch == 0) return 0;
-  // grid.y is limited to 65535: more heads go in slices
-  for (int b0 = 0; b0 < BH; b0 += 65535) {
-    const int nb = std::min(65535, BH - b0);
+  // grid.y is limited to 65535: more heads go in slices (b0 ends at BH: a step
+  // of 65535 would pass 2^31 behind the last heads that an int counts)
+  for (int b0 = 0, nb; b0 < BH; b0 += nb) {
+    nb = std::min(65535, BH - b0);
     ChunkArgs<Tin> s = a;
     const size_t t = (size_t)b0 * p.N, mat = (size_t)p.dk * p.dv;
     s.q += t * p.dk; s.k += t * p.dk; s.dq += t * p.dk; s.dk += t * p.dk;

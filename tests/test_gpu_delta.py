@@ -532,3 +532,11 @@ def test_an_earlier_error_is_not_this_calls(cuda_device, dt, d):
         outs.append(torch.empty_like(x["v"]))
         T.ttt_delta_step(p.desc(N=1), x["q"], x["k"], x["v"], x["g"], x["beta"], None, 2, S, outs[-1])
     assert torch.equal(*pools) and torch.equal(*outs)
+
+
+@pytest.mark.parametrize("dt,dk,dv,N,B,H", [("f32", 3, 2, 2, 7, 10001), ("bf16", 8, 8, 1, 1, 65537)])
+def test_more_heads_than_a_grid_dimension(cuda_device, dt, dk, dv, N, B, H):
+    """The chunk gradients go over the heads in slices of 65,535."""
+    p = Problem(B, H, N, dk, dv, dt)
+    p.check_fwd(p.fwd())
+    p.check_bwd(p.bwd())
