@@ -35,7 +35,12 @@ constexpr int THREADS = 512;   // of every CTA: four column groups of 128 rows
 // diagonal, so what is above the diagonal may be anything, before and after.
 //
 // The joins are warp-level tensor products, a tile of 16 x 16 a warp, with
-// every float32 value as a sum of two tf32 ones (three products; 2^-22).  With
+// every float32 value as a sum of two tf32 ones (three products).  hi is rounded
+// to nearest, so lo is at most 2^-11 of the value and of either sign; lo's own
+// lowest bits, which the product does not read, are below 2^-21 of it, and lo lo,
+// which is left out, below 2^-22: a product of two values is off by 2^-20 + 2^-22
+// at most (1.2e-6; 4.6e-7 the largest of four million random ones, and no bias.
+// A hi cut off instead of rounded: 1.6e-6, all towards zero).  With
 // FFMA, what the register tiles read from shared memory bound them: 4 x 4 a
 // thread took 8100 cycles for blocks of 64, two CTAs an SM.  (The blocks are
 // too small for tcgen05: its operands would have to be split into planes and
@@ -45,8 +50,8 @@ constexpr int LDA = 132;
 struct Tf32 {
   uint32_t hi, lo;
   TTT_DEVICE_INLINE explicit Tf32(float x) {
-    hi = __float_as_uint(x) & 0xffffe000u;
-    lo = __float_as_uint(x - __uint_as_float(hi));   // its own lowest bits are not read
+    hi = (__float_as_uint(x) + 0x1000u) & 0xffffe000u;   // NaN and infinity leave NaN in lo
+    lo = __float_as_uint(x - __uint_as_float(hi));
   }
 };
 TTT_DEVICE_INLINE void mma_16x8x8(float (&c)[4], const uint32_t (&a)[4], const uint32_t (&b)[2]) {
