@@ -540,3 +540,66 @@ def test_more_heads_than_a_grid_dimension(cuda_device, dt, dk, dv, N, B, H):
     p = Problem(B, H, N, dk, dv, dt)
     p.check_fwd(p.fwd())
     p.check_bwd(p.bwd())
+
+
+# ------------------------------------------------------------------ the precision of each form
+def in_chunks(p, backward):
+    """Whether the call runs on tensor cores (the workspaces of the two forms differ)."""
+    B, H, N, dk, dv = p.shape
+    if not backward:
+        return T.ttt_delta_workspace_bytes(p.desc()) > T.TTT_STATUS_BYTES
+    f32 = T.make_delta_desc(B, H, N, dk, dv, in_dtype="f32", out_dtype="f32")
+    return T.ttt_delta_bwd_workspace_bytes(p.desc()) != T.ttt_delta_bwd_workspace_bytes(f32)
+
+
+def norm_near(got, ref, limit, what):
+    got = got.detach().double().cpu().numpy()
+    err = np.linalg.norm(got - ref) / np.linalg.norm(ref)
+    assert err <= limit, f"{what}: {err:.2e} of the norm, limit {limit:.1e}"
+
+
+@pytest.mark.parametrize("N,B,H", [(1, 1, 2), (77, 1, 2), (128, 1, 2), (20, 3, 16)])
+@pytest.mark.parametrize("d", [64, 128])
+def test_short_bf16_sequences_have_the_float32_bounds(cuda_device, d, N, B, H):
+    """bf16 heads of 64 and 128 that go token by token: float32 throughout, so
+    the bounds of the float32 path, and the inputs' type for what is rounded to it."""
+    p = Problem(B, H, N, d, d, "bf16")
+    assert not in_chunks(p, False) and not in_chunks(p, True)
+    s = 8 * np.sqrt(d * N) * 2.0 ** -24
+    ref, S = delta_recurrent(*(p.host(n) for n in ("q", "k", "v", "g", "beta")), p.host("S0"))
+    for out in ("f32", "bf16"):
+        o, S_end = p.fwd(out=out)
+        near(o, ref, HALF[out], s, "out")
+        near(S_end, S, HALF["f32"], s, "S")
+    want = delta_backward(*(p.host(n) for n in ("q", "k", "v", "g", "beta", "dout", "S0", "dS")))
+    for name, a, b in zip(("dq", "dk", "dv", "dg", "dbeta", "dS0"), p.bwd(), want):
+        near(a, b, HALF["f32" if name == "dS0" else "bf16"], 2 * s, name)
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("decay", [True, False])
+@pytest.mark.parametrize("start", [True, False])
+def test_states_and_float32_outputs_of_the_chunk_form(cuda_device, d, decay, start):
+    """Norm-wise limits of the float32 results on tensor cores.
+
+    An operand hi + lo is off by at most 2^-18 (two roundings of 2^-9 each), 0.4
+    of that in the mean square, and the lo lo left out of a product of two pairs
+    is as much: 2.4e-6 a product, norm-wise, as terms of either sign add up.
+    Without decay the state goes through three in turn (T gam K, rho W, M S: 3.7e-6)
+    in every chunk, of which the contraction I + M keeps less with every further
+    one: twice to three times that, 1e-5.  Outputs join W S0, P U and Q S0 to it:
+    1.5e-5.  With decays of 0.05 a token the mean chunk keeps e^-7 of the state
+    before it, so S and dS0 are H and Hb, whose operands have three planes (2^-26):
+    what is left is T diag(beta) above (its diagonal is exact, and the rest is a
+    third of it in norm: 5e-7), the decays' exponentials (2^-22, 2.4e-7) and the
+    truncated sum of 128 terms (2^-24 each): 2e-6.  Two planes would leave 2^-18.
+    """
+    p = Problem(1, 2, 1024, d, d, "bf16", decay=decay, start=start)
+    assert in_chunks(p, False) and in_chunks(p, True)
+    ref, S = delta_recurrent(*(p.host(n) for n in ("q", "k", "v", "g", "beta")), p.host("S0"))
+    o, S_end = p.fwd(out="f32")
+    dS0 = p.bwd()[-1]
+    want = delta_backward(*(p.host(n) for n in ("q", "k", "v", "g", "beta", "dout", "S0", "dS")))[-1]
+    norm_near(S_end, S, 2e-6 if decay else 1e-5, "S")
+    norm_near(dS0, want, 2e-6 if decay else 1e-5, "dS0")
+    norm_near(o, ref, 1.5e-5, "out")
