@@ -212,3 +212,16 @@ def test_an_earlier_error_is_not_this_calls(cuda_device):
         T.ttt_norm_bwd(d, p["x"], p["w"], p["z"], p["dout"], *g[1:], ws)
         outs.append(g)
     assert all(torch.equal(a, b) for a, b in zip(*outs))
+
+
+def test_float32_gates_have_float32_precision(cuda_device):
+    """Rows of ones gated by z in [-80, 80], each value against its own size.  The
+    exponential is good to 2 ulp (2^-23 each), 1 + e rounds once, the quotient is
+    good to 2 ulp, and r, the norm's and the gate's products round seven times:
+    (4 + 1 + 4 + 7) 2^-24."""
+    z = torch.linspace(-80, 80, 1 << 16, device="cuda").view(-1, 128)
+    x, out = torch.ones_like(z), torch.empty_like(z)
+    d = T.make_norm_desc(len(z), 128, gate="sigmoid", dtype="f32")
+    T.ttt_norm_fwd(d, x, None, z, None, out)
+    ref = row_norm(host(x), None, host(z), gate="sigmoid", eps=d.eps)
+    assert (np.abs(host(out) - ref) / ref).max() <= 16 * U
