@@ -3,8 +3,15 @@
 //
 // Tiles: [rows][64] bf16 with 128-byte rows and 128-byte swizzle ("atoms");
 // a 128-row atom is 16 KB.  A derived matrix is a pair of atoms rows, hi =
-// bf16(x) and lo = bf16(x - hi): off by at most 2^-17 of the value, where one
-// bf16 alone would be off by 2^-9 and show in the float32 state.
+// bf16(x) and lo = bf16(x - hi): off by at most 2^-18 of the value, where one
+// bf16 alone would be off by 2^-9 and show in the float32 state.  Three products
+// join two pairs (lo lo, at most 2^-18, is left out): a float32 output is off by
+// 6e-6 of its norm and S without decay by 4.4e-6, where float32 operands would
+// leave 2e-7 to 5e-7; bf16 results round at 2^-9.  Carrying every operand in
+// three planes would take six products in the place of three and half as much
+// shared memory and traffic again, and three planes of some of T, W, M and X
+// still leave 1.2e-6 or more; so only the terms that S and dS0 consist of where
+// the state decays, H and Hb, have them (5e-7 and 1e-6; 2.7e-6 and 3e-6 with two).
 #pragma once
 
 #include "kernels.h"
@@ -26,6 +33,10 @@ struct Gates {
   float down[C];           // exp(G_e - G_j), e the last token of j's block of 16
   float part[8];
 };
+// Off by (2 + 1.16 |d|) 2^-23 of exp(d) at most, so for d <= 0 by 2^-22 = 2.4e-7 of
+// the largest factor 1.  With expf S comes out 2 % nearer to 64 bits (5.0e-7 of
+// its norm in the place of 5.1e-7, 1024 tokens of heads of 64) and the calls take 5
+// to 9 % longer (64 heads of 64, 32K tokens: 1742 us against 1652).
 TTT_DEVICE_INLINE float gate_exp(float d) { return __expf(d); }
 TTT_DEVICE_INLINE float gate_clamp(float g) { return g < -200.f ? -200.f : g > 200.f ? 200.f : g; }
 
@@ -203,7 +214,7 @@ TTT_DEVICE_INLINE void products(const P&... p) {
   for (int ks = 0; ks < STEPS; ++ks) (p.step(ks), ...);
 }
 // The hi + lo pair of an operand: lo is `second` bytes after hi.  A product of
-// two pairs is lo hi + hi lo + hi hi (lo lo is below 2^-17 of it twice over).
+// two pairs is lo hi + hi lo + hi hi (lo lo, at most 2^-18 of it, is left out).
 struct Pair {
   Op hi;
   uint32_t second;
