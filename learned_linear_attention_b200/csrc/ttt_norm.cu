@@ -301,9 +301,12 @@ struct Shape { int T, V; };
 // Threads of a row and vectors of a thread: few threads keep several rows'
 // loads in flight in a warp, one vector a thread keeps accesses whole and the
 // next row in registers.  A warp takes a row of up to four float32 vectors a
-// thread (512 of them: 79 us against 96 for a whole CTA a row, 134 MB in and
-// out); bf16 vectors hold twice the values, and rows of more than two a thread go
-// to several warps (512 values: 46 us against 57; 1024 values: 67 against 44).
+// thread (65,536 rows of 512 with gate and residual 82 us, against 97 for 128
+// threads a row; without them 50 against 70; gradients 120 against 113 and 82
+// against 84).  bf16 vectors hold twice the values: up to two a thread (65,536
+// rows of 512 with gate and residual 47 us against 64, gradients 79 against 133);
+// rows of more go to several warps (32,768 rows of 1024 45 us, against 68 for a
+// warp a row with four; gradients 76 against 95).
 Shape norm_shape(int D, int per_vec) {
   const int nv = (D + per_vec - 1) / per_vec, most = per_vec == 4 ? 128 : 64;
   int T = 4;
@@ -314,7 +317,9 @@ Shape norm_shape(int D, int per_vec) {
   return {T, V};
 }
 
-// `per_sm` CTAs an SM: as many as are resident (see __launch_bounds__), so that all take the same number of rows
+// `per_sm` CTAs an SM, 4 forward and 3 backward: as many as are resident where a
+// thread holds one vector (see __launch_bounds__), so that all take the same
+// number of rows.  With more vectors fewer are resident and the others follow.
 int norm_grid(long long rows, int T, int sms, int per_sm) {
   const long long groups = THREADS / T;
   return (int)std::max<long long>(1, std::min<long long>((rows + groups - 1) / groups, (long long)sms * per_sm));
@@ -328,9 +333,13 @@ int launch_t(const NormArgs& a, int grid, size_t smem, cudaStream_t stream) {
     const auto kernel = BWD ? norm_bwd_kernel<E, T_, V_> : norm_fwd_kernel<E, T_, V_>; \
     return launch_plain(kernel, dim3(grid), dim3(THREADS), smem, stream, a) == cudaSuccess ? 0 : -1; \
   }
-  TTT_NORM(4, 1) TTT_NORM(8, 1) TTT_NORM(16, 1) TTT_NORM(32, 1) TTT_NORM(32, 2) TTT_NORM(32, 4)
-  TTT_NORM(128, 1)
-  TTT_NORM(256, 1) TTT_NORM(256, 2) TTT_NORM(256, 4) TTT_NORM(256, 8)
+  TTT_NORM(4, 1) TTT_NORM(8, 1) TTT_NORM(16, 1) TTT_NORM(32, 1) TTT_NORM(32, 2)
+  TTT_NORM(256, 1) TTT_NORM(256, 2) TTT_NORM(256, 4)
+  if constexpr (Vec<E>::N == 4) {   // the others that norm_shape gives for the type
+    TTT_NORM(32, 4) TTT_NORM(256, 8)
+  } else {
+    TTT_NORM(128, 1)
+  }
 #undef TTT_NORM
   return -1;
 }
