@@ -427,8 +427,8 @@ TTT_DEVICE_INLINE void prep_cta(uint8_t* smem, const CUtensorMap& mapK, const CU
 // (that form: 1.5 and 2.1).
 struct ChainArgs {
   const float* gend;
-  DeltaChain dir[2];       // forward, backward
-  int BH, first;           // the first CTAs take dir[first]
+  DeltaChain dir[2];       // forward; backward, by the CTAs behind the forward ones
+  int BH;
   Slab slab;
   DevStatus st;
 };
@@ -459,7 +459,7 @@ TTT_DEVICE_INLINE void chain_cta(uint8_t* smem, const CUtensorMap& mapM, const C
   ChainBars& bars = *reinterpret_cast<ChainBars*>(smem + SM::BAR);
   const int tid = threadIdx.x, warp = warp_index(), lane = tid & 31;
   const int slice = block % DA, nch = a.slab.len;
-  const bool rev = a.first + block / (DA * a.BH) == 1;
+  const bool rev = block >= (unsigned)(DA * a.BH);
   const float* H = rev ? a.dir[1].H : a.dir[0].H;
   const float* S_in = rev ? a.dir[1].S_in : a.dir[0].S_in;
   float* S_out = rev ? a.dir[1].S_out : a.dir[0].S_out;
@@ -817,24 +817,21 @@ int prep_launch(const DeltaLaunch& p, const DeltaPrepOut& o, cudaStream_t stream
 }
 
 template <int D>
-int chain_launch(const DeltaLaunch& p, const float* gend, const __nv_bfloat16* M, const DeltaChain* fwd,
-                 const DeltaChain* rev, cudaStream_t stream) {
+int chain_launch(const DeltaLaunch& p, const float* gend, const __nv_bfloat16* M, const DeltaChain& fwd,
+                 const DeltaChain& rev, cudaStream_t stream) {
   const int BH = p.B * p.H, nch = tiles_of(p.N, C);
   const uint64_t nc = (uint64_t)BH * nch, rs = D * 2;
   CUtensorMap mm, mf, mr;
   if (make_tmap_bf16_3d(&mm, M, D, D, 2 * nc, rs, D * rs, 64, D) ||
-      make_tmap_bf16_3d(&mf, fwd ? fwd->X : rev->X, D, D, 2 * nc, rs, D * rs, 64, D) ||
-      make_tmap_bf16_3d(&mr, rev ? rev->X : fwd->X, D, D, 2 * nc, rs, D * rs, 64, D))
+      make_tmap_bf16_3d(&mf, fwd.X, D, D, 2 * nc, rs, D * rs, 64, D) ||
+      make_tmap_bf16_3d(&mr, rev.X, D, D, 2 * nc, rs, D * rs, 64, D))
     return -1;
   static std::atomic<uint64_t> attr{0};
   if (allow_dynamic_smem(delta_chain_kernel<D>, (int)ChainSmem<D>::TOTAL, attr)) return -1;
-  ChainArgs a{gend, {}, BH, fwd ? 0 : 1, Slab{0, nch, 0}, p.st};
-  if (fwd) a.dir[0] = *fwd;
-  if (rev) a.dir[1] = *rev;
-  const unsigned dirs = (fwd ? 1 : 0) + (rev ? 1 : 0);
+  const ChainArgs a{gend, {fwd, rev}, BH, Slab{0, nch, 0}, p.st};
   prof_before(K_DELTA_CHAIN, stream);
   const cudaError_t err = launch_pdl(
-      delta_chain_kernel<D>, dim3(dirs * (unsigned)(BH * (D / 64))), dim3(THREADS), ChainSmem<D>::TOTAL, stream,
+      delta_chain_kernel<D>, dim3(2u * (unsigned)(BH * (D / 64))), dim3(THREADS), ChainSmem<D>::TOTAL, stream,
       mm, mf, mr, a);
   prof_after(K_DELTA_CHAIN, stream);
   return err == cudaSuccess ? 0 : -1;
@@ -885,7 +882,7 @@ int fwd_launch(const DeltaLaunch& p, cudaStream_t stream) {
     if (j >= 1 && j <= slabs) {
       // every slab's recurrence starts from S and leaves its end there
       const DeltaChain dir{f32(w.H), p.S, p.S, nullptr};
-      a.chain = ChainArgs{f32(w.gend), {dir, {}}, BH, 0, slab(j - 1), p.st};
+      a.chain = ChainArgs{f32(w.gend), {dir, {}}, BH, slab(j - 1), p.st};
       a.n_chain = (unsigned)(BH * (D / 64));
     }
     if (j >= 2) {
@@ -944,8 +941,8 @@ DeltaUmmaWorkspace delta_umma_layout(int BH, int N, int D, int sms) {
 int launch_delta_prep(const DeltaLaunch& p, const DeltaPrepOut& o, cudaStream_t stream) {
   return p.dk == 64 ? prep_launch<64>(p, o, stream) : prep_launch<128>(p, o, stream);
 }
-int launch_delta_chain(const DeltaLaunch& p, const float* gend, const __nv_bfloat16* M, const DeltaChain* fwd,
-                       const DeltaChain* rev, cudaStream_t stream) {
+int launch_delta_chain(const DeltaLaunch& p, const float* gend, const __nv_bfloat16* M, const DeltaChain& fwd,
+                       const DeltaChain& rev, cudaStream_t stream) {
   return p.dk == 64 ? chain_launch<64>(p, gend, M, fwd, rev, stream)
                     : chain_launch<128>(p, gend, M, fwd, rev, stream);
 }

@@ -363,7 +363,7 @@ struct DeltaChain {         // one direction of the state recurrence
 };
 // All chunks at once, each with buffers of its own.
 int launch_delta_prep(const DeltaLaunch& p, const DeltaPrepOut& o, cudaStream_t stream);
-// fwd nullable; rev nullable: X <- exp(G_last) X + M^T X + H, from the last chunk
-int launch_delta_chain(const DeltaLaunch& p, const float* gend, const __nv_bfloat16* M, const DeltaChain* fwd,
-                       const DeltaChain* rev, cudaStream_t stream);
+// both directions side by side; rev: X <- exp(G_last) X + M^T X + H, from the last chunk
+int launch_delta_chain(const DeltaLaunch& p, const float* gend, const __nv_bfloat16* M, const DeltaChain& fwd,
+                       const DeltaChain& rev, cudaStream_t stream);
 }  // namespace ttt

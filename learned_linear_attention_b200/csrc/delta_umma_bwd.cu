@@ -714,7 +714,7 @@ int bwd_launch(const DeltaBwdLaunch& L, cudaStream_t stream) {
       delta_hb_kernel<D>, dim3(grid), dim3(THREADS), HbSmem<D>::TOTAL, stream,
       mq, mk, md, mw, my, HbArgs{g, beta, f32(w.Hb), p.N, nch, p.scale, p.st});
   prof_after(K_DELTA_HB, stream);
-  if (launch_delta_chain(p, o.gend, o.M, &fwd, &rev, stream)) return -1;
+  if (launch_delta_chain(p, o.gend, o.M, fwd, rev, stream)) return -1;
   prof_before(K_DELTA_VALS, stream);
   const cudaError_t e_vals = launch_pdl(
       delta_vals_kernel<D>, dim3(grid), dim3(THREADS), ValsSmem<D>::TOTAL, stream,

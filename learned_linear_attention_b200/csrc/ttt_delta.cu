@@ -75,13 +75,14 @@ struct Stage {
 };
 
 // The next tile's tokens wait in registers while this one is worked on.  A
-// thread keeps its row of k and q and its column of the value tensor.
-template <typename Tin, int R4>
+// thread keeps its row of k and q and its column of the value tensor.  Without Q
+// (the replay, which reads nothing out) there are no queries.
+template <typename Tin, int R4, bool Q>
 struct Fetch {
   static constexpr int RW = R4 == 3 ? 128 : 32 * R4;      // threads of a token's row
   static constexpr int TS = THREADS / RW, NX = TT / TS;   // tokens side by side, and of a thread
   static constexpr int WS = THREADS / COLS, NW = TT / WS;
-  Tin k[NX], q[NX], w[NW], g, b;
+  Tin k[NX], q[Q ? NX : 1], w[NW], g, b;
   const Tin *kp, *qp, *wp, *gp, *bp;
   int N, dk, dv, r, tr, tw, tid;
   bool row, col;
@@ -92,20 +93,20 @@ struct Fetch {
     col = c0 + tid % COLS < dv;
     const size_t tok = bh * N;
     kp = k_ + tok * dk + r;
-    qp = q_ != nullptr ? q_ + tok * dk + r : nullptr;
+    if constexpr (Q) qp = q_ + tok * dk + r;
     wp = w_ + tok * dv + c0 + tid % COLS;
     gp = g_ != nullptr ? g_ + tok : nullptr;
     bp = b_ + tok;
   }
-  TTT_DEVICE_INLINE void load(int t0) {   // t0 may lie before the first or behind the last token
+  TTT_DEVICE_INLINE void load(int t0) {
     const Tin zero = from_f<Tin>(0.f);
-    const int n = t0 < 0 ? 0 : N - t0;
+    const int n = N - t0;
     const size_t x0 = ((size_t)t0 + tr) * dk, w0 = ((size_t)t0 + tw) * dv;
 #pragma unroll
     for (int i = 0; i < NX; ++i) {
       const bool in = row && tr + i * TS < n;
       k[i] = in ? kp[x0 + (size_t)(i * TS * dk)] : zero;
-      q[i] = in && qp != nullptr ? qp[x0 + (size_t)(i * TS * dk)] : zero;
+      if constexpr (Q) q[i] = in ? qp[x0 + (size_t)(i * TS * dk)] : zero;
     }
 #pragma unroll
     for (int i = 0; i < NW; ++i) w[i] = col && tw + i * WS < n ? wp[w0 + (size_t)(i * WS * dv)] : zero;
@@ -120,7 +121,7 @@ struct Fetch {
 #pragma unroll
       for (int i = 0; i < NX; ++i) {
         st.k[tr + i * TS][r] = to_f(k[i]);
-        st.q[tr + i * TS][r] = to_f(q[i]);
+        if constexpr (Q) st.q[tr + i * TS][r] = to_f(q[i]);
       }
     }
 #pragma unroll
@@ -143,8 +144,8 @@ TTT_DEVICE_INLINE void write_os(const Stage<R4>& st, T* dst, int n, int dv, int 
 }
 
 // Coefficients of the staged tokens: thread 16 b + d takes one of the 16
-// products within block b.
-template <int R4>
+// products within block b, the first ten of them with queries.
+template <int R4, bool Q>
 TTT_DEVICE_INLINE void coefficients(Stage<R4>& st, int tid) {
   const int base = tid / 16 * 4, d = tid % 16;
   // d: 0..9 q.k with (t, i) in lower-triangle order, 10..15 k.k below the diagonal
@@ -153,27 +154,29 @@ TTT_DEVICE_INLINE void coefficients(Stage<R4>& st, int tid) {
   const float* x = d < 10 ? st.q[base + t] : st.k[base + t];
   const float* y = st.k[base + i];
   float a0 = 0.f, a1 = 0.f, a2 = 0.f, a3 = 0.f;
+  if (Q || d >= 10) {
 #pragma unroll
-  for (int r = 0; r < 32 * R4; r += 4) {
-    const float4 u = *reinterpret_cast<const float4*>(x + r), v = *reinterpret_cast<const float4*>(y + r);
-    a0 = fmaf(u.x, v.x, a0);
-    a1 = fmaf(u.y, v.y, a1);
-    a2 = fmaf(u.z, v.z, a2);
-    a3 = fmaf(u.w, v.w, a3);
+    for (int r = 0; r < 32 * R4; r += 4) {
+      const float4 u = *reinterpret_cast<const float4*>(x + r), v = *reinterpret_cast<const float4*>(y + r);
+      a0 = fmaf(u.x, v.x, a0);
+      a1 = fmaf(u.y, v.y, a1);
+      a2 = fmaf(u.z, v.z, a2);
+      a3 = fmaf(u.w, v.w, a3);
+    }
   }
   float f = (a0 + a1) + (a2 + a3);
   const float4 av = *reinterpret_cast<const float4*>(st.a + base);
   if (i < 1 && t >= 1) f *= av.y;
   if (i < 2 && t >= 2) f *= av.z;
   if (i < 3 && t >= 3) f *= av.w;
-  if (d < 10) st.qk[base + t][i] = f;
-  else st.kk[base + t][i] = f;
+  if (d >= 10) st.kk[base + t][i] = f;
+  else if (Q) st.qk[base + t][i] = f;
   if (d < 4) {   // token d of the block
     st.A[base + d] = av.x * (d >= 1 ? av.y : 1.f) * (d >= 2 ? av.z : 1.f) * (d >= 3 ? av.w : 1.f);
     st.R[base + d] = (d < 1 ? av.y : 1.f) * (d < 2 ? av.z : 1.f) * (d < 3 ? av.w : 1.f);
 #pragma unroll
     for (int m = 0; m < 4; ++m) {
-      if (m > d) st.qk[base + d][m] = 0.f;
+      if (Q && m > d) st.qk[base + d][m] = 0.f;
       if (m >= d) st.kk[base + d][m] = 0.f;
     }
   }
@@ -221,8 +224,8 @@ TTT_DEVICE_INLINE float part_dot(const float (&x)[4 * R4], const float (&y)[4 * 
 // A CTA's 128 state threads walk tiles of TT tokens.  With HELP, 128 more
 // threads stage the next tile, form its coefficients and write the last one's
 // values meanwhile, in two buffers: what is left between tiles is one barrier.
-template <typename Tin, int R4, bool HELP, typename K, typename W, typename F>
-TTT_DEVICE_INLINE void walk_tiles(Stage<R4>* st, Fetch<Tin, R4>& f, int nch, bool down, float wscale, int tid,
+template <typename Tin, int R4, bool Q, bool HELP, typename K, typename W, typename F>
+TTT_DEVICE_INLINE void walk_tiles(Stage<R4>* st, Fetch<Tin, R4, Q>& f, int nch, bool down, float wscale, int tid,
                                   K keep, W work, F write) {
   if (nch == 0) return;
   // the i-th tile of the walk starts at token t0(i)
@@ -235,7 +238,7 @@ TTT_DEVICE_INLINE void walk_tiles(Stage<R4>* st, Fetch<Tin, R4>& f, int nch, boo
       f.put(s, wscale);
       named_bar_sync(1, THREADS);
       if (i + 1 < nch) f.load(t0(i + 1));
-      coefficients(s, h);
+      coefficients<R4, Q>(s, h);
     };
     if (helper) {
       f.load(t0(0));
@@ -259,7 +262,7 @@ TTT_DEVICE_INLINE void walk_tiles(Stage<R4>* st, Fetch<Tin, R4>& f, int nch, boo
       f.put(st[0], wscale);
       __syncthreads();
       if (i + 1 < nch) f.load(t0(i + 1));
-      coefficients(st[0], tid);
+      coefficients<R4, Q>(st[0], tid);
       keep(t0(i));
       __syncthreads();
       work(st[0], t0(i));
@@ -369,8 +372,8 @@ TTT_DEVICE_INLINE void rec_cta(Stage<R4>* st, const Tin* __restrict__ q, const T
     for (int i = 0; i < 4 * R4; ++i) s[i] = 0.f;
   }
   const int nch = tiles_of(N, TT);
-  Fetch<Tin, R4> f(k, KEEP ? nullptr : q, v, g, beta, bh, N, dk, dv, c0, tid % THREADS);
-  walk_tiles<Tin, R4, HELP>(
+  Fetch<Tin, R4, !KEEP> f(k, q, v, g, beta, bh, N, dk, dv, c0, tid % THREADS);
+  walk_tiles<Tin, R4, !KEEP, HELP>(
       st, f, nch, false, 1.f, tid,
       [&](int t0) {
         if constexpr (KEEP) col.store(Sc + (bh * nch + t0 / TT) * mat, s);
@@ -474,8 +477,8 @@ TTT_DEVICE_INLINE void rev_cta(Stage<R4>* st, const Tin* __restrict__ q, const T
     for (int i = 0; i < 4 * R4; ++i) x[i] = 0.f;
   }
   const int nch = tiles_of(N, TT);
-  Fetch<Tin, R4> f(k, q, dout, g, beta, bh, N, dk, dv, c0, tid % THREADS);
-  walk_tiles<Tin, R4, HELP>(
+  Fetch<Tin, R4, true> f(k, q, dout, g, beta, bh, N, dk, dv, c0, tid % THREADS);
+  walk_tiles<Tin, R4, true, HELP>(
       st, f, nch, true, scale, tid,
       [&](int t0) { col.store(Xc + (bh * nch + t0 / TT) * mat, x); },
       [&](Stage<R4>& t, int t0) { rev_tile<R4>(t, x, min(TT, N - t0), col.l, cl); },
