@@ -263,7 +263,10 @@ int ttt_delta_step(const ttt_delta_desc* desc, const void* q, const void* k, con
  *   TTT_NORM_L2:  r = 1 / max(|x|, eps)
  *   act: TTT_GATE_NONE 1; TTT_GATE_SILU z sigmoid(z); TTT_GATE_SIGMOID sigmoid(z)
  *
- * x, z, res, out: [rows, D] contiguous in `dtype`; w: [D] float32.
+ * x, z, res, out: [rows, D] contiguous in `dtype`; w: [D] float32.  r is
+ * formed in float32 from the sum of the squares, so a row whose sum passes
+ * float32's range (values of 1e19 and more) counts as infinitely long, with r =
+ * 0, and squares below it (values of 1e-23 and less) count as 0.
  * ---------------------------------------------------------------------- */
 typedef enum { TTT_NORM_RMS = 0, TTT_NORM_L2 = 1 } ttt_norm_kind;
 typedef enum { TTT_GATE_NONE = 0, TTT_GATE_SILU = 1, TTT_GATE_SIGMOID = 2 } ttt_gate;
@@ -272,7 +275,7 @@ typedef struct {
   int D;                /* 1..8192, D * sizeof(element) a multiple of 16     */
   ttt_norm_kind kind;
   ttt_gate gate;
-  float eps;            /* > 0                                               */
+  float eps;            /* > 0 (TTT_NORM_L2: a normal number, 1.2e-38 or more) */
   float scale;          /* of the normalised term                            */
   ttt_dtype dtype;
 } ttt_norm_desc;

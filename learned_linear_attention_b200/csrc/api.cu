@@ -3,6 +3,7 @@
 #include <stdio.h>
 #include <stdlib.h>
 #include <string.h>
+#include <float.h>
 #include <math.h>
 
 #include <algorithm>
@@ -422,6 +423,7 @@ static int check_norm(const ttt_norm_desc* d) {
   if (d->gate != TTT_GATE_NONE && d->gate != TTT_GATE_SILU && d->gate != TTT_GATE_SIGMOID)
     return TTT_ERR_ARG;
   if (!(d->eps > 0.f) || d->scale != d->scale) return TTT_ERR_ARG;
+  if (d->kind == TTT_NORM_L2 && d->eps < FLT_MIN) return TTT_ERR_ARG;   // 1 / eps is a row's factor
   if (!dtype_ok(d->dtype)) return TTT_ERR_DTYPE;
   if (d->D > 8192) return TTT_ERR_UNSUPPORTED;
   if (d->D * dtype_bytes(d->dtype) % 16 != 0) return TTT_ERR_ALIGN;

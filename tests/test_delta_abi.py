@@ -220,3 +220,14 @@ def test_workspace_of_the_longest_sequences():
             one = 4 + 2 * pair + 3 * mat
             assert chunks / 6 * one <= _bytes("ttt_delta_workspace_bytes", d) <= (chunks + 8) * one + 4096
             assert _bytes("ttt_delta_layer_workspace_bytes", d) >= _bytes("ttt_delta_workspace_bytes", d) + 3 * N * D * 2
+
+
+def test_norm_refuses_an_eps_whose_inverse_is_infinite():
+    """A row of zeros has the factor 1 / eps: with eps below 1.2e-38 it would be 0 times infinity."""
+    for eps in (1e-40, 1.4e-45, 1.1754942e-38):
+        for call in (_norm, _norm_bwd):
+            assert call(T.make_norm_desc(5, 64, kind="l2", gate="silu", eps=eps)) == T.TTT_ERR_ARG
+        # (rms: the mean of squares is added to it; nothing but the pointers is wrong here)
+        assert _norm(T.make_norm_desc(5, 64, gate="silu", eps=eps), x=0) == T.TTT_ERR_ARG
+        assert _norm(T.make_norm_desc(0, 64, gate="silu", eps=eps)) == T.TTT_OK
+    assert _norm(T.make_norm_desc(0, 64, kind="l2", gate="silu", eps=1.1754944e-38)) == T.TTT_OK

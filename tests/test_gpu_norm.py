@@ -225,3 +225,29 @@ def test_float32_gates_have_float32_precision(cuda_device):
     T.ttt_norm_fwd(d, x, None, z, None, out)
     ref = row_norm(host(x), None, host(z), gate="sigmoid", eps=d.eps)
     assert (np.abs(host(out) - ref) / ref).max() <= 16 * U
+
+
+@pytest.mark.parametrize("dt", ["f32", "bf16"])
+@pytest.mark.parametrize("kind,eps", [("rms", 1e-6), ("l2", 1e-6), ("l2", 1.1754944e-38)])
+def test_rows_at_the_ends_of_the_range(cuda_device, dt, kind, eps):
+    """A row whose squares' sum is infinite has r = 0; a row of zeros stays zero
+    with the smallest eps.  Rows beside them are as without them."""
+    p = make(5, 64, dt, True, "silu", True)
+    d = T.make_norm_desc(5, 64, kind=kind, gate="silu", eps=eps, dtype=dt)
+    ws = T.alloc_workspace(T.ttt_norm_bwd_workspace_bytes(d))
+
+    def run():
+        out, dx, dz, dw = torch.empty_like(p["x"]), torch.empty_like(p["x"]), torch.empty_like(p["x"]), torch.empty_like(p["w"])
+        T.ttt_norm_fwd(d, p["x"], p["w"], p["z"], p["res"], out)
+        T.ttt_norm_bwd(d, p["x"], p["w"], p["z"], p["dout"], dx, dw, dz, ws)
+        return out, dx, dz, dw
+
+    want = run()
+    p["x"][1], p["x"][3] = 2e19, 0
+    out, dx, dz, dw = run()
+    for r in (1, 3):
+        assert torch.equal(out[r], p["res"][r])
+        assert bool((dz[r] == 0).all())
+    assert bool((dx[1] == 0).all()) and bool(torch.isfinite(dw).all())
+    for a, b in zip((out, dx, dz), want):
+        assert torch.equal(a[[0, 2, 4]], b[[0, 2, 4]])
