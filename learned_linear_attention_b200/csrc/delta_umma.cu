@@ -179,7 +179,7 @@ TTT_DEVICE_INLINE void invert(float* A, int warp, int lane) {
 // ------------------------------------------------------------------ prep
 // A chunk takes about 22 us with two CTAs an SM (heads of 64), a third of it
 // the inverse, the rest the latency of two rounds of products, splits and
-// stores: 2048 chunks 164 us, and no unit is more than half busy.
+// stores: 2048 chunks 166 us, and no unit is more than half busy.
 struct PrepArgs {
   const __nv_bfloat16 *g, *beta;
   float* gend;             // [BH nch] exp(G_last)
@@ -902,15 +902,18 @@ int fwd_launch(const DeltaLaunch& p, cudaStream_t stream) {
 }  // namespace
 
 // Short sequences go token by token: the chunk kernels' latency is that of a
-// whole chunk and of three launches (23 us forward, 47 us backward at D = 64;
-// 32 and 60 at 128), the recurrent ones' 0.09 us a token at D = 64 and 0.14 at
-// 128 (backward 0.11 and 0.16, behind 15 and 31), times the rounds that their
+// whole chunk and of three launches (23 us forward, 50 us backward at D = 64;
+// 31 and 62 at 128), the recurrent ones' 0.1 us a token at D = 64 and 0.14 at 128
+// (backward the same behind 24 and 40), times the rounds that their
 // CTAs of 16 value columns take on the device.  Both grow alike with the heads
 // once the chunks too fill it, so rounds count up to 5.  Token by token against
-// chunks, us: forward 8 heads of 64, 128 tokens 16 / 17, 256 tokens 28 / 23;
-// 128 heads, 32 tokens 15 / 23, 64 tokens 25 / 23.  Backward 8 heads of 64, 256
-// tokens 44 / 48, 512 tokens 69 / 50; of 128, 128 tokens 57 / 60, 256 tokens 75 /
-// 62; 128 heads of 64, 32 tokens 41 / 52, 64 tokens 63 / 52.
+// chunks, us: forward 8 heads of 64, 128 tokens 17 / 23, 256 tokens 29 / 23; of
+// 128, 128 tokens 25 / 31, 256 tokens 43 / 32; 128 heads of 64, 32 tokens 16 / 23,
+// 64 tokens 27 / 23.  Backward 8 heads of 64, 256 tokens 47 / 50, 300 tokens 51 /
+// 51, 512 tokens 72 / 52; of 128, 128 tokens 59 / 62, 200 tokens 72 / 63; 128 heads
+// of 64, 32 tokens 41 / 53, 64 tokens 69 / 54.  Heads of other sizes, or of two,
+// go token by token at every length: the tiles, the operands' layouts and the
+// D x D recurrence are written for one D.
 bool delta_uses_umma(int bf16, int dk, int dv, long long BH, int N, int sms, bool backward) {
   if (!bf16 || dk != dv || (dk != 64 && dk != 128)) return false;
   const double rounds = (double)BH * (dv / 16) * (backward ? 2 : 1) / sms;

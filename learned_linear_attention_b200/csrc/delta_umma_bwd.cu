@@ -183,8 +183,9 @@ __global__ void __launch_bounds__(THREADS, 1)
 }
 
 // ------------------------------------------------------------------ values
-// Bound by HBM, which it reads T, W, Ut, the border states and what Hb left
-// from: 2048 chunks of heads of 64 134 us, 4.6 TB/s.
+// Reads T, W, Ut, the border states and what Hb left, 0.6 GB in 135 us for 2048
+// chunks of heads of 64: 4.5 TB/s, two thirds of what HBM gives.  Bound by the
+// latency of those loads, which one CTA an SM (its shared memory) does not hide.
 struct ValsArgs {
   const __nv_bfloat16 *g, *beta, *v;
   const float* Ut;
@@ -336,7 +337,8 @@ __global__ void __launch_bounds__(THREADS, 1)
 
 // ------------------------------------------------------------------ keys
 // One CTA an SM, by its shared memory; bound by the latency of its four rounds
-// of products: 2048 chunks of heads of 64 187 us.
+// of products: 2048 chunks of heads of 64 196 us (188 without the pairs' part of
+// dg, of which only what the last round does not hide counts).
 struct KeysArgs {
   const __nv_bfloat16 *g, *beta;
   __nv_bfloat16 *dq, *dk;

@@ -526,7 +526,8 @@ __global__ void __launch_bounds__(HELP ? 2 * THREADS : THREADS) delta_states_ker
 // tokens behind t then enter with both signs, and where the decays are strong
 // what is left of them is larger than dg_t.)
 // One CTA per chunk and head, every matrix in shared memory, whose reads and
-// the latency of the phases bound it: 10 us for one chunk of heads of 64.
+// the latency of the phases bound it: 12 us for one chunk of heads of 64, 2 of
+// them for dg.
 constexpr int CB = TT;          // tokens of a chunk
 constexpr int GTHREADS = 256;
 
@@ -862,8 +863,10 @@ size_t chunk_grad_smem(int dk, int dv) { return sizeof(float) * GradSmem(dk, dv)
 // columns four at a time, the other threads split dk.  The state slice is
 // read into registers in one sweep, the two dot products over dk (S^T k, and
 // q.S' from q.S and q.k) are joined through shared memory in one exchange,
-// and the slice is written back: bound by the state's bytes (256 rows of 16
-// heads of 128: 522 MB in 98 us, 5.4 TB/s).
+// and the slice is written back: bound by the state's bytes (247 rows of 16
+// heads of 128: 522 MB in 95 us, 5.5 TB/s).  To find the rows that share a
+// state every CTA reads all B slots, from L2: 1 KB beside 32 KB of state at 256
+// rows, as much as the state at 8192.
 constexpr int STHREADS = 128;
 
 template <typename Tin, typename Tout, int VC>

@@ -5,8 +5,8 @@
 // CTA of 256), each holding the same V 16-byte vectors of every row it meets,
 // so a row is read once, its sum of squares is a few shuffles, and the
 // weight's gradient is summed in registers over the CTA's rows.  Bound by
-// memory: 262,144 rows of 128 bf16 with gate and residual 6.2 TB/s, their
-// gradients 5.1.
+// memory: 262,144 rows of 128 bf16 with gate and residual 45 us, 6.0 TB/s, their
+// gradients 68 us, 5.0.
 #include <algorithm>
 #include <type_traits>
 
