@@ -638,7 +638,8 @@ struct OutSmem {
   static constexpr uint32_t OP = DA * ATOM, SA = D * 128;
   static constexpr uint32_t Q = 0, K = OP, W = 2 * OP;              // W hi, lo
   static constexpr uint32_t S = 4 * OP;                             // S0 hi, lo
-  static constexpr uint32_t U = 0;                                  // hi, lo, over Q and K
+  static constexpr uint32_t U = 0, QS = 3 * ATOM;                   // behind the first products: three planes, Q S0
+  static_assert(QS + C * 64 * 4 <= S + 2 * SA, "in the place of the operands");
   static constexpr uint32_t GATES = S + 2 * SA, BAR = GATES + sizeof(Gates), TOTAL = BAR + 64;
 };
 
@@ -648,7 +649,7 @@ TTT_DEVICE_INLINE void out_cta(uint8_t* smem, const CUtensorMap& mapQ, const CUt
                                unsigned block) {
   using SM = OutSmem<D>;
   constexpr int DA = D / 64;
-  constexpr uint32_t TM_P = 0, TM_W = 128, TM_Q = 192, TM_COLS = 256;   // P U takes W S0's place
+  constexpr uint32_t TM_P = 0, TM_W = 128, TM_Q = 192, TM_COLS = 256;   // P U takes Q S0's place
   Bars& bars = *reinterpret_cast<Bars*>(smem + SM::BAR);
   Gates& gates = *reinterpret_cast<Gates*>(smem + SM::GATES);
   const int tid = threadIdx.x, warp = warp_index(), lane = tid & 31;
@@ -687,55 +688,82 @@ TTT_DEVICE_INLINE void out_cta(uint8_t* smem, const CUtensorMap& mapQ, const CUt
       mma_commit(&bars.mma);
     }
     if (!ph.mma_done(2)) return;
-    // U = Ut - W S0
+    // U = Ut - W S0, and Q S0 into shared memory (this thread's values stay its own)
+    float* qs = reinterpret_cast<float*>(smem + SM::QS) + (cg * 4 * C + row) * 4;
     {
       float w[16];
       tmem_ld16(tmem + lanes + TM_W + cg * 16, w);
 #pragma unroll
       for (int i = 0; i < 16; ++i) u[i] -= w[i];
-      store8_split(sb + SM::U, sb + SM::U + ATOM, row, cg * 16, u);
-      store8_split(sb + SM::U, sb + SM::U + ATOM, row, cg * 16 + 8, u + 8);
+#pragma unroll
+      for (int i = 0; i < 16; i += 8)
+        store8_split3(sb + SM::U, sb + SM::U + ATOM, sb + SM::U + 2 * ATOM, row, cg * 16 + i, u + i);
+      tmem_ld16(tmem + lanes + TM_Q + cg * 16, w);
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        *reinterpret_cast<float4*>(qs + i * C * 4) = make_float4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
     }
-    // P = Gam . Q K^T on and below the diagonal, hi and lo, becomes an operand in
-    // tensor memory in the place of Q K^T
-    uint32_t ph_[16], pl[16];
+    // P = Gam . Q K^T on and below the diagonal becomes an operand in tensor memory
+    // in the place of Q K^T and W S0, three planes of 64 columns
+    float x[32];
 #pragma unroll
     for (int b = 0; b < 2; ++b) {
       const int c0 = cg * 32 + b * 16;
-      float x[16];
       if (c0 <= q4 * 32 + 31) {
-        tmem_ld16(tmem + lanes + TM_P + c0, x);
-        weigh16<true>(gates, q4 * 32, row, c0, 1.f, x);
+        tmem_ld16(tmem + lanes + TM_P + c0, x + 16 * b);
+        weigh16<true>(gates, q4 * 32, row, c0, 1.f, x + 16 * b);
       } else {
 #pragma unroll
-        for (int j = 0; j < 16; ++j) x[j] = 0.f;
+        for (int j = 0; j < 16; ++j) x[16 * b + j] = 0.f;
       }
-#pragma unroll
-      for (int j = 0; j < 8; ++j) split2(x[2 * j], x[2 * j + 1], ph_[8 * b + j], pl[8 * b + j]);
     }
     tc_fence_before();
-    __syncthreads();   // all of Q K^T has been read
+    __syncthreads();   // all of Q K^T and W S0 has been read
     tc_fence_after();
-    tmem_st16_issue(tmem + lanes + TM_P + cg * 16, ph_);
-    tmem_st16_issue(tmem + lanes + TM_P + 64 + cg * 16, pl);
+#pragma unroll
+    for (int b = 0; b < 2; ++b)
+#pragma unroll
+      for (int p = 0; p < 3; ++p) {
+        uint32_t h[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          float *v = x + 16 * b + 2 * j;
+          h[j] = pack_bf16x2(v[0], v[1]);
+          v[0] -= bf16lo(h[j]);
+          v[1] -= bf16hi(h[j]);
+        }
+        tmem_st8_issue(tmem + lanes + TM_P + 64 * p + cg * 16 + 8 * b, h);
+      }
     tmem_wait_st();
     ph.publish();
     if (warp == 0 && elect_one()) {
+      // two planes would leave 2.6e-6 of the outputs for P and for U each, and lo lo
+      // 2.8e-6 (together 4.7e-6); these leave 4e-8, and the outputs are as far off as S0
+      // and W S0, 9e-7.  It takes 2 to 3 % of the call (64 heads of 64, 32K tokens: 1689
+      // us against 1653)
       const Pair U{{sb + SM::U, ATOM, true}, ATOM};
-      const uint32_t hi = tmem + TM_P, lo = hi + 64;
-      products<8>(Prod(tmem + TM_W, lo, U.hi, 64, false));
-      products<8>(Prod(tmem + TM_W, hi, U.lo(), 64, true));
-      products<8>(Prod(tmem + TM_W, hi, U.hi, 64, true));
+      const uint32_t hi = tmem + TM_P, lo = hi + 64, rest = hi + 128, o = tmem + TM_Q;
+      products<8>(Prod(o, rest, U.hi, 64, false));
+      products<8>(Prod(o, hi, U.plane(2), 64, true));
+      products<8>(Prod(o, lo, U.lo(), 64, true));
+      products<8>(Prod(o, lo, U.hi, 64, true));
+      products<8>(Prod(o, hi, U.lo(), 64, true));
+      products<8>(Prod(o, hi, U.hi, 64, true));
       mma_commit(&bars.mma);
     }
     if (!ph.mma_done(3)) return;
     const float gam = a.scale * gate_decay(gates, row);
-    float o[16], qs[16];
-    tmem_ld16(tmem + lanes + TM_W + cg * 16, o);
-    tmem_ld16(tmem + lanes + TM_Q + cg * 16, qs);
+    float o[16];
+    tmem_ld16(tmem + lanes + TM_Q + cg * 16, o);
     if (row >= id.n) return;
 #pragma unroll
-    for (int i = 0; i < 16; ++i) o[i] = fmaf(gam, qs[i], a.scale * o[i]);
+    for (int i = 0; i < 16; i += 4) {
+      const float4 v = *reinterpret_cast<const float4*>(qs + i * C);
+      o[i] = fmaf(gam, v.x, a.scale * o[i]);
+      o[i + 1] = fmaf(gam, v.y, a.scale * o[i + 1]);
+      o[i + 2] = fmaf(gam, v.z, a.scale * o[i + 2]);
+      o[i + 3] = fmaf(gam, v.w, a.scale * o[i + 3]);
+    }
     const size_t at = (id.tok + row) * D + slice * 64 + cg * 16;
     if (a.out_bf16) {
       store_bf16_row16(static_cast<__nv_bfloat16*>(a.out) + at, o);

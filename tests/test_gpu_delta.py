@@ -603,3 +603,17 @@ def test_states_and_float32_outputs_of_the_chunk_form(cuda_device, d, decay, sta
     norm_near(S_end, S, 2e-6 if decay else 1e-5, "S")
     norm_near(dS0, want, 2e-6 if decay else 1e-5, "dS0")
     norm_near(o, ref, 1.5e-5, "out")
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("start", [True, False])
+def test_float32_outputs_of_the_chunk_form_with_decay(cuda_device, d, start):
+    """P and U in three planes (2^-26 an operand, products down to 2^-27 kept), so the
+    outputs are off by what two planes of S0 (2^-18, 0.4 in the mean square: 1.5e-6 of
+    Q S0, which the decay makes a third of the outputs in norm: 5e-7) and of T diag(beta)
+    (5e-7) leave, the exponentials' 2^-22 and the sums: 2e-6.  Two planes of P or U
+    would leave 2.5e-6 more."""
+    p = Problem(1, 2, 1024, d, d, "bf16", start=start)
+    assert in_chunks(p, False)
+    ref, _ = delta_recurrent(*(p.host(n) for n in ("q", "k", "v", "g", "beta")), p.host("S0"))
+    norm_near(p.fwd(out="f32")[0], ref, 2e-6, "out")
