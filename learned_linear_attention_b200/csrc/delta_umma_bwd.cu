@@ -20,7 +20,7 @@
 // reverse recurrence runs over the same Mc, side
 // by side with the forward one:
 //   delta_prep_kernel      K, V -> W, Ut, T, Mc, Hc
-//   delta_hb_kernel        Q, K, dO, W -> Hb, -scale P^T dO
+//   delta_hb_kernel        Q, K, dO, W -> Hb, Z = -scale P^T dO
 //   delta_chain_kernel     S0 and X1 of every chunk, dS0
 //   delta_vals_kernel      U, Y, dV, first part of dbeta; 64 value columns a CTA
 //   delta_keys_kernel      dQ, dK, r, w, sums of V, second part of dbeta; 64 key columns a CTA
@@ -59,7 +59,7 @@ TTT_DEVICE_INLINE float row_total(const float* red, int row) {
 // heads of 64 116 us.
 struct HbArgs {
   const __nv_bfloat16 *g, *beta;
-  float* H;
+  float *H, *Z;            // Z = -scale P^T dO: [BH nch][D / 64] float32 tiles [128][64]
   int N, nch;
   float scale;
   DevStatus st;
@@ -77,8 +77,7 @@ struct HbSmem {
 template <int D>
 __global__ void __launch_bounds__(THREADS, 1)
     delta_hb_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_constant__ CUtensorMap mapK,
-                    const __grid_constant__ CUtensorMap mapD, const __grid_constant__ CUtensorMap mapW,
-                    const __grid_constant__ CUtensorMap mapY, HbArgs a) {
+                    const __grid_constant__ CUtensorMap mapD, const __grid_constant__ CUtensorMap mapW, HbArgs a) {
   using SM = HbSmem<D>;
   constexpr int DA = D / 64;
   constexpr uint32_t TM_P = 0, TM_U = 128, TM_COLS = 256;   // Hb's accumulators take their places
@@ -148,6 +147,7 @@ __global__ void __launch_bounds__(THREADS, 1)
         store8_split3(at, at + ATOM, at + 2 * ATOM, row, cg * 16 + j, u + j);
         store8_split3(at + 3 * ATOM, at + 4 * ATOM, at + 5 * ATOM, row, cg * 16 + j, d);
       }
+      store_tile16(a.Z + (id.ci * DA + id.slice) * C * 64, C, row, cg * 16, u);
     }
     ph.publish();
     if (warp == 0 && elect_one()) {
@@ -159,11 +159,6 @@ __global__ void __launch_bounds__(THREADS, 1)
       products<8>(Prod(tmem + 64, Wt.lo(), U.hi, D, 128, true));
       products<8>(Prod(tmem, Qmn, G.hi, D, 192, true));
       mma_commit(&bars.mma);
-    }
-    if (warp == 1 && elect_one()) {
-      for (int h = 0; h < 2; ++h)
-        tma_store_3d(&mapY, smem + SM::P + h * ATOM, 64 * id.slice, 0, (int)(2 * id.ci + h));
-      bulk_commit();
     }
     if (!ph.mma_done(4)) return;
     const int r = D == 64 ? q4 * 16 + lane : row;
@@ -188,7 +183,7 @@ __global__ void __launch_bounds__(THREADS, 1)
 // latency of those loads, which one CTA an SM (its shared memory) does not hide.
 struct ValsArgs {
   const __nv_bfloat16 *g, *beta, *v;
-  const float* Ut;
+  const float *Ut, *Z;     // Z in the memory that Y takes
   __nv_bfloat16* dv;
   float* bpart;            // [D / 64][BH N]
   int N, nch;
@@ -223,7 +218,7 @@ __global__ void __launch_bounds__(THREADS, 1)
   const ChunkId id(blockIdx.x, DA, Slab{0, a.nch, 0}, a.N);
   const uint32_t sb = smem_u32(smem);
   const uint32_t tmem = cta_begin(bars, TM_COLS, warp, [&]() {
-    mbar_arrive_expect_tx(&bars.load[0], 3 * DA * ATOM + 2 * ATOM + 4 * SM::SA);
+    mbar_arrive_expect_tx(&bars.load[0], 3 * DA * ATOM + 4 * SM::SA);
     for (int i = 0; i < DA; ++i) {
       tma_load_3d(smem + SM::K + i * ATOM, &mapK, &bars.load[0], 64 * i, id.t0, (int)id.bh);
       for (int h = 0; h < 2; ++h)
@@ -233,13 +228,17 @@ __global__ void __launch_bounds__(THREADS, 1)
       const int z = (int)(2 * id.ci + h), x = 64 * id.slice;
       tma_load_3d(smem + SM::S + h * SM::SA, &mapS, &bars.load[0], x, 0, z);
       tma_load_3d(smem + SM::X + h * SM::SA, &mapX, &bars.load[0], x, 0, z);
-      tma_load_3d(smem + SM::Y + h * ATOM, &mapY, &bars.load[0], x, 0, z);
     }
   });
   Phase ph{Waiter{&bars.abort, a.st, 1400}, &bars.mma, 0};
   const int q4 = warp & 3, cg = warp >> 2, row = q4 * 32 + lane;
   const uint32_t lanes = (uint32_t)(q4 * 32) << 16;
   if (cg == 1) load_gates(gates, a.g ? a.g + id.tok : nullptr, a.beta + id.tok, id.n, row);
+  // this thread's 16 values of Ut and Z, while the operands travel
+  const size_t at_slice = id.ci * DA + id.slice;
+  float u[16], y[16];
+  load_tile16(a.Ut + id.ci * C * D, C, row, id.slice * 64 + cg * 16, u);
+  load_tile16(a.Z + at_slice * C * 64, C, row, cg * 16, y);
   int loads = 1;
   auto work = [&]() {
     const Op K{sb + SM::K, ATOM, false};
@@ -261,16 +260,14 @@ __global__ void __launch_bounds__(THREADS, 1)
           tma_load_3d(smem + SM::T + (2 * h + i) * ATOM, &mapT, &bars.load[1], 64 * i, 0, (int)(2 * id.ci + h));
     }
     loads = 2;
-    // U = Ut - W S0;  dU = rho K X1 - (-scale P^T dO), in place
+    // U = Ut - W S0;  dU = rho K X1 - Z, whose third plane takes X1's place (dU is what
+    // dV is made of: two planes, and lo lo left out, would be 3e-6 of it)
     {
       const float rho = gate_ratio(gates, C - 1, row);
       const int c = cg * 16;
-      float w[16], x[16], u[16], y[16];
-      load_tile16(a.Ut + id.ci * C * D, C, row, id.slice * 64 + c, u);
+      float w[16], x[16];
       tmem_ld16(tmem + lanes + TM_W + c, w);
       tmem_ld16(tmem + lanes + TM_X + c, x);
-#pragma unroll
-      for (int b = 0; b < 16; b += 8) load8_split(sb + SM::Y, sb + SM::Y + ATOM, row, c + b, y + b);
 #pragma unroll
       for (int i = 0; i < 16; ++i) {
         u[i] -= w[i];
@@ -279,7 +276,7 @@ __global__ void __launch_bounds__(THREADS, 1)
 #pragma unroll
       for (int b = 0; b < 16; b += 8) {
         store8_split(sb + SM::U, sb + SM::U + ATOM, row, c + b, u + b);
-        store8_split(sb + SM::Y, sb + SM::Y + ATOM, row, c + b, y + b);
+        store8_split3(sb + SM::Y, sb + SM::Y + ATOM, sb + SM::X, row, c + b, y + b);
       }
     }
     ph.publish();
@@ -290,7 +287,9 @@ __global__ void __launch_bounds__(THREADS, 1)
     }
     if (warp == 0 && ph.W.wait_warp(&bars.load[1], 0, 3) && elect_one()) {
       const Pair Tt{{sb + SM::T, ATOM, true}, 2 * ATOM}, dU{{sb + SM::Y, ATOM, true}, ATOM};
-      products<8>(Prod(tmem + TM_Y, Tt.lo(), dU.hi, 128, 64, false));
+      products<8>(Prod(tmem + TM_Y, Tt.hi, Op{sb + SM::X, ATOM, true}, 128, 64, false));
+      products<8>(Prod(tmem + TM_Y, Tt.lo(), dU.lo(), 128, 64, true));
+      products<8>(Prod(tmem + TM_Y, Tt.lo(), dU.hi, 128, 64, true));
       products<8>(Prod(tmem + TM_Y, Tt.hi, dU.lo(), 128, 64, true));
       products<8>(Prod(tmem + TM_Y, Tt.hi, dU.hi, 128, 64, true));
       mma_commit(&bars.mma);
@@ -300,7 +299,7 @@ __global__ void __launch_bounds__(THREADS, 1)
       float acc = 0.f;
       const float beta = gates.beta[row], gam = gate_decay(gates, row);
       const size_t at = (id.tok + row) * D + id.slice * 64 + cg * 16;
-      float y[16], z[16];
+      float z[16];
       tmem_ld16(tmem + lanes + TM_Y + cg * 16, y);
       tmem_ld16(tmem + lanes + TM_Z + cg * 16, z);
 #pragma unroll
@@ -326,7 +325,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     ph.publish();
     if (warp == 1 && elect_one()) {
       for (int h = 0; h < 2; ++h)
-        tma_store_3d(&mapY, smem + SM::Y + h * ATOM, 64 * id.slice, 0, (int)(2 * id.ci + h));
+        tma_store_3d(&mapY, smem + SM::Y + h * ATOM, 0, 0, (int)(2 * at_slice + h));
       bulk_commit();
     }
     if (cg == 0 && row < id.n) a.bpart[id.slice * a.tokens + id.tok + row] = row_total(red, row);
@@ -389,7 +388,7 @@ __global__ void __launch_bounds__(THREADS, 1)
       for (int h = 0; h < 2; ++h) {
         const int z = (int)(2 * id.ci + h);
         tma_load_3d(smem + SM::U + (h * DA + i) * ATOM, &mapU, &bars.load[0], 64 * i, 0, z);
-        tma_load_3d(smem + SM::Y + (h * DA + i) * ATOM, &mapY, &bars.load[0], 64 * i, 0, z);
+        tma_load_3d(smem + SM::Y + (h * DA + i) * ATOM, &mapY, &bars.load[0], 0, 0, (int)(2 * (id.ci * DA + i) + h));
         tma_load_3d(smem + SM::S + (h * DA + i) * SM::HA, &mapS, &bars.load[0], 64 * i, 64 * id.slice, z);
         tma_load_3d(smem + SM::X + (h * DA + i) * SM::HA, &mapX, &bars.load[0], 64 * i, 64 * id.slice, z);
       }
@@ -697,7 +696,7 @@ int bwd_launch(const DeltaBwdLaunch& L, cudaStream_t stream) {
       make_tmap_bf16_3d(&md, L.dout, D, p.N, BH, rs, p.N * rs, 64, C) ||
       make_tmap_bf16_3d(&mw, o.W, D, C, 2 * nc, rs, C * rs, 64, C) ||
       make_tmap_bf16_3d(&mu, ws + w.U, D, C, 2 * nc, rs, C * rs, 64, C) ||
-      make_tmap_bf16_3d(&my, ws + w.Y, D, C, 2 * nc, rs, C * rs, 64, C) ||
+      make_tmap_bf16_3d(&my, ws + w.Y, 64, C, 2 * DA * nc, 128, ATOM, 64, C) ||   // [BH nch][D / 64][hi, lo][128][64]
       make_tmap_bf16_3d(&mt, o.T, C, C, 2 * nc, 2 * C, 2 * C * C, 64, C) ||
       make_tmap_bf16_3d(&ms, fwd.X, D, D, 2 * nc, rs, D * rs, 64, D) ||
       make_tmap_bf16_3d(&mx, rev.X, D, D, 2 * nc, rs, D * rs, 64, D) ||
@@ -714,14 +713,14 @@ int bwd_launch(const DeltaBwdLaunch& L, cudaStream_t stream) {
   prof_before(K_DELTA_HB, stream);
   const cudaError_t e_hb = launch_pdl(
       delta_hb_kernel<D>, dim3(grid), dim3(THREADS), HbSmem<D>::TOTAL, stream,
-      mq, mk, md, mw, my, HbArgs{g, beta, f32(w.Hb), p.N, nch, p.scale, p.st});
+      mq, mk, md, mw, HbArgs{g, beta, f32(w.Hb), f32(w.Y), p.N, nch, p.scale, p.st});
   prof_after(K_DELTA_HB, stream);
   if (launch_delta_chain(p, o.gend, o.M, fwd, rev, stream)) return -1;
   prof_before(K_DELTA_VALS, stream);
   const cudaError_t e_vals = launch_pdl(
       delta_vals_kernel<D>, dim3(grid), dim3(THREADS), ValsSmem<D>::TOTAL, stream,
       mk, mw, mu, my, mt, ms, mx,
-      ValsArgs{g, beta, (const __nv_bfloat16*)p.v, o.U, (__nv_bfloat16*)L.dv, f32(w.bpart), p.N, nch, tokens, p.st});
+      ValsArgs{g, beta, (const __nv_bfloat16*)p.v, o.U, f32(w.Y), (__nv_bfloat16*)L.dv, f32(w.bpart), p.N, nch, tokens, p.st});
   prof_after(K_DELTA_VALS, stream);
   prof_before(K_DELTA_KEYS, stream);
   const cudaError_t e_keys = launch_pdl(
