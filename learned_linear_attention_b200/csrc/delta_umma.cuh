@@ -290,7 +290,7 @@ struct ChunkId {
   }
 };
 struct Bars {
-  uint64_t load[2], mma, aux, fin;   // aux, fin: of product groups waited for beside those of mma
+  uint64_t load[3], mma, aux, fin, half;   // aux, fin, half: of product groups waited for beside those of mma
   uint32_t tmem, abort;
 };
 // Barriers and `cols` TMEM columns, before the first phase; returns the TMEM
@@ -302,11 +302,11 @@ struct Bars {
 template <typename F>
 TTT_DEVICE_INLINE uint32_t cta_begin(Bars& b, uint32_t cols, int warp, F loads) {
   if (warp == 0 && elect_one()) {
-    mbar_init(&b.load[0], 1);
-    mbar_init(&b.load[1], 1);
+    for (int i = 0; i < 3; ++i) mbar_init(&b.load[i], 1);
     mbar_init(&b.mma, 1);
     mbar_init(&b.aux, 1);
     mbar_init(&b.fin, 1);
+    mbar_init(&b.half, 1);
     b.abort = 0;
     fence_barrier_init();
     pdl_wait();
@@ -324,12 +324,13 @@ TTT_DEVICE_INLINE uint32_t cta_begin(Bars& b, uint32_t cols, int warp, F loads) 
   return __shfl_sync(0xffffffffu, b.tmem, 0);
 }
 // After the last phase, or an aborted one: nothing in flight outlives the CTA.
-// `loads` counts the load barriers in use.  Warp 0's elected thread issues the
+// `loads` has a bit for each load barrier in use.  Warp 0's elected thread issues the
 // products, warp 1's the stores: an election has one outcome, so the threads
 // that wait here are the same ones.
 TTT_DEVICE_INLINE void cta_end(Bars& b, const Phase& ph, int loads, uint32_t tmem, uint32_t cols, int warp) {
   if (warp == 0 && ph.W.aborted() && elect_one()) {
-    for (int i = 0; i < loads; ++i) ph.W.drain(&b.load[i], 0);
+    for (int i = 0; i < 3; ++i)
+      if (loads >> i & 1) ph.W.drain(&b.load[i], 0);
     mma_commit(&b.mma);
     ph.W.drain(&b.mma, 0);
     ph.W.drain(&b.mma, 1);

@@ -47,6 +47,13 @@ TTT_DEVICE_INLINE void store16_square(uint32_t base, int row, int c0, const floa
   store8_split(hi, lo, row, c0 & 63, x);
   store8_split(hi, lo, row, (c0 & 63) + 8, x + 8);
 }
+// the same, and a third plane [0, 1] at `rest`
+TTT_DEVICE_INLINE void store16_square3(uint32_t base, uint32_t rest, int row, int c0, const float* x) {
+  const uint32_t at = (uint32_t)(c0 >> 6) * ATOM;
+#pragma unroll
+  for (int i = 0; i < 16; i += 8)
+    store8_split3(base + at, base + at + 2 * ATOM, rest + at, row, (c0 & 63) + i, x + i);
+}
 // the column groups' sums of a row, [group][row]
 TTT_DEVICE_INLINE float row_total(const float* red, int row) {
   return (red[row] + red[C + row]) + (red[2 * C + row] + red[3 * C + row]);
@@ -259,9 +266,9 @@ __global__ void __launch_bounds__(THREADS, 1)
         for (int i = 0; i < 2; ++i)
           tma_load_3d(smem + SM::T + (2 * h + i) * ATOM, &mapT, &bars.load[1], 64 * i, 0, (int)(2 * id.ci + h));
     }
-    loads = 2;
-    // U = Ut - W S0;  dU = rho K X1 - Z, whose third plane takes X1's place (dU is what
-    // dV is made of: two planes, and lo lo left out, would be 3e-6 of it)
+    loads = 3;
+    // U = Ut - W S0;  dU = rho K X1 - Z; their third planes take the places of S0 and X1
+    // (two planes, and lo lo left out, would be 3e-6 of dV, and 2.6e-6 of dQ and dK)
     {
       const float rho = gate_ratio(gates, C - 1, row);
       const int c = cg * 16;
@@ -275,14 +282,14 @@ __global__ void __launch_bounds__(THREADS, 1)
       }
 #pragma unroll
       for (int b = 0; b < 16; b += 8) {
-        store8_split(sb + SM::U, sb + SM::U + ATOM, row, c + b, u + b);
+        store8_split3(sb + SM::U, sb + SM::U + ATOM, sb + SM::S, row, c + b, u + b);
         store8_split3(sb + SM::Y, sb + SM::Y + ATOM, sb + SM::X, row, c + b, y + b);
       }
     }
     ph.publish();
     if (warp == 1 && elect_one()) {
-      for (int h = 0; h < 2; ++h)
-        tma_store_3d(&mapU, smem + SM::U + h * ATOM, 64 * id.slice, 0, (int)(2 * id.ci + h));
+      for (int h = 0; h < 3; ++h)
+        tma_store_3d(&mapU, smem + (h < 2 ? SM::U + h * ATOM : SM::S), 0, 0, (int)(3 * at_slice + h));
       bulk_commit();
     }
     if (warp == 0 && ph.W.wait_warp(&bars.load[1], 0, 3) && elect_one()) {
@@ -355,13 +362,16 @@ template <int D>
 struct KeysSmem {
   static constexpr int DA = D / 64;
   static constexpr uint32_t HA = 64 * 128;                    // a [64][64] atom
-  static constexpr uint32_t DO = 0, MQ = DA * ATOM;           // MQ over S0 and X1 (rows of this slice)
-  static constexpr uint32_t S = MQ, X = S + 2 * DA * HA;
-  static constexpr uint32_t U = MQ + 4 * ATOM;                // then Mk
-  static constexpr uint32_t Y = U + 4 * ATOM;                 // then K, Q (this slice)
-  static constexpr uint32_t YB = 2 * DA * ATOM;
-  static constexpr uint32_t RED = DO;                         // behind the first products
-  static constexpr uint32_t GATES = Y + YB, XS = GATES + sizeof(Gates), BAR = XS + 64, TOTAL = BAR + 64;
+  // for the first products: dO; S0 and X1, hi and lo (rows of this slice); U, three
+  // planes; Y, whose hi plane comes into dO's place where D = 128
+  static constexpr uint32_t DO = 0, YHI = D == 64 ? ATOM : 0, S = 2 * ATOM, X = 4 * ATOM, UR = 6 * ATOM;
+  static constexpr uint32_t U = 8 * ATOM, YLO = 12 * ATOM;
+  // behind them: K, Q (this slice), sums; Mq, three planes, and Mk, hi and lo
+  // (heads of 64 have room for K and Q beside the first operands; but loaded with
+  // those, they hold up the first products: 694 us against 688 for 2048 chunks)
+  static constexpr uint32_t K = 0, Q = 12 * ATOM, RED = 13 * ATOM;
+  static constexpr uint32_t MQ = 4 * ATOM, MQR = 2 * ATOM, MK = 8 * ATOM;
+  static constexpr uint32_t GATES = 14 * ATOM, XS = GATES + sizeof(Gates), BAR = XS + 64, TOTAL = BAR + 64;
 };
 
 template <int D>
@@ -382,38 +392,53 @@ __global__ void __launch_bounds__(THREADS, 1)
   const ChunkId id(blockIdx.x, DA, Slab{0, a.nch, 0}, a.N);
   const uint32_t sb = smem_u32(smem);
   const uint32_t tmem = cta_begin(bars, TM_COLS, warp, [&]() {
-    mbar_arrive_expect_tx(&bars.load[0], 5 * DA * ATOM + 4 * DA * SM::HA);
+    mbar_arrive_expect_tx(&bars.load[0], (D == 64 ? 6 : 5) * DA * ATOM + 4 * DA * SM::HA);
     for (int i = 0; i < DA; ++i) {
+      const int zs = (int)(id.ci * DA + i);
       tma_load_3d(smem + SM::DO + i * ATOM, &mapD, &bars.load[0], 64 * i, id.t0, (int)id.bh);
+      for (int h = 0; h < 3; ++h)
+        tma_load_3d(smem + (h < 2 ? SM::U + 2 * h * ATOM : SM::UR) + i * ATOM, &mapU, &bars.load[0], 0, 0, 3 * zs + h);
       for (int h = 0; h < 2; ++h) {
         const int z = (int)(2 * id.ci + h);
-        tma_load_3d(smem + SM::U + (h * DA + i) * ATOM, &mapU, &bars.load[0], 64 * i, 0, z);
-        tma_load_3d(smem + SM::Y + (h * DA + i) * ATOM, &mapY, &bars.load[0], 0, 0, (int)(2 * (id.ci * DA + i) + h));
         tma_load_3d(smem + SM::S + (h * DA + i) * SM::HA, &mapS, &bars.load[0], 64 * i, 64 * id.slice, z);
         tma_load_3d(smem + SM::X + (h * DA + i) * SM::HA, &mapX, &bars.load[0], 64 * i, 64 * id.slice, z);
       }
+      tma_load_3d(smem + SM::YLO + i * ATOM, &mapY, &bars.load[0], 0, 0, 2 * zs + 1);
+      if (D == 64) tma_load_3d(smem + SM::YHI, &mapY, &bars.load[0], 0, 0, 2 * zs);
     }
   });
   Phase ph{Waiter{&bars.abort, a.st, 1500}, &bars.mma, 0};
   const int q4 = warp & 3, cg = warp >> 2, row = q4 * 32 + lane;
   const uint32_t lanes = (uint32_t)(q4 * 32) << 16;
   if (cg == 1) load_gates(gates, a.g ? a.g + id.tok : nullptr, a.beta + id.tok, id.n, row);
-  int loads = 1;
+  int loads = D == 64 ? 1 : 5;
   auto work = [&]() {
-    if (warp == 0 && ph.W.wait_warp(&bars.load[0], 0, 1) && elect_one()) {
-      const Op dO{sb + SM::DO, ATOM, false};
-      const Pair U{{sb + SM::U, ATOM, false}, DA * ATOM}, Y{{sb + SM::Y, ATOM, false}, DA * ATOM};
+    if (warp == 0) {
+      bool ok = ph.W.wait_warp(&bars.load[0], 0, 1);
+      const Op dO{sb + SM::DO, ATOM, false}, Ylo{sb + SM::YLO, ATOM, false}, Yhi{sb + SM::YHI, ATOM, false};
+      const Pair U{{sb + SM::U, ATOM, false}, 2 * ATOM};
       const Pair S{{sb + SM::S, SM::HA, false}, DA * SM::HA}, X{{sb + SM::X, SM::HA, false}, DA * SM::HA};
       auto prod = [&](uint32_t d, const Op& x, const Op& y, int N, bool add) { return Prod(tmem + d, x, y, 128, N, add); };
-      products<D / 16>(prod(TM_A, Y.lo(), U.hi, 128, false), prod(TM_YS, Y.lo(), S.hi, 64, false),
-                       prod(TM_UX, U.lo(), X.hi, 64, false), prod(TM_P, dO, U.lo(), 128, false),
-                       prod(TM_QS, dO, S.lo(), 64, false));
-      products<D / 16>(prod(TM_A, Y.hi, U.lo(), 128, true), prod(TM_YS, Y.hi, S.lo(), 64, true),
-                       prod(TM_UX, U.hi, X.lo(), 64, true), prod(TM_P, dO, U.hi, 128, true),
-                       prod(TM_QS, dO, S.hi, 64, true));
-      products<D / 16>(prod(TM_A, Y.hi, U.hi, 128, true), prod(TM_YS, Y.hi, S.hi, 64, true),
-                       prod(TM_UX, U.hi, X.hi, 64, true));
-      mma_commit(&bars.mma);
+      if (ok && elect_one()) {
+        // those of dO first: its place is free for Y's hi plane while the others run
+        products<D / 16>(prod(TM_P, dO, Op{sb + SM::UR, ATOM, false}, 128, false), prod(TM_QS, dO, S.lo(), 64, false));
+        products<D / 16>(prod(TM_P, dO, U.lo(), 128, true), prod(TM_QS, dO, S.hi, 64, true));
+        products<D / 16>(prod(TM_P, dO, U.hi, 128, true));
+        if (D == 128) mma_commit(&bars.half);
+        products<D / 16>(prod(TM_A, Ylo, U.lo(), 128, false), prod(TM_YS, Ylo, S.hi, 64, false),
+                         prod(TM_UX, U.lo(), X.lo(), 64, false));
+        products<D / 16>(prod(TM_A, Ylo, U.hi, 128, true), prod(TM_UX, U.lo(), X.hi, 64, true));
+        products<D / 16>(prod(TM_UX, U.hi, X.lo(), 64, true));
+        products<D / 16>(prod(TM_UX, U.hi, X.hi, 64, true));
+      }
+      __syncwarp();
+      if (D == 128) ok = ok && ph.W.wait_warp(&bars.load[2], 0, 7);
+      if (ok && elect_one()) {
+        products<D / 16>(prod(TM_A, Yhi, U.lo(), 128, true), prod(TM_YS, Yhi, S.lo(), 64, true));
+        products<D / 16>(prod(TM_A, Yhi, U.hi, 128, true), prod(TM_YS, Yhi, S.hi, 64, true));
+        mma_commit(&bars.mma);
+      }
+      __syncwarp();
     }
     if (ph.W.wait_warp(&bars.load[0], 0, 1)) {   // <X1, S0> of this slice's rows, while they are still here
       float acc = 0.f;
@@ -429,19 +454,28 @@ __global__ void __launch_bounds__(THREADS, 1)
       for (int o = 16; o > 0; o >>= 1) acc += __shfl_xor_sync(0xffffffffu, acc, o);
       if (lane == 0) xs[warp] = acc;
     }
+    if (D == 128 && warp == 2) {
+      if (ph.W.wait_warp(&bars.half, 0, 8) && elect_one()) {
+        mbar_arrive_expect_tx(&bars.load[2], DA * ATOM);
+        for (int i = 0; i < DA; ++i)
+          tma_load_3d(smem + SM::YHI + i * ATOM, &mapY, &bars.load[2], 0, 0, (int)(2 * (id.ci * DA + i)));
+      }
+      __syncwarp();
+    }
     if (!ph.mma_done(2)) return;
-    if (warp == 2 && elect_one()) {   // K and Q take Y's place
+    if (warp == 2 && elect_one()) {   // K and Q take the places of dO and Y
       mbar_arrive_expect_tx(&bars.load[1], (DA + 1) * ATOM);
       for (int i = 0; i < DA; ++i)
-        tma_load_3d(smem + SM::Y + i * ATOM, &mapK, &bars.load[1], 64 * i, id.t0, (int)id.bh);
-      tma_load_3d(smem + SM::Y + DA * ATOM, &mapQ, &bars.load[1], 64 * id.slice, id.t0, (int)id.bh);
+        tma_load_3d(smem + SM::K + i * ATOM, &mapK, &bars.load[1], 64 * i, id.t0, (int)id.bh);
+      tma_load_3d(smem + SM::Q, &mapQ, &bars.load[1], 64 * id.slice, id.t0, (int)id.bh);
     }
     if (tid == 96) {
       float acc = 0.f;
       for (int w = 0; w < THREADS / 32; ++w) acc += xs[w];
       a.xpart[id.slice * a.chunks + id.ci] = acc;
     }
-    loads = 2;
+    loads |= 2;
+    // Mq in three planes (two would be 2.5e-6 of dQ and dK)
 #pragma unroll
     for (int b = 0; b < 2; ++b) {
       const int c0 = cg * 32 + b * 16;
@@ -452,10 +486,10 @@ __global__ void __launch_bounds__(THREADS, 1)
       } else {
         zero16(x);
       }
-      store16_square(sb + SM::MQ, row, c0, x);
+      store16_square3(sb + SM::MQ, sb + SM::MQR, row, c0, x);
     }
     ph.publish();
-    const Op K{sb + SM::Y, ATOM, false};
+    const Op K{sb + SM::K, ATOM, false};
     if (warp == 0 && ph.W.wait_warp(&bars.load[1], 0, 3) && elect_one()) {
       products<D / 16>(Prod(tmem + TM_P, K, K, 128, 128, false));
       mma_commit(&bars.mma);
@@ -483,24 +517,26 @@ __global__ void __launch_bounds__(THREADS, 1)
         zero16(x);
         zero16(v + 16 * b);
       }
-      store16_square(sb + SM::U, row, c0, x);
+      store16_square(sb + SM::MK, row, c0, x);
     }
     red[cg * C + row] = db;
     ph.publish();
-    const Op Kmn{sb + SM::Y + id.slice * ATOM, ATOM, true}, Qmn{sb + SM::Y + DA * ATOM, ATOM, true};
+    const Op Kmn{sb + SM::K + id.slice * ATOM, ATOM, true}, Qmn{sb + SM::Q, ATOM, true};
     // (by a warp whose pairs all lie above the diagonal: issuing takes as long as
     // the products, and the other warps' sums go on meanwhile)
     constexpr int ISSUER = 4;
     if (warp == ISSUER && elect_one()) {
-      const Pair Mq{{sb + SM::MQ, ATOM, false}, 2 * ATOM}, Mk{{sb + SM::U, ATOM, false}, 2 * ATOM};
-      const Pair Mqt{{sb + SM::MQ, ATOM, true}, 2 * ATOM}, Mkt{{sb + SM::U, ATOM, true}, 2 * ATOM};
+      const Pair Mq{{sb + SM::MQ, ATOM, false}, 2 * ATOM}, Mk{{sb + SM::MK, ATOM, false}, 2 * ATOM};
+      const Pair Mqt{{sb + SM::MQ, ATOM, true}, 2 * ATOM}, Mkt{{sb + SM::MK, ATOM, true}, 2 * ATOM};
       if (a.cpart != nullptr) {   // q_i . k_j over this slice's columns, first: it is waited for alone
-        products<4>(Prod(tmem + TM_P, Op{sb + SM::Y + DA * ATOM, ATOM, false},
-                         Op{sb + SM::Y + id.slice * ATOM, ATOM, false}, 128, 128, false));
+        products<4>(Prod(tmem + TM_P, Op{sb + SM::Q, ATOM, false}, Op{sb + SM::K + id.slice * ATOM, ATOM, false}, 128,
+                         128, false));
         mma_commit(&bars.aux);
       }
-      products<8>(Prod(tmem + TM_QK, Mq.lo(), Kmn, 128, 64, false), Prod(tmem + TM_KR, Mk.lo(), Kmn, 128, 64, false),
-                  Prod(tmem + TM_KW, Mqt.lo(), Qmn, 128, 64, false));
+      products<8>(Prod(tmem + TM_QK, Op{sb + SM::MQR, ATOM, false}, Kmn, 128, 64, false),
+                  Prod(tmem + TM_KW, Op{sb + SM::MQR, ATOM, true}, Qmn, 128, 64, false));
+      products<8>(Prod(tmem + TM_QK, Mq.lo(), Kmn, 128, 64, true), Prod(tmem + TM_KR, Mk.lo(), Kmn, 128, 64, false),
+                  Prod(tmem + TM_KW, Mqt.lo(), Qmn, 128, 64, true));
       products<8>(Prod(tmem + TM_KW, Mkt.lo(), Kmn, 128, 64, true));
       products<8>(Prod(tmem + TM_QK, Mq.hi, Kmn, 128, 64, true), Prod(tmem + TM_KR, Mk.hi, Kmn, 128, 64, true),
                   Prod(tmem + TM_KW, Mqt.hi, Qmn, 128, 64, true));
@@ -527,10 +563,14 @@ __global__ void __launch_bounds__(THREADS, 1)
         const uint32_t at = sb + SM::MQ + (uint32_t)(c0 >> 6) * ATOM;
         load8_split(at, at + 2 * ATOM, row, c0 & 63, mq);
         load8_split(at, at + 2 * ATOM, row, (c0 & 63) + 8, mq + 8);
+        float rest[16];
+        const uint32_t rat = sb + SM::MQR + (uint32_t)(c0 >> 6) * ATOM;
+        load8(rat, row, c0 & 63, rest);
+        load8(rat, row, (c0 & 63) + 8, rest + 8);
 #pragma unroll
         for (int j = 0; j < 16; ++j) {
           float& x = v[16 * b + j];
-          x = c0 + j < row ? fmaf(mq[j], qk[j], fk * x) : 0.f;
+          x = c0 + j < row ? fmaf(mq[j] + rest[j], qk[j], fk * x) : 0.f;
           total += x;
         }
       }
@@ -568,8 +608,8 @@ __global__ void __launch_bounds__(THREADS, 1)
     // dq
     tmem_ld16(tmem + lanes + TM_QS + c, x);
     tmem_ld16(tmem + lanes + TM_QK + c, y);
-    load8(sb + SM::Y + DA * ATOM, row, c, t);
-    load8(sb + SM::Y + DA * ATOM, row, c + 8, t + 8);
+    load8(sb + SM::Q, row, c, t);
+    load8(sb + SM::Q, row, c + 8, t + 8);
 #pragma unroll
     for (int i = 0; i < 16; ++i) {
       x[i] *= fq;
@@ -578,8 +618,8 @@ __global__ void __launch_bounds__(THREADS, 1)
     }
     if (row < id.n) store_bf16_row16(a.dq + at, x);
     // dk: the state's part of the first for rs, third for ws
-    load8(sb + SM::Y + id.slice * ATOM, row, c, t);
-    load8(sb + SM::Y + id.slice * ATOM, row, c + 8, t + 8);
+    load8(sb + SM::K + id.slice * ATOM, row, c, t);
+    load8(sb + SM::K + id.slice * ATOM, row, c + 8, t + 8);
     tmem_ld16(tmem + lanes + TM_KR + c, x);
     tmem_ld16(tmem + lanes + TM_YS + c, y);
     tmem_ld16(tmem + lanes + TM_KW + c, z);
@@ -695,7 +735,7 @@ int bwd_launch(const DeltaBwdLaunch& L, cudaStream_t stream) {
       make_tmap_bf16_3d(&mk, p.k, D, p.N, BH, rs, p.N * rs, 64, C) ||
       make_tmap_bf16_3d(&md, L.dout, D, p.N, BH, rs, p.N * rs, 64, C) ||
       make_tmap_bf16_3d(&mw, o.W, D, C, 2 * nc, rs, C * rs, 64, C) ||
-      make_tmap_bf16_3d(&mu, ws + w.U, D, C, 2 * nc, rs, C * rs, 64, C) ||
+      make_tmap_bf16_3d(&mu, ws + w.U, 64, C, 3 * DA * nc, 128, ATOM, 64, C) ||   // [BH nch][D / 64][three planes][128][64]
       make_tmap_bf16_3d(&my, ws + w.Y, 64, C, 2 * DA * nc, 128, ATOM, 64, C) ||   // [BH nch][D / 64][hi, lo][128][64]
       make_tmap_bf16_3d(&mt, o.T, C, C, 2 * nc, 2 * C, 2 * C * C, 64, C) ||
       make_tmap_bf16_3d(&ms, fwd.X, D, D, 2 * nc, rs, D * rs, 64, D) ||
@@ -753,7 +793,7 @@ DeltaUmmaBwdWorkspace delta_umma_bwd_layout(int BH, int N, int D) {
   const size_t tile = nc * 2 * C * D * 2, mat = nc * 4 * D * D;
   w.gend = take(nc * 4);
   w.W = take(tile);
-  w.U = take(tile);
+  w.U = take(tile / 2 * 3);
   w.Ut = take(tile);
   w.Y = take(tile);
   w.T = take(nc * 2 * C * C * 2);

@@ -212,8 +212,8 @@ def test_workspace_of_the_longest_sequences():
         for D in (64, 128):
             d, chunks, slices = T.make_delta_desc(1, 1, N, D, D), -(-N // 128), D // 64
             pair, mat = 2 * 128 * D * 2, 4 * D * D
-            # W, U, Ut, Y; T; M, H, Hb and two border states; sums of tokens and chunks
-            want = 512 + up(4 * chunks) + 4 * up(pair * chunks) + up(chunks * 2 * 128 * 128 * 2) + 5 * up(mat * chunks)
+            # W, Ut, Y; U in three planes; T; M, H, Hb and two border states; sums of tokens and chunks
+            want = 512 + up(4 * chunks) + 3 * up(pair * chunks) + up(pair * chunks // 2 * 3) + up(chunks * 2 * 128 * 128 * 2) + 5 * up(mat * chunks)
             want += 4 * up(4 * slices * N) + up(4 * N) + up(4 * slices * chunks)
             assert _bytes("ttt_delta_bwd_workspace_bytes", d) == want
             # forward: at most three slabs, at least one chunk in six
