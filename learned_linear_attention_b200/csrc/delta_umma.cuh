@@ -5,13 +5,14 @@
 // a 128-row atom is 16 KB.  A derived matrix is a pair of atoms rows, hi =
 // bf16(x) and lo = bf16(x - hi): off by at most 2^-18 of the value, where one
 // bf16 alone would be off by 2^-9 and show in the float32 state.  Three products
-// join two pairs (lo lo, at most 2^-18, is left out).  Where that would be most of
-// a result's error it is carried in three planes: H and Hb, which S and dS0 consist
-// of where the state decays (off by 5e-7 and 1e-6 of the norm; 2.7e-6 and 3e-6 with
-// two), and P and U of the outputs (9e-7; 4.7e-6 with two).  Without decay the two
-// planes of T, W, M and X leave 4.4e-6 of S, where float32 operands would leave
-// 5e-7: three planes of all four would take twice the products and half as much
-// memory again, three of any of them leave 1.2e-6 or more.
+// join two pairs (lo lo, at most 2^-18, is left out).  What would be most of a
+// result's error is carried in three planes, errors by their norm: H and Hb, which S
+// and dS0 consist of where the state decays (off by 5e-7 and 1e-6; 2.7e-6 and 3e-6
+// with two planes); P and U of the outputs (9e-7; 4.7e-6); dU, U and Mq of the
+// gradients (1e-6 to 1.5e-6 before they are rounded to bf16; 4e-6).  Without decay
+// the two planes of T, W, M and X leave 4.4e-6 of S, where float32 operands would
+// leave 5e-7: three planes of all four would take twice the products and half as
+// much memory again, three of any of them leave 1.2e-6 or more.
 #pragma once
 
 #include "kernels.h"

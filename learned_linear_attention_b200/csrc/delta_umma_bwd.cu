@@ -63,7 +63,7 @@ TTT_DEVICE_INLINE float row_total(const float* red, int row) {
 // Hb is what dS0 is made of, in float32: its operands are carried in three
 // planes (hi + lo alone left 3e-6 of dS0, mostly by scale gam dO).  Its shared
 // memory leaves one CTA an SM, whose phases' latency bounds it: 2048 chunks of
-// heads of 64 116 us.
+// heads of 64 119 us.
 struct HbArgs {
   const __nv_bfloat16 *g, *beta;
   float *H, *Z;            // Z = -scale P^T dO: [BH nch][D / 64] float32 tiles [128][64]
@@ -185,9 +185,9 @@ __global__ void __launch_bounds__(THREADS, 1)
 }
 
 // ------------------------------------------------------------------ values
-// Reads T, W, Ut, the border states and what Hb left, 0.6 GB in 135 us for 2048
-// chunks of heads of 64: 4.5 TB/s, two thirds of what HBM gives.  Bound by the
-// latency of those loads, which one CTA an SM (its shared memory) does not hide.
+// Reads T, W, Ut, the border states and what Hb left and writes U and Y, 0.64 GB in
+// 140 us for 2048 chunks of heads of 64: 4.6 TB/s, 70 % of what HBM gives.  Bound by
+// the latency of the loads, which one CTA an SM (its shared memory) does not hide.
 struct ValsArgs {
   const __nv_bfloat16 *g, *beta, *v;
   const float *Ut, *Z;     // Z in the memory that Y takes
@@ -343,8 +343,9 @@ __global__ void __launch_bounds__(THREADS, 1)
 
 // ------------------------------------------------------------------ keys
 // One CTA an SM, by its shared memory; bound by the latency of its four rounds
-// of products: 2048 chunks of heads of 64 196 us (188 without the pairs' part of
-// dg, of which only what the last round does not hide counts).
+// of products: 2048 chunks of heads of 64 213 us (188 without the pairs' part of dg,
+// of which only what the last round does not hide counts, and without the third
+// planes of U and Mq).
 struct KeysArgs {
   const __nv_bfloat16 *g, *beta;
   __nv_bfloat16 *dq, *dk;
