@@ -930,18 +930,18 @@ int fwd_launch(const DeltaLaunch& p, cudaStream_t stream) {
 }  // namespace
 
 // Short sequences go token by token: the chunk kernels' latency is that of a
-// whole chunk and of three launches (23 us forward, 50 us backward at D = 64;
-// 31 and 62 at 128), the recurrent ones' 0.1 us a token at D = 64 and 0.14 at 128
-// (backward the same behind 24 and 40), times the rounds that their
-// CTAs of 16 value columns take on the device.  Both grow alike with the heads
-// once the chunks too fill it, so rounds count up to 5.  Token by token against
-// chunks, us: forward 8 heads of 64, 128 tokens 17 / 23, 256 tokens 29 / 23; of
-// 128, 128 tokens 25 / 31, 256 tokens 43 / 32; 128 heads of 64, 32 tokens 16 / 23,
-// 64 tokens 27 / 23.  Backward 8 heads of 64, 256 tokens 47 / 50, 300 tokens 51 /
-// 51, 512 tokens 72 / 52; of 128, 128 tokens 59 / 62, 200 tokens 72 / 63; 128 heads
-// of 64, 32 tokens 41 / 53, 64 tokens 69 / 54.  Heads of other sizes, or of two,
-// go token by token at every length: the tiles, the operands' layouts and the
-// D x D recurrence are written for one D.
+// whole chunk and of three launches (23 us forward, 52 us backward at D = 64;
+// 32 and 64 at 128), the recurrent ones' 0.1 us a token at D = 64 and 0.14 at 128
+// (backward the same behind 24 and 40), times the rounds that their CTAs of 16
+// value columns take on the device.  Both grow alike with the heads once the
+// chunks too fill it, so rounds count up to 5.  Token by token against chunks, us:
+// forward 8 heads of 64, 128 tokens 17 / 24, 256 tokens 29 / 23; of 128, 128 tokens
+// 25 / 32, 256 tokens 43 / 33; 128 heads of 64, 32 tokens 16 / 24, 64 tokens 27 /
+// 24.  Backward 8 heads of 64, 256 tokens 47 / 51, 300 tokens 51 / 53, 512 tokens
+// 72 / 54; of 128, 128 tokens 59 / 64, 200 tokens 72 / 65; 128 heads of 64, 32
+// tokens 41 / 55, 64 tokens 69 / 56.  Heads of other sizes, or of two, go token by
+// token at every length: the tiles, the operands' layouts and the D x D recurrence
+// are written for one D.
 bool delta_uses_umma(int bf16, int dk, int dv, long long BH, int N, int sms, bool backward) {
   if (!bf16 || dk != dv || (dk != 64 && dk != 128)) return false;
   const double rounds = (double)BH * (dv / 16) * (backward ? 2 : 1) / sms;
