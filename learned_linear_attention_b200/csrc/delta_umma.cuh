@@ -294,6 +294,7 @@ struct Bars {
   uint64_t load[3], mma, aux, fin, half;   // aux, fin, half: of product groups waited for beside those of mma
   uint32_t tmem, abort;
 };
+static_assert(sizeof(Bars) <= 64, "the layouts leave 64 bytes");
 // Barriers and `cols` TMEM columns, before the first phase; returns the TMEM
 // base.  An elected thread of warp 0 issues the first loads (on load[0]) as
 // soon as the barriers stand and the launch before this one is complete (every
