@@ -201,7 +201,7 @@ struct PrepSmem {
   static constexpr uint32_t GATES = T + TBYTES;
   static constexpr uint32_t COL = GATES + sizeof(Gates);   // gam, rho
   static constexpr uint32_t BAR = COL + 2 * C * 4;
-  static constexpr uint32_t TOTAL = BAR + 64;
+  static constexpr uint32_t TOTAL = BAR + 80;
 };
 
 template <int D>
@@ -640,7 +640,7 @@ struct OutSmem {
   static constexpr uint32_t S = 4 * OP;                             // S0 hi, lo
   static constexpr uint32_t U = 0, QS = 3 * ATOM;                   // behind the first products: three planes, Q S0
   static_assert(QS + C * 64 * 4 <= S + 2 * SA, "in the place of the operands");
-  static constexpr uint32_t GATES = S + 2 * SA, BAR = GATES + sizeof(Gates), TOTAL = BAR + 64;
+  static constexpr uint32_t GATES = S + 2 * SA, BAR = GATES + sizeof(Gates), TOTAL = BAR + 80;
 };
 
 template <int D>

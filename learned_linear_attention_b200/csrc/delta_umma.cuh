@@ -291,10 +291,10 @@ struct ChunkId {
   }
 };
 struct Bars {
-  uint64_t load[3], mma, aux, fin, half;   // aux, fin, half: of product groups waited for beside those of mma
+  uint64_t load[4], mma, aux, fin, half;   // aux, fin, half: of product groups waited for beside those of mma
   uint32_t tmem, abort;
 };
-static_assert(sizeof(Bars) <= 64, "the layouts leave 64 bytes");
+static_assert(sizeof(Bars) <= 80, "the layouts leave 80 bytes");
 // Barriers and `cols` TMEM columns, before the first phase; returns the TMEM
 // base.  An elected thread of warp 0 issues the first loads (on load[0]) as
 // soon as the barriers stand and the launch before this one is complete (every
@@ -304,7 +304,7 @@ static_assert(sizeof(Bars) <= 64, "the layouts leave 64 bytes");
 template <typename F>
 TTT_DEVICE_INLINE uint32_t cta_begin(Bars& b, uint32_t cols, int warp, F loads) {
   if (warp == 0 && elect_one()) {
-    for (int i = 0; i < 3; ++i) mbar_init(&b.load[i], 1);
+    for (int i = 0; i < 4; ++i) mbar_init(&b.load[i], 1);
     mbar_init(&b.mma, 1);
     mbar_init(&b.aux, 1);
     mbar_init(&b.fin, 1);
@@ -331,7 +331,7 @@ TTT_DEVICE_INLINE uint32_t cta_begin(Bars& b, uint32_t cols, int warp, F loads) 
 // that wait here are the same ones.
 TTT_DEVICE_INLINE void cta_end(Bars& b, const Phase& ph, int loads, uint32_t tmem, uint32_t cols, int warp) {
   if (warp == 0 && ph.W.aborted() && elect_one()) {
-    for (int i = 0; i < 3; ++i)
+    for (int i = 0; i < 4; ++i)
       if (loads >> i & 1) ph.W.drain(&b.load[i], 0);
     mma_commit(&b.mma);
     ph.W.drain(&b.mma, 0);

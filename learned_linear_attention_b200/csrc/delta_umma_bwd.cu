@@ -63,7 +63,7 @@ TTT_DEVICE_INLINE float row_total(const float* red, int row) {
 // Hb is what dS0 is made of, in float32: its operands are carried in three
 // planes (hi + lo alone left 3e-6 of dS0, mostly by scale gam dO).  Its shared
 // memory leaves one CTA an SM, whose phases' latency bounds it: 2048 chunks of
-// heads of 64 119 us.
+// heads of 64 118 us.
 struct HbArgs {
   const __nv_bfloat16 *g, *beta;
   float *H, *Z;            // Z = -scale P^T dO: [BH nch][D / 64] float32 tiles [128][64]
@@ -78,7 +78,7 @@ struct HbSmem {
   // three planes of P over K; then three each of -scale P^T dO, scale gam dO
   static constexpr uint32_t Q = 0, P = DA * ATOM;
   static constexpr uint32_t W = P + 6 * ATOM, DO = W + 2 * DA * ATOM;
-  static constexpr uint32_t GATES = DO + ATOM, BAR = GATES + sizeof(Gates), TOTAL = BAR + 64;
+  static constexpr uint32_t GATES = DO + ATOM, BAR = GATES + sizeof(Gates), TOTAL = BAR + 80;
 };
 
 template <int D>
@@ -137,9 +137,9 @@ __global__ void __launch_bounds__(THREADS, 1)
       mma_commit(&bars.mma);
     }
     if (!ph.mma_done(3)) return;
+    float u[16];
+    tmem_ld16(tmem + lanes + TM_U + cg * 16, u);
     {
-      float u[16];
-      tmem_ld16(tmem + lanes + TM_U + cg * 16, u);
       const float f = a.scale * gate_decay(gates, row);
 #pragma unroll
       for (int j = 0; j < 16; j += 8) {
@@ -154,7 +154,6 @@ __global__ void __launch_bounds__(THREADS, 1)
         store8_split3(at, at + ATOM, at + 2 * ATOM, row, cg * 16 + j, u + j);
         store8_split3(at + 3 * ATOM, at + 4 * ATOM, at + 5 * ATOM, row, cg * 16 + j, d);
       }
-      store_tile16(a.Z + (id.ci * DA + id.slice) * C * 64, C, row, cg * 16, u);
     }
     ph.publish();
     if (warp == 0 && elect_one()) {
@@ -167,6 +166,7 @@ __global__ void __launch_bounds__(THREADS, 1)
       products<8>(Prod(tmem, Qmn, G.hi, D, 192, true));
       mma_commit(&bars.mma);
     }
+    store_tile16(a.Z + (id.ci * DA + id.slice) * C * 64, C, row, cg * 16, u);
     if (!ph.mma_done(4)) return;
     const int r = D == 64 ? q4 * 16 + lane : row;
     float h[16];
@@ -205,7 +205,7 @@ struct ValsSmem {
   static constexpr uint32_t T = 0;                            // W first
   static constexpr uint32_t K = 4 * ATOM, S = K + DA * ATOM, X = S + 2 * SA, U = X + 2 * SA, Y = U + 2 * ATOM;
   static constexpr uint32_t RED = K;                          // behind the first products
-  static constexpr uint32_t GATES = Y + 2 * ATOM, BAR = GATES + sizeof(Gates), TOTAL = BAR + 64;
+  static constexpr uint32_t GATES = Y + 2 * ATOM, BAR = GATES + sizeof(Gates), TOTAL = BAR + 80;
 };
 
 template <int D>
@@ -343,7 +343,7 @@ __global__ void __launch_bounds__(THREADS, 1)
 
 // ------------------------------------------------------------------ keys
 // One CTA an SM, by its shared memory; bound by the latency of its four rounds
-// of products: 2048 chunks of heads of 64 213 us (188 without the pairs' part of dg,
+// of products: 2048 chunks of heads of 64 211 us (188 without the pairs' part of dg,
 // of which only what the last round does not hide counts, and without the third
 // planes of U and Mq).
 struct KeysArgs {
@@ -369,10 +369,11 @@ struct KeysSmem {
   static constexpr uint32_t U = 8 * ATOM, YLO = 12 * ATOM;
   // behind them: K, Q (this slice), sums; Mq, three planes, and Mk, hi and lo
   // (heads of 64 have room for K and Q beside the first operands; but loaded with
-  // those, they hold up the first products: 694 us against 688 for 2048 chunks)
+  // those, they hold up the first products: 694 us against 688 for the gradients of
+  // 2048 chunks)
   static constexpr uint32_t K = 0, Q = 12 * ATOM, RED = 13 * ATOM;
   static constexpr uint32_t MQ = 4 * ATOM, MQR = 2 * ATOM, MK = 8 * ATOM;
-  static constexpr uint32_t GATES = 14 * ATOM, XS = GATES + sizeof(Gates), BAR = XS + 64, TOTAL = BAR + 64;
+  static constexpr uint32_t GATES = 14 * ATOM, XS = GATES + sizeof(Gates), BAR = XS + 64, TOTAL = BAR + 80;
 };
 
 template <int D>
@@ -393,26 +394,30 @@ __global__ void __launch_bounds__(THREADS, 1)
   const ChunkId id(blockIdx.x, DA, Slab{0, a.nch, 0}, a.N);
   const uint32_t sb = smem_u32(smem);
   const uint32_t tmem = cta_begin(bars, TM_COLS, warp, [&]() {
-    mbar_arrive_expect_tx(&bars.load[0], (D == 64 ? 6 : 5) * DA * ATOM + 4 * DA * SM::HA);
+    // what the first products read, then the others' operands
+    mbar_arrive_expect_tx(&bars.load[0], 4 * DA * ATOM + 2 * DA * SM::HA);
     for (int i = 0; i < DA; ++i) {
-      const int zs = (int)(id.ci * DA + i);
       tma_load_3d(smem + SM::DO + i * ATOM, &mapD, &bars.load[0], 64 * i, id.t0, (int)id.bh);
       for (int h = 0; h < 3; ++h)
-        tma_load_3d(smem + (h < 2 ? SM::U + 2 * h * ATOM : SM::UR) + i * ATOM, &mapU, &bars.load[0], 0, 0, 3 * zs + h);
-      for (int h = 0; h < 2; ++h) {
-        const int z = (int)(2 * id.ci + h);
-        tma_load_3d(smem + SM::S + (h * DA + i) * SM::HA, &mapS, &bars.load[0], 64 * i, 64 * id.slice, z);
-        tma_load_3d(smem + SM::X + (h * DA + i) * SM::HA, &mapX, &bars.load[0], 64 * i, 64 * id.slice, z);
-      }
-      tma_load_3d(smem + SM::YLO + i * ATOM, &mapY, &bars.load[0], 0, 0, 2 * zs + 1);
-      if (D == 64) tma_load_3d(smem + SM::YHI, &mapY, &bars.load[0], 0, 0, 2 * zs);
+        tma_load_3d(smem + (h < 2 ? SM::U + 2 * h * ATOM : SM::UR) + i * ATOM, &mapU, &bars.load[0], 0, 0,
+                    (int)(3 * (id.ci * DA + i)) + h);
+      for (int h = 0; h < 2; ++h)
+        tma_load_3d(smem + SM::S + (h * DA + i) * SM::HA, &mapS, &bars.load[0], 64 * i, 64 * id.slice, (int)(2 * id.ci + h));
+    }
+    mbar_arrive_expect_tx(&bars.load[3], (D == 64 ? 2 : 1) * DA * ATOM + 2 * DA * SM::HA);
+    for (int i = 0; i < DA; ++i) {
+      const int zs = (int)(2 * (id.ci * DA + i));
+      tma_load_3d(smem + SM::YLO + i * ATOM, &mapY, &bars.load[3], 0, 0, zs + 1);
+      for (int h = 0; h < 2; ++h)
+        tma_load_3d(smem + SM::X + (h * DA + i) * SM::HA, &mapX, &bars.load[3], 64 * i, 64 * id.slice, (int)(2 * id.ci + h));
+      if (D == 64) tma_load_3d(smem + SM::YHI, &mapY, &bars.load[3], 0, 0, zs);
     }
   });
   Phase ph{Waiter{&bars.abort, a.st, 1500}, &bars.mma, 0};
   const int q4 = warp & 3, cg = warp >> 2, row = q4 * 32 + lane;
   const uint32_t lanes = (uint32_t)(q4 * 32) << 16;
   if (cg == 1) load_gates(gates, a.g ? a.g + id.tok : nullptr, a.beta + id.tok, id.n, row);
-  int loads = D == 64 ? 1 : 5;
+  int loads = D == 64 ? 9 : 13;
   auto work = [&]() {
     if (warp == 0) {
       bool ok = ph.W.wait_warp(&bars.load[0], 0, 1);
@@ -426,6 +431,10 @@ __global__ void __launch_bounds__(THREADS, 1)
         products<D / 16>(prod(TM_P, dO, U.lo(), 128, true), prod(TM_QS, dO, S.hi, 64, true));
         products<D / 16>(prod(TM_P, dO, U.hi, 128, true));
         if (D == 128) mma_commit(&bars.half);
+      }
+      __syncwarp();
+      ok = ok && ph.W.wait_warp(&bars.load[3], 0, 9);
+      if (ok && elect_one()) {
         products<D / 16>(prod(TM_A, Ylo, U.lo(), 128, false), prod(TM_YS, Ylo, S.hi, 64, false),
                          prod(TM_UX, U.lo(), X.lo(), 64, false));
         products<D / 16>(prod(TM_A, Ylo, U.hi, 128, true), prod(TM_UX, U.lo(), X.hi, 64, true));
@@ -441,7 +450,7 @@ __global__ void __launch_bounds__(THREADS, 1)
       }
       __syncwarp();
     }
-    if (ph.W.wait_warp(&bars.load[0], 0, 1)) {   // <X1, S0> of this slice's rows, while they are still here
+    if (ph.W.wait_warp(&bars.load[0], 0, 1) && ph.W.wait_warp(&bars.load[3], 0, 9)) {   // <X1, S0> of this slice's rows, while they are still here
       float acc = 0.f;
       for (int e = tid; e < 64 * D / 8; e += THREADS) {
         const int r = e / (D / 8), c = e % (D / 8) * 8;
