@@ -635,3 +635,29 @@ def test_gradients_of_the_chunk_form_round_as_their_float32_values_do(cuda_devic
     for name, a, b in zip(("dq", "dk", "dv"), p.bwd(), want):
         other = (a.cpu() != torch.from_numpy(b).to(torch.bfloat16)).double().mean().item()
         assert other <= {"dq": 1.4e-3, "dk": 1.9e-3, "dv": 1.4e-3}[name], f"{name}: {other:.2e} of the values"
+
+
+@pytest.mark.parametrize("B,H,N", [(1, 2, 400), (4, 20, 130)])
+@pytest.mark.parametrize("start", [True, False])
+def test_chunk_form_gradients_without_decay(cuda_device, B, H, N, start):
+    for d in (64, 128):
+        p = Problem(B, H, N, d, d, "bf16", decay=False, start=start)
+        assert in_chunks(p, True)
+        p.check_bwd(p.bwd())
+
+
+def test_gradients_on_two_streams_at_once(cuda_device):
+    """Calls of either size and form side by side, each with its own workspace: the same bits."""
+    ps = [Problem(2, 4, N, d, d, dt, seed=N) for d, N, dt in ((64, 700, "bf16"), (128, 500, "bf16"), (32, 200, "f32"))]
+    want = [p.bwd() for p in ps]
+    streams = [torch.cuda.Stream() for _ in ps]
+    outs = [p.new_grads() for p in ps]
+    wss = [T.alloc_workspace(T.ttt_delta_bwd_workspace_bytes(p.desc())) for p in ps]
+    torch.cuda.synchronize()
+    for _ in range(4):
+        for p, s, g, ws in zip(ps, streams, outs, wss):
+            x = p.dev
+            T.ttt_delta_bwd(p.desc(), x["q"], x["k"], x["v"], x["g"], x["beta"], p.S0, x["dout"], p.dS, *g, ws, stream=s)
+    torch.cuda.synchronize()
+    assert all(T.ttt_check_device_status(ws) == T.TTT_OK for ws in wss)
+    assert all(torch.equal(a, b) for w, g in zip(want, outs) for a, b in zip(w, g))
