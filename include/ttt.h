@@ -188,7 +188,7 @@ int ttt_linear_bwd(const ttt_linear_desc* desc, const void* q, const void* k, co
  * carried as bf16 hi + lo (about 17 significant bits; three planes in what S and dS0 are made of) with
  * float32 sums, and the state stays float32: S and dS0 come out to about 1e-6 of
  * their norm, as a float32 out does, without decay (or with one that leaves much
- * of the state over 128 tokens) to 5e-6.  Every other type and size runs
+ * of the state over 128 tokens) to 6e-6.  Every other type and size runs
  * in float32 on CUDA cores, four tokens at a time (2e-7 to 5e-7), so a caller
  * who wants that of bf16 values passes them as float32.  An infinity or NaN in a
  * token reaches the tokens behind it, and on tensor cores all of its chunk,
