@@ -185,7 +185,8 @@ int ttt_linear_bwd(const ttt_linear_desc* desc, const void* q, const void* k, co
  * The sequence form and its gradients with bf16 inputs and dk = dv = 64 or
  * 128 run on tensor cores in chunks of 128 tokens once they hold some 200
  * tokens (some 40 where there are many heads): every derived operand there is
- * carried as bf16 hi + lo (about 17 significant bits; three planes in what S and dS0 are made of) with
+ * carried as bf16 hi + lo (about 17 significant bits), in three planes where that
+ * would be most of a result's error, with
  * float32 sums, and the state stays float32: S and dS0 come out to about 1e-6 of
  * their norm, as a float32 out does, without decay (or with one that leaves much
  * of the state over 128 tokens) to 6e-6.  Every other type and size runs
